@@ -2,9 +2,24 @@
 
 The computation lives in ``libcconv.so`` (C ABI: ``include/cconv.h``); this package is its
 thin Python binding with the same names, plus the build step and the seeded synthetic
-input generators.  Importing the package does not load the library; the first call does,
-and raises if it has not been built.
+input generators.  The mixer operators that follow the convolution (per-head norm of queries
+and keys with the position rotation, linear attention with a decay per token and head) live
+in ``libcattn.so`` (C ABI: ``include/cattn.h``).  Importing the package does not load the
+libraries; the first call does, and raises if they have not been built.
 """
+from .attn import (  # noqa: F401
+    attn_describe,
+    cattn_device_fault,
+    cattn_linear_bwd,
+    cattn_linear_bwd_workspace_bytes,
+    cattn_linear_fwd,
+    cattn_linear_fwd_workspace_bytes,
+    cattn_linear_update,
+    cattn_qknorm_bwd,
+    cattn_qknorm_bwd_workspace_bytes,
+    cattn_qknorm_fwd,
+)
+from .attn_autograd import decay_attention, qk_norm_rope  # noqa: F401
 from .autograd import causal_conv1d  # noqa: F401
 from .binding import (  # noqa: F401
     CCONV_ACT_NONE,

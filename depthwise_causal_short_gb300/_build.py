@@ -1,10 +1,11 @@
-"""Build the sm_103a CUDA library ``libcconv.so`` in-tree (nvcc, no cmake).
+"""Build the sm_103a CUDA libraries ``libcconv.so`` and ``libcattn.so`` in-tree (nvcc, no cmake).
 
     python -m depthwise_causal_short_gb300._build
 
-Each ``csrc/*.cu`` translation unit is compiled in parallel for sm_103a only and linked
-into one shared library exporting the C ABI of ``include/cconv.h`` (hidden visibility for
-everything else, CUDA runtime linked statically).
+Each translation unit is compiled in parallel for sm_103a only; ``csrc/*.cu`` are linked into
+``libcconv.so`` (C ABI: ``include/cconv.h``), ``csrc/attn/*.cu`` into ``libcattn.so`` (C ABI:
+``include/cattn.h``), with hidden visibility for everything else and the CUDA runtime linked
+statically.
 """
 from __future__ import annotations
 
@@ -21,6 +22,7 @@ INCLUDE = ROOT / "include"
 OBJ_DIR = PKG / "_build"
 LIB_DIR = PKG / "_lib"
 LIB = LIB_DIR / "libcconv.so"
+ATTN_LIB = LIB_DIR / "libcattn.so"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [
@@ -41,20 +43,34 @@ def sources() -> list[Path]:
     return sorted(CSRC.glob("*.cu"))
 
 
-def _inputs() -> list[Path]:
-    return sources() + sorted(CSRC.glob("*.cuh")) + sorted(INCLUDE.glob("*.h")) + [Path(__file__)]
+def attn_sources() -> list[Path]:
+    return sorted((CSRC / "attn").glob("*.cu"))
+
+
+def _inputs(lib: Path) -> list[Path]:
+    """Everything `lib` is built from."""
+    shared = sorted(CSRC.glob("*.cuh")) + [INCLUDE / "cconv.h", Path(__file__)]
+    if lib == LIB:
+        return sources() + shared
+    return attn_sources() + sorted((CSRC / "attn").glob("*.cuh")) + [INCLUDE / "cattn.h"] + shared
+
+
+def _newer(lib: Path) -> bool:
+    if not lib.exists():
+        return False
+    t = lib.stat().st_mtime
+    return all(p.stat().st_mtime <= t for p in _inputs(lib))
 
 
 def up_to_date() -> bool:
-    if not LIB.exists():
-        return False
-    t = LIB.stat().st_mtime
-    return all(p.stat().st_mtime <= t for p in _inputs())
+    return _newer(LIB) and _newer(ATTN_LIB)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> Path:
-    """Compile and link libcconv.so unless it is newer than every source."""
-    if not force and not extra_flags and up_to_date():
+    """Compile and link each library unless it is newer than every source of it."""
+    todo = [(lib, srcs) for lib, srcs in ((LIB, sources()), (ATTN_LIB, attn_sources()))
+            if force or extra_flags or not _newer(lib)]
+    if not todo:
         return LIB
     OBJ_DIR.mkdir(parents=True, exist_ok=True)
     LIB_DIR.mkdir(parents=True, exist_ok=True)
@@ -72,13 +88,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         return obj
 
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        objs = list(ex.map(compile_one, sources()))
-    tmp = LIB.with_suffix(f".{os.getpid()}.tmp")
-    cmd = [exe, *ARCH, "-shared", "-cudart", "static", "-o", str(tmp), *map(str, objs)]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of libcconv.so failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+        built = {src: ex.submit(compile_one, src) for _, srcs in todo for src in srcs}
+    for lib, srcs in todo:
+        objs = [built[src].result() for src in srcs]
+        tmp = lib.with_suffix(f".{os.getpid()}.tmp")
+        cmd = [exe, *ARCH, "-shared", "-cudart", "static", "-o", str(tmp), *map(str, objs)]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link of {lib.name} failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, lib)
     return LIB
 
 

@@ -1,0 +1,56 @@
+// attn.cuh -- what the mixer kernels of libcattn share, on top of the convolution's helpers.
+#pragma once
+
+#include "../common.cuh"
+#include "../../../include/cattn.h"
+
+namespace cattn {
+
+using cconv::launch_pdl;
+using cconv::report_cuda;
+
+enum FaultCode : unsigned {
+  kFaultWait = 1u,      // a bounded wait ran out
+  kFaultSeqlens = 4u,   // an ill-formed cu_seqlens was passed
+  kFaultPosition = 8u,  // a position outside the rotation tables
+};
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 16;
+constexpr int kMaxK = 128;
+constexpr int kMaxV = 256;
+
+// Each translation unit owns a device fault word and registers a reader of it.
+struct FaultReader {
+  explicit FaultReader(int (*read)(unsigned*));
+};
+
+inline bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// A [total, H, C] bf16 activation with strides (st, sh): the rules of cattn.h.
+inline int check_rows(const void* p, int64_t total, int64_t H, int64_t st, int64_t sh) {
+  if (!aligned(p, 16)) return CCONV_ERR_ALIGN;
+  if (total > 1) {
+    if (st < 1) return CCONV_ERR_STRIDE;
+    if (st % 8 != 0) return CCONV_ERR_ALIGN;
+  }
+  if (H > 1) {
+    if (sh < 1) return CCONV_ERR_STRIDE;
+    if (sh % 8 != 0) return CCONV_ERR_ALIGN;
+  }
+  return CCONV_OK;
+}
+
+// Rows [a, b) of sequence i, inside [0, total] whatever cu_seqlens holds.
+__device__ __forceinline__ void sequence_rows(const int32_t* cu, int i, int total, int& a, int& b) {
+  a = min(max(cu[i], 0), total);
+  b = min(max(cu[i + 1], a), total);
+}
+
+__device__ __forceinline__ float clamp_decay(float g) { return g < -128.f ? -128.f : g; }
+
+// Checks n state indices against S slots (negative, >= S, repeated; -1 allowed with pad), and
+// nseq + 1 row offsets when cu is given; writes status[0..1] when idx is given.  One CTA.
+int launch_checks(const int32_t* idx, int64_t n, int64_t S, int pad, int32_t* status,
+                  const int32_t* cu, int64_t nseq, int64_t total, cudaStream_t stream);
+
+}  // namespace cattn
