@@ -49,8 +49,11 @@ __device__ __forceinline__ void sequence_rows(const int32_t* cu, int i, int tota
 __device__ __forceinline__ float clamp_decay(float g) { return g < -128.f ? -128.f : g; }
 
 // Checks n state indices against S slots (negative, >= S, repeated; -1 allowed with pad), and
-// nseq + 1 row offsets when cu is given; writes status[0..1] when idx is given.  One CTA.
+// nseq + 1 row offsets when cu is given; writes status[0..1] when idx is given, and with
+// `cstart` the offsets of the sequences' 128-token chunks (an empty sequence has one; all zero
+// for ill-formed offsets).  One CTA.
 int launch_checks(const int32_t* idx, int64_t n, int64_t S, int pad, int32_t* status,
-                  const int32_t* cu, int64_t nseq, int64_t total, cudaStream_t stream);
+                  const int32_t* cu, int64_t nseq, int64_t total, int32_t* cstart,
+                  cudaStream_t stream);
 
 }  // namespace cattn

@@ -69,6 +69,7 @@ struct CheckArgs {
   const int32_t* idx;
   const int32_t* cu;
   int32_t* status;
+  int32_t* cstart;
   int64_t S;
   int n, nseq, total, pad;
 };
@@ -86,7 +87,34 @@ __global__ void __launch_bounds__(kCheckThreads) cattn_check_kernel(CheckArgs p)
       bad |= i == 0 ? c != 0 : c < p.cu[i - 1];
       bad |= i == p.nseq && c != p.total;
     }
-    if (bad) atomicOr(&g_fault_host, kFaultSeqlens);
+    bad = __syncthreads_or(bad);
+    if (bad && tid == 0) atomicOr(&g_fault_host, kFaultSeqlens);
+    if (p.cstart) {
+      // running sum of the chunk counts, kCheckThreads sequences at a time
+      __shared__ int sums[kCheckThreads / 32];
+      int carry = 0;
+      for (int at = 0; at < p.nseq; at += kCheckThreads) {
+        const int i = at + tid;
+        const int len = i < p.nseq && !bad ? p.cu[i + 1] - p.cu[i] : 0;
+        int x = i < p.nseq && !bad ? max(1, (len + 127) / 128) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (tid % 32 >= o) x += y;
+        }
+        if (tid % 32 == 31) sums[tid / 32] = x;
+        __syncthreads();
+        int all = 0;
+        for (int w = 0; w < kCheckThreads / 32; ++w) {
+          if (w < tid / 32) x += sums[w];
+          all += sums[w];
+        }
+        if (i < p.nseq) p.cstart[i + 1] = carry + x;
+        carry += all;
+        __syncthreads();
+      }
+      if (tid == 0) p.cstart[0] = 0;
+    }
   }
   if (!p.idx) return;
   for (int i = tid; i < static_cast<int>((p.S + 31) / 32); i += kCheckThreads) seen[i] = 0;
@@ -114,8 +142,9 @@ __global__ void __launch_bounds__(kCheckThreads) cattn_check_kernel(CheckArgs p)
 }
 
 int launch_checks(const int32_t* idx, int64_t n, int64_t S, int pad, int32_t* status,
-                  const int32_t* cu, int64_t nseq, int64_t total, cudaStream_t stream) {
-  CheckArgs a{idx, cu, status, S, static_cast<int>(n), static_cast<int>(nseq),
+                  const int32_t* cu, int64_t nseq, int64_t total, int32_t* cstart,
+                  cudaStream_t stream) {
+  CheckArgs a{idx, cu, status, cstart, S, static_cast<int>(n), static_cast<int>(nseq),
               static_cast<int>(total), pad};
   const size_t smem = idx ? static_cast<size_t>((S + 31) / 32) * 4 : 0;
   if (smem > 32 * 1024 &&

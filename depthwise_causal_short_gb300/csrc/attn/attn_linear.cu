@@ -15,7 +15,7 @@
 // and q_i . dq'_i sums the pairs j < i that end at i, k_j . dk'_j the pairs i > j that start at
 // j.  (With the products i = j in both sums they would cancel only to rounding, and drown the
 // dg of heads that forget fast.)
-#include "attn_linear.cuh"
+#include "attn_chunk_host.h"
 
 namespace cattn {
 
@@ -24,6 +24,7 @@ using cconv::bf16_to_f32;
 constexpr int kCols = 32;   // columns of M in one CTA (one a lane)
 constexpr int kWarps = 4;   // rows of M are dealt out to the warps
 constexpr int kTile = 16;   // tokens staged at once
+constexpr int64_t kMaxSeqs = int64_t(1) << 30;
 
 struct SweepArgs {
   Rows a, b, c;
@@ -235,7 +236,7 @@ int check_linear(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t
 static int check_states(const int32_t* cu, int64_t nseq, const float* initial, const float* fin,
                         const int32_t* idx, int64_t S, int32_t* status) {
   if (!cu) return CCONV_ERR_NULL;
-  if (nseq < 1 || nseq > (int64_t(1) << 31) - 2) return CCONV_ERR_SHAPE;
+  if (nseq < 1 || nseq > kMaxSeqs) return CCONV_ERR_SHAPE;
   if (!aligned(cu, 4)) return CCONV_ERR_ALIGN;
   if (idx) {
     if (!status) return CCONV_ERR_NULL;
@@ -279,8 +280,23 @@ static size_t bwd_bytes(int64_t total, int64_t Hv, int64_t K) {
   return static_cast<size_t>(total) * Hv * (2 * K + 2 * slices_of(K)) * 4;
 }
 
+// CTAs of the chunked kernels: one per SM, or one per unit where there can be no more units.
+static int chunk_grid(int64_t total, int64_t nseq, int64_t Hv, int64_t V, int* grid) {
+  int dev = 0, sms = 0;
+  if (report_cuda("cudaGetDevice", cudaGetDevice(&dev)) != cudaSuccess ||
+      report_cuda("cudaDeviceGetAttribute",
+                  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+    return CCONV_ERR_CUDA;
+  const int64_t units = Hv * ((V + 127) / 128) * (total / 128 + nseq);
+  *grid = static_cast<int>(units < sms ? units : sms);
+  return CCONV_OK;
+}
+
+// The chunk offsets at the head of the workspace.
+static size_t offsets_bytes(int64_t nseq) { return (static_cast<size_t>(nseq + 1) * 4 + 15) / 16 * 16; }
+
 static int check_sizes(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv, int64_t K, int64_t V) {
-  if (total < 0 || total > kMaxRows || nseq < 1 || nseq > (int64_t(1) << 31) - 2 || Hk < 1 ||
+  if (total < 0 || total > kMaxRows || nseq < 1 || nseq > kMaxSeqs || Hk < 1 ||
       Hv < 1 || Hv > 65535 || Hv % Hk != 0 || K < 8 || K > kMaxK || V < 8 || V > kMaxV)
     return CCONV_ERR_SHAPE;
   return CCONV_OK;
@@ -294,8 +310,11 @@ extern "C" CCONV_API int cattn_linear_fwd_workspace_bytes(int64_t total, int64_t
   using namespace cattn;
   if (!bytes) return CCONV_ERR_NULL;
   const int rc = check_sizes(total, nseq, Hk, Hv, K, V);
-  if (rc == CCONV_OK) *bytes = 0;
-  return rc;
+  int grid = 0;
+  if (rc != CCONV_OK) return rc;
+  if (chunk_grid(total, nseq, Hv, V, &grid) != CCONV_OK) return CCONV_ERR_CUDA;
+  *bytes = offsets_bytes(nseq) + chunk_fwd_bytes(grid);
+  return CCONV_OK;
 }
 
 extern "C" CCONV_API int cattn_linear_bwd_workspace_bytes(int64_t total, int64_t nseq, int64_t Hk,
@@ -315,25 +334,31 @@ extern "C" CCONV_API int cattn_linear_fwd(
     const float* initial_state, float* final_state, const int32_t* state_indices, int64_t S,
     int32_t* status_dev, void* o, void* workspace, size_t workspace_bytes, cconv_stream_t stream) {
   using namespace cattn;
-  (void)workspace, (void)workspace_bytes;
   int rc = check_linear(q, sqt, sqh, k, skt, skh, v, svt, svh, g, sgt, sgh, total, Hk, Hv, K, V, o);
   if (rc == CCONV_OK)
     rc = check_states(cu_seqlens, nseq, initial_state, final_state, state_indices, S, status_dev);
   if (rc != CCONV_OK) return rc;
-  rc = launch_checks(state_indices, nseq, S, 0, status_dev, cu_seqlens, nseq, total, stream);
+  int grid = 0;
+  if (chunk_grid(total, nseq, Hv, V, &grid) != CCONV_OK) return CCONV_ERR_CUDA;
+  if (!workspace || workspace_bytes < offsets_bytes(nseq) + chunk_fwd_bytes(grid))
+    return CCONV_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return CCONV_ERR_ALIGN;
+  int32_t* cstart = static_cast<int32_t*>(workspace);
+  rc = launch_checks(state_indices, nseq, S, 0, status_dev, cu_seqlens, nseq, total, cstart, stream);
   if (rc != CCONV_OK) return rc;
-  SweepArgs p{};
-  p.a = rows(q, sqt, sqh), p.b = rows(k, skt, skh), p.c = rows(v, svt, svh);
-  p.g = Gates{g, sgt, sgh};
-  p.s = shape_of(total, Hk, Hv, K, V, nseq);
-  p.ha = p.hb = p.s.Hk, p.hc = p.s.Hv, p.A = p.s.K, p.C = p.s.V;
-  p.cu = cu_seqlens;
-  p.slots = Slots{state_indices, S};
-  p.m0 = initial_state, p.m1 = final_state, p.m1_slots = true, p.m1_scale = 1.f;
-  p.status = state_indices ? status_dev : nullptr;
-  p.scale = scale;
-  p.out = static_cast<uint16_t*>(o);
-  return launch_sweep(p, false, stream);
+  ChunkCall c{};
+  c.q = rows(q, sqt, sqh), c.k = rows(k, skt, skh), c.v = rows(v, svt, svh);
+  c.g = Gates{g, sgt, sgh};
+  c.s = shape_of(total, Hk, Hv, K, V, nseq);
+  c.cu = cu_seqlens, c.cstart = cstart;
+  c.slots = Slots{state_indices, S};
+  c.initial = initial_state, c.fin = final_state;
+  c.status = state_indices ? status_dev : nullptr;
+  c.scale = scale;
+  c.o = static_cast<uint16_t*>(o);
+  c.carry = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + offsets_bytes(nseq));
+  c.grid = grid;
+  return launch_chunk_fwd(c, stream);
 }
 
 extern "C" CCONV_API int cattn_linear_bwd(
@@ -358,7 +383,8 @@ extern "C" CCONV_API int cattn_linear_bwd(
     if (!workspace || workspace_bytes < bwd_bytes(total, Hv, K)) return CCONV_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return CCONV_ERR_ALIGN;
   }
-  rc = launch_checks(state_indices, nseq, S, 0, status_dev, cu_seqlens, nseq, total, stream);
+  rc = launch_checks(state_indices, nseq, S, 0, status_dev, cu_seqlens, nseq, total, nullptr,
+                     stream);
   if (rc != CCONV_OK) return rc;
 
   const Rows rq = rows(q, sqt, sqh), rk = rows(k, skt, skh), rv = rows(v, svt, svh),

@@ -121,7 +121,7 @@ extern "C" CCONV_API int cattn_linear_update(
   if (S < 1 || (state_indices ? S > CCONV_UPDATE_MAX_SLOTS : S < N)) return CCONV_ERR_SHAPE;
   if (!aligned(state, 16) || !aligned(status_dev, 4) || !aligned(state_indices, 4))
     return CCONV_ERR_ALIGN;
-  if (launch_checks(state_indices, N, S, pad_rows, status_dev, nullptr, 0, 0, stream) != CCONV_OK)
+  if (launch_checks(state_indices, N, S, pad_rows, status_dev, nullptr, 0, 0, nullptr, stream) != CCONV_OK)
     return CCONV_ERR_CUDA;
   UpdateArgs a{};
   a.q = Rows{static_cast<const uint16_t*>(q), sqt, sqh};

@@ -51,6 +51,9 @@ CASES = [
     ([257, 300], 1, 3, 96, 40), ([5, 500], 1, 1, 40, 136), ([384], 1, 8, 32, 128),
     ([130, 2, 126], 3, 3, 72, 256), ([700], 1, 1, 64, 96), ([1] * 40, 2, 2, 64, 32),
     ([1000], 1, 1, 128, 128), ([1, 255, 256, 1], 1, 2, 120, 200),
+    # more chunks than SMs: ranges of several chunks, heads and sequences
+    ([1] * 200, 1, 4, 32, 32), ([128] * 20 + [5] * 20, 2, 8, 32, 32), ([700, 0, 1300], 2, 16, 32, 40),
+    ([2500], 8, 8, 16, 16), ([90, 2, 300] * 5, 4, 16, 24, 136),
 ]
 
 
