@@ -32,7 +32,15 @@ struct Plan {
 };
 
 struct Range {
-  int64_t u0, u1;  // units of this CTA
+  int64_t u0, u1;  // units of this CTA, [u0, u1)
+};
+
+// The part of a range that continues in the next range (the previous one for a sweep from the
+// last token): [u0, u1), empty if the range's end is a sequence's end; `closed` if the sequence
+// starts (ends) in this range.
+struct Tail {
+  int64_t u0, u1;
+  bool closed;
 };
 
 __device__ __forceinline__ int64_t unit_count(const Plan& p, int& nch) {
@@ -84,11 +92,54 @@ struct Walker {
       load();
     }
   }
+  __device__ __forceinline__ void prev() {
+    --c;
+    if (c < 0) {
+      c = nch - 1;
+      seq = p->nseq - 1;
+      --ht;
+      load();
+    } else if (c < cs) {
+      --seq;
+      load();
+    }
+  }
+  template <bool REV>
+  __device__ __forceinline__ void step() {
+    if (REV)
+      prev();
+    else
+      next();
+  }
   __device__ __forceinline__ bool first() const { return c == cs; }
   __device__ __forceinline__ bool last() const { return c == ce - 1; }
   __device__ __forceinline__ int row0() const { return base + (c - cs) * kChunk; }
   __device__ __forceinline__ int rows() const { return min(kChunk, len - (c - cs) * kChunk); }
 };
+
+template <bool REV>
+__device__ __forceinline__ Tail tail_of(const Plan& p, int nch, int64_t units, const Range& r) {
+  Tail t{r.u1, r.u1, false};
+  if (r.u0 >= r.u1) return t;
+  Walker w;
+  if (!REV) {
+    if (r.u1 == units) return t;
+    w.seek(&p, nch, r.u1);
+    if (w.first()) return t;
+    const int64_t began = r.u1 - (w.c - w.cs);
+    t.closed = began >= r.u0;
+    t.u0 = t.closed ? began : r.u0;
+  } else {
+    if (r.u0 == 0) return t;
+    w.seek(&p, nch, r.u0);
+    if (w.first()) return t;
+    const int64_t ends = r.u0 + (w.ce - w.c);
+    t.closed = ends <= r.u1;
+    t.u0 = r.u0;
+    t.u1 = t.closed ? ends : r.u1;
+  }
+  return t;
+}
 
 // One chunk's gates, made by one warp for the others.  All exponents are sums of gates of one
 // sign, never differences of running sums, so that the factors are accurate to a few 2^-22
@@ -99,6 +150,7 @@ struct alignas(16) Gate {
   float lp[kChunk];    // log2 of the decay from before the block to token t
   float er[kChunk];    // decay from before the chunk to token t
   float kw[kChunk];    // decay from token s to the end of the chunk
+  float pe[kChunk];    // decay from before the block to token t
   float block[4];      // log2 decay of each block
   float total;         // decay of the chunk
   int row0, n, ht, seq, flags;
@@ -152,6 +204,7 @@ __device__ __forceinline__ void make_gate(Gate& s, const float (&g)[4], int lane
     s.a[t] = exp2_fast(g[b]);
     s.ws[t] = exp2_fast(post[b]);
     s.lp[t] = pre[b];
+    s.pe[t] = exp2_fast(pre[b]);
     s.er[t] = exp2_fast(pre[b] + before);
     s.kw[t] = exp2_fast(post[b] + behind);
   }

@@ -6,6 +6,8 @@
 // Two kernels over the same ranges of units (attn_chunk.cuh):
 //   OUT = false  the state a range hands on: only the chunks since the last start of a sequence
 //   OUT = true   the outputs; a range that starts inside a sequence sums the handed-on states
+// The backward uses the first for the states and, with REV, for their gradients: the chunks
+// from the last to the first, with (q, do) for (k, v) and er for kw.
 //
 // Roles of a CTA's 16 warps: one warp streams tiles by TMA through a ring of 32 KB slots, one
 // thread issues every tcgen05.mma, one warp makes the gates; four warps turn scores into P and
@@ -77,7 +79,7 @@ struct ChunkArgs {
   (wait_phase((bar), static_cast<uint32_t>(parity) & 1u, gave_up, &g_fault_fwd))
 #define CATTN_WARP_WAIT(bar, parity) (__all_sync(0xffffffffu, CATTN_WAIT(bar, parity)))
 
-template <bool OUT>
+template <bool OUT, bool REV>
 __global__ void __launch_bounds__(Layout<OUT>::kThreads, 1)
     cattn_linear_chunk_kernel(const __grid_constant__ ChunkArgs p) {
   using L = Layout<OUT>;
@@ -140,30 +142,20 @@ __global__ void __launch_bounds__(Layout<OUT>::kThreads, 1)
   const int64_t parts = min(static_cast<int64_t>(gridDim.x), units);
   Range range{0, 0};
   if (blockIdx.x < parts) range = range_of(units, parts, blockIdx.x);
-  const int64_t end = range.u1;
-  bool open_end = false;     // the range ends inside a sequence
-  int64_t tail = range.u1;   // that sequence's first unit in this range
-  bool closed = false;       // and the sequence began there
-  if (range.u0 < range.u1 && range.u1 < units) {
-    Walker w;
-    w.seek(&p.plan, nch, range.u1);
-    open_end = !w.first();
-    const int64_t began = range.u1 - (w.c - w.cs);
-    closed = began >= range.u0;
-    tail = open_end ? (closed ? began : range.u0) : range.u1;
-  }
-  if (!OUT) range.u0 = tail;  // nothing else is handed on
+  const Tail tail = tail_of<REV>(p.plan, nch, units, range);
+  if (!OUT) range = Range{tail.u0, tail.u1};  // nothing else is handed on
+  const int64_t count = range.u1 - range.u0, start = REV ? range.u1 - 1 : range.u0;
   const int pk = p.K > kPanelCols ? 2 : 1;
 
-  if (range.u0 < end) {
+  if (count > 0) {
   if (warp == 0) {
     // ---- tiles ----
     if (lane == 0) {
       Walker w;
-      w.seek(&p.plan, nch, range.u0);
+      w.seek(&p.plan, nch, start);
       int tile = 0;
       bool ok = true;
-      for (int64_t u = range.u0; u < end && ok; ++u) {
+      for (int64_t i = 0; i < count && ok; ++i) {
         if (w.rows() > 0) {
           const int hv = w.ht / p.plan.tiles, vt = w.ht % p.plan.tiles;
           const int hk = hv / p.ratio, row = w.row0();
@@ -176,12 +168,12 @@ __global__ void __launch_bounds__(Layout<OUT>::kThreads, 1)
             const int panels = isv ? pv : pk;
             uint8_t* dst = base + L::kRing + slot * kTileBytes;
             cconv::mbar_arrive_expect_tx(&full[slot], panels * kPanelBytes);
-            for (int i = 0; i < panels; ++i)
-              cconv::tma_load_3d(dst + i * kPanelBytes, map, &full[slot],
-                                 (isv ? vt * 128 : 0) + i * kPanelCols, isv ? hv : hk, row);
+            for (int c = 0; c < panels; ++c)
+              cconv::tma_load_3d(dst + c * kPanelBytes, map, &full[slot],
+                                 (isv ? vt * 128 : 0) + c * kPanelCols, isv ? hv : hk, row);
           }
         }
-        if (u + 1 < end) w.next();
+        if (i + 1 < count) w.step<REV>();
       }
       cconv::drain_issued<L::kSlots>(full, tile);
     }
@@ -193,7 +185,7 @@ __global__ void __launch_bounds__(Layout<OUT>::kThreads, 1)
       const uint32_t ring = smem + L::kRing;
       const int ksteps = (p.K + 15) / 16;
       const uint32_t d_scores = mma_desc(128, false, false);
-      for (int64_t u = range.u0; u < end && ok; ++u, ++unit) {
+      for (; unit < count && ok; ++unit) {
         const int gs = unit % kGateStages;
         if (!(ok = CATTN_WAIT(&gfull[gs], unit / kGateStages))) break;
         const Gate& gt = gates[gs];
@@ -275,9 +267,9 @@ __global__ void __launch_bounds__(Layout<OUT>::kThreads, 1)
   } else if (warp == 2) {
     // ---- gates ----
     Walker w;
-    w.seek(&p.plan, nch, range.u0);
-    int unit = 0;
-    for (int64_t u = range.u0; u < end; ++u, ++unit) {
+    w.seek(&p.plan, nch, start);
+    for (int64_t i = 0; i < count; ++i) {
+      const int unit = static_cast<int>(i);
       const int gs = unit % kGateStages, n = w.rows(), row0 = w.row0();
       const int hv = w.ht / p.plan.tiles;
       float g[4];
@@ -293,24 +285,25 @@ __global__ void __launch_bounds__(Layout<OUT>::kThreads, 1)
         gt.ht = w.ht;
         gt.seq = w.seq;
         int f = 0;
-        if (u == range.u0 || w.first()) f |= kSegment;
-        if ((f & kSegment) && !w.first()) f |= kMiddle;
-        if (!w.first() || p.initial) f |= kHasState;
+        const bool first = REV ? w.last() : w.first();
+        if (i == 0 || first) f |= kSegment;
+        if ((f & kSegment) && !first) f |= kMiddle;
+        if (!first || p.initial) f |= kHasState;
         if (w.last() && p.fin && OUT) f |= kFinish;
-        if (OUT ? (!w.last() && u + 1 < end) || (f & kFinish) : true) f |= kNeedKv;
-        if (u >= tail && closed) f |= kSplitSeq;
+        if (OUT ? (!w.last() && i + 1 < count) || (f & kFinish) : true) f |= kNeedKv;
+        if (range.u0 + i >= tail.u0 && tail.closed) f |= kSplitSeq;
         gt.flags = f;
       }
       __syncwarp();
       if (lane == 0) cconv::mbar_arrive(&gfull[gs]);
-      if (u + 1 < end) w.next();
+      if (i + 1 < count) w.step<REV>();
     }
   } else if (OUT && warp >= 4 && warp < 8) {
     // ---- scores to P, and the outputs ----
     const int wq = warp - 4, row = wq * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-    int unit = 0, scs = 0;
-    for (int64_t u = range.u0; u < end; ++u, ++unit) {
+    int scs = 0;
+    for (int unit = 0; unit < count; ++unit) {
       const int gs = unit % kGateStages;
       if (!CATTN_WARP_WAIT(&gfull[gs], unit / kGateStages)) break;
       const Gate& gt = gates[gs];
@@ -419,7 +412,7 @@ __global__ void __launch_bounds__(Layout<OUT>::kThreads, 1)
     float passed = 1.f;  // decay of the chunks so far (what is handed on)
     int tile = 0, unit = 0, kvs = 0, subs = 0, pubs = 0, fixes = 0;
     bool ok = true;
-    for (int64_t u = range.u0; u < end && ok; ++u, ++unit) {
+    for (; unit < count && ok; ++unit) {
       const int gs = unit % kGateStages;
       if (!(ok = CATTN_WARP_WAIT(&gfull[gs], unit / kGateStages))) break;
       const Gate& gt = gates[gs];
@@ -464,7 +457,7 @@ __global__ void __launch_bounds__(Layout<OUT>::kThreads, 1)
             S[4 * i] = x.x, S[4 * i + 1] = x.y, S[4 * i + 2] = x.z, S[4 * i + 3] = x.w;
           }
         }
-        if (!OUT && closed && p.initial && p.fin) {
+        if (!OUT && tail.closed && p.initial && p.fin) {
           // the outputs' kernel reads this copy: by then final_state may have replaced it
           float4* to = reinterpret_cast<float4*>(p.copy + static_cast<int64_t>(blockIdx.x) * kStateFloats);
 #pragma unroll
@@ -507,7 +500,7 @@ __global__ void __launch_bounds__(Layout<OUT>::kThreads, 1)
           for (int b = 0; b < blocks; ++b, ++subs) {
             if (subs >= 2 && !(ok = CATTN_WARP_WAIT(&kpempty[subs & 1], (subs >> 1) - 1))) break;
             const int t = b * kSub + r;
-            const float w = gt.kw[t];
+            const float w = REV ? gt.er[t] : gt.kw[t];
             const uint32_t dst = smem + L::kKp + (subs & 1) * kSubBytes;
             for (int q = 0; q < pk; ++q) {
               uint32_t hi[4], mid[4], lo[4];
@@ -564,7 +557,7 @@ __global__ void __launch_bounds__(Layout<OUT>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         to[(half * 16 + i) * 128 + krow] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
-      if (st == 0) p.decay[blockIdx.x] = closed ? -1.f : passed;
+      if (st == 0) p.decay[blockIdx.x] = tail.closed ? -1.f : passed;
     }
   }
   }
@@ -608,10 +601,10 @@ int encode_tile_map(CUtensorMap* map, const Rows& x, int64_t total, int64_t H, i
   return r == CUDA_SUCCESS ? CCONV_OK : CCONV_ERR_CUDA;
 }
 
-template <bool OUT>
+template <bool OUT, bool REV>
 static int launch(const ChunkArgs& a, int grid, cudaStream_t stream) {
   using L = Layout<OUT>;
-  auto kern = cattn_linear_chunk_kernel<OUT>;
+  auto kern = cattn_linear_chunk_kernel<OUT, REV>;
   if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(kern), L::kBytes) != CCONV_OK)
     return CCONV_ERR_CUDA;
   return launch_pdl(kern, dim3(grid), dim3(L::kThreads), L::kBytes, stream, a) == cudaSuccess
@@ -644,8 +637,10 @@ int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream) {
   a.ratio = c.s.Hv / c.s.Hk;
   a.Hv = c.s.Hv, a.K = c.s.K, a.V = c.s.V;
   a.wide = aligned(c.o, 32) && c.s.V % 16 == 0;
-  rc = launch<false>(a, c.grid, stream);
-  return rc == CCONV_OK ? launch<true>(a, c.grid, stream) : rc;
+  if (c.part == kStates) return launch<false, false>(a, c.grid, stream);
+  if (c.part == kStateGrads) return launch<false, true>(a, c.grid, stream);
+  rc = launch<false, false>(a, c.grid, stream);
+  return rc == CCONV_OK ? launch<true, false>(a, c.grid, stream) : rc;
 }
 
 size_t chunk_fwd_bytes(int grid) {

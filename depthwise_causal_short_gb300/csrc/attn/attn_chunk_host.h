@@ -5,7 +5,12 @@
 
 namespace cattn {
 
+// What launch_chunk_fwd does: the whole forward, or only the states that ranges hand on, or the
+// gradients of states (k and v then hold q and do).
+enum ChunkPart { kForward, kStates, kStateGrads };
+
 struct ChunkCall {
+  ChunkPart part;
   Rows q, k, v;
   Gates g;
   LinearShape s;
@@ -21,6 +26,24 @@ struct ChunkCall {
   int grid;
 };
 
+struct ChunkBwdCall {
+  Rows q, k, v, d_o;
+  Gates g;
+  LinearShape s;  // total > 0
+  const int32_t* cu;
+  const int32_t* cstart;
+  Slots slots;
+  const float* initial;
+  float* dinit;
+  float scale;
+  uint16_t *dq, *dk, *dv;
+  float *part_q, *part_k;   // [Hv * tiles][total][K] on 32-byte boundaries, or NULL: dq and dk
+  float *dots_q, *dots_k;   // [3][Hv * tiles][total]
+  float *carry_s, *carry_d; // what kStates and kStateGrads wrote
+  int grid;
+};
+
+int launch_chunk_bwd(const ChunkBwdCall& c, cudaStream_t stream);
 int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream);
 size_t chunk_fwd_bytes(int grid);
 int encode_tile_map(CUtensorMap* map, const Rows& x, int64_t total, int64_t H, int64_t C);

@@ -1,14 +1,9 @@
 // attn_linear.cu -- linear attention with a decay for each token and head over packed
-// sequences: the entry points and the recurrence.
+// sequences: the entry points, and the sums that finish the backward.
 //
-// One sweep gives all four products: with roles (a, b, c),
-//
-//   M <- e^{g} M + b_t c_t^T,   out_t = M^T a_t        M: [A, C], A = |a| = |b|, C = |c|
-//
-//   o  : a = q,  b = k,  c = v   forwards   (M = S)
-//   dq : a = do, b = v,  c = k   forwards   (M = S^T)
-//   dk : a = v,  b = do, c = q   backwards  (M = D^T)
-//   dv : a = k,  b = q,  c = do  backwards  (M = D)
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T,  o_t = scale q_t^T S_t
+//   D_t = scale q_t do_t^T + e^{g_{t+1}} D_{t+1}
+//   dq_t = scale S_t do_t,  dk_t = D_t v_t,  dv_t = D_t^T k_t
 //
 // and dg_t = sum over i >= t of (q_i . dq'_i - k_i . dk'_i), where dq' and dk' leave out the
 // token's own product with itself: a change of g_t moves every pair (i, j) with j < t <= i,
@@ -19,169 +14,42 @@
 
 namespace cattn {
 
-using cconv::bf16_to_f32;
-
-constexpr int kCols = 32;   // columns of M in one CTA (one a lane)
-constexpr int kWarps = 4;   // rows of M are dealt out to the warps
-constexpr int kTile = 16;   // tokens staged at once
 constexpr int64_t kMaxSeqs = int64_t(1) << 30;
 
-struct SweepArgs {
-  Rows a, b, c;
-  Gates g;
-  int ha, hb, hc;        // heads of a, b, c (value heads map onto them)
-  int A, C;
-  LinearShape s;
-  const int32_t* cu;
-  Slots slots;
-  const float* m0;       // [S, Hv, K, V] or NULL
-  float* m1;             // written at the end of each sequence, or NULL
-  const int32_t* status; // states are written only if status is NULL or [0] == CCONV_OK
-  bool m1_slots;         // m1's slot is the sequence's state slot (else the sequence)
-  bool transposed;       // M is S^T: m0 and m1 are [C, A] in memory
-  float m1_scale;
-  float scale;
-  uint16_t* out;         // [total, Hv, C] bf16, or
-  float* out32;          // the same in fp32, and
-  Rows x;                // with it the dots of x (c's heads) and out without the token's own
-  float* dots;           // product, of this CTA's columns: [slice, total, Hv]
-};
-
-// One CTA: one sequence, one value head, kCols columns.
-template <int ROWS, bool REVERSE>
-__global__ void __launch_bounds__(kWarps * 32) cattn_linear_sweep_kernel(SweepArgs p) {
-  cconv::grid_dependency_wait();
-  cconv::grid_launch_dependents();
-  __shared__ float sa[kTile][kWarps * ROWS], sb[kTile][kWarps * ROWS];
-  __shared__ float part[kTile][kWarps][kCols], own[kTile][kWarps];
-  __shared__ float decay[kTile];
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int slices = (p.C + kCols - 1) / kCols;
-  const int64_t cta = blockIdx.x;
-  const int slice = static_cast<int>(cta % slices);
-  const int h = static_cast<int>(cta / slices % p.s.Hv);
-  const int seq = static_cast<int>(cta / slices / p.s.Hv);
-  const int col = slice * kCols + lane;
-  const bool on = col < p.C;
-  int t0, t1;
-  sequence_rows(p.cu, seq, p.s.total, t0, t1);
-  const int ha = h / (p.s.Hv / p.ha), hb = h / (p.s.Hv / p.hb), hc = h / (p.s.Hv / p.hc);
-  const int64_t slot = p.slots.of(seq);
-  const int64_t head = static_cast<int64_t>(p.A) * p.C;
-
-  float m[ROWS];
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    const int row = warp * ROWS + r;
-    m[r] = 0.f;
-    if (p.m0 && slot >= 0 && on && row < p.A) {
-      const int64_t at = p.transposed ? static_cast<int64_t>(col) * p.A + row
-                                      : static_cast<int64_t>(row) * p.C + col;
-      m[r] = p.m0[(slot * p.s.Hv + h) * head + at];
-    }
-  }
-  float next = 0.f;  // backwards: the gate of the token after the current one
-  const int n = t1 - t0;
-  for (int base = 0; base < n; base += kTile) {
-    const int count = min(kTile, n - base);
-    __syncthreads();
-    for (int e = threadIdx.x; e < count * p.A; e += kWarps * 32) {
-      const int i = e / p.A, r = e % p.A;
-      const int64_t t = REVERSE ? t1 - 1 - (base + i) : t0 + base + i;
-      sa[i][r] = bf16_to_f32(p.a.p[t * p.a.st + ha * p.a.sh + r]);
-      sb[i][r] = bf16_to_f32(p.b.p[t * p.b.st + hb * p.b.sh + r]);
-    }
-    if (threadIdx.x < count) {
-      const int64_t t = REVERSE ? t1 - 1 - (base + threadIdx.x) : t0 + base + threadIdx.x;
-      if (REVERSE)
-        decay[threadIdx.x] = t + 1 < t1 ? expf(p.g.at(t + 1, h)) : 0.f;
-      else
-        decay[threadIdx.x] = expf(p.g.at(t, h));
-    }
-    __syncthreads();
-    for (int i = 0; i < count; ++i) {
-      const int64_t t = REVERSE ? t1 - 1 - (base + i) : t0 + base + i;
-      const float c = on ? bf16_to_f32(p.c.p[t * p.c.st + hc * p.c.sh + col]) : 0.f;
-      const float d = decay[i];
-      float acc = 0.f, ab = 0.f;
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        if (warp * ROWS + r < p.A) {
-          const float av = sa[i][warp * ROWS + r], bv = sb[i][warp * ROWS + r];
-          m[r] *= d;
-          acc = fmaf(av, m[r], acc);
-          ab = fmaf(av, bv, ab);
-          m[r] = fmaf(bv, c, m[r]);
-        }
-      }
-      part[i][warp][lane] = acc;
-      if (lane == 0) own[i][warp] = ab;
-    }
-    __syncthreads();
-    for (int i = warp; i < count; i += kWarps) {
-      const int64_t t = REVERSE ? t1 - 1 - (base + i) : t0 + base + i;
-      float y = 0.f, ab = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        y += part[i][w][lane];
-        ab += own[i][w];
-      }
-      if (p.dots) {
-        float dot = on ? y * bf16_to_f32(p.x.p[t * p.x.st + hc * p.x.sh + col]) : 0.f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0)
-          p.dots[(static_cast<int64_t>(slice) * p.s.total + t) * p.s.Hv + h] = p.scale * dot;
-      }
-      if (on) y = fmaf(ab, bf16_to_f32(p.c.p[t * p.c.st + hc * p.c.sh + col]), y);
-      y *= p.scale;
-      if (on) {
-        const int64_t at = (t * p.s.Hv + h) * p.C + col;
-        if (p.out)
-          p.out[at] = cconv::f32_to_bf16(y);
-        else
-          p.out32[at] = y;
-      }
-    }
-  }
-  if (!p.m1 || (p.status && p.status[0] != CCONV_OK)) return;
-  if (REVERSE) next = n > 0 ? expf(p.g.at(t0, h)) : 0.f;
-  const int64_t to = p.m1_slots ? slot : seq;
-  if (to < 0) return;
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    const int row = warp * ROWS + r;
-    if (on && row < p.A) {
-      const int64_t at = p.transposed ? static_cast<int64_t>(col) * p.A + row
-                                      : static_cast<int64_t>(row) * p.C + col;
-      p.m1[(to * p.s.Hv + h) * head + at] = (REVERSE ? next * p.m1_scale : p.m1_scale) * m[r];
-    }
-  }
-}
-
-// Sums the value heads of each query / key head: dst[t, hk, :] = sum over h of src[t, h, :].
-// One warp for each (t, hk).
+// dst[t, hk, :] = sum over the (value head, column tile) parts of key head hk, in their order.
+// A thread takes 8 channels of one row; bound by memory (4 bytes a part, 2 out).
 __global__ void __launch_bounds__(256)
-    cattn_linear_heads_kernel(const float* src, LinearShape s, uint16_t* dst) {
+    cattn_linear_heads_kernel(const float* part, int total, int Hk, int K, int parts, uint16_t* dst) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
-  const int lane = threadIdx.x % 32;
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / 32;
-  if (w >= static_cast<int64_t>(s.total) * s.Hk) return;
-  const int64_t t = w / s.Hk;
-  const int hk = static_cast<int>(w % s.Hk), r = s.Hv / s.Hk;
-  for (int c = lane; c < s.K; c += 32) {
-    float sum = 0.f;
-    for (int i = 0; i < r; ++i) sum += src[(t * s.Hv + static_cast<int64_t>(hk) * r + i) * s.K + c];
-    dst[(t * s.Hk + hk) * s.K + c] = cconv::f32_to_bf16(sum);
+  const int pieces = K / 8;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i >= static_cast<int64_t>(total) * Hk * pieces) return;
+  const int piece = static_cast<int>(i % pieces);
+  const int hk = static_cast<int>(i / pieces % Hk);
+  const int64_t t = i / pieces / Hk;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll 4
+  for (int j = 0; j < parts; ++j) {
+    const float4* src = reinterpret_cast<const float4*>(
+        part + ((static_cast<int64_t>(hk) * parts + j) * total + t) * K + piece * 8);
+    const float4 x = __ldcs(src), y = __ldcs(src + 1);
+    a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+    b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
   }
+  using cconv::f2_pack;
+  using cconv::f2_to_bf16x2;
+  *reinterpret_cast<uint4*>(dst + (t * Hk + hk) * K + piece * 8) =
+      make_uint4(f2_to_bf16x2(f2_pack(a.x, a.y)), f2_to_bf16x2(f2_pack(a.z, a.w)),
+                 f2_to_bf16x2(f2_pack(b.x, b.y)), f2_to_bf16x2(f2_pack(b.z, b.w)));
 }
 
-// dg_t = sum over i >= t of its sequence of (qdot_i - kdot_i).  One warp for each sequence and
-// value head, walking from the last token in steps of 32.
+// dg_t = sum over i >= t of its sequence of (qdot_i - kdot_i), each the sum of `slices` times
+// `tiles` parts.  One warp for each sequence and value head, walking from the last token in
+// steps of 32.
 __global__ void __launch_bounds__(128)
-    cattn_linear_dg_kernel(const float* qdot, const float* kdot, int slices, LinearShape s,
-                           const int32_t* cu, float* dg) {
+    cattn_linear_dg_kernel(const float* qdot, const float* kdot, int slices, int tiles,
+                           LinearShape s, const int32_t* cu, float* dg) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
   const int lane = threadIdx.x % 32;
@@ -190,21 +58,24 @@ __global__ void __launch_bounds__(128)
   const int seq = static_cast<int>(w / s.Hv), h = static_cast<int>(w % s.Hv);
   int t0, t1;
   sequence_rows(cu, seq, s.total, t0, t1);
-  const int64_t pitch = static_cast<int64_t>(s.total) * s.Hv;
+  const int64_t slice = static_cast<int64_t>(s.Hv) * tiles * s.total;
   float carry = 0.f;
   for (int hi = t1; hi > t0; hi -= 32) {
     const int t = hi - 1 - lane;
-    const int64_t at = static_cast<int64_t>(t) * s.Hv + h;
     float x = 0.f;
     if (t >= t0)
-      for (int i = 0; i < slices; ++i) x += qdot[i * pitch + at] - kdot[i * pitch + at];
+      for (int i = 0; i < slices; ++i)
+        for (int j = 0; j < tiles; ++j) {
+          const int64_t at = i * slice + (static_cast<int64_t>(h) * tiles + j) * s.total + t;
+          x += qdot[at] - kdot[at];
+        }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const float y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
     x += carry;
-    if (t >= t0) dg[at] = x;
+    if (t >= t0) dg[static_cast<int64_t>(t) * s.Hv + h] = x;
     carry = __shfl_sync(0xffffffffu, x, 31);
   }
 }
@@ -248,21 +119,6 @@ static int check_states(const int32_t* cu, int64_t nseq, const float* initial, c
   return aligned(initial, 16) && aligned(fin, 16) ? CCONV_OK : CCONV_ERR_ALIGN;
 }
 
-static int launch_sweep(const SweepArgs& p, bool reverse, cudaStream_t stream) {
-  const int64_t slices = (p.C + kCols - 1) / kCols;
-  const int64_t ctas = slices * p.s.Hv * p.s.nseq;
-  if (ctas > (int64_t(1) << 31) - 1) return CCONV_ERR_SHAPE;
-  const dim3 grid(static_cast<unsigned>(ctas)), block(kWarps * 32);
-  cudaError_t e;
-  if (p.A <= 128)
-    e = reverse ? launch_pdl(cattn_linear_sweep_kernel<32, true>, grid, block, 0, stream, p)
-                : launch_pdl(cattn_linear_sweep_kernel<32, false>, grid, block, 0, stream, p);
-  else
-    e = reverse ? launch_pdl(cattn_linear_sweep_kernel<64, true>, grid, block, 0, stream, p)
-                : launch_pdl(cattn_linear_sweep_kernel<64, false>, grid, block, 0, stream, p);
-  return e == cudaSuccess ? CCONV_OK : CCONV_ERR_CUDA;
-}
-
 static LinearShape shape_of(int64_t total, int64_t Hk, int64_t Hv, int64_t K, int64_t V,
                             int64_t nseq) {
   return LinearShape{static_cast<int>(total), static_cast<int>(Hk), static_cast<int>(Hv),
@@ -271,13 +127,6 @@ static LinearShape shape_of(int64_t total, int64_t Hk, int64_t Hv, int64_t K, in
 
 static Rows rows(const void* p, int64_t st, int64_t sh) {
   return Rows{static_cast<const uint16_t*>(p), st, sh};
-}
-
-static int64_t slices_of(int64_t C) { return (C + kCols - 1) / kCols; }
-
-// Workspace of the backward: dq and dk of each value head, and their dots with q and k.
-static size_t bwd_bytes(int64_t total, int64_t Hv, int64_t K) {
-  return static_cast<size_t>(total) * Hv * (2 * K + 2 * slices_of(K)) * 4;
 }
 
 // CTAs of the chunked kernels: one per SM, or one per unit where there can be no more units.
@@ -294,6 +143,34 @@ static int chunk_grid(int64_t total, int64_t nseq, int64_t Hv, int64_t V, int* g
 
 // The chunk offsets at the head of the workspace.
 static size_t offsets_bytes(int64_t nseq) { return (static_cast<size_t>(nseq + 1) * 4 + 15) / 16 * 16; }
+
+constexpr int kSlices = 3;  // parts of a unit's dots
+
+// What a backward call keeps in its workspace, from a 256-byte boundary.
+struct BwdWork {
+  size_t offsets, carry_s, carry_d, dots_q, dots_k, part_q, part_k, bytes;
+};
+static BwdWork bwd_work(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv, int64_t K, int64_t V,
+                        int grid) {
+  const size_t tiles = static_cast<size_t>((V + 127) / 128), heads = static_cast<size_t>(Hv) * tiles;
+  const bool parts = heads > static_cast<size_t>(Hk);
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t r = at;
+    at += (n + 255) / 256 * 256;
+    return r;
+  };
+  BwdWork w{};
+  w.offsets = take(offsets_bytes(nseq));
+  w.carry_s = take(chunk_fwd_bytes(grid));
+  w.carry_d = take(chunk_fwd_bytes(grid));
+  w.dots_q = take(kSlices * heads * static_cast<size_t>(total) * 4);
+  w.dots_k = take(kSlices * heads * static_cast<size_t>(total) * 4);
+  w.part_q = take(parts ? heads * static_cast<size_t>(total) * K * 4 : 0);
+  w.part_k = take(parts ? heads * static_cast<size_t>(total) * K * 4 : 0);
+  w.bytes = at + 256;
+  return w;
+}
 
 static int check_sizes(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv, int64_t K, int64_t V) {
   if (total < 0 || total > kMaxRows || nseq < 1 || nseq > kMaxSeqs || Hk < 1 ||
@@ -323,8 +200,11 @@ extern "C" CCONV_API int cattn_linear_bwd_workspace_bytes(int64_t total, int64_t
   using namespace cattn;
   if (!bytes) return CCONV_ERR_NULL;
   const int rc = check_sizes(total, nseq, Hk, Hv, K, V);
-  if (rc == CCONV_OK) *bytes = bwd_bytes(total, Hv, K);
-  return rc;
+  int grid = 0;
+  if (rc != CCONV_OK) return rc;
+  if (chunk_grid(total, nseq, Hv, V, &grid) != CCONV_OK) return CCONV_ERR_CUDA;
+  *bytes = bwd_work(total, nseq, Hk, Hv, K, V, grid).bytes;
+  return CCONV_OK;
 }
 
 extern "C" CCONV_API int cattn_linear_fwd(
@@ -375,66 +255,81 @@ extern "C" CCONV_API int cattn_linear_bwd(
     rc = check_states(cu_seqlens, nseq, initial_state, nullptr, state_indices, S, status_dev);
   if (rc != CCONV_OK) return rc;
   if (!aligned(d_initial_state, 16)) return CCONV_ERR_ALIGN;
+  int grid = 0;
+  if (chunk_grid(total, nseq, Hv, V, &grid) != CCONV_OK) return CCONV_ERR_CUDA;
+  const BwdWork w = bwd_work(total, nseq, Hk, Hv, K, V, grid);
   if (total > 0) {
     if (!do_ || !dq || !dk || !dg) return CCONV_ERR_NULL;
     rc = check_rows(do_, total, Hv, sot, soh);
     if (rc != CCONV_OK) return rc;
     if (!aligned(dq, 16) || !aligned(dk, 16) || !aligned(dg, 16)) return CCONV_ERR_ALIGN;
-    if (!workspace || workspace_bytes < bwd_bytes(total, Hv, K)) return CCONV_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < w.bytes) return CCONV_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return CCONV_ERR_ALIGN;
   }
-  rc = launch_checks(state_indices, nseq, S, 0, status_dev, cu_seqlens, nseq, total, nullptr,
-                     stream);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(workspace) + 255) & ~static_cast<uintptr_t>(255));
+  int32_t* cstart = total > 0 ? reinterpret_cast<int32_t*>(ws + w.offsets) : nullptr;
+  rc = launch_checks(state_indices, nseq, S, 0, status_dev, cu_seqlens, nseq, total, cstart, stream);
+  if (rc != CCONV_OK) return rc;
+  if (total == 0) {
+    if (d_initial_state && !cconv::recording_launches() &&
+        report_cuda("cudaMemsetAsync",
+                    cudaMemsetAsync(d_initial_state, 0, static_cast<size_t>(nseq) * Hv * K * V * 4,
+                                    stream)) != cudaSuccess)
+      return CCONV_ERR_CUDA;
+    return CCONV_OK;
+  }
+
+  ChunkCall states{};
+  states.part = kStates;
+  states.q = rows(q, sqt, sqh), states.k = rows(k, skt, skh), states.v = rows(v, svt, svh);
+  states.g = Gates{g, sgt, sgh};
+  states.s = shape_of(total, Hk, Hv, K, V, nseq);
+  states.cu = cu_seqlens, states.cstart = cstart;
+  states.slots = Slots{state_indices, S};
+  states.initial = initial_state;
+  states.grid = grid;
+  states.carry = reinterpret_cast<float*>(ws + w.carry_s);
+  rc = launch_chunk_fwd(states, stream);
+  if (rc != CCONV_OK) return rc;
+  ChunkCall grads = states;
+  grads.part = kStateGrads;
+  grads.k = states.q, grads.v = rows(do_, sot, soh);
+  grads.initial = nullptr;
+  grads.carry = reinterpret_cast<float*>(ws + w.carry_d);
+  rc = launch_chunk_fwd(grads, stream);
   if (rc != CCONV_OK) return rc;
 
-  const Rows rq = rows(q, sqt, sqh), rk = rows(k, skt, skh), rv = rows(v, svt, svh),
-             ro = rows(do_, sot, soh);
-  float* part_q = static_cast<float*>(workspace);
-  float* part_k = part_q + total * Hv * K;
-  float* qdot = part_k + total * Hv * K;
-  float* kdot = qdot + total * Hv * slices_of(K);
-  SweepArgs base{};
-  base.g = Gates{g, sgt, sgh};
-  base.s = shape_of(total, Hk, Hv, K, V, nseq);
-  base.cu = cu_seqlens;
-  base.slots = Slots{state_indices, S};
-  base.scale = scale;
-  const int hk = base.s.Hk, hv = base.s.Hv;
-
-  SweepArgs p = base;  // dq
-  p.a = ro, p.ha = hv, p.b = rv, p.hb = hv, p.c = rk, p.hc = hk;
-  p.A = base.s.V, p.C = base.s.K;
-  p.m0 = initial_state, p.transposed = true;
-  p.out32 = part_q, p.x = rq, p.dots = qdot;
-  rc = launch_sweep(p, false, stream);
+  ChunkBwdCall c{};
+  c.q = states.q, c.k = states.k, c.v = states.v, c.d_o = grads.v;
+  c.g = states.g, c.s = states.s, c.cu = cu_seqlens, c.cstart = cstart, c.slots = states.slots;
+  c.initial = initial_state, c.dinit = d_initial_state, c.scale = scale;
+  c.dq = static_cast<uint16_t*>(dq), c.dk = static_cast<uint16_t*>(dk);
+  c.dv = static_cast<uint16_t*>(dv);
+  const int tiles = static_cast<int>((V + 127) / 128), parts = static_cast<int>(Hv / Hk) * tiles;
+  if (parts > 1) {
+    c.part_q = reinterpret_cast<float*>(ws + w.part_q);
+    c.part_k = reinterpret_cast<float*>(ws + w.part_k);
+  }
+  c.dots_q = reinterpret_cast<float*>(ws + w.dots_q);
+  c.dots_k = reinterpret_cast<float*>(ws + w.dots_k);
+  c.carry_s = states.carry, c.carry_d = grads.carry;
+  c.grid = grid;
+  rc = launch_chunk_bwd(c, stream);
   if (rc != CCONV_OK) return rc;
 
-  p = base;  // dk
-  p.a = rv, p.ha = hv, p.b = ro, p.hb = hv, p.c = rq, p.hc = hk;
-  p.A = base.s.V, p.C = base.s.K;
-  p.out32 = part_k, p.x = rk, p.dots = kdot;
-  rc = launch_sweep(p, true, stream);
-  if (rc != CCONV_OK) return rc;
-
-  p = base;  // dv, and the gradient of the initial states
-  p.a = rk, p.ha = hk, p.b = rq, p.hb = hk, p.c = ro, p.hc = hv;
-  p.A = base.s.K, p.C = base.s.V;
-  p.out = static_cast<uint16_t*>(dv);
-  p.m1 = d_initial_state, p.m1_scale = scale;
-  rc = launch_sweep(p, true, stream);
-  if (rc != CCONV_OK || total == 0) return rc;
-
-  const unsigned warps = static_cast<unsigned>((total * Hk + 7) / 8);
+  if (parts > 1) {
+    const unsigned ctas = static_cast<unsigned>((total * Hk * (K / 8) + 255) / 256);
+    for (int side = 0; side < 2; ++side)
+      if (launch_pdl(cattn_linear_heads_kernel, dim3(ctas), dim3(256), 0, stream,
+                     static_cast<const float*>(side ? c.part_k : c.part_q), c.s.total, c.s.Hk, c.s.K,
+                     parts, side ? c.dk : c.dq) != cudaSuccess)
+        return CCONV_ERR_CUDA;
+  }
   const unsigned lines = static_cast<unsigned>((nseq * Hv + 3) / 4);
-  if (launch_pdl(cattn_linear_heads_kernel, dim3(warps), dim3(256), 0, stream,
-                 static_cast<const float*>(part_q), base.s, static_cast<uint16_t*>(dq)) !=
-          cudaSuccess ||
-      launch_pdl(cattn_linear_heads_kernel, dim3(warps), dim3(256), 0, stream,
-                 static_cast<const float*>(part_k), base.s, static_cast<uint16_t*>(dk)) !=
-          cudaSuccess ||
-      launch_pdl(cattn_linear_dg_kernel, dim3(lines), dim3(128), 0, stream,
-                 static_cast<const float*>(qdot), static_cast<const float*>(kdot),
-                 static_cast<int>(slices_of(K)), base.s, cu_seqlens, dg) != cudaSuccess)
-    return CCONV_ERR_CUDA;
-  return CCONV_OK;
+  return launch_pdl(cattn_linear_dg_kernel, dim3(lines), dim3(128), 0, stream,
+                    static_cast<const float*>(c.dots_q), static_cast<const float*>(c.dots_k),
+                    kSlices, tiles, c.s, cu_seqlens, dg) == cudaSuccess
+             ? CCONV_OK
+             : CCONV_ERR_CUDA;
 }
