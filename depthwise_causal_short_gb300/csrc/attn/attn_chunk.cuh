@@ -20,6 +20,13 @@ constexpr int kSubPanel = kSub * 128;          // bytes of a block's 64-column p
 constexpr int kSubTile = 2 * kSubPanel;
 constexpr int kSubBytes = kSplit * kSubTile;
 constexpr int kGateStages = 3;
+constexpr int kRowStep = 16 * 128 / 16;        // descriptor units (16 bytes) of 16 tile rows
+
+// Descriptor offset of 16 columns' step j of a tile (columns as the contraction).
+__device__ __forceinline__ uint64_t col_step(int j) {
+  return static_cast<uint64_t>((j >> 2) * (kPanelBytes / 16) + (j & 3) * 2);
+}
+
 constexpr int kStateFloats = 128 * 128;        // a state in the workspace
 
 // Chunk offsets of the sequences: cstart[nseq + 1], an empty sequence has one (empty) chunk.
@@ -164,68 +171,102 @@ enum GateFlags : int {
   kSplitSeq = 32, // this sequence began in this range and goes on in the next
 };
 
-__device__ __forceinline__ float shfl_scan_up(float x, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const float y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  return x;
-}
-__device__ __forceinline__ float shfl_scan_down(float x, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const float y = __shfl_down_sync(0xffffffffu, x, o);
-    if (lane + o < 32) x += y;
-  }
-  return x;
+using cconv::f2;
+using cconv::f2_add;
+using cconv::f2_fma;
+using cconv::f2_mul;
+using cconv::f2_pack;
+using cconv::f2_splat;
+using cconv::f2_to_bf16x2;
+using cconv::bf16x2_to_f2;
+
+__device__ __forceinline__ f2 pair(const uint32_t* x, int i) {
+  return f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// g: the log2 decays of tokens 4 lane .. 4 lane + 3; a block of 32 tokens is 8 lanes.
 __device__ __forceinline__ void make_gate(Gate& s, const float (&g)[4], int lane) {
-  float pre[4], post[4], tot[4];
+  const float own = (g[0] + g[1]) + (g[2] + g[3]);
+  // sums over the block's lanes before and after this one, and over the chunk's blocks
+  float before = 0.f, after = 0.f, up = own, down = own;
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    const float x = __shfl_up_sync(0xffffffffu, up, o, 8), y = __shfl_down_sync(0xffffffffu, down, o, 8);
+    if ((lane & 7) >= o) up += x;
+    if ((lane & 7) + o < 8) down += y;
+  }
+  const float x = __shfl_up_sync(0xffffffffu, up, 1, 8), y = __shfl_down_sync(0xffffffffu, down, 1, 8);
+  if ((lane & 7) > 0) before = x;
+  if ((lane & 7) < 7) after = y;
+  float head = 0.f, rest = 0.f, all = 0.f;
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
-    pre[b] = shfl_scan_up(g[b], lane);
-    const float after = __shfl_down_sync(0xffffffffu, g[b], 1);
-    post[b] = shfl_scan_down(lane == 31 ? 0.f : after, lane);
-    tot[b] = __shfl_sync(0xffffffffu, pre[b], 31);
+    const float t = __shfl_sync(0xffffffffu, down, 8 * b);
+    if (b < lane / 8) head += t;
+    if (b > lane / 8) rest += t;
+    all += t;
+    if (lane == 0) s.block[b] = t;
   }
+  float pre[4], post[4];
+  pre[0] = before + g[0], pre[1] = pre[0] + g[1], pre[2] = pre[1] + g[2], pre[3] = pre[2] + g[3];
+  post[3] = after, post[2] = after + g[3], post[1] = post[2] + g[2], post[0] = post[1] + g[1];
+  float v[6][4];
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    float before = 0.f, behind = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i < b) before += tot[i];
-      if (i > b) behind += tot[i];
-    }
-    const int t = 32 * b + lane;
-    s.a[t] = exp2_fast(g[b]);
-    s.ws[t] = exp2_fast(post[b]);
-    s.lp[t] = pre[b];
-    s.pe[t] = exp2_fast(pre[b]);
-    s.er[t] = exp2_fast(pre[b] + before);
-    s.kw[t] = exp2_fast(post[b] + behind);
+  for (int j = 0; j < 4; ++j) {
+    v[0][j] = exp2_fast(g[j]);
+    v[1][j] = exp2_fast(post[j]);
+    v[2][j] = pre[j];
+    v[3][j] = exp2_fast(head + pre[j]);
+    v[4][j] = exp2_fast(post[j] + rest);
+    v[5][j] = exp2_fast(pre[j]);
   }
-  if (lane < 4) s.block[lane] = lane == 0 ? tot[0] : lane == 1 ? tot[1] : lane == 2 ? tot[2] : tot[3];
-  if (lane == 0) s.total = exp2_fast(tot[0] + tot[1] + tot[2] + tot[3]);
+  float* rows = s.a;  // a, ws, lp, er, kw, pe follow one another
+#pragma unroll
+  for (int i = 0; i < 6; ++i)
+    *reinterpret_cast<float4*>(rows + i * kChunk + 4 * lane) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+  if (lane == 0) s.total = exp2_fast(all);
 }
 
-// Waits for a phase of `bar`, at most kWaitLimitNs; gives up at once where another role of the
-// CTA has.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* gave_up,
-                                           unsigned* fault) {
-  if (cconv::mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = cconv::global_timer_ns();
-  for (uint32_t n = 1;; ++n) {
-    if (cconv::mbar_try_wait(bar, parity)) return true;
-    if ((n & 63u) == 0 && (*gave_up || cconv::global_timer_ns() - t0 > cconv::kWaitLimitNs)) {
-      *gave_up = 1;
-      atomicOr(fault, kFaultWait);
-      return false;
-    }
+// Tries of one wait: some tenths of a second at least, against waits of microseconds.
+constexpr int kWaitTries = 1 << 22;
+
+// The loads of a tile slot must have landed before a CTA's shared memory goes: waits for the last
+// of `uses` phases of `full`, with a limit.
+__device__ __forceinline__ void drain(uint32_t full, int uses) {
+#pragma unroll 1
+  for (int n = kWaitTries / 16; uses > 0 && n != 0; --n)
+    if (bar_try(full, static_cast<uint32_t>(uses - 1) & 1u)) return;
+}
+
+// Waits for a phase of `bar`; false when it gives up (then the role ends, and the roles that wait
+// for it give up in their turn).  Kept short: it is inlined at every wait, and the kernels' loops
+// have to fit the instruction cache.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (int n = kWaitTries; n != 0; --n)
+    if (bar_try(bar, parity)) return true;
+  return false;
+}
+
+// How the roles of a kernel meet: an mbarrier wait tells an odd phase from an even one only, so
+// a role (1) waits for every phase of a barrier that it uses, in order, needed or not, and (2)
+// holds back the phase after the one it waits for (whoever waits for a tile also gives it back).
+// Where a role follows another that it does not hold back, it follows a counter:
+
+__device__ __forceinline__ void set_count(uint32_t at, int value) {
+  asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(at), "r"(value) : "memory");
+}
+// Waits until the count reaches `value`; false when it gives up.
+__device__ __forceinline__ bool wait_count(uint32_t at, int value) {
+#pragma unroll 1
+  for (int n = kWaitTries; n != 0; --n) {
+    int now;
+    asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(now) : "r"(at) : "memory");
+    if (now >= value) return true;
   }
+  return false;
 }
 
 // Zeroes rows [n, 128) of a tile: rows of the next sequence must not meet a matrix product,
@@ -238,21 +279,51 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int panels, int n, int 
   }
 }
 
-// x rounded to bf16 three times: x = hi + mid + lo to 24 bits.  Eight values at a time.
-__device__ __forceinline__ void split3(const float* x, uint32_t* hi, uint32_t* mid, uint32_t* lo) {
+// S (a row of 64 pairs) to the workspace, 16 bytes a lane side by side.
+__device__ __forceinline__ void put_state(const f2* S, float* dst, int row) {
+  ulonglong2* to = reinterpret_cast<ulonglong2*>(dst);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) to[i * 128 + row] = make_ulonglong2(S[2 * i], S[2 * i + 1]);
+}
+
+// Adds up what the ranges next to range `at` hand on (by = -1: those before it, 1: after it), to
+// the one where the sequence starts (ends).
+__device__ __forceinline__ void gather_state(f2* S, const float* carry, const float* decay,
+                                             int64_t at, int64_t parts, int by, int row) {
+  float coef = 1.f;
+  for (int64_t j = at + by; j >= 0 && j < parts; j += by) {
+    const ulonglong2* src = reinterpret_cast<const ulonglong2*>(carry + j * kStateFloats);
+    const float d = decay[j];
+    const f2 c = f2_splat(coef);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const ulonglong2 x = src[i * 128 + row];
+      S[2 * i] = f2_fma(c, x.x, S[2 * i]);
+      S[2 * i + 1] = f2_fma(c, x.y, S[2 * i + 1]);
+    }
+    if (d < 0.f) break;
+    coef *= d;
+    if (coef == 0.f) break;
+  }
+}
+
+// Eight bf16 values times w, each rounded to bf16 three times: x = hi + mid + lo to 24 bits.
+// The three terms of 16 bytes go to `at`, at + step and at + 2 step.
+__device__ __forceinline__ void store_split(const uint4& in, float w, uint32_t at, uint32_t step) {
+  const uint32_t word[4] = {in.x, in.y, in.z, in.w};
+  const f2 w2 = f2_splat(w), minus = f2_splat(-1.f);
+  uint32_t t[3][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float a = x[2 * i], b = x[2 * i + 1];
-    const uint32_t h = pack_bf16(a, b);
-    a -= __uint_as_float(h << 16);
-    b -= __uint_as_float(h & 0xffff0000u);
-    const uint32_t m = pack_bf16(a, b);
-    a -= __uint_as_float(m << 16);
-    b -= __uint_as_float(m & 0xffff0000u);
-    hi[i] = h;
-    mid[i] = m;
-    lo[i] = pack_bf16(a, b);
+    f2 x = f2_mul(bf16x2_to_f2(word[i]), w2);
+    t[0][i] = f2_to_bf16x2(x);
+    x = f2_fma(bf16x2_to_f2(t[0][i]), minus, x);
+    t[1][i] = f2_to_bf16x2(x);
+    x = f2_fma(bf16x2_to_f2(t[1][i]), minus, x);
+    t[2][i] = f2_to_bf16x2(x);
   }
+#pragma unroll
+  for (int s = 0; s < kSplit; ++s) sts128(at + s * step, t[s][0], t[s][1], t[s][2], t[s][3]);
 }
 
 }  // namespace cattn

@@ -17,13 +17,20 @@
 // chunks scale * er * q . (dO S^T) and scale * kw * k . (V D^T), for which S and D are read as
 // two bf16 terms (16 bits).
 //
-// Roles of the 16 warps are the forward's: tiles, matrix products, gates; four warps turn the
-// score tiles into P, eight keep the state and finish the outputs.  The ring's four slots hold
-// one tile each of v, do, k and q, refilled as soon as its last reader is done.  TMEM:
-//   KV = false  [0,128) M1, then P   [128,256) M2, then P K   [256,384) dO S^T   [384,512) K^T V
+// Roles of the 20 warps: one warp streams tiles, one thread issues the products of the outputs
+// and one those of the state, one warp makes the gates; four warps each turn score tiles into P,
+// make decayed rows, keep the state, and finish the outputs.  The ring's four slots hold one
+// tile each of v, do, k and q, refilled as soon as its last reader is done.  TMEM:
+//   KV = false  [0,128) M1, then P   [128,256) M2   [256,384) dq   [384,512) K^T V
 //   KV = true   [0,128) M1, then P1 | Q^T dO (columns 0-63)   [128,256) M2, then P2 | Q^T dO (64-)
-//               [256,384) dk         [384,512) dv: V D^T and K D are scaled in place, P Q and
-//               P dO accumulate on them
+//               [256,384) dk         [384,512) dv
+// The products with the state are scaled in place by their rows' decays, and P's products
+// accumulate on them.  Finished tiles leave by TMA through the buffer of the bf16 state, as the
+// forward's outputs do.
+//
+// Bound by shared memory: the tensor cores read both operands of every product there (64 cycles
+// of 128 bytes for 128 x 128 x 16), some 5500 cycles a chunk, and the warps' accesses and TMEM
+// loads add as much again.
 #include "attn_chunk.cuh"
 #include "attn_chunk_host.h"
 
@@ -41,9 +48,9 @@ static int read_fault(unsigned* out) {
 }
 static FaultReader reader(read_fault);
 
-constexpr int kStateWarps = 8;
-constexpr int kBwdThreads = 512;
+constexpr int kBwdThreads = 640;
 constexpr int kBwdGates = 2;
+constexpr int kBwdReaders = 4 * 4 + 2;            // warps and threads that read a gate
 constexpr int kBlock = 16;                        // tokens of one decayed block
 constexpr int kBlockPanel = kBlock * 128;
 constexpr int kBlockTile = 2 * kBlockPanel;
@@ -52,7 +59,7 @@ enum Slot : int { kV = 0, kDo = 1, kK = 2, kQ = 3, kBwdSlots = 4 };
 
 // shared memory, from a 1024-byte boundary
 constexpr int kOffKp = kBwdSlots * kTileBytes;          // two blocks of decayed rows
-constexpr int kOffS = kOffKp + 2 * kBlockBytes;         // the state as two bf16 terms
+constexpr int kOffS = kOffKp + 2 * kBlockBytes;         // the state as two bf16 terms; outputs
 constexpr int kOffGates = kOffS + 2 * kTileBytes;
 constexpr int kOffBars = kOffGates + kBwdGates * sizeof(Gate);
 constexpr int kBwdBytes = kOffBars + 40 * 8 + 1024;
@@ -60,71 +67,79 @@ static_assert(kBwdBytes <= 232448, "shared memory of one CTA");
 
 struct BwdArgs {
   CUtensorMap mq, mk, mv, mo;
+  CUtensorMap out_k, out_v;  // dq or dk (or their parts) and dv
   Plan plan;
   Gates g;
   Slots slots;
   const float* initial;
   float* dinit;             // KV: [nseq, Hv, K, V] or NULL
-  uint16_t *dq, *dk, *dv;   // dq or dk in bf16 where one unit makes a row of them, else
+  uint16_t *dqk, *dv;       // dq or dk in bf16 where one unit makes a row of them, else
   float* part;              // [units' (head, tile)][total][K] partial sums
-  float* dots;              // [3][heads * tiles][total]
+  float* dots;              // [2][heads * tiles][total]
   const float* carry;       // states handed on
   const float* decay;
   float scale;
   int rows, ratio, Hk, Hv, K, V;
-  int wide_k, wide_v;       // rows of dq, dk and of dv allow 32-byte stores
 };
 
-#define CATTN_WAIT(bar, parity) \
-  (wait_phase((bar), static_cast<uint32_t>(parity) & 1u, gave_up, &g_fault_bwd))
+#define CATTN_WAIT(bar, parity) (wait_phase((bar), static_cast<uint32_t>(parity) & 1u))
 #define CATTN_WARP_WAIT(bar, parity) (__all_sync(0xffffffffu, CATTN_WAIT(bar, parity)))
 
-// Stores 32 fp32 values times `f` as bf16 to columns [c, c + 32) of a row of `width` columns.
-__device__ __forceinline__ void store_bf16(uint16_t* row, int c, int width, bool wide,
-                                           const uint32_t* x, float f) {
-  uint32_t y[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    y[i] = pack_bf16(f * __uint_as_float(x[2 * i]), f * __uint_as_float(x[2 * i + 1]));
-  if (wide && c + 32 <= width) {
-    stg256(row + c, y);
-    stg256(row + c + 16, y + 8);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (c + 8 * i < width)
-        *reinterpret_cast<uint4*>(row + c + 8 * i) =
-            make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-  }
-}
-
-// The same in fp32 (rows of K floats, K % 8 == 0, on 32-byte boundaries).
-__device__ __forceinline__ void store_f32(float* row, int c, int width, const uint32_t* x, float f) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t y[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = __float_as_uint(f * __uint_as_float(x[8 * i + j]));
-    if (c + 8 * i < width) stg256(row + c + 8 * i, y);
-  }
-}
-
 // Dot of 32 fp32 values with columns [c, c + 32) of row `row` of a bf16 tile.
-__device__ __forceinline__ float dot_tile(uint32_t tile, int row, int c, const uint32_t* x) {
-  float dot = 0.f;
+__device__ __forceinline__ f2 dot_tile(uint32_t tile, int row, int c, const uint32_t* x, f2 dot) {
+  const uint32_t at = tile + (c >> 6) * kPanelBytes;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int col = c + 8 * i;
-    const uint4 w = lds128_at(tile + (col / kPanelCols) * kPanelBytes +
-                              swizzled(row, (col % kPanelCols) / 8));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      dot = fmaf(__uint_as_float(u[j] << 16), __uint_as_float(x[8 * i + 2 * j]), dot);
-      dot = fmaf(__uint_as_float(u[j] & 0xffff0000u), __uint_as_float(x[8 * i + 2 * j + 1]), dot);
-    }
+    const uint4 w = lds128_at(at + swizzled(row, ((c >> 3) & 7) + i));
+    dot = f2_fma(bf16x2_to_f2(w.x), pair(x, 4 * i), dot);
+    dot = f2_fma(bf16x2_to_f2(w.y), pair(x, 4 * i + 1), dot);
+    dot = f2_fma(bf16x2_to_f2(w.z), pair(x, 4 * i + 2), dot);
+    dot = f2_fma(bf16x2_to_f2(w.w), pair(x, 4 * i + 3), dot);
   }
   return dot;
+}
+
+__device__ __forceinline__ void scale32(uint32_t* x, float f) {
+  const f2 s = f2_splat(f);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float a, b;
+    cconv::f2_unpack(f2_mul(s, pair(x, i)), a, b);
+    x[2 * i] = __float_as_uint(a);
+    x[2 * i + 1] = __float_as_uint(b);
+  }
+}
+
+// 128 columns of a TMEM tile, scaled, as bf16 or fp32 rows: to the staging buffer (panels of 128
+// bytes a row, 128-byte swizzle) or, for the rows of a partial chunk, straight to memory.
+// Columns at or past `width` are left out in steps of 8.
+template <bool F32>
+__device__ __forceinline__ void finish_tile(uint32_t tmem, uint32_t stage, bool whole, bool live,
+                                            int row, int width, float scale, void* dst) {
+#pragma unroll 1
+  for (int c = 0; c < width; c += 32) {
+    uint32_t x[32];
+    tmem_ld32(tmem + c, x);
+    tmem_wait_ld();
+    tmem_use32(x);
+    scale32(x, scale);
+    if (!F32) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = f2_to_bf16x2(pair(x, i));
+    }
+    constexpr int kPieces = F32 ? 8 : 4, kCols = F32 ? 4 : 8;  // 16-byte pieces of the batch
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int piece = F32 ? i : ((c >> 3) & 7) + i;
+      const int panel = F32 ? c >> 5 : c >> 6;
+      if (whole)
+        sts128(stage + panel * kPanelBytes + swizzled(row, piece), x[4 * i], x[4 * i + 1], x[4 * i + 2],
+               x[4 * i + 3]);
+      else if (live && c + kCols * i < width)
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(dst) + (c + kCols * i) * (F32 ? 4 : 2)) =
+            make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    }
+  }
 }
 
 template <bool KV>
@@ -133,44 +148,49 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   Gate* gates = reinterpret_cast<Gate*>(base + kOffGates);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + kOffBars);
-  uint64_t *full = bars, *empty = bars + kBwdSlots;
-  uint64_t *gfull = empty + kBwdSlots, *gempty = gfull + kBwdGates;
-  uint64_t *kpfull = gempty + kBwdGates, *kpempty = kpfull + 2;
-  uint64_t *fixed = kpempty + 2, *scfull = fixed + 1, *pfull = scfull + 1, *kvfull = pfull + 1;
-  uint64_t *kvfree = kvfull + 1, *sfull = kvfree + 1, *sempty = sfull + 1, *infull = sempty + 1;
-  uint64_t *scaled = infull + 1, *ofull = scaled + 1, *ofree = ofull + 1, *alldone = ofree + 1;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(alldone + 1);
-  volatile int* gave_up = reinterpret_cast<int*>(tmem_at + 1);
+  const uint32_t smem = smem_addr(base);
+  const uint32_t full = smem + kOffBars, empty = full + 8 * kBwdSlots;
+  const uint32_t gfull = empty + 8 * kBwdSlots, gempty = gfull + 8 * kBwdGates;
+  const uint32_t kpfull = gempty + 8 * kBwdGates, kpempty = kpfull + 16;
+  const uint32_t fixed = kpempty + 16, scfull = fixed + 8, pfull = scfull + 8, kvfull = pfull + 8;
+  const uint32_t kvfree = kvfull + 8, sfull = kvfree + 8, sempty = sfull + 8, infull = sempty + 8;
+  const uint32_t scaled = infull + 8, ofull = scaled + 8, ofree = ofull + 8;
+  const uint32_t osync = ofree + 8, alldone = osync + 8;  // one for each issuing thread
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(base + kOffBars + 39 * 8);
+  const uint32_t stored = smem + kOffBars + 38 * 8;  // chunks whose outputs have left the buffer
+  constexpr int kDot = KV ? kK : kQ;  // the tile that the rows' dots read
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBwdSlots; ++i) {
-      cconv::mbar_init(&full[i], 1);
-      // the tile that the rows' dots read goes when the state warps are done with it
-      cconv::mbar_init(&empty[i], i == (KV ? kK : kQ) ? kStateWarps : 1);
+      bar_init(full + 8 * i, 1);
+      // readers: the outputs' products, and for one tile each the four warps that take the dots,
+      // those that make decayed rows, and (the tile whose rows meet them) the state's products
+      const int users = i == kDot || i == (KV ? kQ : kK) ? 5 : i == (KV ? kDo : kV) ? 6 : 1;
+      bar_init(empty + 8 * i, users);
     }
     for (int i = 0; i < kBwdGates; ++i) {
-      cconv::mbar_init(&gfull[i], 1);
-      cconv::mbar_init(&gempty[i], 4 + kStateWarps + 1);
+      bar_init(gfull + 8 * i, 1);
+      bar_init(gempty + 8 * i, kBwdReaders);
     }
     for (int i = 0; i < 2; ++i) {
-      cconv::mbar_init(&kpfull[i], kStateWarps);
-      cconv::mbar_init(&kpempty[i], 1);
+      bar_init(kpfull + 8 * i, 4);
+      bar_init(kpempty + 8 * i, 1);
+      bar_init(alldone + 8 * i, 1);
     }
-    cconv::mbar_init(fixed, kStateWarps);
-    cconv::mbar_init(scfull, 1);
-    cconv::mbar_init(pfull, 4);
-    cconv::mbar_init(kvfull, 1);
-    cconv::mbar_init(kvfree, kStateWarps);
-    cconv::mbar_init(sfull, kStateWarps);
-    cconv::mbar_init(sempty, 1);
-    cconv::mbar_init(infull, 1);
-    cconv::mbar_init(scaled, kStateWarps);
-    cconv::mbar_init(ofull, 1);
-    cconv::mbar_init(ofree, kStateWarps);
-    cconv::mbar_init(alldone, 1);
-    *gave_up = 0;
+    bar_init(fixed, 4);
+    bar_init(scfull, 1);
+    bar_init(pfull, 4);
+    bar_init(kvfull, 1);
+    bar_init(kvfree, 4);
+    bar_init(sfull, 4);
+    bar_init(sempty, 1);
+    bar_init(infull, 1);
+    bar_init(scaled, 4);
+    bar_init(ofull, 1);
+    bar_init(ofree, 4);
+    set_count(stored, 0);
+    bar_init(osync, 4);
     cconv::fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(tmem_at, 512);
@@ -179,12 +199,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     cconv::prefetch_tensormap(&p.mk);
     cconv::prefetch_tensormap(&p.mv);
     cconv::prefetch_tensormap(&p.mo);
+    cconv::prefetch_tensormap(&p.out_k);
+    if (KV) cconv::prefetch_tensormap(&p.out_v);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
-  const uint32_t smem = smem_addr(base);
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
 
@@ -193,178 +214,194 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int64_t parts = min(static_cast<int64_t>(gridDim.x), units);
   Range range{0, 0};
   if (blockIdx.x < parts) range = range_of(units, parts, blockIdx.x);
-  const int64_t count = range.u1 - range.u0, start = KV ? range.u1 - 1 : range.u0;
+  const int count = static_cast<int>(range.u1 - range.u0);
+  const int64_t start = KV ? range.u1 - 1 : range.u0;
   const int pk = p.K > kPanelCols ? 2 : 1;
   const uint32_t av = smem + kV * kTileBytes, ao = smem + kDo * kTileBytes;
   const uint32_t ak = smem + kK * kTileBytes, aq = smem + kQ * kTileBytes;
 
+  bool ok = true;  // no wait of this thread's has given up
   if (count > 0) {
+  if (warp < 4) {
+  // Registers: 96 a thread at the launch, 40 + 120 + 64 + 168 + 88 after.
+  set_registers<40, false>();
   if (warp == 0) {
     // ---- tiles ----
-    if (lane == 0) {
+    if (elect_one()) {
       Walker w;
       w.seek(&p.plan, nch, start);
-      int use = 0;
-      bool ok = true;
-      for (int64_t i = 0; i < count && ok; ++i) {
+      int use = 0, part = 0;
+      for (int i = 0; i < count && ok; ++i) {
         if (w.rows() > 0) {
           const int hv = w.ht / p.plan.tiles, vt = w.ht % p.plan.tiles;
           const int hk = hv / p.ratio, row = w.row0();
           const int pv = p.V - vt * 128 > kPanelCols ? 2 : 1;
+#pragma unroll 1
           for (int j = 0; j < kBwdSlots; ++j) {
-            if (use > 0 && !(ok = CATTN_WAIT(&empty[j], use - 1))) break;
+            if (use > 0 && !(ok = CATTN_WAIT(empty + 8 * j, use - 1))) break;
+            part = j + 1;
             const bool isv = j == kV || j == kDo;
             const CUtensorMap* map = j == kV ? &p.mv : j == kDo ? &p.mo : j == kK ? &p.mk : &p.mq;
             const int panels = isv ? pv : pk;
-            cconv::mbar_arrive_expect_tx(&full[j], panels * kPanelBytes);
+            bar_expect(full + 8 * j, panels * kPanelBytes);
+#pragma unroll 1
             for (int c = 0; c < panels; ++c)
-              cconv::tma_load_3d(base + j * kTileBytes + c * kPanelBytes, map, &full[j],
-                                 (isv ? vt * 128 : 0) + c * kPanelCols, isv ? hv : hk, row);
+              load_box(smem + j * kTileBytes + c * kPanelBytes, map, full + 8 * j,
+                       (isv ? vt * 128 : 0) + c * kPanelCols, isv ? hv : hk, row);
           }
           if (!ok) break;
           ++use;
+          part = 0;
         }
         if (i + 1 < count) w.step<KV>();
       }
-      // one copy into each slot for each use (a use that gave up half-way counts none: its
-      // copies are waited for too, as the phase after)
-      for (int j = 0; j < kBwdSlots; ++j) {
-        if (use > 0) (void)cconv::mbar_wait_bounded(&full[j], (use - 1) & 1, cconv::kDrainLimitNs);
-        if (!ok) (void)cconv::mbar_wait_bounded(&full[j], use & 1, cconv::kDrainLimitNs);
-      }
+      for (int j = 0; j < kBwdSlots; ++j) drain(full + 8 * j, use + (j < part ? 1 : 0));
     }
   } else if (warp == 1) {
-    // ---- matrix products ----
-    if (lane == 0) {
-      int use = 0, subs = 0, pubs = 0, fixes = 0, kvs = 0;
-      bool ok = true;
+    // ---- scores, products with the state, and products of P ----
+    if (elect_one()) {
+      int use = 0, pubs = 0, fixes = 0, kvs = 0;
       const int kk = (p.K + 15) / 16, nk = kk * 16;
+      const uint32_t ds = mma_desc(128, false, false), dst = mma_desc(nk, false, false);
+      const uint32_t dk = mma_desc(nk, false, true);
+      const uint64_t tv = tile_desc(av, 0), to = tile_desc(ao, 0), tk = tile_desc(ak, 0);
+      const uint64_t tq = tile_desc(aq, 0), tS = tile_desc(smem + kOffS, 0);
+      const uint64_t rows_k = tile_desc(KV ? aq : ak, kPanelBytes), rows_o = tile_desc(ao, kPanelBytes);
+      const uint64_t rows_S = tile_desc(smem + kOffS, kPanelBytes);
       for (int unit = 0; unit < count && ok; ++unit) {
         const int gs = unit % kBwdGates;
-        if (!(ok = CATTN_WAIT(&gfull[gs], unit / kBwdGates))) break;
+        if (!(ok = CATTN_WAIT(gfull + 8 * gs, unit / kBwdGates))) break;
         const Gate& gt = gates[gs];
-        const int n = gt.n, flags = gt.flags, ht = gt.ht;
+        const int n = gt.n, flags = gt.flags;
         if (n > 0) {
-          const int vw = min(128, p.V - ht % p.plan.tiles * 128);
-          const int kv = (vw + 15) / 16, nv = kv * 16;
+          const int kv = (min(128, p.V - gt.ht % p.plan.tiles * 128) + 15) / 16, nv = kv * 16;
           const int steps = (n + 15) / 16;
-          for (int j = 0; j < kBwdSlots && ok; ++j) ok = CATTN_WAIT(&full[j], use);
+          const uint32_t dv = mma_desc(nv, false, true);
+#pragma unroll 1
+          for (int j = 0; j < kBwdSlots && ok; ++j) ok = CATTN_WAIT(full + 8 * j, use);
           if (!ok) break;
-          if (n < kChunk) {
-            if (!(ok = CATTN_WAIT(fixed, fixes))) break;
-            ++fixes;
-          }
-          // the score tiles overwrite the last chunk's P, outputs and state product
-          if (use > 0) {
-            if (!(ok = CATTN_WAIT(ofull, use - 1))) break;
-            if (!(ok = CATTN_WAIT(ofree, use - 1))) break;
-          }
+          if (n < kChunk && !(ok = CATTN_WAIT(fixed, fixes++))) break;
+          // the score tiles overwrite the last chunk's P (and, for KV, its state product)
+          if (use > 0 && !(ok = CATTN_WAIT(ofull, use - 1))) break;
           if (KV && kvs > 0 && !(ok = CATTN_WAIT(kvfree, kvs - 1))) break;
           tc_fence_after();
-          const uint32_t ds = mma_desc(128, false, false);
-          for (int j = 0; j < kv; ++j) {
-            const uint32_t off = (j / 4) * kPanelBytes + (j % 4) * 32;
-            mma_ss(tmem, tile_desc((KV ? av : ao) + off, 0), tile_desc((KV ? ao : av) + off, 0), ds,
-                   j > 0);
-          }
-          for (int j = 0; j < kk; ++j) {
-            const uint32_t off = (j / 4) * kPanelBytes + (j % 4) * 32;
-            mma_ss(tmem + 128, tile_desc((KV ? ak : aq) + off, 0), tile_desc((KV ? aq : ak) + off, 0),
-                   ds, j > 0);
-          }
+#pragma unroll 1
+          for (int j = 0; j < kv; ++j)
+            mma_ss(tmem, (KV ? tv : to) + col_step(j), (KV ? to : tv) + col_step(j), ds, j > 0);
+#pragma unroll 1
+          for (int j = 0; j < kk; ++j)
+            mma_ss(tmem + 128, (KV ? tk : tq) + col_step(j), (KV ? tq : tk) + col_step(j), ds, j > 0);
           mma_commit(scfull);
-          if (flags & kHasState) {
+          if (!KV) mma_commit(empty + 8 * kQ);
+          if (use > 0 && !(ok = CATTN_WAIT(ofree, use - 1))) break;
+          const bool has = flags & kHasState;
+          if (has) {
             if (!(ok = CATTN_WAIT(sfull, pubs))) break;
             ++pubs;
             tc_fence_after();
             // dO S^T or V D^T: the state's rows are the output's columns, its columns are summed
-            const uint32_t d = mma_desc(nk, false, false);
-            for (int term = 0; term < 2; ++term)
-              for (int j = 0; j < kv; ++j) {
-                const uint32_t off = (j / 4) * kPanelBytes + (j % 4) * 32;
-                mma_ss(tmem + 256, tile_desc((KV ? av : ao) + off, 0),
-                       tile_desc(smem + kOffS + term * kTileBytes + off, 0), d, term + j > 0);
-              }
+#pragma unroll 1
+            for (int j = 0; j < 2 * kv; ++j) {
+              const int term = j >= kv, c = term ? j - kv : j;
+              mma_ss(tmem + 256, (KV ? tv : to) + col_step(c), tS + term * (kTileBytes / 16) + col_step(c),
+                     dst, j > 0);
+            }
             if (KV) {
-              const uint32_t dd = mma_desc(nv, false, true);
+#pragma unroll 1
               for (int j = 0; j < kk; ++j)
-                mma_ss(tmem + 384, tile_desc(ak + (j / 4) * kPanelBytes + (j % 4) * 32, 0),
-                       tile_desc(smem + kOffS + j * 2048, kPanelBytes), dd, j > 0);
+                mma_ss(tmem + 384, tk + col_step(j), rows_S + j * kRowStep, dv, j > 0);
             }
             mma_commit(infull);
             mma_commit(sempty);
           }
-          mma_commit(KV ? &empty[kV] : &empty[kDo]);
+          mma_commit(KV ? empty + 8 * kV : empty + 8 * kDo);
+          if (KV) mma_commit(empty + 8 * kK);
+          if (!KV) mma_commit(empty + 8 * kV);
+          if (!(ok = CATTN_WAIT(pfull, use))) break;
+          if (has && !(ok = CATTN_WAIT(scaled, pubs - 1))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int j = 0; j < steps; ++j)
+            mma_ts(tmem + 256, tmem + j * 8, rows_k + j * kRowStep, dk, has || j > 0);
           if (KV) {
-            if (!(ok = CATTN_WAIT(pfull, use))) break;
-            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < steps; ++j)
+              mma_ts(tmem + 384, tmem + 128 + j * 8, rows_o + j * kRowStep, dv, has || j > 0);
           }
-          if (flags & kNeedKv) {
-            const uint32_t b = KV ? ao : av;
-            const int n0 = KV ? min(nv, 64) : nv;
-            const uint32_t d0 = mma_desc(n0, true, true), d1 = mma_desc(nv > 64 ? nv - 64 : 16, true, true);
-            for (int blk = 0; blk < steps; ++blk, ++subs) {
-              if (!(ok = CATTN_WAIT(&kpfull[subs & 1], subs >> 1))) break;
+          mma_commit(ofull);
+          mma_commit(empty + 8 * (KV ? kQ : kK));
+          if (KV) mma_commit(empty + 8 * kDo);
+          if (KV && (flags & kNeedKv)) ++kvs;
+          ++use;
+        }
+        bar_arrive(gempty + 8 * gs);
+      }
+      mma_commit(alldone);
+      drain(alldone, 1);
+    }
+  } else if (warp == 3) {
+    // ---- (kw . K)^T V or (er . Q)^T dO ----
+    if (elect_one()) {
+      int use = 0, subs = 0, fixes = 0, kvs = 0;
+      constexpr int kVals = KV ? kDo : kV;
+      const uint64_t rows_v = tile_desc(KV ? ao : av, kPanelBytes);
+      for (int unit = 0; unit < count && ok; ++unit) {
+        const int gs = unit % kBwdGates;
+        if (!(ok = CATTN_WAIT(gfull + 8 * gs, unit / kBwdGates))) break;
+        const Gate& gt = gates[gs];
+        const int n = gt.n;
+        if (n > 0) {
+          const int nv = (min(128, p.V - gt.ht % p.plan.tiles * 128) + 15) / 16 * 16;
+          const int steps = (n + 15) / 16;
+          if (!(ok = CATTN_WAIT(full + 8 * kVals, use))) break;
+          if (n < kChunk && !(ok = CATTN_WAIT(fixed, fixes++))) break;
+          // its columns: for KV those of the score tiles, else its own
+          if (KV && !(ok = CATTN_WAIT(pfull, use))) break;
+          if (gt.flags & kNeedKv) {
+            if (!KV && kvs > 0 && !(ok = CATTN_WAIT(kvfree, kvs - 1))) break;
+            const uint32_t d0 = mma_desc(KV ? min(nv, 64) : nv, true, true);
+            const uint32_t d1 = mma_desc(nv > 64 ? nv - 64 : 16, true, true);
+#pragma unroll 1
+            for (int b = 0; b < steps; ++b, ++subs) {
+              if (!(ok = CATTN_WAIT(kpfull + 8 * (subs & 1), subs >> 1))) break;
               tc_fence_after();
+              const uint64_t a = tile_desc(smem + kOffKp + (subs & 1) * kBlockBytes, kBlockPanel);
+#pragma unroll
               for (int s = 0; s < kSplit; ++s) {
-                const uint64_t a = tile_desc(smem + kOffKp + (subs & 1) * kBlockBytes + s * kBlockTile,
-                                             kBlockPanel);
-                mma_ss(tmem + (KV ? 64 : 384), a, tile_desc(b + blk * 2048, kPanelBytes), d0, blk + s > 0);
+                mma_ss(tmem + (KV ? 64 : 384), a + s * (kBlockTile / 16), rows_v + b * kRowStep, d0,
+                       b + s > 0);
                 if (KV && nv > 64)
-                  mma_ss(tmem + 192, a, tile_desc(b + kPanelBytes + blk * 2048, kPanelBytes), d1,
-                         blk + s > 0);
+                  mma_ss(tmem + 192, a + s * (kBlockTile / 16),
+                         rows_v + kPanelBytes / 16 + b * kRowStep, d1, b + s > 0);
               }
-              mma_commit(&kpempty[subs & 1]);
+              mma_commit(kpempty + 8 * (subs & 1));
             }
             if (!ok) break;
             mma_commit(kvfull);
             ++kvs;
-          }
-          if (!KV) {
-            mma_commit(&empty[kV]);
-            if (!(ok = CATTN_WAIT(pfull, use))) break;
-            tc_fence_after();
-            const uint32_t d = mma_desc(nk, false, true);
-            for (int j = 0; j < steps; ++j)
-              mma_ts(tmem + 128, tmem + j * 8, tile_desc(ak + j * 2048, kPanelBytes), d, j > 0);
-            mma_commit(ofull);
-            mma_commit(&empty[kK]);
+            mma_commit(empty + 8 * kVals);
           } else {
-            const bool add = flags & kHasState;
-            if (add) {
-              if (!(ok = CATTN_WAIT(scaled, pubs - 1))) break;
-              tc_fence_after();
-            }
-            const uint32_t dk = mma_desc(nk, false, true), dv = mma_desc(nv, false, true);
-            for (int j = 0; j < steps; ++j)
-              mma_ts(tmem + 256, tmem + j * 8, tile_desc(aq + j * 2048, kPanelBytes), dk, add || j > 0);
-            for (int j = 0; j < steps; ++j)
-              mma_ts(tmem + 384, tmem + 128 + j * 8, tile_desc(ao + j * 2048, kPanelBytes), dv,
-                     add || j > 0);
-            mma_commit(ofull);
-            mma_commit(&empty[kQ]);
-            mma_commit(&empty[kDo]);
+            bar_arrive(empty + 8 * kVals);
           }
           ++use;
         }
-        cconv::mbar_arrive(&gempty[gs]);
+        bar_arrive(gempty + 8 * gs);
       }
-      mma_commit(alldone);
-      (void)cconv::mbar_wait_bounded(alldone, 0, cconv::kDrainLimitNs);
+      mma_commit(alldone + 8);
+      drain(alldone + 8, 1);
     }
-  } else if (warp == 2) {
+  } else {
     // ---- gates ----
     Walker w;
     w.seek(&p.plan, nch, start);
-    for (int64_t i = 0; i < count; ++i) {
-      const int unit = static_cast<int>(i);
+    for (int unit = 0; unit < count; ++unit) {
       const int gs = unit % kBwdGates, n = w.rows(), row0 = w.row0();
       const int hv = w.ht / p.plan.tiles;
       float g[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        g[b] = 32 * b + lane < n ? kLog2e * p.g.at(row0 + 32 * b + lane, hv) : 0.f;
-      if (unit >= kBwdGates && !CATTN_WARP_WAIT(&gempty[gs], unit / kBwdGates - 1)) break;
+      for (int j = 0; j < 4; ++j)
+        g[j] = 4 * lane + j < n ? kLog2e * p.g.at(row0 + 4 * lane + j, hv) : 0.f;
+      if (unit >= kBwdGates && !(ok = CATTN_WARP_WAIT(gempty + 8 * gs, unit / kBwdGates - 1))) break;
       Gate& gt = gates[gs];
       make_gate(gt, g, lane);
       if (lane == 0) {
@@ -374,34 +411,38 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         gt.seq = w.seq;
         int f = 0;
         const bool first = KV ? w.last() : w.first(), last = KV ? w.first() : w.last();
-        if (i == 0 || first) f |= kSegment;
+        if (unit == 0 || first) f |= kSegment;
         if ((f & kSegment) && !first) f |= kMiddle;
         if (!first || (!KV && p.initial)) f |= kHasState;
         if (KV && last && p.dinit) f |= kFinish;
-        if ((!last && i + 1 < count) || (f & kFinish)) f |= kNeedKv;
+        if ((!last && unit + 1 < count) || (f & kFinish)) f |= kNeedKv;
         gt.flags = f;
       }
       __syncwarp();
-      if (lane == 0) cconv::mbar_arrive(&gfull[gs]);
-      if (i + 1 < count) w.step<KV>();
+      if (lane == 0) bar_arrive(gfull + 8 * gs);
+      if (unit + 1 < count) w.step<KV>();
     }
-  } else if (warp >= 4 && warp < 8) {
+  }
+  } else if (warp < 8) {
     // ---- score tiles to P ----
+    set_registers<120, true>();
     const int wq = warp - 4, row = wq * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     int use = 0;
     for (int unit = 0; unit < count; ++unit) {
       const int gs = unit % kBwdGates;
-      if (!CATTN_WARP_WAIT(&gfull[gs], unit / kBwdGates)) break;
+      if (!(ok = CATTN_WARP_WAIT(gfull + 8 * gs, unit / kBwdGates))) break;
       const Gate& gt = gates[gs];
-      const int n = gt.n, row0 = gt.row0, ht = gt.ht;
+      const int n = gt.n;
       if (n > 0) {
         const float own = KV ? gt.ws[row] : gt.lp[row];
-        if (!CATTN_WARP_WAIT(scfull, use)) break;
+        if (!(ok = CATTN_WARP_WAIT(scfull, use))) break;
         tc_fence_after();
-        float sum = 0.f;  // pairs of different tokens
+        f2 sum = 0;  // pairs of different tokens
+        // (P's columns [16 b, 16 b + 16) lie in score columns that are read or not needed)
+#pragma unroll 1
         for (int b = 0; b < 4; ++b) {
-          uint32_t x[32], z[32], y[16], y2[16];
+          uint32_t x[32], z[32];
           const bool live = KV ? b >= wq : b <= wq;
           if (live) {
             tmem_ld32(tmem + lanes + b * 32, x);
@@ -413,307 +454,310 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (live && b != wq) {
             float e = KV ? 0.f : own;
             const int lo = KV ? wq + 1 : b + 1, hi = KV ? b : wq;
+#pragma unroll 1
             for (int i = lo; i < hi; ++i) e += gt.block[i];
-            const float ut = KV ? own * exp2_fast(e) : exp2_fast(e);
+            const f2 ut = f2_splat(KV ? own * exp2_fast(e) : exp2_fast(e));
             const float* cols = (KV ? gt.pe : gt.ws) + b * 32;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 w = *reinterpret_cast<const float2*>(cols + 2 * i);
-              const float w0 = ut * w.x, w1 = ut * w.y;
-              const float p0 = __uint_as_float(x[2 * i]) * w0, p1 = __uint_as_float(x[2 * i + 1]) * w1;
-              const float z0 = __uint_as_float(z[2 * i]), z1 = __uint_as_float(z[2 * i + 1]);
-              y[i] = pack_bf16(p0, p1);
-              if (KV) y2[i] = pack_bf16(z0 * w0, z1 * w1);
-              sum = fmaf(p0, z0, sum);
-              sum = fmaf(p1, z1, sum);
+            for (int i = 0; i < 8; ++i) {
+              const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(cols + 4 * i);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const f2 wj = f2_mul(ut, j ? w.y : w.x);
+                const f2 pj = f2_mul(pair(x, 2 * i + j), wj), zj = pair(z, 2 * i + j);
+                sum = f2_fma(pj, zj, sum);
+                x[2 * i + j] = f2_to_bf16x2(pj);
+                if (KV) z[2 * i + j] = f2_to_bf16x2(f2_mul(zj, wj));
+              }
             }
           } else if (b == wq) {
             // the diagonal block: the decay as a running product away from the row's token
-            float w = 1.f, held = 0.f, held2 = 0.f;
+            float w = 1.f, s = 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int c = KV ? i : 31 - i;
-              const bool off = KV ? c > lane : c < lane;
-              if (off) w *= gt.a[b * 32 + (KV ? c : c + 1)];
-              const bool on = off || c == lane;
-              const float v = on ? __uint_as_float(x[c]) * w : 0.f;
-              const float v2 = on ? __uint_as_float(z[c]) * w : 0.f;
-              if (off) sum = fmaf(v, __uint_as_float(z[c]), sum);
-              if (i & 1) {
-                y[c / 2] = KV ? pack_bf16(held, v) : pack_bf16(v, held);
-                if (KV) y2[c / 2] = pack_bf16(held2, v2);
-              } else {
-                held = v;
-                held2 = v2;
+            for (int i = 0; i < 8; ++i) {
+              const int i4 = KV ? i : 7 - i;
+              const float4 a4 = *reinterpret_cast<const float4*>(&gt.a[b * 32 + 4 * i4]);
+              const float a[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+              for (int jj = 0; jj < 4; ++jj) {
+                const int j = KV ? jj : 3 - jj, c = 4 * i4 + j;
+                const bool off = KV ? c > lane : c < lane, on = off || c == lane;
+                if (KV && off) w *= a[j];
+                const float v = on ? __uint_as_float(x[c]) * w : 0.f;
+                if (off) s = fmaf(v, __uint_as_float(z[c]), s);
+                x[c] = __float_as_uint(v);
+                if (KV) z[c] = on ? __float_as_uint(__uint_as_float(z[c]) * w) : 0u;
+                if (!KV && on) w *= a[j];
               }
+            }
+            sum = f2_add(sum, f2_pack(s, 0.f));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              x[i] = f2_to_bf16x2(pair(x, i));
+              if (KV) z[i] = f2_to_bf16x2(pair(z, i));
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = y2[i] = 0;
+            for (int i = 0; i < 16; ++i) x[i] = z[i] = 0;
           }
-          // (P's columns [16 b, 16 b + 16) lie in score columns that are read or not needed)
-          tmem_st16(tmem + lanes + b * 16, y);
-          if (KV) tmem_st16(tmem + lanes + 128 + b * 16, y2);
+          tmem_st16(tmem + lanes + b * 16, x);
+          if (KV) tmem_st16(tmem + lanes + 128 + b * 16, z);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) cconv::mbar_arrive(pfull);
+        if (lane == 0) bar_arrive(pfull);
+        float s0, s1;
+        cconv::f2_unpack(sum, s0, s1);
         if (row < n)
-          p.dots[static_cast<int64_t>(ht) * p.rows + row0 + row] = p.scale * sum;
+          p.dots[static_cast<int64_t>(gt.ht) * p.rows + gt.row0 + row] = p.scale * (s0 + s1);
         ++use;
       }
       __syncwarp();
-      if (lane == 0) cconv::mbar_arrive(&gempty[gs]);
+      if (lane == 0) bar_arrive(gempty + 8 * gs);
     }
-  } else if (warp >= 8) {
-    // ---- the state, and the outputs ----
-    const int st = threadIdx.x - 256;
-    const int half = st / 128, krow = st % 128;  // columns [64 half, 64 half + 64) of row krow
-    const uint32_t lanes = static_cast<uint32_t>(krow & ~31) << 16;
-    float S[64];
-#pragma unroll
-    for (int i = 0; i < 64; ++i) S[i] = 0.f;
-    int use = 0, subs = 0, pubs = 0, kvs = 0;
-    bool ok = true;
+  } else if (warp < 12) {
+    // ---- decayed rows ----
+    set_registers<64, false>();
+    const int kt = threadIdx.x - 256;
+    constexpr int kKeys = KV ? kQ : kK, kVals = KV ? kDo : kV;
+    const uint32_t src = KV ? aq : ak;
+    int use = 0, subs = 0;
     for (int unit = 0; unit < count && ok; ++unit) {
       const int gs = unit % kBwdGates;
-      if (!(ok = CATTN_WARP_WAIT(&gfull[gs], unit / kBwdGates))) break;
+      if (!(ok = CATTN_WARP_WAIT(gfull + 8 * gs, unit / kBwdGates))) break;
       const Gate& gt = gates[gs];
-      const int n = gt.n, flags = gt.flags, ht = gt.ht, row0 = gt.row0;
-      const int hv = ht / p.plan.tiles, vt = ht % p.plan.tiles;
-      const int vw = min(128, p.V - vt * 128);
-      const bool has = flags & kHasState;
-      if (flags & kSegment) {
-#pragma unroll
-        for (int i = 0; i < 64; ++i) S[i] = 0.f;
-        if (flags & kMiddle) {
-          // what the ranges before this one (after it, for KV) hand on
-          float coef = 1.f;
-          const int64_t by = KV ? 1 : -1;
-          for (int64_t j = blockIdx.x + by; j >= 0 && j < parts; j += by) {
-            const float4* src = reinterpret_cast<const float4*>(p.carry + j * kStateFloats);
-            const float d = p.decay[j];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float4 x = src[(half * 16 + i) * 128 + krow];
-              S[4 * i] = fmaf(coef, x.x, S[4 * i]);
-              S[4 * i + 1] = fmaf(coef, x.y, S[4 * i + 1]);
-              S[4 * i + 2] = fmaf(coef, x.z, S[4 * i + 2]);
-              S[4 * i + 3] = fmaf(coef, x.w, S[4 * i + 3]);
-            }
-            if (d < 0.f) break;
-            coef *= d;
-            if (coef == 0.f) break;
-          }
-        } else if (!KV && p.initial && krow < p.K) {
-          const int64_t slot = p.slots.of(gt.seq);
-          const float* src = p.initial + ((slot * p.Hv + hv) * p.K + krow) * p.V + vt * 128 + half * 64;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (slot >= 0 && half * 64 + 4 * i < vw) x = *reinterpret_cast<const float4*>(src + 4 * i);
-            S[4 * i] = x.x, S[4 * i + 1] = x.y, S[4 * i + 2] = x.z, S[4 * i + 3] = x.w;
-          }
-        }
-      }
+      const int n = gt.n;
       if (n > 0) {
+        if (!(ok = CATTN_WARP_WAIT(full + 8 * kKeys, use))) break;
+        if (!(ok = CATTN_WARP_WAIT(full + 8 * kVals, use))) break;
         if (n < kChunk) {
           // the tiles whose rows are summed over
-          const uint32_t t0 = KV ? aq : ak, t1 = KV ? ao : av;
-          if (!(ok = CATTN_WARP_WAIT(&full[KV ? kQ : kK], use))) break;
-          zero_rows(t0, pk, n, st, kStateWarps * 32);
-          if (!(ok = CATTN_WARP_WAIT(&full[KV ? kDo : kV], use))) break;
-          zero_rows(t1, vw > kPanelCols ? 2 : 1, n, st, kStateWarps * 32);
+          zero_rows(src, pk, n, kt, 128);
+          zero_rows(KV ? ao : av, p.V - gt.ht % p.plan.tiles * 128 > kPanelCols ? 2 : 1, n, kt, 128);
           cconv::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) cconv::mbar_arrive(fixed);
+          if (lane == 0) bar_arrive(fixed);
         }
-        if (has) {
-          if (pubs > 0 && !(ok = CATTN_WARP_WAIT(sempty, pubs - 1))) break;
-          ++pubs;
-          const uint32_t dst = smem + kOffS + half * kPanelBytes;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float a = S[8 * i + 2 * j], b = S[8 * i + 2 * j + 1];
-              hi[j] = pack_bf16(a, b);
-              lo[j] = pack_bf16(a - __uint_as_float(hi[j] << 16),
-                                b - __uint_as_float(hi[j] & 0xffff0000u));
-            }
-            sts128(dst + swizzled(krow, i), hi[0], hi[1], hi[2], hi[3]);
-            sts128(dst + kTileBytes + swizzled(krow, i), lo[0], lo[1], lo[2], lo[3]);
-          }
-          cconv::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) cconv::mbar_arrive(sfull);
-        }
-        const int steps = (n + 15) / 16;
-        if (flags & kNeedKv) {
-          if (!(ok = CATTN_WARP_WAIT(&full[KV ? kQ : kK], use))) break;
-          const uint32_t src = KV ? aq : ak;
-          const int r = st / 16, piece = st % 16;  // one 16-byte piece of one token
+        if (lane == 0) bar_arrive(empty + 8 * kVals);
+        if (gt.flags & kNeedKv) {
+          const int steps = (n + 15) / 16;
+          const float* weights = KV ? gt.er : gt.kw;
+#pragma unroll 1
           for (int b = 0; b < steps; ++b, ++subs) {
-            if (subs >= 2 && !(ok = CATTN_WARP_WAIT(&kpempty[subs & 1], (subs >> 1) - 1))) break;
-            const int t = b * kBlock + r;
-            const float w = KV ? gt.er[t] : gt.kw[t];
-            if (piece < 8 * pk) {
-              const int q = piece / 8, at8 = piece % 8;
-              uint32_t hi[4], mid[4], lo[4];
-              const uint4 raw4 = lds128_at(src + q * kPanelBytes + swizzled(t, at8));
-              float x[8];
-              cconv::f2_unpack(cconv::bf16x2_to_f2(raw4.x), x[0], x[1]);
-              cconv::f2_unpack(cconv::bf16x2_to_f2(raw4.y), x[2], x[3]);
-              cconv::f2_unpack(cconv::bf16x2_to_f2(raw4.z), x[4], x[5]);
-              cconv::f2_unpack(cconv::bf16x2_to_f2(raw4.w), x[6], x[7]);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] = t < n ? x[i] * w : 0.f;
-              split3(x, hi, mid, lo);
-              const uint32_t at = smem + kOffKp + (subs & 1) * kBlockBytes + q * kBlockPanel +
-                                  swizzled(r, at8);
-              sts128(at, hi[0], hi[1], hi[2], hi[3]);
-              sts128(at + kBlockTile, mid[0], mid[1], mid[2], mid[3]);
-              sts128(at + 2 * kBlockTile, lo[0], lo[1], lo[2], lo[3]);
+            if (subs >= 2 && !(ok = CATTN_WARP_WAIT(kpempty + 8 * (subs & 1), (subs >> 1) - 1))) break;
+            const uint32_t dst = smem + kOffKp + (subs & 1) * kBlockBytes;
+#pragma unroll 2
+            for (int e = kt; e < kBlock * 8 * pk; e += 128) {
+              const int r = e >> (2 + pk), piece = e & (8 * pk - 1), t = b * kBlock + r;
+              const uint32_t q = piece >> 3, at = swizzled(r, piece & 7);
+              uint4 in = lds128_at(src + q * kPanelBytes + b * kBlock * 128 + at);
+              if (t >= n) in = make_uint4(0, 0, 0, 0);
+              store_split(in, weights[t], dst + q * kBlockPanel + at, kBlockTile);
             }
             cconv::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) cconv::mbar_arrive(&kpfull[subs & 1]);
+            if (lane == 0) bar_arrive(kpfull + 8 * (subs & 1));
           }
           if (!ok) break;
         }
-        // rows of the output this thread finishes: row krow, columns [64 half, + 64)
-        const float rowf = KV ? gt.kw[krow] : gt.er[krow];
-        float dot = 0.f;
-        if (KV && has) {
-          if (!(ok = CATTN_WARP_WAIT(infull, pubs - 1))) break;
-          if (!(ok = CATTN_WARP_WAIT(&full[kK], use))) break;
+        __syncwarp();
+        if (lane == 0) bar_arrive(empty + 8 * kKeys);
+        ++use;
+      }
+      __syncwarp();
+      if (lane == 0) bar_arrive(gempty + 8 * gs);
+    }
+  } else if (warp < 16) {
+    // ---- the state: a row of 128 columns a thread ----
+    set_registers<168, true>();
+    const int krow = threadIdx.x - 384;
+    const uint32_t lanes = static_cast<uint32_t>(krow & ~31) << 16;
+    f2 S[64];
+#pragma unroll
+    for (int i = 0; i < 64; ++i) S[i] = 0;
+    int pubs = 0, kvs = 0, done = 0;
+    for (int unit = 0; unit < count && ok; ++unit) {
+      const int gs = unit % kBwdGates;
+      if (!(ok = CATTN_WARP_WAIT(gfull + 8 * gs, unit / kBwdGates))) break;
+      const Gate& gt = gates[gs];
+      const int n = gt.n, flags = gt.flags;
+      const int hv = gt.ht / p.plan.tiles, vt = gt.ht % p.plan.tiles;
+      const int vw = min(128, p.V - vt * 128);
+      if (flags & kSegment) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) S[i] = 0;
+        if (flags & kMiddle) {
+          // what the ranges before this one (after it, for KV) hand on
+          gather_state(S, p.carry, p.decay, blockIdx.x, parts, KV ? 1 : -1, krow);
+        } else if (!KV && p.initial && krow < p.K) {
+          const int64_t slot = p.slots.of(gt.seq);
+          const float* src = p.initial + ((slot * p.Hv + hv) * p.K + krow) * p.V + vt * 128;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            ulonglong2 x = make_ulonglong2(0, 0);
+            if (slot >= 0 && 4 * i < vw) x = *reinterpret_cast<const ulonglong2*>(src + 4 * i);
+            S[2 * i] = x.x, S[2 * i + 1] = x.y;
+          }
+        }
+      }
+      if (n > 0 && (flags & kHasState)) {
+        if (pubs > 0 && !(ok = CATTN_WARP_WAIT(sempty, pubs - 1))) break;
+        if (!(ok = __all_sync(0xffffffffu, wait_count(stored, done)))) break;
+        ++pubs;
+        const f2 minus = f2_splat(-1.f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            hi[j] = f2_to_bf16x2(S[4 * i + j]);
+            lo[j] = f2_to_bf16x2(f2_fma(bf16x2_to_f2(hi[j]), minus, S[4 * i + j]));
+          }
+          const uint32_t at = smem + kOffS + i / 8 * kPanelBytes + swizzled(krow, i % 8);
+          sts128(at, hi[0], hi[1], hi[2], hi[3]);
+          sts128(at + kTileBytes, lo[0], lo[1], lo[2], lo[3]);
+        }
+        cconv::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(sfull);
+      }
+      if (n > 0 && (flags & kNeedKv)) {
+        const f2 d = f2_splat(gt.total);
+        if (!(ok = CATTN_WARP_WAIT(kvfull, kvs))) break;
+        ++kvs;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t x[16];
+          tmem_ld16(tmem + lanes + (KV ? (c / 4) * 128 + 64 + (c % 4) * 16 : 384 + c * 16), x);
+          tmem_wait_ld();
+          tmem_use16(x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) S[c * 8 + i] = f2_fma(d, S[c * 8 + i], pair(x, i));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(kvfree);
+      }
+      if (n > 0) ++done;
+      if (KV && (flags & kFinish) && krow < p.K) {
+        float* dst = p.dinit + ((static_cast<int64_t>(gt.seq) * p.Hv + hv) * p.K + krow) * p.V + vt * 128;
+        const f2 sc = f2_splat(p.scale);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (4 * i < vw)
+            *reinterpret_cast<ulonglong2*>(dst + 4 * i) =
+                make_ulonglong2(f2_mul(sc, S[2 * i]), f2_mul(sc, S[2 * i + 1]));
+      }
+      __syncwarp();
+      if (lane == 0) bar_arrive(gempty + 8 * gs);
+    }
+  } else {
+    // ---- the outputs: a row a thread ----
+    set_registers<88, false>();
+    const int row = threadIdx.x - 512;
+    const uint32_t lanes = static_cast<uint32_t>(row & ~31) << 16;
+    int use = 0, pubs = 0, syncs = 0;
+    // the four warps meet (with a limit, as every wait)
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) bar_arrive(osync);
+      return ok = CATTN_WARP_WAIT(osync, syncs++);
+    };
+    for (int unit = 0; unit < count && ok; ++unit) {
+      const int gs = unit % kBwdGates;
+      if (!(ok = CATTN_WARP_WAIT(gfull + 8 * gs, unit / kBwdGates))) break;
+      const Gate& gt = gates[gs];
+      const int n = gt.n, ht = gt.ht, row0 = gt.row0;
+      if (n > 0) {
+        const int hv = ht / p.plan.tiles, vt = ht % p.plan.tiles, vw = min(128, p.V - vt * 128);
+        const float rowf = KV ? gt.kw[row] : gt.er[row];
+        f2 dot = 0;
+        if (!(ok = CATTN_WARP_WAIT(full + 8 * kDot, use))) break;
+        if (gt.flags & kHasState) {
+          if (!(ok = CATTN_WARP_WAIT(infull, pubs))) break;
+          ++pubs;
           tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            // two batches of dk, two of dv
-            const int col = half * 64 + (c & 1) * 32;
-            const bool isk = c < 2;
-            if (col < (isk ? p.K : vw)) {
-              uint32_t x[32];
-              const uint32_t at = tmem + lanes + (isk ? 256 : 384) + col;
-              tmem_ld32(at, x);
-              tmem_wait_ld();
-              tmem_use32(x);
-              if (isk) dot += dot_tile(ak, krow, col, x);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(rowf * __uint_as_float(x[i]));
-              tmem_st16(at, x);
-              tmem_st16(at + 16, x + 16);
-            }
+#pragma unroll 1
+          for (int c = 0; c < (KV ? 256 : 128); c += 32) {
+            if (c < 128 ? c >= p.K : c - 128 >= vw) continue;
+            uint32_t x[32];
+            tmem_ld32(tmem + lanes + 256 + c, x);
+            tmem_wait_ld();
+            tmem_use32(x);
+            if (c < 128) dot = dot_tile(KV ? ak : aq, row, c, x, dot);
+            scale32(x, rowf);
+            tmem_st16(tmem + lanes + 256 + c, x);
+            tmem_st16(tmem + lanes + 256 + c + 16, x + 16);
           }
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) cconv::mbar_arrive(scaled);
+          if (lane == 0) bar_arrive(scaled);
         }
-        if (KV) {
-          if (!has && !(ok = CATTN_WARP_WAIT(scfull, use))) break;  // K Q^T reads the tile too
-          __syncwarp();
-          if (lane == 0) cconv::mbar_arrive(&empty[kK]);
-        }
-        if (flags & kNeedKv) {
-          const float d = gt.total;
-          if (!(ok = CATTN_WARP_WAIT(kvfull, kvs))) break;
-          ++kvs;
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t x[32];
-            tmem_ld32(tmem + lanes + (KV ? half * 128 + 64 : 384 + half * 64) + c * 32, x);
-            tmem_wait_ld();
-            tmem_use32(x);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              S[c * 32 + i] = fmaf(d, S[c * 32 + i], __uint_as_float(x[i]));
-          }
-          tc_fence_before();
-          if (KV) {
-            __syncwarp();
-            if (lane == 0) cconv::mbar_arrive(kvfree);
-          }
-        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(empty + 8 * kDot);
+        const int64_t t = row0 + row;
+        float d0, d1;
+        cconv::f2_unpack(dot, d0, d1);
+        if (row < n)
+          p.dots[(static_cast<int64_t>(p.plan.heads) * p.plan.tiles + ht) * p.rows + t] =
+              p.scale * rowf * (d0 + d1);
         if (!(ok = CATTN_WARP_WAIT(ofull, use))) break;
-        if (!KV && !(ok = CATTN_WARP_WAIT(&full[kQ], use))) break;
         tc_fence_after();
+        const bool whole = n == kChunk, live = row < n;
         const int hk = hv / p.ratio;
-        const int64_t t = row0 + krow;
-        float* prow = p.part ? p.part + (static_cast<int64_t>(ht) * p.rows + t) * p.K : nullptr;
-        uint16_t* krow_out = (KV ? p.dk : p.dq) + (t * p.Hk + hk) * p.K;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int col = half * 64 + c * 32;
-          if (col < p.K) {
-            uint32_t x[32];
-            tmem_ld32(tmem + lanes + (KV ? 256 : 128) + col, x);
-            if (!KV && has) {
-              uint32_t z[32];
-              tmem_ld32(tmem + lanes + 256 + col, z);
-              tmem_wait_ld();
-              tmem_use32(x);
-              tmem_use32(z);
-              dot += dot_tile(aq, krow, col, z);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                x[i] = __float_as_uint(fmaf(rowf, __uint_as_float(z[i]), __uint_as_float(x[i])));
-            } else {
-              tmem_wait_ld();
-              tmem_use32(x);
-            }
-            if (krow < n) {
-              if (prow)
-                store_f32(prow, col, p.K, x, p.scale);
-              else
-                store_bf16(krow_out, col, p.K, p.wide_k, x, p.scale);
-            }
+        const uint32_t stage = smem + kOffS;
+        if (p.part)
+          finish_tile<true>(tmem + lanes + 256, stage, whole, live, row, p.K, p.scale,
+                            p.part + (static_cast<int64_t>(ht) * p.rows + t) * p.K);
+        else
+          finish_tile<false>(tmem + lanes + 256, stage, whole, live, row, p.K, p.scale,
+                             p.dqk + (t * p.Hk + hk) * p.K);
+        if (whole) {
+          cconv::fence_proxy_async_smem();
+          if (!meet()) break;
+          if (row == 0) {
+            const int cols = p.part ? 32 : 64;
+#pragma unroll 1
+            for (int c = 0, i = 0; c < p.K; c += cols, ++i)
+              store_box(&p.out_k, stage + i * kPanelBytes, c, p.part ? ht : hk, row0);
+            stores_commit();
+            if (KV) stores_wait_read();
           }
+          if (KV && !meet()) break;
         }
         if (KV) {
-          uint16_t* vrow = p.dv + (t * p.Hv + hv) * p.V + vt * 128;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int col = half * 64 + c * 32;
-            if (col < vw) {
-              uint32_t x[32];
-              tmem_ld32(tmem + lanes + 384 + col, x);
-              tmem_wait_ld();
-              tmem_use32(x);
-              if (krow < n) store_bf16(vrow, col, vw, p.wide_v, x, p.scale);
+          finish_tile<false>(tmem + lanes + 384, stage, whole, live, row, vw, p.scale,
+                             p.dv + (t * p.Hv + hv) * p.V + vt * 128);
+          if (whole) {
+            cconv::fence_proxy_async_smem();
+            if (!meet()) break;
+            if (row == 0) {
+#pragma unroll 1
+              for (int c = 0, i = 0; c < vw; c += 64, ++i)
+                store_box(&p.out_v, stage + i * kPanelBytes, vt * 128 + c, hv, row0);
+              stores_commit();
             }
           }
         }
-        if (krow < n)
-          p.dots[(static_cast<int64_t>(1 + half) * p.plan.heads * p.plan.tiles + ht) * p.rows + t] =
-              p.scale * rowf * dot;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (!KV) cconv::mbar_arrive(&empty[kQ]);
-          cconv::mbar_arrive(ofree);
+        if (lane == 0) bar_arrive(ofree);
+        if (row == 0) {
+          stores_wait_read();
+          set_count(stored, use + 1);
         }
         ++use;
       }
-      if (KV && (flags & kFinish) && krow < p.K) {
-        float* dst = p.dinit + ((static_cast<int64_t>(gt.seq) * p.Hv + hv) * p.K + krow) * p.V +
-                     vt * 128 + half * 64;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (half * 64 + 4 * i < vw)
-            *reinterpret_cast<float4*>(dst + 4 * i) =
-                make_float4(p.scale * S[4 * i], p.scale * S[4 * i + 1], p.scale * S[4 * i + 2],
-                            p.scale * S[4 * i + 3]);
-      }
       __syncwarp();
-      if (lane == 0) cconv::mbar_arrive(&gempty[gs]);
+      if (lane == 0) bar_arrive(gempty + 8 * gs);
     }
+    if (row == 0) stores_wait();  // all of it is written
   }
   }
+  if (!ok) atomicOr(&g_fault_bwd, kFaultWait);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -733,31 +777,39 @@ static int launch_sweep(const BwdArgs& a, int grid, cudaStream_t stream) {
              : CCONV_ERR_CUDA;
 }
 
+// Map of dq or dk, or of their parts.
+static int out_map(CUtensorMap* map, uint16_t* d, float* part, const ChunkBwdCall& c) {
+  const int tiles = (c.s.V + 127) / 128;
+  if (part) return encode_part_map(map, part, c.s.total, int64_t(c.s.Hv) * tiles, c.s.K);
+  return encode_tile_map(map, Rows{d, int64_t(c.s.Hk) * c.s.K, c.s.K}, c.s.total, c.s.Hk, c.s.K);
+}
+
 int launch_chunk_bwd(const ChunkBwdCall& c, cudaStream_t stream) {
   BwdArgs a{};
   int rc = encode_tile_map(&a.mq, c.q, c.s.total, c.s.Hk, c.s.K);
   if (rc == CCONV_OK) rc = encode_tile_map(&a.mk, c.k, c.s.total, c.s.Hk, c.s.K);
   if (rc == CCONV_OK) rc = encode_tile_map(&a.mv, c.v, c.s.total, c.s.Hv, c.s.V);
   if (rc == CCONV_OK) rc = encode_tile_map(&a.mo, c.d_o, c.s.total, c.s.Hv, c.s.V);
+  if (rc == CCONV_OK)
+    rc = encode_tile_map(&a.out_v, Rows{c.dv, int64_t(c.s.Hv) * c.s.V, c.s.V}, c.s.total, c.s.Hv, c.s.V);
+  if (rc == CCONV_OK) rc = out_map(&a.out_k, c.dq, c.part_q, c);
   if (rc != CCONV_OK) return rc;
   a.plan = Plan{c.cu, c.cstart, c.s.nseq, (c.s.V + 127) / 128, c.s.Hv};
   a.g = c.g;
   a.slots = c.slots;
   a.initial = c.initial;
   a.dinit = c.dinit;
-  a.dq = c.dq, a.dk = c.dk, a.dv = c.dv;
+  a.dqk = c.dq, a.dv = c.dv;
   a.scale = c.scale;
   a.rows = c.s.total, a.ratio = c.s.Hv / c.s.Hk;
   a.Hk = c.s.Hk, a.Hv = c.s.Hv, a.K = c.s.K, a.V = c.s.V;
-  a.wide_v = aligned(c.dv, 32) && c.s.V % 16 == 0;
-  const bool even = c.s.K % 16 == 0;
-  a.wide_k = even && aligned(c.dq, 32);
   a.carry = c.carry_s;
   a.decay = c.carry_s + static_cast<int64_t>(c.grid) * 2 * kStateFloats;
   a.part = c.part_q, a.dots = c.dots_q;
   rc = launch_sweep<false>(a, c.grid, stream);
+  if (rc == CCONV_OK) rc = out_map(&a.out_k, c.dk, c.part_k, c);
   if (rc != CCONV_OK) return rc;
-  a.wide_k = even && aligned(c.dk, 32);
+  a.dqk = c.dk;
   a.carry = c.carry_d;
   a.decay = c.carry_d + static_cast<int64_t>(c.grid) * 2 * kStateFloats;
   a.part = c.part_k, a.dots = c.dots_k;

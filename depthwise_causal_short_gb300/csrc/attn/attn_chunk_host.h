@@ -38,7 +38,7 @@ struct ChunkBwdCall {
   float scale;
   uint16_t *dq, *dk, *dv;
   float *part_q, *part_k;   // [Hv * tiles][total][K] on 32-byte boundaries, or NULL: dq and dk
-  float *dots_q, *dots_k;   // [3][Hv * tiles][total]
+  float *dots_q, *dots_k;   // [2][Hv * tiles][total]
   float *carry_s, *carry_d; // what kStates and kStateGrads wrote
   int grid;
 };
@@ -46,6 +46,7 @@ struct ChunkBwdCall {
 int launch_chunk_bwd(const ChunkBwdCall& c, cudaStream_t stream);
 int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream);
 size_t chunk_fwd_bytes(int grid);
+int encode_part_map(CUtensorMap* map, float* x, int64_t total, int64_t parts, int64_t C);
 int encode_tile_map(CUtensorMap* map, const Rows& x, int64_t total, int64_t H, int64_t C);
 
 }  // namespace cattn

@@ -45,38 +45,55 @@ __global__ void __launch_bounds__(256)
 }
 
 // dg_t = sum over i >= t of its sequence of (qdot_i - kdot_i), each the sum of `slices` times
-// `tiles` parts.  One warp for each sequence and value head, walking from the last token in
-// steps of 32.
-__global__ void __launch_bounds__(128)
+// `tiles` parts.  One CTA for each sequence and value head walks from the last token in steps of
+// kDgThreads * kDgPer: a thread sums kDgPer tokens, warps and CTA scan the sums.
+constexpr int kDgThreads = 512, kDgPer = 4;
+__global__ void __launch_bounds__(kDgThreads)
     cattn_linear_dg_kernel(const float* qdot, const float* kdot, int slices, int tiles,
                            LinearShape s, const int32_t* cu, float* dg) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
-  const int lane = threadIdx.x % 32;
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / 32;
-  if (w >= static_cast<int64_t>(s.nseq) * s.Hv) return;
-  const int seq = static_cast<int>(w / s.Hv), h = static_cast<int>(w % s.Hv);
+  __shared__ float sums[kDgThreads / 32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int seq = static_cast<int>(blockIdx.x) / s.Hv, h = static_cast<int>(blockIdx.x) % s.Hv;
   int t0, t1;
   sequence_rows(cu, seq, s.total, t0, t1);
   const int64_t slice = static_cast<int64_t>(s.Hv) * tiles * s.total;
   float carry = 0.f;
-  for (int hi = t1; hi > t0; hi -= 32) {
-    const int t = hi - 1 - lane;
-    float x = 0.f;
-    if (t >= t0)
-      for (int i = 0; i < slices; ++i)
-        for (int j = 0; j < tiles; ++j) {
-          const int64_t at = i * slice + (static_cast<int64_t>(h) * tiles + j) * s.total + t;
-          x += qdot[at] - kdot[at];
-        }
+  for (int hi = t1; hi > t0; hi -= kDgThreads * kDgPer) {
+    // this thread's tokens are top, top - 1, ..
+    const int top = hi - 1 - static_cast<int>(threadIdx.x) * kDgPer;
+    float x[kDgPer];
+#pragma unroll
+    for (int k = 0; k < kDgPer; ++k) x[k] = 0.f;
+    for (int i = 0; i < slices; ++i)
+      for (int j = 0; j < tiles; ++j) {
+        const int64_t at = i * slice + (static_cast<int64_t>(h) * tiles + j) * s.total + top;
+#pragma unroll
+        for (int k = 0; k < kDgPer; ++k)
+          if (top - k >= t0) x[k] += qdot[at - k] - kdot[at - k];
+      }
+#pragma unroll
+    for (int k = 1; k < kDgPer; ++k) x[k] += x[k - 1];
+    float run = x[kDgPer - 1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const float y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+      const float y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += y;
     }
-    x += carry;
-    if (t >= t0) dg[static_cast<int64_t>(t) * s.Hv + h] = x;
-    carry = __shfl_sync(0xffffffffu, x, 31);
+    if (lane == 31) sums[warp] = run;
+    __syncthreads();
+    float before = carry;
+    for (int w = 0; w < kDgThreads / 32; ++w) {
+      if (w < warp) before += sums[w];
+      carry += sums[w];
+    }
+    __syncthreads();
+    const float other = __shfl_up_sync(0xffffffffu, run, 1);  // the lanes before this one
+    if (lane > 0) before += other;
+#pragma unroll
+    for (int k = 0; k < kDgPer; ++k)
+      if (top - k >= t0) dg[static_cast<int64_t>(top - k) * s.Hv + h] = before + x[k];
   }
 }
 
@@ -104,10 +121,10 @@ int check_linear(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t
   return aligned(o, 16) ? CCONV_OK : CCONV_ERR_ALIGN;
 }
 
-static int check_states(const int32_t* cu, int64_t nseq, const float* initial, const float* fin,
+static int check_states(const int32_t* cu, int64_t nseq, int64_t Hv, const float* initial, const float* fin,
                         const int32_t* idx, int64_t S, int32_t* status) {
   if (!cu) return CCONV_ERR_NULL;
-  if (nseq < 1 || nseq > kMaxSeqs) return CCONV_ERR_SHAPE;
+  if (nseq < 1 || nseq > kMaxSeqs || nseq * Hv > (int64_t(1) << 31) - 1) return CCONV_ERR_SHAPE;
   if (!aligned(cu, 4)) return CCONV_ERR_ALIGN;
   if (idx) {
     if (!status) return CCONV_ERR_NULL;
@@ -144,7 +161,7 @@ static int chunk_grid(int64_t total, int64_t nseq, int64_t Hv, int64_t V, int* g
 // The chunk offsets at the head of the workspace.
 static size_t offsets_bytes(int64_t nseq) { return (static_cast<size_t>(nseq + 1) * 4 + 15) / 16 * 16; }
 
-constexpr int kSlices = 3;  // parts of a unit's dots
+constexpr int kSlices = 2;  // parts of a unit's dots
 
 // What a backward call keeps in its workspace, from a 256-byte boundary.
 struct BwdWork {
@@ -216,7 +233,7 @@ extern "C" CCONV_API int cattn_linear_fwd(
   using namespace cattn;
   int rc = check_linear(q, sqt, sqh, k, skt, skh, v, svt, svh, g, sgt, sgh, total, Hk, Hv, K, V, o);
   if (rc == CCONV_OK)
-    rc = check_states(cu_seqlens, nseq, initial_state, final_state, state_indices, S, status_dev);
+    rc = check_states(cu_seqlens, nseq, Hv, initial_state, final_state, state_indices, S, status_dev);
   if (rc != CCONV_OK) return rc;
   int grid = 0;
   if (chunk_grid(total, nseq, Hv, V, &grid) != CCONV_OK) return CCONV_ERR_CUDA;
@@ -252,7 +269,7 @@ extern "C" CCONV_API int cattn_linear_bwd(
   using namespace cattn;
   int rc = check_linear(q, sqt, sqh, k, skt, skh, v, svt, svh, g, sgt, sgh, total, Hk, Hv, K, V, dv);
   if (rc == CCONV_OK)
-    rc = check_states(cu_seqlens, nseq, initial_state, nullptr, state_indices, S, status_dev);
+    rc = check_states(cu_seqlens, nseq, Hv, initial_state, nullptr, state_indices, S, status_dev);
   if (rc != CCONV_OK) return rc;
   if (!aligned(d_initial_state, 16)) return CCONV_ERR_ALIGN;
   int grid = 0;
@@ -326,10 +343,10 @@ extern "C" CCONV_API int cattn_linear_bwd(
                      parts, side ? c.dk : c.dq) != cudaSuccess)
         return CCONV_ERR_CUDA;
   }
-  const unsigned lines = static_cast<unsigned>((nseq * Hv + 3) / 4);
-  return launch_pdl(cattn_linear_dg_kernel, dim3(lines), dim3(128), 0, stream,
-                    static_cast<const float*>(c.dots_q), static_cast<const float*>(c.dots_k),
-                    kSlices, tiles, c.s, cu_seqlens, dg) == cudaSuccess
+  return launch_pdl(cattn_linear_dg_kernel, dim3(static_cast<unsigned>(nseq * Hv)), dim3(kDgThreads),
+                    0, stream, static_cast<const float*>(c.dots_q),
+                    static_cast<const float*>(c.dots_k), kSlices, tiles, c.s, cu_seqlens,
+                    dg) == cudaSuccess
              ? CCONV_OK
              : CCONV_ERR_CUDA;
 }

@@ -104,7 +104,9 @@ CCONV_API int cattn_linear_bwd_workspace_bytes(int64_t total, int64_t nseq, int6
  *   q, k      [total, Hk, K] bf16, strided;  v  [total, Hv, V] bf16, strided.
  *   g         [total, Hv] fp32 natural logarithms of the decays, at g + t * sgt + h * sgh with
  *             any strides >= 0 (sgt = 0: one decay per head).  Values below -128 count as -128
- *             (exp(-128) is zero in fp32), so -inf forgets everything before the token.
+ *             (exp(-128) is zero in fp32), so -inf forgets everything before the token.  Decays
+ *             are at most 1 (g <= 0); what has decayed below 2^-127 counts as forgotten, also
+ *             if later values of g are positive.
  *   scale     factor of the outputs.
  *   initial_state  [S, Hv, K, V] fp32 contiguous, or NULL (zeros).
  *   final_state    [S, Hv, K, V] fp32 output, or NULL.  May be the same array as initial_state.

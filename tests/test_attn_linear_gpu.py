@@ -95,6 +95,26 @@ def test_parity(lens, Hk, Hv, K, V, states):
         _check(grads[4], want[4], STATE_TOL, "d_initial_state")
 
 
+@pytest.mark.parametrize("lens,Hk,Hv,K,V,states", [
+    ([90, 2, 300] * 5, 4, 16, 24, 136, False), ([1] * 300, 2, 4, 32, 32, False),
+    ([128, 5, 0, 129] * 12, 4, 8, 64, 64, True), ([1500, 33, 800], 8, 16, 128, 128, False),
+    ([64, 400, 1, 128, 0, 0] * 8, 1, 8, 72, 256, False),
+])
+def test_repeats_are_bit_identical(lens, Hk, Hv, K, V, states):
+    # many chunks that need no state, short ranges, several tiles of V: the roles of a CTA drift
+    # apart as far as they can here, and every run must still meet at the same places
+    q, k, v, g, do, s0 = (t.cuda() for t in plain.linear_inputs(lens, Hk, Hv, K, V, seed=K))
+    cu, init = _cu(lens), s0 if states else None
+    first = None
+    for _ in range(25):
+        got = [t for t in (*cc.cattn_linear_bwd(q, k, v, g, do, cu, initial_state=init),
+                           *cc.cattn_linear_fwd(q, k, v, g, cu, initial_state=init, final_state=True)[:2])
+               if t is not None]
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
+    assert cc.cattn_device_fault() == 0
+
+
 def test_gradients_against_differences():
     # the loss's change along random directions, from the 64-bit forward, against the kernel's
     # gradients: they carry the bf16 tolerance, of the sum of their parts' sizes
