@@ -8,10 +8,11 @@
 //
 // Bound by memory: 4 bytes a channel forward, 6 backward, against some 10 fp32 operations.
 // A group of 4 to 32 lanes holds one head (8 channels, one 16-byte access, a lane), so the
-// sums over a head are a few shuffles.  A group takes one token and walks several of its heads:
-// the table row is read once for them (it is fp32, twice the bytes of a head's channels), and
-// kBatch heads' loads are in flight at once.  Everything between the bf16 load and the one
-// rounding at the store is fp32.
+// sums over a head are a few shuffles; the rotation's partners exchange the raw bf16 words.  A
+// group takes one token and kHeads of its heads at a time: the table row, fp32 and so twice the
+// bytes of a head's channels, is read once for them, and all their loads are in flight
+// together.  A CTA works on queries or on keys only, so that one set of weights (and of their
+// sums) is live.  Everything between the bf16 load and the one rounding at the store is fp32.
 #include "attn.cuh"
 
 namespace cattn {
@@ -36,36 +37,30 @@ static int read_fault(unsigned* out) {
 static FaultReader reader(read_fault);
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;      // heads in flight per group, forward
-constexpr int kBatchBwd = 2;   // and backward (two tensors each)
+constexpr int kHeads = 4;  // heads of an item
+constexpr int kFwdCtas = 4, kBwdCtas = 2;  // CTAs per SM of a full grid
+
+struct Side {
+  const uint16_t *x, *dy;
+  uint16_t* out;  // y, or dx
+  int64_t st, sh, dt, dh;
+  const void* w;
+  int H, heads, splits;  // heads; heads of an item (1 or kHeads); items of a token
+  int64_t items;
+};
 
 struct NormArgs {
-  const uint16_t *q, *k, *dyq, *dyk;
-  uint16_t *oq, *ok;  // yq, yk or dq, dk
-  int64_t sqt, sqh, skt, skh, syqt, syqh, sykt, sykh;
-  const void *wq, *wk;
+  Side side[2];  // queries, keys
   const float *cos, *sin;
   const int32_t* pos;
-  float* part;  // backward: [grid][2][K] partial sums of dwq, dwk (NULL: not wanted)
+  float* part;  // backward: [grid][K] partial sums of the weights' gradients (NULL: not wanted)
   int64_t P;
-  int total, Hq, Hk, K, R, wdt;
-  int heads;      // heads of one item
-  int splits;     // items per token
-  int64_t items;  // total * splits
-  float inv;      // 1 / K or 1
+  int ctas_q;   // CTAs of the queries; the others are the keys'
+  int K, R, wdt;
+  float inv;    // 1 / K or 1
   float eps;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float* x) {
-  f2_unpack(bf16x2_to_f2(v.x), x[0], x[1]);
-  f2_unpack(bf16x2_to_f2(v.y), x[2], x[3]);
-  f2_unpack(bf16x2_to_f2(v.z), x[4], x[5]);
-  f2_unpack(bf16x2_to_f2(v.w), x[6], x[7]);
-}
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  return make_uint4(f2_to_bf16x2(f2_pack(x[0], x[1])), f2_to_bf16x2(f2_pack(x[2], x[3])),
-                    f2_to_bf16x2(f2_pack(x[4], x[5])), f2_to_bf16x2(f2_pack(x[6], x[7])));
-}
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -81,30 +76,6 @@ __device__ __forceinline__ float group_sum(float s) {
   return s;
 }
 
-// Turns the group's 8 channels a lane by `dir` * angle.  c, s: the lane's table entries (ones
-// and zeros in the channels that are not rotated).
-template <int LANES, bool INTER>
-__device__ __forceinline__ void rotate(float* u, const float* c, const float* s, int lane, int half,
-                                       float dir) {
-  if constexpr (INTER) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = u[2 * j], b = u[2 * j + 1], sn = dir * s[j];
-      u[2 * j] = a * c[j] - b * sn;
-      u[2 * j + 1] = b * c[j] + a * sn;
-    }
-  } else {
-    // Lanes [0, half) hold the first channels of the pairs, lanes [half, 2 half) the second.
-    const int peer = lane < half ? lane + half : lane < 2 * half ? lane - half : lane;
-    const float sign = lane < half ? -dir : dir;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float other = __shfl_sync(0xffffffffu, u[j], peer, LANES);
-      u[j] = u[j] * c[j] + other * (sign * s[j]);
-    }
-  }
-}
-
 __device__ __forceinline__ void load_weight(const void* w, int wdt, int c0, bool on, float* out) {
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -114,202 +85,285 @@ __device__ __forceinline__ void load_weight(const void* w, int wdt, int c0, bool
                                 : bf16_to_f32(static_cast<const uint16_t*>(w)[c0 + j]);
 }
 
+// The lane that holds the other channels of a lane's pairs: lanes [0, half) the first, lanes
+// [half, 2 half) the second of each pair (itself for channels that are not rotated).
+__device__ __forceinline__ int peer_of(int lane, int half) {
+  return lane < half ? lane + half : lane < 2 * half ? lane - half : lane;
+}
+
+template <int LANES>
+__device__ __forceinline__ uint4 exchange(const uint4& v, int peer) {
+  return make_uint4(__shfl_sync(0xffffffffu, v.x, peer, LANES),
+                    __shfl_sync(0xffffffffu, v.y, peer, LANES),
+                    __shfl_sync(0xffffffffu, v.z, peer, LANES),
+                    __shfl_sync(0xffffffffu, v.w, peer, LANES));
+}
+
+// A lane's 4 or 8 table entries in one access: as two, every line would be fetched twice.
+__device__ __forceinline__ void ld_table(const float* p, float (&v)[8]) {
+  asm volatile("ld.global.nc.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+                 "=f"(v[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void ld_table(const float* p, float (&v)[4]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+}
+
+// The factors of a lane's 8 channels, in pairs: y = x . C + partner . S, where `partner` holds the
+// other channel of each pair (partner_of).  Ones and zeros in the channels that are not rotated.
+template <bool INTER>
+__device__ __forceinline__ void load_angles(const NormArgs& p, int t, int lane, float dir, f2* C, f2* S) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) C[j] = cconv::f2_splat(1.f), S[j] = 0;
+  if (lane * 8 >= p.R) return;
+  int64_t at = p.pos ? p.pos[t] : t;
+  if (at < 0 || at >= p.P) {
+    if (lane == 0) atomicOr(&g_fault_qknorm, kFaultPosition);
+    at = at < 0 ? 0 : p.P - 1;
+  }
+  const int half = p.R / 2;
+  const bool second = !INTER && lane * 8 >= half;
+  const int64_t col = at * half + (INTER ? lane * 4 : second ? lane * 8 - half : lane * 8);
+  if constexpr (INTER) {
+    float c[4], s[4];
+    ld_table(p.cos + col, c);
+    ld_table(p.sin + col, s);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) C[j] = f2_pack(c[j], c[j]), S[j] = f2_pack(-dir * s[j], dir * s[j]);
+  } else {
+    float c[8], s[8];
+    ld_table(p.cos + col, c);
+    ld_table(p.sin + col, s);
+    const f2 sign = cconv::f2_splat(second ? dir : -dir);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      C[j] = f2_pack(c[2 * j], c[2 * j + 1]);
+      S[j] = cconv::f2_mul(sign, f2_pack(s[2 * j], s[2 * j + 1]));
+    }
+  }
+}
+
+// The words with the other channel of each pair: of the partner lane, or the own ones swapped.
 template <int LANES, bool INTER>
-struct Angles {
-  static constexpr int N = INTER ? 4 : 8;
-  float c[N], s[N];
-  __device__ __forceinline__ void load(const NormArgs& p, int t, int lane) {
+__device__ __forceinline__ uint4 partner_of(const uint4& v, int peer) {
+  if constexpr (INTER)
+    return make_uint4(__byte_perm(v.x, 0, 0x1032), __byte_perm(v.y, 0, 0x1032),
+                      __byte_perm(v.z, 0, 0x1032), __byte_perm(v.w, 0, 0x1032));
+  return exchange<LANES>(v, peer);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, f2* x) {
+  x[0] = bf16x2_to_f2(v.x), x[1] = bf16x2_to_f2(v.y);
+  x[2] = bf16x2_to_f2(v.z), x[3] = bf16x2_to_f2(v.w);
+}
+__device__ __forceinline__ uint4 pack8(const f2* x) {
+  return make_uint4(f2_to_bf16x2(x[0]), f2_to_bf16x2(x[1]), f2_to_bf16x2(x[2]), f2_to_bf16x2(x[3]));
+}
+template <int LANES>
+__device__ __forceinline__ float group_dot(const f2* a, const f2* b) {
+  f2 d = cconv::f2_mul(a[0], b[0]);
 #pragma unroll
-    for (int j = 0; j < N; ++j) c[j] = 1.f, s[j] = 0.f;
-    if (lane * 8 >= p.R) return;
-    int64_t at = p.pos ? p.pos[t] : t;
-    if (at < 0 || at >= p.P) {
-      if (lane == 0) atomicOr(&g_fault_qknorm, kFaultPosition);
-      at = at < 0 ? 0 : p.P - 1;
-    }
-    const int half = p.R / 2;
-    const int64_t col = INTER ? lane * 4 : (lane * 8 < half ? lane * 8 : lane * 8 - half);
-    const float4* pc = reinterpret_cast<const float4*>(p.cos + at * half + col);
-    const float4* ps = reinterpret_cast<const float4*>(p.sin + at * half + col);
-#pragma unroll
-    for (int j = 0; j < N / 4; ++j) {
-      const float4 a = __ldg(pc + j), b = __ldg(ps + j);
-      c[4 * j] = a.x, c[4 * j + 1] = a.y, c[4 * j + 2] = a.z, c[4 * j + 3] = a.w;
-      s[4 * j] = b.x, s[4 * j + 1] = b.y, s[4 * j + 2] = b.z, s[4 * j + 3] = b.w;
-    }
+  for (int j = 1; j < 4; ++j) d = cconv::f2_fma(a[j], b[j], d);
+  float d0, d1;
+  f2_unpack(d, d0, d1);
+  return group_sum<LANES>(d0 + d1);
+}
+
+// Where a group stands among its side's items (token, head block).
+struct Cursor {
+  int64_t it, step, items;
+  int t, s, t_step, s_step, splits;
+  __device__ __forceinline__ Cursor(const Side& side, int64_t first, int64_t stride)
+      : it(first), step(stride), items(side.items), splits(side.splits) {
+    t = static_cast<int>(it / splits), s = static_cast<int>(it % splits);
+    t_step = static_cast<int>(step / splits), s_step = static_cast<int>(step % splits);
+  }
+  __device__ __forceinline__ void next() {  // without dividing
+    it += step;
+    t += t_step;
+    s += s_step;
+    if (s >= splits) s -= splits, ++t;
   }
 };
 
 template <int LANES, bool INTER>
-__global__ void __launch_bounds__(kThreads) cattn_qknorm_fwd_kernel(NormArgs p) {
+__global__ void __launch_bounds__(kThreads, kFwdCtas)
+    cattn_qknorm_fwd_kernel(const __grid_constant__ NormArgs p) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
   constexpr int kGroups = kThreads / LANES;
   const int lane = threadIdx.x % LANES;
   const bool on = lane * 8 < p.K;
-  float wq[8], wk[8];
-  load_weight(p.wq, p.wdt, lane * 8, on, wq);
-  load_weight(p.wk, p.wdt, lane * 8, on, wk);
-  const int all = p.Hq + p.Hk;
+  const bool isk = blockIdx.x >= p.ctas_q;
+  const Side& side = p.side[isk];
+  const int cta = isk ? blockIdx.x - p.ctas_q : blockIdx.x, ctas = isk ? gridDim.x - p.ctas_q : p.ctas_q;
+  const int peer = INTER ? lane : peer_of(lane, p.R / 16);
+  // The weights of each lane's channels and of the other ones of their pairs.
+  __shared__ ulonglong2 weights[2][2][LANES];
+  if (threadIdx.x < LANES) {
+    float w[8], o[8];
+    load_weight(side.w, p.wdt, lane * 8, on, w);
+    load_weight(side.w, p.wdt, peer * 8, peer * 8 < p.K, o);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      weights[0][j][lane] = make_ulonglong2(f2_pack(w[4 * j], w[4 * j + 1]), f2_pack(w[4 * j + 2], w[4 * j + 3]));
+      weights[1][j][lane] = INTER ? make_ulonglong2(f2_pack(o[4 * j + 1], o[4 * j]), f2_pack(o[4 * j + 3], o[4 * j + 2]))
+                                  : make_ulonglong2(f2_pack(o[4 * j], o[4 * j + 1]), f2_pack(o[4 * j + 2], o[4 * j + 3]));
+    }
+  }
+  __syncthreads();
+  const int64_t st = side.st, sh = side.sh;
+  const int H = side.H, heads = side.heads;
   // Whole warps walk the items together, so that every shuffle has its 32 lanes.
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
-  const int64_t mine = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / LANES;
-  const int64_t warp0 = mine - (threadIdx.x % 32) / LANES;
-  for (int64_t base = warp0, it = mine; base < p.items; base += step, it += step) {
-    const bool live = it < p.items;
-    const int t = live ? static_cast<int>(it / p.splits) : 0;
-    const int h0 = live ? static_cast<int>(it % p.splits) * p.heads : 0;
-    Angles<LANES, INTER> ang;
-    ang.load(p, t, lane);
-    for (int hb = 0; hb < p.heads; hb += kBatch) {
-      uint4 raw[kBatch];
+  const int64_t mine = (threadIdx.x % 32) / LANES;
+  for (Cursor at(side, static_cast<int64_t>(cta) * kGroups + threadIdx.x / LANES,
+                 static_cast<int64_t>(ctas) * kGroups);
+       at.it - mine < at.items; at.next()) {
+    const bool live = at.it < at.items;
+    const int t = live ? at.t : 0, h0 = live ? at.s * heads : 0;
+    const int n = live && on ? min(heads, H - h0) : 0;
+    uint4 raw[kHeads];
+    const uint16_t* x0 = side.x + t * st + h0 * sh + lane * 8;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int h = h0 + hb + i;
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (live && on && hb + i < p.heads && h < all)
-          raw[i] = ld_stream(h < p.Hq ? p.q + t * p.sqt + h * p.sqh + lane * 8
-                                      : p.k + t * p.skt + (h - p.Hq) * p.skh + lane * 8);
-      }
+    for (int i = 0; i < kHeads; ++i, x0 += sh) {
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (i < n) raw[i] = ld_stream(x0);
+    }
+    // y = r (x . A + partner . B): weights and angles in one pair of factors a channel
+    f2 A[4], B[4];
+    load_angles<INTER>(p, t, lane, 1.f, A, B);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int h = h0 + hb + i;
-        const bool isq = h < p.Hq, used = live && hb + i < p.heads && h < all;
-        float x[8];
-        unpack8(raw[i], x);
-        float ss = 0.f;
+    for (int j = 0; j < 2; ++j) {
+      const ulonglong2 w = weights[0][j][lane], o = weights[1][j][lane];
+      A[2 * j] = cconv::f2_mul(A[2 * j], w.x), A[2 * j + 1] = cconv::f2_mul(A[2 * j + 1], w.y);
+      B[2 * j] = cconv::f2_mul(B[2 * j], o.x), B[2 * j + 1] = cconv::f2_mul(B[2 * j + 1], o.y);
+    }
+    uint16_t* y0 = side.out + (static_cast<int64_t>(t) * H + h0) * p.K + lane * 8;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-        const float r = rsqrtf(group_sum<LANES>(ss) * p.inv + p.eps);
+    for (int i = 0; i < kHeads; ++i, y0 += p.K) {
+      if (i >= heads) break;
+      f2 x[4], o[4];
+      unpack8(raw[i], x);
+      const f2 r = cconv::f2_splat(rsqrtf(group_dot<LANES>(x, x) * p.inv + p.eps));
+      unpack8(partner_of<LANES, INTER>(raw[i], peer), o);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= r * (isq ? wq[j] : wk[j]);
-        if (p.R > 0) rotate<LANES, INTER>(x, ang.c, ang.s, lane, p.R / 16, 1.f);
-        if (used && on) {
-          uint16_t* y = isq ? p.oq + (static_cast<int64_t>(t) * p.Hq + h) * p.K
-                            : p.ok + (static_cast<int64_t>(t) * p.Hk + h - p.Hq) * p.K;
-          *reinterpret_cast<uint4*>(y + lane * 8) = pack8(x);
-        }
-      }
+      for (int j = 0; j < 4; ++j)
+        x[j] = cconv::f2_mul(r, cconv::f2_fma(o[j], B[j], cconv::f2_mul(x[j], A[j])));
+      if (i < n) *reinterpret_cast<uint4*>(y0) = pack8(x);
     }
   }
 }
 
 template <int LANES, bool INTER>
-__global__ void __launch_bounds__(kThreads) cattn_qknorm_bwd_kernel(NormArgs p) {
+__global__ void __launch_bounds__(kThreads, kBwdCtas)
+    cattn_qknorm_bwd_kernel(const __grid_constant__ NormArgs p) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
   constexpr int kGroups = kThreads / LANES;
   const int lane = threadIdx.x % LANES;
   const bool on = lane * 8 < p.K;
-  float wq[8], wk[8], dwq[8], dwk[8];
-  load_weight(p.wq, p.wdt, lane * 8, on, wq);
-  load_weight(p.wk, p.wdt, lane * 8, on, wk);
+  const bool isk = blockIdx.x >= p.ctas_q;
+  const Side& side = p.side[isk];
+  const int cta = isk ? blockIdx.x - p.ctas_q : blockIdx.x, ctas = isk ? gridDim.x - p.ctas_q : p.ctas_q;
+  const int peer = INTER ? lane : peer_of(lane, p.R / 16);
+  f2 w[4], dw[4];
+  {
+    float w1[8];
+    load_weight(side.w, p.wdt, lane * 8, on, w1);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) dwq[j] = dwk[j] = 0.f;
-  const int all = p.Hq + p.Hk;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
-  const int64_t mine = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / LANES;
-  const int64_t warp0 = mine - (threadIdx.x % 32) / LANES;
-  for (int64_t base = warp0, it = mine; base < p.items; base += step, it += step) {
-    const bool live = it < p.items;
-    const int t = live ? static_cast<int>(it / p.splits) : 0;
-    const int h0 = live ? static_cast<int>(it % p.splits) * p.heads : 0;
-    Angles<LANES, INTER> ang;
-    ang.load(p, t, lane);
-    for (int hb = 0; hb < p.heads; hb += kBatchBwd) {
-      uint4 rx[kBatchBwd], ry[kBatchBwd];
+    for (int j = 0; j < 4; ++j) w[j] = f2_pack(w1[2 * j], w1[2 * j + 1]), dw[j] = 0;
+  }
+  const int64_t st = side.st, sh = side.sh, dt = side.dt, dh = side.dh;
+  const int H = side.H, heads = side.heads;
+  const int64_t mine = (threadIdx.x % 32) / LANES;
+  for (Cursor at(side, static_cast<int64_t>(cta) * kGroups + threadIdx.x / LANES,
+                 static_cast<int64_t>(ctas) * kGroups);
+       at.it - mine < at.items; at.next()) {
+    const bool live = at.it < at.items;
+    const int t = live ? at.t : 0, h0 = live ? at.s * heads : 0;
+    const int n = live && on ? min(heads, H - h0) : 0;
+    uint4 rx[kHeads], ry[kHeads];
+    const uint16_t* x0 = side.x + t * st + h0 * sh + lane * 8;
+    const uint16_t* d0 = side.dy + t * dt + h0 * dh + lane * 8;
 #pragma unroll
-      for (int i = 0; i < kBatchBwd; ++i) {
-        const int h = h0 + hb + i;
-        rx[i] = ry[i] = make_uint4(0, 0, 0, 0);
-        if (live && on && hb + i < p.heads && h < all) {
-          const bool isq = h < p.Hq;
-          rx[i] = ld_stream(isq ? p.q + t * p.sqt + h * p.sqh + lane * 8
-                                : p.k + t * p.skt + (h - p.Hq) * p.skh + lane * 8);
-          ry[i] = ld_stream(isq ? p.dyq + t * p.syqt + h * p.syqh + lane * 8
-                                : p.dyk + t * p.sykt + (h - p.Hq) * p.sykh + lane * 8);
-        }
+    for (int i = 0; i < kHeads; ++i, x0 += sh, d0 += dh) {
+      rx[i] = ry[i] = make_uint4(0, 0, 0, 0);
+      if (i < n) {
+        rx[i] = ld_stream(x0);
+        ry[i] = ld_stream(d0);
       }
+    }
+    f2 C[4], S[4];
+    load_angles<INTER>(p, t, lane, -1.f, C, S);
+    uint16_t* y0 = side.out + (static_cast<int64_t>(t) * H + h0) * p.K + lane * 8;
 #pragma unroll
-      for (int i = 0; i < kBatchBwd; ++i) {
-        const int h = h0 + hb + i;
-        const bool isq = h < p.Hq, used = live && hb + i < p.heads && h < all;
-        float x[8], d[8];
-        unpack8(rx[i], x);
-        unpack8(ry[i], d);
-        float ss = 0.f;
+    for (int i = 0; i < kHeads; ++i, y0 += p.K) {
+      if (i >= heads) break;
+      f2 x[4], d[4], o[4];
+      unpack8(rx[i], x);
+      unpack8(ry[i], d);
+      unpack8(partner_of<LANES, INTER>(ry[i], peer), o);
+      const float norm = group_dot<LANES>(x, x) * p.inv + p.eps;
+      const f2 r = cconv::f2_splat(live && h0 + i < H ? rsqrtf(norm) : 0.f);  // no head: nothing to sum
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-        const float norm = group_sum<LANES>(ss) * p.inv + p.eps;
-        const float r = used ? rsqrtf(norm) : 0.f;  // no head: nothing for the weights' sums
-        if (p.R > 0) rotate<LANES, INTER>(d, ang.c, ang.s, lane, p.R / 16, -1.f);
-        float dot = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float n = x[j] * r, dn = d[j] * (isq ? wq[j] : wk[j]);
-          if (isq)
-            dwq[j] = fmaf(d[j], n, dwq[j]);
-          else
-            dwk[j] = fmaf(d[j], n, dwk[j]);
-          dot = fmaf(dn, n, dot);
-          x[j] = n;
-          d[j] = dn;
-        }
-        const float m = group_sum<LANES>(dot) * p.inv;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = r * (d[j] - x[j] * m);
-        if (used && on) {
-          uint16_t* y = isq ? p.oq + (static_cast<int64_t>(t) * p.Hq + h) * p.K
-                            : p.ok + (static_cast<int64_t>(t) * p.Hk + h - p.Hq) * p.K;
-          *reinterpret_cast<uint4*>(y + lane * 8) = pack8(d);
-        }
+      for (int j = 0; j < 4; ++j) {
+        x[j] = cconv::f2_mul(x[j], r);
+        d[j] = cconv::f2_fma(o[j], S[j], cconv::f2_mul(d[j], C[j]));
+        dw[j] = cconv::f2_fma(d[j], x[j], dw[j]);
+        d[j] = cconv::f2_mul(d[j], w[j]);
       }
+      const f2 m = cconv::f2_splat(-group_dot<LANES>(d, x) * p.inv);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[j] = cconv::f2_mul(r, cconv::f2_fma(x[j], m, d[j]));
+      if (i < n) *reinterpret_cast<uint4*>(y0) = pack8(d);
     }
   }
   if (!p.part) return;
   // The CTA's sums: one row per group, added up group by group in a fixed order.
   __shared__ float rows[kGroups][LANES * 8 + 1];
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) rows[threadIdx.x / LANES][lane * 8 + j] = side ? dwk[j] : dwq[j];
-    __syncthreads();
-    for (int c = threadIdx.x; c < p.K; c += kThreads) {
-      float s = 0.f;
+  for (int j = 0; j < 4; ++j)
+    f2_unpack(dw[j], rows[threadIdx.x / LANES][lane * 8 + 2 * j], rows[threadIdx.x / LANES][lane * 8 + 2 * j + 1]);
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.K; c += kThreads) {
+    float s = 0.f;
 #pragma unroll 8
-      for (int gidx = 0; gidx < kGroups; ++gidx) s += rows[gidx][c];
-      p.part[(static_cast<int64_t>(blockIdx.x) * 2 + side) * p.K + c] = s;
-    }
-    __syncthreads();
+    for (int gidx = 0; gidx < kGroups; ++gidx) s += rows[gidx][c];
+    p.part[static_cast<int64_t>(blockIdx.x) * p.K + c] = s;
   }
 }
 
-// Adds the CTAs' partial sums in a fixed order: 8 lanes of rows a column, then across them.
+// Adds the CTAs' partial sums in a fixed order: kReduceRows lanes of rows a column, then across
+// them.  Columns of the queries' weights first, then the keys'.
 constexpr int kReduceCols = 32, kReduceRows = 16;
 __global__ void __launch_bounds__(kReduceCols* kReduceRows)
-    cattn_qknorm_dw_kernel(const float* part, int n, int K, int wdt, void* dwq, void* dwk) {
+    cattn_qknorm_dw_kernel(const float* part, int ctas_q, int ctas, int K, int wdt, void* dwq, void* dwk) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
   __shared__ float sums[kReduceRows][kReduceCols + 1];
-  const int c = blockIdx.x * kReduceCols + threadIdx.x;
+  const int col = blockIdx.x * kReduceCols + threadIdx.x;
+  const bool isk = col >= K;
+  const int c = isk ? col - K : col;
   float s = 0.f;
-  if (c < 2 * K) {
+  if (col < 2 * K) {
+    const int first = isk ? ctas_q : 0, last = isk ? ctas : ctas_q;
 #pragma unroll 8
-    for (int i = threadIdx.y; i < n; i += kReduceRows) s += part[static_cast<int64_t>(i) * 2 * K + c];
+    for (int i = first + threadIdx.y; i < last; i += kReduceRows) s += part[static_cast<int64_t>(i) * K + c];
   }
   sums[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
-  if (threadIdx.y != 0 || c >= 2 * K) return;
+  if (threadIdx.y != 0 || col >= 2 * K) return;
   s = 0.f;
 #pragma unroll
   for (int i = 0; i < kReduceRows; ++i) s += sums[i][threadIdx.x];
-  void* dst = c < K ? dwq : dwk;
+  void* dst = isk ? dwk : dwq;
   if (!dst) return;
-  const int at = c < K ? c : c - K;
   if (wdt == CCONV_F32)
-    static_cast<float*>(dst)[at] = s;
+    static_cast<float*>(dst)[c] = s;
   else
-    static_cast<uint16_t*>(dst)[at] = cconv::f32_to_bf16(s);
+    static_cast<uint16_t*>(dst)[c] = cconv::f32_to_bf16(s);
 }
 
 static int sm_count(int* sms) {
@@ -323,25 +377,29 @@ static int sm_count(int* sms) {
 
 static int lanes_of(int64_t K) { return K <= 32 ? 4 : K <= 64 ? 8 : K <= 128 ? 16 : 32; }
 
-// Items and grid of a call.  With many tokens a group walks all heads of its token and the
-// table row is read once; with few, heads are dealt out until the machine is full or each
-// group has one batch.
-static void plan(NormArgs& p, int sms, int batch, int ctas_per_sm, int* grid) {
+// Items and grid of a call: kHeads heads an item where that fills the machine, else one head;
+// CTAs are dealt to queries and keys by their heads.
+static int plan(NormArgs& p, int64_t total, int sms, int ctas_per_sm) {
   const int lanes = lanes_of(p.K), groups = kThreads / lanes;
-  const int all = p.Hq + p.Hk;
-  const int64_t full = static_cast<int64_t>(sms) * ctas_per_sm * groups;
-  p.heads = (all + batch - 1) / batch * batch;
-  while (p.heads > batch && static_cast<int64_t>(p.total) * ((all + p.heads - 1) / p.heads) < full)
-    p.heads = (p.heads / 2 + batch - 1) / batch * batch;
-  if (p.total < full / all) p.heads = 1;
-  p.splits = (all + p.heads - 1) / p.heads;
-  p.items = static_cast<int64_t>(p.total) * p.splits;
-  const int64_t need = (p.items + groups - 1) / groups;
-  const int64_t most = static_cast<int64_t>(sms) * ctas_per_sm;
-  *grid = static_cast<int>(need < most ? need : most);
+  const int64_t all = p.side[0].H + p.side[1].H, most = static_cast<int64_t>(sms) * ctas_per_sm;
+  const int heads = total * all >= most * groups * kHeads ? kHeads : 1;
+  int64_t need[2];
+  for (int i = 0; i < 2; ++i) {
+    Side& s = p.side[i];
+    s.heads = heads;
+    s.splits = (s.H + heads - 1) / heads;
+    s.items = total * s.splits;
+    need[i] = (s.items + groups - 1) / groups;
+  }
+  int64_t q = need[0], k = need[1];
+  if (q + k > most) {
+    q = most * need[0] / (need[0] + need[1]);
+    q = q < 1 ? 1 : q > most - 1 ? most - 1 : q;
+    k = most - q;
+  }
+  p.ctas_q = static_cast<int>(q);
+  return static_cast<int>(q + k);
 }
-
-constexpr int kFwdCtas = 8, kBwdCtas = 4;  // CTAs per SM of a full grid
 
 static int check(const NormArgs& p, int64_t total, int64_t Hq, int64_t Hk, int64_t K, int wdt,
                  int mode, float eps, int64_t R, int64_t P) {
@@ -355,17 +413,18 @@ static int check(const NormArgs& p, int64_t total, int64_t Hq, int64_t Hk, int64
   if (R > 0) {
     if (!p.cos || !p.sin) return CCONV_ERR_NULL;
     if (P < 1 || (!p.pos && P < total)) return CCONV_ERR_SHAPE;
-    if (!aligned(p.cos, 16) || !aligned(p.sin, 16)) return CCONV_ERR_ALIGN;
+    if (!aligned(p.cos, 32) || !aligned(p.sin, 32)) return CCONV_ERR_ALIGN;
     if (p.pos && !aligned(p.pos, 4)) return CCONV_ERR_ALIGN;
   }
   const size_t ew = wdt == CCONV_F32 ? 4 : 2;
-  if (!aligned(p.wq, ew) || !aligned(p.wk, ew)) return CCONV_ERR_ALIGN;
+  if (!aligned(p.side[0].w, ew) || !aligned(p.side[1].w, ew)) return CCONV_ERR_ALIGN;
   if (total == 0) return CCONV_OK;
-  if (!p.q || !p.k || !p.oq || !p.ok) return CCONV_ERR_NULL;
-  int rc = check_rows(p.q, total, Hq, p.sqt, p.sqh);
-  if (rc == CCONV_OK) rc = check_rows(p.k, total, Hk, p.skt, p.skh);
+  const Side &q = p.side[0], &k = p.side[1];
+  if (!q.x || !k.x || !q.out || !k.out) return CCONV_ERR_NULL;
+  int rc = check_rows(q.x, total, Hq, q.st, q.sh);
+  if (rc == CCONV_OK) rc = check_rows(k.x, total, Hk, k.st, k.sh);
   if (rc != CCONV_OK) return rc;
-  return aligned(p.oq, 16) && aligned(p.ok, 16) ? CCONV_OK : CCONV_ERR_ALIGN;
+  return aligned(q.out, 16) && aligned(k.out, 16) ? CCONV_OK : CCONV_ERR_ALIGN;
 }
 
 using Kernel = void (*)(NormArgs);
@@ -397,21 +456,19 @@ extern "C" CCONV_API int cattn_qknorm_fwd(const void* q, int64_t sqt, int64_t sq
                                           void* yk, cconv_stream_t stream) {
   using namespace cattn;
   NormArgs p{};
-  p.q = static_cast<const uint16_t*>(q);
-  p.k = static_cast<const uint16_t*>(k);
-  p.oq = static_cast<uint16_t*>(yq);
-  p.ok = static_cast<uint16_t*>(yk);
-  p.sqt = sqt, p.sqh = sqh, p.skt = skt, p.skh = skh;
-  p.wq = wq, p.wk = wk, p.cos = cos, p.sin = sin, p.pos = positions;
+  p.side[0] = Side{static_cast<const uint16_t*>(q), nullptr, static_cast<uint16_t*>(yq), sqt, sqh, 0, 0,
+                   wq, static_cast<int>(Hq), 0, 0, 0};
+  p.side[1] = Side{static_cast<const uint16_t*>(k), nullptr, static_cast<uint16_t*>(yk), skt, skh, 0, 0,
+                   wk, static_cast<int>(Hk), 0, 0, 0};
+  p.cos = cos, p.sin = sin, p.pos = positions;
   const int rc = check(p, total, Hq, Hk, K, wdt, mode, eps, R, P);
   if (rc != CCONV_OK || total == 0) return rc;
-  p.P = P, p.total = static_cast<int>(total), p.Hq = static_cast<int>(Hq);
-  p.Hk = static_cast<int>(Hk), p.K = static_cast<int>(K), p.R = static_cast<int>(R), p.wdt = wdt;
+  p.P = P, p.K = static_cast<int>(K), p.R = static_cast<int>(R), p.wdt = wdt;
   p.inv = mode == CATTN_NORM_RMS ? 1.f / static_cast<float>(K) : 1.f;
   p.eps = eps;
-  int sms = 0, grid = 0;
+  int sms = 0;
   if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
-  plan(p, sms, kBatch, kFwdCtas, &grid);
+  const int grid = plan(p, total, sms, kFwdCtas);
   return launch_pdl(pick_fwd(lanes_of(K), interleaved != 0), dim3(grid), dim3(kThreads), 0, stream,
                     p) == cudaSuccess
              ? CCONV_OK
@@ -425,7 +482,7 @@ extern "C" CCONV_API int cattn_qknorm_bwd_workspace_bytes(int64_t total, int64_t
   if (total < 0 || total > kMaxRows || Hq < 1 || Hk < 1 || K < 1 || K > 256) return CCONV_ERR_SHAPE;
   int sms = 0;
   if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
-  *bytes = static_cast<size_t>(sms) * kBwdCtas * 2 * static_cast<size_t>(K) * 4;
+  *bytes = static_cast<size_t>(sms) * kBwdCtas * static_cast<size_t>(K) * 4;
   return CCONV_OK;
 }
 
@@ -438,15 +495,11 @@ extern "C" CCONV_API int cattn_qknorm_bwd(
     void* workspace, size_t workspace_bytes, cconv_stream_t stream) {
   using namespace cattn;
   NormArgs p{};
-  p.q = static_cast<const uint16_t*>(q);
-  p.k = static_cast<const uint16_t*>(k);
-  p.dyq = static_cast<const uint16_t*>(dyq);
-  p.dyk = static_cast<const uint16_t*>(dyk);
-  p.oq = static_cast<uint16_t*>(dq);
-  p.ok = static_cast<uint16_t*>(dk);
-  p.sqt = sqt, p.sqh = sqh, p.skt = skt, p.skh = skh;
-  p.syqt = syqt, p.syqh = syqh, p.sykt = sykt, p.sykh = sykh;
-  p.wq = wq, p.wk = wk, p.cos = cos, p.sin = sin, p.pos = positions;
+  p.side[0] = Side{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(dyq),
+                   static_cast<uint16_t*>(dq), sqt, sqh, syqt, syqh, wq, static_cast<int>(Hq), 0, 0, 0};
+  p.side[1] = Side{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(dyk),
+                   static_cast<uint16_t*>(dk), skt, skh, sykt, sykh, wk, static_cast<int>(Hk), 0, 0, 0};
+  p.cos = cos, p.sin = sin, p.pos = positions;
   int rc = check(p, total, Hq, Hk, K, wdt, mode, eps, R, P);
   if (rc != CCONV_OK) return rc;
   if (total > 0) {
@@ -461,17 +514,16 @@ extern "C" CCONV_API int cattn_qknorm_bwd(
   if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
   const bool sums = dwq || dwk;
   if (sums) {
-    if (!workspace || workspace_bytes < static_cast<size_t>(sms) * kBwdCtas * 2 * K * 4)
+    if (!workspace || workspace_bytes < static_cast<size_t>(sms) * kBwdCtas * K * 4)
       return CCONV_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return CCONV_ERR_ALIGN;
     p.part = static_cast<float*>(workspace);
   }
-  p.P = P, p.total = static_cast<int>(total), p.Hq = static_cast<int>(Hq);
-  p.Hk = static_cast<int>(Hk), p.K = static_cast<int>(K), p.R = static_cast<int>(R), p.wdt = wdt;
+  p.P = P, p.K = static_cast<int>(K), p.R = static_cast<int>(R), p.wdt = wdt;
   p.inv = mode == CATTN_NORM_RMS ? 1.f / static_cast<float>(K) : 1.f;
   p.eps = eps;
   if (total > 0) {
-    plan(p, sms, kBatchBwd, kBwdCtas, &grid);
+    grid = plan(p, total, sms, kBwdCtas);
     if (launch_pdl(pick_bwd(lanes_of(K), interleaved != 0), dim3(grid), dim3(kThreads), 0, stream,
                    p) != cudaSuccess)
       return CCONV_ERR_CUDA;
@@ -480,7 +532,7 @@ extern "C" CCONV_API int cattn_qknorm_bwd(
   const int cols = static_cast<int>(2 * K);
   return launch_pdl(cattn_qknorm_dw_kernel, dim3((cols + kReduceCols - 1) / kReduceCols),
                     dim3(kReduceCols, kReduceRows), 0, stream,
-                    static_cast<const float*>(workspace), grid, static_cast<int>(K),
+                    static_cast<const float*>(workspace), p.ctas_q, grid, static_cast<int>(K),
                     static_cast<int>(wdt), dwq, dwk) == cudaSuccess
              ? CCONV_OK
              : CCONV_ERR_CUDA;

@@ -53,7 +53,7 @@ typedef enum {
  *
  *   q, k      [total, Hq, K], [total, Hk, K] bf16, strided.  total may be 0.
  *   wq, wk    [K] weights in wdt, or NULL (no weight).
- *   cos, sin  [P, R/2] fp32 contiguous tables, 16-byte aligned; not read when R == 0.
+ *   cos, sin  [P, R/2] fp32 contiguous tables, 32-byte aligned; not read when R == 0.
  *   R         rotated channels: 0 <= R <= K, a multiple of 16.
  *   interleaved  0: channel c < R/2 pairs with c + R/2; 1: channel 2c pairs with 2c + 1.
  *             Pair c turns by table column c.
