@@ -24,6 +24,9 @@ struct FaultReader {
   explicit FaultReader(int (*read)(unsigned*));
 };
 
+int bind_context();
+int sm_count(int* sms);
+
 inline bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 // A [total, H, C] bf16 activation with strides (st, sh): the rules of cattn.h.
@@ -47,6 +50,20 @@ __device__ __forceinline__ void sequence_rows(const int32_t* cu, int i, int tota
 }
 
 __device__ __forceinline__ float clamp_decay(float g) { return g < -128.f ? -128.f : g; }
+
+// The offences of up to 32 state indices, one a lane (s: the lane's, -1 among them with pad).
+// Every lane of the warp gets the union.
+__device__ __forceinline__ unsigned check_indices(int s, int n, int64_t S, bool pad, int lane) {
+  unsigned bad = 0;
+  const bool live = lane < n && !(pad && s == -1);
+  if (live && s < 0) bad = CCONV_IDX_NEGATIVE;
+  if (live && s >= S) bad = CCONV_IDX_OUT_OF_RANGE;
+  const bool slot = live && bad == 0;
+  // lanes without a usable slot get values of their own
+  const unsigned same = __match_any_sync(0xffffffffu, slot ? s : -2 - lane);
+  if (slot && (same & (same - 1))) bad = CCONV_IDX_DUPLICATE;
+  return __reduce_or_sync(0xffffffffu, bad);
+}
 
 // Checks n state indices against S slots (negative, >= S, repeated; -1 allowed with pad), and
 // nseq + 1 row offsets when cu is given; writes status[0..1] when idx is given, and with

@@ -30,13 +30,61 @@ __device__ __forceinline__ uint64_t col_step(int j) {
 constexpr int kStateFloats = 128 * 128;        // a state in the workspace
 
 // Chunk offsets of the sequences: cstart[nseq + 1], an empty sequence has one (empty) chunk.
+// Up to kSmallPlan sequences, every CTA makes them itself (small_plan), with the checks of the
+// row offsets and state indices: that costs less than a launch before the kernels.
 struct Plan {
   const int32_t* cu;
   const int32_t* cstart;
   int nseq;
   int tiles;  // column tiles of V
   int heads;  // value heads
+  int small, total;
+  const int32_t* idx;  // state indices, their slots, and where the verdict goes
+  int64_t S;
+  int32_t* status;
 };
+constexpr int kSmallPlan = 32;
+struct SmallPlan {
+  int32_t cu[kSmallPlan + 1], cstart[kSmallPlan + 1];
+  int32_t usable;  // the state indices are
+};
+
+// All threads of the CTA; ends with a barrier.  `report`: this CTA writes the verdicts.
+__device__ __forceinline__ void small_plan(Plan& p, SmallPlan& s, bool report, unsigned* fault) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const int a = lane < p.nseq ? p.cu[lane] : 0, b = lane < p.nseq ? p.cu[lane + 1] : 0;
+    bool bad = lane < p.nseq && (b < a || (lane == 0 && a != 0) || (lane == p.nseq - 1 && b != p.total));
+    bad = __any_sync(0xffffffffu, bad);
+    int x = lane < p.nseq && !bad ? max(1, (b - a + kChunk - 1) / kChunk) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane < p.nseq) {
+      s.cu[lane] = a;
+      s.cu[lane + 1] = b;  // (lane + 1 writes the same value)
+      s.cstart[lane + 1] = x;
+    }
+    unsigned off = 0;
+    if (p.idx) off = check_indices(lane < p.nseq ? p.idx[lane] : -1, p.nseq, p.S, false, lane);
+    if (lane == 0) {
+      s.cstart[0] = 0;
+      s.usable = off == 0;
+      if (report) {
+        if (bad) atomicOr(fault, kFaultSeqlens);
+        if (p.idx) {
+          p.status[0] = off ? CCONV_ERR_INDEX : CCONV_OK;
+          p.status[1] = static_cast<int>(off);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  p.cu = s.cu;
+  p.cstart = s.cstart;
+}
 
 struct Range {
   int64_t u0, u1;  // units of this CTA, [u0, u1)

@@ -208,9 +208,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t tmem = *tmem_at;
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
+  __shared__ SmallPlan small;
+  Plan plan = p.plan;
+  if (plan.small) small_plan(plan, small, false, &g_fault_bwd);
 
   int nch;
-  const int64_t units = unit_count(p.plan, nch);
+  const int64_t units = unit_count(plan, nch);
   const int64_t parts = min(static_cast<int64_t>(gridDim.x), units);
   Range range{0, 0};
   if (blockIdx.x < parts) range = range_of(units, parts, blockIdx.x);
@@ -229,11 +232,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // ---- tiles ----
     if (elect_one()) {
       Walker w;
-      w.seek(&p.plan, nch, start);
+      w.seek(&plan, nch, start);
       int use = 0, part = 0;
       for (int i = 0; i < count && ok; ++i) {
         if (w.rows() > 0) {
-          const int hv = w.ht / p.plan.tiles, vt = w.ht % p.plan.tiles;
+          const int hv = w.ht / plan.tiles, vt = w.ht % plan.tiles;
           const int hk = hv / p.ratio, row = w.row0();
           const int pv = p.V - vt * 128 > kPanelCols ? 2 : 1;
 #pragma unroll 1
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const Gate& gt = gates[gs];
         const int n = gt.n, flags = gt.flags;
         if (n > 0) {
-          const int kv = (min(128, p.V - gt.ht % p.plan.tiles * 128) + 15) / 16, nv = kv * 16;
+          const int kv = (min(128, p.V - gt.ht % plan.tiles * 128) + 15) / 16, nv = kv * 16;
           const int steps = (n + 15) / 16;
           const uint32_t dv = mma_desc(nv, false, true);
 #pragma unroll 1
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const Gate& gt = gates[gs];
         const int n = gt.n;
         if (n > 0) {
-          const int nv = (min(128, p.V - gt.ht % p.plan.tiles * 128) + 15) / 16 * 16;
+          const int nv = (min(128, p.V - gt.ht % plan.tiles * 128) + 15) / 16 * 16;
           const int steps = (n + 15) / 16;
           if (!(ok = CATTN_WAIT(full + 8 * kVals, use))) break;
           if (n < kChunk && !(ok = CATTN_WAIT(fixed, fixes++))) break;
@@ -393,10 +396,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   } else {
     // ---- gates ----
     Walker w;
-    w.seek(&p.plan, nch, start);
+    w.seek(&plan, nch, start);
     for (int unit = 0; unit < count; ++unit) {
       const int gs = unit % kBwdGates, n = w.rows(), row0 = w.row0();
-      const int hv = w.ht / p.plan.tiles;
+      const int hv = w.ht / plan.tiles;
       float g[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -534,7 +537,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (n < kChunk) {
           // the tiles whose rows are summed over
           zero_rows(src, pk, n, kt, 128);
-          zero_rows(KV ? ao : av, p.V - gt.ht % p.plan.tiles * 128 > kPanelCols ? 2 : 1, n, kt, 128);
+          zero_rows(KV ? ao : av, p.V - gt.ht % plan.tiles * 128 > kPanelCols ? 2 : 1, n, kt, 128);
           cconv::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) bar_arrive(fixed);
@@ -582,7 +585,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!(ok = CATTN_WARP_WAIT(gfull + 8 * gs, unit / kBwdGates))) break;
       const Gate& gt = gates[gs];
       const int n = gt.n, flags = gt.flags;
-      const int hv = gt.ht / p.plan.tiles, vt = gt.ht % p.plan.tiles;
+      const int hv = gt.ht / plan.tiles, vt = gt.ht % plan.tiles;
       const int vw = min(128, p.V - vt * 128);
       if (flags & kSegment) {
 #pragma unroll
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const Gate& gt = gates[gs];
       const int n = gt.n, ht = gt.ht, row0 = gt.row0;
       if (n > 0) {
-        const int hv = ht / p.plan.tiles, vt = ht % p.plan.tiles, vw = min(128, p.V - vt * 128);
+        const int hv = ht / plan.tiles, vt = ht % plan.tiles, vw = min(128, p.V - vt * 128);
         const float rowf = KV ? gt.kw[row] : gt.er[row];
         f2 dot = 0;
         if (!(ok = CATTN_WARP_WAIT(full + 8 * kDot, use))) break;
@@ -702,7 +705,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         float d0, d1;
         cconv::f2_unpack(dot, d0, d1);
         if (row < n)
-          p.dots[(static_cast<int64_t>(p.plan.heads) * p.plan.tiles + ht) * p.rows + t] =
+          p.dots[(static_cast<int64_t>(plan.heads) * plan.tiles + ht) * p.rows + t] =
               p.scale * rowf * (d0 + d1);
         if (!(ok = CATTN_WARP_WAIT(ofull, use))) break;
         tc_fence_after();
@@ -794,7 +797,7 @@ int launch_chunk_bwd(const ChunkBwdCall& c, cudaStream_t stream) {
     rc = encode_tile_map(&a.out_v, Rows{c.dv, int64_t(c.s.Hv) * c.s.V, c.s.V}, c.s.total, c.s.Hv, c.s.V);
   if (rc == CCONV_OK) rc = out_map(&a.out_k, c.dq, c.part_q, c);
   if (rc != CCONV_OK) return rc;
-  a.plan = Plan{c.cu, c.cstart, c.s.nseq, (c.s.V + 127) / 128, c.s.Hv};
+  a.plan = Plan{c.cu, c.cstart, c.s.nseq, (c.s.V + 127) / 128, c.s.Hv, c.cstart == nullptr, c.s.total, nullptr, 0, nullptr};
   a.g = c.g;
   a.slots = c.slots;
   a.initial = c.initial;

@@ -60,13 +60,13 @@ struct ChunkArgs {
   Slots slots;
   const float* initial;
   float* fin;
-  const int32_t* status;
   uint16_t* o;
   float* carry;   // [grid] states handed on
   float* decay;   // [grid] their decays; negative: the sequence began in that range
   float* copy;    // [grid] initial states of split sequences (final_state may overwrite them)
   float scale;
   int rows, ratio, Hv, K, V;
+  int report;     // the tail kernel writes a small plan's verdicts (the backward's first)
 };
 
 #define CATTN_WAIT(bar, parity) (wait_phase((bar), static_cast<uint32_t>(parity) & 1u))
@@ -131,14 +131,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const uint32_t tmem = *tmem_at;
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
+  __shared__ SmallPlan small;
+  Plan plan = p.plan;
+  if (plan.small) small_plan(plan, small, blockIdx.x == 0, &g_fault_fwd);
 
   // The CTA's units.
   int nch;
-  const int64_t units = unit_count(p.plan, nch);
+  const int64_t units = unit_count(plan, nch);
   const int64_t parts = min(static_cast<int64_t>(gridDim.x), units);
   Range range{0, 0};
   if (blockIdx.x < parts) range = range_of(units, parts, blockIdx.x);
-  const Tail tail = tail_of<false>(p.plan, nch, units, range);
+  const Tail tail = tail_of<false>(plan, nch, units, range);
   const int64_t count = range.u1 - range.u0;
   const int pk = p.K > kPanelCols ? 2 : 1;
 
@@ -151,11 +154,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     // ---- tiles ----
     if (elect_one()) {
       Walker w;
-      w.seek(&p.plan, nch, range.u0);
+      w.seek(&plan, nch, range.u0);
       int chunk = 0, part = 0;
       for (int64_t i = 0; i < count && ok; ++i) {
         if (w.rows() > 0) {
-          const int hv = w.ht / p.plan.tiles, vt = w.ht % p.plan.tiles;
+          const int hv = w.ht / plan.tiles, vt = w.ht % plan.tiles;
           const int hk = hv / p.ratio, row = w.row0();
           const int pv = p.V - vt * 128 > kPanelCols ? 2 : 1;
 #pragma unroll 1
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const Gate& gt = gates[gs];
         const int n = gt.n, flags = gt.flags;
         if (n > 0) {
-          const int nv = (min(128, p.V - gt.ht % p.plan.tiles * 128) + 15) / 16 * 16;
+          const int nv = (min(128, p.V - gt.ht % plan.tiles * 128) + 15) / 16 * 16;
           const uint32_t d_out = mma_desc(nv, false, true);
           const int key = scs & 1;
           if (!(ok = CATTN_WAIT(full + 8 * key, scs >> 1))) break;
@@ -254,7 +257,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const Gate& gt = gates[gs];
         const int n = gt.n, flags = gt.flags;
         if (n > 0) {
-          const int nv = (min(128, p.V - gt.ht % p.plan.tiles * 128) + 15) / 16 * 16;
+          const int nv = (min(128, p.V - gt.ht % plan.tiles * 128) + 15) / 16 * 16;
           if (!(ok = CATTN_WAIT(full + 8 * kValue, chunk))) break;
           if (n < kChunk && !(ok = CATTN_WAIT(vfixed, fixes++))) break;
           ++chunk;
@@ -290,11 +293,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   } else if (warp == 2) {
     // ---- gates ----
     Walker w;
-    w.seek(&p.plan, nch, range.u0);
+    w.seek(&plan, nch, range.u0);
     for (int64_t i = 0; i < count; ++i) {
       const int unit = static_cast<int>(i);
       const int gs = unit % kGateStages, n = w.rows(), row0 = w.row0();
-      const int hv = w.ht / p.plan.tiles;
+      const int hv = w.ht / plan.tiles;
       float g[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -383,7 +386,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         tc_fence_before();
         if (!(ok = CATTN_WARP_WAIT(full + 8 * kValue, scs))) break;
         if (n < kChunk) {
-          zero_rows(smem + kValue * kTileBytes, p.V - ht % p.plan.tiles * 128 > kPanelCols ? 2 : 1, n, row,
+          zero_rows(smem + kValue * kTileBytes, p.V - ht % plan.tiles * 128 > kPanelCols ? 2 : 1, n, row,
                     128);
           cconv::fence_proxy_async_smem();
         }
@@ -395,8 +398,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (!(ok = CATTN_WARP_WAIT(ofull, scs))) break;
         ++scs;
         tc_fence_after();
-        const int vt = ht % p.plan.tiles, vw = min(128, p.V - vt * 128);
-        uint16_t* dst = p.o + (static_cast<int64_t>(row0 + row) * p.Hv + ht / p.plan.tiles) * p.V +
+        const int vt = ht % plan.tiles, vw = min(128, p.V - vt * 128);
+        uint16_t* dst = p.o + (static_cast<int64_t>(row0 + row) * p.Hv + ht / plan.tiles) * p.V +
                         vt * 128;
         const f2 es = f2_splat(p.scale * er), sc = f2_splat(p.scale);
         // The outputs of a full chunk leave through the buffer of the bf16 state (Q S is done, and
@@ -441,7 +444,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if (whole) {
 #pragma unroll 1
             for (int c = 0; c < vw; c += kPanelCols)
-              store_box(&p.mo, smem + kOffS + (c >> 6) * kPanelBytes, vt * 128 + c, ht / p.plan.tiles,
+              store_box(&p.mo, smem + kOffS + (c >> 6) * kPanelBytes, vt * 128 + c, ht / plan.tiles,
                         row0);
             stores_commit();
             stores_wait_read();
@@ -508,7 +511,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (!(ok = CATTN_WARP_WAIT(gfull + 8 * (gs), unit / kGateStages))) break;
       const Gate& gt = gates[gs];
       const int n = gt.n, flags = gt.flags, ht = gt.ht;
-      const int hv = ht / p.plan.tiles, vt = ht % p.plan.tiles;
+      const int hv = ht / plan.tiles, vt = ht % plan.tiles;
       const int vw = min(128, p.V - vt * 128);
       if (flags & kSegment) {
         const int64_t slot = p.slots.of(gt.seq);
@@ -565,7 +568,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (lane == 0) bar_arrive(kvfree);
       }
       if (n > 0) ++done;
-      if ((flags & kFinish) && krow < p.K && !(p.status && p.status[0] != CCONV_OK)) {
+      if ((flags & kFinish) && krow < p.K &&
+          (!plan.idx || (plan.small ? small.usable != 0 : plan.status[0] == CCONV_OK))) {
         const int64_t slot = p.slots.of(gt.seq);
         float* dst = p.fin + ((slot * p.Hv + hv) * p.K + krow) * p.V + vt * 128;
         if (slot >= 0) {
@@ -659,13 +663,16 @@ __global__ void __launch_bounds__(kTailThreads, 1)
   const uint32_t tmem = *tmem_at;
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
+  __shared__ SmallPlan small;
+  Plan plan = p.plan;
+  if (plan.small) small_plan(plan, small, p.report && blockIdx.x == 0, &g_fault_fwd);
 
   int nch;
-  const int64_t units = unit_count(p.plan, nch);
+  const int64_t units = unit_count(plan, nch);
   const int64_t parts = min(static_cast<int64_t>(gridDim.x), units);
   Range range{0, 0};
   if (blockIdx.x < parts) range = range_of(units, parts, blockIdx.x);
-  const Tail tail = tail_of<REV>(p.plan, nch, units, range);
+  const Tail tail = tail_of<REV>(plan, nch, units, range);
   const int count = static_cast<int>(tail.u1 - tail.u0);
   const int64_t start = REV ? tail.u0 : tail.u1 - 1;
   const int pk = p.K > kPanelCols ? 2 : 1;
@@ -679,7 +686,7 @@ __global__ void __launch_bounds__(kTailThreads, 1)
           const int gs = unit % kTailGates;
           if (!(ok = CATTN_WAIT(gfull + 8 * gs, unit / kTailGates))) break;
           const TailGate& gt = gates[gs];
-          const int hv = gt.ht / p.plan.tiles, vt = gt.ht % p.plan.tiles, row = gt.row0;
+          const int hv = gt.ht / plan.tiles, vt = gt.ht % plan.tiles, row = gt.row0;
           const int pv = p.V - vt * 128 > kPanelCols ? 2 : 1;
           const bool last = gt.last;
 #pragma unroll 1
@@ -709,7 +716,7 @@ __global__ void __launch_bounds__(kTailThreads, 1)
           const TailGate& gt = gates[gs];
           const int n = gt.n;
           const bool last = gt.last;
-          const int nv = (min(128, p.V - gt.ht % p.plan.tiles * 128) + 15) / 16 * 16;
+          const int nv = (min(128, p.V - gt.ht % plan.tiles * 128) + 15) / 16 * 16;
           const int tk = 2 * unit, tv = tk + 1;
           if (!(ok = CATTN_WAIT(full + 8 * (tv % kTailSlots), tv / kTailSlots))) break;
           if (n < kChunk && !(ok = CATTN_WAIT(vfixed, 0))) break;
@@ -741,9 +748,9 @@ __global__ void __launch_bounds__(kTailThreads, 1)
     } else if (warp == 2) {
       // ---- gates ----
       Walker w;
-      w.seek(&p.plan, nch, start);
+      w.seek(&plan, nch, start);
       float g[4], run = 0.f;
-      const int hv = w.ht / p.plan.tiles;
+      const int hv = w.ht / plan.tiles;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         g[j] = 4 * lane + j < w.rows() ? kLog2e * p.g.at(w.row0() + 4 * lane + j, hv) : 0.f;
@@ -807,7 +814,7 @@ __global__ void __launch_bounds__(kTailThreads, 1)
         if (n < kChunk) {  // a sequence's last chunk: once in a tail
           if (!(ok = CATTN_WARP_WAIT(full + 8 * (tv % kTailSlots), tv / kTailSlots))) break;
           zero_rows(smem + tv % kTailSlots * kTileBytes,
-                    p.V - ht % p.plan.tiles * 128 > kPanelCols ? 2 : 1, n, kt, kTailKeyWarps * 32);
+                    p.V - ht % plan.tiles * 128 > kPanelCols ? 2 : 1, n, kt, kTailKeyWarps * 32);
           cconv::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) bar_arrive(vfixed);
@@ -839,7 +846,7 @@ __global__ void __launch_bounds__(kTailThreads, 1)
         tc_fence_after();
         const int krow = threadIdx.x - 128;
         const uint32_t lanes = static_cast<uint32_t>(krow & ~31) << 16;
-        const int hv = ht / p.plan.tiles, vt = ht % p.plan.tiles, vw = min(128, p.V - vt * 128);
+        const int hv = ht / plan.tiles, vt = ht % plan.tiles, vw = min(128, p.V - vt * 128);
         const int64_t slot = p.slots.of(seq);
         const float rest = exp2_fast(*passed);
         const bool start_state = !REV && tail.closed && p.initial && slot >= 0 && krow < p.K;
@@ -944,7 +951,8 @@ int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream) {
   ChunkArgs a{};
   int rc = CCONV_OK;
   if (c.s.total > 0) {
-    rc = encode_tile_map(&a.mq, c.q, c.s.total, c.s.Hk, c.s.K);
+    rc = bind_context();
+    if (rc == CCONV_OK) rc = encode_tile_map(&a.mq, c.q, c.s.total, c.s.Hk, c.s.K);
     if (rc == CCONV_OK) rc = encode_tile_map(&a.mk, c.k, c.s.total, c.s.Hk, c.s.K);
     if (rc == CCONV_OK) rc = encode_tile_map(&a.mv, c.v, c.s.total, c.s.Hv, c.s.V);
     if (rc == CCONV_OK && c.part == kForward)
@@ -952,12 +960,12 @@ int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream) {
     if (rc != CCONV_OK) return rc;
   }
   const int tiles = (c.s.V + 127) / 128;
-  a.plan = Plan{c.cu, c.cstart, c.s.nseq, tiles, c.s.Hv};
+  a.plan = Plan{c.cu, c.cstart, c.s.nseq, tiles, c.s.Hv, c.cstart == nullptr, c.s.total, c.slots.idx, c.slots.S, c.status};
   a.g = c.g;
   a.slots = c.slots;
   a.initial = c.initial;
   a.fin = c.fin;
-  a.status = c.status;
+  a.report = c.part == kStates;
   a.o = c.o;
   a.carry = c.carry;
   a.copy = c.carry + static_cast<int64_t>(c.grid) * kStateFloats;
@@ -966,6 +974,9 @@ int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream) {
   a.rows = c.s.total;
   a.ratio = c.s.Hv / c.s.Hk;
   a.Hv = c.s.Hv, a.K = c.s.K, a.V = c.s.V;
+  // with at most 128 rows no sequence has a second chunk, and nothing is handed on
+  if (c.part == kForward && c.s.total <= kChunk)
+    return launch(cattn_linear_chunk_kernel, kFwdThreads, kFwdBytes, a, c.grid, stream);
   rc = launch(c.part == kStateGrads ? cattn_linear_tail_kernel<true> : cattn_linear_tail_kernel<false>,
               kTailThreads, kTailBytes, a, c.grid, stream);
   if (rc != CCONV_OK || c.part != kForward) return rc;

