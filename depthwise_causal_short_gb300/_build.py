@@ -5,7 +5,8 @@
 Each translation unit is compiled in parallel for sm_103a only; ``csrc/*.cu`` are linked into
 ``libcconv.so`` (C ABI: ``include/cconv.h``), ``csrc/attn/*.cu`` into ``libcattn.so`` (C ABI:
 ``include/cattn.h``), with hidden visibility for everything else and the CUDA runtime linked
-statically.
+statically.  ``csrc/attn/py/attn_py.cpp`` becomes ``_cattn.so``, libcattn's PyTorch binding (a
+CPython extension, host compiler).
 """
 from __future__ import annotations
 
@@ -23,6 +24,7 @@ OBJ_DIR = PKG / "_build"
 LIB_DIR = PKG / "_lib"
 LIB = LIB_DIR / "libcconv.so"
 ATTN_LIB = LIB_DIR / "libcattn.so"
+ATTN_PY = LIB_DIR / "_cattn.so"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [
@@ -47,9 +49,15 @@ def attn_sources() -> list[Path]:
     return sorted((CSRC / "attn").glob("*.cu"))
 
 
+def attn_binding() -> Path:
+    return CSRC / "attn" / "py" / "attn_py.cpp"
+
+
 def _inputs(lib: Path) -> list[Path]:
     """Everything `lib` is built from."""
     shared = sorted(CSRC.glob("*.cuh")) + [INCLUDE / "cconv.h", Path(__file__)]
+    if lib == ATTN_PY:
+        return [attn_binding(), INCLUDE / "cattn.h", INCLUDE / "cconv.h", Path(__file__)]
     if lib == LIB:
         return sources() + shared
     return attn_sources() + sorted((CSRC / "attn").glob("*.cuh")) + [INCLUDE / "cattn.h"] + shared
@@ -63,14 +71,15 @@ def _newer(lib: Path) -> bool:
 
 
 def up_to_date() -> bool:
-    return _newer(LIB) and _newer(ATTN_LIB)
+    return _newer(LIB) and _newer(ATTN_LIB) and _newer(ATTN_PY)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> Path:
     """Compile and link each library unless it is newer than every source of it."""
     todo = [(lib, srcs) for lib, srcs in ((LIB, sources()), (ATTN_LIB, attn_sources()))
             if force or extra_flags or not _newer(lib)]
-    if not todo:
+    binding = force or not _newer(ATTN_PY)
+    if not todo and not binding:
         return LIB
     OBJ_DIR.mkdir(parents=True, exist_ok=True)
     LIB_DIR.mkdir(parents=True, exist_ok=True)
@@ -87,16 +96,41 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        built = {src: ex.submit(compile_one, src) for _, srcs in todo for src in srcs}
-    for lib, srcs in todo:
-        objs = [built[src].result() for src in srcs]
-        tmp = lib.with_suffix(f".{os.getpid()}.tmp")
-        cmd = [exe, *ARCH, "-shared", "-cudart", "static", "-o", str(tmp), *map(str, objs)]
+    def compile_binding() -> Path:
+        import sysconfig
+
+        import torch
+        root = Path(torch.__file__).resolve().parent
+        obj = OBJ_DIR / "attn_py.o"
+        cuda = Path(exe).resolve().parent.parent
+        dirs = [root / "include", root / "include" / "torch" / "csrc" / "api" / "include",
+                cuda / "include", sysconfig.get_paths()["include"]]
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               *[a for d in dirs for a in ("-isystem", str(d))], "-c", str(attn_binding()), "-o", str(obj)]
         r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on {attn_binding().name}:\n{r.stdout}\n{r.stderr}")
+        return obj
+
+    def link(lib: Path, cmd: list[str]):
+        tmp = lib.with_suffix(f".{os.getpid()}.tmp")
+        r = subprocess.run([*cmd, "-o", str(tmp)], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link of {lib.name} failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, lib)
+
+    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        py_obj = ex.submit(compile_binding) if binding else None
+        built = {src: ex.submit(compile_one, src) for _, srcs in todo for src in srcs}
+    for lib, srcs in todo:
+        link(lib, [exe, *ARCH, "-shared", "-cudart", "static", *[str(built[src].result()) for src in srcs]])
+    if py_obj is not None:
+        import torch
+        libs = Path(torch.__file__).resolve().parent / "lib"
+        link(ATTN_PY, ["g++", "-shared", str(py_obj.result()), f"-L{LIB_DIR}", "-lcattn",
+                       "-Wl,-rpath,$ORIGIN", f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+                       "-lc10_cuda"])
     return LIB
 
 

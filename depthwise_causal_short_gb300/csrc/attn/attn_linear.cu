@@ -272,14 +272,16 @@ extern "C" CCONV_API int cattn_linear_bwd(
     rc = check_states(cu_seqlens, nseq, Hv, initial_state, nullptr, state_indices, S, status_dev);
   if (rc != CCONV_OK) return rc;
   if (!aligned(d_initial_state, 16)) return CCONV_ERR_ALIGN;
-  int grid = 0;
-  if (chunk_grid(total, nseq, Hv, V, &grid) != CCONV_OK) return CCONV_ERR_CUDA;
-  const BwdWork w = bwd_work(total, nseq, Hk, Hv, K, V, grid);
   if (total > 0) {
     if (!do_ || !dq || !dk || !dg) return CCONV_ERR_NULL;
     rc = check_rows(do_, total, Hv, sot, soh);
     if (rc != CCONV_OK) return rc;
     if (!aligned(dq, 16) || !aligned(dk, 16) || !aligned(dg, 16)) return CCONV_ERR_ALIGN;
+  }
+  int grid = 0;
+  if (chunk_grid(total, nseq, Hv, V, &grid) != CCONV_OK) return CCONV_ERR_CUDA;
+  const BwdWork w = bwd_work(total, nseq, Hk, Hv, K, V, grid);
+  if (total > 0) {
     if (!workspace || workspace_bytes < w.bytes) return CCONV_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return CCONV_ERR_ALIGN;
   }
