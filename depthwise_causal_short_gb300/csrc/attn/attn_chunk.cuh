@@ -217,6 +217,7 @@ enum GateFlags : int {
   kNeedKv = 8,    // the state after it is needed
   kFinish = 16,   // and it is the sequence's last: a final state
   kSplitSeq = 32, // this sequence began in this range and goes on in the next
+  kAnchor = 64,   // the range's first unit, inside a sequence
 };
 
 using cconv::f2;

@@ -15,7 +15,9 @@
 // pairs that are not a token with itself: inside the chunk scale * sum M1 . M2 . L without the
 // diagonal, whose factors come from fp32 products of the inputs and are never rounded; across
 // chunks scale * er * q . (dO S^T) and scale * kw * k . (V D^T), for which S and D are read as
-// two bf16 terms (16 bits).
+// two bf16 terms (16 bits).  Summed over a whole sequence, those 16 bits would show (2.7e-5 of the
+// dg of heads that forget fast, 8192 tokens): so each range also gives dg at its start as the
+// product of the two whole fp32 states, and the sums in between are tied to these anchors.
 //
 // Roles of the 20 warps: one warp streams tiles, one thread issues the products of the outputs
 // and one those of the state, one warp makes the gates; four warps each turn score tiles into P,
@@ -76,6 +78,8 @@ struct BwdArgs {
   uint16_t *dqk, *dv;       // dq or dk in bf16 where one unit makes a row of them, else
   float* part;              // [units' (head, tile)][total][K] partial sums
   float* dots;              // [2][heads * tiles][total]
+  float* states;            // [grid] the states before the ranges: the first sweep's, for anchors
+  float* anchors;           // KV: [grid][4] parts of scale <D, S> there
   const float* carry;       // states handed on
   const float* decay;
   float scale;
@@ -418,7 +422,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if ((f & kSegment) && !first) f |= kMiddle;
         if (!first || (!KV && p.initial)) f |= kHasState;
         if (KV && last && p.dinit) f |= kFinish;
-        if ((!last && unit + 1 < count) || (f & kFinish)) f |= kNeedKv;
+        if (KV ? !last || (f & kFinish) : !last && unit + 1 < count) f |= kNeedKv;
+        if (KV && !last && unit + 1 == count) f |= kAnchor;
         gt.flags = f;
       }
       __syncwarp();
@@ -593,6 +598,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (flags & kMiddle) {
           // what the ranges before this one (after it, for KV) hand on
           gather_state(S, p.carry, p.decay, blockIdx.x, parts, KV ? 1 : -1, krow);
+          if (!KV) put_state(S, p.states + static_cast<int64_t>(blockIdx.x) * kStateFloats, krow);
         } else if (!KV && p.initial && krow < p.K) {
           const int64_t slot = p.slots.of(gt.seq);
           const float* src = p.initial + ((slot * p.Hv + hv) * p.K + krow) * p.V + vt * 128;
@@ -644,6 +650,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (lane == 0) bar_arrive(kvfree);
       }
       if (n > 0) ++done;
+      if (KV && (flags & kAnchor)) {
+        // dg of the range's first token: the pairs across its start, from both whole states
+        const ulonglong2* at = reinterpret_cast<const ulonglong2*>(
+            p.states + static_cast<int64_t>(blockIdx.x) * kStateFloats);
+        f2 sum = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (krow < p.K && 4 * i < vw) {
+            const ulonglong2 x = at[i * 128 + krow];
+            sum = f2_fma(S[2 * i], x.x, f2_fma(S[2 * i + 1], x.y, sum));
+          }
+        float a, b;
+        cconv::f2_unpack(sum, a, b);
+        a += b;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        if (lane == 0) p.anchors[blockIdx.x * 4 + krow / 32] = p.scale * a;
+      }
       if (KV && (flags & kFinish) && krow < p.K) {
         float* dst = p.dinit + ((static_cast<int64_t>(gt.seq) * p.Hv + hv) * p.K + krow) * p.V + vt * 128;
         const f2 sc = f2_splat(p.scale);
@@ -809,6 +833,9 @@ int launch_chunk_bwd(const ChunkBwdCall& c, cudaStream_t stream) {
   a.carry = c.carry_s;
   a.decay = c.carry_s + static_cast<int64_t>(c.grid) * 2 * kStateFloats;
   a.part = c.part_q, a.dots = c.dots_q;
+  // (the hand-on kernels use neither of these for the backward)
+  a.states = c.carry_s + static_cast<int64_t>(c.grid) * kStateFloats;
+  a.anchors = c.carry_d + static_cast<int64_t>(c.grid) * kStateFloats;
   rc = launch_sweep<false>(a, c.grid, stream);
   if (rc == CCONV_OK) rc = out_map(&a.out_k, c.dk, c.part_k, c);
   if (rc != CCONV_OK) return rc;

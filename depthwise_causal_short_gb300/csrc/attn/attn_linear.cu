@@ -10,6 +10,7 @@
 // and q_i . dq'_i sums the pairs j < i that end at i, k_j . dk'_j the pairs i > j that start at
 // j.  (With the products i = j in both sums they would cancel only to rounding, and drown the
 // dg of heads that forget fast.)
+#include "attn_chunk.cuh"
 #include "attn_chunk_host.h"
 
 namespace cattn {
@@ -45,56 +46,112 @@ __global__ void __launch_bounds__(256)
                  f2_to_bf16x2(f2_pack(b.x, b.y)), f2_to_bf16x2(f2_pack(b.z, b.w)));
 }
 
-// dg_t = sum over i >= t of its sequence of (qdot_i - kdot_i), each the sum of `slices` times
-// `tiles` parts.  One CTA for each sequence and value head walks from the last token in steps of
-// kDgThreads * kDgPer: a thread sums kDgPer tokens, warps and CTA scan the sums.
+// dg of one sequence and value head, from the rows' sums x_i = qdot_i - kdot_i:
+//   dg_t = dg_b + sum of x_i over t <= i < b
+// between the anchors a <= t < b: the starts of the ranges that lie in the sequence (where
+// dg_a = scale <D, S> is known from the whole states), the sequence's end (0), and its start
+// (0 without an initial state; with one not known).  What the sum to a misses of dg_a, rounding of the x_i, is
+// spread evenly over the tokens between.  One CTA for each sequence and head, column tile
+// by column tile, in steps of kDgThreads * kDgPer tokens from the end.
 constexpr int kDgThreads = 512, kDgPer = 4;
-__global__ void __launch_bounds__(kDgThreads)
-    cattn_linear_dg_kernel(const float* qdot, const float* kdot, int slices, int tiles,
-                           LinearShape s, const int32_t* cu, float* dg) {
+constexpr int kSlices = 2;  // parts of a unit's dots
+
+struct DgArgs {
+  Plan plan;
+  const float *qdot, *kdot;  // [kSlices][heads * tiles][total]
+  const float* anchors;      // [grid][4]
+  int grid, open;            // ranges; whether the sequences have initial states
+  float* dg;
+};
+
+__global__ void __launch_bounds__(kDgThreads) cattn_linear_dg_kernel(const __grid_constant__ DgArgs p) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
+  __shared__ SmallPlan small;
   __shared__ float sums[kDgThreads / 32];
+  Plan plan = p.plan;
+  if (plan.small) small_plan(plan, small, false, nullptr);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int seq = static_cast<int>(blockIdx.x) / s.Hv, h = static_cast<int>(blockIdx.x) % s.Hv;
-  int t0, t1;
-  sequence_rows(cu, seq, s.total, t0, t1);
-  const int64_t slice = static_cast<int64_t>(s.Hv) * tiles * s.total;
-  float carry = 0.f;
-  for (int hi = t1; hi > t0; hi -= kDgThreads * kDgPer) {
-    // this thread's tokens are top, top - 1, ..
-    const int top = hi - 1 - static_cast<int>(threadIdx.x) * kDgPer;
-    float x[kDgPer];
+  const int seq = static_cast<int>(blockIdx.x) / plan.heads, h = static_cast<int>(blockIdx.x) % plan.heads;
+  int nch;
+  const int64_t units = unit_count(plan, nch);
+  if (units == 0) return;
+  const int64_t parts = min(static_cast<int64_t>(p.grid), units);
+  const int cs = plan.cstart[seq], ce = plan.cstart[seq + 1];
+  const int t0 = plan.cu[seq], t1 = plan.cu[seq + 1];
+  const int64_t slice = static_cast<int64_t>(plan.heads) * plan.tiles * plan.total;
+  constexpr int kStep = kDgThreads * kDgPer;
+
+  for (int tile = 0; tile < plan.tiles; ++tile) {
+    const int64_t ht = static_cast<int64_t>(h) * plan.tiles + tile;
+    const int64_t first = ht * nch + cs, end = ht * nch + ce;
+    const float *q = p.qdot + ht * plan.total, *k = p.kdot + ht * plan.total;
+    // x of this thread's tokens top, top - 1, .. above `from`, and their running sums
+    auto load = [&](int top, int from, float* x) {
 #pragma unroll
-    for (int k = 0; k < kDgPer; ++k) x[k] = 0.f;
-    for (int i = 0; i < slices; ++i)
-      for (int j = 0; j < tiles; ++j) {
-        const int64_t at = i * slice + (static_cast<int64_t>(h) * tiles + j) * s.total + top;
+      for (int j = 0; j < kDgPer; ++j) x[j] = 0.f;
 #pragma unroll
-        for (int k = 0; k < kDgPer; ++k)
-          if (top - k >= t0) x[k] += qdot[at - k] - kdot[at - k];
+      for (int i = 0; i < kSlices; ++i)
+#pragma unroll
+        for (int j = 0; j < kDgPer; ++j)
+          if (top - j >= from) x[j] += q[i * slice + top - j] - k[i * slice + top - j];
+#pragma unroll
+      for (int j = 1; j < kDgPer; ++j) x[j] += x[j - 1];
+    };
+    int64_t i = (end * parts + units - 1) / units - 1;  // the last range that starts before `end`
+    int right = t1;
+    float known = 0.f;  // dg at `right`
+    while (right > t0) {
+      const int64_t at = units * i / parts;
+      const bool inside = at > first;
+      const int left = inside ? t0 + static_cast<int>(at - first) * kChunk : t0;
+      const bool tied = inside || !p.open;
+      const float* a = p.anchors + 4 * i;
+      const float anchor = inside ? (a[0] + a[1]) + (a[2] + a[3]) : 0.f;
+      float total = 0.f, x[kDgPer];
+      for (int hi = right; hi > left; hi -= kStep) {
+        load(hi - 1 - static_cast<int>(threadIdx.x) * kDgPer, left, x);
+        float s = x[kDgPer - 1];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) sums[warp] = s;
+        __syncthreads();
+        for (int w = 0; w < kDgThreads / 32; ++w) total += sums[w];
+        __syncthreads();
       }
+      const float miss = tied ? (anchor - (known + total)) / static_cast<float>(right - left) : 0.f;
+      float carry = known;
+      for (int hi = right; hi > left; hi -= kStep) {
+        const int top = hi - 1 - static_cast<int>(threadIdx.x) * kDgPer;
+        load(top, left, x);
+        float run = x[kDgPer - 1];
 #pragma unroll
-    for (int k = 1; k < kDgPer; ++k) x[k] += x[k - 1];
-    float run = x[kDgPer - 1];
+        for (int o = 1; o < 32; o <<= 1) {
+          const float y = __shfl_up_sync(0xffffffffu, run, o);
+          if (lane >= o) run += y;
+        }
+        if (lane == 31) sums[warp] = run;
+        __syncthreads();
+        float before = carry;
+        for (int w = 0; w < kDgThreads / 32; ++w) {
+          if (w < warp) before += sums[w];
+          carry += sums[w];
+        }
+        __syncthreads();
+        const float other = __shfl_up_sync(0xffffffffu, run, 1);  // the lanes before this one
+        if (lane > 0) before += other;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const float y = __shfl_up_sync(0xffffffffu, run, o);
-      if (lane >= o) run += y;
+        for (int j = 0; j < kDgPer; ++j)
+          if (top - j >= left) {
+            const float v = before + x[j] + miss * static_cast<float>(right - (top - j));
+            float* to = p.dg + static_cast<int64_t>(top - j) * plan.heads + h;
+            *to = tile ? *to + v : v;
+          }
+      }
+      known = tied ? anchor : known + total;
+      right = left;
+      --i;
     }
-    if (lane == 31) sums[warp] = run;
-    __syncthreads();
-    float before = carry;
-    for (int w = 0; w < kDgThreads / 32; ++w) {
-      if (w < warp) before += sums[w];
-      carry += sums[w];
-    }
-    __syncthreads();
-    const float other = __shfl_up_sync(0xffffffffu, run, 1);  // the lanes before this one
-    if (lane > 0) before += other;
-#pragma unroll
-    for (int k = 0; k < kDgPer; ++k)
-      if (top - k >= t0) dg[static_cast<int64_t>(top - k) * s.Hv + h] = before + x[k];
   }
 }
 
@@ -158,8 +215,6 @@ static int chunk_grid(int64_t total, int64_t nseq, int64_t Hv, int64_t V, int* g
 
 // The chunk offsets at the head of the workspace.
 static size_t offsets_bytes(int64_t nseq) { return (static_cast<size_t>(nseq + 1) * 4 + 15) / 16 * 16; }
-
-constexpr int kSlices = 2;  // parts of a unit's dots
 
 // What a backward call keeps in its workspace, from a 256-byte boundary.
 struct BwdWork {
@@ -349,10 +404,14 @@ extern "C" CCONV_API int cattn_linear_bwd(
                      parts, side ? c.dk : c.dq) != cudaSuccess)
         return CCONV_ERR_CUDA;
   }
-  return launch_pdl(cattn_linear_dg_kernel, dim3(static_cast<unsigned>(nseq * Hv)), dim3(kDgThreads),
-                    0, stream, static_cast<const float*>(c.dots_q),
-                    static_cast<const float*>(c.dots_k), kSlices, tiles, c.s, cu_seqlens,
-                    dg) == cudaSuccess
+  DgArgs d{};
+  d.plan = Plan{cu_seqlens, cstart, c.s.nseq, tiles, c.s.Hv, cstart == nullptr, c.s.total, nullptr, 0, nullptr};
+  d.qdot = c.dots_q, d.kdot = c.dots_k;
+  d.anchors = c.carry_d + static_cast<int64_t>(grid) * kStateFloats;
+  d.grid = grid, d.open = initial_state != nullptr;
+  d.dg = dg;
+  return launch_pdl(cattn_linear_dg_kernel, dim3(static_cast<unsigned>(nseq * Hv)), dim3(kDgThreads), 0,
+                    stream, d) == cudaSuccess
              ? CCONV_OK
              : CCONV_ERR_CUDA;
 }
