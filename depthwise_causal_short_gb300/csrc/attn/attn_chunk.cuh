@@ -28,6 +28,9 @@ __device__ __forceinline__ uint64_t col_step(int j) {
 }
 
 constexpr int kStateFloats = 128 * 128;        // a state in the workspace
+// In place of the decay of what a range hands on: its sequence starts (ends) there; nothing is
+// handed on.
+constexpr float kChainStart = -1.f, kNoTail = -2.f;
 
 // Chunk offsets of the sequences: cstart[nseq + 1], an empty sequence has one (empty) chunk.
 // Up to kSmallPlan sequences, every CTA makes them itself (small_plan), with the checks of the
@@ -335,10 +338,22 @@ __device__ __forceinline__ void put_state(const f2* S, float* dst, int row) {
   for (int i = 0; i < 32; ++i) to[i * 128 + row] = make_ulonglong2(S[2 * i], S[2 * i + 1]);
 }
 
+// A row of a state in memory, `width` of its columns.
+__device__ __forceinline__ void load_state(f2* S, const float* src, int width) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    Pairs4 x{};
+    if (8 * i < width) x = ld_pairs(src + 8 * i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) S[4 * i + j] = x.v[j];
+  }
+}
+
 // Adds up what the ranges next to range `at` hand on (by = -1: those before it, 1: after it), to
-// the one where the sequence starts (ends).
+// the one where the sequence starts (ends); the nearest one's is the whole where they are joined.
 __device__ __forceinline__ void gather_state(f2* S, const float* carry, const float* decay,
-                                             int64_t at, int64_t parts, int by, int row) {
+                                             int64_t at, int64_t parts, int by, bool joined,
+                                             int row) {
   float coef = 1.f;
   for (int64_t j = at + by; j >= 0 && j < parts; j += by) {
     const ulonglong2* src = reinterpret_cast<const ulonglong2*>(carry + j * kStateFloats);
@@ -350,7 +365,7 @@ __device__ __forceinline__ void gather_state(f2* S, const float* carry, const fl
       S[2 * i] = f2_fma(c, x.x, S[2 * i]);
       S[2 * i + 1] = f2_fma(c, x.y, S[2 * i + 1]);
     }
-    if (d < 0.f) break;
+    if (joined || d < 0.f) break;
     coef *= d;
     if (coef == 0.f) break;
   }

@@ -84,6 +84,7 @@ struct BwdArgs {
   const float* decay;
   float scale;
   int rows, ratio, Hk, Hv, K, V;
+  int joined;               // the states handed on are whole
 };
 
 #define CATTN_WAIT(bar, parity) (wait_phase((bar), static_cast<uint32_t>(parity) & 1u))
@@ -597,17 +598,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int i = 0; i < 64; ++i) S[i] = 0;
         if (flags & kMiddle) {
           // what the ranges before this one (after it, for KV) hand on
-          gather_state(S, p.carry, p.decay, blockIdx.x, parts, KV ? 1 : -1, krow);
+          gather_state(S, p.carry, p.decay, blockIdx.x, parts, KV ? 1 : -1, p.joined, krow);
           if (!KV) put_state(S, p.states + static_cast<int64_t>(blockIdx.x) * kStateFloats, krow);
         } else if (!KV && p.initial && krow < p.K) {
           const int64_t slot = p.slots.of(gt.seq);
           const float* src = p.initial + ((slot * p.Hv + hv) * p.K + krow) * p.V + vt * 128;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            ulonglong2 x = make_ulonglong2(0, 0);
-            if (slot >= 0 && 4 * i < vw) x = *reinterpret_cast<const ulonglong2*>(src + 4 * i);
-            S[2 * i] = x.x, S[2 * i + 1] = x.y;
-          }
+          if (slot >= 0) load_state(S, src, vw);
         }
       }
       if (n > 0 && (flags & kHasState)) {
@@ -672,10 +668,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         float* dst = p.dinit + ((static_cast<int64_t>(gt.seq) * p.Hv + hv) * p.K + krow) * p.V + vt * 128;
         const f2 sc = f2_splat(p.scale);
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (4 * i < vw)
-            *reinterpret_cast<ulonglong2*>(dst + 4 * i) =
-                make_ulonglong2(f2_mul(sc, S[2 * i]), f2_mul(sc, S[2 * i + 1]));
+        for (int i = 0; i < 16; ++i)
+          if (8 * i < vw) {
+            const f2 x[4] = {f2_mul(sc, S[4 * i]), f2_mul(sc, S[4 * i + 1]), f2_mul(sc, S[4 * i + 2]),
+                             f2_mul(sc, S[4 * i + 3])};
+            st_pairs(dst + 8 * i, x);
+          }
       }
       __syncwarp();
       if (lane == 0) bar_arrive(gempty + 8 * gs);
@@ -829,6 +827,7 @@ int launch_chunk_bwd(const ChunkBwdCall& c, cudaStream_t stream) {
   a.dqk = c.dq, a.dv = c.dv;
   a.scale = c.scale;
   a.rows = c.s.total, a.ratio = c.s.Hv / c.s.Hk;
+  a.joined = c.joined;
   a.Hk = c.s.Hk, a.Hv = c.s.Hv, a.K = c.s.K, a.V = c.s.V;
   a.carry = c.carry_s;
   a.decay = c.carry_s + static_cast<int64_t>(c.grid) * 2 * kStateFloats;

@@ -62,10 +62,11 @@ struct ChunkArgs {
   float* fin;
   uint16_t* o;
   float* carry;   // [grid] states handed on
-  float* decay;   // [grid] their decays; negative: the sequence began in that range
+  float* decay;   // [grid] their decays, kChainStart or kNoTail
   float* copy;    // [grid] initial states of split sequences (final_state may overwrite them)
   float scale;
   int rows, ratio, Hv, K, V;
+  int joined;     // the states handed on are whole (the scan kernel ran)
   int report;     // the tail kernel writes a small plan's verdicts (the backward's first)
 };
 
@@ -519,20 +520,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int i = 0; i < 64; ++i) S[i] = 0;
         if (flags & kMiddle) {
           // what the ranges before this one hand on, back to the one where the sequence began
-          gather_state(S, p.carry, p.decay, blockIdx.x, parts, -1, krow);
+          gather_state(S, p.carry, p.decay, blockIdx.x, parts, -1, p.joined, krow);
         } else if (p.initial && slot >= 0 && krow < p.K) {
           const float* src = p.initial + ((slot * p.Hv + hv) * p.K + krow) * p.V + vt * 128;
           const ulonglong2* from = reinterpret_cast<const ulonglong2*>(
               p.copy + static_cast<int64_t>(blockIdx.x) * kStateFloats);
           const bool saved = (flags & kSplitSeq) && p.fin;  // final_state may have replaced it
+          if (saved) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            ulonglong2 x = make_ulonglong2(0, 0);
-            if (saved)
-              x = from[i * 128 + krow];
-            else if (4 * i < vw)
-              x = *reinterpret_cast<const ulonglong2*>(src + 4 * i);
-            S[2 * i] = x.x, S[2 * i + 1] = x.y;
+            for (int i = 0; i < 32; ++i) {
+              const ulonglong2 x = from[i * 128 + krow];
+              S[2 * i] = x.x, S[2 * i + 1] = x.y;
+            }
+          } else {
+            load_state(S, src, vw);
           }
         }
       }
@@ -574,9 +575,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         float* dst = p.fin + ((slot * p.Hv + hv) * p.K + krow) * p.V + vt * 128;
         if (slot >= 0) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (4 * i < vw)
-              *reinterpret_cast<ulonglong2*>(dst + 4 * i) = make_ulonglong2(S[2 * i], S[2 * i + 1]);
+          for (int i = 0; i < 16; ++i)
+            if (8 * i < vw) st_pairs(dst + 8 * i, &S[4 * i]);
         }
       }
       __syncwarp();
@@ -677,6 +677,7 @@ __global__ void __launch_bounds__(kTailThreads, 1)
   const int64_t start = REV ? tail.u0 : tail.u1 - 1;
   const int pk = p.K > kPanelCols ? 2 : 1;
   bool ok = true;  // no wait of this thread's has given up
+  if (count == 0 && threadIdx.x == 0) p.decay[blockIdx.x] = kNoTail;
   if (count > 0) {
     if (warp == 0) {
       // ---- tiles: as the gates ask for them ----
@@ -878,7 +879,7 @@ __global__ void __launch_bounds__(kTailThreads, 1)
             if (!REV && tail.closed && p.initial && p.fin) copy[(c * 8 + i) * 128 + krow] = s0;
           }
         }
-        if (krow == 0) p.decay[blockIdx.x] = tail.closed ? -1.f : rest;
+        if (krow == 0) p.decay[blockIdx.x] = tail.closed ? kChainStart : rest;
       }
     }
   }
@@ -889,6 +890,55 @@ __global__ void __launch_bounds__(kTailThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_free(tmem, 256);
+  }
+}
+
+// Joins what the ranges hand on along each chain of ranges of one sequence, in place: carry[i]
+// becomes the whole state at the end (REV: start) of range i.  For long chains: a sweep's CTA would read every state of its chain, one after the other
+// (0.8 us each); here each thread follows 16 bytes of it along the chain with kScanAhead reads in
+// flight.  grid: (ranges, slices of a state, directions); the CTAs of ranges that do not start a
+// chain have nothing to do.
+constexpr int kScanThreads = 256, kScanAhead = 8, kMaxRanges = 1024;
+constexpr int kScanSlices = kStateFloats / 4 / kScanThreads;
+struct ScanArgs {
+  float* carry[2];
+  const float* decay[2];
+  int grid;
+};
+__global__ void __launch_bounds__(kScanThreads) cattn_linear_scan_kernel(const __grid_constant__ ScanArgs p) {
+  cconv::grid_dependency_wait();
+  cconv::grid_launch_dependents();
+  __shared__ float decay[kMaxRanges];
+  const int rev = blockIdx.z, by = rev ? -1 : 1, first = blockIdx.x;
+  for (int i = threadIdx.x; i < p.grid; i += kScanThreads) decay[i] = p.decay[rev][i];
+  __syncthreads();
+  if (decay[first] != kChainStart) return;
+  constexpr int64_t kPitch = kStateFloats / 4;
+  float4* states = reinterpret_cast<float4*>(p.carry[rev]) + blockIdx.y * kScanThreads + threadIdx.x;
+  float4 run = states[first * kPitch];
+  for (int i = first + by;;) {
+    int n = 0;  // the next ranges that go on with the chain
+    float4 x[kScanAhead];
+#pragma unroll
+    for (int j = 0; j < kScanAhead; ++j) {
+      const int r = i + j * by;
+      if (n == j && r >= 0 && r < p.grid && decay[r] >= 0.f) {
+        x[j] = states[r * kPitch];
+        n = j + 1;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kScanAhead; ++j)
+      if (j < n) {
+        const float d = decay[i + j * by];
+        run.x = fmaf(d, run.x, x[j].x);
+        run.y = fmaf(d, run.y, x[j].y);
+        run.z = fmaf(d, run.z, x[j].z);
+        run.w = fmaf(d, run.w, x[j].w);
+        states[(i + j * by) * kPitch] = run;
+      }
+    if (n < kScanAhead) return;
+    i += n * by;
   }
 }
 
@@ -947,6 +997,25 @@ static int launch(void (*kern)(ChunkArgs), int threads, int bytes, const ChunkAr
              : CCONV_ERR_CUDA;
 }
 
+// A chain has at most ceil(ranges / (heads * tiles)) + 1 states.  With 10 of them at most (16 heads)
+// the scan's launch costs more than it saves (forward of 16384 rows 112 us against 108); with 31
+// (4 heads) it saves a third of a backward (62 us against 102).
+constexpr int kLongChain = 12;
+int launch_scan(const ChunkCall& c, float* forward, float* backward, bool* scanned, cudaStream_t stream) {
+  const int tiles = (c.s.V + 127) / 128;
+  *scanned = c.grid > kLongChain * c.s.Hv * tiles && c.grid <= kMaxRanges;
+  if (!*scanned) return CCONV_OK;
+  ScanArgs a{};
+  a.carry[0] = forward, a.carry[1] = backward;
+  const int64_t decays = static_cast<int64_t>(c.grid) * 2 * kStateFloats;
+  a.decay[0] = forward + decays, a.decay[1] = backward ? backward + decays : nullptr;
+  a.grid = c.grid;
+  return launch_pdl(cattn_linear_scan_kernel, dim3(c.grid, kScanSlices, backward ? 2 : 1),
+                    dim3(kScanThreads), 0, stream, a) == cudaSuccess
+             ? CCONV_OK
+             : CCONV_ERR_CUDA;
+}
+
 int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream) {
   ChunkArgs a{};
   int rc = CCONV_OK;
@@ -980,6 +1049,10 @@ int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream) {
   rc = launch(c.part == kStateGrads ? cattn_linear_tail_kernel<true> : cattn_linear_tail_kernel<false>,
               kTailThreads, kTailBytes, a, c.grid, stream);
   if (rc != CCONV_OK || c.part != kForward) return rc;
+  bool joined = false;
+  rc = launch_scan(c, c.carry, nullptr, &joined, stream);
+  if (rc != CCONV_OK) return rc;
+  a.joined = joined;
   return launch(cattn_linear_chunk_kernel, kFwdThreads, kFwdBytes, a, c.grid, stream);
 }
 

@@ -41,8 +41,11 @@ struct ChunkBwdCall {
   float *dots_q, *dots_k;   // [2][Hv * tiles][total]
   float *carry_s, *carry_d; // what kStates and kStateGrads wrote
   int grid;
+  bool joined;
 };
 
+// Joins the states that ranges hand on (of either direction, or both), where chains are long.
+int launch_scan(const ChunkCall& c, float* forward, float* backward, bool* scanned, cudaStream_t stream);
 int launch_chunk_bwd(const ChunkBwdCall& c, cudaStream_t stream);
 int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream);
 size_t chunk_fwd_bytes(int grid);

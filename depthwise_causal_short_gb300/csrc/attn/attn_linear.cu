@@ -50,10 +50,11 @@ __global__ void __launch_bounds__(256)
 //   dg_t = dg_b + sum of x_i over t <= i < b
 // between the anchors a <= t < b: the starts of the ranges that lie in the sequence (where
 // dg_a = scale <D, S> is known from the whole states), the sequence's end (0), and its start
-// (0 without an initial state; with one not known).  What the sum to a misses of dg_a, rounding of the x_i, is
-// spread evenly over the tokens between.  One CTA for each sequence and head, column tile
-// by column tile, in steps of kDgThreads * kDgPer tokens from the end.
-constexpr int kDgThreads = 512, kDgPer = 4;
+// (0 without an initial state; with one not known).  What the sum to a misses of dg_a, rounding
+// of the x_i, is spread evenly over the tokens between.  One CTA for each sequence and head,
+// column tile by column tile; a warp takes a stretch between anchors, kDgPer tokens a lane, from
+// its end, first for the whole sum and then for the running one.
+constexpr int kDgThreads = 256, kDgPer = 8;
 constexpr int kSlices = 2;  // parts of a unit's dots
 
 struct DgArgs {
@@ -68,7 +69,6 @@ __global__ void __launch_bounds__(kDgThreads) cattn_linear_dg_kernel(const __gri
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
   __shared__ SmallPlan small;
-  __shared__ float sums[kDgThreads / 32];
   Plan plan = p.plan;
   if (plan.small) small_plan(plan, small, false, nullptr);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -79,14 +79,15 @@ __global__ void __launch_bounds__(kDgThreads) cattn_linear_dg_kernel(const __gri
   const int64_t parts = min(static_cast<int64_t>(p.grid), units);
   const int cs = plan.cstart[seq], ce = plan.cstart[seq + 1];
   const int t0 = plan.cu[seq], t1 = plan.cu[seq + 1];
+  if (t0 == t1) return;
   const int64_t slice = static_cast<int64_t>(plan.heads) * plan.tiles * plan.total;
-  constexpr int kStep = kDgThreads * kDgPer;
+  constexpr int kStep = 32 * kDgPer;
 
   for (int tile = 0; tile < plan.tiles; ++tile) {
     const int64_t ht = static_cast<int64_t>(h) * plan.tiles + tile;
     const int64_t first = ht * nch + cs, end = ht * nch + ce;
     const float *q = p.qdot + ht * plan.total, *k = p.kdot + ht * plan.total;
-    // x of this thread's tokens top, top - 1, .. above `from`, and their running sums
+    // x of this lane's tokens top, top - 1, .. down to `from`, summed up one after the other
     auto load = [&](int top, int from, float* x) {
 #pragma unroll
       for (int j = 0; j < kDgPer; ++j) x[j] = 0.f;
@@ -98,31 +99,36 @@ __global__ void __launch_bounds__(kDgThreads) cattn_linear_dg_kernel(const __gri
 #pragma unroll
       for (int j = 1; j < kDgPer; ++j) x[j] += x[j - 1];
     };
-    int64_t i = (end * parts + units - 1) / units - 1;  // the last range that starts before `end`
-    int right = t1;
-    float known = 0.f;  // dg at `right`
-    while (right > t0) {
-      const int64_t at = units * i / parts;
-      const bool inside = at > first;
-      const int left = inside ? t0 + static_cast<int>(at - first) * kChunk : t0;
-      const bool tied = inside || !p.open;
+    auto anchor = [&](int64_t i) {
       const float* a = p.anchors + 4 * i;
-      const float anchor = inside ? (a[0] + a[1]) + (a[2] + a[3]) : 0.f;
-      float total = 0.f, x[kDgPer];
-      for (int hi = right; hi > left; hi -= kStep) {
-        load(hi - 1 - static_cast<int>(threadIdx.x) * kDgPer, left, x);
-        float s = x[kDgPer - 1];
+      return (a[0] + a[1]) + (a[2] + a[3]);
+    };
+    // the last range that starts before `end`, and the first that starts after `first`
+    const int64_t hi_range = (end * parts + units - 1) / units - 1;
+    int64_t lo_range = first * parts / units;
+    while (units * lo_range / parts <= first) ++lo_range;
+    // stretch 0 ends at the sequence's end; stretch j at the start of range hi_range + 1 - j
+    const int64_t stretches = hi_range >= lo_range ? hi_range - lo_range + 2 : 1;
+    for (int64_t j = warp; j < stretches; j += kDgThreads / 32) {
+      const int64_t i = hi_range - j;  // the range whose start it begins at
+      const bool inside = j + 1 < stretches, tied = inside || !p.open;
+      const int right = j == 0 ? t1 : t0 + static_cast<int>(units * (i + 1) / parts - first) * kChunk;
+      const int left = inside ? t0 + static_cast<int>(units * i / parts - first) * kChunk : t0;
+      const float known = j == 0 ? 0.f : anchor(i + 1);  // dg at `right`
+      float x[kDgPer], miss = 0.f;
+      if (tied) {
+        float total = 0.f;
+        for (int hi = right; hi > left; hi -= kStep) {
+          load(hi - 1 - lane * kDgPer, left, x);
+          total += x[kDgPer - 1];
+        }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) sums[warp] = s;
-        __syncthreads();
-        for (int w = 0; w < kDgThreads / 32; ++w) total += sums[w];
-        __syncthreads();
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        miss = ((inside ? anchor(i) : 0.f) - (known + total)) / static_cast<float>(right - left);
       }
-      const float miss = tied ? (anchor - (known + total)) / static_cast<float>(right - left) : 0.f;
       float carry = known;
       for (int hi = right; hi > left; hi -= kStep) {
-        const int top = hi - 1 - static_cast<int>(threadIdx.x) * kDgPer;
+        const int top = hi - 1 - lane * kDgPer;
         load(top, left, x);
         float run = x[kDgPer - 1];
 #pragma unroll
@@ -130,28 +136,19 @@ __global__ void __launch_bounds__(kDgThreads) cattn_linear_dg_kernel(const __gri
           const float y = __shfl_up_sync(0xffffffffu, run, o);
           if (lane >= o) run += y;
         }
-        if (lane == 31) sums[warp] = run;
-        __syncthreads();
-        float before = carry;
-        for (int w = 0; w < kDgThreads / 32; ++w) {
-          if (w < warp) before += sums[w];
-          carry += sums[w];
-        }
-        __syncthreads();
-        const float other = __shfl_up_sync(0xffffffffu, run, 1);  // the lanes before this one
-        if (lane > 0) before += other;
+        float before = __shfl_up_sync(0xffffffffu, run, 1);  // the lanes before this one
+        before = lane > 0 ? carry + before : carry;
+        carry += __shfl_sync(0xffffffffu, run, 31);
 #pragma unroll
-        for (int j = 0; j < kDgPer; ++j)
-          if (top - j >= left) {
-            const float v = before + x[j] + miss * static_cast<float>(right - (top - j));
-            float* to = p.dg + static_cast<int64_t>(top - j) * plan.heads + h;
+        for (int jj = 0; jj < kDgPer; ++jj)
+          if (top - jj >= left) {
+            const float v = before + x[jj] + miss * static_cast<float>(right - (top - jj));
+            float* to = p.dg + static_cast<int64_t>(top - jj) * plan.heads + h;
             *to = tile ? *to + v : v;
           }
       }
-      known = tied ? anchor : known + total;
-      right = left;
-      --i;
     }
+    __syncthreads();  // the next tile adds to this one's dg, in other warps
   }
 }
 
@@ -191,7 +188,7 @@ static int check_states(const int32_t* cu, int64_t nseq, int64_t Hv, const float
   } else if ((initial || fin) && S < nseq) {
     return CCONV_ERR_SHAPE;
   }
-  return aligned(initial, 16) && aligned(fin, 16) ? CCONV_OK : CCONV_ERR_ALIGN;
+  return aligned(initial, 32) && aligned(fin, 32) ? CCONV_OK : CCONV_ERR_ALIGN;
 }
 
 static LinearShape shape_of(int64_t total, int64_t Hk, int64_t Hv, int64_t K, int64_t V,
@@ -326,7 +323,7 @@ extern "C" CCONV_API int cattn_linear_bwd(
   if (rc == CCONV_OK)
     rc = check_states(cu_seqlens, nseq, Hv, initial_state, nullptr, state_indices, S, status_dev);
   if (rc != CCONV_OK) return rc;
-  if (!aligned(d_initial_state, 16)) return CCONV_ERR_ALIGN;
+  if (!aligned(d_initial_state, 32)) return CCONV_ERR_ALIGN;
   if (total > 0) {
     if (!do_ || !dq || !dk || !dg) return CCONV_ERR_NULL;
     rc = check_rows(do_, total, Hv, sot, soh);
@@ -378,7 +375,12 @@ extern "C" CCONV_API int cattn_linear_bwd(
   rc = launch_chunk_fwd(grads, stream);
   if (rc != CCONV_OK) return rc;
 
+  bool joined = false;
+  rc = launch_scan(states, states.carry, grads.carry, &joined, stream);
+  if (rc != CCONV_OK) return rc;
+
   ChunkBwdCall c{};
+  c.joined = joined;
   c.q = states.q, c.k = states.k, c.v = states.v, c.d_o = grads.v;
   c.g = states.g, c.s = states.s, c.cu = cu_seqlens, c.cstart = cstart, c.slots = states.slots;
   c.initial = initial_state, c.dinit = d_initial_state, c.scale = scale;

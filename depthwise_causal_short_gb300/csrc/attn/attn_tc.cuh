@@ -222,10 +222,19 @@ __device__ __forceinline__ uint4 lds128_at(uint32_t addr) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ void stg256(void* p, const uint32_t* r) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+// 32 bytes of a state: whole sectors, where threads hold rows.
+struct alignas(32) Pairs4 {
+  unsigned long long v[4];
+};
+__device__ __forceinline__ Pairs4 ld_pairs(const float* p) {
+  Pairs4 x;
+  asm volatile("ld.global.v4.b64 {%0,%1,%2,%3}, [%4];"
+               : "=l"(x.v[0]), "=l"(x.v[1]), "=l"(x.v[2]), "=l"(x.v[3])
+               : "l"(p));
+  return x;
+}
+__device__ __forceinline__ void st_pairs(float* p, const unsigned long long* v) {
+  asm volatile("st.global.v4.b64 [%0], {%1,%2,%3,%4};" ::"l"(p), "l"(v[0]), "l"(v[1]), "l"(v[2]), "l"(v[3])
                : "memory");
 }
-
 }  // namespace cattn

@@ -108,7 +108,8 @@ CCONV_API int cattn_linear_bwd_workspace_bytes(int64_t total, int64_t nseq, int6
  *             are at most 1 (g <= 0); what has decayed below 2^-127 counts as forgotten, also
  *             if later values of g are positive.
  *   scale     factor of the outputs.
- *   initial_state  [S, Hv, K, V] fp32 contiguous, or NULL (zeros).
+ *   initial_state  [S, Hv, K, V] fp32 contiguous, 32-byte aligned (as the other states), or NULL
+ *             (zeros).
  *   final_state    [S, Hv, K, V] fp32 output, or NULL.  May be the same array as initial_state.
  *   state_indices  int32[nseq] in device memory, or NULL: sequence i's state lives in slot
  *             state_indices[i] (else slot i, and S >= nseq).  Indices are checked on the device

@@ -415,3 +415,23 @@ def test_prompt_then_tokens_equal_the_whole_sequence():
         y, _ = cc.cattn_linear_update(*[x[t:t + 1] for x in args], pool, idx)
         _check(y, o[t:t + 1], BF16_TOL, f"token {t}")
     _check(pool[2:], fin, STATE_TOL, "state")
+
+
+def test_one_head_over_many_ranges_equals_pieces():
+    # one head, so that its chain of ranges is as long as the machine is wide: whole against
+    # halves that hand their state on through memory
+    Hk, Hv, K, V, n = 1, 1, 64, 64, 9000
+    q, k, v, g, do, _ = (t.cuda() for t in plain.linear_inputs([n], Hk, Hv, K, V, seed=43, reach=4.0))
+    g = g * 0.02
+    o, fin, _ = cc.cattn_linear_fwd(q, k, v, g, _cu([n]), final_state=True)
+    a = 4500
+    first = [t[:a] for t in (q, k, v)] + [g[:a].contiguous()]
+    rest = [t[a:] for t in (q, k, v)] + [g[a:].contiguous()]
+    o1, mid, _ = cc.cattn_linear_fwd(*first, _cu([a]), final_state=True)
+    o2, end, _ = cc.cattn_linear_fwd(*rest, _cu([n - a]), initial_state=mid, final_state=True)
+    _check(torch.cat((o1, o2)), o.double().cpu(), 2 * BF16_TOL, "o")
+    _check(end, fin.double().cpu(), 2 * STATE_TOL, "state")
+    whole = cc.cattn_linear_bwd(q, k, v, g, do, _cu([n]))
+    part = cc.cattn_linear_bwd(*rest, do[a:], _cu([n - a]), initial_state=mid)
+    for name, x, y, tol in zip(("dq", "dk", "dv", "dg"), whole, part, (BF16_TOL,) * 3 + (DG_TOL,)):
+        _check(x[a:], y.double().cpu(), 2 * tol, name)
