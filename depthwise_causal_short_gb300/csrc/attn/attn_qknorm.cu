@@ -12,7 +12,10 @@
 // group takes one token and kHeads of its heads at a time: the table row, fp32 and so twice the
 // bytes of a head's channels, is read once for them, and all their loads are in flight
 // together.  A CTA works on queries or on keys only, so that one set of weights (and of their
-// sums) is live.  Everything between the bf16 load and the one rounding at the store is fp32.
+// sums) is live.  Four CTAs of 64 registers a thread forward and two of 128 backward: more (5 / 3)
+// spill and take 1.2 times as long, and items of 2 or 8 heads, or the next item's channels fetched
+// ahead, are slower as well.  16384 rows, 8 + 8 heads of 128: 25.3 us forward (5.5 TB/s of needed
+// bytes), 41.7 us backward with the weights' gradients (4.9 TB/s).  Everything between the bf16 load and the one rounding at the store is fp32.
 #include "attn.cuh"
 
 namespace cattn {
@@ -114,11 +117,11 @@ __device__ __forceinline__ void ld_table(const float* p, float (&v)[4]) {
 // The factors of a lane's 8 channels, in pairs: y = x . C + partner . S, where `partner` holds the
 // other channel of each pair (partner_of).  Ones and zeros in the channels that are not rotated.
 template <bool INTER>
-__device__ __forceinline__ void load_angles(const NormArgs& p, int t, int lane, float dir, f2* C, f2* S) {
+__device__ __forceinline__ void load_angles(const NormArgs& p, int64_t at, int lane, float dir,
+                                            f2* C, f2* S) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) C[j] = cconv::f2_splat(1.f), S[j] = 0;
   if (lane * 8 >= p.R) return;
-  int64_t at = p.pos ? p.pos[t] : t;
   if (at < 0 || at >= p.P) {
     if (lane == 0) atomicOr(&g_fault_qknorm, kFaultPosition);
     at = at < 0 ? 0 : p.P - 1;
@@ -188,6 +191,14 @@ struct Cursor {
   }
 };
 
+// The table row of a cursor's token.  Read one item ahead, so that the table is fetched beside
+// the channels and not one more latency behind them (16384 rows of 16 heads of 128: 27.9 to 25.3 us
+// forward, 47.6 to 41.7 us backward).
+__device__ __forceinline__ int64_t position(const NormArgs& p, const Cursor& at) {
+  const int t = at.it < at.items ? at.t : 0;
+  return p.pos && p.R > 0 ? __ldg(p.pos + t) : t;
+}
+
 template <int LANES, bool INTER>
 __global__ void __launch_bounds__(kThreads, kFwdCtas)
     cattn_qknorm_fwd_kernel(const __grid_constant__ NormArgs p) {
@@ -218,12 +229,16 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
   const int H = side.H, heads = side.heads;
   // Whole warps walk the items together, so that every shuffle has its 32 lanes.
   const int64_t mine = (threadIdx.x % 32) / LANES;
-  for (Cursor at(side, static_cast<int64_t>(cta) * kGroups + threadIdx.x / LANES,
-                 static_cast<int64_t>(ctas) * kGroups);
-       at.it - mine < at.items; at.next()) {
+  Cursor at(side, static_cast<int64_t>(cta) * kGroups + threadIdx.x / LANES,
+            static_cast<int64_t>(ctas) * kGroups);
+  int64_t row = position(p, at);
+  while (at.it - mine < at.items) {
+    const int64_t pos = row;
     const bool live = at.it < at.items;
     const int t = live ? at.t : 0, h0 = live ? at.s * heads : 0;
     const int n = live && on ? min(heads, H - h0) : 0;
+    at.next();
+    row = position(p, at);
     uint4 raw[kHeads];
     const uint16_t* x0 = side.x + t * st + h0 * sh + lane * 8;
 #pragma unroll
@@ -233,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas)
     }
     // y = r (x . A + partner . B): weights and angles in one pair of factors a channel
     f2 A[4], B[4];
-    load_angles<INTER>(p, t, lane, 1.f, A, B);
+    load_angles<INTER>(p, pos, lane, 1.f, A, B);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const ulonglong2 w = weights[0][j][lane], o = weights[1][j][lane];
@@ -278,12 +293,16 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
   const int64_t st = side.st, sh = side.sh, dt = side.dt, dh = side.dh;
   const int H = side.H, heads = side.heads;
   const int64_t mine = (threadIdx.x % 32) / LANES;
-  for (Cursor at(side, static_cast<int64_t>(cta) * kGroups + threadIdx.x / LANES,
-                 static_cast<int64_t>(ctas) * kGroups);
-       at.it - mine < at.items; at.next()) {
+  Cursor at(side, static_cast<int64_t>(cta) * kGroups + threadIdx.x / LANES,
+            static_cast<int64_t>(ctas) * kGroups);
+  int64_t row = position(p, at);
+  while (at.it - mine < at.items) {
+    const int64_t pos = row;
     const bool live = at.it < at.items;
     const int t = live ? at.t : 0, h0 = live ? at.s * heads : 0;
     const int n = live && on ? min(heads, H - h0) : 0;
+    at.next();
+    row = position(p, at);
     uint4 rx[kHeads], ry[kHeads];
     const uint16_t* x0 = side.x + t * st + h0 * sh + lane * 8;
     const uint16_t* d0 = side.dy + t * dt + h0 * dh + lane * 8;
@@ -296,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
       }
     }
     f2 C[4], S[4];
-    load_angles<INTER>(p, t, lane, -1.f, C, S);
+    load_angles<INTER>(p, pos, lane, -1.f, C, S);
     uint16_t* y0 = side.out + (static_cast<int64_t>(t) * H + h0) * p.K + lane * 8;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i, y0 += p.K) {
