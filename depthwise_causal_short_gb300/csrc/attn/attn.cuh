@@ -27,7 +27,7 @@ struct FaultReader {
 int bind_context();
 int sm_count(int* sms);
 
-inline bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+__host__ __device__ inline bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 // A [total, H, C] bf16 activation with strides (st, sh): the rules of cattn.h.
 inline int check_rows(const void* p, int64_t total, int64_t H, int64_t st, int64_t sh) {

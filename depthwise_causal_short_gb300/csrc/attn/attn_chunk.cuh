@@ -5,6 +5,10 @@
 // of V, chunk), ordered so that the chunks of one head follow one another; each CTA takes one
 // contiguous range of units, equal to within one unit whatever the lengths of the sequences
 // are.  A range that ends inside a sequence hands its state on through the workspace.
+//
+// Where the sums over the value heads (and column tiles) of one key head are made by the CTAs of a
+// cluster, such a group of `group` neighbours shares one range of (key head, chunk), and each takes
+// one of its members: range i of member m is CTA i * group + m.
 #pragma once
 
 #include "attn_tc.cuh"
@@ -41,6 +45,7 @@ struct Plan {
   int nseq;
   int tiles;  // column tiles of V
   int heads;  // value heads
+  int group;  // CTAs that share a range: 1, or the members of a key head
   int small, total;
   const int32_t* idx;  // state indices, their slots, and where the verdict goes
   int64_t S;
@@ -92,6 +97,11 @@ __device__ __forceinline__ void small_plan(Plan& p, SmallPlan& s, bool report, u
 struct Range {
   int64_t u0, u1;  // units of this CTA, [u0, u1)
 };
+// How many ranges there are.
+__device__ __forceinline__ int64_t range_count(const Plan& p, int64_t grid, int64_t units) {
+  const int64_t ranges = grid / p.group;
+  return ranges < units ? ranges : units;
+}
 
 // The part of a range that continues in the next range (the previous one for a sweep from the
 // last token): [u0, u1), empty if the range's end is a sequence's end; `closed` if the sequence
@@ -103,7 +113,7 @@ struct Tail {
 
 __device__ __forceinline__ int64_t unit_count(const Plan& p, int& nch) {
   nch = p.cstart[p.nseq];
-  return static_cast<int64_t>(p.heads) * p.tiles * nch;
+  return static_cast<int64_t>(p.heads) * p.tiles / p.group * nch;
 }
 __device__ __forceinline__ Range range_of(int64_t units, int64_t parts, int64_t i) {
   return Range{units * i / parts, units * (i + 1) / parts};
@@ -122,10 +132,10 @@ struct Walker {
     base = p->cu[seq];
     len = p->cu[seq + 1] - base;
   }
-  __device__ __forceinline__ void seek(const Plan* plan, int chunks, int64_t u) {
+  __device__ __forceinline__ void seek(const Plan* plan, int chunks, int64_t u, int member = 0) {
     p = plan;
     nch = chunks;
-    ht = static_cast<int>(u / nch);
+    ht = static_cast<int>(u / nch) * p->group + member;
     c = static_cast<int>(u % nch);
     int lo = 0, hi = p->nseq - 1;  // the last sequence whose first chunk is <= c
     while (lo < hi) {
@@ -143,7 +153,7 @@ struct Walker {
     if (c == nch) {
       c = 0;
       seq = 0;
-      ++ht;
+      ht += p->group;
       load();
     } else if (c == ce) {
       ++seq;
@@ -155,7 +165,7 @@ struct Walker {
     if (c < 0) {
       c = nch - 1;
       seq = p->nseq - 1;
-      --ht;
+      ht -= p->group;
       load();
     } else if (c < cs) {
       --seq;
@@ -321,6 +331,23 @@ __device__ __forceinline__ bool wait_count(uint32_t at, int value) {
   return false;
 }
 
+// The same between the CTAs of a cluster: a count in the shared memory of CTA `rank`, and the wait
+// for a count that another one sets.  What the writer did before is seen after the wait.
+__device__ __forceinline__ void set_remote(uint32_t at, int rank, int value) {
+  uint32_t there;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+  asm volatile("st.release.cluster.shared::cluster.b32 [%0], %1;" ::"r"(there), "r"(value) : "memory");
+}
+__device__ __forceinline__ bool wait_remote(uint32_t at, int value) {
+#pragma unroll 1
+  for (int n = kWaitTries; n != 0; --n) {
+    int now;
+    asm volatile("ld.acquire.cluster.shared::cta.b32 %0, [%1];" : "=r"(now) : "r"(at) : "memory");
+    if (now >= value) return true;
+  }
+  return false;
+}
+
 // Zeroes rows [n, 128) of a tile: rows of the next sequence must not meet a matrix product,
 // where 0 * NaN is not 0.  `threads` threads, i of them this one.
 __device__ __forceinline__ void zero_rows(uint32_t tile, int panels, int n, int i, int threads) {
@@ -349,13 +376,14 @@ __device__ __forceinline__ void load_state(f2* S, const float* src, int width) {
   }
 }
 
-// Adds up what the ranges next to range `at` hand on (by = -1: those before it, 1: after it), to
-// the one where the sequence starts (ends); the nearest one's is the whole where they are joined.
+// Adds up what the ranges next to CTA `at`'s hand on (by < 0: those before it, > 0: after it; by
+// the CTAs of a range), to the one where the sequence starts (ends); the nearest one's is the
+// whole where they are joined.
 __device__ __forceinline__ void gather_state(f2* S, const float* carry, const float* decay,
-                                             int64_t at, int64_t parts, int by, bool joined,
+                                             int64_t at, int64_t ctas, int by, bool joined,
                                              int row) {
   float coef = 1.f;
-  for (int64_t j = at + by; j >= 0 && j < parts; j += by) {
+  for (int64_t j = at + by; j >= 0 && j < ctas; j += by) {
     const ulonglong2* src = reinterpret_cast<const ulonglong2*>(carry + j * kStateFloats);
     const float d = decay[j];
     const f2 c = f2_splat(coef);

@@ -669,9 +669,10 @@ __global__ void __launch_bounds__(kTailThreads, 1)
 
   int nch;
   const int64_t units = unit_count(plan, nch);
-  const int64_t parts = min(static_cast<int64_t>(gridDim.x), units);
+  const int64_t parts = range_count(plan, gridDim.x, units);
+  const int place = blockIdx.x / plan.group, member = blockIdx.x % plan.group;
   Range range{0, 0};
-  if (blockIdx.x < parts) range = range_of(units, parts, blockIdx.x);
+  if (place < parts) range = range_of(units, parts, place);
   const Tail tail = tail_of<REV>(plan, nch, units, range);
   const int count = static_cast<int>(tail.u1 - tail.u0);
   const int64_t start = REV ? tail.u0 : tail.u1 - 1;
@@ -749,7 +750,7 @@ __global__ void __launch_bounds__(kTailThreads, 1)
     } else if (warp == 2) {
       // ---- gates ----
       Walker w;
-      w.seek(&plan, nch, start);
+      w.seek(&plan, nch, start, member);
       float g[4], run = 0.f;
       const int hv = w.ht / plan.tiles;
 #pragma unroll
@@ -894,7 +895,7 @@ __global__ void __launch_bounds__(kTailThreads, 1)
 }
 
 // Joins what the ranges hand on along each chain of ranges of one sequence, in place: carry[i]
-// becomes the whole state at the end (REV: start) of range i.  For long chains: a sweep's CTA would read every state of its chain, one after the other
+// becomes the whole state at the end (REV: start) of CTA i's range.  For long chains: a sweep's CTA would read every state of its chain, one after the other
 // (0.8 us each); here each thread follows 16 bytes of it along the chain with kScanAhead reads in
 // flight.  grid: (ranges, slices of a state, directions); the CTAs of ranges that do not start a
 // chain have nothing to do.
@@ -903,13 +904,13 @@ constexpr int kScanSlices = kStateFloats / 4 / kScanThreads;
 struct ScanArgs {
   float* carry[2];
   const float* decay[2];
-  int grid;
+  int grid, group;
 };
 __global__ void __launch_bounds__(kScanThreads) cattn_linear_scan_kernel(const __grid_constant__ ScanArgs p) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
   __shared__ float decay[kMaxRanges];
-  const int rev = blockIdx.z, by = rev ? -1 : 1, first = blockIdx.x;
+  const int rev = blockIdx.z, by = rev ? -p.group : p.group, first = blockIdx.x;
   for (int i = threadIdx.x; i < p.grid; i += kScanThreads) decay[i] = p.decay[rev][i];
   __syncthreads();
   if (decay[first] != kChainStart) return;
@@ -1009,7 +1010,7 @@ int launch_scan(const ChunkCall& c, float* forward, float* backward, bool* scann
   a.carry[0] = forward, a.carry[1] = backward;
   const int64_t decays = static_cast<int64_t>(c.grid) * 2 * kStateFloats;
   a.decay[0] = forward + decays, a.decay[1] = backward ? backward + decays : nullptr;
-  a.grid = c.grid;
+  a.grid = c.grid, a.group = c.group;
   return launch_pdl(cattn_linear_scan_kernel, dim3(c.grid, kScanSlices, backward ? 2 : 1),
                     dim3(kScanThreads), 0, stream, a) == cudaSuccess
              ? CCONV_OK
@@ -1029,7 +1030,7 @@ int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream) {
     if (rc != CCONV_OK) return rc;
   }
   const int tiles = (c.s.V + 127) / 128;
-  a.plan = Plan{c.cu, c.cstart, c.s.nseq, tiles, c.s.Hv, c.cstart == nullptr, c.s.total, c.slots.idx, c.slots.S, c.status};
+  a.plan = Plan{c.cu, c.cstart, c.s.nseq, tiles, c.s.Hv, c.group, c.cstart == nullptr, c.s.total, c.slots.idx, c.slots.S, c.status};
   a.g = c.g;
   a.slots = c.slots;
   a.initial = c.initial;

@@ -24,6 +24,7 @@ struct ChunkCall {
   uint16_t* o;
   float* carry;  // chunk_fwd_bytes(grid)
   int grid;
+  int group;     // CTAs that share a range (kForward: 1)
 };
 
 struct ChunkBwdCall {
@@ -37,15 +38,19 @@ struct ChunkBwdCall {
   float* dinit;
   float scale;
   uint16_t *dq, *dk, *dv;
-  float *part_q, *part_k;   // [Hv * tiles][total][K] on 32-byte boundaries, or NULL: dq and dk
+  float *part_q, *part_k;   // [Hv * tiles][total][K] on 32-byte boundaries, or NULL: one part, or the ring
   float *dots_q, *dots_k;   // [2][Hv * tiles][total]
   float *carry_s, *carry_d; // what kStates and kStateGrads wrote
-  int grid;
+  float* ring;              // sum_bytes(grid, K), or NULL: no clusters
+  int grid, group;
   bool joined;
 };
 
 // Joins the states that ranges hand on (of either direction, or both), where chains are long.
 int launch_scan(const ChunkCall& c, float* forward, float* backward, bool* scanned, cudaStream_t stream);
+// CTAs of the backward's sweeps that can be resident as clusters of `group`.
+int cluster_ctas(int group, int* ctas);
+size_t sum_bytes(int grid, int64_t K);
 int launch_chunk_bwd(const ChunkBwdCall& c, cudaStream_t stream);
 int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream);
 size_t chunk_fwd_bytes(int grid);

@@ -51,104 +51,130 @@ __global__ void __launch_bounds__(256)
 // between the anchors a <= t < b: the starts of the ranges that lie in the sequence (where
 // dg_a = scale <D, S> is known from the whole states), the sequence's end (0), and its start
 // (0 without an initial state; with one not known).  What the sum to a misses of dg_a, rounding
-// of the x_i, is spread evenly over the tokens between.  One CTA for each sequence and head,
-// column tile by column tile; a warp takes a stretch between anchors, kDgPer tokens a lane, from
-// its end, first for the whole sum and then for the running one.
-constexpr int kDgThreads = 256, kDgPer = 8;
+// of the x_i, is spread evenly over the tokens between.  One CTA for each stretch between anchors:
+// the first `grid` ones for those that begin at their range's start, the others for those that
+// begin at a sequence's; a launch for each column tile of V, the second of which adds.  A stretch
+// is cut into a part for each warp, whose sums meet in shared memory before the running ones are
+// made (a warp a stretch, with 8 stretches in a CTA, took 22 us of 16384 rows and 16 heads where
+// this takes 10).
+constexpr int kDgThreads = 256, kDgPer = 4, kDgWarps = kDgThreads / 32;
 constexpr int kSlices = 2;  // parts of a unit's dots
 
 struct DgArgs {
   Plan plan;
   const float *qdot, *kdot;  // [kSlices][heads * tiles][total]
   const float* anchors;      // [grid][4]
-  int grid, open;            // ranges; whether the sequences have initial states
+  int grid, open, tile;      // CTAs of the sweeps; whether the sequences have initial states
   float* dg;
 };
+
+// Stretch `at`, by the whole CTA; `sums`: a float a warp.
+__device__ __forceinline__ void dg_stretch(const DgArgs& p, const Plan& plan, int nch, int64_t units,
+                                           int64_t at, float* sums) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t ranges = range_count(plan, p.grid, units);
+  const bool inside = at < p.grid;  // it begins at a range's start
+  int64_t u, range = 0;  // its first unit, and the range that this is in
+  Walker w;
+  if (inside) {
+    range = at / plan.group;
+    if (range >= ranges) return;
+    u = units * range / ranges;
+    w.seek(&plan, nch, u, static_cast<int>(at % plan.group));
+    if (w.first() || w.ht % plan.tiles != p.tile) return;
+  } else {
+    const int seq = static_cast<int>((at - p.grid) / plan.heads);
+    const int ht = static_cast<int>((at - p.grid) % plan.heads) * plan.tiles + p.tile;
+    u = static_cast<int64_t>(ht / plan.group) * nch + plan.cstart[seq];
+    w.seek(&plan, nch, u, ht % plan.group);
+    range = u * ranges / units;
+    while (units * range / ranges > u) --range;
+    while (units * (range + 1) / ranges <= u) ++range;
+  }
+  const int h = w.ht / plan.tiles, member = w.ht % plan.group;
+  auto anchor = [&](int64_t i) {
+    const float* a = p.anchors + 4 * (i * plan.group + member);
+    return (a[0] + a[1]) + (a[2] + a[3]);
+  };
+  const int64_t end = u - w.c + w.ce, stop = units * (range + 1) / ranges;
+  const bool reaches = stop >= end;  // the sequence's end
+  const int left = w.row0();
+  const int right = reaches ? w.base + w.len : left + static_cast<int>(stop - u) * kChunk;
+  if (right <= left) return;
+  const float known = reaches ? 0.f : anchor(range + 1);  // dg at `right`
+  const bool tied = inside || !p.open;
+
+  const int64_t slice = static_cast<int64_t>(plan.heads) * plan.tiles * plan.total;
+  const float* q = p.qdot + static_cast<int64_t>(w.ht) * plan.total;
+  const float* k = p.kdot + static_cast<int64_t>(w.ht) * plan.total;
+  constexpr int kStep = 32 * kDgPer;
+  // this warp's tokens [from, to): whole steps, from the right end on
+  const int each = ((right - left + kStep - 1) / kStep + kDgWarps - 1) / kDgWarps * kStep;
+  const int to = max(left, right - warp * each), from = max(left, to - each);
+  // x of this lane's tokens top, top - 1, .., summed up one after the other
+  auto load = [&](int top, float* x) {
+#pragma unroll
+    for (int j = 0; j < kDgPer; ++j) x[j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSlices; ++i)
+#pragma unroll
+      for (int j = 0; j < kDgPer; ++j)
+        if (top - j >= from) x[j] += q[i * slice + top - j] - k[i * slice + top - j];
+#pragma unroll
+    for (int j = 1; j < kDgPer; ++j) x[j] += x[j - 1];
+  };
+  float x[kDgPer], total = 0.f;
+  for (int hi = to; hi > from; hi -= kStep) {
+    load(hi - 1 - lane * kDgPer, x);
+    total += x[kDgPer - 1];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) sums[warp] = total;
+  __syncthreads();
+  float carry = known, all = known;
+#pragma unroll
+  for (int i = 0; i < kDgWarps; ++i) {
+    if (i < warp) carry += sums[i];
+    all += sums[i];
+  }
+  const float miss = tied ? ((inside ? anchor(range) : 0.f) - all) / static_cast<float>(right - left) : 0.f;
+  for (int hi = to; hi > from; hi -= kStep) {
+    const int top = hi - 1 - lane * kDgPer;
+    load(top, x);
+    float run = x[kDgPer - 1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += y;
+    }
+    float before = __shfl_up_sync(0xffffffffu, run, 1);  // the lanes before this one
+    before = lane > 0 ? carry + before : carry;
+    carry += __shfl_sync(0xffffffffu, run, 31);
+#pragma unroll
+    for (int j = 0; j < kDgPer; ++j)
+      if (top - j >= from) {
+        const float v = before + x[j] + miss * static_cast<float>(right - (top - j));
+        float* dst = p.dg + static_cast<int64_t>(top - j) * plan.heads + h;
+        *dst = p.tile ? *dst + v : v;
+      }
+  }
+}
 
 __global__ void __launch_bounds__(kDgThreads) cattn_linear_dg_kernel(const __grid_constant__ DgArgs p) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
   __shared__ SmallPlan small;
+  __shared__ float sums[kDgWarps];
   Plan plan = p.plan;
   if (plan.small) small_plan(plan, small, false, nullptr);
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int seq = static_cast<int>(blockIdx.x) / plan.heads, h = static_cast<int>(blockIdx.x) % plan.heads;
   int nch;
   const int64_t units = unit_count(plan, nch);
   if (units == 0) return;
-  const int64_t parts = min(static_cast<int64_t>(p.grid), units);
-  const int cs = plan.cstart[seq], ce = plan.cstart[seq + 1];
-  const int t0 = plan.cu[seq], t1 = plan.cu[seq + 1];
-  if (t0 == t1) return;
-  const int64_t slice = static_cast<int64_t>(plan.heads) * plan.tiles * plan.total;
-  constexpr int kStep = 32 * kDgPer;
-
-  for (int tile = 0; tile < plan.tiles; ++tile) {
-    const int64_t ht = static_cast<int64_t>(h) * plan.tiles + tile;
-    const int64_t first = ht * nch + cs, end = ht * nch + ce;
-    const float *q = p.qdot + ht * plan.total, *k = p.kdot + ht * plan.total;
-    // x of this lane's tokens top, top - 1, .. down to `from`, summed up one after the other
-    auto load = [&](int top, int from, float* x) {
-#pragma unroll
-      for (int j = 0; j < kDgPer; ++j) x[j] = 0.f;
-#pragma unroll
-      for (int i = 0; i < kSlices; ++i)
-#pragma unroll
-        for (int j = 0; j < kDgPer; ++j)
-          if (top - j >= from) x[j] += q[i * slice + top - j] - k[i * slice + top - j];
-#pragma unroll
-      for (int j = 1; j < kDgPer; ++j) x[j] += x[j - 1];
-    };
-    auto anchor = [&](int64_t i) {
-      const float* a = p.anchors + 4 * i;
-      return (a[0] + a[1]) + (a[2] + a[3]);
-    };
-    // the last range that starts before `end`, and the first that starts after `first`
-    const int64_t hi_range = (end * parts + units - 1) / units - 1;
-    int64_t lo_range = first * parts / units;
-    while (units * lo_range / parts <= first) ++lo_range;
-    // stretch 0 ends at the sequence's end; stretch j at the start of range hi_range + 1 - j
-    const int64_t stretches = hi_range >= lo_range ? hi_range - lo_range + 2 : 1;
-    for (int64_t j = warp; j < stretches; j += kDgThreads / 32) {
-      const int64_t i = hi_range - j;  // the range whose start it begins at
-      const bool inside = j + 1 < stretches, tied = inside || !p.open;
-      const int right = j == 0 ? t1 : t0 + static_cast<int>(units * (i + 1) / parts - first) * kChunk;
-      const int left = inside ? t0 + static_cast<int>(units * i / parts - first) * kChunk : t0;
-      const float known = j == 0 ? 0.f : anchor(i + 1);  // dg at `right`
-      float x[kDgPer], miss = 0.f;
-      if (tied) {
-        float total = 0.f;
-        for (int hi = right; hi > left; hi -= kStep) {
-          load(hi - 1 - lane * kDgPer, left, x);
-          total += x[kDgPer - 1];
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        miss = ((inside ? anchor(i) : 0.f) - (known + total)) / static_cast<float>(right - left);
-      }
-      float carry = known;
-      for (int hi = right; hi > left; hi -= kStep) {
-        const int top = hi - 1 - lane * kDgPer;
-        load(top, left, x);
-        float run = x[kDgPer - 1];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float y = __shfl_up_sync(0xffffffffu, run, o);
-          if (lane >= o) run += y;
-        }
-        float before = __shfl_up_sync(0xffffffffu, run, 1);  // the lanes before this one
-        before = lane > 0 ? carry + before : carry;
-        carry += __shfl_sync(0xffffffffu, run, 31);
-#pragma unroll
-        for (int jj = 0; jj < kDgPer; ++jj)
-          if (top - jj >= left) {
-            const float v = before + x[jj] + miss * static_cast<float>(right - (top - jj));
-            float* to = p.dg + static_cast<int64_t>(top - jj) * plan.heads + h;
-            *to = tile ? *to + v : v;
-          }
-      }
-    }
-    __syncthreads();  // the next tile adds to this one's dg, in other warps
+  const int64_t count = p.grid + static_cast<int64_t>(plan.nseq) * plan.heads;
+  for (int64_t at = blockIdx.x; at < count; at += gridDim.x) {
+    dg_stretch(p, plan, nch, units, at, sums);
+    __syncthreads();  // (whole CTAs leave a stretch early)
   }
 }
 
@@ -210,17 +236,37 @@ static int chunk_grid(int64_t total, int64_t nseq, int64_t Hv, int64_t V, int* g
   return CCONV_OK;
 }
 
+// CTAs of the backward, and how many share a range: the members of a key head (its value heads
+// and their column tiles) as a cluster, where these are 2 or 4.  Measured on 16384 rows with heads
+// of 128, clusters against sums through memory, us: 2 members 382 / 431, 4 members 384 / 430 (V of
+// 256: 402 / 446), but 3 members 416 / 334, 5 332 / 285, 6 343 / 331, 7 483 / 376, 8 432 / 424: the
+// chip holds 138 CTAs in clusters of 3, and all members of a cluster wait for the slowest.
+static int bwd_grid(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv, int64_t V, int* grid,
+                    int* group) {
+  *group = 1;
+  if (chunk_grid(total, nseq, Hv, V, grid) != CCONV_OK) return CCONV_ERR_CUDA;
+  const int64_t tiles = (V + 127) / 128, members = Hv / Hk * tiles;
+  if (members != 2 && members != 4) return CCONV_OK;
+  int ctas = 0;
+  if (cluster_ctas(static_cast<int>(members), &ctas) != CCONV_OK) return CCONV_ERR_CUDA;
+  if (ctas < members) return CCONV_OK;
+  const int64_t ranges = Hk * (total / 128 + nseq), most = ctas / members;
+  *group = static_cast<int>(members);
+  *grid = static_cast<int>(members * (ranges < most ? ranges : most));
+  return CCONV_OK;
+}
+
 // The chunk offsets at the head of the workspace.
 static size_t offsets_bytes(int64_t nseq) { return (static_cast<size_t>(nseq + 1) * 4 + 15) / 16 * 16; }
 
 // What a backward call keeps in its workspace, from a 256-byte boundary.
 struct BwdWork {
-  size_t offsets, carry_s, carry_d, dots_q, dots_k, part_q, part_k, bytes;
+  size_t offsets, carry_s, carry_d, dots_q, dots_k, part_q, part_k, ring, bytes;
 };
 static BwdWork bwd_work(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv, int64_t K, int64_t V,
-                        int grid) {
+                        int grid, int group) {
   const size_t tiles = static_cast<size_t>((V + 127) / 128), heads = static_cast<size_t>(Hv) * tiles;
-  const bool parts = heads > static_cast<size_t>(Hk);
+  const bool parts = group == 1 && heads > static_cast<size_t>(Hk);
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t r = at;
@@ -235,6 +281,7 @@ static BwdWork bwd_work(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv, int
   w.dots_k = take(kSlices * heads * static_cast<size_t>(total) * 4);
   w.part_q = take(parts ? heads * static_cast<size_t>(total) * K * 4 : 0);
   w.part_k = take(parts ? heads * static_cast<size_t>(total) * K * 4 : 0);
+  w.ring = take(group > 1 ? sum_bytes(grid, K) : 0);
   w.bytes = at + 256;
   return w;
 }
@@ -267,10 +314,10 @@ extern "C" CCONV_API int cattn_linear_bwd_workspace_bytes(int64_t total, int64_t
   using namespace cattn;
   if (!bytes) return CCONV_ERR_NULL;
   const int rc = check_sizes(total, nseq, Hk, Hv, K, V);
-  int grid = 0;
+  int grid = 0, group = 1;
   if (rc != CCONV_OK) return rc;
-  if (chunk_grid(total, nseq, Hv, V, &grid) != CCONV_OK) return CCONV_ERR_CUDA;
-  *bytes = bwd_work(total, nseq, Hk, Hv, K, V, grid).bytes;
+  if (bwd_grid(total, nseq, Hk, Hv, V, &grid, &group) != CCONV_OK) return CCONV_ERR_CUDA;
+  *bytes = bwd_work(total, nseq, Hk, Hv, K, V, grid, group).bytes;
   return CCONV_OK;
 }
 
@@ -306,7 +353,7 @@ extern "C" CCONV_API int cattn_linear_fwd(
   c.scale = scale;
   c.o = static_cast<uint16_t*>(o);
   c.carry = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + offsets_bytes(nseq));
-  c.grid = grid;
+  c.grid = grid, c.group = 1;
   return launch_chunk_fwd(c, stream);
 }
 
@@ -330,9 +377,9 @@ extern "C" CCONV_API int cattn_linear_bwd(
     if (rc != CCONV_OK) return rc;
     if (!aligned(dq, 16) || !aligned(dk, 16) || !aligned(dg, 16)) return CCONV_ERR_ALIGN;
   }
-  int grid = 0;
-  if (chunk_grid(total, nseq, Hv, V, &grid) != CCONV_OK) return CCONV_ERR_CUDA;
-  const BwdWork w = bwd_work(total, nseq, Hk, Hv, K, V, grid);
+  int grid = 0, group = 1;
+  if (bwd_grid(total, nseq, Hk, Hv, V, &grid, &group) != CCONV_OK) return CCONV_ERR_CUDA;
+  const BwdWork w = bwd_work(total, nseq, Hk, Hv, K, V, grid, group);
   if (total > 0) {
     if (!workspace || workspace_bytes < w.bytes) return CCONV_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return CCONV_ERR_ALIGN;
@@ -363,7 +410,7 @@ extern "C" CCONV_API int cattn_linear_bwd(
   states.slots = Slots{state_indices, S};
   states.initial = initial_state;
   states.status = status_dev;
-  states.grid = grid;
+  states.grid = grid, states.group = group;
   states.carry = reinterpret_cast<float*>(ws + w.carry_s);
   rc = launch_chunk_fwd(states, stream);
   if (rc != CCONV_OK) return rc;
@@ -387,18 +434,20 @@ extern "C" CCONV_API int cattn_linear_bwd(
   c.dq = static_cast<uint16_t*>(dq), c.dk = static_cast<uint16_t*>(dk);
   c.dv = static_cast<uint16_t*>(dv);
   const int tiles = static_cast<int>((V + 127) / 128), parts = static_cast<int>(Hv / Hk) * tiles;
-  if (parts > 1) {
+  if (group > 1) {
+    c.ring = reinterpret_cast<float*>(ws + w.ring);
+  } else if (parts > 1) {
     c.part_q = reinterpret_cast<float*>(ws + w.part_q);
     c.part_k = reinterpret_cast<float*>(ws + w.part_k);
   }
   c.dots_q = reinterpret_cast<float*>(ws + w.dots_q);
   c.dots_k = reinterpret_cast<float*>(ws + w.dots_k);
   c.carry_s = states.carry, c.carry_d = grads.carry;
-  c.grid = grid;
+  c.grid = grid, c.group = group;
   rc = launch_chunk_bwd(c, stream);
   if (rc != CCONV_OK) return rc;
 
-  if (parts > 1) {
+  if (c.part_q) {
     const unsigned ctas = static_cast<unsigned>((total * Hk * (K / 8) + 255) / 256);
     for (int side = 0; side < 2; ++side)
       if (launch_pdl(cattn_linear_heads_kernel, dim3(ctas), dim3(256), 0, stream,
@@ -407,13 +456,15 @@ extern "C" CCONV_API int cattn_linear_bwd(
         return CCONV_ERR_CUDA;
   }
   DgArgs d{};
-  d.plan = Plan{cu_seqlens, cstart, c.s.nseq, tiles, c.s.Hv, cstart == nullptr, c.s.total, nullptr, 0, nullptr};
+  d.plan = Plan{cu_seqlens, cstart, c.s.nseq, tiles, c.s.Hv, group, cstart == nullptr, c.s.total, nullptr, 0, nullptr};
   d.qdot = c.dots_q, d.kdot = c.dots_k;
   d.anchors = c.carry_d + static_cast<int64_t>(grid) * kStateFloats;
   d.grid = grid, d.open = initial_state != nullptr;
   d.dg = dg;
-  return launch_pdl(cattn_linear_dg_kernel, dim3(static_cast<unsigned>(nseq * Hv)), dim3(kDgThreads), 0,
-                    stream, d) == cudaSuccess
-             ? CCONV_OK
-             : CCONV_ERR_CUDA;
+  const int64_t stretches = grid + nseq * Hv, most = 1 << 20;
+  for (d.tile = 0; d.tile < tiles; ++d.tile)
+    if (launch_pdl(cattn_linear_dg_kernel, dim3(static_cast<unsigned>(stretches < most ? stretches : most)),
+                   dim3(kDgThreads), 0, stream, d) != cudaSuccess)
+      return CCONV_ERR_CUDA;
+  return CCONV_OK;
 }

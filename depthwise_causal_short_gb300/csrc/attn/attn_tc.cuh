@@ -93,6 +93,13 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
+// All threads of all CTAs of a cluster.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n"
+      "barrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
 // Box of shared memory to a 3-D tensor map (parts outside the tensor are left out); the issuing
 // thread's group of stores, and the wait until shared memory has been read.
 __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, int c, int h, int t) {

@@ -435,3 +435,41 @@ def test_one_head_over_many_ranges_equals_pieces():
     part = cc.cattn_linear_bwd(*rest, do[a:], _cu([n - a]), initial_state=mid)
     for name, x, y, tol in zip(("dq", "dk", "dv", "dg"), whole, part, (BF16_TOL,) * 3 + (DG_TOL,)):
         _check(x[a:], y.double().cpu(), 2 * tol, name)
+
+
+@pytest.mark.parametrize("K", [8, 24, 40, 128])
+@pytest.mark.parametrize("Hk,Hv,V", [(3, 6, 64), (2, 8, 40), (2, 2, 200), (1, 2, 136), (1, 3, 64), (1, 6, 8),
+                                     (2, 10, 136)])
+def test_sums_over_a_key_heads_members(Hk, Hv, V, K):
+    # 2 and 4 members (value heads and their column tiles) are added up by a cluster, a share of the
+    # columns each (at K = 8 one member has them all), other numbers through memory
+    lens = [128, 0, 300, 1, 640, 77]
+    q, k, v, g, do, s0 = plain.linear_inputs(lens, Hk, Hv, K, V, seed=K + Hv)
+    leaves = [t.double().requires_grad_() for t in (q, k, v, g, s0)]
+    o, _ = plain.linear(*leaves[:4], cu_of(lens), K ** -0.5, leaves[4])
+    want = torch.autograd.grad(o, leaves, do.double())
+    args = [t.cuda() for t in (q, k, v, g, do)]
+    grads = cc.cattn_linear_bwd(*args, _cu(lens), initial_state=s0.cuda())
+    for name, a, b, tol in zip(("dq", "dk", "dv", "dg", "d_initial_state"), grads, want,
+                               (BF16_TOL, BF16_TOL, BF16_TOL, DG_TOL, STATE_TOL)):
+        _check(a, b, tol, name)
+
+
+def test_backwards_side_by_side():
+    # the CTAs of a cluster wait for one another: they must be there whatever else runs
+    cases = []
+    for seed, (Hk, Hv, V) in enumerate([(4, 8, 128), (2, 8, 128), (4, 4, 256), (1, 1, 64)]):
+        lens = [700 + 100 * seed, 33, 1200]
+        cases.append((_cu(lens), [t.cuda() for t in plain.linear_inputs(lens, Hk, Hv, 64, V, seed=seed)[:5]]))
+    want = [cc.cattn_linear_bwd(*args, cu) for cu, args in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[] for _ in cases]
+    for _ in range(20):
+        for i, (cu, args) in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(cc.cattn_linear_bwd(*args, cu))
+    torch.cuda.synchronize()
+    for runs, ref in zip(got, want):
+        for grads in runs:
+            assert all(torch.equal(a, b) for a, b in zip(grads[:4], ref[:4]))
