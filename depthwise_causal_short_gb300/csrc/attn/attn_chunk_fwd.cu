@@ -621,9 +621,7 @@ constexpr int kTailBytes = kTailBars + 32 * 8 + 1024;
 static_assert(kTailBytes <= 232448, "shared memory of one CTA");
 
 template <bool REV>
-__global__ void __launch_bounds__(kTailThreads, 1)
-    cattn_linear_tail_kernel(const __grid_constant__ ChunkArgs p) {
-  extern __shared__ uint8_t raw[];
+__device__ __forceinline__ void tail_state(const ChunkArgs& p, uint8_t* raw, SmallPlan& small) {
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   TailGate* gates = reinterpret_cast<TailGate*>(base + kTailOffGates);
   const uint32_t smem = smem_addr(base);
@@ -663,7 +661,6 @@ __global__ void __launch_bounds__(kTailThreads, 1)
   const uint32_t tmem = *tmem_at;
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
-  __shared__ SmallPlan small;
   Plan plan = p.plan;
   if (plan.small) small_plan(plan, small, p.report && blockIdx.x == 0, &g_fault_fwd);
 
@@ -894,6 +891,26 @@ __global__ void __launch_bounds__(kTailThreads, 1)
   }
 }
 
+__global__ void __launch_bounds__(kTailThreads, 1)
+    cattn_linear_tail_kernel(const __grid_constant__ ChunkArgs p) {
+  extern __shared__ uint8_t raw[];
+  __shared__ SmallPlan small;
+  tail_state<false>(p, raw, small);
+}
+// The backward's: the states and their gradients (blockIdx.y = 1) in one launch.  How much a range
+// has to read depends on its gates, and the CTAs that are done early make room for others: 67 us
+// against 72 for two launches (16384 rows, 16 heads), 4 of 62 us of a small ragged call.  (The
+// forward has a kernel of its own: in this one it took 2 us longer.)
+__global__ void __launch_bounds__(kTailThreads, 1)
+    cattn_linear_tails_kernel(const __grid_constant__ ChunkArgs states, const __grid_constant__ ChunkArgs grads) {
+  extern __shared__ uint8_t raw[];
+  __shared__ SmallPlan small;
+  if (blockIdx.y == 0)
+    tail_state<false>(states, raw, small);
+  else
+    tail_state<true>(grads, raw, small);
+}
+
 // Joins what the ranges hand on along each chain of ranges of one sequence, in place: carry[i]
 // becomes the whole state at the end (REV: start) of CTA i's range.  For long chains: a sweep's CTA would read every state of its chain, one after the other
 // (0.8 us each); here each thread follows 16 bytes of it along the chain with kScanAhead reads in
@@ -989,15 +1006,6 @@ int encode_part_map(CUtensorMap* map, float* x, int64_t total, int64_t parts, in
   return r == CUDA_SUCCESS ? CCONV_OK : CCONV_ERR_CUDA;
 }
 
-static int launch(void (*kern)(ChunkArgs), int threads, int bytes, const ChunkArgs& a, int grid,
-                  cudaStream_t stream) {
-  if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(kern), bytes) != CCONV_OK)
-    return CCONV_ERR_CUDA;
-  return launch_pdl(kern, dim3(grid), dim3(threads), bytes, stream, a) == cudaSuccess
-             ? CCONV_OK
-             : CCONV_ERR_CUDA;
-}
-
 // A chain has at most ceil(ranges / (heads * tiles)) + 1 states.  With 10 of them at most (16 heads)
 // the scan's launch costs more than it saves (forward of 16384 rows 112 us against 108); with 31
 // (4 heads) it saves a third of a backward (62 us against 102).
@@ -1017,25 +1025,25 @@ int launch_scan(const ChunkCall& c, float* forward, float* backward, bool* scann
              : CCONV_ERR_CUDA;
 }
 
-int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream) {
-  ChunkArgs a{};
+static int chunk_args(const ChunkCall& c, ChunkArgs& a) {
   int rc = CCONV_OK;
   if (c.s.total > 0) {
     rc = bind_context();
     if (rc == CCONV_OK) rc = encode_tile_map(&a.mq, c.q, c.s.total, c.s.Hk, c.s.K);
     if (rc == CCONV_OK) rc = encode_tile_map(&a.mk, c.k, c.s.total, c.s.Hk, c.s.K);
     if (rc == CCONV_OK) rc = encode_tile_map(&a.mv, c.v, c.s.total, c.s.Hv, c.s.V);
-    if (rc == CCONV_OK && c.part == kForward)
+    if (rc == CCONV_OK && c.o)
       rc = encode_tile_map(&a.mo, Rows{c.o, int64_t(c.s.Hv) * c.s.V, c.s.V}, c.s.total, c.s.Hv, c.s.V);
     if (rc != CCONV_OK) return rc;
   }
   const int tiles = (c.s.V + 127) / 128;
-  a.plan = Plan{c.cu, c.cstart, c.s.nseq, tiles, c.s.Hv, c.group, c.cstart == nullptr, c.s.total, c.slots.idx, c.slots.S, c.status};
+  a.plan = Plan{c.cu, c.cstart, c.s.nseq, tiles, c.s.Hv, c.group, c.cstart == nullptr, c.s.total,
+                c.slots.idx, c.slots.S, c.status};
   a.g = c.g;
   a.slots = c.slots;
   a.initial = c.initial;
   a.fin = c.fin;
-  a.report = c.part == kStates;
+  a.report = c.o == nullptr;
   a.o = c.o;
   a.carry = c.carry;
   a.copy = c.carry + static_cast<int64_t>(c.grid) * kStateFloats;
@@ -1044,17 +1052,38 @@ int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream) {
   a.rows = c.s.total;
   a.ratio = c.s.Hv / c.s.Hk;
   a.Hv = c.s.Hv, a.K = c.s.K, a.V = c.s.V;
-  // with at most 128 rows no sequence has a second chunk, and nothing is handed on
-  if (c.part == kForward && c.s.total <= kChunk)
-    return launch(cattn_linear_chunk_kernel, kFwdThreads, kFwdBytes, a, c.grid, stream);
-  rc = launch(c.part == kStateGrads ? cattn_linear_tail_kernel<true> : cattn_linear_tail_kernel<false>,
-              kTailThreads, kTailBytes, a, c.grid, stream);
-  if (rc != CCONV_OK || c.part != kForward) return rc;
-  bool joined = false;
-  rc = launch_scan(c, c.carry, nullptr, &joined, stream);
+  return CCONV_OK;
+}
+
+template <class... Args>
+static int launch(void (*kern)(Args...), dim3 grid, int threads, int bytes, cudaStream_t stream,
+                  const Args&... args) {
+  if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(kern), bytes) != CCONV_OK)
+    return CCONV_ERR_CUDA;
+  return launch_pdl(kern, grid, dim3(threads), bytes, stream, args...) == cudaSuccess ? CCONV_OK
+                                                                                     : CCONV_ERR_CUDA;
+}
+
+int launch_chunk_states(const ChunkCall& states, const ChunkCall& grads, cudaStream_t stream) {
+  ChunkArgs a{}, b{};
+  int rc = chunk_args(states, a);
+  if (rc == CCONV_OK) rc = chunk_args(grads, b);
   if (rc != CCONV_OK) return rc;
-  a.joined = joined;
-  return launch(cattn_linear_chunk_kernel, kFwdThreads, kFwdBytes, a, c.grid, stream);
+  return launch(cattn_linear_tails_kernel, dim3(states.grid, 2), kTailThreads, kTailBytes, stream, a, b);
+}
+
+int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream) {
+  ChunkArgs a{};
+  int rc = chunk_args(c, a);
+  // with at most 128 rows no sequence has a second chunk, and nothing is handed on
+  if (rc == CCONV_OK && c.s.total > kChunk) {
+    rc = launch(cattn_linear_tail_kernel, dim3(c.grid), kTailThreads, kTailBytes, stream, a);
+    bool joined = false;
+    if (rc == CCONV_OK) rc = launch_scan(c, c.carry, nullptr, &joined, stream);
+    a.joined = joined;
+  }
+  return rc == CCONV_OK ? launch(cattn_linear_chunk_kernel, dim3(c.grid), kFwdThreads, kFwdBytes, stream, a)
+                        : rc;
 }
 
 size_t chunk_fwd_bytes(int grid) {

@@ -5,12 +5,9 @@
 
 namespace cattn {
 
-// What launch_chunk_fwd does: the whole forward, or only the states that ranges hand on, or the
-// gradients of states (k and v then hold q and do).
-enum ChunkPart { kForward, kStates, kStateGrads };
-
+// A forward (launch_chunk_fwd), or for the backward the states that ranges hand on and, with q and
+// do in k and v, the gradients of states (launch_chunk_states; o is NULL).
 struct ChunkCall {
-  ChunkPart part;
   Rows q, k, v;
   Gates g;
   LinearShape s;
@@ -24,7 +21,7 @@ struct ChunkCall {
   uint16_t* o;
   float* carry;  // chunk_fwd_bytes(grid)
   int grid;
-  int group;     // CTAs that share a range (kForward: 1)
+  int group;     // CTAs that share a range (forward: 1)
 };
 
 struct ChunkBwdCall {
@@ -40,7 +37,7 @@ struct ChunkBwdCall {
   uint16_t *dq, *dk, *dv;
   float *part_q, *part_k;   // [Hv * tiles][total][K] on 32-byte boundaries, or NULL: one part, or the ring
   float *dots_q, *dots_k;   // [2][Hv * tiles][total]
-  float *carry_s, *carry_d; // what kStates and kStateGrads wrote
+  float *carry_s, *carry_d; // what launch_chunk_states wrote
   float* ring;              // sum_bytes(grid, K), or NULL: no clusters
   int grid, group;
   bool joined;
@@ -53,6 +50,7 @@ int cluster_ctas(int group, int* ctas);
 size_t sum_bytes(int grid, int64_t K);
 int launch_chunk_bwd(const ChunkBwdCall& c, cudaStream_t stream);
 int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream);
+int launch_chunk_states(const ChunkCall& states, const ChunkCall& grads, cudaStream_t stream);
 size_t chunk_fwd_bytes(int grid);
 int encode_part_map(CUtensorMap* map, float* x, int64_t total, int64_t parts, int64_t C);
 int encode_tile_map(CUtensorMap* map, const Rows& x, int64_t total, int64_t H, int64_t C);

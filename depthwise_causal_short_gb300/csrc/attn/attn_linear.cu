@@ -402,7 +402,6 @@ extern "C" CCONV_API int cattn_linear_bwd(
   }
 
   ChunkCall states{};
-  states.part = kStates;
   states.q = rows(q, sqt, sqh), states.k = rows(k, skt, skh), states.v = rows(v, svt, svh);
   states.g = Gates{g, sgt, sgh};
   states.s = shape_of(total, Hk, Hv, K, V, nseq);
@@ -412,14 +411,11 @@ extern "C" CCONV_API int cattn_linear_bwd(
   states.status = status_dev;
   states.grid = grid, states.group = group;
   states.carry = reinterpret_cast<float*>(ws + w.carry_s);
-  rc = launch_chunk_fwd(states, stream);
-  if (rc != CCONV_OK) return rc;
   ChunkCall grads = states;
-  grads.part = kStateGrads;
   grads.k = states.q, grads.v = rows(do_, sot, soh);
   grads.initial = nullptr;
   grads.carry = reinterpret_cast<float*>(ws + w.carry_d);
-  rc = launch_chunk_fwd(grads, stream);
+  rc = launch_chunk_states(states, grads, stream);
   if (rc != CCONV_OK) return rc;
 
   bool joined = false;
