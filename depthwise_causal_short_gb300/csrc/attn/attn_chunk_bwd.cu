@@ -824,29 +824,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const bool whole = n == kChunk, live = row < n;
         const int hk = hv / p.ratio;
         const uint32_t stage = smem + kOffS;
-        if (group > 1) {
-          float4* ring = p.ring + (blockIdx.x * 2 + (use & 1)) * (p.K * (kChunk / 4)) + row;
-          ring_tile(tmem + lanes + 256, p.K, p.scale, ring);
-          __syncwarp();
-          if (lane < group) set_remote(smem + kOffCounts + 4 * (wq * kMaxGroup + member), lane, use + 1);
-        } else if (p.part)
-          finish_tile<true>(tmem + lanes + 256, stage, whole, live, row, p.K, p.scale,
-                            p.part + (static_cast<int64_t>(ht) * p.rows + t) * p.K);
-        else
-          finish_tile<false>(tmem + lanes + 256, stage, whole, live, row, p.K, p.scale,
-                             p.dqk + (t * p.Hk + hk) * p.K);
-        if (whole && group == 1) {
-          cconv::fence_proxy_async_smem();
-          if (!meet()) break;
-          if (row == 0) {
-            const int cols = p.part ? 32 : 64;
+        if (group == 1) {
+          if (p.part)
+            finish_tile<true>(tmem + lanes + 256, stage, whole, live, row, p.K, p.scale,
+                              p.part + (static_cast<int64_t>(ht) * p.rows + t) * p.K);
+          else
+            finish_tile<false>(tmem + lanes + 256, stage, whole, live, row, p.K, p.scale,
+                               p.dqk + (t * p.Hk + hk) * p.K);
+          if (whole) {
+            cconv::fence_proxy_async_smem();
+            if (!meet()) break;
+            if (row == 0) {
+              const int cols = p.part ? 32 : 64;
 #pragma unroll 1
-            for (int c = 0, i = 0; c < p.K; c += cols, ++i)
-              store_box(&p.out_k, stage + i * kPanelBytes, c, p.part ? ht : hk, row0);
-            stores_commit();
-            if (KV) stores_wait_read();
+              for (int c = 0, i = 0; c < p.K; c += cols, ++i)
+                store_box(&p.out_k, stage + i * kPanelBytes, c, p.part ? ht : hk, row0);
+              stores_commit();
+              if (KV) stores_wait_read();
+            }
+            if (KV && !meet()) break;
           }
-          if (KV && !meet()) break;
         }
         if (KV) {
           finish_tile<false>(tmem + lanes + 384, stage, whole, live, row, vw, p.scale,
@@ -862,13 +859,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
           }
         }
+        // the state may have its buffer back: in a cluster before the ring is written (166 us of
+        // the sweep of 16384 rows; after it 170)
+        auto leave = [&]() {
+          if (row != 0) return;
+          stores_wait_read();
+          set_count(stored, use + 1);
+        };
+        if (group > 1) {
+          leave();
+          __syncwarp();
+          ring_tile(tmem + lanes + 256, p.K, p.scale,
+                    p.ring + (blockIdx.x * 2 + (use & 1)) * (p.K * (kChunk / 4)) + row);
+          __syncwarp();
+          if (lane < group) set_remote(smem + kOffCounts + 4 * (wq * kMaxGroup + member), lane, use + 1);
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(ofree);
-        if (row == 0) {
-          stores_wait_read();
-          set_count(stored, use + 1);
-        }
+        if (group == 1) leave();
         ++use;
       }
       __syncwarp();
