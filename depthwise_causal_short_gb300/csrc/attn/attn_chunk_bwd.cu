@@ -120,6 +120,21 @@ __device__ __forceinline__ void scale32(uint32_t* x, float f) {
   }
 }
 
+// Scales `width` columns of a TMEM tile in place, a row a thread.
+__device__ __forceinline__ void scale_tile(uint32_t tmem, int width, float f) {
+#pragma unroll 1
+  for (int c = 0; c < width; c += 32) {
+    uint32_t x[32];
+    tmem_ld32(tmem + c, x);
+    tmem_wait_ld();
+    tmem_use32(x);
+    scale32(x, f);
+    tmem_st16(tmem + c, x);
+    tmem_st16(tmem + c + 16, x + 16);
+  }
+  tmem_wait_st();
+}
+
 // 128 columns of a TMEM tile, scaled, as bf16 or fp32 rows: to the staging buffer (panels of 128
 // bytes a row, 128-byte swizzle) or, for the rows of a partial chunk, straight to memory.
 // Columns at or past `width` are left out in steps of 8.
@@ -260,7 +275,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bar_init(sfull, 4);
     bar_init(sempty, 1);
     bar_init(infull, 1);
-    bar_init(scaled, 4);
+    bar_init(scaled, KV ? 8 : 4);
     bar_init(ofull, 1);
     bar_init(ofree, 4);
     set_count(stored, 0);
@@ -510,7 +525,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     set_registers<120, true>();
     const int wq = warp - 4, row = wq * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-    int use = 0;
+    int use = 0, pubs = 0;
     for (int unit = 0; unit < count; ++unit) {
       const int gs = unit % kBwdGates;
       if (!(ok = CATTN_WARP_WAIT(gfull + 8 * gs, unit / kBwdGates))) break;
@@ -594,6 +609,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (row < n)
           p.dots[static_cast<int64_t>(gt.ht) * p.rows + gt.row0 + row] = p.scale * (s0 + s1);
         ++use;
+        if (KV && (gt.flags & kHasState)) {
+          // half of the products with the state are scaled here: these warps wait most of the time
+          const int vw = min(128, p.V - gt.ht % plan.tiles * 128);
+          if (!(ok = CATTN_WARP_WAIT(infull, pubs))) break;
+          ++pubs;
+          tc_fence_after();
+          scale_tile(tmem + lanes + 384, vw, gt.kw[row]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(scaled);
+        }
       }
       __syncwarp();
       if (lane == 0) bar_arrive(gempty + 8 * gs);
@@ -795,13 +821,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           ++pubs;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < (KV ? 256 : 128); c += 32) {
-            if (c < 128 ? c >= p.K : c - 128 >= vw) continue;
+          for (int c = 0; c < p.K; c += 32) {
             uint32_t x[32];
             tmem_ld32(tmem + lanes + 256 + c, x);
             tmem_wait_ld();
             tmem_use32(x);
-            if (c < 128) dot = dot_tile(KV ? ak : aq, row, c, x, dot);
+            dot = dot_tile(KV ? ak : aq, row, c, x, dot);
             scale32(x, rowf);
             tmem_st16(tmem + lanes + 256 + c, x);
             tmem_st16(tmem + lanes + 256 + c + 16, x + 16);
