@@ -15,9 +15,10 @@
 // pairs that are not a token with itself: inside the chunk scale * sum M1 . M2 . L without the
 // diagonal, whose factors come from fp32 products of the inputs and are never rounded; across
 // chunks scale * er * q . (dO S^T) and scale * kw * k . (V D^T), for which S and D are read as
-// two bf16 terms (16 bits).  Summed over a whole sequence, those 16 bits would show (2.7e-5 of the
-// dg of heads that forget fast, 8192 tokens): so each range also gives dg at its start as the
-// product of the two whole fp32 states, and the sums in between are tied to these anchors.
+// three bf16 terms (24 bits; with two, the 16 bits showed: 1e-6 to 7e-6 of dg, where an initial state
+// meets a few tokens).  There is room for two terms at a time: the first replaces the second once
+// that is read (8 % of the time).  Each range also gives dg at its start as the product of the two
+// whole fp32 states, and the sums in between are tied to these anchors.
 //
 // Roles of the 20 warps: one warp streams tiles, one thread issues the products of the outputs
 // and one those of the state, one warp makes the gates; four warps each turn score tiles into P,
@@ -63,7 +64,7 @@ enum Slot : int { kV = 0, kDo = 1, kK = 2, kQ = 3, kBwdSlots = 4 };
 
 // shared memory, from a 1024-byte boundary
 constexpr int kOffKp = kBwdSlots * kTileBytes;          // two blocks of decayed rows
-constexpr int kOffS = kOffKp + 2 * kBlockBytes;         // the state as two bf16 terms; outputs
+constexpr int kOffS = kOffKp + 2 * kBlockBytes;         // two bf16 terms of the state; outputs
 constexpr int kOffGates = kOffS + 2 * kTileBytes;
 constexpr int kOffBars = kOffGates + kBwdGates * sizeof(Gate);
 constexpr int kOffCounts = kOffBars + 40 * 8;           // [4 warps][kMaxGroup]: see ring_tile
@@ -118,6 +119,22 @@ __device__ __forceinline__ void scale32(uint32_t* x, float f) {
     x[2 * i] = __float_as_uint(a);
     x[2 * i + 1] = __float_as_uint(b);
   }
+}
+
+// The upper halves of a pair's two words, which are its values cut off to bf16; `rest`: what they leave.
+__device__ __forceinline__ uint32_t cut_off(f2 x, f2& rest) {
+  float a, b;
+  cconv::f2_unpack(x, a, b);
+  const uint32_t u = __float_as_uint(a), v = __float_as_uint(b);
+  rest = f2_fma(f2_pack(__uint_as_float(u & 0xffff0000u), __uint_as_float(v & 0xffff0000u)), f2_splat(-1.f), x);
+  return __byte_perm(u, v, 0x7632);
+}
+
+// A pair's second and third bf16 terms: what its rounding to bf16 leaves has 16 bits at most.
+__device__ __forceinline__ void split_rest(f2 s, uint32_t& mid, uint32_t& low) {
+  f2 rest = f2_fma(bf16x2_to_f2(f2_to_bf16x2(s)), f2_splat(-1.f), s);
+  mid = cut_off(rest, rest);
+  low = cut_off(rest, rest);
 }
 
 // Scales `width` columns of a TMEM tile in place, a row a thread.
@@ -356,13 +373,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   } else if (warp == 1) {
     // ---- scores, products with the state, and products of P ----
     if (elect_one()) {
-      int use = 0, pubs = 0, fixes = 0, kvs = 0;
+      int use = 0, pubs = 0, ins = 0, fixes = 0, kvs = 0;
       const int kk = (p.K + 15) / 16, nk = kk * 16;
       const uint32_t ds = mma_desc(128, false, false), dst = mma_desc(nk, false, false);
       const uint32_t dk = mma_desc(nk, false, true);
       const uint64_t tv = tile_desc(av, 0), to = tile_desc(ao, 0), tk = tile_desc(ak, 0);
       const uint64_t tq = tile_desc(aq, 0), tS = tile_desc(smem + kOffS, 0);
       const uint64_t rows_k = tile_desc(KV ? aq : ak, kPanelBytes), rows_o = tile_desc(ao, kPanelBytes);
+      const uint64_t tvo = KV ? tv : to;
       const uint64_t rows_S = tile_desc(smem + kOffS, kPanelBytes);
       for (int unit = 0; unit < count && ok; ++unit) {
         const int gs = unit % kBwdGates;
@@ -395,13 +413,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (!(ok = CATTN_WAIT(sfull, pubs))) break;
             ++pubs;
             tc_fence_after();
-            // dO S^T or V D^T: the state's rows are the output's columns, its columns are summed
+            // dO S^T or V D^T: the state's rows are the output's columns, its columns are summed;
+            // its small terms first
 #pragma unroll 1
-            for (int j = 0; j < 2 * kv; ++j) {
-              const int term = j >= kv, c = term ? j - kv : j;
-              mma_ss(tmem + 256, (KV ? tv : to) + col_step(c), tS + term * (kTileBytes / 16) + col_step(c),
-                     dst, j > 0);
-            }
+            for (int j = 0; j < kv; ++j) mma_ss(tmem + 256, tvo + col_step(j), tS + col_step(j), dst, j > 0);
+            mma_commit(sempty);
+#pragma unroll 1
+            for (int j = 0; j < kv; ++j)
+              mma_ss(tmem + 256, tvo + col_step(j), tS + kTileBytes / 16 + col_step(j), dst, true);
+            if (!(ok = CATTN_WAIT(sfull, pubs))) break;
+            ++pubs;
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < kv; ++j) mma_ss(tmem + 256, tvo + col_step(j), tS + col_step(j), dst, true);
             if (KV) {
 #pragma unroll 1
               for (int j = 0; j < kk; ++j)
@@ -409,12 +433,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             mma_commit(infull);
             mma_commit(sempty);
+            ++ins;
           }
           mma_commit(KV ? empty + 8 * kV : empty + 8 * kDo);
           if (KV) mma_commit(empty + 8 * kK);
           if (!KV) mma_commit(empty + 8 * kV);
           if (!(ok = CATTN_WAIT(pfull, use))) break;
-          if (has && !(ok = CATTN_WAIT(scaled, pubs - 1))) break;
+          if (has && !(ok = CATTN_WAIT(scaled, ins - 1))) break;
           tc_fence_after();
 #pragma unroll 1
           for (int j = 0; j < steps; ++j)
@@ -710,19 +735,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (pubs > 0 && !(ok = CATTN_WARP_WAIT(sempty, pubs - 1))) break;
         if (!(ok = __all_sync(0xffffffffu, wait_count(stored, done)))) break;
         ++pubs;
-        const f2 minus = f2_splat(-1.f);
+        const uint32_t at = smem + kOffS;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          uint32_t hi[4], lo[4];
+          uint32_t mid[4], low[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            hi[j] = f2_to_bf16x2(S[4 * i + j]);
-            lo[j] = f2_to_bf16x2(f2_fma(bf16x2_to_f2(hi[j]), minus, S[4 * i + j]));
-          }
-          const uint32_t at = smem + kOffS + i / 8 * kPanelBytes + swizzled(krow, i % 8);
-          sts128(at, hi[0], hi[1], hi[2], hi[3]);
-          sts128(at + kTileBytes, lo[0], lo[1], lo[2], lo[3]);
+          for (int j = 0; j < 4; ++j) split_rest(S[4 * i + j], mid[j], low[j]);
+          const uint32_t to = at + i / 8 * kPanelBytes + swizzled(krow, i % 8);
+          sts128(to, mid[0], mid[1], mid[2], mid[3]);
+          sts128(to + kTileBytes, low[0], low[1], low[2], low[3]);
         }
+        cconv::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(sfull);
+        if (!(ok = CATTN_WARP_WAIT(sempty, pubs - 1))) break;  // the middle terms are read
+        ++pubs;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          sts128(at + i / 8 * kPanelBytes + swizzled(krow, i % 8), f2_to_bf16x2(S[4 * i]),
+                 f2_to_bf16x2(S[4 * i + 1]), f2_to_bf16x2(S[4 * i + 2]), f2_to_bf16x2(S[4 * i + 3]));
         cconv::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) bar_arrive(sfull);

@@ -473,3 +473,21 @@ def test_backwards_side_by_side():
     for runs, ref in zip(got, want):
         for grads in runs:
             assert all(torch.equal(a, b) for a, b in zip(grads[:4], ref[:4]))
+
+
+@pytest.mark.parametrize("lens,Hk,Hv,K,V", [
+    ([6, 1, 2], 3, 3, 32, 64), ([40] * 5, 2, 2, 128, 256), ([200, 130], 2, 8, 128, 128), ([1] * 9, 1, 2, 64, 40),
+])
+def test_dg_where_initial_states_outweigh_the_tokens(lens, Hk, Hv, K, V):
+    # with states of size 8 nearly all of dg is q (S do): S must be read with all its 24 bits.  In the 2-norm,
+    # where 16 bits would show as 2^-17 / 3 (2.5e-6) of each pair: 1e-6, the products' 2^-24 (6e-8), the matrix
+    # sums cut off at each of up to 24 steps of 16 terms (24 * 2^-24 / 2 = 7e-7) and the fp32 sums over K and
+    # the tokens, rounded and so of the order of 2^-24 times the root of their number (1e-7)
+    q, k, v, g, do, s0 = plain.linear_inputs(lens, Hk, Hv, K, V, seed=K + V)
+    s0 = 8 * s0
+    leaves = [t.double().requires_grad_() for t in (q, k, v, g, s0)]
+    o, _ = plain.linear(*leaves[:4], cu_of(lens), K ** -0.5, leaves[4])
+    want = torch.autograd.grad(o, leaves[3], do.double())[0]
+    dg = cc.cattn_linear_bwd(*(t.cuda() for t in (q, k, v, g, do)), _cu(lens), initial_state=s0.cuda())[3]
+    err = float((dg.double().cpu() - want).norm() / want.norm())
+    assert err <= 1e-6, err
