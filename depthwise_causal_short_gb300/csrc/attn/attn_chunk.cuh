@@ -399,6 +399,42 @@ __device__ __forceinline__ void gather_state(f2* S, const float* carry, const fl
   }
 }
 
+// Calls of at most 64 rows keep P in two bf16 terms (FINE kernels): their products are few, and over
+// a few tokens the rounding of single scores does not average out (up to 1.75 times the error of the
+// bf16 store; with more tokens it is 1.4 times that whatever the inputs are).  64 tokens take 7.7 us
+// with two terms and with one.  Decided chunk by chunk, the larger calls paid for it: 112 us against
+// 110 for 16384 rows, 416 against 384 for their gradient.  Columns of TMEM: block b's first terms at
+// 32 b and its second ones 16 on, over scores that are read; with one term at 16 b.
+constexpr int kFineTokens = 64;
+
+// P times `steps` rows of 16 tokens at `rows`, onto `out` (from zero unless `add`).
+template <bool FINE>
+__device__ __forceinline__ void mma_p(uint32_t out, uint32_t p, uint64_t rows, uint32_t desc, int steps,
+                                      bool add) {
+#pragma unroll 1
+  for (int j = 0; j < (FINE ? 2 * steps : steps); ++j) {
+    const int step = FINE ? j >> 1 : j;
+    mma_ts(out, p + (FINE ? (step >> 1) * 32 + (step & 1) * 8 + (j & 1) * 16 : j * 8), rows + step * kRowStep,
+           desc, add || j > 0);
+  }
+}
+template <bool FINE>
+__device__ __forceinline__ void put_p(uint32_t tmem, int b, const uint32_t (&x)[32]) {
+  uint32_t y[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) y[i] = f2_to_bf16x2(pair(x, i));
+  tmem_st16(tmem + b * (FINE ? 32 : 16), y);
+  if (!FINE) return;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) y[i] = f2_to_bf16x2(f2_fma(bf16x2_to_f2(y[i]), f2_splat(-1.f), pair(x, i)));
+  tmem_st16(tmem + b * 32 + 16, y);
+}
+__device__ __forceinline__ void put_pair(uint32_t (&x)[32], int i, f2 v) {
+  float a, b;
+  cconv::f2_unpack(v, a, b);
+  x[2 * i] = __float_as_uint(a), x[2 * i + 1] = __float_as_uint(b);
+}
+
 // Eight bf16 values times w, each rounded to bf16 three times: x = hi + mid + lo to 24 bits.
 // The three terms of 16 bytes go to `at`, at + step and at + 2 step.
 __device__ __forceinline__ void store_split(const uint4& in, float w, uint32_t at, uint32_t step) {

@@ -250,7 +250,7 @@ __device__ __forceinline__ void sum_ring(const float4* from, int group, int pitc
   }
 }
 
-template <bool KV>
+template <bool KV, bool FINE>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     cattn_linear_chunk_bwd_kernel(const __grid_constant__ BwdArgs p) {
   extern __shared__ uint8_t raw[];
@@ -443,14 +443,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (!(ok = CATTN_WAIT(pfull, use))) break;
           if (has && !(ok = CATTN_WAIT(scaled, ins - 1))) break;
           tc_fence_after();
-#pragma unroll 1
-          for (int j = 0; j < steps; ++j)
-            mma_ts(tmem + 256, tmem + j * 8, rows_k + j * kRowStep, dk, has || j > 0);
-          if (KV) {
-#pragma unroll 1
-            for (int j = 0; j < steps; ++j)
-              mma_ts(tmem + 384, tmem + 128 + j * 8, rows_o + j * kRowStep, dv, has || j > 0);
-          }
+          mma_p<FINE>(tmem + 256, tmem, rows_k, dk, steps, has);
+          if (KV) mma_p<FINE>(tmem + 384, tmem + 128, rows_o, dv, steps, has);
           mma_commit(ofull);
           mma_commit(empty + 8 * (KV ? kQ : kK));
           if (KV) mma_commit(empty + 8 * kDo);
@@ -563,9 +557,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!(ok = CATTN_WARP_WAIT(scfull, use))) break;
         tc_fence_after();
         f2 sum = 0;  // pairs of different tokens
-        // (P's columns [16 b, 16 b + 16) lie in score columns that are read or not needed)
+        // (P's columns lie in score columns that are read or not needed)
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < (FINE ? kFineTokens / 32 : 4); ++b) {
           uint32_t x[32], z[32];
           const bool live = KV ? b >= wq : b <= wq;
           if (live) {
@@ -590,8 +584,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const f2 wj = f2_mul(ut, j ? w.y : w.x);
                 const f2 pj = f2_mul(pair(x, 2 * i + j), wj), zj = pair(z, 2 * i + j);
                 sum = f2_fma(pj, zj, sum);
-                x[2 * i + j] = f2_to_bf16x2(pj);
-                if (KV) z[2 * i + j] = f2_to_bf16x2(f2_mul(zj, wj));
+                put_pair(x, 2 * i + j, pj);
+                if (KV) put_pair(z, 2 * i + j, f2_mul(zj, wj));
               }
             }
           } else if (b == wq) {
@@ -615,17 +609,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               }
             }
             sum = f2_add(sum, f2_pack(s, 0.f));
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              x[i] = f2_to_bf16x2(pair(x, i));
-              if (KV) z[i] = f2_to_bf16x2(pair(z, i));
-            }
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = z[i] = 0;
+            for (int i = 0; i < 32; ++i) x[i] = z[i] = 0;
           }
-          tmem_st16(tmem + lanes + b * 16, x);
-          if (KV) tmem_st16(tmem + lanes + 128 + b * 16, z);
+          put_p<FINE>(tmem + lanes, b, x);
+          if (KV) put_p<FINE>(tmem + lanes + 128, b, z);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -752,6 +741,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (lane == 0) bar_arrive(sfull);
         if (!(ok = CATTN_WARP_WAIT(sempty, pubs - 1))) break;  // the middle terms are read
         ++pubs;
+        // (rounded anew: kept from above, the first terms would spill)
+#pragma unroll
+        for (int i = 0; i < 64; ++i) asm volatile("" : "+l"(S[i]));
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           sts128(at + i / 8 * kPanelBytes + swizzled(krow, i % 8), f2_to_bf16x2(S[4 * i]),
@@ -971,7 +963,7 @@ static cudaLaunchConfig_t cluster_config(cudaLaunchAttribute (&attr)[2], int gri
 
 template <bool KV>
 static int launch_sweep(const BwdArgs& a, int grid, cudaStream_t stream) {
-  auto kern = cattn_linear_chunk_bwd_kernel<KV>;
+  auto kern = a.rows <= kFineTokens ? cattn_linear_chunk_bwd_kernel<KV, true> : cattn_linear_chunk_bwd_kernel<KV, false>;
   if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(kern), kBwdBytes) != CCONV_OK)
     return CCONV_ERR_CUDA;
   if (a.plan.group == 1 || cconv::recording_launches())
@@ -992,7 +984,7 @@ int cluster_ctas(int group, int* ctas) {
   if (report_cuda("cudaGetDevice", cudaGetDevice(&device)) != cudaSuccess) return CCONV_ERR_CUDA;
   std::atomic<int>* at = device < kDevices ? &known[device][group] : nullptr;
   if (at && (*ctas = at->load(std::memory_order_relaxed)) > 0) return CCONV_OK;
-  auto kern = cattn_linear_chunk_bwd_kernel<true>;
+  auto kern = cattn_linear_chunk_bwd_kernel<true, false>;
   if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(kern), kBwdBytes) != CCONV_OK)
     return CCONV_ERR_CUDA;
   cudaLaunchAttribute attr[2];

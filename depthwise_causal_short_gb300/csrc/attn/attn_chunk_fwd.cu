@@ -79,6 +79,7 @@ struct ChunkArgs {
 #define CATTN_WAIT(bar, parity) (wait_phase((bar), static_cast<uint32_t>(parity) & 1u))
 #define CATTN_WARP_WAIT(bar, parity) (__all_sync(0xffffffffu, CATTN_WAIT(bar, parity)))
 
+template <bool FINE>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     cattn_linear_chunk_kernel(const __grid_constant__ ChunkArgs p) {
   extern __shared__ uint8_t raw[];
@@ -240,10 +241,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if (!(ok = CATTN_WAIT(pfull, scs))) break;
           ++scs;
           tc_fence_after();
-          const int steps = (n + 15) / 16;
-#pragma unroll 1
-          for (int j = 0; j < steps; ++j)
-            mma_ts(tmem + 128, tmem + j * 8, dv + j * kRowStep, d_out, j > 0);
+          mma_p<FINE>(tmem + 128, tmem, dv, d_out, (n + 15) / 16, false);
           mma_commit(ofull);
           mma_commit(empty + 8 * kValue);
         }
@@ -349,8 +347,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (!(ok = CATTN_WARP_WAIT(scfull, scs))) break;
         tc_fence_after();
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < (FINE ? kFineTokens / 32 : 4); ++b) {
           uint32_t x[32], y[16];
+          const auto put = [&](int i, f2 v) {  // one term is rounded at once: 110 us against 114
+            if (FINE)
+              put_pair(x, i, v);
+            else
+              y[i] = f2_to_bf16x2(v);
+          };
           if (b <= wq) {
             tmem_ld32(tmem + lanes + b * 32, x);
             tmem_wait_ld();
@@ -364,8 +368,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const ulonglong2 ws = *reinterpret_cast<const ulonglong2*>(&gt.ws[b * 32 + i * 4]);
-              y[2 * i] = f2_to_bf16x2(f2_mul(pair(x, 2 * i), f2_mul(ut, ws.x)));
-              y[2 * i + 1] = f2_to_bf16x2(f2_mul(pair(x, 2 * i + 1), f2_mul(ut, ws.y)));
+              put(2 * i, f2_mul(pair(x, 2 * i), f2_mul(ut, ws.x)));
+              put(2 * i + 1, f2_mul(pair(x, 2 * i + 1), f2_mul(ut, ws.y)));
             }
           } else if (b == wq) {
             // the diagonal block: the decay from s to t as a running product down from t
@@ -380,14 +384,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 v[j] = c <= lane ? __uint_as_float(x[c]) * w : 0.f;
                 if (c <= lane) w *= j == 3 ? a.w : j == 2 ? a.z : j == 1 ? a.y : a.x;
               }
-              y[2 * i] = pack_bf16(v[0], v[1]);
-              y[2 * i + 1] = pack_bf16(v[2], v[3]);
+              put(2 * i, f2_pack(v[0], v[1]));
+              put(2 * i + 1, f2_pack(v[2], v[3]));
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = 0;
+            for (int i = 0; i < 16; ++i) put(i, 0);
           }
-          tmem_st16(tmem + lanes + b * 16, y);
+          if (FINE)
+            put_p<FINE>(tmem + lanes, b, x);
+          else
+            tmem_st16(tmem + lanes + b * 16, y);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -1088,8 +1095,9 @@ int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream) {
     if (rc == CCONV_OK) rc = launch_scan(c, c.carry, nullptr, &joined, stream);
     a.joined = joined;
   }
-  return rc == CCONV_OK ? launch(cattn_linear_chunk_kernel, dim3(c.grid), kFwdThreads, kFwdBytes, stream, a)
-                        : rc;
+  if (rc != CCONV_OK) return rc;
+  return launch(c.s.total <= kFineTokens ? cattn_linear_chunk_kernel<true> : cattn_linear_chunk_kernel<false>,
+                dim3(c.grid), kFwdThreads, kFwdBytes, stream, a);
 }
 
 size_t chunk_fwd_bytes(int grid) {

@@ -205,10 +205,6 @@ __device__ __forceinline__ void set_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return cconv::f2_to_bf16x2(cconv::f2_pack(lo, hi));
-}
-
 // exp2, relative error 2^-22, subnormal results flushed to zero.
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;

@@ -491,3 +491,18 @@ def test_dg_where_initial_states_outweigh_the_tokens(lens, Hk, Hv, K, V):
     dg = cc.cattn_linear_bwd(*(t.cuda() for t in (q, k, v, g, do)), _cu(lens), initial_state=s0.cuda())[3]
     err = float((dg.double().cpu() - want).norm() / want.norm())
     assert err <= 1e-6, err
+
+
+@pytest.mark.parametrize("lens,Hk,Hv,K,V", [([1], 1, 2, 128, 256), ([3, 0, 2], 2, 4, 32, 96), ([40], 1, 3, 64, 64),
+                                           ([63, 1], 2, 2, 96, 128)])
+def test_few_tokens_are_rounded_at_the_store_only(lens, Hk, Hv, K, V):
+    # up to 64 rows keep their scores in two bf16 terms (2^-17): what is left is the store, which rounds by
+    # up to 2^-8 of a value
+    q, k, v, g, do, _ = plain.linear_inputs(lens, Hk, Hv, K, V, seed=V)
+    leaves = [t.double().requires_grad_() for t in (q, k, v, g)]
+    o, _ = plain.linear(*leaves, cu_of(lens), K ** -0.5, None)
+    want = torch.autograd.grad(o, leaves[:3], do.double(), allow_unused=True)
+    args = [t.cuda() for t in (q, k, v, g)]
+    got = [cc.cattn_linear_fwd(*args, _cu(lens))[0], *cc.cattn_linear_bwd(*args, do.cuda(), _cu(lens))[:3]]
+    for name, a, b in zip(("o", "dq", "dk", "dv"), got, (o.detach(), *want)):
+        _check(a, b, 1.05 * 2.0 ** -8, name)
