@@ -35,7 +35,7 @@
 // of 128 bytes for 128 x 128 x 16), some 5500 cycles a chunk, and the warps' accesses and TMEM
 // loads add as much again; then by the chain of the roles, 17000 (dq) and 20000 cycles, as there is
 // no room for a second slot a tile or, in TMEM, for D's product beside the scores.  16384 rows in 2
-// sequences, 16 value heads on 8 key heads of 128: 141 and 170 us of the backward's 392.
+// sequences, 16 value heads on 8 key heads of 128: 133 and 172 us of the backward's 383.
 #include "attn_chunk.cuh"
 #include "attn_chunk_host.h"
 
@@ -70,7 +70,7 @@ constexpr int kOffS = kOffKp + 2 * kBlockBytes;         // two bf16 terms of the
 constexpr int kOffGates = kOffS + 2 * kTileBytes;
 constexpr int kOffBars = kOffGates + kBwdGates * sizeof(Gate);
 constexpr int kOffCounts = kOffBars + 40 * 8;           // [4 warps][kMaxGroup]: see ring_tile
-constexpr int kMaxGroup = 4;
+constexpr int kMaxGroup = 8;
 constexpr int kBwdBytes = kOffCounts + 4 * kMaxGroup * 4 + 1024;
 static_assert(kBwdBytes <= 232448, "shared memory of one CTA");
 

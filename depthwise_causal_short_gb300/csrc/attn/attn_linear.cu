@@ -16,6 +16,7 @@
 namespace cattn {
 
 constexpr int64_t kMaxSeqs = int64_t(1) << 30;
+constexpr int64_t kMaxGroup = 8;    // CTAs of a cluster
 constexpr int64_t kSmallSeqs = 32;  // kSmallPlan: the kernels plan for themselves
 
 // dst[t, hk, :] = sum over the (value head, column tile) parts of key head hk, in their order.
@@ -238,16 +239,17 @@ static int chunk_grid(int64_t total, int64_t nseq, int64_t Hv, int64_t V, int* g
 }
 
 // CTAs of the backward, and how many share a range: the members of a key head (its value heads
-// and their column tiles) as a cluster, where these are 2 or 4.  Measured on 16384 rows with heads
-// of 128, clusters against sums through memory, us: 2 members 382 / 431, 4 members 384 / 430 (V of
-// 256: 402 / 446), but 3 members 416 / 334, 5 332 / 285, 6 343 / 331, 7 483 / 376, 8 432 / 424: the
-// chip holds 138 CTAs in clusters of 3, and all members of a cluster wait for the slowest.
+// and their column tiles) as a cluster, where these are even and at most 8.  Measured on 16384 rows
+// with heads of 128, clusters against sums through memory, us: 2 members 380 / 448, 4 members
+// 379 / 445 (V of 256: 392 / 467), 6 members 330 / 346, 8 members 416 / 446, but 3 members 401 / 348,
+// 5 335 / 298, 7 443 / 396: a share of an odd number of 8-column pieces is half as fast to add up and
+// to store, and all members wait for the slowest.
 static int bwd_grid(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv, int64_t V, int* grid,
                     int* group) {
   *group = 1;
   if (chunk_grid(total, nseq, Hv, V, grid) != CCONV_OK) return CCONV_ERR_CUDA;
   const int64_t tiles = (V + 127) / 128, members = Hv / Hk * tiles;
-  if (members != 2 && members != 4) return CCONV_OK;
+  if (members % 2 != 0 || members > kMaxGroup) return CCONV_OK;
   int ctas = 0;
   if (cluster_ctas(static_cast<int>(members), &ctas) != CCONV_OK) return CCONV_ERR_CUDA;
   if (ctas < members) return CCONV_OK;
