@@ -21,11 +21,12 @@
 // and the copy of S that Q S reads, once each, and o at the store.  The products that build the
 // state keep 24 bits of the decayed keys (three bf16 terms), so states stay accurate to fp32.
 //
-// Bound by shared memory and by the chain of the roles: 48 products of 128 x 128 x 16 a chunk are
-// 3000 cycles of the tensor cores, which with the warps' accesses keep shared memory busy for 4700;
-// a chunk takes 8000.  16384 rows in 2 sequences, 16 value heads on 8 key heads of 128: 110 us (37 of
-// them the states handed on), 1.8 TB/s of needed bytes; one chunk 7.5 us.  Two slots for k and one
-// for v took as long as one and two; tiles fetched to L2 ahead 1 % longer.
+// Bound by the chain of the roles within a chunk: its 48 products of 128 x 128 x 16 are 3000 cycles of
+// the tensor cores, which with the warps' accesses keep shared memory busy for 4700; it takes 8000
+// (tensor cores active 25 % of the time, load / store unit 29 %, DRAM 40 %).  16384 rows in 2
+// sequences, 16 value heads on 8 key heads of 128: 110 us (37 of them the states handed on), 1.8 TB/s
+// of needed bytes; one chunk 7.5 us.  Two slots for v and one for k took as long as one and two; tiles
+// fetched to L2 ahead 1 % longer.
 #include <cudaTypedefs.h>
 
 #include <mutex>
