@@ -5,8 +5,8 @@
 //
 // Two kernels over the same ranges of units (attn_chunk.cuh): cattn_linear_tail_kernel computes
 // the state that each range hands on, cattn_linear_chunk_kernel the outputs; a range that starts
-// inside a sequence sums the handed-on states.  The backward uses the first for the states and,
-// with REV, for their gradients: (q, do) for (k, v), decays to the range's start.
+// inside a sequence sums the handed-on states.  cattn_linear_tails_kernel is the backward's first:
+// the states and, with REV, their gradients: (q, do) for (k, v), decays to the range's start.
 //
 // Roles of a CTA's 16 warps: one warp streams tiles by TMA through a ring of 32 KB slots, one
 // thread issues the products of the outputs and one those of the state, one warp makes the
@@ -926,8 +926,8 @@ __global__ void __launch_bounds__(kTailThreads, 1)
 }
 
 // Joins what the ranges hand on along each chain of ranges of one sequence, in place: carry[i]
-// becomes the whole state at the end (REV: start) of CTA i's range.  For long chains: a sweep's CTA would read every state of its chain, one after the other
-// (0.8 us each); here each thread follows 16 bytes of it along the chain with kScanAhead reads in
+// becomes the whole state at the end (REV: start) of CTA i's range.  For long chains: a sweep's CTA
+// would read every state of its chain, one after the other (0.8 us each); here each thread follows 16 bytes of it along the chain with kScanAhead reads in
 // flight.  grid: (ranges, slices of a state, directions); the CTAs of ranges that do not start a
 // chain have nothing to do.
 constexpr int kScanThreads = 256, kScanAhead = 8, kMaxRanges = 1024;
