@@ -871,6 +871,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           p.dots[(static_cast<int64_t>(plan.heads) * plan.tiles + ht) * p.rows + t] =
               p.scale * rowf * (d0 + d1);
         if (!(ok = CATTN_WARP_WAIT(ofull, use))) break;
+        // The last chunk's outputs may still be on their way out of the staging buffer: `ofree` does
+        // not wait for them, and only a chunk with a state is held back by the state's warps.
+        if (!(ok = __all_sync(0xffffffffu, wait_count(stored, use)))) break;
         tc_fence_after();
         const bool whole = n == kChunk, live = row < n;
         const int hk = hv / p.ratio;

@@ -1,0 +1,50 @@
+"""The mixer's kernels where their parts meet each other, earlier kernels and other streams (GPU).
+
+Tolerances are those of test_attn_linear_gpu.py, where they are derived.
+"""
+import pytest
+import torch
+
+import depthwise_causal_short_gb300 as cc
+from depthwise_causal_short_gb300 import _build
+from tests import attn_plain as plain
+from tests.helpers import rel_err
+
+pytestmark = pytest.mark.gpu
+BF16_TOL = 8e-3
+DG_TOL = 2e-5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    _build.build()
+    yield
+    assert cc.cattn_device_fault() == 0
+
+
+def _cu(lens):
+    return torch.tensor([0] + list(lens), dtype=torch.int32).cumsum(0).to(torch.int32).cuda()
+
+
+def _inputs(lens, Hk, Hv, K, V, seed=0):
+    return plain.linear_inputs(lens, Hk, Hv, K, V, seed=seed)
+
+
+@pytest.mark.parametrize("lens,Hk,Hv,K,V", [
+    ([128] * 40, 16, 16, 64, 64), ([128] * 24, 4, 12, 128, 128), ([256, 128] * 10, 1, 9, 32, 128),
+])
+def test_whole_chunks_without_a_state_share_the_staging_buffer(lens, Hk, Hv, K, V):
+    # Members of a key head that are no cluster (1, 3 and 9 of them) finish their chunks in the staging
+    # buffer; whole chunks that need no state follow one another there with nothing else to wait for.
+    q, k, v, g, do, _ = _inputs(lens, Hk, Hv, K, V, seed=V)
+    leaves = [t.double().requires_grad_() for t in (q, k, v, g)]
+    cu = [0] + torch.tensor(lens).cumsum(0).tolist()
+    want = torch.autograd.grad(plain.linear(*leaves, cu, K ** -0.5)[0], leaves, do.double())
+    args = [t.cuda() for t in (q, k, v, g, do)]
+    first = cc.cattn_linear_bwd(*args, _cu(lens))[:4]
+    for name, a, b, tol in zip(("dq", "dk", "dv", "dg"), first, want, (BF16_TOL,) * 3 + (DG_TOL,)):
+        assert rel_err(a.double().cpu(), b) <= tol, name
+    for _ in range(20):
+        assert all(torch.equal(a, b) for a, b in zip(cc.cattn_linear_bwd(*args, _cu(lens))[:4], first))
