@@ -99,11 +99,14 @@ struct BwdArgs {
 #define CATTN_WAIT(bar, parity) (wait_phase((bar), static_cast<uint32_t>(parity) & 1u))
 #define CATTN_WARP_WAIT(bar, parity) (__all_sync(0xffffffffu, CATTN_WAIT(bar, parity)))
 
-// Dot of 32 fp32 values with columns [c, c + 32) of row `row` of a bf16 tile.
-__device__ __forceinline__ f2 dot_tile(uint32_t tile, int row, int c, const uint32_t* x, f2 dot) {
+// Dot of 32 fp32 values with columns [c, c + 32) of row `row` of a bf16 tile, those below `width` only:
+// the products write 16 columns at a time, and what tensor memory holds past them may be NaN, which the
+// tile's zeros there would not take out.
+__device__ __forceinline__ f2 dot_tile(uint32_t tile, int row, int c, int width, const uint32_t* x, f2 dot) {
   const uint32_t at = tile + (c >> 6) * kPanelBytes;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    if (c + 8 * i >= width) break;
     const uint4 w = lds128_at(at + swizzled(row, ((c >> 3) & 7) + i));
     dot = f2_fma(bf16x2_to_f2(w.x), pair(x, 4 * i), dot);
     dot = f2_fma(bf16x2_to_f2(w.y), pair(x, 4 * i + 1), dot);
@@ -852,7 +855,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tmem_ld32(tmem + lanes + 256 + c, x);
             tmem_wait_ld();
             tmem_use32(x);
-            dot = dot_tile(KV ? ak : aq, row, c, x, dot);
+            dot = dot_tile(KV ? ak : aq, row, c, p.K, x, dot);
             scale32(x, rowf);
             tmem_st16(tmem + lanes + 256 + c, x);
             tmem_st16(tmem + lanes + 256 + c + 16, x + 16);

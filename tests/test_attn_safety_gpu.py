@@ -48,3 +48,21 @@ def test_whole_chunks_without_a_state_share_the_staging_buffer(lens, Hk, Hv, K, 
         assert rel_err(a.double().cpu(), b) <= tol, name
     for _ in range(20):
         assert all(torch.equal(a, b) for a, b in zip(cc.cattn_linear_bwd(*args, _cu(lens))[:4], first))
+
+
+@pytest.mark.parametrize("Hk,Hv", [(2, 2), (1, 2)])
+@pytest.mark.parametrize("K", [8, 16, 40, 48, 72, 80, 104, 112])
+def test_dg_does_not_see_what_tensor_memory_held(K, Hk, Hv):
+    # Products over K channels write a multiple of 16 columns; the rows' dots must not read on to the next
+    # multiple of 32.  A forward on NaN leaves NaN there.
+    n = 128 * 300
+    bad = torch.full((n, 1, 128), float("nan"), dtype=torch.bfloat16).cuda()
+    bad_g = torch.zeros(n, 1).cuda()
+    lens = [300, 129, 1]
+    q, k, v, g, do, s0 = (t.cuda() for t in _inputs(lens, Hk, Hv, K, 64, seed=K))
+    cc.cattn_linear_fwd(*(torch.zeros_like(bad),) * 3, bad_g, _cu([n]))
+    want = cc.cattn_linear_bwd(q, k, v, g, do, _cu(lens), initial_state=s0)
+    cc.cattn_linear_fwd(bad, bad, bad, bad_g, _cu([n]))
+    got = cc.cattn_linear_bwd(q, k, v, g, do, _cu(lens), initial_state=s0)
+    for a, b in zip(got, want):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
