@@ -954,7 +954,8 @@ __global__ void __launch_bounds__(kScanThreads) cattn_linear_scan_kernel(const _
 #pragma unroll
     for (int j = 0; j < kScanAhead; ++j) {
       const int r = i + j * by;
-      if (n == j && r >= 0 && r < p.grid && decay[r] >= 0.f) {
+      // (a NaN decay goes on with the chain: all that follows it is NaN)
+      if (n == j && r >= 0 && r < p.grid && decay[r] != kChainStart && decay[r] != kNoTail) {
         x[j] = states[r * kPitch];
         n = j + 1;
       }

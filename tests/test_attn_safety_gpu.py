@@ -66,3 +66,22 @@ def test_dg_does_not_see_what_tensor_memory_held(K, Hk, Hv):
     got = cc.cattn_linear_bwd(q, k, v, g, do, _cu(lens), initial_state=s0)
     for a, b in zip(got, want):
         assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("Hv,n", [(1, 5000), (2, 4000), (8, 3000)])
+def test_a_nan_gate_reaches_all_that_comes_after_it(Hv, n):
+    # few heads and long sequences: the states that ranges hand on are joined by a kernel of their own
+    Hk, K, V, at = 1, 64, 64, n // 2 - 77
+    q, k, v, g, do, s0 = (t.cuda() for t in _inputs([n], Hk, Hv, K, V, seed=n))
+    g = g * 1e-3  # nothing is forgotten
+    clean = cc.cattn_linear_fwd(q, k, v, g, _cu([n]), initial_state=s0)[0]
+    g[at, Hv - 1] = float("nan")
+    o, fin, _ = cc.cattn_linear_fwd(q, k, v, g, _cu([n]), initial_state=s0, final_state=True)
+    assert o[at:, Hv - 1].isnan().all() and fin[0, Hv - 1].isnan().all()
+    # (tokens of the same chunk before it may see it too)
+    assert torch.equal(o[:at - 127], clean[:at - 127]) and torch.equal(o[:, :Hv - 1], clean[:, :Hv - 1])
+    dq, dk, dv, dg, ds = cc.cattn_linear_bwd(q, k, v, g, do, _cu([n]), initial_state=s0)
+    assert dq[at:].isnan().all() and dk[:at].isnan().all() and dv[:at, Hv - 1].isnan().all()
+    assert dg[:, Hv - 1].isnan().all() and ds[0, Hv - 1].isnan().all()
+    for t in (dv[:, :Hv - 1], dg[:, :Hv - 1], ds[0, :Hv - 1]):
+        assert torch.isfinite(t).all()
