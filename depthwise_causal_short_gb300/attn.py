@@ -5,6 +5,11 @@ Like the convolution's binding, it only checks and marshals arguments and alloca
 caller does not pass: every step of the computation runs in the library's CUDA kernels, and there
 is no fallback.  The checks and the call are compiled (csrc/attn/py/attn_py.cpp, ``_cattn.so``);
 this module holds the signatures.  load() gives the C ABI itself, through ctypes.
+
+``stream`` (a torch stream or a raw handle) runs a call there, as under ``with
+torch.cuda.stream(stream)``: the caller orders it after what made the inputs and before what reads
+the results; tensors that the call makes for itself, the workspace among them, are safe by
+themselves.
 """
 from __future__ import annotations
 

@@ -3,8 +3,8 @@
 //
 // The C ABI sees pointers and sizes only, so every tensor's shape, dtype and layout is checked
 // here first (TypeError / ValueError), then that all live on one CUDA device (ValueError); then the
-// call runs with that device current, on its current stream unless one is given.  A nonzero
-// status raises CConvError.  Nothing is computed here.  It is compiled because the smallest calls
+// call runs with that device current, on its current stream unless one is given, and with tensors of
+// its own from that stream's memory.  A nonzero status raises CConvError.  Nothing is computed here.  It is compiled because the smallest calls
 // take 2 to 8 us on the device: the same checks in Python with ctypes cost 15 to 20 us a call.
 //
 // The functions take their arguments by position; attn.py holds the signatures that users see.
@@ -128,9 +128,8 @@ c10::DeviceIndex check_device(std::initializer_list<const Arg*> all) {
   return static_cast<c10::DeviceIndex>(index);
 }
 
-// None: the device's current stream; a torch stream; or a raw handle.
-cconv_stream_t stream_of(PyObject* o, c10::DeviceIndex dev) {
-  if (o == Py_None) return reinterpret_cast<cconv_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream());
+// A torch stream, or a raw handle.
+cudaStream_t stream_of(PyObject* o, c10::DeviceIndex dev) {
   PyObject* raw = PyObject_GetAttrString(o, "cuda_stream");
   if (raw) {
     PyObject* index = PyObject_GetAttrString(o, "device_index");
@@ -151,8 +150,43 @@ cconv_stream_t stream_of(PyObject* o, c10::DeviceIndex dev) {
   const unsigned long long v = PyLong_AsUnsignedLongLong(raw);
   Py_DECREF(raw);
   if (PyErr_Occurred()) throw Raised{};
-  return reinterpret_cast<cconv_stream_t>(v);
+  return reinterpret_cast<cudaStream_t>(v);
 }
+
+// The device and stream of a call, current while it runs: its own device's current stream where None
+// is given.  What the call allocates comes from that stream's memory, so that a workspace, which is
+// freed when the call returns, goes to nothing that does not wait for the kernels.  (From another
+// stream's memory it could be handed out, and written, while they still use it.)
+class Place {
+ public:
+  Place(PyObject* stream, c10::DeviceIndex dev)
+      : dev_(dev), caller_(c10::cuda::getCurrentCUDAStream(dev)), stream_(caller_), device_(dev) {
+    if (stream == Py_None) return;
+    cudaStream_t raw = stream_of(stream, dev);
+    if (raw == cudaStreamLegacy) raw = nullptr;  // the same stream; the allocator knows it by this
+    stream_ = c10::cuda::getStreamFromExternal(raw, dev);
+    aside_.reset_stream(stream_);
+  }
+  cconv_stream_t handle() const { return reinterpret_cast<cconv_stream_t>(stream_.stream()); }
+  at::Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
+    return at::empty(shape, at::TensorOptions().dtype(type).device(c10::Device(at::kCUDA, dev_)));
+  }
+  // The argument, or a new tensor in its place, for the caller to use and free on its own stream.
+  void out_or_new(const Arg& a, at::Tensor& own, at::IntArrayRef shape, at::ScalarType type) const {
+    if (a.given()) {
+      own = *a.t;
+      return;
+    }
+    own = make(shape, type);
+    if (stream_.stream() != caller_.stream()) own.record_stream(caller_.unwrap());
+  }
+
+ private:
+  c10::DeviceIndex dev_;
+  c10::cuda::CUDAStream caller_, stream_;
+  c10::cuda::CUDAGuard device_;
+  c10::cuda::OptionalCUDAStreamGuard aside_;
+};
 
 void check_rc(int rc, const char* call) {
   if (rc == CCONV_OK) return;
@@ -162,17 +196,6 @@ void check_rc(int rc, const char* call) {
     Py_DECREF(e);
   }
   throw Raised{};
-}
-
-at::Tensor make(at::IntArrayRef shape, at::ScalarType type, c10::DeviceIndex dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(c10::Device(at::kCUDA, dev)));
-}
-
-// The argument, or a new tensor in its place (held by `own`).
-const at::Tensor& out_or_new(const Arg& a, at::Tensor& own, at::IntArrayRef shape, at::ScalarType type,
-                             c10::DeviceIndex dev) {
-  own = a.given() ? *a.t : make(shape, type, dev);
-  return own;
 }
 
 float as_float(PyObject* o) {
@@ -272,16 +295,16 @@ PyObject* qknorm_fwd(PyObject* const* a, Py_ssize_t count) {
   check_disjoint(yq, {&n.q, &n.k});
   check_disjoint(yk, {&n.q, &n.k, &yq});
   const auto dev = check_device({&n.q, &n.k, &n.wq, &n.wk, &n.cos, &n.sin, &n.pos, &yq, &yk});
-  const c10::cuda::CUDAGuard guard(dev);
+  const Place place(a[12], dev);
   at::Tensor oq, ok;
-  out_or_new(yq, oq, {n.total, n.Hq, n.K}, at::kBFloat16, dev);
-  out_or_new(yk, ok, {n.total, n.Hk, n.K}, at::kBFloat16, dev);
+  place.out_or_new(yq, oq, {n.total, n.Hq, n.K}, at::kBFloat16);
+  place.out_or_new(yk, ok, {n.total, n.Hk, n.K}, at::kBFloat16);
   const at::Tensor &q = *n.q.t, &k = *n.k.t;
   check_rc(cattn_qknorm_fwd(q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1),
                             n.total, n.Hq, n.Hk, n.K, n.wq.ptr(), n.wk.ptr(), n.wdt, n.mode, n.eps,
                             static_cast<const float*>(n.cos.ptr()), static_cast<const float*>(n.sin.ptr()),
                             n.P, n.R, n.inter, static_cast<const int32_t*>(n.pos.ptr()), oq.data_ptr(),
-                            ok.data_ptr(), stream_of(a[12], dev)),
+                            ok.data_ptr(), place.handle()),
            "cattn_qknorm_fwd");
   return tuple({&oq, &ok});
 }
@@ -310,18 +333,18 @@ PyObject* qknorm_bwd(PyObject* const* a, Py_ssize_t count) {
   if (ws.given() && !ws.t->is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
   const auto dev = check_device({&n.q, &n.k, &dyq, &dyk, &n.wq, &n.wk, &n.cos, &n.sin, &n.pos, &dq, &dk, &dwq,
                                  &dwk, &ws});
-  const c10::cuda::CUDAGuard guard(dev);
+  const Place place(a[17], dev);
   at::Tensor oq, ok, wq, wk, work;
-  out_or_new(dq, oq, {n.total, n.Hq, n.K}, at::kBFloat16, dev);
-  out_or_new(dk, ok, {n.total, n.Hk, n.K}, at::kBFloat16, dev);
-  if (n.wq.given()) out_or_new(dwq, wq, {n.K}, n.wq.t->scalar_type(), dev);
-  if (n.wk.given()) out_or_new(dwk, wk, {n.K}, n.wk.t->scalar_type(), dev);
+  place.out_or_new(dq, oq, {n.total, n.Hq, n.K}, at::kBFloat16);
+  place.out_or_new(dk, ok, {n.total, n.Hk, n.K}, at::kBFloat16);
+  if (n.wq.given()) place.out_or_new(dwq, wq, {n.K}, n.wq.t->scalar_type());
+  if (n.wk.given()) place.out_or_new(dwk, wk, {n.K}, n.wk.t->scalar_type());
   if (ws.given()) {
     work = *ws.t;
   } else if (wq.defined() || wk.defined()) {
     size_t bytes = 0;
     check_rc(cattn_qknorm_bwd_workspace_bytes(n.total, n.Hq, n.Hk, n.K, &bytes), "cattn_qknorm_bwd_workspace_bytes");
-    work = make({static_cast<int64_t>(bytes)}, at::kByte, dev);
+    work = place.make({static_cast<int64_t>(bytes)}, at::kByte);
   }
   const at::Tensor &q = *n.q.t, &k = *n.k.t, &yq = *dyq.t, &yk = *dyk.t;
   check_rc(cattn_qknorm_bwd(q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1),
@@ -331,7 +354,7 @@ PyObject* qknorm_bwd(PyObject* const* a, Py_ssize_t count) {
                             n.P, n.R, n.inter, static_cast<const int32_t*>(n.pos.ptr()), oq.data_ptr(),
                             ok.data_ptr(), wq.defined() ? wq.data_ptr() : nullptr,
                             wk.defined() ? wk.data_ptr() : nullptr, work.defined() ? work.data_ptr() : nullptr,
-                            work.defined() ? work.nbytes() : 0, stream_of(a[17], dev)),
+                            work.defined() ? work.nbytes() : 0, place.handle()),
            "cattn_qknorm_bwd");
   return tuple({&oq, &ok, &wq, &wk});
 }
@@ -389,11 +412,11 @@ int64_t check_cu(const Arg& a) {
       static_cast<const float*>((n).g.t->data_ptr()), (n).g.t->stride(0), (n).g.t->stride(1)
 
 at::Tensor workspace_of(const Arg& ws, int (*query)(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, size_t*),
-                        const char* call, const Linear& n, int64_t nseq, c10::DeviceIndex dev) {
+                        const char* call, const Linear& n, int64_t nseq, const Place& place) {
   if (ws.given()) return *ws.t;
   size_t bytes = 0;
   check_rc(query(n.rows, nseq, n.Hk, n.Hv, n.K, n.V, &bytes), call);
-  return make({static_cast<int64_t>(bytes < 16 ? 16 : bytes)}, at::kByte, dev);
+  return place.make({static_cast<int64_t>(bytes < 16 ? 16 : bytes)}, at::kByte);
 }
 
 // q, k, v, g, scale, cu_seqlens, initial_state, final_state (a tensor, True or None), state_indices,
@@ -428,18 +451,18 @@ PyObject* linear_fwd(PyObject* const* a, Py_ssize_t count) {
   check_disjoint(fin, {&n.q, &n.k, &n.v, &n.g});
   if (ws.given() && !ws.t->is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
   const auto dev = check_device({&n.q, &n.k, &n.v, &n.g, &cu, &init, &fin, &idx, &status, &o, &ws});
-  const c10::cuda::CUDAGuard guard(dev);
+  const Place place(a[12], dev);
   at::Tensor out, final_state, st;
-  out_or_new(o, out, {n.rows, n.Hv, n.V}, at::kBFloat16, dev);
-  if (want || fin.given()) out_or_new(fin, final_state, {nseq, n.Hv, n.K, n.V}, at::kFloat, dev);
-  if (idx.given()) out_or_new(status, st, {2}, at::kInt, dev);
-  const at::Tensor work = workspace_of(ws, cattn_linear_fwd_workspace_bytes, "cattn_linear_fwd_workspace_bytes", n, nseq, dev);
+  place.out_or_new(o, out, {n.rows, n.Hv, n.V}, at::kBFloat16);
+  if (want || fin.given()) place.out_or_new(fin, final_state, {nseq, n.Hv, n.K, n.V}, at::kFloat);
+  if (idx.given()) place.out_or_new(status, st, {2}, at::kInt);
+  const at::Tensor work = workspace_of(ws, cattn_linear_fwd_workspace_bytes, "cattn_linear_fwd_workspace_bytes", n, nseq, place);
   check_rc(cattn_linear_fwd(QKVG(n), n.rows, n.Hk, n.Hv, n.K, n.V, static_cast<const int32_t*>(cu.ptr()), nseq,
                             n.scale, static_cast<const float*>(init.ptr()),
                             final_state.defined() ? static_cast<float*>(final_state.data_ptr()) : nullptr,
                             static_cast<const int32_t*>(idx.ptr()), S,
                             st.defined() ? static_cast<int32_t*>(st.data_ptr()) : nullptr, out.data_ptr(),
-                            work.data_ptr(), work.nbytes(), stream_of(a[12], dev)),
+                            work.data_ptr(), work.nbytes(), place.handle()),
            "cattn_linear_fwd");
   return tuple({&out, &final_state, &st});
 }
@@ -483,21 +506,21 @@ PyObject* linear_bwd(PyObject* const* a, Py_ssize_t count) {
   check_disjoint(dg, {&dq, &dk, &dv});
   if (ws.given() && !ws.t->is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
   const auto dev = check_device({&n.q, &n.k, &n.v, &n.g, &dout, &cu, &init, &idx, &status, &dq, &dk, &dv, &dg, &ds, &ws});
-  const c10::cuda::CUDAGuard guard(dev);
+  const Place place(a[17], dev);
   at::Tensor oq, ok, ov, og, os;
-  out_or_new(dq, oq, n.q.t->sizes(), at::kBFloat16, dev);
-  out_or_new(dk, ok, n.q.t->sizes(), at::kBFloat16, dev);
-  out_or_new(dv, ov, n.v.t->sizes(), at::kBFloat16, dev);
-  out_or_new(dg, og, {n.rows, n.Hv}, at::kFloat, dev);
-  if (want) out_or_new(ds, os, {nseq, n.Hv, n.K, n.V}, at::kFloat, dev);
-  const at::Tensor work = workspace_of(ws, cattn_linear_bwd_workspace_bytes, "cattn_linear_bwd_workspace_bytes", n, nseq, dev);
+  place.out_or_new(dq, oq, n.q.t->sizes(), at::kBFloat16);
+  place.out_or_new(dk, ok, n.q.t->sizes(), at::kBFloat16);
+  place.out_or_new(dv, ov, n.v.t->sizes(), at::kBFloat16);
+  place.out_or_new(dg, og, {n.rows, n.Hv}, at::kFloat);
+  if (want) place.out_or_new(ds, os, {nseq, n.Hv, n.K, n.V}, at::kFloat);
+  const at::Tensor work = workspace_of(ws, cattn_linear_bwd_workspace_bytes, "cattn_linear_bwd_workspace_bytes", n, nseq, place);
   const at::Tensor& d = *dout.t;
   check_rc(cattn_linear_bwd(QKVG(n), d.data_ptr(), d.stride(0), d.stride(1), n.rows, n.Hk, n.Hv, n.K, n.V,
                             static_cast<const int32_t*>(cu.ptr()), nseq, n.scale, static_cast<const float*>(init.ptr()),
                             static_cast<const int32_t*>(idx.ptr()), S, static_cast<int32_t*>(status.out()),
                             oq.data_ptr(), ok.data_ptr(), ov.data_ptr(), static_cast<float*>(og.data_ptr()),
                             os.defined() ? static_cast<float*>(os.data_ptr()) : nullptr, work.data_ptr(),
-                            work.nbytes(), stream_of(a[17], dev)),
+                            work.nbytes(), place.handle()),
            "cattn_linear_bwd");
   return tuple({&oq, &ok, &ov, &og, &os});
 }
@@ -517,13 +540,13 @@ PyObject* linear_update(PyObject* const* a, Py_ssize_t count) {
   check_disjoint(o, {&n.q, &n.k, &n.v, &n.g, &state});
   if (status.given()) check_status(status);
   const auto dev = check_device({&n.q, &n.k, &n.v, &n.g, &state, &idx, &o, &status});
-  const c10::cuda::CUDAGuard guard(dev);
+  const Place place(a[10], dev);
   at::Tensor out, st;
-  out_or_new(o, out, n.v.t->sizes(), at::kBFloat16, dev);
-  out_or_new(status, st, {2}, at::kInt, dev);
+  place.out_or_new(o, out, n.v.t->sizes(), at::kBFloat16);
+  place.out_or_new(status, st, {2}, at::kInt);
   check_rc(cattn_linear_update(QKVG(n), n.rows, n.Hk, n.Hv, n.K, n.V, n.scale, static_cast<float*>(state.out()), S,
                                static_cast<const int32_t*>(idx.ptr()), as_bool(a[7]), out.data_ptr(),
-                               static_cast<int32_t*>(st.data_ptr()), stream_of(a[10], dev)),
+                               static_cast<int32_t*>(st.data_ptr()), place.handle()),
            "cattn_linear_update");
   return tuple({&out, &st});
 }

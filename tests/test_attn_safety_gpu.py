@@ -85,3 +85,65 @@ def test_a_nan_gate_reaches_all_that_comes_after_it(Hv, n):
     assert dg[:, Hv - 1].isnan().all() and ds[0, Hv - 1].isnan().all()
     for t in (dv[:, :Hv - 1], dg[:, :Hv - 1], ds[0, :Hv - 1]):
         assert torch.isfinite(t).all()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_given_streams_calls_keep_their_memory_until_it_has_used_it(raw):
+    # the calls wait on a busy stream while the current one takes and fills all the memory it is given
+    lens, Hk, Hv, K, V = [700, 300], 2, 4, 64, 64
+    q, k, v, g, do, s0 = (t.cuda() for t in _inputs(lens, Hk, Hv, K, V, seed=3))
+    cu, w = _cu(lens), torch.rand(K).cuda()
+    pool = torch.randn(2, Hv, K, V).cuda()
+
+    def calls(**kw):
+        state = pool.clone()
+        torch.cuda.synchronize()
+        if kw:
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(200_000_000)  # some 0.1 s
+        return (*cc.cattn_linear_fwd(q, k, v, g, cu, initial_state=s0, final_state=True, **kw)[:2],
+                *cc.cattn_linear_bwd(q, k, v, g, do, cu, initial_state=s0, **kw),
+                *cc.cattn_qknorm_fwd(q, k, wq=w, wk=w, **kw),
+                *cc.cattn_qknorm_bwd(q, k, k, q, wq=w, wk=w, **kw),
+                *cc.cattn_linear_update(q[:2], k[:2], v[:2], g[:2], state, **kw), state)
+
+    sizes = [16, 512, 2048, 1 << 20, 2 << 20, 8 << 20, 20 << 20, 64 << 20] * 6
+    sizes += [cc.cattn_linear_fwd_workspace_bytes(1000, 2, Hk, Hv, K, V),
+              cc.cattn_linear_bwd_workspace_bytes(1000, 2, Hk, Hv, K, V),
+              cc.cattn_qknorm_bwd_workspace_bytes(1000, Hk, Hk, K)] * 4
+
+    def take():  # blocks of every size that a call has just freed, and many more
+        return [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes]
+
+    want = calls()
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    for first in (True, False):  # the first time, memory comes from the device, which waits for the streams
+        got = calls(stream=stream)
+        fill = take()
+        if first:
+            torch.cuda.synchronize()
+            del got, fill
+    torch.cuda.current_stream().synchronize()
+    assert not side.query()  # the calls are still to run
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert all(bool((t == 255).all()) for t in fill)
+
+
+def test_what_a_given_streams_call_returns_is_free_for_the_caller_to_use():
+    # a result that is dropped while the caller's stream still reads it is not given to the next call
+    q = torch.randn(4096, 8, 128).bfloat16().cuda()
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    first = cc.cattn_qknorm_fwd(q, q)[0]
+    torch.cuda.synchronize()
+    y, _ = cc.cattn_qknorm_fwd(q, q, stream=side)
+    here.wait_stream(side)
+    torch.cuda._sleep(200_000_000)
+    copy = y.clone()  # after the sleep
+    del y, _
+    for _ in range(4):
+        cc.cattn_qknorm_fwd(-q, -q, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, first)
