@@ -167,7 +167,8 @@ def cattn_linear_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
     o_t = scale q_t^T S_t.  q, k [total, Hk, K], v [total, Hv, V] bf16; g [total, Hv] fp32 (any
     strides, e.g. expanded from [Hv]); cu_seqlens int32 [nseq+1]; scale defaults to K^-0.5.
     States fp32 [S, Hv, K, V]; final_state=True allocates [nseq, Hv, K, V]; with state_indices
-    int32 [nseq] sequence i's state is slot state_indices[i] and a status int32[2] is written.
+    int32 [nseq] sequence i's state is slot state_indices[i] of both and a status int32[2] is written
+    (a pool of more than nseq slots then wants a tensor for final_state, e.g. the pool itself).
     Returns (o, final_state or None, status or None)."""
     return _calls().linear_fwd(q, k, v, g, scale, cu_seqlens, initial_state, final_state, state_indices,
                                status, o, workspace, stream)

@@ -442,6 +442,12 @@ PyObject* linear_fwd(PyObject* const* a, Py_ssize_t count) {
   if (idx.given()) {
     check_exact(idx, {nseq}, at::kInt);
     if (status.given()) check_status(status);
+    // (a new array holds a slot for each sequence: the pool's other indices have no place in it)
+    if (want && init.given() && init.t->size(0) > nseq)
+      raise(PyExc_ValueError,
+            "final_state=True makes %lld slots, but state_indices name slots of initial_state, which has %lld: pass a "
+            "tensor for final_state (the pool itself updates it in place)",
+            (long long)nseq, (long long)init.t->size(0));
   } else if (pools && S < nseq) {
     raise(PyExc_ValueError, "without state_indices sequence i uses slot i: state arrays need at least nseq=%lld slots",
           (long long)nseq);

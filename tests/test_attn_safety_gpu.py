@@ -147,3 +147,19 @@ def test_what_a_given_streams_call_returns_is_free_for_the_caller_to_use():
         cc.cattn_qknorm_fwd(-q, -q, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(copy, first)
+
+
+def test_a_new_final_state_with_slots_of_a_larger_pool_is_refused():
+    lens, Hk, Hv, K, V = [5, 3], 1, 1, 16, 16
+    q, k, v, g, _, _ = (t.cuda() for t in _inputs(lens, Hk, Hv, K, V))
+    pool = torch.randn(9, Hv, K, V).cuda()
+    idx = torch.tensor([7, 1], dtype=torch.int32).cuda()
+    with pytest.raises(ValueError, match="final_state"):
+        cc.cattn_linear_fwd(q, k, v, g, _cu(lens), initial_state=pool, final_state=True, state_indices=idx)
+    # as many slots as sequences: any order of them
+    pool, idx = pool[:2].contiguous(), torch.tensor([1, 0], dtype=torch.int32).cuda()
+    want = cc.cattn_linear_fwd(q, k, v, g, _cu(lens), initial_state=pool[[1, 0]].contiguous(), final_state=True)
+    o, fin, status = cc.cattn_linear_fwd(q, k, v, g, _cu(lens), initial_state=pool, final_state=True,
+                                         state_indices=idx)
+    assert status.tolist() == [0, 0]
+    assert torch.equal(o, want[0]) and torch.equal(fin[[1, 0]], want[1])
