@@ -54,6 +54,7 @@ Arg tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) raise(PyExc_TypeError, "%s must be a torch.Tensor, got %s", name, Py_TYPE(o)->tp_name);
   return Arg{name, &THPVariable_Unpack(o)};
 }
+const Arg none{"", nullptr};
 Arg optional(PyObject* o, const char* name) {
   return o == Py_None ? Arg{name, nullptr} : tensor(o, name);
 }
@@ -101,15 +102,19 @@ void extent(const at::Tensor& t, uintptr_t* a, uintptr_t* b) {
   *b = *a + static_cast<uintptr_t>(span) * t.element_size();
 }
 
-// An output may overlap nothing that the call reads.
-void check_disjoint(const Arg& out, std::initializer_list<const Arg*> ins) {
-  if (!out.given()) return;
+// What a call writes may overlap nothing that it reads, nor what else it writes.
+void check_disjoint(std::initializer_list<const Arg*> outs, std::initializer_list<const Arg*> ins) {
   uintptr_t a0, a1, b0, b1;
-  extent(*out.t, &a0, &a1);
-  for (const Arg* in : ins) {
-    if (!in->given()) continue;
-    extent(*in->t, &b0, &b1);
-    if (a0 < b1 && b0 < a1) raise(PyExc_ValueError, "%s overlaps %s", out.name, in->name);
+  for (const Arg* const* out = outs.begin(); out != outs.end(); ++out) {
+    if (!(*out)->given()) continue;
+    extent(*(*out)->t, &a0, &a1);
+    auto against = [&](const Arg* x) {
+      if (!x->given()) return;
+      extent(*x->t, &b0, &b1);
+      if (a0 < b1 && b0 < a1) raise(PyExc_ValueError, "%s overlaps %s", (*out)->name, x->name);
+    };
+    for (const Arg* in : ins) against(in);
+    for (const Arg* const* other = outs.begin(); other != out; ++other) against(*other);
   }
 }
 
@@ -292,8 +297,7 @@ PyObject* qknorm_fwd(PyObject* const* a, Py_ssize_t count) {
   const Arg yq = optional(a[10], "yq"), yk = optional(a[11], "yk");
   if (yq.given()) check_exact(yq, {n.total, n.Hq, n.K}, at::kBFloat16);
   if (yk.given()) check_exact(yk, {n.total, n.Hk, n.K}, at::kBFloat16);
-  check_disjoint(yq, {&n.q, &n.k});
-  check_disjoint(yk, {&n.q, &n.k, &yq});
+  check_disjoint({&yq, &yk}, {&n.q, &n.k, &n.wq, &n.wk, &n.cos, &n.sin, &n.pos});
   const auto dev = check_device({&n.q, &n.k, &n.wq, &n.wk, &n.cos, &n.sin, &n.pos, &yq, &yk});
   const Place place(a[12], dev);
   at::Tensor oq, ok;
@@ -322,8 +326,6 @@ PyObject* qknorm_bwd(PyObject* const* a, Py_ssize_t count) {
   check_same_shape(dyk, n.k);
   if (dq.given()) check_exact(dq, {n.total, n.Hq, n.K}, at::kBFloat16);
   if (dk.given()) check_exact(dk, {n.total, n.Hk, n.K}, at::kBFloat16);
-  check_disjoint(dq, {&n.q, &n.k, &dyq, &dyk});
-  check_disjoint(dk, {&n.q, &n.k, &dyq, &dyk, &dq});
   const Arg* sums[2][2] = {{&dwq, &n.wq}, {&dwk, &n.wk}};
   for (auto& s : sums) {
     if (!s[0]->given()) continue;
@@ -331,6 +333,7 @@ PyObject* qknorm_bwd(PyObject* const* a, Py_ssize_t count) {
     check_exact(*s[0], {n.K}, s[1]->t->scalar_type());
   }
   if (ws.given() && !ws.t->is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
+  check_disjoint({&dq, &dk, &dwq, &dwk, &ws}, {&n.q, &n.k, &dyq, &dyk, &n.wq, &n.wk, &n.cos, &n.sin, &n.pos});
   const auto dev = check_device({&n.q, &n.k, &dyq, &dyk, &n.wq, &n.wk, &n.cos, &n.sin, &n.pos, &dq, &dk, &dwq,
                                  &dwk, &ws});
   const Place place(a[17], dev);
@@ -453,9 +456,11 @@ PyObject* linear_fwd(PyObject* const* a, Py_ssize_t count) {
           (long long)nseq);
   }
   if (o.given()) check_exact(o, {n.rows, n.Hv, n.V}, at::kBFloat16);
-  check_disjoint(o, {&n.q, &n.k, &n.v, &n.g, &init, &fin});
-  check_disjoint(fin, {&n.q, &n.k, &n.v, &n.g});
   if (ws.given() && !ws.t->is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
+  check_disjoint({&o, &status, &ws, &fin}, {&n.q, &n.k, &n.v, &n.g, &cu, &idx});
+  // the initial state may be the final state's array, but no other part of it
+  const bool in_place = fin.given() && init.given() && fin.ptr() == init.ptr();
+  check_disjoint({&o, &status, &ws, in_place ? &none : &fin}, {&init});
   const auto dev = check_device({&n.q, &n.k, &n.v, &n.g, &cu, &init, &fin, &idx, &status, &o, &ws});
   const Place place(a[12], dev);
   at::Tensor out, final_state, st;
@@ -505,12 +510,8 @@ PyObject* linear_bwd(PyObject* const* a, Py_ssize_t count) {
   if (dv.given()) check_exact(dv, n.v.t->sizes(), at::kBFloat16);
   if (dg.given()) check_exact(dg, {n.rows, n.Hv}, at::kFloat);
   if (ds.given()) check_exact(ds, {nseq, n.Hv, n.K, n.V}, at::kFloat);
-  for (const Arg& out : {dq, dk, dv, dg, ds})
-    check_disjoint(out, {&n.q, &n.k, &n.v, &n.g, &dout, &init});
-  check_disjoint(dk, {&dq});
-  check_disjoint(dv, {&dq, &dk});
-  check_disjoint(dg, {&dq, &dk, &dv});
   if (ws.given() && !ws.t->is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
+  check_disjoint({&dq, &dk, &dv, &dg, &ds, &status, &ws}, {&n.q, &n.k, &n.v, &n.g, &dout, &cu, &init, &idx});
   const auto dev = check_device({&n.q, &n.k, &n.v, &n.g, &dout, &cu, &init, &idx, &status, &dq, &dk, &dv, &dg, &ds, &ws});
   const Place place(a[17], dev);
   at::Tensor oq, ok, ov, og, os;
@@ -543,8 +544,8 @@ PyObject* linear_update(PyObject* const* a, Py_ssize_t count) {
   else if (S < n.rows)
     raise(PyExc_ValueError, "without state_indices row i uses slot i: state needs S >= N=%lld", (long long)n.rows);
   if (o.given()) check_exact(o, n.v.t->sizes(), at::kBFloat16);
-  check_disjoint(o, {&n.q, &n.k, &n.v, &n.g, &state});
   if (status.given()) check_status(status);
+  check_disjoint({&o, &state, &status}, {&n.q, &n.k, &n.v, &n.g, &idx});
   const auto dev = check_device({&n.q, &n.k, &n.v, &n.g, &state, &idx, &o, &status});
   const Place place(a[10], dev);
   at::Tensor out, st;
