@@ -1,13 +1,15 @@
 """qk_norm_rope and decay_attention: the mixer's calls as differentiable PyTorch functions.
 
 Only marshalling lives here, as in the convolution's causal_conv1d: the forward is one
-cattn_*_fwd call, the backward one cattn_*_bwd call.
+cattn_*_fwd call, the backward one cattn_*_bwd call.  The gradients have no gradients of their own:
+a second backward through them (create_graph=True) raises.
 """
 from __future__ import annotations
 
 import torch
 
 from . import attn
+from .autograd import once
 
 
 class _QkNormRope(torch.autograd.Function):
@@ -25,6 +27,7 @@ class _QkNormRope(torch.autograd.Function):
                                                  wk=wk, cos=cos, sin=sin, positions=positions,
                                                  **ctx.kw)
         need = ctx.needs_input_grad
+        dq, dk, dwq, dwk = once("qk_norm_rope", (dq, dk, dwq, dwk), (dyq, dyk, q, k, wq, wk))
         return (dq if need[0] else None, dk if need[1] else None, dwq if need[2] else None,
                 dwk if need[3] else None, None, None, None, None, None, None)
 
@@ -58,6 +61,8 @@ class _DecayAttention(torch.autograd.Function):
         dq, dk, dv, dg, ds = attn.cattn_linear_bwd(q, k, v, g, do.contiguous(), cu_seqlens,
                                                    scale=ctx.scale, initial_state=initial_state,
                                                    want_dinit=want)
+        dq, dk, dv, dg, ds = once("decay_attention", (dq, dk, dv, dg, ds),
+                                  (do, q, k, v, g, initial_state))
         return (dq if need[0] else None, dk if need[1] else None, dv if need[2] else None,
                 dg if need[3] else None, None, ds if want else None, None, None)
 

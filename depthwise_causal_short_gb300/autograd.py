@@ -11,13 +11,39 @@ Layouts: x [B, T, D] bf16 (B = 1 with cu_seqlens, whose rows are the packed sequ
 weight [D, W] fp32 or bf16; bias [D] or None; states [N, D, W-1] bf16 (N = B, or the number
 of sequences), oldest entry first, the decode pool's layout.  The final state is returned
 as a constant (no gradient flows into it); gradients flow to x, weight, bias and
-initial_state.
+initial_state.  They have no gradients of their own: a second backward through them
+(create_graph=True) raises.
 """
 from __future__ import annotations
 
 import torch
 
 from . import binding as cc
+
+
+class _Once(torch.autograd.Function):
+    """Hands `count` gradients on; a backward through them raises."""
+
+    @staticmethod
+    def forward(ctx, name, count, *tensors):
+        ctx.name = name
+        return tuple(t.view_as(t) for t in tensors[:count])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.name}: its gradients have no gradients of their own")
+
+
+def once(name: str, grads: tuple, depends: tuple) -> tuple:
+    """The gradients that a backward returns, for a graph that is kept (create_graph=True):
+    without this they would be constants there, and what is made of them would add zeros to
+    the gradients of `depends`, without a word."""
+    depends = [t for t in depends if t is not None and t.requires_grad]
+    if not depends or not torch.is_grad_enabled():
+        return grads
+    given = [t for t in grads if t is not None]
+    out = iter(_Once.apply(name, len(given), *given, *depends))
+    return tuple(None if t is None else next(out) for t in grads)
 
 
 def _packed_cu(x: torch.Tensor, cu_seqlens: torch.Tensor | None) -> torch.Tensor:
@@ -70,6 +96,7 @@ class _CausalConv1d(torch.autograd.Function):
                 initial_state=initial_state, want_dbias=need_b,
                 want_dinit=initial_state is not None and need_s)
             dx = dx.view(x.shape)
+        dx, dw, db, ds = once("causal_conv1d", (dx, dw, db, ds), (dy, x, weight, bias, initial_state))
         return (dx if need_x else None, dw if need_w else None, db if need_b else None,
                 ds if need_s else None, None, None, None)
 

@@ -163,3 +163,23 @@ def test_a_new_final_state_with_slots_of_a_larger_pool_is_refused():
                                          state_indices=idx)
     assert status.tolist() == [0, 0]
     assert torch.equal(o, want[0]) and torch.equal(fin[[1, 0]], want[1])
+
+
+@pytest.mark.parametrize("constant", [False, True])
+def test_second_derivatives_are_refused(constant):
+    # the gradients' kernels have no gradient of their own: an error, not a penalty of zero (with a
+    # constant gradient of the outputs too: dq still depends on k)
+    q, k, v, g, do, s0 = (t.cuda().requires_grad_() for t in _inputs([20, 7], 1, 2, 32, 32))
+    w = torch.ones(32).cuda().requires_grad_()
+    x, cw = torch.randn(1, 30, 64).bfloat16().cuda().requires_grad_(), torch.rand(64, 4).cuda().requires_grad_()
+    for o, leaves in ((cc.decay_attention(q, k, v, g, _cu([20, 7]), s0)[0], (q, k, v, g, s0)),
+                      (cc.qk_norm_rope(q, k, w, w)[0], (q, w)),
+                      (cc.causal_conv1d(x, cw)[0], (x, cw)),
+                      (cc.causal_conv1d(x, cw, cu_seqlens=_cu([12, 18]))[0], (x, cw))):
+        loss = o.float().sum() if constant else o.float().square().sum()
+        grads = torch.autograd.grad(loss, leaves, create_graph=True)
+        plain_grads = torch.autograd.grad(loss, leaves, retain_graph=True)
+        for a, b in zip(grads, plain_grads):
+            assert torch.equal(a, b) and not b.requires_grad
+            with pytest.raises(RuntimeError, match="no gradients of their own"):
+                (loss + a.float().square().sum()).backward(retain_graph=True)
