@@ -60,7 +60,8 @@ def _inputs(lib: Path) -> list[Path]:
         return [attn_binding(), INCLUDE / "cattn.h", INCLUDE / "cconv.h", Path(__file__)]
     if lib == LIB:
         return sources() + shared
-    return attn_sources() + sorted((CSRC / "attn").glob("*.cuh")) + [INCLUDE / "cattn.h"] + shared
+    headers = sorted((CSRC / "attn").glob("*.cuh")) + sorted((CSRC / "attn").glob("*.h"))
+    return attn_sources() + headers + [INCLUDE / "cattn.h"] + shared
 
 
 def _newer(lib: Path) -> bool:
@@ -135,6 +136,5 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
 
 
 if __name__ == "__main__":
-    import sys
-    print(build(force=True, verbose="-v" in sys.argv,
+        print(build(force=True, verbose="-v" in sys.argv,
                 extra_flags=["-Xptxas", "-v"] if "-v" in sys.argv else None))
