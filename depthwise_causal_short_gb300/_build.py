@@ -13,6 +13,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sys
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -64,8 +65,20 @@ def _inputs(lib: Path) -> list[Path]:
     return attn_sources() + headers + [INCLUDE / "cattn.h"] + shared
 
 
+def _torch_stamp() -> Path:
+    """Names the interpreter and the torch that _cattn.so was built against."""
+    return OBJ_DIR / "attn_py.torch"
+
+
+def _torch_version() -> str:
+    import torch
+    return f"{sys.version} / {torch.__version__} / {Path(torch.__file__).resolve().parent}"
+
+
 def _newer(lib: Path) -> bool:
     if not lib.exists():
+        return False
+    if lib == ATTN_PY and (not _torch_stamp().exists() or _torch_stamp().read_text() != _torch_version()):
         return False
     t = lib.stat().st_mtime
     return all(p.stat().st_mtime <= t for p in _inputs(lib))
@@ -129,12 +142,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     if py_obj is not None:
         import torch
         libs = Path(torch.__file__).resolve().parent / "lib"
+        _torch_stamp().unlink(missing_ok=True)
         link(ATTN_PY, ["g++", "-shared", str(py_obj.result()), f"-L{LIB_DIR}", "-lcattn",
                        "-Wl,-rpath,$ORIGIN", f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10",
                        "-lc10_cuda"])
+        _torch_stamp().write_text(_torch_version())
     return LIB
 
 
 if __name__ == "__main__":
-        print(build(force=True, verbose="-v" in sys.argv,
+    import sys
+    print(build(force=True, verbose="-v" in sys.argv,
                 extra_flags=["-Xptxas", "-v"] if "-v" in sys.argv else None))

@@ -45,3 +45,10 @@ def test_a_newer_header_makes_its_library_stale():
     finally:
         os.utime(header, ns=(old.st_atime_ns, old.st_mtime_ns))
     assert _build.up_to_date()
+
+
+def test_the_binding_is_stale_for_another_torch(monkeypatch):
+    import torch
+    assert _build._newer(_build.ATTN_PY)
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    assert not _build._newer(_build.ATTN_PY) and _build._newer(_build.ATTN_LIB)
