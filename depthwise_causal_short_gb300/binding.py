@@ -275,6 +275,24 @@ def _stream(stream, dev: torch.device) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
+def _new(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
+    """A tensor that the call makes: from the memory of the stream that it runs on.  From the
+    current stream's, a workspace, which is freed when the call returns, could be handed out and
+    written while the kernels on another stream still use it.  Results are held for the current
+    stream when the caller frees them."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    handle = _stream(stream, dev).value or 0
+    own = torch.cuda.default_stream(dev) if handle in (0, 1) else \
+        torch.cuda.ExternalStream(handle, device=dev)  # (1: the legacy default stream by name)
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(own):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if own.cuda_stream != here.cuda_stream:
+        t.record_stream(here)
+    return t
+
+
 def _run(dev: torch.device, fn, *args):
     """fn(*args) with `dev` current (the library launches on the current device)."""
     if dev.index == torch.cuda.current_device():
@@ -299,7 +317,7 @@ def cconv_fwd(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None
         _disjoint((("y", y),), (("x", x),))
     dev = _device(("x", "w", "bias", "y"), (x, w, bias, y))
     if y is None:
-        y = torch.empty((B, T, D), dtype=torch.bfloat16, device=dev)
+        y = _new((B, T, D), torch.bfloat16, dev, stream)
     rc = _run(dev, load().cconv_fwd, _ptr(x), B, T, D, x.stride(0), x.stride(1), _ptr(w),
               _ptr(bias), _wdt(w), W, _ptr(y), _stream(stream, dev))
     _check(rc, "cconv_fwd")
@@ -349,14 +367,13 @@ def cconv_bwd(x: torch.Tensor, dy: torch.Tensor, w: torch.Tensor,
     dev = _device(("x", "dy", "w", "bias", "dx", "dw", "dbias", "workspace"),
                   (x, dy, w, bias, dx, dw, dbias if want_dbias else None, workspace))
     if dx is None:
-        dx = torch.empty((B, T, D), dtype=torch.bfloat16, device=dev)
+        dx = _new((B, T, D), torch.bfloat16, dev, stream)
     if dw is None:
-        dw = torch.empty((D, W), dtype=w.dtype, device=dev)
+        dw = _new((D, W), w.dtype, dev, stream)
     if want_dbias and dbias is None:
-        dbias = torch.empty((D,), dtype=w.dtype, device=dev)
+        dbias = _new((D,), w.dtype, dev, stream)
     if workspace is None:
-        workspace = torch.empty(cconv_bwd_workspace_bytes(B, T, D, W, dev), dtype=torch.uint8,
-                                device=dev)
+        workspace = _new(cconv_bwd_workspace_bytes(B, T, D, W, dev), torch.uint8, dev, stream)
     rc = _run(dev, load().cconv_bwd, _ptr(x), x.stride(0), x.stride(1), _ptr(dy), dy.stride(0),
               dy.stride(1), B, T, D, _ptr(w), _ptr(bias), _wdt(w), W, _ptr(dx), _ptr(dw),
               _ptr(dbias if want_dbias else None), _ptr(workspace),
@@ -416,9 +433,9 @@ def cconv_update(x: torch.Tensor, state: torch.Tensor, w: torch.Tensor,
     dev = _device(("x", "state", "w", "bias", "state_indices", "y", "status"),
                   (x, state, w, bias, state_indices, y, status))
     if y is None:
-        y = torch.empty((N, D), dtype=torch.bfloat16, device=dev)
+        y = _new((N, D), torch.bfloat16, dev, stream)
     if status is None:
-        status = torch.empty(2, dtype=torch.int32, device=dev)
+        status = _new(2, torch.int32, dev, stream)
     rc = _run(dev, load().cconv_update, _ptr(x), N, D, x.stride(0), _ptr(state), S,
               _ptr(state_indices), _ptr(w), _ptr(bias), _wdt(w), W, _ptr(y), _ptr(status),
               _stream(stream, dev))
@@ -490,11 +507,11 @@ def cconv_fwd_varlen(x: torch.Tensor, cu_seqlens: torch.Tensor, w: torch.Tensor,
                   (x, cu_seqlens, w, bias, initial_state, final_state, state_indices,
                    status if state_indices is not None else None, y))
     if want_final:
-        final_state = torch.empty((nseq, D, L), dtype=torch.bfloat16, device=dev)
+        final_state = _new((nseq, D, L), torch.bfloat16, dev, stream)
     if state_indices is not None and status is None:
-        status = torch.empty(2, dtype=torch.int32, device=dev)
+        status = _new(2, torch.int32, dev, stream)
     if y is None:
-        y = torch.empty((total, D), dtype=torch.bfloat16, device=dev)
+        y = _new((total, D), torch.bfloat16, dev, stream)
     rc = _run(dev, load().cconv_fwd_varlen, _ptr(x), total, D, x.stride(0), _ptr(cu_seqlens),
               nseq, _ptr(w), _ptr(bias), _wdt(w), W, act, _ptr(initial_state), _ptr(final_state),
               _ptr(state_indices), S, _ptr(status if state_indices is not None else None),
@@ -568,16 +585,16 @@ def cconv_bwd_varlen(x: torch.Tensor, dy: torch.Tensor, cu_seqlens: torch.Tensor
                    dbias if want_dbias else None, d_initial_state if want_dinit else None,
                    workspace))
     if dx is None:
-        dx = torch.empty((total, D), dtype=torch.bfloat16, device=dev)
+        dx = _new((total, D), torch.bfloat16, dev, stream)
     if dw is None:
-        dw = torch.empty((D, W), dtype=w.dtype, device=dev)
+        dw = _new((D, W), w.dtype, dev, stream)
     if want_dbias and dbias is None:
-        dbias = torch.empty((D,), dtype=w.dtype, device=dev)
+        dbias = _new((D,), w.dtype, dev, stream)
     if want_dinit and d_initial_state is None:
-        d_initial_state = torch.empty((nseq, D, L), dtype=torch.bfloat16, device=dev)
+        d_initial_state = _new((nseq, D, L), torch.bfloat16, dev, stream)
     if workspace is None:
-        workspace = torch.empty(max(cconv_bwd_varlen_workspace_bytes(total, D, W, dev), 16),
-                                dtype=torch.uint8, device=dev)
+        workspace = _new(max(cconv_bwd_varlen_workspace_bytes(total, D, W, dev), 16), torch.uint8,
+                         dev, stream)
     rc = _run(dev, load().cconv_bwd_varlen,
               _ptr(x), x.stride(0), _ptr(dy), dy.stride(0), total, D, _ptr(cu_seqlens), nseq,
               _ptr(w), _ptr(bias), _wdt(w), W, act, _ptr(initial_state), _ptr(state_indices), S,
@@ -616,9 +633,9 @@ def cconv_update_ex(x: torch.Tensor, state: torch.Tensor, w: torch.Tensor,
     dev = _device(("x", "state", "w", "bias", "state_indices", "cache_seqlens", "y", "status"),
                   (x, state, w, bias, state_indices, cache_seqlens, y, status))
     if y is None:
-        y = torch.empty((N, D), dtype=torch.bfloat16, device=dev)
+        y = _new((N, D), torch.bfloat16, dev, stream)
     if status is None:
-        status = torch.empty(2, dtype=torch.int32, device=dev)
+        status = _new(2, torch.int32, dev, stream)
     rc = _run(dev, load().cconv_update_ex, _ptr(x), N, D, x.stride(0), _ptr(state), S, L,
               _ptr(state_indices), int(bool(pad_rows)), _ptr(cache_seqlens), _ptr(w), _ptr(bias),
               _wdt(w), W, act, _ptr(y), _ptr(status), _stream(stream, dev))
@@ -690,7 +707,7 @@ def cconv_fwd_multi(xs, ws, biases=None, *, ys=None, stream=None):
                   [(f"x[{k}]", t) for k, t in enumerate(xs)])
     dev = _device(*reversed(_listed(("x", xs), ("w", ws), ("bias", biases), ("ys", ys or []))))
     if ys is None:
-        ys = [torch.empty(x.shape, dtype=torch.bfloat16, device=dev) for x in xs]
+        ys = [_new(x.shape, torch.bfloat16, dev, stream) for x in xs]
     rc = _run(dev, load().cconv_fwd_multi, n, _parr(xs), _iarr(Ds),
               _iarr([x.stride(0) for x in xs]), _iarr([x.stride(1) for x in xs]), _parr(ws),
               _parr(biases), _parr(ys), B, T, _wdt(ws[0]), W, _stream(stream, dev))
@@ -738,14 +755,14 @@ def cconv_bwd_multi(xs, dys, ws, biases=None, *, want_dbias: bool | None = None,
                                     ("dbiases", (dbiases or []) if want_dbias else []),
                                     ("workspace", [workspace]))))
     if dxs is None:
-        dxs = [torch.empty(x.shape, dtype=torch.bfloat16, device=dev) for x in xs]
+        dxs = [_new(x.shape, torch.bfloat16, dev, stream) for x in xs]
     if dws is None:
-        dws = [torch.empty((D, W), dtype=wdtype, device=dev) for D in Ds]
+        dws = [_new((D, W), wdtype, dev, stream) for D in Ds]
     if want_dbias and dbiases is None:
-        dbiases = [torch.empty((D,), dtype=wdtype, device=dev) for D in Ds]
+        dbiases = [_new((D,), wdtype, dev, stream) for D in Ds]
     if workspace is None:
-        workspace = torch.empty(cconv_bwd_multi_workspace_bytes(Ds, B, T, W, dev),
-                                dtype=torch.uint8, device=dev)
+        workspace = _new(cconv_bwd_multi_workspace_bytes(Ds, B, T, W, dev), torch.uint8, dev,
+                         stream)
     rc = _run(dev, load().cconv_bwd_multi,
               n, _parr(xs), _iarr([x.stride(0) for x in xs]), _iarr([x.stride(1) for x in xs]),
               _parr(dys), _iarr([d.stride(0) for d in dys]), _iarr([d.stride(1) for d in dys]),
