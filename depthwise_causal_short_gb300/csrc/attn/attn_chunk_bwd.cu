@@ -99,14 +99,11 @@ struct BwdArgs {
 #define CATTN_WAIT(bar, parity) (wait_phase((bar), static_cast<uint32_t>(parity) & 1u))
 #define CATTN_WARP_WAIT(bar, parity) (__all_sync(0xffffffffu, CATTN_WAIT(bar, parity)))
 
-// Dot of 32 fp32 values with columns [c, c + 32) of row `row` of a bf16 tile, those below `width` only:
-// the products write 16 columns at a time, and what tensor memory holds past them may be NaN, which the
-// tile's zeros there would not take out.
-__device__ __forceinline__ f2 dot_tile(uint32_t tile, int row, int c, int width, const uint32_t* x, f2 dot) {
+// Dot of 32 fp32 values with columns [c, c + 32) of row `row` of a bf16 tile.
+__device__ __forceinline__ f2 dot_tile(uint32_t tile, int row, int c, const uint32_t* x, f2 dot) {
   const uint32_t at = tile + (c >> 6) * kPanelBytes;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (c + 8 * i >= width) break;
     const uint4 w = lds128_at(at + swizzled(row, ((c >> 3) & 7) + i));
     dot = f2_fma(bf16x2_to_f2(w.x), pair(x, 4 * i), dot);
     dot = f2_fma(bf16x2_to_f2(w.y), pair(x, 4 * i + 1), dot);
@@ -381,7 +378,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (elect_one()) {
       int use = 0, pubs = 0, ins = 0, fixes = 0, kvs = 0;
       const int kk = (p.K + 15) / 16, nk = kk * 16;
-      const uint32_t ds = mma_desc(128, false, false), dst = mma_desc(nk, false, false);
+      // The rows' dots take the state's product 32 columns at a time: all of these are written (past K
+      // with the zeros of the state's rows there), as what an earlier kernel left in tensor memory may
+      // be NaN, which the zeros of q or k would not take out.
+      const uint32_t ds = mma_desc(128, false, false), dst = mma_desc((p.K + 31) / 32 * 32, false, false);
       const uint32_t dk = mma_desc(nk, false, true);
       const uint64_t tv = tile_desc(av, 0), to = tile_desc(ao, 0), tk = tile_desc(ak, 0);
       const uint64_t tq = tile_desc(aq, 0), tS = tile_desc(smem + kOffS, 0);
@@ -855,7 +855,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tmem_ld32(tmem + lanes + 256 + c, x);
             tmem_wait_ld();
             tmem_use32(x);
-            dot = dot_tile(KV ? ak : aq, row, c, p.K, x, dot);
+            dot = dot_tile(KV ? ak : aq, row, c, x, dot);
             scale32(x, rowf);
             tmem_st16(tmem + lanes + 256 + c, x);
             tmem_st16(tmem + lanes + 256 + c + 16, x + 16);
@@ -875,8 +875,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               p.scale * rowf * (d0 + d1);
         if (!(ok = CATTN_WARP_WAIT(ofull, use))) break;
         // The last chunk's outputs may still be on their way out of the staging buffer: `ofree` does
-        // not wait for them, and only a chunk with a state is held back by the state's warps.
-        if (!(ok = __all_sync(0xffffffffu, wait_count(stored, use)))) break;
+        // not wait for them, and only a chunk with a state is held back by the state's warps.  (In a
+        // cluster they have left before `ofree`.)
+        if (group == 1 && !(ok = __all_sync(0xffffffffu, wait_count(stored, use)))) break;
         tc_fence_after();
         const bool whole = n == kChunk, live = row < n;
         const int hk = hv / p.ratio;
