@@ -183,3 +183,27 @@ def test_second_derivatives_are_refused(constant):
             assert torch.equal(a, b) and not b.requires_grad
             with pytest.raises(RuntimeError, match="no gradients of their own"):
                 (loss + a.float().square().sum()).backward(retain_graph=True)
+
+
+@pytest.mark.parametrize("Hk,Hv", [(1, 1), (1, 2), (1, 3)])
+@pytest.mark.parametrize("K,V", [(8, 8), (40, 40), (72, 136), (104, 200), (64, 24), (24, 256)])
+def test_results_do_not_depend_on_what_ran_before(K, V, Hk, Hv):
+    # calls on NaN leave NaN in shared and tensor memory of every SM
+    n = 128 * 300
+    g = torch.zeros(n, 1).cuda()
+    lens = [200, 0, 129, 1, 384]
+    q, k, v, gates, do, s0 = (t.cuda() for t in _inputs(lens, Hk, Hv, K, V, seed=K))
+
+    def after(value):
+        x = torch.full((n, 1, 128), value, dtype=torch.bfloat16).cuda()
+        out = []
+        for states in (None, s0):
+            cc.cattn_linear_fwd(x, x, x, g, _cu([n]))
+            out += cc.cattn_linear_fwd(q, k, v, gates, _cu(lens), initial_state=states, final_state=True)[:2]
+            cc.cattn_linear_bwd(x, x, x, g, x, _cu([n]))
+            out += [t for t in cc.cattn_linear_bwd(q, k, v, gates, do, _cu(lens), initial_state=states)
+                    if t is not None]
+        return out
+
+    for a, b in zip(after(float("nan")), after(0.0)):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
