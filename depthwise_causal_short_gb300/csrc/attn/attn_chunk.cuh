@@ -399,11 +399,15 @@ __device__ __forceinline__ void gather_state(f2* S, const float* carry, const fl
   }
 }
 
-// Calls of at most 64 rows keep P in two bf16 terms (FINE kernels): their products are few, and over
-// a few tokens the rounding of single scores does not average out (up to 1.75 times the error of the
-// bf16 store; with more tokens it is 1.4 times that whatever the inputs are).  64 tokens take 7.7 us
-// with two terms and with one.  Decided chunk by chunk, the larger calls paid for it: 112 us against
-// 110 for 16384 rows, 416 against 384 for their gradient.  Columns of TMEM: block b's first terms at
+// Calls of at most 64 rows keep P in two bf16 terms (FINE kernels).  Over a few tokens the rounding of
+// single scores does not average out (up to 1.75 times the error of the bf16 store; with more tokens it
+// is 1.4 times that whatever the inputs are).  What that turns on is the length of each sequence, which
+// the host does not know: 64 rows is the largest call that is sure to have no longer chunk, and for
+// longer ones the dk, dv sweep has no room (D's product takes columns 64 to 127 of each score tile).
+// So a short sequence in a call of more than 64 rows has its scores in one term, like the long ones
+// beside it.  64 tokens take 7.7 us with two terms and with one; decided chunk by chunk, the larger
+// calls paid for it: 112 us against 110 for 16384 rows, 416 against 384 for their gradient.  (The state
+// that the forward's Q S reads has one term in every call.)  Columns of TMEM: block b's first terms at
 // 32 b and its second ones 16 on, over scores that are read; with one term at 16 b.
 constexpr int kFineTokens = 64;
 

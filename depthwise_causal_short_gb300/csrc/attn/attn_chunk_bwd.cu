@@ -36,7 +36,8 @@
 // loads add as much again.  Bound by the chain of the roles, 17000 (dq) and 20000 cycles a chunk, as
 // there is no room for a second slot a tile or, in TMEM, for D's product beside the scores (tensor
 // cores active 23 % of the time, load / store unit 31 to 37 %, DRAM 23 %).  16384 rows in 2
-// sequences, 16 value heads on 8 key heads of 128: 133 and 172 us of the backward's 383.
+// sequences, 16 value heads on 8 key heads of 128: 135 and 171 us of the backward's 385.  The
+// compiler spills some 150 (dq) to 190 bytes a thread of the roles that share these kernels.
 #include "attn_chunk.cuh"
 #include "attn_chunk_host.h"
 
@@ -917,8 +918,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
           }
         }
-        // the state may have its buffer back: in a cluster before the ring is written (166 us of
-        // the sweep of 16384 rows; after it 170)
+        // the state may have its buffer back: in a cluster before the ring is written (2 % of the
+        // sweep of 16384 rows against after it)
         auto leave = [&]() {
           if (row != 0) return;
           stores_wait_read();

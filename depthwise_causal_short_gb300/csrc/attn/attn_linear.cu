@@ -240,9 +240,9 @@ static int chunk_grid(int64_t total, int64_t nseq, int64_t Hv, int64_t V, int* g
 
 // CTAs of the backward, and how many share a range: the members of a key head (its value heads
 // and their column tiles) as a cluster, where these are even and at most 8.  Measured on 16384 rows
-// with heads of 128, clusters against sums through memory, us: 2 members 380 / 448, 4 members
-// 379 / 445 (V of 256: 392 / 467), 6 members 330 / 346, 8 members 416 / 446, but 3 members 401 / 348,
-// 5 335 / 298, 7 443 / 396: a share of an odd number of 8-column pieces is half as fast to add up and
+// with heads of 128, clusters against sums through memory, us: 2 members 381 / 447, 4 members
+// 379 / 443 (V of 256: 395 / 470), 6 members 332 / 350, 8 members 416 / 449, but 3 members 398 / 350,
+// 5 353 / 300, 7 448 / 396: a share of an odd number of 8-column pieces is half as fast to add up and
 // to store, and all members wait for the slowest.
 static int bwd_grid(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv, int64_t V, int* grid,
                     int* group) {

@@ -32,6 +32,12 @@
  *     in device memory, cu[0] = 0, non-decreasing, cu[nseq] = total; empty sequences are
  *     allowed.  The host never reads it.  An ill-formed vector gives unspecified results,
  *     every access stays inside the buffers, and cattn_device_fault() reports bit 4.
+ *   - A workspace is the call's until its work on `stream` is done.
+ *   - Precision: sums, norms, gates and states are fp32.  Rounded to bf16 are the results, once,
+ *     and inside the linear attention's matrix products the decayed scores (in calls of at most
+ *     64 rows they keep 16 bits) and, in the forward, the states as the queries read them: errors
+ *     of 2.3e-3 in the 2-norm, of which the store alone makes 1.7e-3.  States, their gradients and
+ *     dg are as exact as sums in fp32.
  *   - Results are bit-identical from run to run for the same inputs and device.
  */
 #ifndef CATTN_H
