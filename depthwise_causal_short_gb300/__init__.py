@@ -9,7 +9,13 @@ libraries; the first call does, and raises if they have not been built.
 """
 from .attn import (  # noqa: F401
     attn_describe,
+    cattn_delta_fwd,
+    cattn_delta_fwd_workspace_bytes,
+    cattn_delta_update,
     cattn_device_fault,
+    cattn_layernorm_bwd,
+    cattn_layernorm_bwd_workspace_bytes,
+    cattn_layernorm_fwd,
     cattn_linear_bwd,
     cattn_linear_bwd_workspace_bytes,
     cattn_linear_fwd,

@@ -32,12 +32,14 @@ _SZ = ctypes.c_size_t
 
 CATTN_NORM_RMS = 0
 CATTN_NORM_L2 = 1
+CATTN_NORM_LAYER = 2
 
 _lib = None
 _ext = None
 
 _QK = [_P, _I64, _I64, _P, _I64, _I64]
 _QKVG = _QK + [_P, _I64, _I64, _P, _I64, _I64]
+_QKVGB = _QKVG + [_P, _I64, _I64]
 _SIGNATURES = {
     "cattn_qknorm_fwd": _QK + [_I64] * 4 + [_P, _P, _INT, _INT, _F32, _P, _P, _I64, _I64, _INT, _P,
                                              _P, _P, _P],
@@ -50,6 +52,13 @@ _SIGNATURES = {
     "cattn_linear_bwd": _QKVG + [_P, _I64, _I64] + [_I64] * 5 + [_P, _I64, _F32, _P, _P, _I64, _P, _P,
                                                                  _P, _P, _P, _P, _P, _SZ, _P],
     "cattn_linear_update": _QKVG + [_I64] * 5 + [_F32, _P, _I64, _P, _INT, _P, _P, _P],
+    "cattn_delta_fwd_workspace_bytes": [_I64] * 6 + [ctypes.POINTER(_SZ)],
+    "cattn_delta_fwd": _QKVGB + [_I64] * 5 + [_P, _I64, _F32, _P, _P, _P, _I64, _P, _P, _P, _SZ, _P],
+    "cattn_delta_update": _QKVGB + [_I64] * 5 + [_F32, _P, _I64, _P, _INT, _P, _P, _P],
+    "cattn_layernorm_fwd": [_P, _I64, _I64] * 2 + [_I64] * 3 + [_P, _P, _INT, _INT, _F32, _P, _P],
+    "cattn_layernorm_bwd_workspace_bytes": [_I64] * 3 + [ctypes.POINTER(_SZ)],
+    "cattn_layernorm_bwd": [_P, _I64, _I64] * 3 + [_I64] * 3 + [_P, _P, _INT, _INT, _F32, _P, _P, _P, _P,
+                                                                _P, _SZ, _P],
     "cattn_describe_begin": [],
     "cattn_describe_end": [ctypes.POINTER(KernelDesc), _INT, ctypes.POINTER(_INT)],
     "cattn_device_fault": [ctypes.POINTER(ctypes.c_int32)],
@@ -199,6 +208,72 @@ def cattn_linear_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: to
     bf16; g [N, Hv] fp32.  pad_rows: index -1 marks a padding row (no state access, o row not
     written).  Returns (o [N, Hv, V], status int32[2] on the device)."""
     return _calls().linear_update(q, k, v, g, scale, state, state_indices, pad_rows, o, status, stream)
+
+
+# ---------------------------------------------------------------------------------------
+# the gated delta rule
+# ---------------------------------------------------------------------------------------
+
+def cattn_delta_fwd_workspace_bytes(total: int, nseq: int, Hk: int, Hv: int, K: int, V: int,
+                                    device=None) -> int:
+    """Workspace cattn_delta_fwd needs on `device` (default: the current CUDA device)."""
+    return _bytes("cattn_delta_fwd_workspace_bytes", device, total, nseq, Hk, Hv, K, V)
+
+
+def cattn_delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                    beta: torch.Tensor, cu_seqlens: torch.Tensor, *, scale: float | None = None,
+                    initial_state: torch.Tensor | None = None,
+                    final_state: torch.Tensor | bool | None = None,
+                    state_indices: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                    o: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                    stream=None):
+    """The gated delta rule over packed sequences: S_t = exp(g_t) S_{t-1} + k_t u_t^T with u_t =
+    beta_t (v_t - (exp(g_t) S_{t-1})^T k_t), o_t = scale q_t^T S_t.  beta [total, Hv] fp32 (any
+    strides); everything else as in cattn_linear_fwd.  Returns (o, final_state or None, status or
+    None)."""
+    return _calls().delta_fwd(q, k, v, g, scale, cu_seqlens, initial_state, final_state, state_indices,
+                              status, o, workspace, stream, beta)
+
+
+def cattn_delta_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                       beta: torch.Tensor, state: torch.Tensor,
+                       state_indices: torch.Tensor | None = None, *, scale: float | None = None,
+                       pad_rows: bool = False, o: torch.Tensor | None = None,
+                       status: torch.Tensor | None = None, stream=None):
+    """One token of the gated delta rule for each of N sequences, on the pool state fp32 [S, Hv, K,
+    V]; beta [N, Hv] fp32, everything else as in cattn_linear_update.  Returns (o [N, Hv, V], status
+    int32[2] on the device)."""
+    return _calls().delta_update(q, k, v, g, scale, state, state_indices, pad_rows, o, status, stream, beta)
+
+
+# ---------------------------------------------------------------------------------------
+# layer norm, with the gate of a mixer's outputs
+# ---------------------------------------------------------------------------------------
+
+def cattn_layernorm_fwd(x: torch.Tensor, w: torch.Tensor | None = None,
+                        b: torch.Tensor | None = None, *, gate: torch.Tensor | None = None,
+                        mode: str = "layer", eps: float = 1e-6, y: torch.Tensor | None = None,
+                        stream=None):
+    """Layer norm of x [total, C] or of each head of x [total, H, C] (bf16), or with mode "rms" the
+    norm by the root mean square: (x - mean) / sqrt(var + eps) * w + b, times silu(gate) where a
+    gate of x's shape is given.  w and b [C] fp32 or bf16.  Returns y."""
+    return _calls().layernorm_fwd(x, w, b, gate, mode, eps, y, stream)
+
+
+def cattn_layernorm_bwd_workspace_bytes(total: int, H: int, C: int, device=None) -> int:
+    """Workspace cattn_layernorm_bwd needs on `device` (default: the current CUDA device)."""
+    return _bytes("cattn_layernorm_bwd_workspace_bytes", device, total, H, C)
+
+
+def cattn_layernorm_bwd(x: torch.Tensor, dy: torch.Tensor, w: torch.Tensor | None = None,
+                        b: torch.Tensor | None = None, *, gate: torch.Tensor | None = None,
+                        mode: str = "layer", eps: float = 1e-6, dx: torch.Tensor | None = None,
+                        dw: torch.Tensor | None = None, db: torch.Tensor | None = None,
+                        dgate: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        stream=None):
+    """Gradient of cattn_layernorm_fwd: (dx, dw or None, db or None, dgate or None), those of the
+    tensors that are given."""
+    return _calls().layernorm_bwd(x, w, b, gate, mode, eps, dy, dx, dw, db, dgate, workspace, stream)
 
 
 def cattn_device_fault() -> int:

@@ -1,0 +1,74 @@
+// attn_delta.cu -- the gated delta rule over packed sequences: the entry points.
+#include "attn_delta.cuh"
+
+namespace cattn {
+
+constexpr int64_t kInKernelChecks = 32;  // state indices that the chain's CTAs check themselves
+constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
+
+static size_t record_bytes(int64_t total, int64_t nseq, int64_t Hv) {
+  return total > 0 ? static_cast<size_t>(delta_slots(total, nseq) * Hv) * kRecordBytes : 0;
+}
+static uint8_t* align256(void* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 255) & ~static_cast<uintptr_t>(255));
+}
+static bool grids_fit(int64_t total, int64_t nseq, int64_t Hv, int64_t V) {
+  return nseq * Hv * ((V + kColumns - 1) / kColumns) <= kMaxGrid && delta_slots(total, nseq) * Hv <= kMaxGrid;
+}
+static Rows rows(const void* p, int64_t st, int64_t sh) {
+  return Rows{static_cast<const uint16_t*>(p), st, sh};
+}
+
+}  // namespace cattn
+
+extern "C" CCONV_API int cattn_delta_fwd_workspace_bytes(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv,
+                                                         int64_t K, int64_t V, size_t* bytes) {
+  using namespace cattn;
+  if (!bytes) return CCONV_ERR_NULL;
+  const int rc = check_sizes(total, nseq, Hk, Hv, K, V);
+  if (rc != CCONV_OK) return rc;
+  if (!grids_fit(total, nseq, Hv, V)) return CCONV_ERR_SHAPE;
+  *bytes = record_bytes(total, nseq, Hv) + 256;
+  return CCONV_OK;
+}
+
+extern "C" CCONV_API int cattn_delta_fwd(
+    const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt, int64_t skh, const void* v,
+    int64_t svt, int64_t svh, const float* g, int64_t sgt, int64_t sgh, const float* beta, int64_t sbt,
+    int64_t sbh, int64_t total, int64_t Hk, int64_t Hv, int64_t K, int64_t V, const int32_t* cu_seqlens,
+    int64_t nseq, float scale, const float* initial_state, float* final_state,
+    const int32_t* state_indices, int64_t S, int32_t* status_dev, void* o, void* workspace,
+    size_t workspace_bytes, cconv_stream_t stream) {
+  using namespace cattn;
+  int rc = check_linear(q, sqt, sqh, k, skt, skh, v, svt, svh, g, sgt, sgh, total, Hk, Hv, K, V, o);
+  if (rc == CCONV_OK && total > 0) rc = check_gates(beta, total, Hv, sbt, sbh);
+  if (rc == CCONV_OK)
+    rc = check_states(cu_seqlens, nseq, Hv, initial_state, final_state, state_indices, S, status_dev);
+  if (rc != CCONV_OK) return rc;
+  if (!grids_fit(total, nseq, Hv, V)) return CCONV_ERR_SHAPE;
+  if (!workspace || workspace_bytes < record_bytes(total, nseq, Hv) + 256) return CCONV_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return CCONV_ERR_ALIGN;
+  const bool checked = state_indices && nseq > kInKernelChecks;
+  if (checked) {
+    rc = launch_checks(state_indices, nseq, S, 0, status_dev, nullptr, 0, 0, nullptr, stream);
+    if (rc != CCONV_OK) return rc;
+  }
+  DeltaCall c{};
+  c.q = rows(q, sqt, sqh), c.k = rows(k, skt, skh), c.v = rows(v, svt, svh);
+  c.g = Gates{g, sgt, sgh}, c.beta = Gates{beta, sbt, sbh};
+  c.s = LinearShape{static_cast<int>(total), static_cast<int>(Hk), static_cast<int>(Hv),
+                    static_cast<int>(K), static_cast<int>(V), static_cast<int>(nseq)};
+  c.cu = cu_seqlens;
+  c.slots = Slots{state_indices, S};
+  c.checked = checked;
+  c.status = status_dev;
+  c.scale = scale;
+  c.initial = initial_state, c.fin = final_state;
+  c.o = static_cast<uint16_t*>(o);
+  c.records = align256(workspace);
+  if (total > 0) {
+    rc = launch_delta_prep(c, stream);
+    if (rc != CCONV_OK) return rc;
+  }
+  return launch_delta_fwd(c, stream);
+}

@@ -1,0 +1,483 @@
+// attn_layernorm.cu -- layer norm of rows or heads (or their norm by the root mean square), with weight,
+// bias and the gate silu(z), and its gradient with the sums for weight and bias.
+//
+//   n = (x - m) r,  m = mean(x) (layer) or 0 (rms),  r = (mean((x - m)^2) + eps)^-1/2
+//   y = (n w + b) silu(z)
+//   du = dy silu(z),  dz = dy (n w + b) silu'(z),  dn = du w
+//   dx = r (dn - n mean(dn n) - mean(dn)),  dw = sum of du n,  db = sum of du     (rms: no mean(dn))
+//
+// Bound by memory: every tensor is read or written once, and the gradient makes the statistics again
+// from x, which it reads anyway.  A group of GROUP threads owns a row, 8 channels (16 bytes) of each
+// of PIECES pieces a thread; the next row's loads are issued before this row's sums.  The squares are
+// summed after the mean is known (as sum(x^2) - C m^2 they would cancel for rows far from zero).
+// The sums over rows stay in registers for all rows of a thread, meet in the CTA, and then, a row of
+// the workspace for each CTA, in a second kernel; in the same order in every run.
+#include "attn_chunk.cuh"
+
+namespace cattn {
+
+struct LnArgs {
+  const uint16_t *x, *z, *dy;
+  int64_t sxt, sxh, szt, szh, syt, syh;
+  const void *w, *b;
+  uint16_t *y, *dz;  // y, or dx
+  float* part;       // [CTAs][2][C], or NULL
+  int64_t rows;
+  int H, C, wdt, layer;
+  float inv, eps;
+};
+
+constexpr int kLnThreads = 256;
+constexpr int kMaxNorm = 8192;
+constexpr int ln_threads(int group) { return group > kLnThreads ? group : group > 32 ? group : kLnThreads; }
+constexpr int kLnCtas = 8;  // CTAs of 256 threads an SM
+
+using cconv::f2_unpack;
+
+__device__ __forceinline__ void widen(const uint4& raw, float* x) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f2_unpack(bf16x2_to_f2(w[i]), x[2 * i], x[2 * i + 1]);
+}
+__device__ __forceinline__ uint4 narrow(const float* x) {
+  return make_uint4(f2_to_bf16x2(f2_pack(x[0], x[1])), f2_to_bf16x2(f2_pack(x[2], x[3])),
+                    f2_to_bf16x2(f2_pack(x[4], x[5])), f2_to_bf16x2(f2_pack(x[6], x[7])));
+}
+// Eight weights from channel c on.
+__device__ __forceinline__ void load_weights(const void* w, int wdt, int c, float rest, bool on, float* x) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = rest;
+  if (!w || !on) return;
+  if (wdt == CCONV_F32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __ldg(static_cast<const float*>(w) + c + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = cconv::bf16_to_f32(__ldg(static_cast<const unsigned short*>(w) + c + i));
+  }
+}
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + exp2_fast(-kLog2e * z)); }
+
+// The sums of a and b over the row's group.  Across warps by shared memory, in turn through two
+// buffers: whoever writes the one again has passed the barrier after the other's reads.
+template <int GROUP>
+__device__ __forceinline__ void group_sum(float& a, float& b, float2 (*buf)[32], int& turn) {
+#pragma unroll
+  for (int o = (GROUP < 32 ? GROUP : 32) / 2; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if constexpr (GROUP > 32) {
+    float2* at = buf[turn];
+    turn ^= 1;
+    if (threadIdx.x % 32 == 0) at[threadIdx.x / 32] = make_float2(a, b);
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int i = 0; i < GROUP / 32; ++i) {
+      a += at[i].x;
+      b += at[i].y;
+    }
+  }
+}
+
+// Row (t, h) and the step to this group's next one.
+struct RowWalk {
+  int64_t r, step, t, dt;
+  int h, dh, H;
+  __device__ __forceinline__ RowWalk(int64_t first, int64_t by, int heads)
+      : r(first), step(by), t(first / heads), dt(by / heads), h(static_cast<int>(first % heads)),
+        dh(static_cast<int>(by % heads)), H(heads) {}
+  __device__ __forceinline__ void next() {
+    r += step;
+    t += dt;
+    h += dh;
+    if (h >= H) h -= H, ++t;
+  }
+};
+
+// Statistics of a row of x: x becomes n; returns r (0 for a row that is not there, whatever eps is).
+template <int GROUP, int PIECES>
+__device__ __forceinline__ float normalise(float (&x)[PIECES][8], const bool (&on)[PIECES], bool live, const LnArgs& p,
+                                           float2 (*buf)[32], int& turn) {
+  float m = 0.f, unused = 0.f;
+  if (p.layer) {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m += x[i][j];
+    group_sum<GROUP>(m, unused, buf, turn);
+    m *= p.inv;
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[i][j] = on[i] ? x[i][j] - m : 0.f;
+      s = fmaf(x[i][j], x[i][j], s);
+    }
+  group_sum<GROUP>(s, unused, buf, turn);
+  const float r = live ? rsqrtf(fmaf(s, p.inv, p.eps)) : 0.f;
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[i][j] *= r;
+  return r;
+}
+
+template <int GROUP, int PIECES, bool GATE>
+__global__ void __launch_bounds__(ln_threads(GROUP)) cattn_layernorm_fwd_kernel(const LnArgs p) {
+  cconv::grid_dependency_wait();
+  cconv::grid_launch_dependents();
+  __shared__ float2 buf[2][32];
+  int turn = 0;
+  constexpr int kRows = ln_threads(GROUP) / GROUP;
+  const int lane = threadIdx.x % GROUP;
+  bool on[PIECES];
+  float w[PIECES][8], b[PIECES][8];
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int c = (lane + i * GROUP) * 8;
+    on[i] = c < p.C;
+    load_weights(p.w, p.wdt, c, 1.f, on[i], w[i]);
+    load_weights(p.b, p.wdt, c, 0.f, on[i], b[i]);
+  }
+  RowWalk at(static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / GROUP,
+             static_cast<int64_t>(gridDim.x) * kRows, p.H);
+  uint4 nx[PIECES], nz[PIECES];
+  auto fetch = [&] {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      nx[i] = nz[i] = make_uint4(0, 0, 0, 0);
+      if (at.r < p.rows && on[i]) {
+        const int c = (lane + i * GROUP) * 8;
+        nx[i] = __ldcs(reinterpret_cast<const uint4*>(p.x + at.t * p.sxt + at.h * p.sxh + c));
+        if (GATE) nz[i] = __ldcs(reinterpret_cast<const uint4*>(p.z + at.t * p.szt + at.h * p.szh + c));
+      }
+    }
+  };
+  fetch();
+  // (whole warps, and with GROUP > 32 whole CTAs, leave the loop together)
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.rows;
+       first += static_cast<int64_t>(gridDim.x) * kRows) {
+    const int64_t row = at.r;
+    float x[PIECES][8];
+    uint4 z[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      widen(nx[i], x[i]);
+      z[i] = nz[i];
+    }
+    at.next();
+    fetch();
+    normalise<GROUP, PIECES>(x, on, row < p.rows, p, buf, turn);
+    if (row < p.rows) {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        if (!on[i]) continue;
+        float g[8];
+        if (GATE) widen(z[i], g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[i][j] = fmaf(x[i][j], w[i][j], b[i][j]);
+          if (GATE) x[i][j] *= g[j] * sigmoid(g[j]);
+        }
+        __stcs(reinterpret_cast<uint4*>(p.y + row * p.C + (lane + i * GROUP) * 8), narrow(x[i]));
+      }
+    }
+  }
+}
+
+// This CTA's sums s (of its groups' rows) to `dst` [C].
+template <int GROUP, int PIECES>
+__device__ __forceinline__ void put_sums(float (&s)[PIECES][8], const bool (&on)[PIECES], float* dst, int C,
+                                         float* shared) {
+  const int lane = threadIdx.x % GROUP;
+  if constexpr (GROUP > 32) {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+      if (on[i])
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          *reinterpret_cast<float4*>(dst + (lane + i * GROUP) * 8 + 4 * j) =
+              make_float4(s[i][4 * j], s[i][4 * j + 1], s[i][4 * j + 2], s[i][4 * j + 3]);
+  } else {
+    constexpr int kWarps = kLnThreads / 32, kPitch = GROUP * PIECES * 8;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int o = 16; o >= GROUP; o >>= 1) s[i][j] += __shfl_xor_sync(0xffffffffu, s[i][j], o);
+        if (threadIdx.x % 32 < GROUP) shared[threadIdx.x / 32 * kPitch + (lane + i * GROUP) * 8 + j] = s[i][j];
+      }
+    __syncthreads();
+    for (int c = threadIdx.x; c < C; c += kLnThreads) {
+      float a = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) a += shared[i * kPitch + c];
+      dst[c] = a;
+    }
+    __syncthreads();
+  }
+}
+
+template <int GROUP, int PIECES, bool GATE>
+__global__ void __launch_bounds__(ln_threads(GROUP), GROUP > 32 ? 512 / ln_threads(GROUP) : 2)
+    cattn_layernorm_bwd_kernel(const LnArgs p) {
+  cconv::grid_dependency_wait();
+  cconv::grid_launch_dependents();
+  __shared__ float2 buf[2][32];
+  __shared__ float shared[GROUP > 32 ? 1 : kLnThreads / 32 * GROUP * PIECES * 8];
+  int turn = 0;
+  constexpr int kRows = ln_threads(GROUP) / GROUP;
+  const int lane = threadIdx.x % GROUP;
+  bool on[PIECES];
+  float w[PIECES][8], dw[PIECES][8], db[PIECES][8];
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int c = (lane + i * GROUP) * 8;
+    on[i] = c < p.C;
+    load_weights(p.w, p.wdt, c, 1.f, on[i], w[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.f;
+  }
+  RowWalk at(static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / GROUP,
+             static_cast<int64_t>(gridDim.x) * kRows, p.H);
+  uint4 nx[PIECES], nz[PIECES], ny[PIECES];
+  auto fetch = [&] {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      nx[i] = nz[i] = ny[i] = make_uint4(0, 0, 0, 0);
+      if (at.r < p.rows && on[i]) {
+        const int c = (lane + i * GROUP) * 8;
+        nx[i] = __ldcs(reinterpret_cast<const uint4*>(p.x + at.t * p.sxt + at.h * p.sxh + c));
+        ny[i] = __ldcs(reinterpret_cast<const uint4*>(p.dy + at.t * p.syt + at.h * p.syh + c));
+        if (GATE) nz[i] = __ldcs(reinterpret_cast<const uint4*>(p.z + at.t * p.szt + at.h * p.szh + c));
+      }
+    }
+  };
+  fetch();
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.rows;
+       first += static_cast<int64_t>(gridDim.x) * kRows) {
+    const int64_t row = at.r;
+    float x[PIECES][8], du[PIECES][8];
+    uint4 z[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      widen(nx[i], x[i]);
+      widen(ny[i], du[i]);
+      z[i] = nz[i];
+    }
+    at.next();
+    fetch();
+    const float r = normalise<GROUP, PIECES>(x, on, row < p.rows, p, buf, turn);
+    float along = 0.f, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      if (GATE) {
+        float g[8], b[8];
+        widen(z[i], g);
+        load_weights(p.b, p.wdt, (lane + i * GROUP) * 8, 0.f, on[i], b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float s = sigmoid(g[j]), d = du[i][j] * s;
+          du[i][j] = d * g[j];
+          g[j] = d * fmaf(x[i][j], w[i][j], b[j]) * fmaf(g[j], 1.f - s, 1.f);
+        }
+        if (row < p.rows && on[i])
+          __stcs(reinterpret_cast<uint4*>(p.dz + row * p.C + (lane + i * GROUP) * 8), narrow(g));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // (rows and channels that are not there have du = 0; x is finite there)
+        dw[i][j] = fmaf(du[i][j], x[i][j], dw[i][j]);
+        db[i][j] += du[i][j];
+        du[i][j] *= w[i][j];
+        along = fmaf(du[i][j], x[i][j], along);
+        sum += du[i][j];
+      }
+    }
+    group_sum<GROUP>(along, sum, buf, turn);
+    along *= p.inv;
+    sum = p.layer ? sum * p.inv : 0.f;
+    if (row < p.rows) {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        if (!on[i]) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i][j] = r * (fmaf(-along, x[i][j], du[i][j]) - sum);
+        __stcs(reinterpret_cast<uint4*>(p.y + row * p.C + (lane + i * GROUP) * 8), narrow(x[i]));
+      }
+    }
+  }
+  if (!p.part) return;
+  float* dst = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.C;
+  put_sums<GROUP, PIECES>(dw, on, dst, p.C, shared);
+  put_sums<GROUP, PIECES>(db, on, dst + p.C, p.C, shared);
+}
+
+// dw and db from the CTAs' sums, one after the other in each of kSumRows parts, then these.
+constexpr int kSumCols = 32, kSumRows = 16;
+__global__ void __launch_bounds__(kSumCols * kSumRows)
+    cattn_layernorm_sums_kernel(const float* part, int ctas, int C, int wdt, void* dw, void* db) {
+  cconv::grid_dependency_wait();
+  cconv::grid_launch_dependents();
+  __shared__ float sums[kSumRows][kSumCols];
+  const int c = blockIdx.x * kSumCols + threadIdx.x;  // of 2 C
+  float a = 0.f;
+  if (c < 2 * C) {
+#pragma unroll 8
+    for (int i = threadIdx.y; i < ctas; i += kSumRows) a += __ldcs(part + static_cast<int64_t>(i) * 2 * C + c);
+  }
+  sums[threadIdx.y][threadIdx.x] = a;
+  __syncthreads();
+  if (threadIdx.y != 0 || c >= 2 * C) return;
+#pragma unroll
+  for (int i = 1; i < kSumRows; ++i) a += sums[i][threadIdx.x];
+  void* dst = c < C ? dw : db;
+  if (!dst) return;
+  if (wdt == CCONV_F32)
+    static_cast<float*>(dst)[c % C] = a;
+  else
+    static_cast<uint16_t*>(dst)[c % C] = cconv::f32_to_bf16(a);
+}
+
+struct LnKernel {
+  void (*fwd[2])(LnArgs);
+  void (*bwd[2])(LnArgs);
+  int threads, rows;  // of a CTA
+};
+template <int GROUP, int PIECES>
+static LnKernel kernel_of() {
+  return LnKernel{{cattn_layernorm_fwd_kernel<GROUP, PIECES, false>, cattn_layernorm_fwd_kernel<GROUP, PIECES, true>},
+                  {cattn_layernorm_bwd_kernel<GROUP, PIECES, false>, cattn_layernorm_bwd_kernel<GROUP, PIECES, true>},
+                  ln_threads(GROUP), ln_threads(GROUP) / GROUP};
+}
+// The smallest group that holds a row in two pieces a thread at most (in one where a warp holds it).
+static LnKernel pick(int64_t C) {
+  if (C <= 32) return kernel_of<4, 1>();
+  if (C <= 64) return kernel_of<8, 1>();
+  if (C <= 128) return kernel_of<16, 1>();
+  if (C <= 256) return kernel_of<32, 1>();
+  if (C <= 512) return kernel_of<32, 2>();
+  if (C <= 1024) return kernel_of<128, 1>();
+  if (C <= 2048) return kernel_of<128, 2>();
+  if (C <= 4096) return kernel_of<256, 2>();
+  return kernel_of<512, 2>();
+}
+static int64_t most_ctas(int sms, int threads) { return static_cast<int64_t>(sms) * (kLnCtas * kLnThreads / threads); }
+
+static int check(const void* x, int64_t sxt, int64_t sxh, const void* z, int64_t szt, int64_t szh, int64_t total,
+                 int64_t H, int64_t C, const void* w, const void* b, cconv_dtype wdt, cattn_norm mode, float eps) {
+  if (total < 0 || total > kMaxRows || H < 1 || H > 65535 || C < 1 || C > kMaxNorm) return CCONV_ERR_SHAPE;
+  if ((mode != CATTN_NORM_RMS && mode != CATTN_NORM_LAYER) || !(eps >= 0.f)) return CCONV_ERR_SHAPE;
+  if (wdt != CCONV_F32 && wdt != CCONV_BF16) return CCONV_ERR_DTYPE;
+  if (C % 8 != 0) return CCONV_ERR_ALIGN;
+  const size_t ew = wdt == CCONV_F32 ? 4 : 2;
+  if (!aligned(w, ew) || !aligned(b, ew)) return CCONV_ERR_ALIGN;
+  if (total == 0) return CCONV_OK;
+  if (!x) return CCONV_ERR_NULL;
+  int rc = check_rows(x, total, H, sxt, sxh);
+  if (rc == CCONV_OK && z) rc = check_rows(z, total, H, szt, szh);
+  return rc;
+}
+
+static LnArgs args_of(const void* x, int64_t sxt, int64_t sxh, const void* z, int64_t szt, int64_t szh,
+                      int64_t total, int64_t H, int64_t C, const void* w, const void* b, cconv_dtype wdt,
+                      cattn_norm mode, float eps) {
+  LnArgs a{};
+  a.x = static_cast<const uint16_t*>(x), a.z = static_cast<const uint16_t*>(z);
+  a.sxt = sxt, a.sxh = sxh, a.szt = szt, a.szh = szh;
+  a.w = w, a.b = b;
+  a.rows = total * H;
+  a.H = static_cast<int>(H), a.C = static_cast<int>(C), a.wdt = wdt, a.layer = mode == CATTN_NORM_LAYER;
+  a.inv = 1.f / static_cast<float>(C), a.eps = eps;
+  return a;
+}
+
+}  // namespace cattn
+
+extern "C" CCONV_API int cattn_layernorm_fwd(const void* x, int64_t sxt, int64_t sxh, const void* gate,
+                                             int64_t szt, int64_t szh, int64_t total, int64_t H, int64_t C,
+                                             const void* w, const void* b, cconv_dtype wdt, cattn_norm mode,
+                                             float eps, void* y, cconv_stream_t stream) {
+  using namespace cattn;
+  const int rc = check(x, sxt, sxh, gate, szt, szh, total, H, C, w, b, wdt, mode, eps);
+  if (rc != CCONV_OK || total == 0) return rc;
+  if (!y) return CCONV_ERR_NULL;
+  if (!aligned(y, 16)) return CCONV_ERR_ALIGN;
+  LnArgs a = args_of(x, sxt, sxh, gate, szt, szh, total, H, C, w, b, wdt, mode, eps);
+  a.y = static_cast<uint16_t*>(y);
+  int sms = 0;
+  if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
+  const LnKernel kern = pick(C);
+  const int64_t ctas = (a.rows + kern.rows - 1) / kern.rows, most = most_ctas(sms, kern.threads);
+  return launch_pdl(kern.fwd[gate != nullptr], dim3(static_cast<unsigned>(ctas < most ? ctas : most)),
+                    dim3(kern.threads), 0, stream, a) == cudaSuccess
+             ? CCONV_OK
+             : CCONV_ERR_CUDA;
+}
+
+namespace cattn {
+constexpr int kLnBwdCtas = 4;  // CTAs of 256 threads an SM
+static int64_t bwd_ctas(int sms, int64_t rows, const LnKernel& kern) {
+  const int64_t ctas = (rows + kern.rows - 1) / kern.rows;
+  const int64_t most = static_cast<int64_t>(sms) * (kLnBwdCtas * kLnThreads / kern.threads);
+  return ctas < most ? ctas : most;
+}
+}  // namespace cattn
+
+extern "C" CCONV_API int cattn_layernorm_bwd_workspace_bytes(int64_t total, int64_t H, int64_t C, size_t* bytes) {
+  using namespace cattn;
+  if (!bytes) return CCONV_ERR_NULL;
+  if (total < 0 || total > kMaxRows || H < 1 || H > 65535 || C < 1 || C > kMaxNorm) return CCONV_ERR_SHAPE;
+  int sms = 0;
+  if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
+  const int64_t ctas = bwd_ctas(sms, total * H, pick(C));
+  *bytes = static_cast<size_t>(ctas > 0 ? ctas : 1) * 2 * static_cast<size_t>(C) * 4;
+  return CCONV_OK;
+}
+
+extern "C" CCONV_API int cattn_layernorm_bwd(const void* x, int64_t sxt, int64_t sxh, const void* dy,
+                                             int64_t syt, int64_t syh, const void* gate, int64_t szt,
+                                             int64_t szh, int64_t total, int64_t H, int64_t C, const void* w,
+                                             const void* b, cconv_dtype wdt, cattn_norm mode, float eps,
+                                             void* dx, void* dgate, void* dw, void* db, void* workspace,
+                                             size_t workspace_bytes, cconv_stream_t stream) {
+  using namespace cattn;
+  int rc = check(x, sxt, sxh, gate, szt, szh, total, H, C, w, b, wdt, mode, eps);
+  if (rc != CCONV_OK) return rc;
+  if (total > 0) {
+    if (!dy || !dx || (gate && !dgate)) return CCONV_ERR_NULL;
+    rc = check_rows(dy, total, H, syt, syh);
+    if (rc != CCONV_OK) return rc;
+    if (!aligned(dx, 16) || !aligned(dgate, 16)) return CCONV_ERR_ALIGN;
+  }
+  const size_t ew = wdt == CCONV_F32 ? 4 : 2;
+  if (!aligned(dw, ew) || !aligned(db, ew)) return CCONV_ERR_ALIGN;
+  LnArgs a = args_of(x, sxt, sxh, gate, szt, szh, total, H, C, w, b, wdt, mode, eps);
+  a.dy = static_cast<const uint16_t*>(dy), a.syt = syt, a.syh = syh;
+  a.y = static_cast<uint16_t*>(dx), a.dz = static_cast<uint16_t*>(dgate);
+  int sms = 0;
+  if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
+  const LnKernel kern = pick(C);
+  const int64_t ctas = bwd_ctas(sms, a.rows, kern);
+  const bool sums = dw || db;
+  if (sums) {
+    if (!workspace || workspace_bytes < static_cast<size_t>(ctas > 0 ? ctas : 1) * 2 * C * 4)
+      return CCONV_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return CCONV_ERR_ALIGN;
+    a.part = static_cast<float*>(workspace);
+  }
+  if (total > 0 && launch_pdl(kern.bwd[gate != nullptr], dim3(static_cast<unsigned>(ctas)), dim3(kern.threads), 0,
+                              stream, a) != cudaSuccess)
+    return CCONV_ERR_CUDA;
+  if (!sums) return CCONV_OK;
+  return launch_pdl(cattn_layernorm_sums_kernel, dim3(static_cast<unsigned>((2 * C + kSumCols - 1) / kSumCols)),
+                    dim3(kSumCols, kSumRows), 0, stream, static_cast<const float*>(workspace),
+                    static_cast<int>(ctas), static_cast<int>(C), static_cast<int>(wdt), dw, db) == cudaSuccess
+             ? CCONV_OK
+             : CCONV_ERR_CUDA;
+}

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kDgThreads) cattn_linear_dg_kernel(const __gri
   }
 }
 
-static int check_gates(const float* g, int64_t rows, int64_t H, int64_t st, int64_t sh) {
+int check_gates(const float* g, int64_t rows, int64_t H, int64_t st, int64_t sh) {
   if (!g) return CCONV_ERR_NULL;
   if (!aligned(g, 4)) return CCONV_ERR_ALIGN;
   if ((rows > 1 && st < 0) || (H > 1 && sh < 0)) return CCONV_ERR_STRIDE;
@@ -204,7 +204,7 @@ int check_linear(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t
   return aligned(o, 16) ? CCONV_OK : CCONV_ERR_ALIGN;
 }
 
-static int check_states(const int32_t* cu, int64_t nseq, int64_t Hv, const float* initial, const float* fin,
+int check_states(const int32_t* cu, int64_t nseq, int64_t Hv, const float* initial, const float* fin,
                         const int32_t* idx, int64_t S, int32_t* status) {
   if (!cu) return CCONV_ERR_NULL;
   if (nseq < 1 || nseq > kMaxSeqs || nseq * Hv > (int64_t(1) << 31) - 1) return CCONV_ERR_SHAPE;
@@ -289,7 +289,7 @@ static BwdWork bwd_work(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv, int
   return w;
 }
 
-static int check_sizes(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv, int64_t K, int64_t V) {
+int check_sizes(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv, int64_t K, int64_t V) {
   if (total < 0 || total > kMaxRows || nseq < 1 || nseq > kMaxSeqs || Hk < 1 ||
       Hv < 1 || Hv > 65535 || Hv % Hk != 0 || K < 8 || K > kMaxK || V < 8 || V > kMaxV)
     return CCONV_ERR_SHAPE;

@@ -34,4 +34,13 @@ struct Slots {
   }
 };
 
+// Checks of the entry points' arguments: a cconv_status.
+int check_gates(const float* g, int64_t rows, int64_t H, int64_t st, int64_t sh);
+int check_linear(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt, int64_t skh,
+                 const void* v, int64_t svt, int64_t svh, const float* g, int64_t sgt, int64_t sgh,
+                 int64_t rows, int64_t Hk, int64_t Hv, int64_t K, int64_t V, const void* o);
+int check_states(const int32_t* cu, int64_t nseq, int64_t Hv, const float* initial, const float* fin,
+                 const int32_t* idx, int64_t S, int32_t* status);
+int check_sizes(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv, int64_t K, int64_t V);
+
 }  // namespace cattn

@@ -119,10 +119,6 @@ __global__ void __launch_bounds__(kWarps * 32) cattn_linear_update_kernel(Update
   }
 }
 
-int check_linear(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt, int64_t skh,
-                 const void* v, int64_t svt, int64_t svh, const float* g, int64_t sgt, int64_t sgh,
-                 int64_t rows, int64_t Hk, int64_t Hv, int64_t K, int64_t V, const void* o);
-
 }  // namespace cattn
 
 extern "C" CCONV_API int cattn_linear_update(

@@ -363,7 +363,120 @@ PyObject* qknorm_bwd(PyObject* const* a, Py_ssize_t count) {
 }
 
 // ---------------------------------------------------------------------------------------
-// linear attention
+// layer norm
+// ---------------------------------------------------------------------------------------
+// [rows, heads, channels], or [rows, channels] as one head.
+struct Layer {
+  Arg x, w, b, gate;
+  int64_t total, H, C;
+  cconv_dtype wdt = CCONV_F32;
+  cattn_norm mode;
+  float eps;
+};
+
+void check_layer_rows(const Arg& a) {
+  check_type(a, at::kBFloat16);
+  const int64_t d = a.t->dim();
+  if (d != 2 && d != 3)
+    raise(PyExc_ValueError, "%s must have 2 or 3 dimensions, got shape %s", a.name, shape_of(a.t->sizes()).c_str());
+  if (a.t->size(d - 1) > 1 && a.t->stride(d - 1) != 1)
+    raise(PyExc_ValueError, "%s must have channel stride 1, got strides %s", a.name, shape_of(a.t->strides()).c_str());
+}
+int64_t head_stride(const Arg& a) { return a.given() && a.t->dim() == 3 ? a.t->stride(1) : 0; }
+int64_t row_stride(const Arg& a) { return a.given() ? a.t->stride(0) : 0; }
+
+// x, w, b, gate, mode, eps
+Layer layer_args(PyObject* const* a) {
+  Layer n{tensor(a[0], "x"), optional(a[1], "w"), optional(a[2], "b"), optional(a[3], "gate"), 0, 1, 0};
+  check_layer_rows(n.x);
+  n.total = n.x.t->size(0), n.C = n.x.t->size(n.x.t->dim() - 1);
+  if (n.x.t->dim() == 3) n.H = n.x.t->size(1);
+  if (n.gate.given()) {
+    check_layer_rows(n.gate);
+    check_same_shape(n.gate, n.x);
+  }
+  for (const Arg* w : {&n.w, &n.b}) {
+    if (!w->given()) continue;
+    const auto type = w->t->scalar_type();
+    if (type != at::kFloat && type != at::kBFloat16)
+      raise(PyExc_TypeError, "%s must be a float32 or bfloat16 tensor", w->name);
+    check_exact(*w, {n.C}, type);
+    n.wdt = type == at::kFloat ? CCONV_F32 : CCONV_BF16;
+  }
+  if (n.w.given() && n.b.given() && n.w.t->scalar_type() != n.b.t->scalar_type())
+    raise(PyExc_TypeError, "w and b must have the same dtype");
+  const char* mode = PyUnicode_Check(a[4]) ? PyUnicode_AsUTF8(a[4]) : "";
+  if (!mode) throw Raised{};
+  if (std::string(mode) == "layer")
+    n.mode = CATTN_NORM_LAYER;
+  else if (std::string(mode) == "rms")
+    n.mode = CATTN_NORM_RMS;
+  else
+    raise(PyExc_ValueError, "mode must be 'layer' or 'rms', got %R", a[4]);
+  n.eps = as_float(a[5]);
+  return n;
+}
+
+// .., y, stream
+PyObject* layernorm_fwd(PyObject* const* a, Py_ssize_t count) {
+  ARGS(8);
+  const Layer n = layer_args(a);
+  const Arg y = optional(a[6], "y");
+  if (y.given()) check_exact(y, n.x.t->sizes(), at::kBFloat16);
+  check_disjoint({&y}, {&n.x, &n.w, &n.b, &n.gate});
+  const auto dev = check_device({&n.x, &n.w, &n.b, &n.gate, &y});
+  const Place place(a[7], dev);
+  at::Tensor out;
+  place.out_or_new(y, out, n.x.t->sizes(), at::kBFloat16);
+  check_rc(cattn_layernorm_fwd(n.x.ptr(), row_stride(n.x), head_stride(n.x), n.gate.ptr(), row_stride(n.gate),
+                               head_stride(n.gate), n.total, n.H, n.C, n.w.ptr(), n.b.ptr(), n.wdt, n.mode, n.eps,
+                               out.data_ptr(), place.handle()),
+           "cattn_layernorm_fwd");
+  return THPVariable_Wrap(out);
+}
+
+// .., dy, dx, dw, db, dgate, workspace, stream
+PyObject* layernorm_bwd(PyObject* const* a, Py_ssize_t count) {
+  ARGS(13);
+  const Layer n = layer_args(a);
+  const Arg dy = tensor(a[6], "dy"), dx = optional(a[7], "dx"), dw = optional(a[8], "dw"), db = optional(a[9], "db"),
+            dgate = optional(a[10], "dgate"), ws = optional(a[11], "workspace");
+  check_layer_rows(dy);
+  check_same_shape(dy, n.x);
+  if (dx.given()) check_exact(dx, n.x.t->sizes(), at::kBFloat16);
+  const Arg* of[3][2] = {{&dw, &n.w}, {&db, &n.b}, {&dgate, &n.gate}};
+  for (auto& s : of) {
+    if (!s[0]->given()) continue;
+    if (!s[1]->given()) raise(PyExc_ValueError, "%s without %s", s[0]->name, s[1]->name);
+    check_exact(*s[0], s[1]->t->sizes(), s[1]->t->scalar_type());
+  }
+  if (ws.given() && !ws.t->is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
+  check_disjoint({&dx, &dw, &db, &dgate, &ws}, {&n.x, &dy, &n.w, &n.b, &n.gate});
+  const auto dev = check_device({&n.x, &dy, &n.w, &n.b, &n.gate, &dx, &dw, &db, &dgate, &ws});
+  const Place place(a[12], dev);
+  at::Tensor ox, ow, ob, oz, work;
+  place.out_or_new(dx, ox, n.x.t->sizes(), at::kBFloat16);
+  if (n.w.given()) place.out_or_new(dw, ow, {n.C}, n.w.t->scalar_type());
+  if (n.b.given()) place.out_or_new(db, ob, {n.C}, n.b.t->scalar_type());
+  if (n.gate.given()) place.out_or_new(dgate, oz, n.x.t->sizes(), at::kBFloat16);
+  if (ws.given()) {
+    work = *ws.t;
+  } else if (ow.defined() || ob.defined()) {
+    size_t bytes = 0;
+    check_rc(cattn_layernorm_bwd_workspace_bytes(n.total, n.H, n.C, &bytes), "cattn_layernorm_bwd_workspace_bytes");
+    work = place.make({static_cast<int64_t>(bytes)}, at::kByte);
+  }
+  auto ptr = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+  check_rc(cattn_layernorm_bwd(n.x.ptr(), row_stride(n.x), head_stride(n.x), dy.ptr(), row_stride(dy), head_stride(dy),
+                               n.gate.ptr(), row_stride(n.gate), head_stride(n.gate), n.total, n.H, n.C, n.w.ptr(),
+                               n.b.ptr(), n.wdt, n.mode, n.eps, ox.data_ptr(), ptr(oz), ptr(ow), ptr(ob), ptr(work),
+                               work.defined() ? work.nbytes() : 0, place.handle()),
+           "cattn_layernorm_bwd");
+  return tuple({&ox, &ow, &ob, &oz});
+}
+
+// ---------------------------------------------------------------------------------------
+// linear attention and the delta rule
 // ---------------------------------------------------------------------------------------
 struct Linear {
   Arg q, k, v, g;
@@ -393,6 +506,16 @@ Linear linear_args(PyObject* const* a) {
   return n;
 }
 
+// The delta rule's step sizes, a call's last argument but for outputs of its own.
+Arg beta_arg(PyObject* o, const Linear& n) {
+  const Arg beta = tensor(o, "beta");
+  check_type(beta, at::kFloat);
+  if (beta.t->dim() != 2 || beta.t->size(0) != n.rows || beta.t->size(1) != n.Hv)
+    raise(PyExc_ValueError, "beta must have shape (%lld, %lld), got %s", (long long)n.rows, (long long)n.Hv,
+          shape_of(beta.t->sizes()).c_str());
+  return beta;
+}
+
 int64_t check_states(const Arg& a, const Linear& n) {
   if (a.t->dim() != 4)
     raise(PyExc_ValueError, "%s must be a [S, %lld, %lld, %lld] tensor", a.name, (long long)n.Hv, (long long)n.K,
@@ -414,6 +537,8 @@ int64_t check_cu(const Arg& a) {
       (n).k.t->stride(1), (n).v.t->data_ptr(), (n).v.t->stride(0), (n).v.t->stride(1),                      \
       static_cast<const float*>((n).g.t->data_ptr()), (n).g.t->stride(0), (n).g.t->stride(1)
 
+#define BETA(b) static_cast<const float*>((b).t->data_ptr()), (b).t->stride(0), (b).t->stride(1)
+
 at::Tensor workspace_of(const Arg& ws, int (*query)(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, size_t*),
                         const char* call, const Linear& n, int64_t nseq, const Place& place) {
   if (ws.given()) return *ws.t;
@@ -423,10 +548,12 @@ at::Tensor workspace_of(const Arg& ws, int (*query)(int64_t, int64_t, int64_t, i
 }
 
 // q, k, v, g, scale, cu_seqlens, initial_state, final_state (a tensor, True or None), state_indices,
-// status, o, workspace, stream
-PyObject* linear_fwd(PyObject* const* a, Py_ssize_t count) {
-  ARGS(13);
+// status, o, workspace, stream; of the delta rule: beta
+template <bool DELTA>
+PyObject* sequence_fwd(PyObject* const* a, Py_ssize_t count) {
+  ARGS(DELTA ? 14 : 13);
   const Linear n = linear_args(a);
+  const Arg beta = DELTA ? beta_arg(a[13], n) : none;
   const Arg cu = tensor(a[5], "cu_seqlens"), init = optional(a[6], "initial_state"),
             fin = a[7] == Py_True || a[7] == Py_False ? Arg{"final_state", nullptr} : optional(a[7], "final_state"),
             idx = optional(a[8], "state_indices"), status = idx.given() ? optional(a[9], "status") : Arg{"status", nullptr},
@@ -457,24 +584,30 @@ PyObject* linear_fwd(PyObject* const* a, Py_ssize_t count) {
   }
   if (o.given()) check_exact(o, {n.rows, n.Hv, n.V}, at::kBFloat16);
   if (ws.given() && !ws.t->is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
-  check_disjoint({&o, &status, &ws, &fin}, {&n.q, &n.k, &n.v, &n.g, &cu, &idx});
+  check_disjoint({&o, &status, &ws, &fin}, {&n.q, &n.k, &n.v, &n.g, &beta, &cu, &idx});
   // the initial state may be the final state's array, but no other part of it
   const bool in_place = fin.given() && init.given() && fin.ptr() == init.ptr();
   check_disjoint({&o, &status, &ws, in_place ? &none : &fin}, {&init});
-  const auto dev = check_device({&n.q, &n.k, &n.v, &n.g, &cu, &init, &fin, &idx, &status, &o, &ws});
+  const auto dev = check_device({&n.q, &n.k, &n.v, &n.g, &beta, &cu, &init, &fin, &idx, &status, &o, &ws});
   const Place place(a[12], dev);
   at::Tensor out, final_state, st;
   place.out_or_new(o, out, {n.rows, n.Hv, n.V}, at::kBFloat16);
   if (want || fin.given()) place.out_or_new(fin, final_state, {nseq, n.Hv, n.K, n.V}, at::kFloat);
   if (idx.given()) place.out_or_new(status, st, {2}, at::kInt);
-  const at::Tensor work = workspace_of(ws, cattn_linear_fwd_workspace_bytes, "cattn_linear_fwd_workspace_bytes", n, nseq, place);
-  check_rc(cattn_linear_fwd(QKVG(n), n.rows, n.Hk, n.Hv, n.K, n.V, static_cast<const int32_t*>(cu.ptr()), nseq,
-                            n.scale, static_cast<const float*>(init.ptr()),
-                            final_state.defined() ? static_cast<float*>(final_state.data_ptr()) : nullptr,
-                            static_cast<const int32_t*>(idx.ptr()), S,
-                            st.defined() ? static_cast<int32_t*>(st.data_ptr()) : nullptr, out.data_ptr(),
-                            work.data_ptr(), work.nbytes(), place.handle()),
-           "cattn_linear_fwd");
+  const at::Tensor work =
+      DELTA ? workspace_of(ws, cattn_delta_fwd_workspace_bytes, "cattn_delta_fwd_workspace_bytes", n, nseq, place)
+            : workspace_of(ws, cattn_linear_fwd_workspace_bytes, "cattn_linear_fwd_workspace_bytes", n, nseq, place);
+#define TAIL                                                                                                  \
+  n.rows, n.Hk, n.Hv, n.K, n.V, static_cast<const int32_t*>(cu.ptr()), nseq, n.scale,                         \
+      static_cast<const float*>(init.ptr()),                                                                  \
+      final_state.defined() ? static_cast<float*>(final_state.data_ptr()) : nullptr,                          \
+      static_cast<const int32_t*>(idx.ptr()), S, st.defined() ? static_cast<int32_t*>(st.data_ptr()) : nullptr, \
+      out.data_ptr(), work.data_ptr(), work.nbytes(), place.handle()
+  if constexpr (DELTA)
+    check_rc(cattn_delta_fwd(QKVG(n), BETA(beta), TAIL), "cattn_delta_fwd");
+  else
+    check_rc(cattn_linear_fwd(QKVG(n), TAIL), "cattn_linear_fwd");
+#undef TAIL
   return tuple({&out, &final_state, &st});
 }
 
@@ -532,10 +665,12 @@ PyObject* linear_bwd(PyObject* const* a, Py_ssize_t count) {
   return tuple({&oq, &ok, &ov, &og, &os});
 }
 
-// q, k, v, g, scale, state, state_indices, pad_rows, o, status, stream
-PyObject* linear_update(PyObject* const* a, Py_ssize_t count) {
-  ARGS(11);
+// q, k, v, g, scale, state, state_indices, pad_rows, o, status, stream; of the delta rule: beta
+template <bool DELTA>
+PyObject* token_update(PyObject* const* a, Py_ssize_t count) {
+  ARGS(DELTA ? 12 : 11);
   const Linear n = linear_args(a);
+  const Arg beta = DELTA ? beta_arg(a[11], n) : none;
   const Arg state = tensor(a[5], "state"), idx = optional(a[6], "state_indices"), o = optional(a[8], "o"),
             status = optional(a[9], "status");
   const int64_t S = check_states(state, n);
@@ -545,16 +680,21 @@ PyObject* linear_update(PyObject* const* a, Py_ssize_t count) {
     raise(PyExc_ValueError, "without state_indices row i uses slot i: state needs S >= N=%lld", (long long)n.rows);
   if (o.given()) check_exact(o, n.v.t->sizes(), at::kBFloat16);
   if (status.given()) check_status(status);
-  check_disjoint({&o, &state, &status}, {&n.q, &n.k, &n.v, &n.g, &idx});
-  const auto dev = check_device({&n.q, &n.k, &n.v, &n.g, &state, &idx, &o, &status});
+  check_disjoint({&o, &state, &status}, {&n.q, &n.k, &n.v, &n.g, &beta, &idx});
+  const auto dev = check_device({&n.q, &n.k, &n.v, &n.g, &beta, &state, &idx, &o, &status});
   const Place place(a[10], dev);
   at::Tensor out, st;
   place.out_or_new(o, out, n.v.t->sizes(), at::kBFloat16);
   place.out_or_new(status, st, {2}, at::kInt);
-  check_rc(cattn_linear_update(QKVG(n), n.rows, n.Hk, n.Hv, n.K, n.V, n.scale, static_cast<float*>(state.out()), S,
-                               static_cast<const int32_t*>(idx.ptr()), as_bool(a[7]), out.data_ptr(),
-                               static_cast<int32_t*>(st.data_ptr()), place.handle()),
-           "cattn_linear_update");
+#define TAIL                                                                                                   \
+  n.rows, n.Hk, n.Hv, n.K, n.V, n.scale, static_cast<float*>(state.out()), S,                                  \
+      static_cast<const int32_t*>(idx.ptr()), as_bool(a[7]), out.data_ptr(), static_cast<int32_t*>(st.data_ptr()), \
+      place.handle()
+  if constexpr (DELTA)
+    check_rc(cattn_delta_update(QKVG(n), BETA(beta), TAIL), "cattn_delta_update");
+  else
+    check_rc(cattn_linear_update(QKVG(n), TAIL), "cattn_linear_update");
+#undef TAIL
   return tuple({&out, &st});
 }
 
@@ -576,10 +716,13 @@ PyObject* set_error(PyObject*, PyObject* cls) {
   Py_RETURN_NONE;
 }
 
+constexpr auto linear_fwd = sequence_fwd<false>, delta_fwd = sequence_fwd<true>;
+constexpr auto linear_update = token_update<false>, delta_update = token_update<true>;
+
 #define METHOD(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(entry<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(qknorm_fwd), METHOD(qknorm_bwd), METHOD(linear_fwd), METHOD(linear_bwd),
-                         METHOD(linear_update), {"set_error", set_error, METH_O, nullptr},
+                         METHOD(linear_update), METHOD(delta_fwd), METHOD(delta_update), METHOD(layernorm_fwd), METHOD(layernorm_bwd), {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_cattn", nullptr, -1, methods};
 

@@ -13,6 +13,9 @@
  *                 (a cos - b sin, b cos + a sin)
  *   linear    S_t = exp(g_t) S_{t-1} + k_t v_t^T          S: [K, V] for each value head
  *             o_t = scale * q_t^T S_t
+ *   layernorm y = ((x - mean) / sqrt(var + eps) * w + b) * silu(gate)
+ *   delta     S_t = exp(g_t) S_{t-1} + beta_t k_t (v_t - (exp(g_t) S_{t-1})^T k_t)^T
+ *             o_t = scale * q_t^T S_t
  *
  * Conventions shared by every call (those of cconv.h):
  *   - Queries, keys, values, outputs and their gradients are bf16; g, the states, their
@@ -51,7 +54,8 @@ extern "C" {
 
 typedef enum {
   CATTN_NORM_RMS = 0,
-  CATTN_NORM_L2 = 1
+  CATTN_NORM_L2 = 1,
+  CATTN_NORM_LAYER = 2 /* cattn_layernorm_*: by the standard deviation, from the mean */
 } cattn_norm;
 
 /*
@@ -180,6 +184,77 @@ CCONV_API int cattn_linear_update(const void* q, int64_t sqt, int64_t sqh, const
                                   float scale, float* state, int64_t S,
                                   const int32_t* state_indices, int pad_rows, void* o,
                                   int32_t* status_dev, cconv_stream_t stream);
+
+/* Workspace cattn_delta_fwd needs (at a 16-byte boundary). */
+CCONV_API int cattn_delta_fwd_workspace_bytes(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv,
+                                              int64_t K, int64_t V, size_t* bytes);
+
+/*
+ * cattn_delta_fwd -- the gated delta rule over packed sequences: what a token adds to the state
+ * replaces what its key reads there, by the share beta.
+ *
+ *   q .. g    as in cattn_linear_fwd.
+ *   beta      [total, Hv] fp32 step sizes, at beta + t * sbt + h * sbh with any strides >= 0.  They
+ *             are taken as they are; the recurrence is stable for 0 <= beta |k_t|^2 <= 2.
+ *   scale .. o  as in cattn_linear_fwd.
+ *   Limits on the sizes as in cattn_linear_fwd; nseq * Hv * ceil(V / 32) < 2^31 and
+ *   (total / 64 + nseq) * Hv < 2^31.
+ *   Non-finite values of one sequence never reach another sequence's results; inside a sequence
+ *   they may reach the outputs of up to 63 tokens before theirs.
+ */
+CCONV_API int cattn_delta_fwd(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt,
+                              int64_t skh, const void* v, int64_t svt, int64_t svh, const float* g,
+                              int64_t sgt, int64_t sgh, const float* beta, int64_t sbt, int64_t sbh,
+                              int64_t total, int64_t Hk, int64_t Hv, int64_t K, int64_t V,
+                              const int32_t* cu_seqlens, int64_t nseq, float scale,
+                              const float* initial_state, float* final_state,
+                              const int32_t* state_indices, int64_t S, int32_t* status_dev, void* o,
+                              void* workspace, size_t workspace_bytes, cconv_stream_t stream);
+
+/*
+ * cattn_delta_update -- one token for each of N sequences, on a pooled state: the arguments of
+ * cattn_linear_update, and beta [N, Hv] fp32, strided.
+ */
+CCONV_API int cattn_delta_update(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt,
+                                 int64_t skh, const void* v, int64_t svt, int64_t svh, const float* g,
+                                 int64_t sgt, int64_t sgh, const float* beta, int64_t sbt, int64_t sbh,
+                                 int64_t N, int64_t Hk, int64_t Hv, int64_t K, int64_t V, float scale,
+                                 float* state, int64_t S, const int32_t* state_indices, int pad_rows,
+                                 void* o, int32_t* status_dev, cconv_stream_t stream);
+
+/*
+ * cattn_layernorm_fwd -- layer norm of rows or heads (CATTN_NORM_LAYER) or their norm by the root
+ * mean square (CATTN_NORM_RMS), with weight, bias and gate:
+ *
+ *   y = ((x - m) / sqrt(mean((x - m)^2) + eps) * w + b) * silu(gate)     m = mean(x), RMS: 0
+ *
+ *   x, gate   [total, H, C] bf16, strided; gate may be NULL (no factor).  total may be 0.
+ *   w, b      [C] in wdt, or NULL (1, 0).
+ *   y         [total, H, C] bf16 contiguous output, 16-byte aligned.
+ *   eps >= 0.  C % 8 == 0, 8 <= C <= 8192, 1 <= H <= 65535, total < 2^31 - 16.
+ */
+CCONV_API int cattn_layernorm_fwd(const void* x, int64_t sxt, int64_t sxh, const void* gate,
+                                  int64_t szt, int64_t szh, int64_t total, int64_t H, int64_t C,
+                                  const void* w, const void* b, cconv_dtype wdt, cattn_norm mode,
+                                  float eps, void* y, cconv_stream_t stream);
+
+/* Workspace cattn_layernorm_bwd needs on the current device (16-byte aligned). */
+CCONV_API int cattn_layernorm_bwd_workspace_bytes(int64_t total, int64_t H, int64_t C, size_t* bytes);
+
+/*
+ * cattn_layernorm_bwd -- its gradient; the norm is recomputed from x.
+ *
+ *   dy        [total, H, C] bf16, strided.
+ *   dx, dgate contiguous bf16 outputs, 16-byte aligned; dgate is not written without a gate.
+ *   dw, db    [C] outputs in wdt, or NULL to skip them (the sums run over tokens and heads in a
+ *             fixed order, in fp32; the workspace is not used if both are skipped).
+ */
+CCONV_API int cattn_layernorm_bwd(const void* x, int64_t sxt, int64_t sxh, const void* dy,
+                                  int64_t syt, int64_t syh, const void* gate, int64_t szt,
+                                  int64_t szh, int64_t total, int64_t H, int64_t C, const void* w,
+                                  const void* b, cconv_dtype wdt, cattn_norm mode, float eps, void* dx,
+                                  void* dgate, void* dw, void* db, void* workspace,
+                                  size_t workspace_bytes, cconv_stream_t stream);
 
 /* Launch descriptions of this library's calls; as cconv_describe_begin / cconv_describe_end. */
 CCONV_API int cattn_describe_begin(void);
