@@ -9,6 +9,8 @@ libraries; the first call does, and raises if they have not been built.
 """
 from .attn import (  # noqa: F401
     attn_describe,
+    cattn_delta_bwd,
+    cattn_delta_bwd_workspace_bytes,
     cattn_delta_fwd,
     cattn_delta_fwd_workspace_bytes,
     cattn_delta_update,

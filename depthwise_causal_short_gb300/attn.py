@@ -54,6 +54,9 @@ _SIGNATURES = {
     "cattn_linear_update": _QKVG + [_I64] * 5 + [_F32, _P, _I64, _P, _INT, _P, _P, _P],
     "cattn_delta_fwd_workspace_bytes": [_I64] * 6 + [ctypes.POINTER(_SZ)],
     "cattn_delta_fwd": _QKVGB + [_I64] * 5 + [_P, _I64, _F32, _P, _P, _P, _I64, _P, _P, _P, _SZ, _P],
+    "cattn_delta_bwd_workspace_bytes": [_I64] * 6 + [ctypes.POINTER(_SZ)],
+    "cattn_delta_bwd": _QKVGB + [_P, _I64, _I64] + [_I64] * 5 + [_P, _I64, _F32, _P, _P, _I64, _P, _P,
+                                                                 _P, _P, _P, _P, _P, _P, _SZ, _P],
     "cattn_delta_update": _QKVGB + [_I64] * 5 + [_F32, _P, _I64, _P, _INT, _P, _P, _P],
     "cattn_layernorm_fwd": [_P, _I64, _I64] * 2 + [_I64] * 3 + [_P, _P, _INT, _INT, _F32, _P, _P],
     "cattn_layernorm_bwd_workspace_bytes": [_I64] * 3 + [ctypes.POINTER(_SZ)],
@@ -233,6 +236,27 @@ def cattn_delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     None)."""
     return _calls().delta_fwd(q, k, v, g, scale, cu_seqlens, initial_state, final_state, state_indices,
                               status, o, workspace, stream, beta)
+
+
+def cattn_delta_bwd_workspace_bytes(total: int, nseq: int, Hk: int, Hv: int, K: int, V: int,
+                                    device=None) -> int:
+    """Workspace cattn_delta_bwd needs on `device` (default: the current CUDA device)."""
+    return _bytes("cattn_delta_bwd_workspace_bytes", device, total, nseq, Hk, Hv, K, V)
+
+
+def cattn_delta_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                    beta: torch.Tensor, do: torch.Tensor, cu_seqlens: torch.Tensor, *,
+                    scale: float | None = None, initial_state: torch.Tensor | None = None,
+                    state_indices: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                    want_dinit: bool | None = None, dq: torch.Tensor | None = None,
+                    dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+                    dg: torch.Tensor | None = None, dbeta: torch.Tensor | None = None,
+                    d_initial_state: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """Gradient of cattn_delta_fwd's o: (dq, dk, dv, dg, dbeta, d_initial_state or None).  The final
+    states count as constants.  Arguments as in cattn_linear_bwd; dbeta is [total, Hv] fp32."""
+    return _calls().delta_bwd(q, k, v, g, scale, do, cu_seqlens, initial_state, state_indices, status,
+                              want_dinit, dq, dk, dv, dg, d_initial_state, workspace, stream, beta, dbeta)
 
 
 def cattn_delta_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,

@@ -19,6 +19,31 @@ static Rows rows(const void* p, int64_t st, int64_t sh) {
   return Rows{static_cast<const uint16_t*>(p), st, sh};
 }
 
+// What a backward call keeps in its workspace, from a 256-byte boundary.
+struct DeltaWork {
+  size_t records, z, heads, ends, odots, vdots, bdots, bytes;
+};
+static DeltaWork delta_work(int64_t total, int64_t nseq, int64_t Hv, int64_t V) {
+  const size_t tiles = static_cast<size_t>(delta_tiles(V)), rows = static_cast<size_t>(total) * Hv;
+  const size_t states = total > 0 ? static_cast<size_t>(delta_slots(total, nseq)) * Hv * tiles * kStatePanel : 0;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t r = at;
+    at += (n + 255) / 256 * 256;
+    return r;
+  };
+  DeltaWork w{};
+  w.records = take(record_bytes(total, nseq, Hv));
+  w.z = take(rows * V * 4);
+  w.heads = take(states);
+  w.ends = take(states);
+  w.odots = take(2 * tiles * rows * 4);
+  w.vdots = take(2 * tiles * rows * 4);
+  w.bdots = take(2 * tiles * rows * 4);
+  w.bytes = at + 256;
+  return w;
+}
+
 }  // namespace cattn
 
 extern "C" CCONV_API int cattn_delta_fwd_workspace_bytes(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv,
@@ -71,4 +96,83 @@ extern "C" CCONV_API int cattn_delta_fwd(
     if (rc != CCONV_OK) return rc;
   }
   return launch_delta_fwd(c, stream);
+}
+
+extern "C" CCONV_API int cattn_delta_bwd_workspace_bytes(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv,
+                                                         int64_t K, int64_t V, size_t* bytes) {
+  using namespace cattn;
+  if (!bytes) return CCONV_ERR_NULL;
+  const int rc = check_sizes(total, nseq, Hk, Hv, K, V);
+  if (rc != CCONV_OK) return rc;
+  if (!grids_fit(total, nseq, Hv, V)) return CCONV_ERR_SHAPE;
+  *bytes = delta_work(total, nseq, Hv, V).bytes;
+  return CCONV_OK;
+}
+
+extern "C" CCONV_API int cattn_delta_bwd(
+    const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt, int64_t skh, const void* v,
+    int64_t svt, int64_t svh, const float* g, int64_t sgt, int64_t sgh, const float* beta, int64_t sbt,
+    int64_t sbh, const void* do_, int64_t sot, int64_t soh, int64_t total, int64_t Hk, int64_t Hv, int64_t K,
+    int64_t V, const int32_t* cu_seqlens, int64_t nseq, float scale, const float* initial_state,
+    const int32_t* state_indices, int64_t S, int32_t* status_dev, void* dq, void* dk, void* dv, float* dg,
+    float* dbeta, float* d_initial_state, void* workspace, size_t workspace_bytes, cconv_stream_t stream) {
+  using namespace cattn;
+  int rc = check_linear(q, sqt, sqh, k, skt, skh, v, svt, svh, g, sgt, sgh, total, Hk, Hv, K, V, dv);
+  if (rc == CCONV_OK && total > 0) rc = check_gates(beta, total, Hv, sbt, sbh);
+  if (rc == CCONV_OK)
+    rc = check_states(cu_seqlens, nseq, Hv, initial_state, nullptr, state_indices, S, status_dev);
+  if (rc != CCONV_OK) return rc;
+  if (!aligned(d_initial_state, 32)) return CCONV_ERR_ALIGN;
+  if (total > 0) {
+    if (!do_ || !dq || !dk || !dg || !dbeta) return CCONV_ERR_NULL;
+    rc = check_rows(do_, total, Hv, sot, soh);
+    if (rc != CCONV_OK) return rc;
+    if (!aligned(dq, 16) || !aligned(dk, 16) || !aligned(dg, 16) || !aligned(dbeta, 16)) return CCONV_ERR_ALIGN;
+  }
+  if (!grids_fit(total, nseq, Hv, V)) return CCONV_ERR_SHAPE;
+  const DeltaWork w = delta_work(total, nseq, Hv, V);
+  if (total > 0) {
+    if (!workspace || workspace_bytes < w.bytes) return CCONV_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return CCONV_ERR_ALIGN;
+  }
+  const bool checked = state_indices && (nseq > kInKernelChecks || total == 0);
+  if (checked || total == 0) {
+    rc = launch_checks(state_indices, nseq, S, 0, status_dev, total == 0 ? cu_seqlens : nullptr, nseq, total,
+                       nullptr, stream);
+    if (rc != CCONV_OK) return rc;
+  }
+  if (total == 0) {
+    if (d_initial_state && !cconv::recording_launches() &&
+        report_cuda("cudaMemsetAsync",
+                    cudaMemsetAsync(d_initial_state, 0, static_cast<size_t>(nseq) * Hv * K * V * 4,
+                                    stream)) != cudaSuccess)
+      return CCONV_ERR_CUDA;
+    return CCONV_OK;
+  }
+  uint8_t* ws = align256(workspace);
+  DeltaCall c{};
+  c.q = rows(q, sqt, sqh), c.k = rows(k, skt, skh), c.v = rows(v, svt, svh), c.d_o = rows(do_, sot, soh);
+  c.g = Gates{g, sgt, sgh}, c.beta = Gates{beta, sbt, sbh};
+  c.s = LinearShape{static_cast<int>(total), static_cast<int>(Hk), static_cast<int>(Hv),
+                    static_cast<int>(K), static_cast<int>(V), static_cast<int>(nseq)};
+  c.cu = cu_seqlens;
+  c.slots = Slots{state_indices, S};
+  c.checked = checked;
+  c.status = status_dev;
+  c.scale = scale;
+  c.initial = initial_state;
+  c.records = ws + w.records;
+  c.z = reinterpret_cast<float*>(ws + w.z);
+  c.heads = ws + w.heads, c.ends = ws + w.ends;
+  c.odots = reinterpret_cast<float*>(ws + w.odots);
+  c.vdots = reinterpret_cast<float*>(ws + w.vdots);
+  c.bdots = reinterpret_cast<float*>(ws + w.bdots);
+  c.dq = static_cast<uint16_t*>(dq), c.dk = static_cast<uint16_t*>(dk), c.dv = static_cast<uint16_t*>(dv);
+  c.dg = dg, c.dbeta = dbeta, c.dinit = d_initial_state;
+  rc = launch_delta_prep(c, stream);
+  if (rc == CCONV_OK) rc = launch_delta_states(c, stream);
+  if (rc == CCONV_OK) rc = launch_delta_back(c, stream);
+  if (rc == CCONV_OK) rc = launch_delta_grads(c, stream);
+  if (rc == CCONV_OK) rc = launch_delta_gates(c, stream);
+  return rc;
 }

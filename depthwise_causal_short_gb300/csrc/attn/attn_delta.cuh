@@ -44,7 +44,29 @@ enum DeltaGate : int { kEf = 0, kEb = 64, kBeta = 128, kTotal = 192 };  // float
 // total / 64 + nseq of them.
 __host__ __device__ inline int64_t delta_slots(int64_t total, int64_t nseq) { return total / kDelta + nseq; }
 
+// The sequence and rows of record slot `slot` (rows [row0, row0 + n)); false if it has none.
+__device__ __forceinline__ bool find_chunk(const int32_t* cu, int nseq, int total, int64_t slot, int lane,
+                                           int& row0, int& n) {
+  // the last sequence whose first slot is not above `slot`, 32 candidates at a time
+  int64_t lo = 0, hi = nseq;  // it is in [lo, hi)
+  while (hi - lo > 1) {
+    const int64_t step = (hi - lo + 31) / 32, i = lo + lane * step;
+    const bool below = i < hi && (i == 0 || min(max(cu[i], 0), total) / kDelta + i <= slot);
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, below) | 1u);
+    lo += last * step;
+    hi = min(hi, lo + step);
+  }
+  int a, b;
+  sequence_rows(cu, static_cast<int>(lo), total, a, b);
+  const int64_t c = slot - lo - a / kDelta;
+  if (c < 0 || c * kDelta >= b - a) return false;
+  row0 = a + static_cast<int>(c) * kDelta;
+  n = min(kDelta, b - row0);
+  return true;
+}
+
 constexpr int kColumns = 32;                       // columns of V of a chain's CTA
+__host__ __device__ inline int delta_tiles(int64_t V) { return static_cast<int>((V + kColumns - 1) / kColumns); }
 constexpr int kTermRow = kColumns * 2;             // bytes of a row of one term: 64-byte swizzle
 
 // Descriptor of terms of `kColumns` columns, rows as the contraction; `panel` bytes between terms.
@@ -102,6 +124,48 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
                : "memory");
 }
 
+// The chains' CTAs.
+constexpr int kChainThreads = 384;  // 4 warps that move and multiply, 8 that own rows
+constexpr int kRowWarps = 8;
+// a slot of the ring, from a 1024-byte boundary
+constexpr int kStageKq = 2 * kPanelBytes;               // panels of 64 rows of K over 64 of Q
+constexpr int kStageBytes = kStageKq + kRecordBytes;
+constexpr int kStages = 2;
+constexpr int kStatePanel = 128 * kTermRow, kTokenPanel = kDelta * kTermRow;  // one term
+
+#define DELTA_WAIT(bar, phase) (wait_phase((bar), static_cast<uint32_t>(phase) & 1u))
+#define DELTA_WARP_WAIT(bar, phase) (__all_sync(0xffffffffu, DELTA_WAIT(bar, phase)))
+
+// The sum of the three terms' products, 16 columns of this thread's row.
+__device__ __forceinline__ void load_sum(uint32_t at, float* x) {
+  uint32_t a[16], b[16], c[16];
+  tmem_ld16(at, a);
+  tmem_ld16(at + kColumns, b);
+  tmem_ld16(at + 2 * kColumns, c);
+  tmem_wait_ld();
+  tmem_use16(a);
+  tmem_use16(b);
+  tmem_use16(c);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(a[i]) + (__uint_as_float(b[i]) + __uint_as_float(c[i]));
+}
+
+__device__ __forceinline__ void load_bf16x16(const uint16_t* src, int width, bool on, uint4 (&x)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (on && 8 * i < width) x[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
+  }
+}
+__device__ __forceinline__ void unpack16(const uint4 (&x)[2], float* y) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cconv::f2_unpack(bf16x2_to_f2(w[j]), y[8 * i + 2 * j], y[8 * i + 2 * j + 1]);
+  }
+}
+
 struct DeltaCall {
   Rows q, k, v, d_o;
   Gates g, beta;          // (beta's values are taken as they are)
@@ -115,9 +179,19 @@ struct DeltaCall {
   float* fin;
   uint16_t* o;
   uint8_t* records;       // [slots][Hv] of kRecordBytes
+  // the gradient's
+  float* z;               // [total][Hv][V]
+  uint8_t *heads, *ends;  // [slots][Hv][tiles] first terms of S_0 and of D
+  float *odots, *vdots, *bdots;  // [2 tiles][Hv][total] parts of o . do, v . dv and dbeta
+  uint16_t *dq, *dk, *dv;
+  float *dg, *dbeta, *dinit;
 };
 
 int launch_delta_prep(const DeltaCall& c, cudaStream_t stream);
 int launch_delta_fwd(const DeltaCall& c, cudaStream_t stream);
+int launch_delta_states(const DeltaCall& c, cudaStream_t stream);  // the gradient's chain of states
+int launch_delta_back(const DeltaCall& c, cudaStream_t stream);    // its chain backwards
+int launch_delta_grads(const DeltaCall& c, cudaStream_t stream);   // dq and dk
+int launch_delta_gates(const DeltaCall& c, cudaStream_t stream);   // dg and dbeta
 
 }  // namespace cattn

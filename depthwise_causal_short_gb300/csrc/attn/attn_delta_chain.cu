@@ -7,6 +7,9 @@
 //   [K; Q] S          -> r = v - ef . (K S),  X = beta r;   ef . (Q S)
 //   [J; P~] X         -> z = r + J X,  u = beta z;          o = scale (ef . (Q S) + P~ X)
 //   K^T (eb . u)      -> S = total S + ..
+// The gradient runs the same chain first (BWD): it leaves z, the first term of every S_0 and o . do in
+// place of o.  Its own chain, from the last chunk to the first, is attn_delta_back.cu.
+//
 // The three terms of S, X and eb . u lie side by side as columns of one operand (N = 96), and their
 // products are added up in registers: A is read once for all three.
 //
@@ -29,13 +32,7 @@ static int read_fault(unsigned* out) {
 }
 static FaultReader reader(read_fault);
 
-constexpr int kChainThreads = 384;  // 4 warps that move and multiply, 8 that own rows
-constexpr int kRowWarps = 8;
 // shared memory, from a 1024-byte boundary
-constexpr int kStageKq = 2 * kPanelBytes;               // panels of 64 rows of K over 64 of Q
-constexpr int kStageBytes = kStageKq + kRecordBytes;
-constexpr int kStages = 2;
-constexpr int kStatePanel = 128 * kTermRow, kTokenPanel = kDelta * kTermRow;  // one term
 constexpr int kOffState = kStages * kStageBytes;
 constexpr int kOffX = kOffState + kTerms * kStatePanel;  // X, then eb . u
 constexpr int kOffChainBars = kOffX + kTerms * kTokenPanel;
@@ -44,7 +41,7 @@ static_assert(kChainBytes <= 232448, "shared memory of one CTA");
 
 struct ChainArgs {
   CUtensorMap mq, mk;
-  Rows v;
+  Rows v, d_o;
   const int32_t* cu;
   Slots slots;
   int32_t* status;
@@ -52,6 +49,9 @@ struct ChainArgs {
   float* fin;
   uint16_t* o;
   const uint8_t* records;
+  float* z;        // [total][Hv][V]
+  uint8_t* heads;  // [slots][Hv][tiles] first terms of S_0
+  float* dots;     // [2 tiles][Hv][total] parts of o . do
   float scale;
   int total, nseq, ratio, Hv, K, V, tiles, checked;
 };
@@ -91,39 +91,7 @@ __device__ __forceinline__ ChainPlace chain_place(const ChainArgs& p, int lane) 
   return w;
 }
 
-#define DELTA_WAIT(bar, phase) (wait_phase((bar), static_cast<uint32_t>(phase) & 1u))
-#define DELTA_WARP_WAIT(bar, phase) (__all_sync(0xffffffffu, DELTA_WAIT(bar, phase)))
-
-// The sum of the three terms' products, 16 columns of this thread's row.
-__device__ __forceinline__ void load_sum(uint32_t at, float* x) {
-  uint32_t a[16], b[16], c[16];
-  tmem_ld16(at, a);
-  tmem_ld16(at + kColumns, b);
-  tmem_ld16(at + 2 * kColumns, c);
-  tmem_wait_ld();
-  tmem_use16(a);
-  tmem_use16(b);
-  tmem_use16(c);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(a[i]) + (__uint_as_float(b[i]) + __uint_as_float(c[i]));
-}
-
-__device__ __forceinline__ void load_bf16x16(const uint16_t* src, int width, bool on, uint4 (&x)[2]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (on && 8 * i < width) x[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
-  }
-}
-__device__ __forceinline__ void unpack16(const uint4 (&x)[2], float* y) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) cconv::f2_unpack(bf16x2_to_f2(w[j]), y[8 * i + 2 * j], y[8 * i + 2 * j + 1]);
-  }
-}
-
+template <bool BWD>
 __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(const __grid_constant__ ChainArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -131,6 +99,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
   const uint32_t full = smem + kOffChainBars, empty = full + 8 * kStages;
   const uint32_t sready = empty + 8 * kStages, xready = sready + 8, uready = xready + 8;
   const uint32_t acc1 = uready + 8, acc2 = acc1 + 8, acc3 = acc2 + 8, alldone = acc3 + 8;
+  const uint32_t kept = alldone + 8;
   __shared__ uint32_t tmem_at;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
@@ -145,6 +114,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
     bar_init(acc2, 1);
     bar_init(acc3, 1);
     bar_init(alldone, 1);
+    bar_init(kept, 1);
     cconv::fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&tmem_at, 256);
@@ -156,7 +126,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
   cconv::grid_launch_dependents();
   const ChainPlace w = chain_place(p, lane);
   const int chunks = (w.b - w.a + kDelta - 1) / kDelta;
-  const bool keep = p.fin != nullptr && w.write;  // the state after the last chunk is needed
+  const bool keep = !BWD && p.fin != nullptr && w.write;  // the state after the last chunk is needed
   const int col0 = w.tile * kColumns;
   bool ok = true;
 
@@ -222,6 +192,20 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
       mma_commit(alldone);
       drain(alldone, 1);
     }
+  } else if (BWD && warp == 2) {
+    // ---- the first term of every S_0 ----
+    if (elect_one()) {
+      const int64_t slot0 = w.a / kDelta + w.seq;
+      for (int c = 0; c < chunks && ok; ++c) {
+        if (!(ok = DELTA_WAIT(sready, c))) break;
+        bulk_store(p.heads + (((slot0 + c) * p.Hv + w.hv) * p.tiles + w.tile) * kStatePanel, smem + kOffState,
+                   kStatePanel);
+        stores_commit();
+        stores_wait_read();
+        bar_arrive(kept);
+      }
+      stores_wait();
+    }
   } else if (warp >= 4) {
     // ---- rows ----
     const int quarter = warp % 4, cg = warp / 4 - 1;     // lanes of TMEM, column group
@@ -245,9 +229,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
     cconv::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) bar_arrive(sready);
-    const uint16_t* v_at = p.v.p + w.hv * p.v.sh + col;
+    const Rows from = key ? p.v : p.d_o;  // rows of v, or (BWD) of do
+    const uint16_t* v_at = from.p + w.hv * from.sh + col;
     uint4 vraw[2];
-    if (key) load_bf16x16(v_at + static_cast<int64_t>(w.a + t) * p.v.st, width, t < w.b - w.a, vraw);
+    if (key || BWD) load_bf16x16(v_at + static_cast<int64_t>(w.a + t) * from.st, width, t < w.b - w.a, vraw);
     for (int c = 0; c < chunks; ++c) {
       const int st = c % kStages, row0 = w.a + c * kDelta, n = min(kDelta, w.b - row0);
       const float* gates = reinterpret_cast<const float*>(base + st * kStageBytes + kStageKq + kTerms * kJpTerm);
@@ -280,22 +265,41 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
       tc_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(xready);
-      if (key && c + 1 < chunks)
-        load_bf16x16(v_at + static_cast<int64_t>(row0 + kDelta + t) * p.v.st, width, row0 + kDelta + t < w.b, vraw);
+      uint4 doraw[2] = {vraw[0], vraw[1]};
+      if ((key || BWD) && c + 1 < chunks)
+        load_bf16x16(v_at + static_cast<int64_t>(row0 + kDelta + t) * from.st, width, row0 + kDelta + t < w.b, vraw);
       if (!(ok = DELTA_WARP_WAIT(acc2, c))) break;
       tc_fence_after();
       load_sum(tmem2 + mine, y);
       if (key) {
         const float f = eb * beta;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = t < n ? f * (r[i] + y[i]) : 0.f;
+        for (int i = 0; i < 16; ++i) {
+          r[i] += y[i];
+          y[i] = t < n ? f * r[i] : 0.f;
+        }
         put_terms(smem + kOffX, kTokenPanel, t, cg, y);
         cconv::fence_proxy_async_smem();
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(uready);
-      if (!key && t < n) {
+      if (BWD && t < n) {
+        if (key) {
+          float* dst = p.z + (static_cast<int64_t>(row0 + t) * p.Hv + w.hv) * p.V + col;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (4 * i < width)
+              *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+        } else {
+          float d[16], sum = 0.f;
+          unpack16(doraw, d);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum = fmaf(d[i], r[i] + y[i], sum);
+          p.dots[(static_cast<int64_t>(w.tile * 2 + cg) * p.Hv + w.hv) * p.total + row0 + t] = p.scale * sum;
+        }
+      }
+      if (!BWD && !key && t < n) {
         uint16_t* dst = p.o + (static_cast<int64_t>(row0 + t) * p.Hv + w.hv) * p.V + col;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -314,6 +318,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
 #pragma unroll
         for (int i = 0; i < 16; ++i) S[i] = row < p.K ? fmaf(total, S[i], y[i]) : 0.f;
         if (c + 1 < chunks) {
+          if (BWD && !(ok = DELTA_WARP_WAIT(kept, c))) break;
           put_terms(smem + kOffState, kStatePanel, row, cg, S);
           cconv::fence_proxy_async_smem();
           tc_fence_before();
@@ -340,7 +345,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
   }
 }
 
-int launch_delta_fwd(const DeltaCall& c, cudaStream_t stream) {
+template <bool BWD>
+static int launch_chain(const DeltaCall& c, cudaStream_t stream) {
   ChainArgs a{};
   int rc = CCONV_OK;
   if (c.s.total > 0) {
@@ -349,21 +355,26 @@ int launch_delta_fwd(const DeltaCall& c, cudaStream_t stream) {
     if (rc == CCONV_OK) rc = encode_tile_map(&a.mk, c.k, c.s.total, c.s.Hk, c.s.K, kDelta);
     if (rc != CCONV_OK) return rc;
   }
-  a.v = c.v;
+  a.v = c.v, a.d_o = c.d_o;
   a.cu = c.cu, a.slots = c.slots, a.status = c.status, a.checked = c.checked;
   a.initial = c.initial, a.fin = c.fin;
   a.o = c.o;
   a.records = c.records;
+  a.z = c.z, a.heads = c.heads, a.dots = c.odots;
   a.scale = c.scale;
   a.total = c.s.total, a.nseq = c.s.nseq, a.ratio = c.s.Hv / c.s.Hk, a.Hv = c.s.Hv, a.K = c.s.K, a.V = c.s.V;
-  a.tiles = (c.s.V + kColumns - 1) / kColumns;
+  a.tiles = delta_tiles(c.s.V);
+  auto kern = cattn_delta_chain_kernel<BWD>;
   const int64_t ctas = static_cast<int64_t>(c.s.nseq) * c.s.Hv * a.tiles;
-  if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(cattn_delta_chain_kernel), kChainBytes) != CCONV_OK)
+  if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(kern), kChainBytes) != CCONV_OK)
     return CCONV_ERR_CUDA;
-  return launch_pdl(cattn_delta_chain_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kChainThreads), kChainBytes,
-                    stream, a) == cudaSuccess
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kChainThreads), kChainBytes, stream, a) ==
+                 cudaSuccess
              ? CCONV_OK
              : CCONV_ERR_CUDA;
 }
+
+int launch_delta_fwd(const DeltaCall& c, cudaStream_t stream) { return launch_chain<false>(c, stream); }
+int launch_delta_states(const DeltaCall& c, cudaStream_t stream) { return launch_chain<true>(c, stream); }
 
 }  // namespace cattn

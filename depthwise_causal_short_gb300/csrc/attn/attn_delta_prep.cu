@@ -38,27 +38,6 @@ struct PrepArgs {
   int total, nseq, ratio, Hv, K;
 };
 
-// The sequence and rows of record slot `slot` (rows [row0, row0 + n)); false if it has none.
-__device__ __forceinline__ bool find_chunk(const int32_t* cu, int nseq, int total, int64_t slot, int lane,
-                                           int& row0, int& n) {
-  // the last sequence whose first slot is not above `slot`, 32 candidates at a time
-  int64_t lo = 0, hi = nseq;  // it is in [lo, hi)
-  while (hi - lo > 1) {
-    const int64_t step = (hi - lo + 31) / 32, i = lo + lane * step;
-    const bool below = i < hi && (i == 0 || min(max(cu[i], 0), total) / kDelta + i <= slot);
-    const int last = 31 - __clz(__ballot_sync(0xffffffffu, below) | 1u);
-    lo += last * step;
-    hi = min(hi, lo + step);
-  }
-  int a, b;
-  sequence_rows(cu, static_cast<int>(lo), total, a, b);
-  const int64_t c = slot - lo - a / kDelta;
-  if (c < 0 || c * kDelta >= b - a) return false;
-  row0 = a + static_cast<int>(c) * kDelta;
-  n = min(kDelta, b - row0);
-  return true;
-}
-
 __global__ void __launch_bounds__(kPrepThreads) cattn_delta_prep_kernel(const __grid_constant__ PrepArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));

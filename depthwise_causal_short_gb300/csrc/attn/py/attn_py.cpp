@@ -612,10 +612,12 @@ PyObject* sequence_fwd(PyObject* const* a, Py_ssize_t count) {
 }
 
 // q, k, v, g, scale, do, cu_seqlens, initial_state, state_indices, status, want_dinit (or None), dq, dk, dv,
-// dg, d_initial_state, workspace, stream
-PyObject* linear_bwd(PyObject* const* a, Py_ssize_t count) {
-  ARGS(18);
+// dg, d_initial_state, workspace, stream; of the delta rule: beta, dbeta
+template <bool DELTA>
+PyObject* sequence_bwd(PyObject* const* a, Py_ssize_t count) {
+  ARGS(DELTA ? 20 : 18);
   const Linear n = linear_args(a);
+  const Arg beta = DELTA ? beta_arg(a[18], n) : none, dbeta = DELTA ? optional(a[19], "dbeta") : none;
   const Arg dout = tensor(a[5], "do"), cu = tensor(a[6], "cu_seqlens"), init = optional(a[7], "initial_state"),
             idx = optional(a[8], "state_indices"), status = idx.given() ? optional(a[9], "status") : Arg{"status", nullptr},
             dq = optional(a[11], "dq"), dk = optional(a[12], "dk"), dv = optional(a[13], "dv"), dg = optional(a[14], "dg"),
@@ -642,26 +644,39 @@ PyObject* linear_bwd(PyObject* const* a, Py_ssize_t count) {
   if (dk.given()) check_exact(dk, n.q.t->sizes(), at::kBFloat16);
   if (dv.given()) check_exact(dv, n.v.t->sizes(), at::kBFloat16);
   if (dg.given()) check_exact(dg, {n.rows, n.Hv}, at::kFloat);
+  if (dbeta.given()) check_exact(dbeta, {n.rows, n.Hv}, at::kFloat);
   if (ds.given()) check_exact(ds, {nseq, n.Hv, n.K, n.V}, at::kFloat);
   if (ws.given() && !ws.t->is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
-  check_disjoint({&dq, &dk, &dv, &dg, &ds, &status, &ws}, {&n.q, &n.k, &n.v, &n.g, &dout, &cu, &init, &idx});
-  const auto dev = check_device({&n.q, &n.k, &n.v, &n.g, &dout, &cu, &init, &idx, &status, &dq, &dk, &dv, &dg, &ds, &ws});
+  check_disjoint({&dq, &dk, &dv, &dg, &dbeta, &ds, &status, &ws},
+                 {&n.q, &n.k, &n.v, &n.g, &beta, &dout, &cu, &init, &idx});
+  const auto dev = check_device({&n.q, &n.k, &n.v, &n.g, &beta, &dout, &cu, &init, &idx, &status, &dq, &dk, &dv, &dg,
+                                 &dbeta, &ds, &ws});
   const Place place(a[17], dev);
-  at::Tensor oq, ok, ov, og, os;
+  at::Tensor oq, ok, ov, og, ob, os;
   place.out_or_new(dq, oq, n.q.t->sizes(), at::kBFloat16);
   place.out_or_new(dk, ok, n.q.t->sizes(), at::kBFloat16);
   place.out_or_new(dv, ov, n.v.t->sizes(), at::kBFloat16);
   place.out_or_new(dg, og, {n.rows, n.Hv}, at::kFloat);
+  if (DELTA) place.out_or_new(dbeta, ob, {n.rows, n.Hv}, at::kFloat);
   if (want) place.out_or_new(ds, os, {nseq, n.Hv, n.K, n.V}, at::kFloat);
-  const at::Tensor work = workspace_of(ws, cattn_linear_bwd_workspace_bytes, "cattn_linear_bwd_workspace_bytes", n, nseq, place);
+  const at::Tensor work =
+      DELTA ? workspace_of(ws, cattn_delta_bwd_workspace_bytes, "cattn_delta_bwd_workspace_bytes", n, nseq, place)
+            : workspace_of(ws, cattn_linear_bwd_workspace_bytes, "cattn_linear_bwd_workspace_bytes", n, nseq, place);
   const at::Tensor& d = *dout.t;
-  check_rc(cattn_linear_bwd(QKVG(n), d.data_ptr(), d.stride(0), d.stride(1), n.rows, n.Hk, n.Hv, n.K, n.V,
-                            static_cast<const int32_t*>(cu.ptr()), nseq, n.scale, static_cast<const float*>(init.ptr()),
-                            static_cast<const int32_t*>(idx.ptr()), S, static_cast<int32_t*>(status.out()),
-                            oq.data_ptr(), ok.data_ptr(), ov.data_ptr(), static_cast<float*>(og.data_ptr()),
-                            os.defined() ? static_cast<float*>(os.data_ptr()) : nullptr, work.data_ptr(),
-                            work.nbytes(), place.handle()),
-           "cattn_linear_bwd");
+  float* dstates = os.defined() ? static_cast<float*>(os.data_ptr()) : nullptr;
+#define MIDDLE                                                                                               \
+  d.data_ptr(), d.stride(0), d.stride(1), n.rows, n.Hk, n.Hv, n.K, n.V, static_cast<const int32_t*>(cu.ptr()), \
+      nseq, n.scale, static_cast<const float*>(init.ptr()), static_cast<const int32_t*>(idx.ptr()), S,       \
+      static_cast<int32_t*>(status.out()), oq.data_ptr(), ok.data_ptr(), ov.data_ptr(),                      \
+      static_cast<float*>(og.data_ptr())
+#define TAIL dstates, work.data_ptr(), work.nbytes(), place.handle()
+  if constexpr (DELTA) {
+    check_rc(cattn_delta_bwd(QKVG(n), BETA(beta), MIDDLE, static_cast<float*>(ob.data_ptr()), TAIL), "cattn_delta_bwd");
+    return tuple({&oq, &ok, &ov, &og, &ob, &os});
+  }
+  check_rc(cattn_linear_bwd(QKVG(n), MIDDLE, TAIL), "cattn_linear_bwd");
+#undef MIDDLE
+#undef TAIL
   return tuple({&oq, &ok, &ov, &og, &os});
 }
 
@@ -717,12 +732,13 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 }
 
 constexpr auto linear_fwd = sequence_fwd<false>, delta_fwd = sequence_fwd<true>;
+constexpr auto linear_bwd = sequence_bwd<false>, delta_bwd = sequence_bwd<true>;
 constexpr auto linear_update = token_update<false>, delta_update = token_update<true>;
 
 #define METHOD(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(entry<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(qknorm_fwd), METHOD(qknorm_bwd), METHOD(linear_fwd), METHOD(linear_bwd),
-                         METHOD(linear_update), METHOD(delta_fwd), METHOD(delta_update), METHOD(layernorm_fwd), METHOD(layernorm_bwd), {"set_error", set_error, METH_O, nullptr},
+                         METHOD(linear_update), METHOD(delta_fwd), METHOD(delta_bwd), METHOD(delta_update), METHOD(layernorm_fwd), METHOD(layernorm_bwd), {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_cattn", nullptr, -1, methods};
 

@@ -185,8 +185,10 @@ CCONV_API int cattn_linear_update(const void* q, int64_t sqt, int64_t sqh, const
                                   const int32_t* state_indices, int pad_rows, void* o,
                                   int32_t* status_dev, cconv_stream_t stream);
 
-/* Workspace cattn_delta_fwd needs (at a 16-byte boundary). */
+/* Workspace cattn_delta_fwd / cattn_delta_bwd need (16-byte aligned). */
 CCONV_API int cattn_delta_fwd_workspace_bytes(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv,
+                                              int64_t K, int64_t V, size_t* bytes);
+CCONV_API int cattn_delta_bwd_workspace_bytes(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv,
                                               int64_t K, int64_t V, size_t* bytes);
 
 /*
@@ -209,6 +211,23 @@ CCONV_API int cattn_delta_fwd(const void* q, int64_t sqt, int64_t sqh, const voi
                               const int32_t* cu_seqlens, int64_t nseq, float scale,
                               const float* initial_state, float* final_state,
                               const int32_t* state_indices, int64_t S, int32_t* status_dev, void* o,
+                              void* workspace, size_t workspace_bytes, cconv_stream_t stream);
+
+/*
+ * cattn_delta_bwd -- its gradient: dq, dk, dv, dg, dbeta and the gradient of the initial states.
+ * Everything else is recomputed.  The final states count as constants (no gradient flows in).
+ *
+ *   do_ .. status_dev, dq .. d_initial_state   as in cattn_linear_bwd.
+ *   dbeta     [total, Hv] fp32 contiguous output, 16-byte aligned.
+ */
+CCONV_API int cattn_delta_bwd(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt,
+                              int64_t skh, const void* v, int64_t svt, int64_t svh, const float* g,
+                              int64_t sgt, int64_t sgh, const float* beta, int64_t sbt, int64_t sbh,
+                              const void* do_, int64_t sot, int64_t soh, int64_t total, int64_t Hk,
+                              int64_t Hv, int64_t K, int64_t V, const int32_t* cu_seqlens,
+                              int64_t nseq, float scale, const float* initial_state,
+                              const int32_t* state_indices, int64_t S, int32_t* status_dev, void* dq,
+                              void* dk, void* dv, float* dg, float* dbeta, float* d_initial_state,
                               void* workspace, size_t workspace_bytes, cconv_stream_t stream);
 
 /*

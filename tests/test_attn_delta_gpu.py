@@ -1,10 +1,17 @@
-"""cattn_delta_fwd / _update against the definition in 64 bits (GPU).
+"""cattn_delta_fwd / _bwd / _update against the definition in 64 bits (GPU).
 
 Tolerances, as max |error| / max |reference|:
   o              4e-3: the store's rounding (2^-8 of an element); the products keep 24 bits of every
                  factor, and of P~ and the state too
   fp32 states    5e-6: products split so that 2^-24 of each is kept, fp32 sums of up to 64 + 128
                  values; errors of earlier chunks decay with the state
+  dv             4e-3: the store's rounding of a sum that keeps 24 bits
+  dq, dk         8e-3: the store rounds by up to 2^-8 (3.9e-3); the matrix operands that are not
+                 inputs (decayed pairs, the states) are rounded too, with independent errors: as for
+                 the linear attention's gradients
+  dg, dbeta      2e-5: fp32 sums of products that keep 24 bits, over up to 128 + 256 channels and
+                 64 tokens; dg is summed up over the tokens behind it, where parts of both signs
+                 cancel down to a tenth
 """
 import pytest
 import torch
@@ -17,6 +24,8 @@ from tests.helpers import rel_err
 pytestmark = pytest.mark.gpu
 O_TOL = 4e-3
 STATE_TOL = 5e-6
+GRAD_TOL = 8e-3
+DG_TOL = 2e-5
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -58,18 +67,31 @@ def _check(a, b, tol, what):
 @pytest.mark.parametrize("states", [False, True])
 def test_parity(lens, Hk, Hv, K, V, states):
     q, k, v, g, beta, do, s0 = plain.delta_inputs(lens, Hk, Hv, K, V, seed=sum(lens) + K)
-    o, fin = plain.delta(*[t.double() for t in (q, k, v, g, beta)], cu_of(lens), K ** -0.5,
-                         s0.double() if states else None)
+    leaves = [t.double().requires_grad_() for t in (q, k, v, g, beta, s0)]
+    o, fin = plain.delta(*leaves[:5], cu_of(lens), K ** -0.5, leaves[5] if states else None)
     args = [t.cuda() for t in (q, k, v, g, beta)]
     cu = _cu(lens)
     init = s0.cuda() if states else None
     go, gfin, status = cc.cattn_delta_fwd(*args, cu, initial_state=init, final_state=True)
     assert status is None
-    _check(gfin, fin, STATE_TOL, "final state")
+    _check(gfin, fin.detach(), STATE_TOL, "final state")
     if sum(lens):
-        _check(go, o, O_TOL, "o")
+        _check(go, o.detach(), O_TOL, "o")
     alone, none, _ = cc.cattn_delta_fwd(*args, cu, initial_state=init)
     assert none is None and torch.equal(alone, go)
+
+    grads = cc.cattn_delta_bwd(*args, do.cuda(), cu, initial_state=init)
+    again = cc.cattn_delta_bwd(*args, do.cuda(), cu, initial_state=init)
+    for a, b in zip(grads, again):
+        assert (a is None and b is None) or torch.equal(a, b)  # a fixed order
+    if not sum(lens):
+        assert not states or not grads[5].any()
+        return
+    want = torch.autograd.grad(o, leaves if states else leaves[:5], do.double(), allow_unused=True)
+    for name, tol, a, b in zip(("dq", "dk", "dv", "dg", "dbeta"), (GRAD_TOL, GRAD_TOL, O_TOL, DG_TOL, DG_TOL), grads, want):
+        _check(a, b, tol, name)
+    if states:
+        _check(grads[5], want[5], STATE_TOL, "d_initial_state")
 
 
 @pytest.mark.parametrize("kind", ["beta_zero", "beta_two", "forget", "keep", "same_keys", "no_decay"])
