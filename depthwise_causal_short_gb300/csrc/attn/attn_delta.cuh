@@ -124,14 +124,19 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
                : "memory");
 }
 
-// The chains' CTAs.
-constexpr int kChainThreads = 384;  // 4 warps that move and multiply, 8 that own rows
-constexpr int kRowWarps = 8;
-// a slot of the ring, from a 1024-byte boundary
-constexpr int kStageKq = 2 * kPanelBytes;               // panels of 64 rows of K over 64 of Q
-constexpr int kStageBytes = kStageKq + kRecordBytes;
+// The chains' CTAs: 4 warps that move and multiply, 8 that own rows of the state and of the tokens,
+// 4 that copy first operands to tensor memory and do what the chain does not wait for.
+constexpr int kChainThreads = 512;
+constexpr int kRowWarps = 8, kCopyWarps = 4;
+// the rings: slots of K and Q, then of records, from a 1024-byte boundary
 constexpr int kStages = 2;
+constexpr int kStageKq = 2 * kPanelBytes;               // panels of 64 rows of K over 64 of Q
+constexpr int kOffRecords = kStages * kStageKq;
+constexpr int kRingBytes = kOffRecords + kStages * kRecordBytes;
 constexpr int kStatePanel = 128 * kTermRow, kTokenPanel = kDelta * kTermRow;  // one term
+constexpr int kUTile = 2 * kTokenPanel;                 // two terms of u of a chunk, 32 columns
+// columns of tensor memory
+constexpr int kTmK = 0, kTmJ = 64, kTmAcc1 = 160, kTmAcc2 = 256, kTmOut1 = 320, kTmOut2 = 384;
 
 #define DELTA_WAIT(bar, phase) (wait_phase((bar), static_cast<uint32_t>(phase) & 1u))
 #define DELTA_WARP_WAIT(bar, phase) (__all_sync(0xffffffffu, DELTA_WAIT(bar, phase)))
@@ -150,19 +155,82 @@ __device__ __forceinline__ void load_sum(uint32_t at, float* x) {
   for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(a[i]) + (__uint_as_float(b[i]) + __uint_as_float(c[i]));
 }
 
-__device__ __forceinline__ void load_bf16x16(const uint16_t* src, int width, bool on, uint4 (&x)[2]) {
+// Eight columns of products whose accumulators lie in two groups of kColumns: the first terms', and
+// the small ones'.
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_use8(uint32_t* r) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (on && 8 * i < width) x[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
+  for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ void load_sum8(uint32_t at, float* x) {
+  uint32_t a[8], b[8];
+  tmem_ld8(at, a);
+  tmem_ld8(at + kColumns, b);
+  tmem_wait_ld();
+  tmem_use8(a);
+  tmem_use8(b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
+}
+__device__ __forceinline__ void put_terms8(uint32_t base, uint32_t panel, int row, int piece, const float* x) {
+  uint4 t[kTerms];
+  split8(x, t);
+  const uint32_t at = base + term_piece(row, piece);
+#pragma unroll
+  for (int s = 0; s < kTerms; ++s) sts128(at + s * panel, t[s].x, t[s].y, t[s].z, t[s].w);
+}
+__device__ __forceinline__ void unpack8(const uint4& x, float* y) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) cconv::f2_unpack(bf16x2_to_f2(w[j]), y[2 * j], y[2 * j + 1]);
+}
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(f2_to_bf16x2(f2_pack(x[0], x[1])), f2_to_bf16x2(f2_pack(x[2], x[3])),
+                    f2_to_bf16x2(f2_pack(x[4], x[5])), f2_to_bf16x2(f2_pack(x[6], x[7])));
+}
+
+// Row `row` of a 64-column panel (128 bytes, swizzled) to 32 columns of tensor memory; zeros unless `on`.
+__device__ __forceinline__ void copy_row(uint32_t tmem, uint32_t panel, int row, bool on) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (on) x = lds128_at(panel + swizzled(row, h * 4 + j));
+      w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
+    }
+    tmem_st16(tmem + 16 * h, w);
   }
 }
-__device__ __forceinline__ void unpack16(const uint4 (&x)[2], float* y) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) cconv::f2_unpack(bf16x2_to_f2(w[j]), y[8 * i + 2 * j], y[8 * i + 2 * j + 1]);
+
+// One chunk's K and Q (a box of 64 channels and 64 tokens each, `panels` of them) and its record.
+__device__ __forceinline__ void load_kq(uint32_t smem, uint32_t bar, const CUtensorMap* mk, const CUtensorMap* mq,
+                                        int st, int panels, int hk, int row0) {
+  bar_expect(bar, panels * 2 * kSideBytes);
+#pragma unroll 1
+  for (int j = 0; j < panels; ++j) {
+    load_box(smem + st * kStageKq + j * kPanelBytes, mk, bar, j * kPanelCols, hk, row0);
+    load_box(smem + st * kStageKq + j * kPanelBytes + kSideBytes, mq, bar, j * kPanelCols, hk, row0);
+  }
+}
+__device__ __forceinline__ void load_record(uint32_t smem, uint32_t bar, const uint8_t* record, int st) {
+  bar_expect(bar, kRecordBytes);
+  bulk_load(smem + kOffRecords + st * kRecordBytes, record, kRecordBytes, bar);
+}
+
+// A (rows of tensor memory at `a`, one term) times three terms of B side by side: the first two as 64
+// columns, the third one into the small ones' group.  `steps` of 16 rows of B.
+__device__ __forceinline__ void mma_terms(uint32_t acc, uint32_t a, uint64_t b, uint32_t panel, int steps) {
+  const uint32_t two = mma_desc(2 * kColumns, false, true), one = mma_desc(kColumns, false, true);
+#pragma unroll 1
+  for (int j = 0; j < steps; ++j) {
+    mma_ts(acc, a + j * 8, b + j * kTermStep, two, j > 0);
+    mma_ts(acc + kColumns, a + j * 8, b + (2 * panel >> 4) + j * kTermStep, one, true);
   }
 }
 
@@ -181,17 +249,19 @@ struct DeltaCall {
   uint8_t* records;       // [slots][Hv] of kRecordBytes
   // the gradient's
   float* z;               // [total][Hv][V]
+  uint8_t* u;             // [slots][Hv][tiles] two terms of u
   uint8_t *heads, *ends;  // [slots][Hv][tiles] first terms of S_0 and of D
-  float *odots, *vdots, *bdots;  // [2 tiles][Hv][total] parts of o . do, v . dv and dbeta
+  float *odots, *vdots, *bdots;  // [tiles][Hv][total] parts of o . do, v . dv and dbeta
   uint16_t *dq, *dk, *dv;
   float *dg, *dbeta, *dinit;
+  double* sums;           // [Hv][slots] of the chunks' terms of dg
 };
 
 int launch_delta_prep(const DeltaCall& c, cudaStream_t stream);
 int launch_delta_fwd(const DeltaCall& c, cudaStream_t stream);
 int launch_delta_states(const DeltaCall& c, cudaStream_t stream);  // the gradient's chain of states
 int launch_delta_back(const DeltaCall& c, cudaStream_t stream);    // its chain backwards
-int launch_delta_grads(const DeltaCall& c, cudaStream_t stream);   // dq and dk
-int launch_delta_gates(const DeltaCall& c, cudaStream_t stream);   // dg and dbeta
+int launch_delta_grads(const DeltaCall& c, cudaStream_t stream);   // dq, dk, dbeta
+int launch_delta_gates(const DeltaCall& c, cudaStream_t stream);   // dg, from the chunks' parts
 
 }  // namespace cattn

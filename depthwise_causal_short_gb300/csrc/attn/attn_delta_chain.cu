@@ -1,17 +1,21 @@
 // attn_delta_chain.cu -- the gated delta rule's chain over the chunks of a sequence.
 //
 // A CTA owns 32 columns of V of one sequence and value head (the columns of a state never meet) and
-// goes through the chunks; the chunk's record (attn_delta_prep.cu) comes through a ring of two slots
-// together with its K and Q.  The state lives in registers in fp32, a row (channel of K) of 16 columns
-// a thread, and as three bf16 terms in shared memory.  Three products a chunk, each behind the last:
-//   [K; Q] S          -> r = v - ef . (K S),  X = beta r;   ef . (Q S)
-//   [J; P~] X         -> z = r + J X,  u = beta z;          o = scale (ef . (Q S) + P~ X)
-//   K^T (eb . u)      -> S = total S + ..
-// The gradient runs the same chain first (BWD): it leaves z, the first term of every S_0 and o . do in
-// place of o.  Its own chain, from the last chunk to the first, is attn_delta_back.cu.
-//
-// The three terms of S, X and eb . u lie side by side as columns of one operand (N = 96), and their
-// products are added up in registers: A is read once for all three.
+// goes through the chunks; a chunk's record (attn_delta_prep.cu) and its K and Q come through rings of two
+// slots.  The state lives in registers in fp32, a row (channel of K) of 16 columns a thread, and as three
+// bf16 terms in shared memory.  Three products a chunk, each behind the last:
+//   K S            -> r = v - ef . (K S),  X = beta r
+//   J X            -> z = r + J X,         u = beta z
+//   K^T (eb . u)   -> S = total S + ..
+// The three terms of S, X and eb . u lie side by side as columns of one operand, so that A is read once
+// for several; the terms' products are added up in registers.  K and J are first operands from tensor
+// memory (in shared memory they took 200 cycles a product of 128 x 96 x 16 beside the next chunk's loads),
+// copied there by four warps, and in lanes 64 to 127 once more: so all four quarters of the row warps have
+// tokens' results to read, 8 columns a thread, where two would have 16.
+// What the chain does not wait for, o = scale (ef . (Q S) + P~ X), fills the tensor cores while the rows
+// work, and goes out through the copying warps.
+// The gradient runs the same chain first (BWD): it leaves z, two terms of u, the first term of every S_0,
+// and o . do in place of o.  Its own chain, from the last chunk to the first, is attn_delta_back.cu.
 //
 // Bound by that chain: a product, its results to registers, the next operand to shared memory.
 #include <cudaTypedefs.h>
@@ -33,10 +37,11 @@ static int read_fault(unsigned* out) {
 static FaultReader reader(read_fault);
 
 // shared memory, from a 1024-byte boundary
-constexpr int kOffState = kStages * kStageBytes;
-constexpr int kOffX = kOffState + kTerms * kStatePanel;  // X, then eb . u
-constexpr int kOffChainBars = kOffX + kTerms * kTokenPanel;
-constexpr int kChainBytes = kOffChainBars + 16 * 8 + 1024;
+constexpr int kOffState = kRingBytes;
+constexpr int kOffX = kOffState + kTerms * kStatePanel;
+constexpr int kOffU = kOffX + kTerms * kTokenPanel;      // eb . u
+constexpr int kOffChainBars = kOffU + kTerms * kTokenPanel;
+constexpr int kChainBytes = kOffChainBars + 20 * 8 + 1024;
 static_assert(kChainBytes <= 232448, "shared memory of one CTA");
 
 struct ChainArgs {
@@ -51,7 +56,8 @@ struct ChainArgs {
   const uint8_t* records;
   float* z;        // [total][Hv][V]
   uint8_t* heads;  // [slots][Hv][tiles] first terms of S_0
-  float* dots;     // [2 tiles][Hv][total] parts of o . do
+  uint8_t* u;      // [slots][Hv][tiles] two terms of u
+  float* dots;     // [tiles][Hv][total] parts of o . do
   float scale;
   int total, nseq, ratio, Hv, K, V, tiles, checked;
 };
@@ -96,94 +102,126 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const uint32_t smem = smem_addr(base);
-  const uint32_t full = smem + kOffChainBars, empty = full + 8 * kStages;
-  const uint32_t sready = empty + 8 * kStages, xready = sready + 8, uready = xready + 8;
-  const uint32_t acc1 = uready + 8, acc2 = acc1 + 8, acc3 = acc2 + 8, alldone = acc3 + 8;
-  const uint32_t kept = alldone + 8;
+  const uint32_t kqfull = smem + kOffChainBars, recfull = kqfull + 8 * kStages, empty = recfull + 8 * kStages;
+  const uint32_t kready = empty + 8 * kStages, jready = kready + 8;                    // operands in tensor memory
+  const uint32_t sready = jready + 8, xready = sready + 8, uready = xready + 8;        // and in shared memory
+  const uint32_t acc1 = uready + 8, acc2 = acc1 + 8, acc3 = acc2 + 8, outs = acc3 + 8; // products
+  const uint32_t outfree = outs + 8, kept = outfree + 8, alldone = kept + 8;
   __shared__ uint32_t tmem_at;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      bar_init(full + 8 * i, 1);
-      bar_init(empty + 8 * i, 1 + kRowWarps);
+      bar_init(kqfull + 8 * i, 1);
+      bar_init(recfull + 8 * i, 1);
+      bar_init(empty + 8 * i, 1 + kRowWarps + kCopyWarps);
     }
+    bar_init(kready, kCopyWarps);
+    bar_init(jready, kCopyWarps);
     bar_init(sready, kRowWarps);
     bar_init(xready, kRowWarps);
     bar_init(uready, kRowWarps);
     bar_init(acc1, 1);
     bar_init(acc2, 1);
     bar_init(acc3, 1);
-    bar_init(alldone, 1);
+    bar_init(outs, 1);
+    bar_init(outfree, kCopyWarps);
     bar_init(kept, 1);
+    bar_init(alldone, 1);
     cconv::fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(&tmem_at, 256);
+  if (warp == 1) tmem_alloc(&tmem_at, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_at, tmem2 = tmem + 128;
+  const uint32_t tmem = tmem_at;
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
   const ChainPlace w = chain_place(p, lane);
   const int chunks = (w.b - w.a + kDelta - 1) / kDelta;
   const bool keep = !BWD && p.fin != nullptr && w.write;  // the state after the last chunk is needed
   const int col0 = w.tile * kColumns;
+  const int64_t slot0 = w.a / kDelta + w.seq;
+  const int panels = p.K > kPanelCols ? 2 : 1;
   bool ok = true;
 
   if (warp == 0) {
-    // ---- tiles and records ----
+    // ---- tiles and records: the next chunk's while this one's products wait for the rows ----
     if (elect_one()) {
-      const int panels = p.K > kPanelCols ? 2 : 1, hk = w.hv / p.ratio;
-      const int64_t slot0 = w.a / kDelta + w.seq;
-      int c = 0;
+      const int hk = w.hv / p.ratio;
+      int c = 0, part = 0;
       for (; c < chunks && ok; ++c) {
         const int st = c % kStages;
         if (c >= kStages && !(ok = DELTA_WAIT(empty + 8 * st, c / kStages - 1))) break;
-        const uint32_t at = smem + st * kStageBytes, bar = full + 8 * st;
-        bar_expect(bar, panels * 2 * kSideBytes + kRecordBytes);
-#pragma unroll 1
-        for (int i = 0; i < panels; ++i) {
-          load_box(at + i * kPanelBytes, &p.mk, bar, i * kPanelCols, hk, w.a + c * kDelta);
-          load_box(at + i * kPanelBytes + kSideBytes, &p.mq, bar, i * kPanelCols, hk, w.a + c * kDelta);
-        }
-        bulk_load(at + kStageKq, p.records + ((slot0 + c) * p.Hv + w.hv) * kRecordBytes, kRecordBytes, bar);
+        if (c > 0 && !(ok = DELTA_WAIT(acc1, c - 1))) break;
+        load_kq(smem, kqfull + 8 * st, &p.mk, &p.mq, st, panels, hk, w.a + c * kDelta);
+        part = 1;
+        if (c > 0 && !(ok = DELTA_WAIT(acc2, c - 1))) break;
+        load_record(smem, recfull + 8 * st, p.records + ((slot0 + c) * p.Hv + w.hv) * kRecordBytes, st);
+        part = 0;
       }
-      for (int st = 0; st < kStages; ++st) drain(full + 8 * st, (c - st + kStages - 1) / kStages);
+      for (int st = 0; st < kStages; ++st) {
+        drain(kqfull + 8 * st, (c + part - st + kStages - 1) / kStages);
+        drain(recfull + 8 * st, (c - st + kStages - 1) / kStages);
+      }
     }
   } else if (warp == 1) {
     // ---- products ----
     if (elect_one()) {
       const int ksteps = (p.K + 15) / 16;
       const uint64_t ds = term_desc(smem + kOffState, kStatePanel), dx = term_desc(smem + kOffX, kTokenPanel);
-      const uint32_t wide = mma_desc(3 * kColumns, false, true);
+      const uint64_t du = term_desc(smem + kOffU, kTokenPanel);
+      const uint32_t two = mma_desc(2 * kColumns, false, true), one = mma_desc(kColumns, false, true);
+      constexpr uint32_t kThirdS = 2 * kStatePanel / 16, kThirdX = 2 * kTokenPanel / 16;
       for (int c = 0; c < chunks && ok; ++c) {
         const int st = c % kStages;
-        const uint32_t at = smem + st * kStageBytes;
-        if (!(ok = DELTA_WAIT(full + 8 * st, c / kStages))) break;
+        const uint32_t kq = smem + st * kStageKq, rec = smem + kOffRecords + st * kRecordBytes;
+        if (!(ok = DELTA_WAIT(kready, c))) break;
         if (!(ok = DELTA_WAIT(sready, c))) break;
         tc_fence_after();
-        const uint64_t dkq = tile_desc(at, 0);
-#pragma unroll 1
-        for (int j = 0; j < ksteps; ++j) mma_ss(tmem, dkq + col_step(j), ds + j * kTermStep, wide, j > 0);
+        mma_terms(tmem + kTmAcc1, tmem + kTmK, ds, kStatePanel, ksteps);  // K S
         mma_commit(acc1);
+        if (c > 0 && !(ok = DELTA_WAIT(outfree, c - 1))) break;
+        tc_fence_after();
+        // Q S (lanes 64 to 127 of this and of P~ X, made of what follows in shared memory, are not read)
+        const uint64_t dq = tile_desc(kq + kSideBytes, 0);
+#pragma unroll 1
+        for (int j = 0; j < ksteps; ++j) {
+          mma_ss(tmem + kTmOut1, dq + col_step(j), ds + j * kTermStep, two, j > 0);
+          if (BWD) mma_ss(tmem + kTmOut1 + kColumns, dq + col_step(j), ds + kThirdS + j * kTermStep, one, true);
+        }
+        if (!(ok = DELTA_WAIT(jready, c))) break;
         if (!(ok = DELTA_WAIT(xready, c))) break;
         tc_fence_after();
+        // J X, terms down to 2^-16
+        mma_terms(tmem + kTmAcc2, tmem + kTmJ, dx, kTokenPanel, kDelta / 16);
 #pragma unroll 1
-        for (int i = 0; i < kTerms; ++i) {
-          const uint64_t da = tile_desc(at + kStageKq + i * kJpTerm, 0);
-          const uint32_t desc = mma_desc((kTerms - i) * kColumns, false, true);
-#pragma unroll 1
-          for (int j = 0; j < kDelta / 16; ++j)
-            mma_ss(tmem2, da + 2 * j, dx + j * kTermStep, desc, i + j > 0);
+        for (int j = 0; j < kDelta / 16; ++j) {
+          mma_ts(tmem + kTmAcc2, tmem + kTmJ + 32 + j * 8, dx + j * kTermStep, two, true);
+          mma_ts(tmem + kTmAcc2 + kColumns, tmem + kTmJ + 64 + j * 8, dx + j * kTermStep, one, true);
         }
         mma_commit(acc2);
+        // P~ X: with two terms o is as exact as its store; o . do takes all
+        const uint64_t dp = tile_desc(rec + kSideBytes, 0);
+        constexpr uint32_t kTerm = kJpTerm / 16;
+#pragma unroll 1
+        for (int j = 0; j < kDelta / 16; ++j) {
+          const uint64_t x = dx + j * kTermStep;
+          mma_ss(tmem + kTmOut2, dp + 2 * j, x, two, j > 0);
+          mma_ss(tmem + kTmOut2, dp + kTerm + 2 * j, x, BWD ? two : one, true);
+          if (BWD) {
+            mma_ss(tmem + kTmOut2 + kColumns, dp + 2 * j, x + kThirdX, one, true);
+            mma_ss(tmem + kTmOut2 + kColumns, dp + 2 * kTerm + 2 * j, x, one, true);
+          }
+        }
+        mma_commit(outs);
         if (!(ok = DELTA_WAIT(uready, c))) break;
         tc_fence_after();
         if (c + 1 < chunks || keep) {
-          const uint64_t da = tile_desc(at, kPanelBytes);
+          const uint64_t da = tile_desc(kq, kPanelBytes);  // K^T (eb . u)
           const uint32_t desc = mma_desc(3 * kColumns, true, true);
 #pragma unroll 1
-          for (int j = 0; j < kDelta / 16; ++j) mma_ss(tmem, da + j * kRowStep, dx + j * kTermStep, desc, j > 0);
+          for (int j = 0; j < kDelta / 16; ++j)
+            mma_ss(tmem + kTmAcc1, da + j * kRowStep, du + j * kTermStep, desc, j > 0);
           mma_commit(acc3);
         }
         mma_commit(empty + 8 * st);
@@ -195,7 +233,6 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
   } else if (BWD && warp == 2) {
     // ---- the first term of every S_0 ----
     if (elect_one()) {
-      const int64_t slot0 = w.a / kDelta + w.seq;
       for (int c = 0; c < chunks && ok; ++c) {
         if (!(ok = DELTA_WAIT(sready, c))) break;
         bulk_store(p.heads + (((slot0 + c) * p.Hv + w.hv) * p.tiles + w.tile) * kStatePanel, smem + kOffState,
@@ -206,14 +243,92 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
       }
       stores_wait();
     }
+  } else if (warp >= 12) {
+    // ---- copies to tensor memory, and the outputs ----
+    const int quarter = warp % 4, t = (quarter & 1) * 32 + lane;  // K and J twice, in lanes 0 and 64 on
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const Rows from = p.d_o;
+    const int width = p.V - col0;
+    for (int c = -1; c < chunks; ++c) {
+      const int next = c + 1, st = next % kStages;
+      if (next < chunks) {
+        const int n = min(kDelta, w.b - w.a - next * kDelta);
+        if (!(ok = DELTA_WARP_WAIT(kqfull + 8 * st, next / kStages))) break;
+        if (n < kDelta && t >= n && quarter < 2) {
+          // rows of the next sequence must not meet K^T (eb . u), where 0 * NaN is not 0
+          for (int k = 0; k < panels; ++k)
+            for (int i = 0; i < 8; ++i) sts128(smem + st * kStageKq + k * kPanelBytes + swizzled(t, i), 0, 0, 0, 0);
+        }
+        if (n < kDelta) cconv::fence_proxy_async_smem();
+        if (c >= 0 && !(ok = DELTA_WARP_WAIT(acc1, c))) break;
+        tc_fence_after();
+        for (int k = 0; k < panels; ++k)
+          copy_row(tmem + lanes + kTmK + 32 * k, smem + st * kStageKq + k * kPanelBytes, t, t < n);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(kready);
+      }
+      if (c >= 0) {
+      const int row0 = w.a + c * kDelta, here = c % kStages;
+      const bool on = quarter < 2 && row0 + t < w.b;
+      uint4 in[4];
+      if (BWD)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          in[i] = make_uint4(0, 0, 0, 0);
+          if (on && 8 * i < width)
+            in[i] = *reinterpret_cast<const uint4*>(from.p + static_cast<int64_t>(row0 + t) * from.st + w.hv * from.sh +
+                                                    col0 + 8 * i);
+        }
+      const float ef = reinterpret_cast<const float*>(base + kOffRecords + here * kRecordBytes + kTerms * kJpTerm)[kEf + t];
+      if (!(ok = DELTA_WARP_WAIT(outs, c))) break;
+      tc_fence_after();
+      float sum = 0.f;
+      if (quarter < 2) {
+        uint16_t* dst = p.o + (static_cast<int64_t>(row0 + t) * p.Hv + w.hv) * p.V + col0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float a[8], b[8];
+          load_sum8(tmem + lanes + kTmOut1 + 8 * i, a);
+          load_sum8(tmem + lanes + kTmOut2 + 8 * i, b);
+          float d[8];
+          if (BWD) unpack8(in[i], d);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            a[j] = p.scale * fmaf(ef, a[j], b[j]);
+            if (BWD) sum = fmaf(a[j], d[j], sum);
+          }
+          if (!BWD && on && 8 * i < width) *reinterpret_cast<uint4*>(dst + 8 * i) = pack8(a);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(outfree);
+      if (lane == 0) bar_arrive(empty + 8 * here);
+      if (BWD && on) p.dots[(static_cast<int64_t>(w.tile) * p.Hv + w.hv) * p.total + row0 + t] = sum;
+      }
+      if (next < chunks) {
+        if (!(ok = DELTA_WARP_WAIT(recfull + 8 * st, next / kStages))) break;
+        if (c >= 0 && !(ok = DELTA_WARP_WAIT(acc2, c))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int i = 0; i < kTerms; ++i)
+          copy_row(tmem + lanes + kTmJ + 32 * i, smem + kOffRecords + st * kRecordBytes + i * kJpTerm, t, true);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(jready);
+      }
+    }
   } else if (warp >= 4) {
-    // ---- rows ----
-    const int quarter = warp % 4, cg = warp / 4 - 1;     // lanes of TMEM, column group
-    const int row = quarter * 32 + lane, col = col0 + cg * 16;
-    const int width = p.V - col;                          // columns of this thread that there are
-    const bool key = quarter < 2;                         // row of K (token) or of Q
-    const int t = row & (kDelta - 1);
-    const uint32_t mine = (static_cast<uint32_t>(quarter * 32) << 16) + cg * 16;
+    // ---- rows: 16 columns of a channel's state, 8 columns of a token ----
+    const int quarter = warp % 4, half = warp / 4 - 1;   // lanes of TMEM, column group
+    const int row = quarter * 32 + lane, col = col0 + half * 16, width = p.V - col;
+    const int t = (quarter & 1) * 32 + lane, piece = (quarter >> 1) * 2 + half;
+    const int tcol = col0 + piece * 8;
+    const bool there = tcol < p.V;                       // the token's columns
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     float S[16];
     {
       const bool has = p.initial && w.slot >= 0 && row < p.K;
@@ -225,101 +340,74 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
         S[4 * i] = x.x, S[4 * i + 1] = x.y, S[4 * i + 2] = x.z, S[4 * i + 3] = x.w;
       }
     }
-    put_terms(smem + kOffState, kStatePanel, row, cg, S);
+    put_terms(smem + kOffState, kStatePanel, row, half, S);
     cconv::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) bar_arrive(sready);
-    const Rows from = key ? p.v : p.d_o;  // rows of v, or (BWD) of do
-    const uint16_t* v_at = from.p + w.hv * from.sh + col;
-    uint4 vraw[2];
-    if (key || BWD) load_bf16x16(v_at + static_cast<int64_t>(w.a + t) * from.st, width, t < w.b - w.a, vraw);
+    const uint16_t* v_at = p.v.p + w.hv * p.v.sh + tcol;
+    auto fetch = [&](int c) {
+      const int64_t at = static_cast<int64_t>(w.a) + c * kDelta + t;
+      return there && at < w.b ? *reinterpret_cast<const uint4*>(v_at + at * p.v.st) : make_uint4(0, 0, 0, 0);
+    };
+    uint4 next = fetch(0);
     for (int c = 0; c < chunks; ++c) {
       const int st = c % kStages, row0 = w.a + c * kDelta, n = min(kDelta, w.b - row0);
-      const float* gates = reinterpret_cast<const float*>(base + st * kStageBytes + kStageKq + kTerms * kJpTerm);
-      if (!(ok = DELTA_WARP_WAIT(full + 8 * st, c / kStages))) break;
+      const float* gates = reinterpret_cast<const float*>(base + kOffRecords + st * kRecordBytes + kTerms * kJpTerm);
+      float r[8], y[8];
+      unpack8(next, r);
+      next = fetch(c + 1);
+      if (!(ok = DELTA_WARP_WAIT(recfull + 8 * st, c / kStages))) break;
       const float ef = gates[kEf + t], eb = gates[kEb + t], beta = gates[kBeta + t], total = gates[kTotal];
-      float r[16], y[16];
       if (!(ok = DELTA_WARP_WAIT(acc1, c))) break;
       tc_fence_after();
-      load_sum(tmem + mine, y);
-      if (key) {
-        float x[16];
-        unpack16(vraw, r);
+      load_sum8(tmem + lanes + kTmAcc1 + piece * 8, y);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          r[i] = t < n ? fmaf(-ef, y[i], r[i]) : 0.f;
-          x[i] = beta * r[i];
-        }
-        put_terms(smem + kOffX, kTokenPanel, t, cg, x);
-        if (n < kDelta && t >= n) {
-          // rows of the next sequence must not meet K^T (eb . u), where 0 * NaN is not 0
-          for (int i = cg * 4; i < cg * 4 + 4; ++i)
-            for (int k = 0; k < (p.K > kPanelCols ? 2 : 1); ++k)
-              sts128(smem + st * kStageBytes + k * kPanelBytes + swizzled(t, i), 0, 0, 0, 0);
-        }
-        cconv::fence_proxy_async_smem();
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) r[i] = ef * y[i];
+      for (int i = 0; i < 8; ++i) {
+        r[i] = t < n ? fmaf(-ef, y[i], r[i]) : 0.f;
+        y[i] = beta * r[i];
       }
+      put_terms8(smem + kOffX, kTokenPanel, t, piece, y);
+      cconv::fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(xready);
-      uint4 doraw[2] = {vraw[0], vraw[1]};
-      if ((key || BWD) && c + 1 < chunks)
-        load_bf16x16(v_at + static_cast<int64_t>(row0 + kDelta + t) * from.st, width, row0 + kDelta + t < w.b, vraw);
       if (!(ok = DELTA_WARP_WAIT(acc2, c))) break;
       tc_fence_after();
-      load_sum(tmem2 + mine, y);
-      if (key) {
-        const float f = eb * beta;
+      load_sum8(tmem + lanes + kTmAcc2 + piece * 8, y);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          r[i] += y[i];
-          y[i] = t < n ? f * r[i] : 0.f;
-        }
-        put_terms(smem + kOffX, kTokenPanel, t, cg, y);
-        cconv::fence_proxy_async_smem();
+      for (int i = 0; i < 8; ++i) {
+        r[i] += y[i];
+        y[i] = t < n ? eb * (beta * r[i]) : 0.f;
       }
+      put_terms8(smem + kOffU, kTokenPanel, t, piece, y);
+      cconv::fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(uready);
-      if (BWD && t < n) {
-        if (key) {
-          float* dst = p.z + (static_cast<int64_t>(row0 + t) * p.Hv + w.hv) * p.V + col;
+      if (BWD) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (4 * i < width)
-              *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-        } else {
-          float d[16], sum = 0.f;
-          unpack16(doraw, d);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) sum = fmaf(d[i], r[i] + y[i], sum);
-          p.dots[(static_cast<int64_t>(w.tile * 2 + cg) * p.Hv + w.hv) * p.total + row0 + t] = p.scale * sum;
-        }
-      }
-      if (!BWD && !key && t < n) {
-        uint16_t* dst = p.o + (static_cast<int64_t>(row0 + t) * p.Hv + w.hv) * p.V + col;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t h[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            h[j] = f2_to_bf16x2(f2_pack(p.scale * (r[8 * i + 2 * j] + y[8 * i + 2 * j]),
-                                        p.scale * (r[8 * i + 2 * j + 1] + y[8 * i + 2 * j + 1])));
-          if (8 * i < width) *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(h[0], h[1], h[2], h[3]);
+        for (int i = 0; i < 8; ++i) y[i] = t < n ? beta * r[i] : 0.f;
+        uint4 u[kTerms];
+        split8(y, u);
+        uint8_t* tile = p.u + (((slot0 + c) * p.Hv + w.hv) * p.tiles + w.tile) * kUTile + term_piece(t, piece);
+        *reinterpret_cast<uint4*>(tile) = u[0];
+        *reinterpret_cast<uint4*>(tile + kTokenPanel) = u[1];
+        if (t < n && there) {
+          float4* dst = reinterpret_cast<float4*>(p.z + (static_cast<int64_t>(row0 + t) * p.Hv + w.hv) * p.V + tcol);
+          dst[0] = make_float4(r[0], r[1], r[2], r[3]);
+          dst[1] = make_float4(r[4], r[5], r[6], r[7]);
         }
       }
       if (c + 1 < chunks || keep) {
+        float x[16];
         if (!(ok = DELTA_WARP_WAIT(acc3, c))) break;
         tc_fence_after();
-        load_sum(tmem + mine, y);
+        load_sum(tmem + lanes + kTmAcc1 + half * 16, x);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) S[i] = row < p.K ? fmaf(total, S[i], y[i]) : 0.f;
+        for (int i = 0; i < 16; ++i) S[i] = row < p.K ? fmaf(total, S[i], x[i]) : 0.f;
         if (c + 1 < chunks) {
           if (BWD && !(ok = DELTA_WARP_WAIT(kept, c))) break;
-          put_terms(smem + kOffState, kStatePanel, row, cg, S);
+          put_terms(smem + kOffState, kStatePanel, row, half, S);
           cconv::fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
@@ -341,7 +429,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_free(tmem, 256);
+    tmem_free(tmem, 512);
   }
 }
 
@@ -360,7 +448,7 @@ static int launch_chain(const DeltaCall& c, cudaStream_t stream) {
   a.initial = c.initial, a.fin = c.fin;
   a.o = c.o;
   a.records = c.records;
-  a.z = c.z, a.heads = c.heads, a.dots = c.odots;
+  a.z = c.z, a.u = c.u, a.heads = c.heads, a.dots = c.odots;
   a.scale = c.scale;
   a.total = c.s.total, a.nseq = c.s.nseq, a.ratio = c.s.Hv / c.s.Hk, a.Hv = c.s.Hv, a.K = c.s.K, a.V = c.s.V;
   a.tiles = delta_tiles(c.s.V);

@@ -1,19 +1,19 @@
 // attn_delta_grads.cu -- the gated delta rule's dq and dk, and the sums that give dg and dbeta.
 //
 // With S_0 and D, the state before a chunk and the gradient of the state behind it, known (the chains
-// left their first bf16 terms), all chunks are done at once; per chunk and value head
+// left their first bf16 terms, and two of u), all chunks are done at once; per chunk and value head
 //   X = scale (do u^T) . L (s <= t),   Y = (dv u^T) . L (s < t)
 //   dq = X K                        + scale ef . (do S_0^T)
 //   dk = X^T Q - (Y + Y^T) K + eb . (u D^T) - ef . (dv S_0^T)
 // summed over the value heads of a key head in the CTA's registers.  do and dv lie one over the other
 // as a first operand of 128 rows, and so do dq and dk as results:
-//   [do; dv] u^T       (u in two terms)      -> X, -Y as bf16
+//   [do; dv] u^T                             -> X, -Y
 //   [do; dv] S_0^T     rows scaled by scale ef and -ef afterwards
 //   [  ; u ] D^T       rows 64.. scaled by eb afterwards
 //   [X; -Y] K,  [0; -Y^T] K,  [0; X^T] Q
 // A CTA goes through (chunk, key head) items; do, dv and the tiles of S_0 and D come by TMA, 64 columns
-// of V at a time, u is made from z.  Roundings to bf16: X, Y, S_0, D and u (for D), once each, and dv,
-// which is an output.
+// of V at a time, and u's two terms.  Roundings to bf16: S_0, D and dv, once each; X, Y and u keep two
+// terms (with one, dk's error in the 2-norm was 2.8e-3, of which its store makes 1.7e-3).
 //
 // dg_t is the sum of o_i . do_i - v_i . dv_i over the tokens i >= t of the sequence.
 #include <cudaTypedefs.h>
@@ -38,41 +38,45 @@ static FaultReader reader(read_fault);
 constexpr int kHalf = kDelta * 128;                       // 64 rows of 64 columns
 constexpr int kStepOut = 2 * kHalf;                       // do over dv
 constexpr int kStepState = 2 * kStatePanel;               // two tiles of S_0; of D
-constexpr int kStepU = 2 * kHalf;                         // second terms of u over the first ones
+constexpr int kUPart = 3 * kTokenPanel;                   // second, first and again second terms of u: a tile
+constexpr int kStepU = 2 * kUPart;
 constexpr int kStepBytes = kStepOut + 2 * kStepState + kStepU;
 constexpr int kGradStages = 2;
 constexpr int kOffGradKq = kGradStages * kStepBytes;
-constexpr int kOffZero = kOffGradKq + kStageKq;           // zeros, X, -Y: 64 rows each
+constexpr int kOffZero = kOffGradKq + kStageKq;           // zeros; X, -Y; their second terms: 64 rows each
 constexpr int kOffXy = kOffZero + kHalf;
-constexpr int kOffLogs = kOffXy + 2 * kHalf;              // log2 decays, and their sums from token 32 on
-constexpr int kOffGradBars = kOffLogs + 4 * kDelta * 4;
-constexpr int kGradBytes = kOffGradBars + 20 * 8 + 1024;
+constexpr int kOffGates = kOffXy + 4 * kHalf;             // of two heads in turn
+constexpr int kHeadGates = 5 * kDelta;                    // floats
+constexpr int kOffGradBars = kOffGates + 2 * kHeadGates * 4;
+constexpr int kGradBytes = kOffGradBars + 24 * 8 + 1024;
 static_assert(kGradBytes <= 232448, "shared memory of one CTA");
 // columns of TMEM
-constexpr int kAccXy = 0, kAccState = 64, kAccEnd = 192, kAccIntra = 320;
+constexpr int kAccXy = 0, kAccState = 128, kAccEnd = 256, kAccIntra = 384;  // X, Y: two heads in turn
+constexpr int kGradThreads = 384;
 
 struct GradArgs {
   CUtensorMap mq, mk, mo, mv;  // q, k, do, dv
-  Gates g, beta;
+  Gates g;
   const int32_t* cu;
-  const float* z;
-  const uint8_t *heads, *ends;
+  const uint8_t *u, *heads, *ends;
+  const float *odots, *vdots, *bdots;
   uint16_t *dq, *dk;
+  float *dg, *dbeta;
+  double* sums;  // [Hv][slots] of the chunks' terms of dg
   float scale;
   int total, nseq, Hk, Hv, K, V, tiles;
   int64_t items;  // slots * Hk
 };
 
-__global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_grads_kernel(const __grid_constant__ GradArgs p) {
+__global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(const __grid_constant__ GradArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const uint32_t smem = smem_addr(base);
   const uint32_t full = smem + kOffGradBars, empty = full + 8 * kGradStages;      // tiles of a step
-  const uint32_t uready = empty + 8 * kGradStages;                                // u of a step
-  const uint32_t kqfull = uready + 8 * kGradStages, kqempty = kqfull + 8;         // an item's K and Q
+  const uint32_t kqfull = empty + 8 * kGradStages, kqempty = kqfull + 8;          // an item's K and Q
   const uint32_t xyfull = kqempty + 8, xyready = xyfull + 8;                      // a head's X and Y
   const uint32_t headfull = xyready + 8, headfree = headfull + 8;                 // a head's sums
-  const uint32_t gready = headfree + 8, alldone = gready + 8;                      // a head's gates
+  const uint32_t gready = headfree + 8, gfree = gready + 16, alldone = gfree + 16;  // a head's gates, in turn
   __shared__ uint32_t tmem_at;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int ratio = p.Hv / p.Hk, steps = (p.V + 63) / 64;
@@ -80,7 +84,6 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_grads_kernel(con
     for (int i = 0; i < kGradStages; ++i) {
       bar_init(full + 8 * i, 1);
       bar_init(empty + 8 * i, 1);
-      bar_init(uready + 8 * i, kRowWarps);
     }
     bar_init(kqfull, 1);
     bar_init(kqempty, 1);
@@ -88,11 +91,14 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_grads_kernel(con
     bar_init(xyready, kRowWarps);
     bar_init(headfull, 1);
     bar_init(headfree, kRowWarps);
-    bar_init(gready, 1);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(gready + 8 * i, 1);
+      bar_init(gfree + 8 * i, kRowWarps);
+    }
     bar_init(alldone, 1);
     cconv::fence_mbar_init();
   }
-  for (int i = threadIdx.x; i < kHalf / 16; i += kChainThreads) sts128(smem + kOffZero + i * 16, 0, 0, 0, 0);
+  for (int i = threadIdx.x; i < kHalf / 16; i += kGradThreads) sts128(smem + kOffZero + i * 16, 0, 0, 0, 0);
   cconv::fence_proxy_async_smem();
   if (warp == 1) tmem_alloc(&tmem_at, 512);
   tc_fence_before();
@@ -129,12 +135,18 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_grads_kernel(con
             if (step >= kGradStages && !(ok = DELTA_WAIT(empty + 8 * st, step / kGradStages - 1))) break;
             const int tiles = min(2, p.tiles - 2 * s);
             const uint32_t dst = smem + st * kStepBytes, bar = full + 8 * st;
-            bar_expect(bar, kStepOut + 2 * tiles * kStatePanel);
+            bar_expect(bar, kStepOut + tiles * (2 * kStatePanel + kUPart));
             load_box(dst, &p.mo, bar, s * 64, hv, row0);
             load_box(dst + kHalf, &p.mv, bar, s * 64, hv, row0);
             const int64_t from = ((slot * p.Hv + hv) * p.tiles + 2 * s) * kStatePanel;
             bulk_load(dst + kStepOut, p.heads + from, tiles * kStatePanel, bar);
             bulk_load(dst + kStepOut + kStepState, p.ends + from, tiles * kStatePanel, bar);
+            for (int i = 0; i < tiles; ++i) {
+              const uint8_t* u = p.u + ((slot * p.Hv + hv) * p.tiles + 2 * s + i) * kUTile;
+              const uint32_t to = dst + kStepOut + 2 * kStepState + i * kUPart;
+              bulk_load(to + kTokenPanel, u, kUTile, bar);
+              bulk_load(to, u + kTokenPanel, kTokenPanel, bar);
+            }
           }
         }
       }
@@ -159,42 +171,60 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_grads_kernel(con
         const uint32_t d_rows = mma_desc(width, false, true), d_cols = mma_desc(width, true, true);
         ok = DELTA_WAIT(kqfull, item);
         for (int h = 0; h < ratio && ok; ++h, ++head) {
-          if (head > 0 && !(ok = DELTA_WAIT(headfree, head - 1))) break;
-          tc_fence_after();
-          for (int s = 0; s < steps && ok; ++s, ++step) {
-            const int st = step % kGradStages;
+          const uint32_t xy_acc = tmem + kAccXy + (head & 1) * kDelta;
+          // X and Y of as many steps as there are slots, then the products with the states
+          int done = 0;
+          for (int s = 0; s < steps && ok; ++s) {
+            const int st = (step + s) % kGradStages;
             const uint32_t src = smem + st * kStepBytes, u = src + kStepOut + 2 * kStepState;
             const int ks = (min(64, p.V - 64 * s) + 15) / 16;
-            if (!(ok = DELTA_WAIT(full + 8 * st, step / kGradStages))) break;
-            if (!(ok = DELTA_WAIT(uready + 8 * st, step / kGradStages))) break;
+            if (!(ok = DELTA_WAIT(full + 8 * st, (step + s) / kGradStages))) break;
             tc_fence_after();
-            const uint64_t a = tile_desc(src, 0), lo = tile_desc(u, 0), hi = tile_desc(u + kHalf, 0);
+            const uint64_t a = tile_desc(src, 0);
 #pragma unroll 1
             for (int j = 0; j < ks; ++j) {
-              mma_ss(tmem + kAccXy, a + 2 * j, hi + 2 * j, d_xy, s + j > 0);
-              mma_ss(tmem + kAccXy, a + 2 * j, lo + 2 * j, d_xy, true);
+              const uint64_t lo = term_desc(u + (j >> 1) * kUPart, 0) + 2 * (j & 1);
+              mma_ss(xy_acc, a + 2 * j, lo + kTokenPanel / 16, d_xy, s + j > 0);
+              mma_ss(xy_acc, a + 2 * j, lo, d_xy, true);
             }
             if (s + 1 == steps) mma_commit(xyfull);
+            if (s + 1 < steps && s + 1 < done + kGradStages) continue;
+            if (done == 0 && head > 0 && !(ok = DELTA_WAIT(headfree, head - 1))) break;
+            tc_fence_after();
+            for (; done <= s; ++done) {
+              const int at_slot = (step + done) % kGradStages;
+              const uint32_t from = smem + at_slot * kStepBytes, uu = from + kStepOut + 2 * kStepState;
+              const uint64_t b = tile_desc(from, 0);
+              const int kd = (min(64, p.V - 64 * done) + 15) / 16;
 #pragma unroll 1
-            for (int j = 0; j < ks; ++j) {
-              const uint64_t state = term_desc(src + kStepOut + (j >> 1) * kStatePanel, 0) + 2 * (j & 1);
-              const uint64_t end = term_desc(src + kStepOut + kStepState + (j >> 1) * kStatePanel, 0) + 2 * (j & 1);
-              mma_ss(tmem + kAccState, a + 2 * j, state, d_state, s + j > 0);
-              mma_ss(tmem + kAccEnd, lo + 2 * j, end, d_state, s + j > 0);
+              for (int j = 0; j < kd; ++j) {
+                const uint32_t tile = (j >> 1) * kStatePanel;
+                const uint64_t state = term_desc(from + kStepOut + tile, 0) + 2 * (j & 1);
+                const uint64_t end = term_desc(from + kStepOut + kStepState + tile, 0) + 2 * (j & 1);
+                const uint64_t lo = term_desc(uu + (j >> 1) * kUPart, 0) + 2 * (j & 1);
+                mma_ss(tmem + kAccState, b + 2 * j, state, d_state, done + j > 0);
+                mma_ss(tmem + kAccEnd, lo, end, d_state, done + j > 0);            // rows 64 on: u's first terms
+                mma_ss(tmem + kAccEnd, lo + kTokenPanel / 16, end, d_state, true);  // and the second ones
+              }
+              mma_commit(empty + 8 * at_slot);
             }
-            mma_commit(empty + 8 * st);
           }
+          step += steps;
           if (!ok || !(ok = DELTA_WAIT(xyready, head))) break;
           tc_fence_after();
           const uint64_t k = tile_desc(smem + kOffGradKq, kPanelBytes);
           const uint64_t q = tile_desc(smem + kOffGradKq + kSideBytes, kPanelBytes);
-          const uint64_t xy = tile_desc(smem + kOffXy, 0);
-          const uint64_t xt = tile_desc(smem + kOffZero, kHalf), yt = tile_desc(smem + kOffZero, 2 * kHalf);
 #pragma unroll 1
-          for (int j = 0; j < kDelta / 16; ++j) {
-            mma_ss(tmem + kAccIntra, xy + 2 * j, k + j * kRowStep, d_rows, h + j > 0);
-            mma_ss(tmem + kAccIntra, yt + j * kRowStep, k + j * kRowStep, d_cols, true);
-            mma_ss(tmem + kAccIntra, xt + j * kRowStep, q + j * kRowStep, d_cols, true);
+          for (int i = 0; i < 2; ++i) {  // first and second terms
+            const uint64_t xy = tile_desc(smem + kOffXy + i * 2 * kHalf, 0);
+            const uint64_t xt = tile_desc(smem + kOffZero, (1 + 2 * i) * kHalf);
+            const uint64_t yt = tile_desc(smem + kOffZero, (2 + 2 * i) * kHalf);
+#pragma unroll 1
+            for (int j = 0; j < kDelta / 16; ++j) {
+              mma_ss(tmem + kAccIntra, xy + 2 * j, k + j * kRowStep, d_rows, h + i + j > 0);
+              mma_ss(tmem + kAccIntra, yt + j * kRowStep, k + j * kRowStep, d_cols, true);
+              mma_ss(tmem + kAccIntra, xt + j * kRowStep, q + j * kRowStep, d_cols, true);
+            }
           }
           mma_commit(headfull);
         }
@@ -209,16 +239,89 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_grads_kernel(con
       mma_commit(alldone);
       drain(alldone, 1);
     }
+  } else if (warp == 2) {
+    // ---- dbeta, and dg summed up from each token to its chunk's end ----
+    for (int64_t at = blockIdx.x; at < p.items; at += gridDim.x) {
+      const int64_t slot = at / p.Hk;
+      int row0, n;
+      if (!find_chunk(p.cu, p.nseq, p.total, slot, lane, row0, n)) continue;
+      for (int h = 0; h < ratio; ++h) {
+        const int hv = static_cast<int>(at % p.Hk) * ratio + h;
+        double x[2], up;
+        float db[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {  // tokens 63 - 2 lane, 62 - 2 lane
+          const int t = kDelta - 1 - 2 * lane - j;
+          x[j] = 0.0, db[j] = 0.f;
+          if (t < n)
+#pragma unroll 4
+            for (int i = 0; i < p.tiles; ++i) {
+              const int64_t from = (static_cast<int64_t>(i) * p.Hv + hv) * p.total + row0 + t;
+              x[j] += static_cast<double>(__ldcs(p.odots + from)) - static_cast<double>(__ldcs(p.vdots + from));
+              db[j] += __ldcs(p.bdots + from);
+            }
+        }
+        up = x[0] + x[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const double y = __shfl_up_sync(0xffffffffu, up, o);
+          if (lane >= o) up += y;
+        }
+        const float sums[2] = {static_cast<float>(up - x[1]), static_cast<float>(up)};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int t = kDelta - 1 - 2 * lane - j;
+          if (t >= n) continue;
+          p.dbeta[static_cast<int64_t>(row0 + t) * p.Hv + hv] = db[j];
+          p.dg[static_cast<int64_t>(row0 + t) * p.Hv + hv] = sums[j];
+        }
+        if (lane == 31) p.sums[hv * (p.items / p.Hk) + slot] = up;
+      }
+    }
+  } else if (warp == 3) {
+    // ---- the heads' gates, two ahead ----
+    int head = 0;
+    for (int64_t at = blockIdx.x; at < p.items && ok; at += gridDim.x) {
+      int row0, n;
+      if (!find_chunk(p.cu, p.nseq, p.total, at / p.Hk, lane, row0, n)) continue;
+      for (int h = 0; h < ratio; ++h, ++head) {
+        const int hv = static_cast<int>(at % p.Hk) * ratio + h;
+        float g[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) g[j] = 2 * lane + j < n ? kLog2e * p.g.at(row0 + 2 * lane + j, hv) : 0.f;
+        // sums of one sign: within the block of 32 tokens (16 lanes), then with the other block
+        const float own = g[0] + g[1];
+        float up = own, down = own;
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) {
+          const float x = __shfl_up_sync(0xffffffffu, up, o, 16), y = __shfl_down_sync(0xffffffffu, down, o, 16);
+          if ((lane & 15) >= o) up += x;
+          if ((lane & 15) + o < 16) down += y;
+        }
+        const float first = __shfl_sync(0xffffffffu, down, 0), second = __shfl_sync(0xffffffffu, down, 16);
+        float before = __shfl_up_sync(0xffffffffu, up, 1, 16), after = __shfl_down_sync(0xffffffffu, down, 1, 16);
+        if ((lane & 15) == 0) before = 0.f;
+        if ((lane & 15) == 15) after = 0.f;
+        const float front = lane < 16 ? 0.f : first, rest = lane < 16 ? second : 0.f;
+        if (head > 1 && !(ok = DELTA_WARP_WAIT(gfree + 8 * (head & 1), head / 2 - 1))) break;
+        float2* to = reinterpret_cast<float2*>(base + kOffGates) + (head & 1) * (kHeadGates / 2) + lane;
+        to[0] = make_float2(exp2_fast(g[0]), exp2_fast(g[1]));                                   // of the token
+        to[32] = make_float2(exp2_fast(before + g[0]), exp2_fast(before + own));                 // from the block's start
+        to[64] = make_float2(exp2_fast(g[1] + after), exp2_fast(after));                         // to its end
+        to[96] = make_float2(exp2_fast(front + before + g[0]), exp2_fast(front + before + own)); // from the chunk's start
+        to[128] = make_float2(exp2_fast(g[1] + after + rest), exp2_fast(after + rest));          // to its end
+        __syncwarp();
+        if (lane == 0) bar_arrive(gready + 8 * (head & 1));
+      }
+    }
   } else if (warp >= 4) {
     // ---- rows ----
-    const int quarter = warp % 4, cg = warp / 4 - 1;
-    const int row = quarter * 32 + lane, t = row & (kDelta - 1);
-    const bool dq = quarter < 2;                      // this thread's row is one of dq; or of dk
+    const int quarter = warp % 4, half = warp / 4 - 1;
+    const int row = quarter * 32 + lane, t = row & (kDelta - 1), block = quarter & 1;
+    const bool dq = quarter < 2;  // this thread's row is one of dq; or of dk
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const int piece = (quarter >> 1) * 2 + cg;        // 16 columns of u of token t
     const int tid = threadIdx.x - 128;
-    float* logs = reinterpret_cast<float*>(base + kOffLogs);
-    int step = 0, item = 0, head = 0;
+    int item = 0, head = 0;
     for (int64_t at = blockIdx.x; at < p.items && ok; at += gridDim.x) {
       const int hk = static_cast<int>(at % p.Hk);
       int row0, n;
@@ -227,67 +330,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_grads_kernel(con
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0.f;
       for (int h = 0; h < ratio && ok; ++h, ++head) {
-        const int hv = hk * ratio + h;
-        // gates: [0, 64) log2 decays, [64, 128) their sums from token 0 or 32 on, [128, 192) ef, [192, 256) eb
-        if (warp == 4) {
-          if (head > 0 && !(ok = DELTA_WARP_WAIT(headfree, head - 1))) break;  // the last head's are read
-          float g[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) g[j] = 2 * lane + j < n ? kLog2e * p.g.at(row0 + 2 * lane + j, hv) : 0.f;
-          float up = g[0] + g[1], down = up, half = up;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const float x = __shfl_up_sync(0xffffffffu, up, o), y = __shfl_down_sync(0xffffffffu, down, o);
-            if (lane >= o) up += x;
-            if (lane + o < 32) down += y;
-          }
-#pragma unroll
-          for (int o = 1; o < 16; o <<= 1) {
-            const float x = __shfl_up_sync(0xffffffffu, half, o, 16);
-            if ((lane & 15) >= o) half += x;
-          }
-          float before = __shfl_up_sync(0xffffffffu, up, 1), after = __shfl_down_sync(0xffffffffu, down, 1);
-          float start = __shfl_up_sync(0xffffffffu, half, 1, 16);
-          if (lane == 0) before = 0.f;
-          if (lane == 31) after = 0.f;
-          if ((lane & 15) == 0) start = 0.f;
-          const int i = 2 * lane;
-          logs[i] = g[0], logs[i + 1] = g[1];
-          logs[64 + i] = start + g[0], logs[64 + i + 1] = start + g[0] + g[1];
-          logs[128 + i] = exp2_fast(before + g[0]), logs[128 + i + 1] = exp2_fast(before + g[0] + g[1]);
-          logs[192 + i] = exp2_fast(g[1] + after), logs[192 + i + 1] = exp2_fast(after);
-          __syncwarp();
-          if (lane == 0) bar_arrive(gready);
-        }
-        if (!(ok = DELTA_WARP_WAIT(gready, head))) break;
-        const float beta = t < n ? __ldg(p.beta.p + (row0 + t) * p.beta.st + hv * p.beta.sh) : 0.f;
-        for (int s = 0; s < steps; ++s, ++step) {
-          // u of token t, 16 columns, in two terms
-          const int st = step % kGradStages, col = s * 64 + piece * 16;
-          float4 z[4];
-          const float4* src = reinterpret_cast<const float4*>(p.z + (static_cast<int64_t>(row0 + t) * p.Hv + hv) * p.V + col);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (t < n && col + 4 * i < p.V) z[i] = src[i];
-          }
-          if (step >= kGradStages && !(ok = DELTA_WARP_WAIT(empty + 8 * st, step / kGradStages - 1))) break;
-          const uint32_t u = smem + st * kStepBytes + kStepOut + 2 * kStepState;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float x[8] = {beta * z[2 * i].x, beta * z[2 * i].y, beta * z[2 * i].z, beta * z[2 * i].w,
-                                beta * z[2 * i + 1].x, beta * z[2 * i + 1].y, beta * z[2 * i + 1].z, beta * z[2 * i + 1].w};
-            uint4 w[kTerms];
-            split8(x, w);
-            const uint32_t to = u + swizzled(t, piece * 2 + i);
-            sts128(to + kHalf, w[0].x, w[0].y, w[0].z, w[0].w);
-            sts128(to, w[1].x, w[1].y, w[1].z, w[1].w);
-          }
-          cconv::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) bar_arrive(uready + 8 * st);
-        }
-        if (!ok) break;
+        const float* gates = reinterpret_cast<const float*>(base + kOffGates) + (head & 1) * kHeadGates;
         if (h == 0) {
           if (!(ok = DELTA_WARP_WAIT(kqfull, item))) break;
           if (n < kDelta) {
@@ -300,50 +343,83 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_grads_kernel(con
             }
           }
         }
+        if (!(ok = DELTA_WARP_WAIT(gready + 8 * (head & 1), head / 2))) break;
         if (!(ok = DELTA_WARP_WAIT(xyfull, head))) break;
         tc_fence_after();
         {
-          uint32_t x[32];
-          tmem_ld32(tmem + lanes + kAccXy + cg * 32, x);
-          tmem_wait_ld();
-          tmem_use32(x);
-          const float f = dq ? p.scale : -1.f;
-          float e = cg == 0 && t >= 32 ? logs[64 + t] : 0.f;
+          // columns s of block `half` times the decay from s to t: across blocks a product of two factors,
+          // in the block itself a running product down from t
+          float x[32];
+          if (half <= block) {
+            uint32_t y[32];
+            tmem_ld32(tmem + lanes + kAccXy + (head & 1) * kDelta + half * 32, y);
+            tmem_wait_ld();
+            tmem_use32(y);
+            const float f = t < n ? (dq ? p.scale : -1.f) : 0.f;
+            if (half < block) {
+              const float u = f * gates[64 + t];
 #pragma unroll
-          for (int i = 31; i >= 0; --i) {
-            const int s = cg * 32 + i;
-            if (i < 31 && s < t) e += logs[s + 1];
-            if (i == 31 && cg == 1 && s < t) e += logs[s + 1 < kDelta ? s + 1 : s];
-            const float v = f * __uint_as_float(x[i]) * exp2_fast(e);
-            x[i] = __float_as_uint(t < n && (s < t || (dq && s == t)) ? v : 0.f);
+              for (int i = 0; i < 8; ++i) {
+                const float4 w = *reinterpret_cast<const float4*>(gates + 128 + 4 * i);
+                x[4 * i] = u * w.x * __uint_as_float(y[4 * i]);
+                x[4 * i + 1] = u * w.y * __uint_as_float(y[4 * i + 1]);
+                x[4 * i + 2] = u * w.z * __uint_as_float(y[4 * i + 2]);
+                x[4 * i + 3] = u * w.w * __uint_as_float(y[4 * i + 3]);
+              }
+            } else {
+              float w = f;
+#pragma unroll
+              for (int i = 7; i >= 0; --i) {
+                const float4 a = *reinterpret_cast<const float4*>(gates + half * 32 + 4 * i);
+#pragma unroll
+                for (int j = 3; j >= 0; --j) {
+                  const int s = 4 * i + j;
+                  x[s] = s < lane || (dq && s == lane) ? __uint_as_float(y[s]) * w : 0.f;
+                  if (s <= lane) w *= j == 3 ? a.w : j == 2 ? a.z : j == 1 ? a.y : a.x;
+                }
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = t < n ? x[i] : 0.f;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = 0.f;
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+            uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = f2_to_bf16x2(pair(x, 4 * i + j));
-            sts128(smem + kOffXy + swizzled(row, cg * 4 + i), w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < 4; ++j) {
+              const f2 v = f2_pack(x[8 * i + 2 * j], x[8 * i + 2 * j + 1]);
+              hi[j] = f2_to_bf16x2(v);
+              lo[j] = f2_to_bf16x2(f2_fma(bf16x2_to_f2(hi[j]), f2_splat(-1.f), v));
+            }
+            const uint32_t to = smem + kOffXy + swizzled(row, half * 4 + i);
+            sts128(to, hi[0], hi[1], hi[2], hi[3]);
+            sts128(to + 2 * kHalf, lo[0], lo[1], lo[2], lo[3]);
           }
         }
         cconv::fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(xyready);
+        const float ef = gates[192 + t], eb = gates[256 + t], f = dq ? p.scale * ef : -ef;
+        __syncwarp();
+        if (lane == 0) bar_arrive(gfree + 8 * (head & 1));
         if (!(ok = DELTA_WARP_WAIT(headfull, head))) break;
         tc_fence_after();
-        const float ef = logs[128 + t], eb = logs[192 + t], f = dq ? p.scale * ef : -ef;
         const bool last = h + 1 == ratio;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const int c = cg * 64 + b * 16;
+          const int c = half * 64 + b * 16;
           if (c >= p.K) continue;
           uint32_t x[16], y[16], w[16];
           tmem_ld16(tmem + lanes + kAccState + c, x);
-          tmem_ld16(tmem + lanes + kAccEnd + c, y);
+          if (!dq) tmem_ld16(tmem + lanes + kAccEnd + c, y);
           if (last) tmem_ld16(tmem + lanes + kAccIntra + c, w);
           tmem_wait_ld();
           tmem_use16(x);
-          tmem_use16(y);
+          if (!dq) tmem_use16(y);
           if (last) tmem_use16(w);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -360,14 +436,10 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_grads_kernel(con
       if (!ok) break;
       ++item;
       if (t < n) {
-        uint16_t* dst = (dq ? p.dq : p.dk) + (static_cast<int64_t>(row0 + t) * p.Hk + hk) * p.K + cg * 64;
+        uint16_t* dst = (dq ? p.dq : p.dk) + (static_cast<int64_t>(row0 + t) * p.Hk + hk) * p.K + half * 64;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = f2_to_bf16x2(f2_pack(acc[8 * i + 2 * j], acc[8 * i + 2 * j + 1]));
-          if (cg * 64 + 8 * i < p.K) *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int i = 0; i < 8; ++i)
+          if (half * 64 + 8 * i < p.K) *reinterpret_cast<uint4*>(dst + 8 * i) = pack8(acc + 8 * i);
       }
     }
   }
@@ -381,63 +453,62 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_grads_kernel(con
   }
 }
 
-// dg and dbeta of one sequence and value head by one CTA, from the last token on, kGateThreads tokens
-// at a time.  The running sum is kept in 64 bits: it adds up terms of both signs over the whole
+// dg, second part: what the chunks behind a token's add.  First the chunks' sums become sums over all
+// later chunks of the sequence, a warp for each sequence and value head; then these are added, a CTA for
+// each chunk.  The sums over chunks are kept in 64 bits: they add up terms of both signs over the whole
 // sequence, and what is left of them is small where a head forgets fast.
-constexpr int kGateThreads = 256;
 struct GateArgs {
   const int32_t* cu;
-  const float *odots, *vdots, *bdots;
-  float *dg, *dbeta;
-  int total, Hv, parts;
+  double* sums;
+  float* dg;
+  int total, nseq, Hv;
+  int64_t slots;
 };
-__global__ void __launch_bounds__(kGateThreads) cattn_delta_gates_kernel(const GateArgs p) {
+constexpr int kGateWarps = 4;
+__global__ void __launch_bounds__(kGateWarps * 32) cattn_delta_scan_kernel(const GateArgs p) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
-  __shared__ double sums[2][kGateThreads / 32];
-  const int hv = static_cast<int>(blockIdx.x % p.Hv), seq = static_cast<int>(blockIdx.x / p.Hv);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kGateWarps + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (i >= static_cast<int64_t>(p.nseq) * p.Hv) return;
+  const int seq = static_cast<int>(i / p.Hv), hv = static_cast<int>(i % p.Hv);
   int a, b;
   sequence_rows(p.cu, seq, p.total, a, b);
-  if (p.cu[seq] < 0 || p.cu[seq + 1] < p.cu[seq] || p.cu[seq + 1] > p.total) return;
+  double* sums = p.sums + hv * p.slots + a / kDelta + seq;
   double carry = 0.0;
-  int turn = 0;
-  for (int64_t top = b; top > a; top -= kGateThreads, turn ^= 1) {
-    const int64_t t = top - 1 - threadIdx.x;
-    double x = 0.0;
-    if (t >= a) {
-      float db = 0.f;
-      for (int i = 0; i < p.parts; ++i) {
-        const int64_t at = (static_cast<int64_t>(i) * p.Hv + hv) * p.total + t;
-        x += static_cast<double>(p.odots[at]) - static_cast<double>(p.vdots[at]);
-        db += p.bdots[at];
-      }
-      p.dbeta[t * p.Hv + hv] = db;
-    }
+  for (int64_t top = (b - a + kDelta - 1) / kDelta; top > 0; top -= 32) {
+    const int64_t c = top - 1 - lane;
+    const double own = c >= 0 ? sums[c] : 0.0;
+    double x = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const double y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) sums[turn][warp] = x;
-    __syncthreads();
-    double before = carry;
-#pragma unroll
-    for (int i = 0; i < kGateThreads / 32; ++i) {
-      if (i < warp) before += sums[turn][i];
-      carry += sums[turn][i];
-    }
-    if (t >= a) p.dg[t * p.Hv + hv] = static_cast<float>(before + x);
+    if (c >= 0) sums[c] = carry + (x - own);
+    carry += __shfl_sync(0xffffffffu, x, 31);
   }
+}
+__global__ void __launch_bounds__(256) cattn_delta_later_kernel(const GateArgs p) {
+  cconv::grid_dependency_wait();
+  cconv::grid_launch_dependents();
+  int row0, n;
+  const int64_t slot = blockIdx.x;
+  if (!find_chunk(p.cu, p.nseq, p.total, slot, threadIdx.x % 32, row0, n)) return;
+  float* dg = p.dg + static_cast<int64_t>(row0) * p.Hv;
+  for (int64_t i = threadIdx.x; i < static_cast<int64_t>(n) * p.Hv; i += blockDim.x)
+    dg[i] = static_cast<float>(p.sums[i % p.Hv * p.slots + slot] + static_cast<double>(dg[i]));
 }
 
 int launch_delta_gates(const DeltaCall& c, cudaStream_t stream) {
-  GateArgs a{c.cu, c.odots, c.vdots, c.bdots, c.dg, c.dbeta, c.s.total, c.s.Hv, 2 * delta_tiles(c.s.V)};
-  const int64_t ctas = static_cast<int64_t>(c.s.nseq) * c.s.Hv;
-  return launch_pdl(cattn_delta_gates_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kGateThreads), 0, stream, a) ==
-                 cudaSuccess
-             ? CCONV_OK
-             : CCONV_ERR_CUDA;
+  const int64_t slots = delta_slots(c.s.total, c.s.nseq);
+  GateArgs a{c.cu, c.sums, c.dg, c.s.total, c.s.nseq, c.s.Hv, slots};
+  const int64_t warps = static_cast<int64_t>(c.s.nseq) * c.s.Hv;
+  if (launch_pdl(cattn_delta_scan_kernel, dim3(static_cast<unsigned>((warps + kGateWarps - 1) / kGateWarps)),
+                 dim3(kGateWarps * 32), 0, stream, a) != cudaSuccess ||
+      launch_pdl(cattn_delta_later_kernel, dim3(static_cast<unsigned>(slots)), dim3(256), 0, stream, a) != cudaSuccess)
+    return CCONV_ERR_CUDA;
+  return CCONV_OK;
 }
 
 int launch_delta_grads(const DeltaCall& c, cudaStream_t stream) {
@@ -450,10 +521,12 @@ int launch_delta_grads(const DeltaCall& c, cudaStream_t stream) {
     rc = encode_tile_map(&a.mv, Rows{c.dv, int64_t(c.s.Hv) * c.s.V, c.s.V}, c.s.total, c.s.Hv, c.s.V, kDelta);
   if (rc == CCONV_OK) rc = sm_count(&sms);
   if (rc != CCONV_OK) return rc;
-  a.g = c.g, a.beta = c.beta;
+  a.g = c.g;
   a.cu = c.cu;
-  a.z = c.z, a.heads = c.heads, a.ends = c.ends;
-  a.dq = c.dq, a.dk = c.dk;
+  a.u = c.u, a.heads = c.heads, a.ends = c.ends;
+  a.odots = c.odots, a.vdots = c.vdots, a.bdots = c.bdots;
+  a.dq = c.dq, a.dk = c.dk, a.dg = c.dg, a.dbeta = c.dbeta;
+  a.sums = c.sums;
   a.scale = c.scale;
   a.total = c.s.total, a.nseq = c.s.nseq, a.Hk = c.s.Hk, a.Hv = c.s.Hv, a.K = c.s.K, a.V = c.s.V;
   a.tiles = delta_tiles(c.s.V);
@@ -461,7 +534,7 @@ int launch_delta_grads(const DeltaCall& c, cudaStream_t stream) {
   const int64_t ctas = a.items < sms ? a.items : sms;
   if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(cattn_delta_grads_kernel), kGradBytes) != CCONV_OK)
     return CCONV_ERR_CUDA;
-  return launch_pdl(cattn_delta_grads_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kChainThreads), kGradBytes,
+  return launch_pdl(cattn_delta_grads_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kGradThreads), kGradBytes,
                     stream, a) == cudaSuccess
              ? CCONV_OK
              : CCONV_ERR_CUDA;

@@ -1,11 +1,12 @@
 // attn_delta_prep.cu -- the gated delta rule's records: J, P~ and the gates of every chunk.
 //
-// A CTA makes one record (64 tokens of one value head).  [K; Q] K^T is one product of 128 x 64 on
-// the tensor cores; thread r then owns row r of [-M; P] and solves X (1 + B M) = row from the last
-// column to the first,
+// A CTA makes one record (64 tokens of one value head).  K K^T and Q K^T are products on the tensor
+// cores; thread t then owns row t of -M and of P and solves X (1 + B M) = row from the last column to the
+// first,
 //     X_s = row_s - sum over i > s of X_i (beta_i M_is),
 // against rows of B M that all threads read from shared memory at the same time.
-// Bound by that solve (2016 multiply-adds a thread, as 1008 packed ones).
+// Bound by these reads: the same 16 bytes for all of a warp still take four turns of shared memory.  So
+// each read serves two rows, and the warp of the first 32 tokens leaves out what is zero.
 #include <cudaTypedefs.h>
 
 #include "attn_chunk_host.h"
@@ -24,11 +25,10 @@ static int read_fault(unsigned* out) {
 }
 static FaultReader reader(read_fault);
 
-constexpr int kPrepThreads = 128;
-// shared memory, from a 1024-byte boundary: the record (K and Q in its place first), then B M
-constexpr int kPrepBm = (kRecordBytes + 1023) / 1024 * 1024;
-constexpr int kPrepBytes = kPrepBm + kDelta * kDelta * 4 + 1024;
-static_assert(2 * 2 * kSideBytes <= kTerms * kJpTerm, "K and Q fit the record's place");
+constexpr int kPrepThreads = 64;
+// shared memory, from a 1024-byte boundary: panels of 64 rows of K over 64 of Q (and what the product
+// with Q reads behind them); B M in their place afterwards
+constexpr int kPrepBytes = 2 * kPanelBytes + kSideBytes + 1024;
 
 struct PrepArgs {
   CUtensorMap mq, mk;
@@ -38,15 +38,64 @@ struct PrepArgs {
   int total, nseq, ratio, Hv, K;
 };
 
-__global__ void __launch_bounds__(kPrepThreads) cattn_delta_prep_kernel(const __grid_constant__ PrepArgs p) {
+// X (1 + B M) = rows, from the last of N columns to the first, for two rows at once (a row of B M in
+// shared memory serves both): bm[s][i] = beta_i M_is, zero for i <= s.
+template <int N>
+__device__ __forceinline__ void solve(f2 (&x)[2][kDelta / 2], const float* bm) {
+#pragma unroll
+  for (int s = N - 2; s >= 0; --s) {
+    f2 acc[2][2] = {{0, 0}, {0, 0}};
+#pragma unroll
+    for (int q = N / 4 - 1; q >= (s + 1) / 4; --q) {  // what the last step made comes last
+      const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(bm + s * kDelta + 4 * q);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        acc[r][0] = f2_fma(x[r][2 * q], m.x, acc[r][0]);
+        acc[r][1] = f2_fma(x[r][2 * q + 1], m.y, acc[r][1]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float a, b, lo, hi;
+      cconv::f2_unpack(f2_add(acc[r][0], acc[r][1]), a, b);
+      cconv::f2_unpack(x[r][s / 2], lo, hi);
+      x[r][s / 2] = s % 2 ? f2_pack(lo, hi - (a + b)) : f2_pack(lo - (a + b), hi);
+    }
+  }
+}
+
+// A row's three terms to the record, 32 bytes (two swizzled pieces) at a time.
+__device__ __forceinline__ void store_row(const f2 (&x)[kDelta / 2], uint8_t* record, int row) {
+#pragma unroll
+  for (int i = 0; i < kDelta / 16; ++i) {
+    uint4 t[2][kTerms];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) cconv::f2_unpack(x[8 * i + 4 * j + k], v[2 * k], v[2 * k + 1]);
+      split8(v, t[j]);
+    }
+    uint8_t* at = record + row * 128 + ((i ^ ((row >> 1) & 3)) << 5);
+    const bool swap = row & 1;
+#pragma unroll
+    for (int s = 0; s < kTerms; ++s) {
+      const uint4 a = swap ? t[1][s] : t[0][s], b = swap ? t[0][s] : t[1][s];
+      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at + s * kJpTerm), "r"(a.x), "r"(a.y),
+                   "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                   : "memory");
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kPrepThreads, 4) cattn_delta_prep_kernel(const __grid_constant__ PrepArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const uint32_t smem = smem_addr(base);
-  float* gates = reinterpret_cast<float*>(base + kTerms * kJpTerm);
-  float* bm = reinterpret_cast<float*>(base + kPrepBm);  // [s][i] = beta_i M_is
+  float* bm = reinterpret_cast<float*>(base);  // [s][i] = beta_i M_is
   __shared__ alignas(8) uint64_t bars[2];
   __shared__ uint32_t tmem_at;
-  __shared__ float logs[kDelta];  // log2 of the tokens' decays
+  __shared__ alignas(16) float logs[kDelta], betas[kDelta];  // [s]: log2 of token s + 1's decay
   const uint32_t loaded = smem_addr(bars), done = loaded + 8;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   if (tid == 0) {
@@ -54,7 +103,7 @@ __global__ void __launch_bounds__(kPrepThreads) cattn_delta_prep_kernel(const __
     bar_init(done, 1);
     cconv::fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(&tmem_at, 64);
+  if (warp == 1) tmem_alloc(&tmem_at, 128);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -67,9 +116,10 @@ __global__ void __launch_bounds__(kPrepThreads) cattn_delta_prep_kernel(const __
   const bool live = find_chunk(p.cu, p.nseq, p.total, slot, lane, row0, n);
   bool ok = true;
   if (live) {
-    const int panels = p.K > kPanelCols ? 2 : 1, ksteps = (p.K + 15) / 16;
+    uint8_t* record = p.records + (slot * p.Hv + hv) * kRecordBytes;
     if (warp == 0) {
       if (elect_one()) {
+        const int panels = p.K > kPanelCols ? 2 : 1, ksteps = (p.K + 15) / 16;
         bar_expect(loaded, panels * 2 * kSideBytes);
         for (int c = 0; c < panels; ++c) {
           load_box(smem + c * kPanelBytes, &p.mk, loaded, c * kPanelCols, hv / p.ratio, row0);
@@ -77,14 +127,21 @@ __global__ void __launch_bounds__(kPrepThreads) cattn_delta_prep_kernel(const __
         }
         ok = wait_phase(loaded, 0);
         if (ok) {
-          const uint64_t d = tile_desc(smem, 0);
+          // lanes 0 to 63 of the results: K K^T in columns 0 to 63, Q K^T in 64 to 127 (M = 128: lanes 64
+          // to 127 hold what follows in shared memory, and are not read)
+          const uint64_t k = tile_desc(smem, 0), q = tile_desc(smem + kSideBytes, 0);
           const uint32_t desc = mma_desc(kDelta, false, false);
-          for (int j = 0; j < ksteps; ++j) mma_ss(tmem, d + col_step(j), d + col_step(j), desc, j > 0);
+          for (int j = 0; j < ksteps; ++j) {
+            mma_ss(tmem, k + col_step(j), k + col_step(j), desc, j > 0);
+            mma_ss(tmem + kDelta, q + col_step(j), k + col_step(j), desc, j > 0);
+          }
+        } else {
+          drain(loaded, 1);
         }
         mma_commit(done);
       }
       __syncwarp();
-    } else if (warp == 1) {
+    } else {
       // gates: two tokens a lane; sums of one sign from the front and from the back
       float g[2], b[2];
 #pragma unroll
@@ -104,77 +161,70 @@ __global__ void __launch_bounds__(kPrepThreads) cattn_delta_prep_kernel(const __
       if (lane == 0) before = 0.f;
       if (lane == 31) after = 0.f;
       const int t = 2 * lane;
-      logs[t] = g[0], logs[t + 1] = g[1];
-      gates[kEf + t] = exp2_fast(before + g[0]), gates[kEf + t + 1] = exp2_fast(before + g[0] + g[1]);
-      gates[kEb + t] = exp2_fast(g[1] + after), gates[kEb + t + 1] = exp2_fast(after);
-      gates[kBeta + t] = b[0], gates[kBeta + t + 1] = b[1];
-      const float all = __shfl_sync(0xffffffffu, down, 0);
-      gates[kTotal + t] = exp2_fast(all), gates[kTotal + t + 1] = 0.f;
+      if (t > 0) logs[t - 1] = g[0];
+      logs[t] = g[1];
+      if (lane == 31) logs[t + 1] = 0.f;
+      betas[t] = b[0], betas[t + 1] = b[1];
+      float2* gates = reinterpret_cast<float2*>(record + kTerms * kJpTerm) + lane;
+      gates[kEf / 2] = make_float2(exp2_fast(before + g[0]), exp2_fast(before + g[0] + g[1]));
+      gates[kEb / 2] = make_float2(exp2_fast(g[1] + after), exp2_fast(after));
+      gates[kBeta / 2] = make_float2(b[0], b[1]);
+      gates[kTotal / 2] = make_float2(exp2_fast(__shfl_sync(0xffffffffu, down, 0)), 0.f);
     }
     __syncthreads();
     ok = wait_phase(done, 0) && ok;
     tc_fence_after();
-    // thread r: row r of [-M; P]
-    const int t = tid & (kDelta - 1);
-    const bool side = tid >= kDelta;
-    float x[kDelta];
+    // thread t: rows t of -M and of P
+    const int t = tid;
+    f2 x[2][kDelta / 2];
+    __syncthreads();  // (K and Q are not needed any more: B M takes their place)
     {
-      uint32_t y[2][32];
-      tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16), y[0]);
-      tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + 32, y[1]);
-      tmem_wait_ld();
-      tmem_use32(y[0]);
-      tmem_use32(y[1]);
+      const uint32_t mine = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+      const float b = betas[t];
       float e = 0.f;  // log2 of the decay from s to t
 #pragma unroll
-      for (int s = kDelta - 1; s >= 0; --s) {
-        if (s < t) e += logs[s + 1 < kDelta ? s + 1 : s];
-        const float v = __uint_as_float(y[s / 32][s % 32]) * exp2_fast(e);
-        x[s] = t < n && (s < t || (s == t && side)) ? (side ? v : -v) : 0.f;
+      for (int h = 1; h >= 0; --h) {
+        uint32_t y[2][32];
+        tmem_ld32(mine + 32 * h, y[0]);
+        tmem_ld32(mine + kDelta + 32 * h, y[1]);
+        tmem_wait_ld();
+        tmem_use32(y[0]);
+        tmem_use32(y[1]);
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {
+          const float4 l = *reinterpret_cast<const float4*>(&logs[32 * h + 4 * i]);  // of tokens s + 1
+          float m[4], q[4];
+#pragma unroll
+          for (int j = 3; j >= 0; --j) {
+            const int s = 32 * h + 4 * i + j;
+            if (s < t) e += j == 3 ? l.w : j == 2 ? l.z : j == 1 ? l.y : l.x;
+            const float w = exp2_fast(e);
+            m[j] = t < n && s < t ? __uint_as_float(y[0][4 * i + j]) * w : 0.f;
+            q[j] = t < n && s <= t ? __uint_as_float(y[1][4 * i + j]) * w : 0.f;
+            bm[s * kDelta + t] = b * m[j];
+          }
+          x[0][16 * h + 2 * i] = f2_pack(-m[0], -m[1]);
+          x[0][16 * h + 2 * i + 1] = f2_pack(-m[2], -m[3]);
+          x[1][16 * h + 2 * i] = f2_pack(q[0], q[1]);
+          x[1][16 * h + 2 * i + 1] = f2_pack(q[2], q[3]);
+        }
       }
     }
-    if (!side) {
-      const float b = -gates[kBeta + t];
-#pragma unroll
-      for (int s = 0; s < kDelta; ++s) bm[s * kDelta + t] = b * x[s];
-    }
-    tc_fence_before();
     __syncthreads();
-#pragma unroll
-    for (int s = kDelta - 2; s >= 0; --s) {
-      f2 acc[2] = {0, 0};
-#pragma unroll
-      for (int q = (s + 1) / 4; q < kDelta / 4; ++q) {
-        const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(bm + s * kDelta + 4 * q);
-        // (columns up to s hold zeros)
-        acc[0] = f2_fma(f2_pack(x[4 * q], x[4 * q + 1]), m.x, acc[0]);
-        acc[1] = f2_fma(f2_pack(x[4 * q + 2], x[4 * q + 3]), m.y, acc[1]);
-      }
-      float a, b;
-      cconv::f2_unpack(f2_add(acc[0], acc[1]), a, b);
-      x[s] -= a + b;
-    }
-#pragma unroll
-    for (int j = 0; j < kDelta / 8; ++j) {
-      uint4 terms[kTerms];
-      split8(x + 8 * j, terms);
-      const uint32_t at = smem + swizzled(tid, j);
-#pragma unroll
-      for (int i = 0; i < kTerms; ++i) sts128(at + i * kJpTerm, terms[i].x, terms[i].y, terms[i].z, terms[i].w);
-    }
-    cconv::fence_proxy_async_smem();
-    __syncthreads();
-    if (tid == 0) {
-      bulk_store(p.records + (slot * p.Hv + hv) * kRecordBytes, smem, kRecordBytes);
-      stores_commit();
-      stores_wait();
-      if (!ok) atomicOr(&g_fault_prep, kFaultWait);
-    }
+    // rows below 32 have zeros in the columns from 32 on
+    if (warp == 0)
+      solve<kDelta / 2>(x, bm);
+    else
+      solve<kDelta>(x, bm);
+    store_row(x[0], record, t);
+    store_row(x[1], record, kDelta + t);
+    if (!ok) atomicOr(&g_fault_prep, kFaultWait);
   }
+  tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_free(tmem, 64);
+    tmem_free(tmem, 128);
   }
 }
 
