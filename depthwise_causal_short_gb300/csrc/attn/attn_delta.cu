@@ -38,9 +38,9 @@ static DeltaWork delta_work(int64_t total, int64_t nseq, int64_t Hv, int64_t V) 
   w.u = take(states / kStatePanel * kUTile);
   w.heads = take(states);
   w.ends = take(states);
-  w.odots = take(tiles * rows * 4);
-  w.vdots = take(tiles * rows * 4);
-  w.bdots = take(tiles * rows * 4);
+  w.odots = take(2 * tiles * rows * 4);
+  w.vdots = take(2 * tiles * rows * 4);
+  w.bdots = take(2 * tiles * rows * 4);
   w.sums = take(static_cast<size_t>(delta_slots(total, nseq)) * Hv * 8);
   w.bytes = at + 256;
   return w;

@@ -24,7 +24,7 @@
 // (attn_delta_chain.cu): a CTA takes 32 of them.
 //
 // Precision: products run on bf16 with fp32 accumulators; an fp32 factor is split into three bf16
-// terms (24 bits), and for two such factors the six products of terms down to 2^-16 are summed.
+// terms (24 bits), and for two such factors the products of terms down to 2^-16 are summed.
 #pragma once
 
 #include "attn_chunk.cuh"
@@ -32,12 +32,27 @@
 namespace cattn {
 
 constexpr int kDelta = 64;                         // tokens of a chunk
-constexpr int kTerms = 3;                          // bf16 terms of an fp32 factor
+constexpr int kTerms = 3;                          // bf16 terms of an fp32 factor that the chain makes
 constexpr int kSideBytes = kDelta * 128;           // 64 rows of a 64-column panel
-constexpr int kJpTerm = 128 * 128;                 // one term of J (rows 0..63) over P~ (64..127)
+constexpr int kPieceBytes = 128 * 16;              // 8 columns (16 bytes a row) of J's and P~'s rows
+constexpr int kTermBytes = 8 * kPieceBytes;        // one term of them
 constexpr int kGateFloats = 256;
-// a chunk's record: the terms of J and P~ as a product reads them from shared memory, then the gates
-constexpr int kRecordBytes = kTerms * kJpTerm + kGateFloats * 4;
+
+// Two operands of 64 rows as one of 128: 16 rows of the first, 16 of the second, and so on.  The results of
+// either then lie in 16 lanes of each quarter of tensor memory, and all warps have some to read.  The row
+// of the first one's row t (the second one's is 16 further on):
+__host__ __device__ constexpr int lane_of(int t) { return t / 16 * 32 + t % 16; }
+constexpr int kOther = 16;
+
+// A chunk's record: two terms of J and P~ (rows as above), the gates, the third terms.  A piece holds 8 columns
+// of all rows, one row after the other: threads that own rows write whole lines, and a product can take either
+// the rows or the columns as the contraction.  Pieces 2i and 2i + 1 of the first term are followed by those
+// of the second, so that with the columns as rows the two terms' products lie as the two operands do.
+constexpr int kRecordGates = 2 * kTermBytes, kRecordThird = kRecordGates + kGateFloats * 4;
+constexpr int kRecordBytes = kRecordThird + kTermBytes;
+__host__ __device__ constexpr int record_piece(int term, int piece, int row) {
+  return (term < 2 ? ((piece / 2) * 4 + term * 2 + piece % 2) * kPieceBytes : kRecordThird + piece * kPieceBytes) + row * 16;
+}
 enum DeltaGate : int { kEf = 0, kEb = 64, kBeta = 128, kTotal = 192 };  // floats of a record's gates
 
 // Chunk c of sequence i has record slot cu[i] / 64 + i + c: no two chunks share one, and there are
@@ -98,18 +113,6 @@ __device__ __forceinline__ void split8(const float* x, uint4 (&out)[kTerms]) {
   for (int s = 0; s < kTerms; ++s) out[s] = make_uint4(t[s][0], t[s][1], t[s][2], t[s][3]);
 }
 
-// Sixteen values of row `row` (column group cg of two) to the three terms at `base`.
-__device__ __forceinline__ void put_terms(uint32_t base, uint32_t panel, int row, int cg, const float* x) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint4 t[kTerms];
-    split8(x + 8 * i, t);
-    const uint32_t at = base + term_piece(row, cg * 2 + i);
-#pragma unroll
-    for (int s = 0; s < kTerms; ++s) sts128(at + s * panel, t[s].x, t[s].y, t[s].z, t[s].w);
-  }
-}
-
 // Contiguous bytes (a multiple of 16, both ends 16-byte aligned) from and to shared memory.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
@@ -124,25 +127,76 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
                : "memory");
 }
 
-// The chains' CTAs: 4 warps that move and multiply, 8 that own rows of the state and of the tokens,
-// 4 that copy first operands to tensor memory and do what the chain does not wait for.
-constexpr int kChainThreads = 512;
-constexpr int kRowWarps = 8, kCopyWarps = 4;
-// the rings: slots of K and Q, then of records, from a 1024-byte boundary
-constexpr int kStages = 2;
-constexpr int kStageKq = 2 * kPanelBytes;               // panels of 64 rows of K over 64 of Q
-constexpr int kOffRecords = kStages * kStageKq;
-constexpr int kRingBytes = kOffRecords + kStages * kRecordBytes;
+// The chains' CTAs: 4 warps that move and multiply, 8 that own rows (and 4 that prepare do).
+constexpr int kRowWarps = 8;
+constexpr int kSlotKq = 2 * kPanelBytes;                // a chunk's K and Q
+constexpr int kSlotBytes = kSlotKq + kRecordBytes;      // and its record
 constexpr int kStatePanel = 128 * kTermRow, kTokenPanel = kDelta * kTermRow;  // one term
 constexpr int kUTile = 2 * kTokenPanel;                 // two terms of u of a chunk, 32 columns
-// columns of tensor memory
-constexpr int kTmK = 0, kTmJ = 64, kTmAcc1 = 160, kTmAcc2 = 256, kTmOut1 = 320, kTmOut2 = 384;
 
 #define DELTA_WAIT(bar, phase) (wait_phase((bar), static_cast<uint32_t>(phase) & 1u))
 #define DELTA_WARP_WAIT(bar, phase) (__all_sync(0xffffffffu, DELTA_WAIT(bar, phase)))
 
-// The sum of the three terms' products, 16 columns of this thread's row.
-__device__ __forceinline__ void load_sum(uint32_t at, float* x) {
+// What a row warp has of 16 tokens and 16 columns: tokens lane / 4 and lane / 4 + 8, columns 2 (lane % 4) and the
+// next one, and those 8 further on, as pairs [columns][token].
+struct Pairs {
+  f2 v[2][2];
+};
+// 16 lanes and 16 columns of tensor memory.
+__device__ __forceinline__ void tmem_ld_pairs(uint32_t addr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_use8(uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(r[i]));
+}
+// The sum of N groups of kColumns columns, `step` columns apart.
+template <int N>
+__device__ __forceinline__ Pairs load_sum(uint32_t at, int step = kColumns) {
+  uint32_t a[N][8];
+#pragma unroll
+  for (int i = 0; i < N; ++i) tmem_ld_pairs(at + i * step, a[i]);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < N; ++i) tmem_use8(a[i]);
+  Pairs s;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      s.v[j][r] = pair(a[N - 1], 2 * j + r);
+#pragma unroll
+      for (int i = N - 2; i >= 0; --i) s.v[j][r] = f2_add(s.v[j][r], pair(a[i], 2 * j + r));
+    }
+  return s;
+}
+// Pairs of token row `row` (+ 8), columns of half h, to the three terms at `base`.
+__device__ __forceinline__ void put_pairs(uint32_t base, int row, int h, int lane, const Pairs& p) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const uint32_t at = base + term_piece(row + 8 * r, 2 * h + j) + (lane & 3) * 4;
+      f2 v = p.v[j][r];
+#pragma unroll
+      for (int s = 0; s < kTerms; ++s) {
+        const uint32_t w = f2_to_bf16x2(v);
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + s * kTokenPanel), "r"(w) : "memory");
+        if (s + 1 < kTerms) v = f2_fma(bf16x2_to_f2(w), f2_splat(-1.f), v);
+      }
+    }
+}
+// The words of a bf16 row at `src` (NULL: zeros) that hold this thread's pairs of columns.
+__device__ __forceinline__ void load_words(const uint16_t* src, int width, int lane, uint32_t (&x)[2]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    x[j] = src && 8 * j < width ? *reinterpret_cast<const uint32_t*>(src + 8 * j + 2 * (lane & 3)) : 0u;
+}
+
+// 16 columns of this thread's row in three terms of kColumns columns: the sum.
+__device__ __forceinline__ void load_sum16(uint32_t at, float* x) {
   uint32_t a[16], b[16], c[16];
   tmem_ld16(at, a);
   tmem_ld16(at + kColumns, b);
@@ -154,28 +208,7 @@ __device__ __forceinline__ void load_sum(uint32_t at, float* x) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(a[i]) + (__uint_as_float(b[i]) + __uint_as_float(c[i]));
 }
-
-// Eight columns of products whose accumulators lie in two groups of kColumns: the first terms', and
-// the small ones'.
-__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(addr));
-}
-__device__ __forceinline__ void tmem_use8(uint32_t* r) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(r[i]));
-}
-__device__ __forceinline__ void load_sum8(uint32_t at, float* x) {
-  uint32_t a[8], b[8];
-  tmem_ld8(at, a);
-  tmem_ld8(at + kColumns, b);
-  tmem_wait_ld();
-  tmem_use8(a);
-  tmem_use8(b);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
-}
+// Eight values of row `row` to the three terms at `base`.
 __device__ __forceinline__ void put_terms8(uint32_t base, uint32_t panel, int row, int piece, const float* x) {
   uint4 t[kTerms];
   split8(x, t);
@@ -193,46 +226,40 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
                     f2_to_bf16x2(f2_pack(x[4], x[5])), f2_to_bf16x2(f2_pack(x[6], x[7])));
 }
 
-// Row `row` of a 64-column panel (128 bytes, swizzled) to 32 columns of tensor memory; zeros unless `on`.
-__device__ __forceinline__ void copy_row(uint32_t tmem, uint32_t panel, int row, bool on) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t w[16];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (on) x = lds128_at(panel + swizzled(row, h * 4 + j));
-      w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
-    }
-    tmem_st16(tmem + 16 * h, w);
-  }
-}
-
-// One chunk's K and Q (a box of 64 channels and 64 tokens each, `panels` of them) and its record.
-__device__ __forceinline__ void load_kq(uint32_t smem, uint32_t bar, const CUtensorMap* mk, const CUtensorMap* mq,
-                                        int st, int panels, int hk, int row0) {
+// One chunk's K and Q, 16 tokens a box, `panels` of 64 channels.
+__device__ __forceinline__ void load_kq(uint32_t slot, uint32_t bar, const CUtensorMap* mk, const CUtensorMap* mq,
+                                        int panels, int hk, int row0) {
   bar_expect(bar, panels * 2 * kSideBytes);
 #pragma unroll 1
-  for (int j = 0; j < panels; ++j) {
-    load_box(smem + st * kStageKq + j * kPanelBytes, mk, bar, j * kPanelCols, hk, row0);
-    load_box(smem + st * kStageKq + j * kPanelBytes + kSideBytes, mq, bar, j * kPanelCols, hk, row0);
-  }
+  for (int j = 0; j < panels; ++j)
+#pragma unroll 1
+    for (int t = 0; t < kDelta; t += 16) {
+      const uint32_t dst = slot + j * kPanelBytes + lane_of(t) * 128;
+      load_box(dst, mk, bar, j * kPanelCols, hk, row0 + t);
+      load_box(dst + kOther * 128, mq, bar, j * kPanelCols, hk, row0 + t);
+    }
 }
-__device__ __forceinline__ void load_record(uint32_t smem, uint32_t bar, const uint8_t* record, int st) {
-  bar_expect(bar, kRecordBytes);
-  bulk_load(smem + kOffRecords + st * kRecordBytes, record, kRecordBytes, bar);
+// Zeroes the rows of tokens n on of a slot's K (and Q): rows of the next sequence must not meet a product over
+// the tokens, where 0 * NaN is not 0.  256 threads, i of them this one.
+__device__ __forceinline__ void zero_tokens(uint32_t slot, int panels, int n, bool q, int i) {
+  const int pieces = (kDelta - n) * 8, sides = q ? 2 : 1;
+  for (int e = i; e < panels * sides * pieces; e += 256) {
+    const int at = e % pieces, which = e / pieces;
+    const int row = lane_of(n + at / 8) + (which % sides) * kOther;
+    sts128(slot + which / sides * kPanelBytes + row * 128 + at % 8 * 16, 0, 0, 0, 0);
+  }
 }
 
-// A (rows of tensor memory at `a`, one term) times three terms of B side by side: the first two as 64
-// columns, the third one into the small ones' group.  `steps` of 16 rows of B.
-__device__ __forceinline__ void mma_terms(uint32_t acc, uint32_t a, uint64_t b, uint32_t panel, int steps) {
-  const uint32_t two = mma_desc(2 * kColumns, false, true), one = mma_desc(kColumns, false, true);
-#pragma unroll 1
-  for (int j = 0; j < steps; ++j) {
-    mma_ts(acc, a + j * 8, b + j * kTermStep, two, j > 0);
-    mma_ts(acc + kColumns, a + j * 8, b + (2 * panel >> 4) + j * kTermStep, one, true);
-  }
+// Descriptors of a record: rows as rows, and columns as rows.
+__device__ __forceinline__ uint64_t record_desc(uint32_t addr, bool columns) {
+  const uint64_t rows8 = 128 >> 4, piece = kPieceBytes >> 4;
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | ((columns ? rows8 : piece) << 16) |
+         ((columns ? piece : rows8) << 32) | (1ull << 46);
 }
+constexpr int kRecordCols = 4 * kPieceBytes / 16;  // descriptor units of 16 columns, and between the terms
+constexpr int kRecordTerm = 2 * kPieceBytes / 16;
+constexpr int kRecordRows = 32 * 16 / 16;          // of 16 of an operand's rows
+constexpr int kKqRows = 32 * 128 / 16;
 
 struct DeltaCall {
   Rows q, k, v, d_o;
@@ -251,7 +278,7 @@ struct DeltaCall {
   float* z;               // [total][Hv][V]
   uint8_t* u;             // [slots][Hv][tiles] two terms of u
   uint8_t *heads, *ends;  // [slots][Hv][tiles] first terms of S_0 and of D
-  float *odots, *vdots, *bdots;  // [tiles][Hv][total] parts of o . do, v . dv and dbeta
+  float *odots, *vdots, *bdots;  // [2 tiles][Hv][total] parts of o . do, v . dv and dbeta
   uint16_t *dq, *dk, *dv;
   float *dg, *dbeta, *dinit;
   double* sums;           // [Hv][slots] of the chunks' terms of dg

@@ -1,13 +1,14 @@
 // attn_delta_back.cu -- the gated delta rule's chain backwards: the gradient of the state.
 //
-// The CTAs, rings, terms and roles of attn_delta_chain.cu, from a sequence's last chunk to its first.
+// The CTAs, ring, terms and roles of attn_delta_chain.cu, from a sequence's last chunk to its first.
 // D, the gradient of the state at the chunk's end, is kept as S is there.  A chunk's products:
 //   K D                                   -> r' = eb . (K D),  X = beta r'
 //   J^T X;  P~^T do                       -> du = r' + J^T X + scale P~^T do,  dv = beta du
 //   K^T (-ef . dv);  Q^T (scale ef . do)  -> D = total D + ..
-// J and P~ are read from their records with the rows as the contraction, their 64 columns twice over (a
-// distance of 0 between the halves of A), so that here too all row warps have results to read.  The
-// products that have do in them wait for nothing of the chain; the copying warps prepare do for them.
+// J and P~ are read from their records with the rows as the contraction; the products of their first terms lie
+// in lanes 0 to 15 of each quarter, those of the second ones in lanes 16 to 31 (in place of Q D).  The products
+// that have do in them wait for nothing of the chain: P~^T do is made a chunk ahead, while the rows work; four
+// warps prepare do for them.
 // It leaves dv, the first term of every D, dbeta = du . z and v . dv.
 #include <cudaTypedefs.h>
 
@@ -27,15 +28,20 @@ static int read_fault(unsigned* out) {
 }
 static FaultReader reader(read_fault);
 
-// shared memory, from a 1024-byte boundary
-constexpr int kOffD = kRingBytes;
+constexpr int kBackThreads = (4 + kRowWarps + 4) * 32;
+// shared memory, from a 1024-byte boundary: a ring of two slots of K, Q and a record without its third terms;
+// these, the slots' pieces 2i and 2i + 1 in turn
+constexpr int kBackSlot = kSlotKq + kRecordThird;
+constexpr int kOffThird = 2 * kBackSlot;
+constexpr int kOffD = kOffThird + 2 * kTermBytes;
 constexpr int kOffDx = kOffD + kTerms * kStatePanel;      // X, then -ef . dv
 constexpr int kOffDo = kOffDx + kTerms * kTokenPanel;     // scale ef . do
-constexpr int kOffDoRaw = kOffDo + kTerms * kTokenPanel;  // do
-constexpr int kOffDots = kOffDoRaw + kTokenPanel;         // [2][4][64] parts of dbeta and v . dv
-constexpr int kOffBackBars = kOffDots + 2 * 4 * kDelta * 4;
+constexpr int kOffDoRaw = kOffDo + kTerms * kTokenPanel;  // do: two slots
+constexpr int kOffBackBars = kOffDoRaw + 2 * kTokenPanel;
 constexpr int kBackBytes = kOffBackBars + 24 * 8 + 1024;
 static_assert(kBackBytes <= 232448, "shared memory of one CTA");
+// columns of tensor memory: three accumulators of three terms, P~^T do; and what the third terms of P~ and J make
+constexpr int kTmFirst = 0, kTmSecond = 96, kTmThird = 192, kTmDo = 288, kTmDoLast = 320, kTmLast = 352;
 
 struct BackArgs {
   CUtensorMap mq, mk;
@@ -44,33 +50,31 @@ struct BackArgs {
   const uint8_t* records;
   const float* z;
   uint8_t* ends;          // [slots][Hv][tiles] first terms of D
-  float *vdots, *bdots;   // [tiles][Hv][total]
+  float *vdots, *bdots;   // [2 tiles][Hv][total]
   uint16_t* dv;
   float* dinit;
   float scale;
   int total, nseq, ratio, Hv, K, V, tiles;
 };
 
-__global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_back_kernel(const __grid_constant__ BackArgs p) {
+__global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const __grid_constant__ BackArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const uint32_t smem = smem_addr(base);
-  const uint32_t kqfull = smem + kOffBackBars, recfull = kqfull + 8 * kStages, empty = recfull + 8 * kStages;
-  const uint32_t kready = empty + 8 * kStages, oready = kready + 8;                    // by the copying warps
-  const uint32_t dready = oready + 8, xready = dready + 8, uready = xready + 8;        // by the rows
-  const uint32_t acc1 = uready + 8, acc2 = acc1 + 8, acc3 = acc2 + 8;                  // products
-  const uint32_t kept = acc3 + 8, dotsfree = kept + 8, alldone = dotsfree + 8;
-  float(*dots)[4][kDelta] = reinterpret_cast<float(*)[4][kDelta]>(base + kOffDots);
+  const uint32_t kfull = smem + kOffBackBars, rfull = kfull + 16, empty = rfull + 16, rawready = empty + 16;
+  const uint32_t oready = rawready + 16, dready = oready + 8, xready = dready + 8, uready = xready + 8;
+  const uint32_t acc1 = uready + 8, acc2 = acc1 + 8, acc3 = acc2 + 8;
+  const uint32_t kept = acc3 + 8, alldone = kept + 8;
   __shared__ uint32_t tmem_at;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      bar_init(kqfull + 8 * i, 1);
-      bar_init(recfull + 8 * i, 1);
-      bar_init(empty + 8 * i, 1 + kRowWarps + kCopyWarps);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(kfull + 8 * i, 1);
+      bar_init(rfull + 8 * i, 1);
+      bar_init(empty + 8 * i, 1 + kRowWarps + 4);
+      bar_init(rawready + 8 * i, 4);
     }
-    bar_init(kready, kCopyWarps);
-    bar_init(oready, kCopyWarps);
+    bar_init(oready, 4);
     bar_init(dready, kRowWarps);
     bar_init(xready, kRowWarps);
     bar_init(uready, kRowWarps);
@@ -78,7 +82,6 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_back_kernel(cons
     bar_init(acc2, 1);
     bar_init(acc3, 1);
     bar_init(kept, 1);
-    bar_init(dotsfree, 1);
     bar_init(alldone, 1);
     cconv::fence_mbar_init();
   }
@@ -101,23 +104,31 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_back_kernel(cons
   bool ok = true;
 
   if (warp == 0) {
-    // ---- tiles and records ----
+    // ---- K, Q and records ----
     if (elect_one()) {
       const int hk = hv / p.ratio;
       int i = 0, part = 0;
       for (; i < chunks && ok; ++i) {
-        const int st = i % kStages, c = chunks - 1 - i;
-        if (i >= kStages && !(ok = DELTA_WAIT(empty + 8 * st, i / kStages - 1))) break;
+        const int st = i & 1, c = chunks - 1 - i;
+        const uint32_t slot = smem + st * kBackSlot;
+        if (i >= 2 && !(ok = DELTA_WAIT(empty + 8 * st, i / 2 - 1))) break;
         if (i > 0 && !(ok = DELTA_WAIT(acc1, i - 1))) break;
-        load_kq(smem, kqfull + 8 * st, &p.mk, &p.mq, st, panels, hk, row_a + c * kDelta);
+        // (the record first: P~^T do needs it, and before the chunk's other products)
+        bar_expect(rfull + 8 * st, kRecordBytes);
+        const uint8_t* record = p.records + ((slot0 + c) * p.Hv + hv) * kRecordBytes;
+        bulk_load(slot + kSlotKq, record, kRecordThird, rfull + 8 * st);
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j)
+          bulk_load(smem + kOffThird + (2 * j + st) * 2 * kPieceBytes, record + kRecordThird + j * 2 * kPieceBytes,
+                    2 * kPieceBytes, rfull + 8 * st);
         part = 1;
         if (i > 0 && !(ok = DELTA_WAIT(acc2, i - 1))) break;
-        load_record(smem, recfull + 8 * st, p.records + ((slot0 + c) * p.Hv + hv) * kRecordBytes, st);
+        load_kq(slot, kfull + 8 * st, &p.mk, &p.mq, panels, hk, row_a + c * kDelta);
         part = 0;
       }
-      for (int st = 0; st < kStages; ++st) {
-        drain(kqfull + 8 * st, (i + part - st + kStages - 1) / kStages);
-        drain(recfull + 8 * st, (i - st + kStages - 1) / kStages);
+      for (int st = 0; st < 2; ++st) {
+        drain(rfull + 8 * st, (i + part - st + 1) / 2);
+        drain(kfull + 8 * st, (i - st + 1) / 2);
       }
     }
   } else if (warp == 1) {
@@ -125,55 +136,67 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_back_kernel(cons
     if (elect_one()) {
       const int ksteps = (p.K + 15) / 16;
       const uint64_t dd = term_desc(smem + kOffD, kStatePanel), dx = term_desc(smem + kOffDx, kTokenPanel);
-      const uint64_t dos = term_desc(smem + kOffDo, kTokenPanel), raw_do = term_desc(smem + kOffDoRaw, kTokenPanel);
-      const uint32_t three = mma_desc(3 * kColumns, true, true), two = mma_desc(2 * kColumns, true, true);
+      const uint64_t dos = term_desc(smem + kOffDo, kTokenPanel);
+      const uint32_t rows = mma_desc(3 * kColumns, false, true), three = mma_desc(3 * kColumns, true, true);
       const uint32_t one = mma_desc(kColumns, true, true);
-      constexpr uint32_t kThirdX = 2 * kTokenPanel / 16, kTerm = kJpTerm / 16;
+      auto early = [&](int i) {  // P~^T do of chunk i
+        const int st = i & 1;
+        if (!(ok = DELTA_WAIT(rfull + 8 * st, i / 2)) || !(ok = DELTA_WAIT(rawready + 8 * st, i / 2))) return;
+        tc_fence_after();
+        const uint64_t dp = record_desc(smem + st * kBackSlot + kSlotKq + kOther * 16, true);
+        const uint64_t from = term_desc(smem + kOffDoRaw + st * kTokenPanel, kTokenPanel);
+#pragma unroll 1
+        for (int j = 0; j < kDelta / 16; ++j)
+          mma_ss(tmem + kTmDo, dp + j * kRecordRows, from + j * kTermStep, one, j > 0);
+        // (third terms: lanes 16 to 31 of each quarter, the other slot's, are not read)
+        const uint64_t third = record_desc(smem + kOffThird + st * 2 * kPieceBytes + kOther * 16, true);
+#pragma unroll 1
+        for (int j = 0; j < kDelta / 16; ++j)
+          mma_ss(tmem + kTmDoLast, third + j * kRecordRows, from + j * kTermStep, one, j > 0);
+      };
+      if (chunks > 0) early(0);
       for (int i = 0; i < chunks && ok; ++i) {
-        const int st = i % kStages;
-        const uint32_t kq = smem + st * kStageKq, rec = smem + kOffRecords + st * kRecordBytes;
-        if (!(ok = DELTA_WAIT(kready, i))) break;
+        const int st = i & 1;
+        const uint32_t slot = smem + st * kBackSlot;
+        if (!(ok = DELTA_WAIT(kfull + 8 * st, i / 2))) break;
         if (!(ok = DELTA_WAIT(dready, i))) break;
         tc_fence_after();
-        mma_terms(tmem + kTmAcc1, tmem + kTmK, dd, kStatePanel, ksteps);  // K D
+        const uint64_t dkq = tile_desc(slot, 0);
+#pragma unroll 1
+        for (int j = 0; j < ksteps; ++j)  // K D
+          mma_ss(tmem + kTmFirst, dkq + col_step(j), dd + j * kTermStep, rows, j > 0);
         mma_commit(acc1);
-        if (!(ok = DELTA_WAIT(oready, i))) break;
-        tc_fence_after();
-        const uint64_t dj = tile_desc(rec, 0), dp = tile_desc(rec + kSideBytes, 0);
-#pragma unroll 1
-        for (int s = 0; s < kTerms; ++s)
-#pragma unroll 1
-          for (int j = 0; j < kDelta / 16; ++j)  // P~^T do
-            mma_ss(tmem + kTmOut1, dp + s * kTerm + j * kRowStep, raw_do + j * kTermStep, one, s + j > 0);
         if (!(ok = DELTA_WAIT(xready, i))) break;
         tc_fence_after();
+        const uint64_t dj = record_desc(slot + kSlotKq, true);
 #pragma unroll 1
-        for (int j = 0; j < kDelta / 16; ++j) {  // J^T X, terms down to 2^-16
-          const uint64_t a = dj + j * kRowStep, x = dx + j * kTermStep;
-          mma_ss(tmem + kTmAcc2, a, x, two, j > 0);
-          mma_ss(tmem + kTmAcc2 + kColumns, a, x + kThirdX, one, true);
-          mma_ss(tmem + kTmAcc2, a + kTerm, x, two, true);
-          mma_ss(tmem + kTmAcc2 + kColumns, a + 2 * kTerm, x, one, true);
-        }
+        for (int j = 0; j < kDelta / 16; ++j)  // J^T X
+          mma_ss(tmem + kTmSecond, dj + j * kRecordRows, dx + j * kTermStep, three, j > 0);
+        const uint64_t third = record_desc(smem + kOffThird + st * 2 * kPieceBytes, true);
+#pragma unroll 1
+        for (int j = 0; j < kDelta / 16; ++j)
+          mma_ss(tmem + kTmLast, third + j * kRecordRows, dx + j * kTermStep, one, j > 0);
         mma_commit(acc2);
         const bool more = i + 1 < chunks || p.dinit;
+        if (!(ok = DELTA_WAIT(oready, i))) break;
+        tc_fence_after();
         if (more) {
-          // (acc1's results were read before xready)
-          const uint64_t da = tile_desc(kq + kSideBytes, kPanelBytes);  // Q^T (scale ef . do)
+          const uint64_t da = tile_desc(slot + kOther * 128, kPanelBytes);  // Q^T (scale ef . do)
 #pragma unroll 1
           for (int j = 0; j < kDelta / 16; ++j)
-            mma_ss(tmem + kTmAcc1, da + j * kRowStep, dos + j * kTermStep, three, j > 0);
+            mma_ss(tmem + kTmThird, da + j * kKqRows, dos + j * kTermStep, three, j > 0);
         }
         if (!(ok = DELTA_WAIT(uready, i))) break;
         tc_fence_after();
         if (more) {
-          const uint64_t da = tile_desc(kq, kPanelBytes);  // K^T (-ef . dv)
+          const uint64_t da = tile_desc(slot, kPanelBytes);  // K^T (-ef . dv)
 #pragma unroll 1
           for (int j = 0; j < kDelta / 16; ++j)
-            mma_ss(tmem + kTmAcc1, da + j * kRowStep, dx + j * kTermStep, three, true);
+            mma_ss(tmem + kTmThird, da + j * kKqRows, dx + j * kTermStep, three, true);
           mma_commit(acc3);
         }
         mma_commit(empty + 8 * st);
+        if (i + 1 < chunks) early(i + 1);
       }
       mma_commit(alldone);
       drain(alldone, 1);
@@ -191,69 +214,33 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_back_kernel(cons
       }
       stores_wait();
     }
-  } else if (warp == 3) {
-    // ---- dbeta and v . dv of the tokens, from their four parts ----
-    for (int i = 0; i < chunks; ++i) {
-      const int row0 = row_a + (chunks - 1 - i) * kDelta, n = min(kDelta, row_b - row0);
-      if (!(ok = DELTA_WARP_WAIT(uready, i))) break;
-      float x[2][2];
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int t = j * 32 + lane;
-          x[a][j] = (dots[a][0][t] + dots[a][1][t]) + (dots[a][2][t] + dots[a][3][t]);
-        }
-      __syncwarp();
-      if (lane == 0) bar_arrive(dotsfree);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int t = j * 32 + lane;
-        if (t >= n) continue;
-        const int64_t at = (static_cast<int64_t>(tile) * p.Hv + hv) * p.total + row0 + t;
-        p.bdots[at] = x[0][j];
-        p.vdots[at] = x[1][j];
-      }
-    }
-  } else if (warp >= 12) {
-    // ---- K to tensor memory; do, raw and scaled, to shared memory ----
-    const int quarter = warp % 4, t = (quarter & 1) * 32 + lane, half = quarter >> 1;
-    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+  } else if (warp >= 4 + kRowWarps) {
+    // ---- do, as it is (a chunk ahead) and scaled: 16 columns of a token ----
+    const int t = (warp & 1) * 32 + lane, half = (warp - 4 - kRowWarps) / 2;
     const int col = col0 + half * 16, width = p.V - col;
     const uint16_t* src = p.d_o.p + hv * p.d_o.sh + col;
-    for (int i = 0; i < chunks; ++i) {
-      const int st = i % kStages, row0 = row_a + (chunks - 1 - i) * kDelta, n = min(kDelta, row_b - row0);
-      uint4 in[2];
+    uint4 in[2];
+    auto put_raw = [&](int i) {
+      const int64_t at = static_cast<int64_t>(row_a) + (chunks - 1 - i) * kDelta + t;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         in[j] = make_uint4(0, 0, 0, 0);
-        if (t < n && 8 * j < width)
-          in[j] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(row0 + t) * p.d_o.st + 8 * j);
+        if (at < row_b && 8 * j < width) in[j] = *reinterpret_cast<const uint4*>(src + at * p.d_o.st + 8 * j);
+        sts128(smem + kOffDoRaw + (i & 1) * kTokenPanel + term_piece(t, half * 2 + j), in[j].x, in[j].y, in[j].z, in[j].w);
       }
-      if (!(ok = DELTA_WARP_WAIT(kqfull + 8 * st, i / kStages))) break;
-      if (n < kDelta) {
-        // rows of the next sequence must not meet K^T and Q^T
-        if (t >= n)
-          for (int k = 0; k < panels; ++k)
-            for (int j = 0; j < 8; ++j)
-              sts128(smem + st * kStageKq + k * kPanelBytes + swizzled(half * kDelta + t, j), 0, 0, 0, 0);
-        cconv::fence_proxy_async_smem();
-      }
-      if (i > 0 && !(ok = DELTA_WARP_WAIT(acc1, i - 1))) break;
-      tc_fence_after();
-      for (int k = 0; k < panels; ++k)
-        copy_row(tmem + lanes + kTmK + 32 * k, smem + st * kStageKq + k * kPanelBytes, t, t < n);
-      tmem_wait_st();
-      tc_fence_before();
+      cconv::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) bar_arrive(kready);
-      if (!(ok = DELTA_WARP_WAIT(recfull + 8 * st, i / kStages))) break;
-      const float f = p.scale * reinterpret_cast<const float*>(base + kOffRecords + st * kRecordBytes + kTerms * kJpTerm)[kEf + t];
-      if (i > 0 && !(ok = DELTA_WARP_WAIT(acc3, i - 1))) break;  // the last chunk's do is not needed any more
+      if (lane == 0) bar_arrive(rawready + 8 * (i & 1));
+    };
+    if (chunks > 0) put_raw(0);
+    for (int i = 0; i < chunks; ++i) {
+      const int st = i & 1;
+      if (!(ok = DELTA_WARP_WAIT(rfull + 8 * st, i / 2))) break;
+      const float f = p.scale * reinterpret_cast<const float*>(base + st * kBackSlot + kSlotKq + kRecordGates)[kEf + t];
+      if (i > 0 && !(ok = DELTA_WARP_WAIT(acc3, i - 1))) break;  // the last chunk's are not needed any more
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float x[8];
-        sts128(smem + kOffDoRaw + term_piece(t, half * 2 + j), in[j].x, in[j].y, in[j].z, in[j].w);
         unpack8(in[j], x);
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] *= f;
@@ -263,93 +250,128 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_back_kernel(cons
       __syncwarp();
       if (lane == 0) bar_arrive(oready);
       if (lane == 0) bar_arrive(empty + 8 * st);
+      // (P~^T do of chunk i - 1, the last reader of that slot, was done before its acc3)
+      if (i + 1 < chunks) put_raw(i + 1);
     }
   } else if (warp >= 4) {
-    // ---- rows: 16 columns of a channel of D, 8 columns of a token ----
-    const int quarter = warp % 4, half = warp / 4 - 1;
-    const int row = quarter * 32 + lane, col = col0 + half * 16, width = p.V - col;
-    const int t = (quarter & 1) * 32 + lane, piece = (quarter >> 1) * 2 + half;
-    const int tcol = col0 + piece * 8;
-    const bool there = tcol < p.V;
-    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    // ---- rows: 16 columns of a channel of D; pairs of columns of two tokens ----
+    const int quarter = warp % 4, h = warp / 4 - 1;
+    const int row = quarter * 32 + lane, col = col0 + h * 16, width = p.V - col;
+    const int t = quarter * 16 + lane / 4;
+    const uint32_t mine = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + h * 16;
+    const uint32_t other = mine + (static_cast<uint32_t>(kOther) << 16);
     float D[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) D[i] = 0.f;
-    put_terms(smem + kOffD, kStatePanel, row, half, D);
+    put_terms8(smem + kOffD, kStatePanel, row, 2 * h, D);
+    put_terms8(smem + kOffD, kStatePanel, row, 2 * h + 1, D + 8);
     cconv::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) bar_arrive(dready);
-    const uint16_t* v_at = p.v.p + hv * p.v.sh + tcol;
-    uint4 vin;
-    float4 zin[2];
+    const uint16_t* v_at = p.v.p + hv * p.v.sh + col;
+    uint32_t vw[2][2];
+    Pairs zin;
     auto fetch = [&](int c) {
-      const int64_t at = static_cast<int64_t>(row_a) + c * kDelta + t;
-      vin = make_uint4(0, 0, 0, 0);
-      zin[0] = zin[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c >= 0 && at < row_b && there) {
-        vin = *reinterpret_cast<const uint4*>(v_at + at * p.v.st);
-        const float4* z = reinterpret_cast<const float4*>(p.z + (at * p.Hv + hv) * p.V + tcol);
-        zin[0] = z[0], zin[1] = z[1];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int64_t at = static_cast<int64_t>(row_a) + c * kDelta + t + 8 * r;
+        const bool on = c >= 0 && at < row_b;
+        load_words(on ? v_at + at * p.v.st : nullptr, width, lane, vw[r]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          zin.v[j][r] = on && 8 * j < width ? *reinterpret_cast<const f2*>(p.z + (at * p.Hv + hv) * p.V + col + 8 * j + 2 * (lane & 3)) : 0;
       }
     };
     fetch(chunks - 1);
     for (int i = 0; i < chunks; ++i) {
-      const int st = i % kStages, c = chunks - 1 - i, row0 = row_a + c * kDelta, n = min(kDelta, row_b - row0);
-      const float* gates = reinterpret_cast<const float*>(base + kOffRecords + st * kRecordBytes + kTerms * kJpTerm);
-      float v[8], r[8], y[8];
-      unpack8(vin, v);
-      const float z[8] = {zin[0].x, zin[0].y, zin[0].z, zin[0].w, zin[1].x, zin[1].y, zin[1].z, zin[1].w};
+      const int st = i & 1, c = chunks - 1 - i, row0 = row_a + c * kDelta, n = min(kDelta, row_b - row0);
+      const float* gates = reinterpret_cast<const float*>(base + st * kBackSlot + kSlotKq + kRecordGates);
+      Pairs v, z = zin;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) v.v[j][r] = bf16x2_to_f2(vw[r][j]);
       fetch(c - 1);
-      if (!(ok = DELTA_WARP_WAIT(recfull + 8 * st, i / kStages))) break;
-      const float ef = gates[kEf + t], eb = gates[kEb + t], beta = gates[kBeta + t], total = gates[kTotal];
+      if (!(ok = DELTA_WARP_WAIT(rfull + 8 * st, i / 2))) break;
+      float ef[2], eb[2], beta[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) ef[r] = gates[kEf + t + 8 * r], eb[r] = gates[kEb + t + 8 * r], beta[r] = gates[kBeta + t + 8 * r];
+      const float total = gates[kTotal];
       if (!(ok = DELTA_WARP_WAIT(acc1, i))) break;
       tc_fence_after();
-      load_sum8(tmem + lanes + kTmAcc1 + piece * 8, r);
+      Pairs y = load_sum<3>(mine + kTmFirst), x;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        r[j] = t < n ? eb * r[j] : 0.f;
-        y[j] = beta * r[j];
-      }
-      put_terms8(smem + kOffDx, kTokenPanel, t, piece, y);
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          y.v[j][r] = f2_mul(f2_splat(eb[r]), y.v[j][r]);  // r'
+          if (t + 8 * r >= n) y.v[j][r] = 0;
+          x.v[j][r] = f2_mul(f2_splat(beta[r]), y.v[j][r]);
+        }
+      put_pairs(smem + kOffDx, t, h, lane, x);
+      if (n < kDelta) zero_tokens(smem + st * kBackSlot, panels, n, true, threadIdx.x - 128);
       cconv::fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(xready);
       if (!(ok = DELTA_WARP_WAIT(acc2, i))) break;
       tc_fence_after();
-      uint32_t d[8];
-      tmem_ld8(tmem + lanes + kTmOut1 + piece * 8, d);
-      load_sum8(tmem + lanes + kTmAcc2 + piece * 8, y);
-      tmem_use8(d);
-      float du_z = 0.f, dv_v = 0.f;
+      {
+        Pairs first = load_sum<3>(mine + kTmSecond), second = load_sum<3>(other + kTmSecond);
+        const Pairs a = load_sum<2>(mine + kTmDo), b = load_sum<1>(other + kTmDo), last = load_sum<1>(mine + kTmLast);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float du = t < n ? r[j] + fmaf(p.scale, __uint_as_float(d[j]), y[j]) : 0.f;
-        du_z = fmaf(du, z[j], du_z);
-        r[j] = beta * du;
-        dv_v = fmaf(r[j], v[j], dv_v);
-        y[j] = -ef * r[j];
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const f2 from_do = f2_mul(f2_splat(p.scale), f2_add(a.v[j][r], b.v[j][r]));
+            second.v[j][r] = f2_add(second.v[j][r], last.v[j][r]);
+            y.v[j][r] = f2_add(y.v[j][r], f2_add(from_do, f2_add(first.v[j][r], second.v[j][r])));  // du
+            if (t + 8 * r >= n) y.v[j][r] = 0;
+            x.v[j][r] = f2_mul(f2_splat(-ef[r] * beta[r]), y.v[j][r]);
+          }
       }
-      put_terms8(smem + kOffDx, kTokenPanel, t, piece, y);
+      put_pairs(smem + kOffDx, t, h, lane, x);
       cconv::fence_proxy_async_smem();
-      if (i > 0 && !(ok = DELTA_WARP_WAIT(dotsfree, i - 1))) break;
-      dots[0][piece][t] = du_z;
-      dots[1][piece][t] = dv_v;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(uready);
-      if (t < n && there)
-        *reinterpret_cast<uint4*>(p.dv + (static_cast<int64_t>(row0 + t) * p.Hv + hv) * p.V + tcol) = pack8(r);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const bool on = t + 8 * r < n;
+        float du_z = 0.f, dv_v = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const f2 dv = f2_mul(f2_splat(beta[r]), y.v[j][r]);
+          float a, b;
+          cconv::f2_unpack(f2_mul(y.v[j][r], z.v[j][r]), a, b);
+          du_z += a + b;
+          cconv::f2_unpack(f2_mul(dv, v.v[j][r]), a, b);
+          dv_v += a + b;
+          if (on && 8 * j < width)
+            *reinterpret_cast<uint32_t*>(p.dv + (static_cast<int64_t>(row0 + t + 8 * r) * p.Hv + hv) * p.V + col + 8 * j +
+                                         2 * (lane & 3)) = f2_to_bf16x2(dv);
+        }
+        du_z += __shfl_xor_sync(0xffffffffu, du_z, 1);
+        dv_v += __shfl_xor_sync(0xffffffffu, dv_v, 1);
+        du_z += __shfl_xor_sync(0xffffffffu, du_z, 2);
+        dv_v += __shfl_xor_sync(0xffffffffu, dv_v, 2);
+        if (on && (lane & 3) == 0) {
+          const int64_t at = (static_cast<int64_t>(tile * 2 + h) * p.Hv + hv) * p.total + row0 + t + 8 * r;
+          p.bdots[at] = du_z;
+          p.vdots[at] = dv_v;
+        }
+      }
       if (i + 1 < chunks || p.dinit) {
-        float x[16];
+        float g[16];
         if (!(ok = DELTA_WARP_WAIT(acc3, i))) break;
         tc_fence_after();
-        load_sum(tmem + lanes + kTmAcc1 + half * 16, x);
+        load_sum16(mine + kTmThird, g);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) D[j] = row < p.K ? fmaf(total, D[j], x[j]) : 0.f;
+        for (int j = 0; j < 16; ++j) D[j] = row < p.K ? fmaf(total, D[j], g[j]) : 0.f;
         if (i + 1 < chunks) {
           if (!(ok = DELTA_WARP_WAIT(kept, i))) break;
-          put_terms(smem + kOffD, kStatePanel, row, half, D);
+          put_terms8(smem + kOffD, kStatePanel, row, 2 * h, D);
+          put_terms8(smem + kOffD, kStatePanel, row, 2 * h + 1, D + 8);
           cconv::fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
@@ -379,8 +401,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_back_kernel(cons
 int launch_delta_back(const DeltaCall& c, cudaStream_t stream) {
   BackArgs a{};
   int rc = bind_context();
-  if (rc == CCONV_OK) rc = encode_tile_map(&a.mq, c.q, c.s.total, c.s.Hk, c.s.K, kDelta);
-  if (rc == CCONV_OK) rc = encode_tile_map(&a.mk, c.k, c.s.total, c.s.Hk, c.s.K, kDelta);
+  if (rc == CCONV_OK) rc = encode_tile_map(&a.mq, c.q, c.s.total, c.s.Hk, c.s.K, 16);
+  if (rc == CCONV_OK) rc = encode_tile_map(&a.mk, c.k, c.s.total, c.s.Hk, c.s.K, 16);
   if (rc != CCONV_OK) return rc;
   a.v = c.v, a.d_o = c.d_o;
   a.cu = c.cu;
@@ -395,7 +417,7 @@ int launch_delta_back(const DeltaCall& c, cudaStream_t stream) {
   const int64_t ctas = static_cast<int64_t>(c.s.nseq) * c.s.Hv * a.tiles;
   if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(cattn_delta_back_kernel), kBackBytes) != CCONV_OK)
     return CCONV_ERR_CUDA;
-  return launch_pdl(cattn_delta_back_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kChainThreads), kBackBytes,
+  return launch_pdl(cattn_delta_back_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kBackThreads), kBackBytes,
                     stream, a) == cudaSuccess
              ? CCONV_OK
              : CCONV_ERR_CUDA;

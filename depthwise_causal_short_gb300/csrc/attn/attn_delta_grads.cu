@@ -43,7 +43,7 @@ constexpr int kStepU = 2 * kUPart;
 constexpr int kStepBytes = kStepOut + 2 * kStepState + kStepU;
 constexpr int kGradStages = 2;
 constexpr int kOffGradKq = kGradStages * kStepBytes;
-constexpr int kOffZero = kOffGradKq + kStageKq;           // zeros; X, -Y; their second terms: 64 rows each
+constexpr int kOffZero = kOffGradKq + kSlotKq;           // zeros; X, -Y; their second terms: 64 rows each
 constexpr int kOffXy = kOffZero + kHalf;
 constexpr int kOffGates = kOffXy + 4 * kHalf;             // of two heads in turn
 constexpr int kHeadGates = 5 * kDelta;                    // floats
@@ -52,7 +52,8 @@ constexpr int kGradBytes = kOffGradBars + 24 * 8 + 1024;
 static_assert(kGradBytes <= 232448, "shared memory of one CTA");
 // columns of TMEM
 constexpr int kAccXy = 0, kAccState = 128, kAccEnd = 256, kAccIntra = 384;  // X, Y: two heads in turn
-constexpr int kGradThreads = 384;
+constexpr int kPartsAhead = 8;  // parts of the sums in flight
+constexpr int kGradThreads = 384, kGradRowWarps = 8;
 
 struct GradArgs {
   CUtensorMap mq, mk, mo, mv;  // q, k, do, dv
@@ -88,12 +89,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
     bar_init(kqfull, 1);
     bar_init(kqempty, 1);
     bar_init(xyfull, 1);
-    bar_init(xyready, kRowWarps);
+    bar_init(xyready, kGradRowWarps);
     bar_init(headfull, 1);
-    bar_init(headfree, kRowWarps);
+    bar_init(headfree, kGradRowWarps);
     for (int i = 0; i < 2; ++i) {
       bar_init(gready + 8 * i, 1);
-      bar_init(gfree + 8 * i, kRowWarps);
+      bar_init(gfree + 8 * i, kGradRowWarps);
     }
     bar_init(alldone, 1);
     cconv::fence_mbar_init();
@@ -247,18 +248,25 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
       if (!find_chunk(p.cu, p.nseq, p.total, slot, lane, row0, n)) continue;
       for (int h = 0; h < ratio; ++h) {
         const int hv = static_cast<int>(at % p.Hk) * ratio + h;
-        double x[2], up;
-        float db[2];
+        double x[2] = {0.0, 0.0}, up;
+        float db[2] = {0.f, 0.f};
+        for (int first = 0; first < 2 * p.tiles; first += kPartsAhead) {
+          float o[kPartsAhead][2], v[kPartsAhead][2], d[kPartsAhead][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {  // tokens 63 - 2 lane, 62 - 2 lane
-          const int t = kDelta - 1 - 2 * lane - j;
-          x[j] = 0.0, db[j] = 0.f;
-          if (t < n)
-#pragma unroll 4
-            for (int i = 0; i < p.tiles; ++i) {
-              const int64_t from = (static_cast<int64_t>(i) * p.Hv + hv) * p.total + row0 + t;
-              x[j] += static_cast<double>(__ldcs(p.odots + from)) - static_cast<double>(__ldcs(p.vdots + from));
-              db[j] += __ldcs(p.bdots + from);
+          for (int i = 0; i < kPartsAhead; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {  // tokens 63 - 2 lane, 62 - 2 lane
+              const int t = kDelta - 1 - 2 * lane - j;
+              const int64_t from = (static_cast<int64_t>(first + i) * p.Hv + hv) * p.total + row0 + t;
+              o[i][j] = v[i][j] = d[i][j] = 0.f;
+              if (t < n && first + i < 2 * p.tiles) o[i][j] = p.odots[from], v[i][j] = p.vdots[from], d[i][j] = p.bdots[from];
+            }
+#pragma unroll
+          for (int i = 0; i < kPartsAhead; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              x[j] += static_cast<double>(o[i][j]) - static_cast<double>(v[i][j]);
+              db[j] += d[i][j];
             }
         }
         up = x[0] + x[1];

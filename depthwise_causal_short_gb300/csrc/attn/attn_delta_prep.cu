@@ -41,17 +41,22 @@ struct PrepArgs {
 // X (1 + B M) = rows, from the last of N columns to the first, for two rows at once (a row of B M in
 // shared memory serves both): bm[s][i] = beta_i M_is, zero for i <= s.
 template <int N>
-__device__ __forceinline__ void solve(f2 (&x)[2][kDelta / 2], const float* bm) {
+__device__ __forceinline__ void solve(f2 (&x)[2][kDelta / 2], uint32_t bm) {
 #pragma unroll
   for (int s = N - 2; s >= 0; --s) {
     f2 acc[2][2] = {{0, 0}, {0, 0}};
+    // all reads of a step first: one after the other's use, each would wait for its own
+    uint4 m[N / 4];
+#pragma unroll
+    for (int q = N / 4 - 1; q >= (s + 1) / 4; --q) m[q] = lds128_at(bm + (s * kDelta + 4 * q) * 4);
 #pragma unroll
     for (int q = N / 4 - 1; q >= (s + 1) / 4; --q) {  // what the last step made comes last
-      const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(bm + s * kDelta + 4 * q);
+      const f2 lo = f2_pack(__uint_as_float(m[q].x), __uint_as_float(m[q].y));
+      const f2 hi = f2_pack(__uint_as_float(m[q].z), __uint_as_float(m[q].w));
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        acc[r][0] = f2_fma(x[r][2 * q], m.x, acc[r][0]);
-        acc[r][1] = f2_fma(x[r][2 * q + 1], m.y, acc[r][1]);
+        acc[r][0] = f2_fma(x[r][2 * q], lo, acc[r][0]);
+        acc[r][1] = f2_fma(x[r][2 * q + 1], hi, acc[r][1]);
       }
     }
 #pragma unroll
@@ -64,27 +69,17 @@ __device__ __forceinline__ void solve(f2 (&x)[2][kDelta / 2], const float* bm) {
   }
 }
 
-// A row's three terms to the record, 32 bytes (two swizzled pieces) at a time.
+// A row's three terms to the record (neighbouring threads have neighbouring rows).
 __device__ __forceinline__ void store_row(const f2 (&x)[kDelta / 2], uint8_t* record, int row) {
 #pragma unroll
-  for (int i = 0; i < kDelta / 16; ++i) {
-    uint4 t[2][kTerms];
+  for (int i = 0; i < kDelta / 8; ++i) {
+    uint4 t[kTerms];
+    float v[8];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float v[8];
+    for (int k = 0; k < 4; ++k) cconv::f2_unpack(x[4 * i + k], v[2 * k], v[2 * k + 1]);
+    split8(v, t);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) cconv::f2_unpack(x[8 * i + 4 * j + k], v[2 * k], v[2 * k + 1]);
-      split8(v, t[j]);
-    }
-    uint8_t* at = record + row * 128 + ((i ^ ((row >> 1) & 3)) << 5);
-    const bool swap = row & 1;
-#pragma unroll
-    for (int s = 0; s < kTerms; ++s) {
-      const uint4 a = swap ? t[1][s] : t[0][s], b = swap ? t[0][s] : t[1][s];
-      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at + s * kJpTerm), "r"(a.x), "r"(a.y),
-                   "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-                   : "memory");
-    }
+    for (int s = 0; s < kTerms; ++s) *reinterpret_cast<uint4*>(record + record_piece(s, i, row)) = t[s];
   }
 }
 
@@ -165,7 +160,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) cattn_delta_prep_kernel(const
       logs[t] = g[1];
       if (lane == 31) logs[t + 1] = 0.f;
       betas[t] = b[0], betas[t + 1] = b[1];
-      float2* gates = reinterpret_cast<float2*>(record + kTerms * kJpTerm) + lane;
+      float2* gates = reinterpret_cast<float2*>(record + kRecordGates) + lane;
       gates[kEf / 2] = make_float2(exp2_fast(before + g[0]), exp2_fast(before + g[0] + g[1]));
       gates[kEb / 2] = make_float2(exp2_fast(g[1] + after), exp2_fast(after));
       gates[kBeta / 2] = make_float2(b[0], b[1]);
@@ -213,11 +208,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4) cattn_delta_prep_kernel(const
     __syncthreads();
     // rows below 32 have zeros in the columns from 32 on
     if (warp == 0)
-      solve<kDelta / 2>(x, bm);
+      solve<kDelta / 2>(x, smem);
     else
-      solve<kDelta>(x, bm);
-    store_row(x[0], record, t);
-    store_row(x[1], record, kDelta + t);
+      solve<kDelta>(x, smem);
+    store_row(x[0], record, lane_of(t));
+    store_row(x[1], record, lane_of(t) + kOther);
     if (!ok) atomicOr(&g_fault_prep, kFaultWait);
   }
   tc_fence_before();
