@@ -261,6 +261,11 @@ constexpr int kRecordTerm = 2 * kPieceBytes / 16;
 constexpr int kRecordRows = 32 * 16 / 16;          // of 16 of an operand's rows
 constexpr int kKqRows = 32 * 128 / 16;
 
+// 128 rows of 16 columns, from shared memory to 8 columns of tensor memory: a first operand's k-step.
+__device__ __forceinline__ void tmem_copy(uint32_t tmem, uint64_t rows) {
+  asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(tmem), "l"(rows) : "memory");
+}
+
 struct DeltaCall {
   Rows q, k, v, d_o;
   Gates g, beta;          // (beta's values are taken as they are)

@@ -38,8 +38,8 @@ constexpr int kOffX = kOffState + kTerms * kStatePanel;  // X, then eb . u
 constexpr int kOffChainBars = kOffX + kTerms * kTokenPanel;
 constexpr int kChainBytes = kOffChainBars + 24 * 8 + 1024;
 static_assert(kChainBytes <= 232448, "shared memory of one CTA");
-// columns of tensor memory: three accumulators of three terms
-constexpr int kTmFirst = 0, kTmSecond = 96, kTmThird = 192;
+// columns of tensor memory: three accumulators of three terms, [K; Q], [J; P~]
+constexpr int kTmFirst = 0, kTmSecond = 96, kTmThird = 192, kTmKq = 288, kTmJp = 352;
 
 struct ChainArgs {
   CUtensorMap mq, mk;
@@ -167,29 +167,42 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
       const uint32_t three = mma_desc(3 * kColumns, false, true), two = mma_desc(2 * kColumns, false, true);
       const uint32_t one = mma_desc(kColumns, false, true);
       const uint32_t last = mma_desc(3 * kColumns, true, true);
+      auto copy_kq = [&](int c) {
+        const int st = c & 1;
+        if (!(ok = DELTA_WAIT(kfull + 8 * st, c / 2))) return;
+        const uint64_t dkq = tile_desc(smem + st * kSlotBytes, 0);
+#pragma unroll 1
+        for (int j = 0; j < ksteps; ++j) tmem_copy(tmem + kTmKq + 8 * j, dkq + col_step(j));
+      };
+      if (chunks > 0) copy_kq(0);
       for (int c = 0; c < chunks && ok; ++c) {
         const int st = c & 1;
         const uint32_t slot = smem + st * kSlotBytes;
-        if (!(ok = DELTA_WAIT(kfull + 8 * st, c / 2))) break;
         if (!(ok = DELTA_WAIT(sready, c))) break;
         tc_fence_after();
-        const uint64_t dkq = tile_desc(slot, 0);
 #pragma unroll 1
         for (int j = 0; j < ksteps; ++j)  // [K; Q] S
-          mma_ss(tmem + kTmFirst, dkq + col_step(j), ds + j * kTermStep, three, j > 0);
+          mma_ts(tmem + kTmFirst, tmem + kTmKq + 8 * j, ds + j * kTermStep, three, j > 0);
         mma_commit(acc1);
         if (!(ok = DELTA_WAIT(rfull + 8 * st, c / 2))) break;
-        if (!(ok = DELTA_WAIT(xready, c))) break;
-        tc_fence_after();
         const uint64_t djp = record_desc(slot + kSlotKq, false);
 #pragma unroll 1
+        for (int j = 0; j < kDelta / 16; ++j) {
+          tmem_copy(tmem + kTmJp + 8 * j, djp + j * kRecordCols);
+          tmem_copy(tmem + kTmJp + 32 + 8 * j, djp + j * kRecordCols + kRecordTerm);
+          tmem_copy(tmem + kTmJp + 64 + 8 * j, djp + kRecordThird / 16 + j * kRecordTerm);
+        }
+        if (!(ok = DELTA_WAIT(xready, c))) break;
+        tc_fence_after();
+#pragma unroll 1
         for (int j = 0; j < kDelta / 16; ++j) {  // [J; P~] X
-          mma_ss(tmem + kTmSecond, djp + j * kRecordCols, dx + j * kTermStep, three, j > 0);
-          mma_ss(tmem + kTmSecond, djp + j * kRecordCols + kRecordTerm, dx + j * kTermStep, two, true);
-          mma_ss(tmem + kTmSecond, djp + kRecordThird / 16 + j * kRecordTerm, dx + j * kTermStep, one, true);
+          mma_ts(tmem + kTmSecond, tmem + kTmJp + 8 * j, dx + j * kTermStep, three, j > 0);
+          mma_ts(tmem + kTmSecond, tmem + kTmJp + 32 + 8 * j, dx + j * kTermStep, two, true);
+          mma_ts(tmem + kTmSecond, tmem + kTmJp + 64 + 8 * j, dx + j * kTermStep, one, true);
         }
         mma_commit(acc2);
-        if (!(ok = DELTA_WAIT(uready, c))) break;
+        if (c + 1 < chunks) copy_kq(c + 1);
+        if (!ok || !(ok = DELTA_WAIT(uready, c))) break;
         tc_fence_after();
         if (c + 1 < chunks || keep) {
           const uint64_t da = tile_desc(slot, kPanelBytes);
