@@ -5,7 +5,10 @@
 // Bound by memory, as the linear attention's update: the fp32 state is read and written once.  A CTA
 // owns a slice of V columns of one row and head and keeps it in registers; S^T k and S^T q are summed
 // in one pass over it (o = scale (a S^T q + (q . k) u) needs no second one), the warps' parts meet in
-// shared memory in a fixed order, and only then is the new state made and written.
+// shared memory in a fixed order, and only then is the new state made and written.  So a CTA reads and writes
+// by turns, and it takes several on an SM to keep memory busy: slices of 64 columns, three CTAs.  256 rows of
+// 16 heads of 128 x 128: 84 us, 6.3 TB/s (94 % of a copy's rate); slices of 128 columns 118 us (two CTAs of 16
+// warps 101), of 32 columns, half lines, 117.
 #include "attn_linear.cuh"
 
 namespace cattn {
@@ -26,6 +29,7 @@ struct DeltaUpdateArgs {
   int slices;  // column slices of a head
 };
 
+
 constexpr int kWarps = 8;
 
 __device__ __forceinline__ void add_scaled(float4& a, float w, const float4& x) {
@@ -35,9 +39,9 @@ __device__ __forceinline__ void add_scaled(float4& a, float w, const float4& x) 
   a.w = fmaf(w, x.w, a.w);
 }
 
-// QUADS: column quads (4 columns) of a slice; 32 / QUADS rows of the state per warp access.
-template <int QUADS>
-__global__ void __launch_bounds__(kWarps * 32) cattn_delta_update_kernel(DeltaUpdateArgs p) {
+// QUADS: column quads (4 columns) of a slice; 32 / QUADS rows of the state per warp access.  CTAS: on an SM.
+template <int QUADS, int CTAS>
+__global__ void __launch_bounds__(kWarps * 32, CTAS) cattn_delta_update_kernel(DeltaUpdateArgs p) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
   constexpr int kPerWarp = 32 / QUADS;             // state rows of one warp access
@@ -163,7 +167,7 @@ extern "C" CCONV_API int cattn_delta_update(
   if (S < 1 || (state_indices ? S > CCONV_UPDATE_MAX_SLOTS : S < N)) return CCONV_ERR_SHAPE;
   if (!aligned(state, 16) || !aligned(status_dev, 4) || !aligned(state_indices, 4))
     return CCONV_ERR_ALIGN;
-  const int quads = static_cast<int>(V / 4) >= 32 ? 32 : static_cast<int>(V / 4) > 8 ? 16 : 8;
+  const int quads = V > 32 ? 16 : 8;
   DeltaUpdateArgs a{};
   a.slices = static_cast<int>((V / 4 + quads - 1) / quads);
   const int64_t ctas = N * Hv * a.slices;
@@ -187,9 +191,7 @@ extern "C" CCONV_API int cattn_delta_update(
   a.scale = scale;
   a.N = static_cast<int>(N), a.Hk = static_cast<int>(Hk), a.Hv = static_cast<int>(Hv);
   a.K = static_cast<int>(K), a.V = static_cast<int>(V);
-  auto kern = quads == 32   ? cattn_delta_update_kernel<32>
-              : quads == 16 ? cattn_delta_update_kernel<16>
-                            : cattn_delta_update_kernel<8>;
+  auto kern = quads == 16 ? cattn_delta_update_kernel<16, 3> : cattn_delta_update_kernel<8, 4>;
   return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kWarps * 32), 0, stream, a) ==
                  cudaSuccess
              ? CCONV_OK

@@ -28,57 +28,83 @@ struct LnArgs {
 };
 
 constexpr int kLnThreads = 256;
+constexpr int kLnAhead = 3;  // rows that the gradient's threads have on the way
 constexpr int kMaxNorm = 8192;
 constexpr int ln_threads(int group) { return group > kLnThreads ? group : group > 32 ? group : kLnThreads; }
-constexpr int kLnCtas = 8;  // CTAs of 256 threads an SM
+// Threads an SM that a kernel's registers leave room for: the grids are that many, and each CTA goes on to
+// the rows that are left.
+constexpr int kLnFwdRoom = 1024;
+constexpr int ln_bwd_room(int group, int pieces, bool gate) {
+  return pieces > 1 ? ln_threads(group) : group == 512 ? (gate ? 512 : 1024) : 768;
+}
 
 using cconv::f2_unpack;
 
-__device__ __forceinline__ void widen(const uint4& raw, float* x) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f2_unpack(bf16x2_to_f2(w[i]), x[2 * i], x[2 * i + 1]);
+// Eight values as four pairs.
+__device__ __forceinline__ void widen(const uint4& raw, f2 (&x)[4]) {
+  x[0] = bf16x2_to_f2(raw.x), x[1] = bf16x2_to_f2(raw.y), x[2] = bf16x2_to_f2(raw.z), x[3] = bf16x2_to_f2(raw.w);
 }
-__device__ __forceinline__ uint4 narrow(const float* x) {
-  return make_uint4(f2_to_bf16x2(f2_pack(x[0], x[1])), f2_to_bf16x2(f2_pack(x[2], x[3])),
-                    f2_to_bf16x2(f2_pack(x[4], x[5])), f2_to_bf16x2(f2_pack(x[6], x[7])));
+__device__ __forceinline__ uint4 narrow(const f2 (&x)[4]) {
+  return make_uint4(f2_to_bf16x2(x[0]), f2_to_bf16x2(x[1]), f2_to_bf16x2(x[2]), f2_to_bf16x2(x[3]));
+}
+__device__ __forceinline__ float both(f2 v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return a + b;
 }
 // Eight weights from channel c on.
-__device__ __forceinline__ void load_weights(const void* w, int wdt, int c, float rest, bool on, float* x) {
+__device__ __forceinline__ void load_weights(const void* w, int wdt, int c, float rest, bool on, f2 (&x)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = rest;
+  for (int i = 0; i < 4; ++i) x[i] = f2_splat(rest);
   if (!w || !on) return;
   if (wdt == CCONV_F32) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __ldg(static_cast<const float*>(w) + c + i);
+    for (int i = 0; i < 4; ++i)
+      x[i] = f2_pack(__ldg(static_cast<const float*>(w) + c + 2 * i), __ldg(static_cast<const float*>(w) + c + 2 * i + 1));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = cconv::bf16_to_f32(__ldg(static_cast<const unsigned short*>(w) + c + i));
-  }
-}
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + exp2_fast(-kLog2e * z)); }
-
-// The sums of a and b over the row's group.  Across warps by shared memory, in turn through two
-// buffers: whoever writes the one again has passed the barrier after the other's reads.
-template <int GROUP>
-__device__ __forceinline__ void group_sum(float& a, float& b, float2 (*buf)[32], int& turn) {
-#pragma unroll
-  for (int o = (GROUP < 32 ? GROUP : 32) / 2; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
-  if constexpr (GROUP > 32) {
-    float2* at = buf[turn];
-    turn ^= 1;
-    if (threadIdx.x % 32 == 0) at[threadIdx.x / 32] = make_float2(a, b);
-    __syncthreads();
-    a = b = 0.f;
-#pragma unroll
-    for (int i = 0; i < GROUP / 32; ++i) {
-      a += at[i].x;
-      b += at[i].y;
+    for (int i = 0; i < 4; ++i) {
+      const unsigned short* at = static_cast<const unsigned short*>(w) + c + 2 * i;
+      x[i] = f2_pack(cconv::bf16_to_f32(__ldg(at)), cconv::bf16_to_f32(__ldg(at + 1)));
     }
   }
+}
+// 1 / (1 + e^-z)
+__device__ __forceinline__ f2 sigmoid(f2 z) {
+  float a, b;
+  f2_unpack(f2_mul(z, f2_splat(-kLog2e)), a, b);
+  return f2_pack(__fdividef(1.f, 1.f + exp2_fast(a)), __fdividef(1.f, 1.f + exp2_fast(b)));
+}
+
+// The sums of N values over the row's group, in every thread of it.  Across warps by shared memory, in turn
+// through two buffers: whoever writes the one again has passed the barrier after the other's reads.  There
+// the warps' values are read a lane each and added up by shuffles (all of them read by all threads, the
+// sums were a third of the instructions for rows of 4096 channels).
+template <int GROUP, int N>
+__device__ __forceinline__ void group_sum(float (&a)[N], float2* buf, int& turn) {
+#pragma unroll
+  for (int o = (GROUP < 32 ? GROUP : 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] += __shfl_xor_sync(0xffffffffu, a[i], o);
+  if constexpr (GROUP > 32) {
+    constexpr int kGroupWarps = GROUP / 32;
+    float2* at = buf + turn * 32;
+    turn ^= 1;
+    if (threadIdx.x % 32 == 0) at[threadIdx.x / 32] = make_float2(a[0], a[N - 1]);
+    __syncthreads();
+    const float2 v = at[threadIdx.x % kGroupWarps];
+    a[0] = v.x, a[N - 1] = N > 1 ? v.y : v.x;
+#pragma unroll
+    for (int o = kGroupWarps / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) a[i] += __shfl_xor_sync(0xffffffffu, a[i], o);
+  }
+}
+
+// 16 bytes to shared memory, zeros (and nothing read) unless `in`.
+__device__ __forceinline__ void copy_async(uint4* dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(cconv::smem_addr(dst)), "l"(src), "r"(in ? 16 : 0)
+               : "memory");
 }
 
 // Row (t, h) and the step to this group's next one.
@@ -98,31 +124,34 @@ struct RowWalk {
 
 // Statistics of a row of x: x becomes n; returns r (0 for a row that is not there, whatever eps is).
 template <int GROUP, int PIECES>
-__device__ __forceinline__ float normalise(float (&x)[PIECES][8], const bool (&on)[PIECES], bool live, const LnArgs& p,
-                                           float2 (*buf)[32], int& turn) {
-  float m = 0.f, unused = 0.f;
+__device__ __forceinline__ float normalise(f2 (&x)[PIECES][4], const bool (&on)[PIECES], bool live, const LnArgs& p,
+                                           float2* buf, int& turn) {
   if (p.layer) {
+    f2 m = 0;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m += x[i][j];
-    group_sum<GROUP>(m, unused, buf, turn);
-    m *= p.inv;
+      for (int j = 0; j < 4; ++j) m = f2_add(m, x[i][j]);
+    float mean[1] = {both(m)};
+    group_sum<GROUP>(mean, buf, turn);
+    m = f2_splat(-mean[0] * p.inv);
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[i][j] = on[i] ? f2_add(x[i][j], m) : 0;
   }
-  float s = 0.f;
+  f2 q = 0;
 #pragma unroll
   for (int i = 0; i < PIECES; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[i][j] = on[i] ? x[i][j] - m : 0.f;
-      s = fmaf(x[i][j], x[i][j], s);
-    }
-  group_sum<GROUP>(s, unused, buf, turn);
-  const float r = live ? rsqrtf(fmaf(s, p.inv, p.eps)) : 0.f;
+    for (int j = 0; j < 4; ++j) q = f2_fma(x[i][j], x[i][j], q);
+  float s[1] = {both(q)};
+  group_sum<GROUP>(s, buf, turn);
+  const float r = live ? rsqrtf(fmaf(s[0], p.inv, p.eps)) : 0.f;
 #pragma unroll
   for (int i = 0; i < PIECES; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[i][j] *= r;
+    for (int j = 0; j < 4; ++j) x[i][j] = f2_mul(x[i][j], f2_splat(r));
   return r;
 }
 
@@ -130,12 +159,12 @@ template <int GROUP, int PIECES, bool GATE>
 __global__ void __launch_bounds__(ln_threads(GROUP)) cattn_layernorm_fwd_kernel(const LnArgs p) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
-  __shared__ float2 buf[2][32];
+  __shared__ float2 buf[64];
   int turn = 0;
   constexpr int kRows = ln_threads(GROUP) / GROUP;
   const int lane = threadIdx.x % GROUP;
   bool on[PIECES];
-  float w[PIECES][8], b[PIECES][8];
+  f2 w[PIECES][4], b[PIECES][4];
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
     const int c = (lane + i * GROUP) * 8;
@@ -162,7 +191,7 @@ __global__ void __launch_bounds__(ln_threads(GROUP)) cattn_layernorm_fwd_kernel(
   for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.rows;
        first += static_cast<int64_t>(gridDim.x) * kRows) {
     const int64_t row = at.r;
-    float x[PIECES][8];
+    f2 x[PIECES][4];
     uint4 z[PIECES];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
@@ -176,12 +205,12 @@ __global__ void __launch_bounds__(ln_threads(GROUP)) cattn_layernorm_fwd_kernel(
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
         if (!on[i]) continue;
-        float g[8];
+        f2 g[4];
         if (GATE) widen(z[i], g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[i][j] = fmaf(x[i][j], w[i][j], b[i][j]);
-          if (GATE) x[i][j] *= g[j] * sigmoid(g[j]);
+        for (int j = 0; j < 4; ++j) {
+          x[i][j] = f2_fma(x[i][j], w[i][j], b[i][j]);
+          if (GATE) x[i][j] = f2_mul(x[i][j], f2_mul(g[j], sigmoid(g[j])));
         }
         __stcs(reinterpret_cast<uint4*>(p.y + row * p.C + (lane + i * GROUP) * 8), narrow(x[i]));
       }
@@ -191,7 +220,7 @@ __global__ void __launch_bounds__(ln_threads(GROUP)) cattn_layernorm_fwd_kernel(
 
 // This CTA's sums s (of its groups' rows) to `dst` [C].
 template <int GROUP, int PIECES>
-__device__ __forceinline__ void put_sums(float (&s)[PIECES][8], const bool (&on)[PIECES], float* dst, int C,
+__device__ __forceinline__ void put_sums(f2 (&s)[PIECES][4], const bool (&on)[PIECES], float* dst, int C,
                                          float* shared) {
   const int lane = threadIdx.x % GROUP;
   if constexpr (GROUP > 32) {
@@ -200,17 +229,17 @@ __device__ __forceinline__ void put_sums(float (&s)[PIECES][8], const bool (&on)
       if (on[i])
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          *reinterpret_cast<float4*>(dst + (lane + i * GROUP) * 8 + 4 * j) =
-              make_float4(s[i][4 * j], s[i][4 * j + 1], s[i][4 * j + 2], s[i][4 * j + 3]);
+          *reinterpret_cast<ulonglong2*>(dst + (lane + i * GROUP) * 8 + 4 * j) = make_ulonglong2(s[i][2 * j], s[i][2 * j + 1]);
   } else {
     constexpr int kWarps = kLnThreads / 32, kPitch = GROUP * PIECES * 8;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
 #pragma unroll
-        for (int o = 16; o >= GROUP; o >>= 1) s[i][j] += __shfl_xor_sync(0xffffffffu, s[i][j], o);
-        if (threadIdx.x % 32 < GROUP) shared[threadIdx.x / 32 * kPitch + (lane + i * GROUP) * 8 + j] = s[i][j];
+        for (int o = 16; o >= GROUP; o >>= 1) s[i][j] = f2_add(s[i][j], __shfl_xor_sync(0xffffffffu, s[i][j], o));
+        if (threadIdx.x % 32 < GROUP)
+          *reinterpret_cast<f2*>(shared + threadIdx.x / 32 * kPitch + (lane + i * GROUP) * 8 + 2 * j) = s[i][j];
       }
     __syncthreads();
     for (int c = threadIdx.x; c < C; c += kLnThreads) {
@@ -224,94 +253,104 @@ __device__ __forceinline__ void put_sums(float (&s)[PIECES][8], const bool (&on)
 }
 
 template <int GROUP, int PIECES, bool GATE>
-__global__ void __launch_bounds__(ln_threads(GROUP), GROUP > 32 ? 512 / ln_threads(GROUP) : 2)
+__global__ void __launch_bounds__(ln_threads(GROUP), ln_bwd_room(GROUP, PIECES, GATE) / ln_threads(GROUP))
     cattn_layernorm_bwd_kernel(const LnArgs p) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
-  __shared__ float2 buf[2][32];
-  __shared__ float shared[GROUP > 32 ? 1 : kLnThreads / 32 * GROUP * PIECES * 8];
+  __shared__ float2 buf[64];
+  __shared__ alignas(8) float shared[GROUP > 32 ? 1 : kLnThreads / 32 * GROUP * PIECES * 8];
   int turn = 0;
   constexpr int kRows = ln_threads(GROUP) / GROUP;
   const int lane = threadIdx.x % GROUP;
   bool on[PIECES];
-  float w[PIECES][8], dw[PIECES][8], db[PIECES][8];
+  f2 w[PIECES][4], dw[PIECES][4], db[PIECES][4];
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
     const int c = (lane + i * GROUP) * 8;
     on[i] = c < p.C;
     load_weights(p.w, p.wdt, c, 1.f, on[i], w[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = 0;
   }
   RowWalk at(static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / GROUP,
              static_cast<int64_t>(gridDim.x) * kRows, p.H);
-  uint4 nx[PIECES], nz[PIECES], ny[PIECES];
-  auto fetch = [&] {
+  // each thread copies its pieces of the rows ahead into a place of its own in shared memory
+  extern __shared__ uint4 ring[];
+  constexpr int kTensors = GATE ? 3 : 2, kThreads = ln_threads(GROUP);
+  auto place = [&](int slot, int tensor, int i) { return ring + ((slot * kTensors + tensor) * PIECES + i) * kThreads + threadIdx.x; };
+  RowWalk ahead = at;
+  int slot = 0;
+  auto fetch = [&](int to) {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      nx[i] = nz[i] = ny[i] = make_uint4(0, 0, 0, 0);
-      if (at.r < p.rows && on[i]) {
-        const int c = (lane + i * GROUP) * 8;
-        nx[i] = __ldcs(reinterpret_cast<const uint4*>(p.x + at.t * p.sxt + at.h * p.sxh + c));
-        ny[i] = __ldcs(reinterpret_cast<const uint4*>(p.dy + at.t * p.syt + at.h * p.syh + c));
-        if (GATE) nz[i] = __ldcs(reinterpret_cast<const uint4*>(p.z + at.t * p.szt + at.h * p.szh + c));
-      }
+      const int c = (lane + i * GROUP) * 8;
+      const bool in = ahead.r < p.rows && on[i];
+      copy_async(place(to, 0, i), in ? p.x + ahead.t * p.sxt + ahead.h * p.sxh + c : p.x, in);
+      copy_async(place(to, 1, i), in ? p.dy + ahead.t * p.syt + ahead.h * p.syh + c : p.dy, in);
+      if (GATE) copy_async(place(to, 2, i), in ? p.z + ahead.t * p.szt + ahead.h * p.szh + c : p.z, in);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ahead.next();
   };
-  fetch();
+#pragma unroll
+  for (int i = 0; i < kLnAhead; ++i) fetch(i);
   for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.rows;
        first += static_cast<int64_t>(gridDim.x) * kRows) {
     const int64_t row = at.r;
-    float x[PIECES][8], du[PIECES][8];
+    at.r += at.step;
+    f2 x[PIECES][4], du[PIECES][4];
     uint4 z[PIECES];
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLnAhead - 1) : "memory");
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      widen(nx[i], x[i]);
-      widen(ny[i], du[i]);
-      z[i] = nz[i];
+      widen(*place(slot, 0, i), x[i]);
+      widen(*place(slot, 1, i), du[i]);
+      if (GATE) z[i] = *place(slot, 2, i);
     }
-    at.next();
-    fetch();
+    fetch(slot);
+    slot = slot + 1 == kLnAhead ? 0 : slot + 1;
     const float r = normalise<GROUP, PIECES>(x, on, row < p.rows, p, buf, turn);
-    float along = 0.f, sum = 0.f;
+    f2 dn_n = 0, dn = 0;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       if (GATE) {
-        float g[8], b[8];
+        f2 g[4], b[4];
         widen(z[i], g);
         load_weights(p.b, p.wdt, (lane + i * GROUP) * 8, 0.f, on[i], b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float s = sigmoid(g[j]), d = du[i][j] * s;
-          du[i][j] = d * g[j];
-          g[j] = d * fmaf(x[i][j], w[i][j], b[j]) * fmaf(g[j], 1.f - s, 1.f);
+        for (int j = 0; j < 4; ++j) {
+          const f2 one = f2_splat(1.f), minus = f2_splat(-1.f), s = sigmoid(g[j]), d = f2_mul(du[i][j], s);
+          du[i][j] = f2_mul(d, g[j]);
+          // silu'(z) = s (1 + z (1 - s))
+          g[j] = f2_mul(f2_mul(d, f2_fma(x[i][j], w[i][j], b[j])), f2_fma(g[j], f2_fma(s, minus, one), one));
         }
         if (row < p.rows && on[i])
           __stcs(reinterpret_cast<uint4*>(p.dz + row * p.C + (lane + i * GROUP) * 8), narrow(g));
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
         // (rows and channels that are not there have du = 0; x is finite there)
-        dw[i][j] = fmaf(du[i][j], x[i][j], dw[i][j]);
-        db[i][j] += du[i][j];
-        du[i][j] *= w[i][j];
-        along = fmaf(du[i][j], x[i][j], along);
-        sum += du[i][j];
+        dw[i][j] = f2_fma(du[i][j], x[i][j], dw[i][j]);
+        db[i][j] = f2_add(db[i][j], du[i][j]);
+        du[i][j] = f2_mul(du[i][j], w[i][j]);
+        dn_n = f2_fma(du[i][j], x[i][j], dn_n);
+        dn = f2_add(dn, du[i][j]);
       }
     }
-    group_sum<GROUP>(along, sum, buf, turn);
-    along *= p.inv;
-    sum = p.layer ? sum * p.inv : 0.f;
+    float sums[2] = {both(dn_n), both(dn)};
+    group_sum<GROUP>(sums, buf, turn);
+    const f2 a = f2_splat(-sums[0] * p.inv), m = f2_splat(p.layer ? -sums[1] * p.inv : 0.f), scale = f2_splat(r);
     if (row < p.rows) {
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
         if (!on[i]) continue;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[i][j] = r * (fmaf(-along, x[i][j], du[i][j]) - sum);
+        for (int j = 0; j < 4; ++j) x[i][j] = f2_mul(scale, f2_add(f2_fma(a, x[i][j], du[i][j]), m));
         __stcs(reinterpret_cast<uint4*>(p.y + row * p.C + (lane + i * GROUP) * 8), narrow(x[i]));
       }
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   if (!p.part) return;
   float* dst = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.C;
   put_sums<GROUP, PIECES>(dw, on, dst, p.C, shared);
@@ -348,26 +387,34 @@ struct LnKernel {
   void (*fwd[2])(LnArgs);
   void (*bwd[2])(LnArgs);
   int threads, rows;  // of a CTA
+  int bwd_bytes[2];   // of its shared memory
+  int bwd_room[2];
 };
 template <int GROUP, int PIECES>
 static LnKernel kernel_of() {
   return LnKernel{{cattn_layernorm_fwd_kernel<GROUP, PIECES, false>, cattn_layernorm_fwd_kernel<GROUP, PIECES, true>},
                   {cattn_layernorm_bwd_kernel<GROUP, PIECES, false>, cattn_layernorm_bwd_kernel<GROUP, PIECES, true>},
-                  ln_threads(GROUP), ln_threads(GROUP) / GROUP};
+                  ln_threads(GROUP), ln_threads(GROUP) / GROUP,
+                  {kLnAhead * 2 * PIECES * ln_threads(GROUP) * 16, kLnAhead * 3 * PIECES * ln_threads(GROUP) * 16},
+                  {ln_bwd_room(GROUP, PIECES, false), ln_bwd_room(GROUP, PIECES, true)}};
 }
-// The smallest group that holds a row in two pieces a thread at most (in one where a warp holds it).
+// The smallest group that holds a row in one piece a thread, to 512 threads: with two pieces (and 256 threads
+// for 4096 channels) the gradient's sums leave registers for half as many CTAs.
 static LnKernel pick(int64_t C) {
   if (C <= 32) return kernel_of<4, 1>();
   if (C <= 64) return kernel_of<8, 1>();
   if (C <= 128) return kernel_of<16, 1>();
   if (C <= 256) return kernel_of<32, 1>();
-  if (C <= 512) return kernel_of<32, 2>();
+  if (C <= 512) return kernel_of<64, 1>();
   if (C <= 1024) return kernel_of<128, 1>();
-  if (C <= 2048) return kernel_of<128, 2>();
-  if (C <= 4096) return kernel_of<256, 2>();
+  if (C <= 2048) return kernel_of<256, 1>();
+  if (C <= 4096) return kernel_of<512, 1>();
   return kernel_of<512, 2>();
 }
-static int64_t most_ctas(int sms, int threads) { return static_cast<int64_t>(sms) * (kLnCtas * kLnThreads / threads); }
+static int64_t ctas_of(int64_t rows, const LnKernel& kern, int sms, int room) {
+  const int64_t ctas = (rows + kern.rows - 1) / kern.rows, most = static_cast<int64_t>(sms) * (room / kern.threads);
+  return ctas < most ? ctas : most;
+}
 
 static int check(const void* x, int64_t sxt, int64_t sxh, const void* z, int64_t szt, int64_t szh, int64_t total,
                  int64_t H, int64_t C, const void* w, const void* b, cconv_dtype wdt, cattn_norm mode, float eps) {
@@ -413,21 +460,11 @@ extern "C" CCONV_API int cattn_layernorm_fwd(const void* x, int64_t sxt, int64_t
   int sms = 0;
   if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
   const LnKernel kern = pick(C);
-  const int64_t ctas = (a.rows + kern.rows - 1) / kern.rows, most = most_ctas(sms, kern.threads);
-  return launch_pdl(kern.fwd[gate != nullptr], dim3(static_cast<unsigned>(ctas < most ? ctas : most)),
-                    dim3(kern.threads), 0, stream, a) == cudaSuccess
+  const int64_t ctas = ctas_of(a.rows, kern, sms, kern.threads > kLnFwdRoom ? kern.threads : kLnFwdRoom);
+  return launch_pdl(kern.fwd[gate != nullptr], dim3(static_cast<unsigned>(ctas)), dim3(kern.threads), 0, stream, a) == cudaSuccess
              ? CCONV_OK
              : CCONV_ERR_CUDA;
 }
-
-namespace cattn {
-constexpr int kLnBwdCtas = 4;  // CTAs of 256 threads an SM
-static int64_t bwd_ctas(int sms, int64_t rows, const LnKernel& kern) {
-  const int64_t ctas = (rows + kern.rows - 1) / kern.rows;
-  const int64_t most = static_cast<int64_t>(sms) * (kLnBwdCtas * kLnThreads / kern.threads);
-  return ctas < most ? ctas : most;
-}
-}  // namespace cattn
 
 extern "C" CCONV_API int cattn_layernorm_bwd_workspace_bytes(int64_t total, int64_t H, int64_t C, size_t* bytes) {
   using namespace cattn;
@@ -435,7 +472,9 @@ extern "C" CCONV_API int cattn_layernorm_bwd_workspace_bytes(int64_t total, int6
   if (total < 0 || total > kMaxRows || H < 1 || H > 65535 || C < 1 || C > kMaxNorm) return CCONV_ERR_SHAPE;
   int sms = 0;
   if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
-  const int64_t ctas = bwd_ctas(sms, total * H, pick(C));
+  // (as many CTAs as either kernel, with a gate and without one, has)
+  const LnKernel kern = pick(C);
+  const int64_t ctas = ctas_of(total * H, kern, sms, kern.bwd_room[0]);
   *bytes = static_cast<size_t>(ctas > 0 ? ctas : 1) * 2 * static_cast<size_t>(C) * 4;
   return CCONV_OK;
 }
@@ -463,7 +502,7 @@ extern "C" CCONV_API int cattn_layernorm_bwd(const void* x, int64_t sxt, int64_t
   int sms = 0;
   if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
   const LnKernel kern = pick(C);
-  const int64_t ctas = bwd_ctas(sms, a.rows, kern);
+  const int64_t ctas = ctas_of(a.rows, kern, sms, kern.bwd_room[gate != nullptr]);
   const bool sums = dw || db;
   if (sums) {
     if (!workspace || workspace_bytes < static_cast<size_t>(ctas > 0 ? ctas : 1) * 2 * C * 4)
@@ -471,7 +510,11 @@ extern "C" CCONV_API int cattn_layernorm_bwd(const void* x, int64_t sxt, int64_t
     if (!aligned(workspace, 16)) return CCONV_ERR_ALIGN;
     a.part = static_cast<float*>(workspace);
   }
-  if (total > 0 && launch_pdl(kern.bwd[gate != nullptr], dim3(static_cast<unsigned>(ctas)), dim3(kern.threads), 0,
+  const int bytes = kern.bwd_bytes[gate != nullptr];
+  if (total > 0 && bytes > 32 * 1024 &&
+      cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(kern.bwd[gate != nullptr]), bytes) != CCONV_OK)
+    return CCONV_ERR_CUDA;
+  if (total > 0 && launch_pdl(kern.bwd[gate != nullptr], dim3(static_cast<unsigned>(ctas)), dim3(kern.threads), bytes,
                               stream, a) != cudaSuccess)
     return CCONV_ERR_CUDA;
   if (!sums) return CCONV_OK;
