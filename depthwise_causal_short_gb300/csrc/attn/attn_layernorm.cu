@@ -8,7 +8,7 @@
 //
 // Bound by memory: every tensor is read or written once, and the gradient makes the statistics again
 // from x, which it reads anyway.  A group of GROUP threads owns a row, 8 channels (16 bytes) of each
-// of PIECES pieces a thread; the next row's loads are issued before this row's sums.  The squares are
+// of PIECES pieces a thread; three rows ahead are on the way to shared memory.  The squares are
 // summed after the mean is known (as sum(x^2) - C m^2 they would cancel for rows far from zero).
 // The sums over rows stay in registers for all rows of a thread, meet in the CTA, and then, a row of
 // the workspace for each CTA, in a second kernel; in the same order in every run.
@@ -34,9 +34,7 @@ constexpr int ln_threads(int group) { return group > kLnThreads ? group : group 
 // Threads an SM that a kernel's registers leave room for: the grids are that many, and each CTA goes on to
 // the rows that are left.
 constexpr int kLnFwdRoom = 1024;
-constexpr int ln_bwd_room(int group, int pieces, bool gate) {
-  return pieces > 1 ? ln_threads(group) : group == 512 ? (gate ? 512 : 1024) : 768;
-}
+constexpr int ln_bwd_room(int pieces) { return pieces > 1 ? 512 : 768; }
 
 using cconv::f2_unpack;
 
@@ -172,34 +170,42 @@ __global__ void __launch_bounds__(ln_threads(GROUP)) cattn_layernorm_fwd_kernel(
     load_weights(p.w, p.wdt, c, 1.f, on[i], w[i]);
     load_weights(p.b, p.wdt, c, 0.f, on[i], b[i]);
   }
-  RowWalk at(static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / GROUP,
-             static_cast<int64_t>(gridDim.x) * kRows, p.H);
-  uint4 nx[PIECES], nz[PIECES];
-  auto fetch = [&] {
+  RowWalk ahead(static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / GROUP,
+                static_cast<int64_t>(gridDim.x) * kRows, p.H);
+  int64_t next = ahead.r;
+  // each thread copies its pieces of the rows ahead into a place of its own in shared memory
+  extern __shared__ uint4 ring[];
+  constexpr int kTensors = GATE ? 2 : 1, kThreads = ln_threads(GROUP);
+  auto place = [&](int slot, int tensor, int i) { return ring + ((slot * kTensors + tensor) * PIECES + i) * kThreads + threadIdx.x; };
+  int slot = 0;
+  auto fetch = [&](int to) {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      nx[i] = nz[i] = make_uint4(0, 0, 0, 0);
-      if (at.r < p.rows && on[i]) {
-        const int c = (lane + i * GROUP) * 8;
-        nx[i] = __ldcs(reinterpret_cast<const uint4*>(p.x + at.t * p.sxt + at.h * p.sxh + c));
-        if (GATE) nz[i] = __ldcs(reinterpret_cast<const uint4*>(p.z + at.t * p.szt + at.h * p.szh + c));
-      }
+      const int c = (lane + i * GROUP) * 8;
+      const bool in = ahead.r < p.rows && on[i];
+      copy_async(place(to, 0, i), in ? p.x + ahead.t * p.sxt + ahead.h * p.sxh + c : p.x, in);
+      if (GATE) copy_async(place(to, 1, i), in ? p.z + ahead.t * p.szt + ahead.h * p.szh + c : p.z, in);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ahead.next();
   };
-  fetch();
+#pragma unroll
+  for (int i = 0; i < kLnAhead; ++i) fetch(i);
   // (whole warps, and with GROUP > 32 whole CTAs, leave the loop together)
   for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.rows;
        first += static_cast<int64_t>(gridDim.x) * kRows) {
-    const int64_t row = at.r;
+    const int64_t row = next;
+    next += ahead.step;
     f2 x[PIECES][4];
     uint4 z[PIECES];
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLnAhead - 1) : "memory");
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      widen(nx[i], x[i]);
-      z[i] = nz[i];
+      widen(*place(slot, 0, i), x[i]);
+      if (GATE) z[i] = *place(slot, 1, i);
     }
-    at.next();
-    fetch();
+    fetch(slot);
+    slot = slot + 1 == kLnAhead ? 0 : slot + 1;
     normalise<GROUP, PIECES>(x, on, row < p.rows, p, buf, turn);
     if (row < p.rows) {
 #pragma unroll
@@ -216,6 +222,7 @@ __global__ void __launch_bounds__(ln_threads(GROUP)) cattn_layernorm_fwd_kernel(
       }
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // This CTA's sums s (of its groups' rows) to `dst` [C].
@@ -253,7 +260,7 @@ __device__ __forceinline__ void put_sums(f2 (&s)[PIECES][4], const bool (&on)[PI
 }
 
 template <int GROUP, int PIECES, bool GATE>
-__global__ void __launch_bounds__(ln_threads(GROUP), ln_bwd_room(GROUP, PIECES, GATE) / ln_threads(GROUP))
+__global__ void __launch_bounds__(ln_threads(GROUP), ln_bwd_room(PIECES) / ln_threads(GROUP))
     cattn_layernorm_bwd_kernel(const LnArgs p) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
@@ -272,13 +279,13 @@ __global__ void __launch_bounds__(ln_threads(GROUP), ln_bwd_room(GROUP, PIECES, 
 #pragma unroll
     for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = 0;
   }
-  RowWalk at(static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / GROUP,
-             static_cast<int64_t>(gridDim.x) * kRows, p.H);
+  RowWalk ahead(static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / GROUP,
+                static_cast<int64_t>(gridDim.x) * kRows, p.H);
+  int64_t next = ahead.r;
   // each thread copies its pieces of the rows ahead into a place of its own in shared memory
   extern __shared__ uint4 ring[];
   constexpr int kTensors = GATE ? 3 : 2, kThreads = ln_threads(GROUP);
   auto place = [&](int slot, int tensor, int i) { return ring + ((slot * kTensors + tensor) * PIECES + i) * kThreads + threadIdx.x; };
-  RowWalk ahead = at;
   int slot = 0;
   auto fetch = [&](int to) {
 #pragma unroll
@@ -296,8 +303,8 @@ __global__ void __launch_bounds__(ln_threads(GROUP), ln_bwd_room(GROUP, PIECES, 
   for (int i = 0; i < kLnAhead; ++i) fetch(i);
   for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.rows;
        first += static_cast<int64_t>(gridDim.x) * kRows) {
-    const int64_t row = at.r;
-    at.r += at.step;
+    const int64_t row = next;
+    next += ahead.step;
     f2 x[PIECES][4], du[PIECES][4];
     uint4 z[PIECES];
     asm volatile("cp.async.wait_group %0;" ::"n"(kLnAhead - 1) : "memory");
@@ -387,19 +394,20 @@ struct LnKernel {
   void (*fwd[2])(LnArgs);
   void (*bwd[2])(LnArgs);
   int threads, rows;  // of a CTA
-  int bwd_bytes[2];   // of its shared memory
-  int bwd_room[2];
+  int piece_bytes;    // shared memory of a tensor's rows ahead
+  int bwd_room;
 };
 template <int GROUP, int PIECES>
 static LnKernel kernel_of() {
   return LnKernel{{cattn_layernorm_fwd_kernel<GROUP, PIECES, false>, cattn_layernorm_fwd_kernel<GROUP, PIECES, true>},
                   {cattn_layernorm_bwd_kernel<GROUP, PIECES, false>, cattn_layernorm_bwd_kernel<GROUP, PIECES, true>},
                   ln_threads(GROUP), ln_threads(GROUP) / GROUP,
-                  {kLnAhead * 2 * PIECES * ln_threads(GROUP) * 16, kLnAhead * 3 * PIECES * ln_threads(GROUP) * 16},
-                  {ln_bwd_room(GROUP, PIECES, false), ln_bwd_room(GROUP, PIECES, true)}};
+                  kLnAhead * PIECES * ln_threads(GROUP) * 16,
+                  ln_bwd_room(PIECES)};
 }
-// The smallest group that holds a row in one piece a thread, to 512 threads: with two pieces (and 256 threads
-// for 4096 channels) the gradient's sums leave registers for half as many CTAs.
+// The smallest group that holds a row in one piece a thread, to 1024 channels, and in two above: 8192 rows of
+// 4096 channels 44 us with 256 threads (their gradient; two CTAs an SM), 57 with 512 and a piece each, 51 with
+// 128 and four.
 static LnKernel pick(int64_t C) {
   if (C <= 32) return kernel_of<4, 1>();
   if (C <= 64) return kernel_of<8, 1>();
@@ -407,13 +415,23 @@ static LnKernel pick(int64_t C) {
   if (C <= 256) return kernel_of<32, 1>();
   if (C <= 512) return kernel_of<64, 1>();
   if (C <= 1024) return kernel_of<128, 1>();
-  if (C <= 2048) return kernel_of<256, 1>();
-  if (C <= 4096) return kernel_of<512, 1>();
+  if (C <= 2048) return kernel_of<128, 2>();
+  if (C <= 4096) return kernel_of<256, 2>();
   return kernel_of<512, 2>();
 }
 static int64_t ctas_of(int64_t rows, const LnKernel& kern, int sms, int room) {
   const int64_t ctas = (rows + kern.rows - 1) / kern.rows, most = static_cast<int64_t>(sms) * (room / kern.threads);
   return ctas < most ? ctas : most;
+}
+
+static int launch_rows(void (*kernel)(LnArgs), const LnKernel& kern, int64_t ctas, int tensors, const LnArgs& a,
+                       cudaStream_t stream) {
+  const int bytes = tensors * kern.piece_bytes;
+  if (bytes > 32 * 1024 && cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), bytes) != CCONV_OK)
+    return CCONV_ERR_CUDA;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kern.threads), bytes, stream, a) == cudaSuccess
+             ? CCONV_OK
+             : CCONV_ERR_CUDA;
 }
 
 static int check(const void* x, int64_t sxt, int64_t sxh, const void* z, int64_t szt, int64_t szh, int64_t total,
@@ -461,9 +479,7 @@ extern "C" CCONV_API int cattn_layernorm_fwd(const void* x, int64_t sxt, int64_t
   if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
   const LnKernel kern = pick(C);
   const int64_t ctas = ctas_of(a.rows, kern, sms, kern.threads > kLnFwdRoom ? kern.threads : kLnFwdRoom);
-  return launch_pdl(kern.fwd[gate != nullptr], dim3(static_cast<unsigned>(ctas)), dim3(kern.threads), 0, stream, a) == cudaSuccess
-             ? CCONV_OK
-             : CCONV_ERR_CUDA;
+  return launch_rows(kern.fwd[gate != nullptr], kern, ctas, gate ? 2 : 1, a, stream);
 }
 
 extern "C" CCONV_API int cattn_layernorm_bwd_workspace_bytes(int64_t total, int64_t H, int64_t C, size_t* bytes) {
@@ -472,9 +488,8 @@ extern "C" CCONV_API int cattn_layernorm_bwd_workspace_bytes(int64_t total, int6
   if (total < 0 || total > kMaxRows || H < 1 || H > 65535 || C < 1 || C > kMaxNorm) return CCONV_ERR_SHAPE;
   int sms = 0;
   if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
-  // (as many CTAs as either kernel, with a gate and without one, has)
   const LnKernel kern = pick(C);
-  const int64_t ctas = ctas_of(total * H, kern, sms, kern.bwd_room[0]);
+  const int64_t ctas = ctas_of(total * H, kern, sms, kern.bwd_room);
   *bytes = static_cast<size_t>(ctas > 0 ? ctas : 1) * 2 * static_cast<size_t>(C) * 4;
   return CCONV_OK;
 }
@@ -502,7 +517,7 @@ extern "C" CCONV_API int cattn_layernorm_bwd(const void* x, int64_t sxt, int64_t
   int sms = 0;
   if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
   const LnKernel kern = pick(C);
-  const int64_t ctas = ctas_of(a.rows, kern, sms, kern.bwd_room[gate != nullptr]);
+  const int64_t ctas = ctas_of(a.rows, kern, sms, kern.bwd_room);
   const bool sums = dw || db;
   if (sums) {
     if (!workspace || workspace_bytes < static_cast<size_t>(ctas > 0 ? ctas : 1) * 2 * C * 4)
@@ -510,12 +525,7 @@ extern "C" CCONV_API int cattn_layernorm_bwd(const void* x, int64_t sxt, int64_t
     if (!aligned(workspace, 16)) return CCONV_ERR_ALIGN;
     a.part = static_cast<float*>(workspace);
   }
-  const int bytes = kern.bwd_bytes[gate != nullptr];
-  if (total > 0 && bytes > 32 * 1024 &&
-      cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(kern.bwd[gate != nullptr]), bytes) != CCONV_OK)
-    return CCONV_ERR_CUDA;
-  if (total > 0 && launch_pdl(kern.bwd[gate != nullptr], dim3(static_cast<unsigned>(ctas)), dim3(kern.threads), bytes,
-                              stream, a) != cudaSuccess)
+  if (total > 0 && launch_rows(kern.bwd[gate != nullptr], kern, ctas, gate ? 3 : 2, a, stream) != CCONV_OK)
     return CCONV_ERR_CUDA;
   if (!sums) return CCONV_OK;
   return launch_pdl(cattn_layernorm_sums_kernel, dim3(static_cast<unsigned>((2 * C + kSumCols - 1) / kSumCols)),
