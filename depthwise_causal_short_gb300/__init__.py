@@ -2,9 +2,10 @@
 
 The computation lives in ``libcconv.so`` (C ABI: ``include/cconv.h``); this package is its
 thin Python binding with the same names, plus the build step and the seeded synthetic
-input generators.  The mixer operators that follow the convolution (per-head norm of queries
-and keys with the position rotation, linear attention with a decay per token and head) live
-in ``libcattn.so`` (C ABI: ``include/cattn.h``).  Importing the package does not load the
+input generators.  The mixer operators around the convolution (per-head norm of queries
+and keys with the position rotation, linear attention with a decay per token and head, the
+gated delta rule, layer norm with the gate of a mixer's outputs) live in ``libcattn.so`` (C
+ABI: ``include/cattn.h``).  Importing the package does not load the
 libraries; the first call does, and raises if they have not been built.
 """
 from .attn import (  # noqa: F401
@@ -27,7 +28,7 @@ from .attn import (  # noqa: F401
     cattn_qknorm_bwd_workspace_bytes,
     cattn_qknorm_fwd,
 )
-from .attn_autograd import decay_attention, qk_norm_rope  # noqa: F401
+from .attn_autograd import decay_attention, delta_attention, layer_norm, qk_norm_rope  # noqa: F401
 from .autograd import causal_conv1d  # noqa: F401
 from .binding import (  # noqa: F401
     CCONV_ACT_NONE,

@@ -1,4 +1,5 @@
-"""qk_norm_rope and decay_attention: the mixer's calls as differentiable PyTorch functions.
+"""qk_norm_rope, decay_attention, delta_attention and layer_norm: the mixer's calls as differentiable
+PyTorch functions.
 
 Only marshalling lives here, as in the convolution's causal_conv1d: the forward is one
 cattn_*_fwd call, the backward one cattn_*_bwd call.  The gradients have no gradients of their own:
@@ -76,3 +77,61 @@ def decay_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     if initial_state is not None and initial_state.shape[0] != cu_seqlens.numel() - 1:
         raise ValueError("initial_state must hold one state per sequence")
     return _DecayAttention.apply(q, k, v, g, cu_seqlens, initial_state, scale, output_final_state)
+
+
+class _DeltaAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, cu_seqlens, initial_state, scale, output_final_state):
+        o, final, _ = attn.cattn_delta_fwd(q, k, v, g, beta, cu_seqlens, scale=scale,
+                                           initial_state=initial_state,
+                                           final_state=bool(output_final_state))
+        ctx.scale = scale
+        ctx.save_for_backward(q, k, v, g, beta, cu_seqlens, initial_state)
+        if final is not None:
+            ctx.mark_non_differentiable(final)
+        return o, final
+
+    @staticmethod
+    def backward(ctx, do, _dfinal):
+        q, k, v, g, beta, cu_seqlens, initial_state = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        want = initial_state is not None and need[6]
+        grads = attn.cattn_delta_bwd(q, k, v, g, beta, do.contiguous(), cu_seqlens, scale=ctx.scale,
+                                     initial_state=initial_state, want_dinit=want)
+        *grads, ds = once("delta_attention", grads, (do, q, k, v, g, beta, initial_state))
+        return (*(d if n else None for d, n in zip(grads, need)), None, ds if want else None, None, None)
+
+
+def delta_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                    beta: torch.Tensor, cu_seqlens: torch.Tensor,
+                    initial_state: torch.Tensor | None = None, scale: float | None = None,
+                    output_final_state: bool = False):
+    """The gated delta rule over packed sequences; returns (o, final_state or None).  Differentiable in
+    q, k, v, g, beta and initial_state [nseq, Hv, K, V]; the final state is a constant.  See
+    attn.cattn_delta_fwd."""
+    if initial_state is not None and initial_state.shape[0] != cu_seqlens.numel() - 1:
+        raise ValueError("initial_state must hold one state per sequence")
+    return _DeltaAttention.apply(q, k, v, g, beta, cu_seqlens, initial_state, scale, output_final_state)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, b, gate, mode, eps):
+        ctx.save_for_backward(x, w, b, gate)
+        ctx.kw = dict(mode=mode, eps=eps)
+        return attn.cattn_layernorm_fwd(x, w, b, gate=gate, **ctx.kw)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, b, gate = ctx.saved_tensors
+        grads = attn.cattn_layernorm_bwd(x, dy.contiguous(), w, b, gate=gate, **ctx.kw)
+        grads = once("layer_norm", grads, (dy, x, w, b, gate))
+        return (*(d if n else None for d, n in zip(grads, ctx.needs_input_grad)), None, None)
+
+
+def layer_norm(x: torch.Tensor, w: torch.Tensor | None = None, b: torch.Tensor | None = None,
+               gate: torch.Tensor | None = None, mode: str = "layer", eps: float = 1e-6):
+    """Layer norm of x [total, C] or of each head of x [total, H, C], or with mode "rms" the norm by the
+    root mean square, times silu(gate) where a gate is given; differentiable in all four tensors.  See
+    attn.cattn_layernorm_fwd."""
+    return _LayerNorm.apply(x, w, b, gate, mode, eps)
