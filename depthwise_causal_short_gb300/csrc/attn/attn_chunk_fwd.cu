@@ -989,19 +989,19 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Map of a [total, H, C] tensor read in boxes of 64 channels of one head and `tokens` tokens.
-int encode_tile_map(CUtensorMap* map, const Rows& x, int64_t total, int64_t H, int64_t C, int tokens) {
+// Map of a [total, H, C] tensor read in boxes of `cols` channels (64, or 32) of one head and `tokens` tokens.
+int encode_tile_map(CUtensorMap* map, const Rows& x, int64_t total, int64_t H, int64_t C, int tokens, int cols) {
   auto enc = encode_fn();
   if (!enc) return CCONV_ERR_CUDA;
   // strides over dimensions of extent 1 are the caller's to leave unset
   const int64_t sh = H > 1 ? x.sh : C, st = total > 1 ? x.st : C * H;
   cuuint64_t dims[3] = {(cuuint64_t)C, (cuuint64_t)H, (cuuint64_t)total};
   cuuint64_t strides[2] = {(cuuint64_t)sh * 2u, (cuuint64_t)st * 2u};
-  cuuint32_t box[3] = {kPanelCols, 1u, static_cast<cuuint32_t>(tokens)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(cols), 1u, static_cast<cuuint32_t>(tokens)};
   cuuint32_t estr[3] = {1u, 1u, 1u};
   const CUresult r =
       enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(x.p), dims, strides, box,
-          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, cols == kPanelCols ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? CCONV_OK : CCONV_ERR_CUDA;
 }

@@ -53,6 +53,7 @@ int launch_chunk_fwd(const ChunkCall& c, cudaStream_t stream);
 int launch_chunk_states(const ChunkCall& states, const ChunkCall& grads, cudaStream_t stream);
 size_t chunk_fwd_bytes(int grid);
 int encode_part_map(CUtensorMap* map, float* x, int64_t total, int64_t parts, int64_t C);
-int encode_tile_map(CUtensorMap* map, const Rows& x, int64_t total, int64_t H, int64_t C, int tokens = 128);
+int encode_tile_map(CUtensorMap* map, const Rows& x, int64_t total, int64_t H, int64_t C, int tokens = 128,
+                    int cols = 64);
 
 }  // namespace cattn

@@ -21,7 +21,7 @@ static Rows rows(const void* p, int64_t st, int64_t sh) {
 
 // What a backward call keeps in its workspace, from a 256-byte boundary.
 struct DeltaWork {
-  size_t records, z, u, heads, ends, odots, vdots, bdots, sums, bytes;
+  size_t records, z, u, heads, ends, odots, vdots, bdots, sums, anchors, adots, bytes;
 };
 static DeltaWork delta_work(int64_t total, int64_t nseq, int64_t Hv, int64_t V) {
   const size_t tiles = static_cast<size_t>(delta_tiles(V)), rows = static_cast<size_t>(total) * Hv;
@@ -36,12 +36,15 @@ static DeltaWork delta_work(int64_t total, int64_t nseq, int64_t Hv, int64_t V) 
   w.records = take(record_bytes(total, nseq, Hv));
   w.z = take(rows * V * 4);
   w.u = take(states / kStatePanel * kUTile);
-  w.heads = take(states);
-  w.ends = take(states);
+  w.heads = take(2 * states);
+  w.ends = take(2 * states);
   w.odots = take(2 * tiles * rows * 4);
   w.vdots = take(2 * tiles * rows * 4);
   w.bdots = take(2 * tiles * rows * 4);
   w.sums = take(static_cast<size_t>(delta_slots(total, nseq)) * Hv * 8);
+  const size_t anchors = total > 0 ? static_cast<size_t>(delta_anchors(total, nseq)) * Hv * tiles : 0;
+  w.anchors = take(anchors * kAnchorFloats * 4);
+  w.adots = take(anchors * kRowWarps * 4);
   w.bytes = at + 256;
   return w;
 }
@@ -171,6 +174,8 @@ extern "C" CCONV_API int cattn_delta_bwd(
   c.vdots = reinterpret_cast<float*>(ws + w.vdots);
   c.bdots = reinterpret_cast<float*>(ws + w.bdots);
   c.sums = reinterpret_cast<double*>(ws + w.sums);
+  c.anchors = reinterpret_cast<float*>(ws + w.anchors);
+  c.adots = reinterpret_cast<float*>(ws + w.adots);
   c.dq = static_cast<uint16_t*>(dq), c.dk = static_cast<uint16_t*>(dk), c.dv = static_cast<uint16_t*>(dv);
   c.dg = dg, c.dbeta = dbeta, c.dinit = d_initial_state;
   rc = launch_delta_prep(c, stream);

@@ -59,9 +59,12 @@ enum DeltaGate : int { kEf = 0, kEb = 64, kBeta = 128, kTotal = 192 };  // float
 // total / 64 + nseq of them.
 __host__ __device__ inline int64_t delta_slots(int64_t total, int64_t nseq) { return total / kDelta + nseq; }
 
-// The sequence and rows of record slot `slot` (rows [row0, row0 + n)); false if it has none.
-__device__ __forceinline__ bool find_chunk(const int32_t* cu, int nseq, int total, int64_t slot, int lane,
-                                           int& row0, int& n) {
+// The chunk of record slot `slot`: rows [row0, row0 + n), number c of the sequence seq with rows [a, b).
+struct Chunk {
+  int seq, a, b, c, row0, n;
+};
+// False if the slot has none.  All lanes of a warp.
+__device__ __forceinline__ bool find_chunk(const int32_t* cu, int nseq, int total, int64_t slot, int lane, Chunk& x) {
   // the last sequence whose first slot is not above `slot`, 32 candidates at a time
   int64_t lo = 0, hi = nseq;  // it is in [lo, hi)
   while (hi - lo > 1) {
@@ -71,12 +74,13 @@ __device__ __forceinline__ bool find_chunk(const int32_t* cu, int nseq, int tota
     lo += last * step;
     hi = min(hi, lo + step);
   }
-  int a, b;
-  sequence_rows(cu, static_cast<int>(lo), total, a, b);
-  const int64_t c = slot - lo - a / kDelta;
-  if (c < 0 || c * kDelta >= b - a) return false;
-  row0 = a + static_cast<int>(c) * kDelta;
-  n = min(kDelta, b - row0);
+  x.seq = static_cast<int>(lo);
+  sequence_rows(cu, x.seq, total, x.a, x.b);
+  const int64_t c = slot - lo - x.a / kDelta;
+  if (c < 0 || c * kDelta >= x.b - x.a) return false;
+  x.c = static_cast<int>(c);
+  x.row0 = x.a + x.c * kDelta;
+  x.n = min(kDelta, x.b - x.row0);
   return true;
 }
 
@@ -266,6 +270,18 @@ __device__ __forceinline__ void tmem_copy(uint32_t tmem, uint64_t rows) {
   asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(tmem), "l"(rows) : "memory");
 }
 
+// dg_t is the sum of o_i . do_i - v_i . dv_i over the tokens i >= t of the sequence.  Rounding adds up along it,
+// so it starts anew at every kAnchorChunks-th chunk, where it is <S_0, D_0>: the chain of the states leaves S_0
+// in fp32 there, its way back the product with D, one part from each row warp.
+constexpr int kAnchorChunks = 8;
+constexpr int kAnchorFloats = 128 * kColumns;
+__host__ __device__ inline int64_t delta_anchors(int64_t total, int64_t nseq) {
+  return total / (kAnchorChunks * kDelta) + nseq;
+}
+__device__ __forceinline__ int64_t anchor_of(int a, int seq, int c) {
+  return a / (kAnchorChunks * kDelta) + seq + c / kAnchorChunks;
+}
+
 struct DeltaCall {
   Rows q, k, v, d_o;
   Gates g, beta;          // (beta's values are taken as they are)
@@ -282,11 +298,12 @@ struct DeltaCall {
   // the gradient's
   float* z;               // [total][Hv][V]
   uint8_t* u;             // [slots][Hv][tiles] two terms of u
-  uint8_t *heads, *ends;  // [slots][Hv][tiles] first terms of S_0 and of D
+  uint8_t *heads, *ends;  // [slots][Hv][tiles] two terms of S_0 and of D
   float *odots, *vdots, *bdots;  // [2 tiles][Hv][total] parts of o . do, v . dv and dbeta
   uint16_t *dq, *dk, *dv;
   float *dg, *dbeta, *dinit;
   double* sums;           // [Hv][slots] of the chunks' terms of dg
+  float *anchors, *adots; // [anchors][Hv][tiles] states, [anchors][Hv][tiles * kRowWarps] parts of products
 };
 
 int launch_delta_prep(const DeltaCall& c, cudaStream_t stream);
@@ -294,6 +311,6 @@ int launch_delta_fwd(const DeltaCall& c, cudaStream_t stream);
 int launch_delta_states(const DeltaCall& c, cudaStream_t stream);  // the gradient's chain of states
 int launch_delta_back(const DeltaCall& c, cudaStream_t stream);    // its chain backwards
 int launch_delta_grads(const DeltaCall& c, cudaStream_t stream);   // dq, dk, dbeta
-int launch_delta_gates(const DeltaCall& c, cudaStream_t stream);   // dg, from the chunks' parts
+int launch_delta_gates(const DeltaCall& c, cudaStream_t stream);   // dg, from the chunks' parts and the anchors
 
 }  // namespace cattn

@@ -9,7 +9,7 @@
 // in lanes 0 to 15 of each quarter, those of the second ones in lanes 16 to 31 (in place of Q D).  The products
 // that have do in them wait for nothing of the chain: P~^T do is made a chunk ahead, while the rows work; four
 // warps prepare do for them.
-// It leaves dv, the first term of every D, dbeta = du . z and v . dv.
+// It leaves dv, two terms of every D, dbeta = du . z, v . dv, and at every kAnchorChunks-th chunk <S_0, D_0>.
 #include <cudaTypedefs.h>
 
 #include "attn_chunk_host.h"
@@ -49,7 +49,9 @@ struct BackArgs {
   const int32_t* cu;
   const uint8_t* records;
   const float* z;
-  uint8_t* ends;          // [slots][Hv][tiles] first terms of D
+  uint8_t* ends;          // [slots][Hv][tiles] two terms of D
+  const float* anchors;   // [anchors][Hv][tiles]
+  float* adots;           // [anchors][Hv][tiles * kRowWarps]
   float *vdots, *bdots;   // [2 tiles][Hv][total]
   uint16_t* dv;
   float* dinit;
@@ -202,12 +204,12 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
       drain(alldone, 1);
     }
   } else if (warp == 2) {
-    // ---- the first term of every D ----
+    // ---- two terms of every D ----
     if (elect_one()) {
       for (int i = 0; i < chunks && ok; ++i) {
         if (!(ok = DELTA_WAIT(dready, i))) break;
-        bulk_store(p.ends + (((slot0 + chunks - 1 - i) * p.Hv + hv) * p.tiles + tile) * kStatePanel, smem + kOffD,
-                   kStatePanel);
+        bulk_store(p.ends + (((slot0 + chunks - 1 - i) * p.Hv + hv) * p.tiles + tile) * 2 * kStatePanel, smem + kOffD,
+                   2 * kStatePanel);
         stores_commit();
         stores_wait_read();
         bar_arrive(kept);
@@ -292,6 +294,10 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
 #pragma unroll
         for (int r = 0; r < 2; ++r) v.v[j][r] = bf16x2_to_f2(vw[r][j]);
       fetch(c - 1);
+      const bool anchor = c > 0 && c % kAnchorChunks == 0;
+      const int64_t anchor_at = (anchor_of(row_a, seq, c) * p.Hv + hv) * p.tiles + tile;
+      const float* state = p.anchors + anchor_at * kAnchorFloats + row * kColumns + h * 16;
+      if (anchor) asm volatile("prefetch.global.L2 [%0];" ::"l"(state));
       if (!(ok = DELTA_WARP_WAIT(rfull + 8 * st, i / 2))) break;
       float ef[2], eb[2], beta[2];
 #pragma unroll
@@ -376,6 +382,18 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
           tc_fence_before();
           __syncwarp();
           if (lane == 0) bar_arrive(dready);
+          if (anchor) {
+            const float4* s = reinterpret_cast<const float4*>(state);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 x = s[j];
+              sum = fmaf(D[4 * j + 3], x.w, fmaf(D[4 * j + 2], x.z, fmaf(D[4 * j + 1], x.y, fmaf(D[4 * j], x.x, sum))));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) p.adots[anchor_at * kRowWarps + warp - 4] = sum;
+          }
         }
       }
       if (lane == 0) bar_arrive(empty + 8 * st);
@@ -409,6 +427,7 @@ int launch_delta_back(const DeltaCall& c, cudaStream_t stream) {
   a.records = c.records;
   a.z = c.z;
   a.ends = c.ends;
+  a.anchors = c.anchors, a.adots = c.adots;
   a.vdots = c.vdots, a.bdots = c.bdots;
   a.dv = c.dv, a.dinit = c.dinit;
   a.scale = c.scale;

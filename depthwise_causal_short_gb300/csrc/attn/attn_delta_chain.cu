@@ -9,8 +9,9 @@
 //   K^T (eb . u)   -> S = total S + ..
 // The three terms of S, X and eb . u lie side by side as columns of one operand (N = 96), so that A is
 // read once for all three; their products are added up in registers.
-// The gradient runs the same chain first (BWD): it leaves z, two terms of u, the first term of every S_0,
-// and o . do in place of o.  Its own chain, from the last chunk to the first, is attn_delta_back.cu.
+// The gradient runs the same chain first (BWD): it leaves z, two terms of u and of every S_0 (and
+// every kAnchorChunks-th in fp32), and o . do in place of o.  Its own chain, from the last chunk to the first,
+// is attn_delta_back.cu.
 //
 // Bound by that chain: a product, its results to registers, the next operand to shared memory.
 #include <cudaTypedefs.h>
@@ -52,9 +53,10 @@ struct ChainArgs {
   uint16_t* o;
   const uint8_t* records;
   float* z;        // [total][Hv][V]
-  uint8_t* heads;  // [slots][Hv][tiles] first terms of S_0
+  uint8_t* heads;  // [slots][Hv][tiles] two terms of S_0
   uint8_t* u;      // [slots][Hv][tiles] two terms of u
   float* dots;     // [2 tiles][Hv][total] parts of o . do
+  float* anchors;  // [anchors][Hv][tiles] of kAnchorFloats: S_0 of every kAnchorChunks-th chunk
   float scale;
   int total, nseq, ratio, Hv, K, V, tiles, checked;
 };
@@ -218,12 +220,12 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
       drain(alldone, 1);
     }
   } else if (BWD && warp == 2) {
-    // ---- the first term of every S_0 ----
+    // ---- two terms of every S_0 ----
     if (elect_one()) {
       for (int c = 0; c < chunks && ok; ++c) {
         if (!(ok = DELTA_WAIT(sready, c))) break;
-        bulk_store(p.heads + (((slot0 + c) * p.Hv + w.hv) * p.tiles + w.tile) * kStatePanel, smem + kOffState,
-                   kStatePanel);
+        bulk_store(p.heads + (((slot0 + c) * p.Hv + w.hv) * p.tiles + w.tile) * 2 * kStatePanel, smem + kOffState,
+                   2 * kStatePanel);
         stores_commit();
         stores_wait_read();
         bar_arrive(kept);
@@ -349,6 +351,12 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
             p.dots[(static_cast<int64_t>(w.tile * 2 + h) * p.Hv + w.hv) * p.total + row0 + t + 8 * r] = sum;
         }
       }
+      if (BWD && c > 0 && c % kAnchorChunks == 0) {
+        float4* to = reinterpret_cast<float4*>(
+            p.anchors + ((anchor_of(w.a, w.seq, c) * p.Hv + w.hv) * p.tiles + w.tile) * kAnchorFloats + row * kColumns + h * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+      }
       if (c + 1 < chunks || keep) {
         float z[16];
         if (!(ok = DELTA_WARP_WAIT(acc3, c))) break;
@@ -400,7 +408,7 @@ static int launch_chain(const DeltaCall& c, cudaStream_t stream) {
   a.initial = c.initial, a.fin = c.fin;
   a.o = c.o;
   a.records = c.records;
-  a.z = c.z, a.u = c.u, a.heads = c.heads, a.dots = c.odots;
+  a.z = c.z, a.u = c.u, a.heads = c.heads, a.dots = c.odots, a.anchors = c.anchors;
   a.scale = c.scale;
   a.total = c.s.total, a.nseq = c.s.nseq, a.ratio = c.s.Hv / c.s.Hk, a.Hv = c.s.Hv, a.K = c.s.K, a.V = c.s.V;
   a.tiles = delta_tiles(c.s.V);

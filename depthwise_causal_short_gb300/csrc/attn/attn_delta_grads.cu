@@ -1,7 +1,7 @@
 // attn_delta_grads.cu -- the gated delta rule's dq and dk, and the sums that give dg and dbeta.
 //
 // With S_0 and D, the state before a chunk and the gradient of the state behind it, known (the chains
-// left their first bf16 terms, and two of u), all chunks are done at once; per chunk and value head
+// left two bf16 terms of them, and of u), all chunks are done at once; per chunk and value head
 //   X = scale (do u^T) . L (s <= t),   Y = (dv u^T) . L (s < t)
 //   dq = X K                        + scale ef . (do S_0^T)
 //   dk = X^T Q - (Y + Y^T) K + eb . (u D^T) - ef . (dv S_0^T)
@@ -11,11 +11,10 @@
 //   [do; dv] S_0^T     rows scaled by scale ef and -ef afterwards
 //   [  ; u ] D^T       rows 64.. scaled by eb afterwards
 //   [X; -Y] K,  [0; -Y^T] K,  [0; X^T] Q
-// A CTA goes through (chunk, key head) items; do, dv and the tiles of S_0 and D come by TMA, 64 columns
-// of V at a time, and u's two terms.  Roundings to bf16: S_0, D and dv, once each; X, Y and u keep two
-// terms (with one, dk's error in the 2-norm was 2.8e-3, of which its store makes 1.7e-3).
-//
-// dg_t is the sum of o_i . do_i - v_i . dv_i over the tokens i >= t of the sequence.
+// A CTA goes through (chunk, key head) items; do, dv, u and the tiles of S_0 and D come by TMA, 32 columns
+// of V at a time, through a ring for what X and Y need and one for the states.  dv is
+// rounded to bf16 once, as it is stored; the other factors keep two terms (with one, dk's error in the 2-norm
+// was 2.8e-3, of which its store makes 1.7e-3).
 #include <cudaTypedefs.h>
 
 #include "attn_chunk_host.h"
@@ -36,13 +35,12 @@ static FaultReader reader(read_fault);
 
 // shared memory, from a 1024-byte boundary
 constexpr int kHalf = kDelta * 128;                       // 64 rows of 64 columns
-constexpr int kStepOut = 2 * kHalf;                       // do over dv
-constexpr int kStepState = 2 * kStatePanel;               // two tiles of S_0; of D
-constexpr int kUPart = 3 * kTokenPanel;                   // second, first and again second terms of u: a tile
-constexpr int kStepU = 2 * kUPart;
-constexpr int kStepBytes = kStepOut + 2 * kStepState + kStepU;
-constexpr int kGradStages = 2;
-constexpr int kOffGradKq = kGradStages * kStepBytes;
+constexpr int kUPart = 3 * kTokenPanel;                   // second, first and again second terms of u
+constexpr int kPairSlot = 2 * kTokenPanel + kUPart;       // do over dv; u
+constexpr int kStateSlot = 4 * kStatePanel;               // two terms of S_0 and of D
+constexpr int kPairSlots = 4, kStateSlots = 2;
+constexpr int kOffStates = kPairSlots * kPairSlot;
+constexpr int kOffGradKq = kOffStates + kStateSlots * kStateSlot;
 constexpr int kOffZero = kOffGradKq + kSlotKq;           // zeros; X, -Y; their second terms: 64 rows each
 constexpr int kOffXy = kOffZero + kHalf;
 constexpr int kOffGates = kOffXy + 4 * kHalf;             // of two heads in turn
@@ -56,7 +54,7 @@ constexpr int kPartsAhead = 8;  // parts of the sums in flight
 constexpr int kGradThreads = 384, kGradRowWarps = 8;
 
 struct GradArgs {
-  CUtensorMap mq, mk, mo, mv;  // q, k, do, dv
+  CUtensorMap mq, mk, mo, mv;  // q, k; do, dv in boxes of 32 columns
   Gates g;
   const int32_t* cu;
   const uint8_t *u, *heads, *ends;
@@ -73,18 +71,23 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const uint32_t smem = smem_addr(base);
-  const uint32_t full = smem + kOffGradBars, empty = full + 8 * kGradStages;      // tiles of a step
-  const uint32_t kqfull = empty + 8 * kGradStages, kqempty = kqfull + 8;          // an item's K and Q
+  const uint32_t pfull = smem + kOffGradBars, pempty = pfull + 8 * kPairSlots;    // do, dv, u of a tile
+  const uint32_t sfull = pempty + 8 * kPairSlots, sempty = sfull + 8 * kStateSlots;  // its states
+  const uint32_t kqfull = sempty + 8 * kStateSlots, kqempty = kqfull + 8;          // an item's K and Q
   const uint32_t xyfull = kqempty + 8, xyready = xyfull + 8;                      // a head's X and Y
   const uint32_t headfull = xyready + 8, headfree = headfull + 8;                 // a head's sums
   const uint32_t gready = headfree + 8, gfree = gready + 16, alldone = gfree + 16;  // a head's gates, in turn
   __shared__ uint32_t tmem_at;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int ratio = p.Hv / p.Hk, steps = (p.V + 63) / 64;
+  const int ratio = p.Hv / p.Hk;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kGradStages; ++i) {
-      bar_init(full + 8 * i, 1);
-      bar_init(empty + 8 * i, 1);
+    for (int i = 0; i < kPairSlots; ++i) {
+      bar_init(pfull + 8 * i, 1);
+      bar_init(pempty + 8 * i, 1);
+    }
+    for (int i = 0; i < kStateSlots; ++i) {
+      bar_init(sfull + 8 * i, 1);
+      bar_init(sempty + 8 * i, 1);
     }
     bar_init(kqfull, 1);
     bar_init(kqempty, 1);
@@ -112,60 +115,73 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
 
   if (warp == 0) {
     // ---- tiles ----
-    int step = 0, item = 0, part = 0;
+    int pairs = 0, states = 0, item = 0, part = 0;
     for (int64_t at = blockIdx.x; at < p.items && ok; at += gridDim.x) {
       const int hk = static_cast<int>(at % p.Hk);
       const int64_t slot = at / p.Hk;
-      int row0, n;
-      if (!find_chunk(p.cu, p.nseq, p.total, slot, lane, row0, n)) continue;
+      Chunk x;
+      if (!find_chunk(p.cu, p.nseq, p.total, slot, lane, x)) continue;
       if (elect_one()) {
         const int panels = p.K > kPanelCols ? 2 : 1;
         if (item > 0) ok = DELTA_WAIT(kqempty, item - 1);
         if (ok) {
           bar_expect(kqfull, panels * 2 * kSideBytes);
           for (int j = 0; j < panels; ++j) {
-            load_box(smem + kOffGradKq + j * kPanelBytes, &p.mk, kqfull, j * kPanelCols, hk, row0);
-            load_box(smem + kOffGradKq + j * kPanelBytes + kSideBytes, &p.mq, kqfull, j * kPanelCols, hk, row0);
+            load_box(smem + kOffGradKq + j * kPanelBytes, &p.mk, kqfull, j * kPanelCols, hk, x.row0);
+            load_box(smem + kOffGradKq + j * kPanelBytes + kSideBytes, &p.mq, kqfull, j * kPanelCols, hk, x.row0);
           }
           part = 1;
         }
         for (int h = 0; h < ratio && ok; ++h) {
           const int hv = hk * ratio + h;
-          for (int s = 0; s < steps && ok; ++s, ++step) {
-            const int st = step % kGradStages;
-            if (step >= kGradStages && !(ok = DELTA_WAIT(empty + 8 * st, step / kGradStages - 1))) break;
-            const int tiles = min(2, p.tiles - 2 * s);
-            const uint32_t dst = smem + st * kStepBytes, bar = full + 8 * st;
-            bar_expect(bar, kStepOut + tiles * (2 * kStatePanel + kUPart));
-            load_box(dst, &p.mo, bar, s * 64, hv, row0);
-            load_box(dst + kHalf, &p.mv, bar, s * 64, hv, row0);
-            const int64_t from = ((slot * p.Hv + hv) * p.tiles + 2 * s) * kStatePanel;
-            bulk_load(dst + kStepOut, p.heads + from, tiles * kStatePanel, bar);
-            bulk_load(dst + kStepOut + kStepState, p.ends + from, tiles * kStatePanel, bar);
-            for (int i = 0; i < tiles; ++i) {
-              const uint8_t* u = p.u + ((slot * p.Hv + hv) * p.tiles + 2 * s + i) * kUTile;
-              const uint32_t to = dst + kStepOut + 2 * kStepState + i * kUPart;
-              bulk_load(to + kTokenPanel, u, kUTile, bar);
-              bulk_load(to, u + kTokenPanel, kTokenPanel, bar);
+          const int64_t first = (slot * p.Hv + hv) * p.tiles;
+          // states follow the pairs as the products take them (below)
+          int done = 0;
+          auto load_states = [&](int end) {
+            for (; done < end && ok; ++done, ++states) {
+              const int st = states % kStateSlots;
+              if (states >= kStateSlots && !(ok = DELTA_WAIT(sempty + 8 * st, states / kStateSlots - 1))) return;
+              const uint32_t dst = smem + kOffStates + st * kStateSlot, bar = sfull + 8 * st;
+              bar_expect(bar, kStateSlot);
+              bulk_load(dst, p.heads + (first + done) * 2 * kStatePanel, 2 * kStatePanel, bar);
+              bulk_load(dst + 2 * kStatePanel, p.ends + (first + done) * 2 * kStatePanel, 2 * kStatePanel, bar);
             }
+          };
+          for (int s = 0; s < p.tiles && ok; ++s, ++pairs) {
+            const int st = pairs % kPairSlots;
+            if (pairs >= kPairSlots && !(ok = DELTA_WAIT(pempty + 8 * st, pairs / kPairSlots - 1))) break;
+            const uint32_t dst = smem + st * kPairSlot, u = dst + 2 * kTokenPanel, bar = pfull + 8 * st;
+            bar_expect(bar, kPairSlot);
+            load_box(dst, &p.mo, bar, s * kColumns, hv, x.row0);
+            load_box(dst + kTokenPanel, &p.mv, bar, s * kColumns, hv, x.row0);
+            const uint8_t* from = p.u + (first + s) * kUTile;
+            bulk_load(u + kTokenPanel, from, kUTile, bar);
+            bulk_load(u, from + kTokenPanel, kTokenPanel, bar);
+            if (s + 1 == p.tiles)
+              load_states(p.tiles);
+            else if (s + 1 >= kPairSlots)
+              load_states(s + 2 - kPairSlots);
           }
         }
       }
       ok = __all_sync(0xffffffffu, ok);
-      step = __reduce_max_sync(0xffffffffu, step);
+      pairs = __reduce_max_sync(0xffffffffu, pairs);
+      states = __reduce_max_sync(0xffffffffu, states);
       if (ok) ++item, part = 0;
     }
     item += __any_sync(0xffffffffu, part);
     if (elect_one()) {
       drain(kqfull, item);
-      for (int st = 0; st < kGradStages; ++st) drain(full + 8 * st, (step - st + kGradStages - 1) / kGradStages);
+      // (a pair's or state's loads that gave up half-way count where they were begun)
+      for (int st = 0; st < kPairSlots; ++st) drain(pfull + 8 * st, (pairs - st + kPairSlots - 1) / kPairSlots);
+      for (int st = 0; st < kStateSlots; ++st) drain(sfull + 8 * st, (states - st + kStateSlots - 1) / kStateSlots);
     }
   } else if (warp == 1) {
     // ---- products ----
-    int step = 0, item = 0, head = 0;
+    int pairs = 0, states = 0, item = 0, head = 0;
     for (int64_t at = blockIdx.x; at < p.items && ok; at += gridDim.x) {
-      int row0, n;
-      if (!find_chunk(p.cu, p.nseq, p.total, at / p.Hk, lane, row0, n)) continue;
+      Chunk x;
+      if (!find_chunk(p.cu, p.nseq, p.total, at / p.Hk, lane, x)) continue;
       if (elect_one()) {
         const int width = p.K > kPanelCols ? 128 : 64;  // channels of the results
         const uint32_t d_xy = mma_desc(kDelta, false, false), d_state = mma_desc(width, false, false);
@@ -173,44 +189,53 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
         ok = DELTA_WAIT(kqfull, item);
         for (int h = 0; h < ratio && ok; ++h, ++head) {
           const uint32_t xy_acc = tmem + kAccXy + (head & 1) * kDelta;
-          // X and Y of as many steps as there are slots, then the products with the states
+          // X and Y of as many tiles as there are slots, then the products with the states of one for each
+          // further one, and of those that are left
           int done = 0;
-          for (int s = 0; s < steps && ok; ++s) {
-            const int st = (step + s) % kGradStages;
-            const uint32_t src = smem + st * kStepBytes, u = src + kStepOut + 2 * kStepState;
-            const int ks = (min(64, p.V - 64 * s) + 15) / 16;
-            if (!(ok = DELTA_WAIT(full + 8 * st, (step + s) / kGradStages))) break;
+          auto with_states = [&](int end) {
+            if (done == 0 && head > 0 && !(ok = DELTA_WAIT(headfree, head - 1))) return;
+            for (; done < end && ok; ++done, ++states) {
+              const int at_pair = (pairs + done) % kPairSlots, at_state = states % kStateSlots;
+              if (!(ok = DELTA_WAIT(sfull + 8 * at_state, states / kStateSlots))) return;
+              tc_fence_after();
+              const uint32_t pair = smem + at_pair * kPairSlot, u = pair + 2 * kTokenPanel;
+              const uint32_t state = smem + kOffStates + at_state * kStateSlot;
+              const int ks = (min(kColumns, p.V - kColumns * done) + 15) / 16;
+#pragma unroll 1
+              for (int j = 0; j < ks; ++j) {
+                const uint64_t second = term_desc(u, 0) + 2 * j, first = second + kTokenPanel / 16;  // at row 64: the other
+                const uint64_t rows = term_desc(pair, 0) + 2 * j, start = term_desc(state, 0) + 2 * j;
+                const uint64_t end = term_desc(state + 2 * kStatePanel, 0) + 2 * j;
+                mma_ss(tmem + kAccState, rows, start, d_state, done + j > 0);
+                mma_ss(tmem + kAccState, rows, start + kStatePanel / 16, d_state, true);
+                mma_ss(tmem + kAccEnd, second, end, d_state, done + j > 0);          // rows 64 on: u's first terms
+                mma_ss(tmem + kAccEnd, second, end + kStatePanel / 16, d_state, true);
+                mma_ss(tmem + kAccEnd, first, end, d_state, true);                    // u's second terms
+              }
+              mma_commit(pempty + 8 * at_pair);
+              mma_commit(sempty + 8 * at_state);
+            }
+          };
+          for (int s = 0; s < p.tiles && ok; ++s) {
+            const int st = (pairs + s) % kPairSlots;
+            const uint32_t pair = smem + st * kPairSlot, u = pair + 2 * kTokenPanel;
+            const int ks = (min(kColumns, p.V - kColumns * s) + 15) / 16;
+            if (!(ok = DELTA_WAIT(pfull + 8 * st, (pairs + s) / kPairSlots))) break;
             tc_fence_after();
-            const uint64_t a = tile_desc(src, 0);
 #pragma unroll 1
             for (int j = 0; j < ks; ++j) {
-              const uint64_t lo = term_desc(u + (j >> 1) * kUPart, 0) + 2 * (j & 1);
-              mma_ss(xy_acc, a + 2 * j, lo + kTokenPanel / 16, d_xy, s + j > 0);
-              mma_ss(xy_acc, a + 2 * j, lo, d_xy, true);
+              const uint64_t a = term_desc(pair, 0) + 2 * j, second = term_desc(u, 0) + 2 * j;
+              mma_ss(xy_acc, a, second + kTokenPanel / 16, d_xy, s + j > 0);
+              mma_ss(xy_acc, a, second, d_xy, true);
             }
-            if (s + 1 == steps) mma_commit(xyfull);
-            if (s + 1 < steps && s + 1 < done + kGradStages) continue;
-            if (done == 0 && head > 0 && !(ok = DELTA_WAIT(headfree, head - 1))) break;
-            tc_fence_after();
-            for (; done <= s; ++done) {
-              const int at_slot = (step + done) % kGradStages;
-              const uint32_t from = smem + at_slot * kStepBytes, uu = from + kStepOut + 2 * kStepState;
-              const uint64_t b = tile_desc(from, 0);
-              const int kd = (min(64, p.V - 64 * done) + 15) / 16;
-#pragma unroll 1
-              for (int j = 0; j < kd; ++j) {
-                const uint32_t tile = (j >> 1) * kStatePanel;
-                const uint64_t state = term_desc(from + kStepOut + tile, 0) + 2 * (j & 1);
-                const uint64_t end = term_desc(from + kStepOut + kStepState + tile, 0) + 2 * (j & 1);
-                const uint64_t lo = term_desc(uu + (j >> 1) * kUPart, 0) + 2 * (j & 1);
-                mma_ss(tmem + kAccState, b + 2 * j, state, d_state, done + j > 0);
-                mma_ss(tmem + kAccEnd, lo, end, d_state, done + j > 0);            // rows 64 on: u's first terms
-                mma_ss(tmem + kAccEnd, lo + kTokenPanel / 16, end, d_state, true);  // and the second ones
-              }
-              mma_commit(empty + 8 * at_slot);
+            if (s + 1 == p.tiles) {
+              mma_commit(xyfull);
+              with_states(p.tiles);
+            } else if (s + 1 >= kPairSlots) {
+              with_states(s + 2 - kPairSlots);
             }
           }
-          step += steps;
+          pairs += p.tiles;
           if (!ok || !(ok = DELTA_WAIT(xyready, head))) break;
           tc_fence_after();
           const uint64_t k = tile_desc(smem + kOffGradKq, kPanelBytes);
@@ -232,7 +257,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
         if (ok) mma_commit(kqempty);
       }
       ok = __all_sync(0xffffffffu, ok);
-      step = __reduce_max_sync(0xffffffffu, step);
+      pairs = __reduce_max_sync(0xffffffffu, pairs);
+      states = __reduce_max_sync(0xffffffffu, states);
       head = __reduce_max_sync(0xffffffffu, head);
       ++item;
     }
@@ -244,8 +270,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
     // ---- dbeta, and dg summed up from each token to its chunk's end ----
     for (int64_t at = blockIdx.x; at < p.items; at += gridDim.x) {
       const int64_t slot = at / p.Hk;
-      int row0, n;
-      if (!find_chunk(p.cu, p.nseq, p.total, slot, lane, row0, n)) continue;
+      Chunk chunk;
+      if (!find_chunk(p.cu, p.nseq, p.total, slot, lane, chunk)) continue;
+      const int row0 = chunk.row0, n = chunk.n;
       for (int h = 0; h < ratio; ++h) {
         const int hv = static_cast<int>(at % p.Hk) * ratio + h;
         double x[2] = {0.0, 0.0}, up;
@@ -290,8 +317,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
     // ---- the heads' gates, two ahead ----
     int head = 0;
     for (int64_t at = blockIdx.x; at < p.items && ok; at += gridDim.x) {
-      int row0, n;
-      if (!find_chunk(p.cu, p.nseq, p.total, at / p.Hk, lane, row0, n)) continue;
+      Chunk chunk;
+      if (!find_chunk(p.cu, p.nseq, p.total, at / p.Hk, lane, chunk)) continue;
+      const int row0 = chunk.row0, n = chunk.n;
       for (int h = 0; h < ratio; ++h, ++head) {
         const int hv = static_cast<int>(at % p.Hk) * ratio + h;
         float g[2];
@@ -332,8 +360,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
     int item = 0, head = 0;
     for (int64_t at = blockIdx.x; at < p.items && ok; at += gridDim.x) {
       const int hk = static_cast<int>(at % p.Hk);
-      int row0, n;
-      if (!find_chunk(p.cu, p.nseq, p.total, at / p.Hk, lane, row0, n)) continue;
+      Chunk chunk;
+      if (!find_chunk(p.cu, p.nseq, p.total, at / p.Hk, lane, chunk)) continue;
+      const int row0 = chunk.row0, n = chunk.n;
       float acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0.f;
@@ -461,62 +490,57 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
   }
 }
 
-// dg, second part: what the chunks behind a token's add.  First the chunks' sums become sums over all
-// later chunks of the sequence, a warp for each sequence and value head; then these are added, a CTA for
-// each chunk.  The sums over chunks are kept in 64 bits: they add up terms of both signs over the whole
-// sequence, and what is left of them is small where a head forgets fast.
+// dg, second part: what the chunks behind a token's add, to the next anchor or the sequence's end.  A CTA
+// for each chunk, a warp for each value head in turn; kept in 64 bits, since terms of both signs cancel.
 struct GateArgs {
   const int32_t* cu;
-  double* sums;
+  const double* sums;
+  const float* adots;
   float* dg;
-  int total, nseq, Hv;
+  int total, nseq, Hv, parts;  // parts of an anchor
   int64_t slots;
 };
-constexpr int kGateWarps = 4;
-__global__ void __launch_bounds__(kGateWarps * 32) cattn_delta_scan_kernel(const GateArgs p) {
+constexpr int kGateThreads = 256;
+__global__ void __launch_bounds__(kGateThreads) cattn_delta_gates_kernel(const GateArgs p) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kGateWarps + threadIdx.x / 32;
+  __shared__ double later[kGateThreads];
   const int lane = threadIdx.x % 32;
-  if (i >= static_cast<int64_t>(p.nseq) * p.Hv) return;
-  const int seq = static_cast<int>(i / p.Hv), hv = static_cast<int>(i % p.Hv);
-  int a, b;
-  sequence_rows(p.cu, seq, p.total, a, b);
-  double* sums = p.sums + hv * p.slots + a / kDelta + seq;
-  double carry = 0.0;
-  for (int64_t top = (b - a + kDelta - 1) / kDelta; top > 0; top -= 32) {
-    const int64_t c = top - 1 - lane;
-    const double own = c >= 0 ? sums[c] : 0.0;
-    double x = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (c >= 0) sums[c] = carry + (x - own);
-    carry += __shfl_sync(0xffffffffu, x, 31);
-  }
-}
-__global__ void __launch_bounds__(256) cattn_delta_later_kernel(const GateArgs p) {
-  cconv::grid_dependency_wait();
-  cconv::grid_launch_dependents();
-  int row0, n;
+  Chunk x;
   const int64_t slot = blockIdx.x;
-  if (!find_chunk(p.cu, p.nseq, p.total, slot, threadIdx.x % 32, row0, n)) return;
-  float* dg = p.dg + static_cast<int64_t>(row0) * p.Hv;
-  for (int64_t i = threadIdx.x; i < static_cast<int64_t>(n) * p.Hv; i += blockDim.x)
-    dg[i] = static_cast<float>(p.sums[i % p.Hv * p.slots + slot] + static_cast<double>(dg[i]));
+  if (!find_chunk(p.cu, p.nseq, p.total, slot, lane, x)) return;
+  const int chunks = (x.b - x.a + kDelta - 1) / kDelta, next = (x.c / kAnchorChunks + 1) * kAnchorChunks;
+  float* dg = p.dg + static_cast<int64_t>(x.row0) * p.Hv;
+  for (int first = 0; first < p.Hv; first += kGateThreads) {
+    const int heads = min(kGateThreads, p.Hv - first);
+    for (int i = threadIdx.x / 32; i < heads; i += kGateThreads / 32) {
+      const int hv = first + i;
+      double sum = 0.0;
+      if (x.c + 1 + lane < min(next, chunks)) sum = p.sums[hv * p.slots + slot + 1 + lane];
+      if (next < chunks) {
+        const float* part = p.adots + (anchor_of(x.a, x.seq, next) * p.Hv + hv) * p.parts;
+        for (int j = lane; j < p.parts; j += 32) sum += static_cast<double>(part[j]);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) later[i] = sum;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < x.n * heads; i += kGateThreads) {
+      float* at = dg + static_cast<int64_t>(i / heads) * p.Hv + first + i % heads;
+      *at = static_cast<float>(later[i % heads] + static_cast<double>(*at));
+    }
+    __syncthreads();
+  }
 }
 
 int launch_delta_gates(const DeltaCall& c, cudaStream_t stream) {
   const int64_t slots = delta_slots(c.s.total, c.s.nseq);
-  GateArgs a{c.cu, c.sums, c.dg, c.s.total, c.s.nseq, c.s.Hv, slots};
-  const int64_t warps = static_cast<int64_t>(c.s.nseq) * c.s.Hv;
-  if (launch_pdl(cattn_delta_scan_kernel, dim3(static_cast<unsigned>((warps + kGateWarps - 1) / kGateWarps)),
-                 dim3(kGateWarps * 32), 0, stream, a) != cudaSuccess ||
-      launch_pdl(cattn_delta_later_kernel, dim3(static_cast<unsigned>(slots)), dim3(256), 0, stream, a) != cudaSuccess)
-    return CCONV_ERR_CUDA;
-  return CCONV_OK;
+  const GateArgs a{c.cu, c.sums, c.adots, c.dg, c.s.total, c.s.nseq, c.s.Hv, delta_tiles(c.s.V) * kRowWarps, slots};
+  return launch_pdl(cattn_delta_gates_kernel, dim3(static_cast<unsigned>(slots)), dim3(kGateThreads), 0, stream, a) ==
+                 cudaSuccess
+             ? CCONV_OK
+             : CCONV_ERR_CUDA;
 }
 
 int launch_delta_grads(const DeltaCall& c, cudaStream_t stream) {
@@ -524,9 +548,9 @@ int launch_delta_grads(const DeltaCall& c, cudaStream_t stream) {
   int rc = bind_context(), sms = 0;
   if (rc == CCONV_OK) rc = encode_tile_map(&a.mq, c.q, c.s.total, c.s.Hk, c.s.K, kDelta);
   if (rc == CCONV_OK) rc = encode_tile_map(&a.mk, c.k, c.s.total, c.s.Hk, c.s.K, kDelta);
-  if (rc == CCONV_OK) rc = encode_tile_map(&a.mo, c.d_o, c.s.total, c.s.Hv, c.s.V, kDelta);
+  if (rc == CCONV_OK) rc = encode_tile_map(&a.mo, c.d_o, c.s.total, c.s.Hv, c.s.V, kDelta, kColumns);
   if (rc == CCONV_OK)
-    rc = encode_tile_map(&a.mv, Rows{c.dv, int64_t(c.s.Hv) * c.s.V, c.s.V}, c.s.total, c.s.Hv, c.s.V, kDelta);
+    rc = encode_tile_map(&a.mv, Rows{c.dv, int64_t(c.s.Hv) * c.s.V, c.s.V}, c.s.total, c.s.Hv, c.s.V, kDelta, kColumns);
   if (rc == CCONV_OK) rc = sm_count(&sms);
   if (rc != CCONV_OK) return rc;
   a.g = c.g;

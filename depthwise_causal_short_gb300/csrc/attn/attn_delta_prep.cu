@@ -107,8 +107,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4) cattn_delta_prep_kernel(const
   cconv::grid_launch_dependents();
   const int hv = static_cast<int>(blockIdx.x % p.Hv);
   const int64_t slot = blockIdx.x / p.Hv;
-  int row0 = 0, n = 0;
-  const bool live = find_chunk(p.cu, p.nseq, p.total, slot, lane, row0, n);
+  Chunk chunk;
+  const bool live = find_chunk(p.cu, p.nseq, p.total, slot, lane, chunk);
+  const int row0 = live ? chunk.row0 : 0, n = live ? chunk.n : 0;
   bool ok = true;
   if (live) {
     uint8_t* record = p.records + (slot * p.Hv + hv) * kRecordBytes;
