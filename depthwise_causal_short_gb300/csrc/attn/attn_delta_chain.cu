@@ -8,7 +8,7 @@
 //   [J; P~] X      -> z = r + J X,  u = beta z;          o = scale (ef . (Q S) + P~ X)
 //   K^T (eb . u)   -> S = total S + ..
 // The three terms of S, X and eb . u lie side by side as columns of one operand (N = 96), so that A is
-// read once for all three; their products are added up in registers.
+// read once for all three; their products are added up in registers.  (Two terms without a state to leave.)
 // The gradient runs the same chain first (BWD): it leaves z, two terms of u and of every S_0 (and
 // every kAnchorChunks-th in fp32), and o . do in place of o.  Its own chain, from the last chunk to the first,
 // is attn_delta_back.cu.
@@ -96,7 +96,7 @@ __device__ __forceinline__ ChainPlace chain_place(const ChainArgs& p, int lane) 
   return w;
 }
 
-template <bool BWD>
+template <bool BWD, int TERMS>
 __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(const __grid_constant__ ChainArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -152,8 +152,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
         load_kq(slot, kfull + 8 * st, &p.mk, &p.mq, panels, hk, w.a + c * kDelta);
         part = 1;
         if (c > 0 && !(ok = DELTA_WAIT(acc2, c - 1))) break;
-        bar_expect(rfull + 8 * st, kRecordBytes);
-        bulk_load(slot + kSlotKq, p.records + ((slot0 + c) * p.Hv + w.hv) * kRecordBytes, kRecordBytes, rfull + 8 * st);
+        constexpr int bytes = TERMS == kTerms ? kRecordBytes : kRecordThird;
+        bar_expect(rfull + 8 * st, bytes);
+        bulk_load(slot + kSlotKq, p.records + ((slot0 + c) * p.Hv + w.hv) * kRecordBytes, bytes, rfull + 8 * st);
         part = 0;
       }
       for (int st = 0; st < 2; ++st) {
@@ -166,9 +167,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
     if (elect_one()) {
       const int ksteps = (p.K + 15) / 16;
       const uint64_t ds = term_desc(smem + kOffState, kStatePanel), dx = term_desc(smem + kOffX, kTokenPanel);
-      const uint32_t three = mma_desc(3 * kColumns, false, true), two = mma_desc(2 * kColumns, false, true);
+      const uint32_t all = mma_desc(TERMS * kColumns, false, true), less = mma_desc((TERMS - 1) * kColumns, false, true);
       const uint32_t one = mma_desc(kColumns, false, true);
-      const uint32_t last = mma_desc(3 * kColumns, true, true);
+      const uint32_t last = mma_desc(TERMS * kColumns, true, true);
       auto copy_kq = [&](int c) {
         const int st = c & 1;
         if (!(ok = DELTA_WAIT(kfull + 8 * st, c / 2))) return;
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
         tc_fence_after();
 #pragma unroll 1
         for (int j = 0; j < ksteps; ++j)  // [K; Q] S
-          mma_ts(tmem + kTmFirst, tmem + kTmKq + 8 * j, ds + j * kTermStep, three, j > 0);
+          mma_ts(tmem + kTmFirst, tmem + kTmKq + 8 * j, ds + j * kTermStep, all, j > 0);
         mma_commit(acc1);
         if (!(ok = DELTA_WAIT(rfull + 8 * st, c / 2))) break;
         const uint64_t djp = record_desc(slot + kSlotKq, false);
@@ -192,15 +193,17 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
         for (int j = 0; j < kDelta / 16; ++j) {
           tmem_copy(tmem + kTmJp + 8 * j, djp + j * kRecordCols);
           tmem_copy(tmem + kTmJp + 32 + 8 * j, djp + j * kRecordCols + kRecordTerm);
-          tmem_copy(tmem + kTmJp + 64 + 8 * j, djp + kRecordThird / 16 + j * kRecordTerm);
+          if (TERMS == kTerms)
+            tmem_copy(tmem + kTmJp + 64 + 8 * j, djp + kRecordThird / 16 + j * kRecordTerm);
         }
         if (!(ok = DELTA_WAIT(xready, c))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int j = 0; j < kDelta / 16; ++j) {  // [J; P~] X
-          mma_ts(tmem + kTmSecond, tmem + kTmJp + 8 * j, dx + j * kTermStep, three, j > 0);
-          mma_ts(tmem + kTmSecond, tmem + kTmJp + 32 + 8 * j, dx + j * kTermStep, two, true);
-          mma_ts(tmem + kTmSecond, tmem + kTmJp + 64 + 8 * j, dx + j * kTermStep, one, true);
+          mma_ts(tmem + kTmSecond, tmem + kTmJp + 8 * j, dx + j * kTermStep, all, j > 0);
+          mma_ts(tmem + kTmSecond, tmem + kTmJp + 32 + 8 * j, dx + j * kTermStep, less, true);
+          if (TERMS == kTerms)
+            mma_ts(tmem + kTmSecond, tmem + kTmJp + 64 + 8 * j, dx + j * kTermStep, one, true);
         }
         mma_commit(acc2);
         if (c + 1 < chunks) copy_kq(c + 1);
@@ -250,8 +253,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
         S[4 * i] = x.x, S[4 * i + 1] = x.y, S[4 * i + 2] = x.z, S[4 * i + 3] = x.w;
       }
     }
-    put_terms8(smem + kOffState, kStatePanel, row, 2 * h, S);
-    put_terms8(smem + kOffState, kStatePanel, row, 2 * h + 1, S + 8);
+    put_terms8<TERMS>(smem + kOffState, kStatePanel, row, 2 * h, S);
+    put_terms8<TERMS>(smem + kOffState, kStatePanel, row, 2 * h + 1, S + 8);
     cconv::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) bar_arrive(sready);
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
       const float total = gates[kTotal];
       if (!(ok = DELTA_WARP_WAIT(acc1, c))) break;
       tc_fence_after();
-      Pairs y = load_sum<3>(mine + kTmFirst), x;
+      Pairs y = load_sum<TERMS>(mine + kTmFirst), x;
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
           if (t + 8 * r >= n) v.v[j][r] = 0;
           x.v[j][r] = f2_mul(f2_splat(beta[r]), v.v[j][r]);
         }
-      put_pairs(smem + kOffX, t, h, lane, x);
+      put_pairs<TERMS>(smem + kOffX, t, h, lane, x);
       if (n < kDelta) zero_tokens(smem + st * kSlotBytes, panels, n, false, threadIdx.x - 128);
       cconv::fence_proxy_async_smem();
       tc_fence_before();
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
       if (lane == 0) bar_arrive(xready);
       if (!(ok = DELTA_WARP_WAIT(acc2, c))) break;
       tc_fence_after();
-      y = load_sum<3>(mine + kTmSecond);
+      y = load_sum<TERMS>(mine + kTmSecond);
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -311,14 +314,14 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
           x.v[j][r] = f2_mul(f2_splat(eb[r] * beta[r]), v.v[j][r]);
           if (t + 8 * r >= n) x.v[j][r] = 0;
         }
-      put_pairs(smem + kOffX, t, h, lane, x);
+      put_pairs<TERMS>(smem + kOffX, t, h, lane, x);
       cconv::fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(uready);
       // what waits for nothing more: o, or o . do, z and u
-      y = load_sum<3>(other + kTmSecond);
-      x = load_sum<3>(other + kTmFirst);
+      y = load_sum<TERMS>(other + kTmSecond);
+      x = load_sum<TERMS>(other + kTmFirst);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const bool on = t + 8 * r < n;
@@ -361,13 +364,13 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
         float z[16];
         if (!(ok = DELTA_WARP_WAIT(acc3, c))) break;
         tc_fence_after();
-        load_sum16(mine + kTmThird, z);
+        load_sum16<TERMS>(mine + kTmThird, z);
 #pragma unroll
         for (int i = 0; i < 16; ++i) S[i] = row < p.K ? fmaf(total, S[i], z[i]) : 0.f;
         if (c + 1 < chunks) {
           if (BWD && !(ok = DELTA_WARP_WAIT(kept, c))) break;
-          put_terms8(smem + kOffState, kStatePanel, row, 2 * h, S);
-          put_terms8(smem + kOffState, kStatePanel, row, 2 * h + 1, S + 8);
+          put_terms8<TERMS>(smem + kOffState, kStatePanel, row, 2 * h, S);
+          put_terms8<TERMS>(smem + kOffState, kStatePanel, row, 2 * h + 1, S + 8);
           cconv::fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
@@ -393,7 +396,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
   }
 }
 
-template <bool BWD>
+template <bool BWD, int TERMS>
 static int launch_chain(const DeltaCall& c, cudaStream_t stream) {
   ChainArgs a{};
   int rc = CCONV_OK;
@@ -412,7 +415,7 @@ static int launch_chain(const DeltaCall& c, cudaStream_t stream) {
   a.scale = c.scale;
   a.total = c.s.total, a.nseq = c.s.nseq, a.ratio = c.s.Hv / c.s.Hk, a.Hv = c.s.Hv, a.K = c.s.K, a.V = c.s.V;
   a.tiles = delta_tiles(c.s.V);
-  auto kern = cattn_delta_chain_kernel<BWD>;
+  auto kern = cattn_delta_chain_kernel<BWD, TERMS>;
   const int64_t ctas = static_cast<int64_t>(c.s.nseq) * c.s.Hv * a.tiles;
   if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(kern), kChainBytes) != CCONV_OK)
     return CCONV_ERR_CUDA;
@@ -422,7 +425,9 @@ static int launch_chain(const DeltaCall& c, cudaStream_t stream) {
              : CCONV_ERR_CUDA;
 }
 
-int launch_delta_fwd(const DeltaCall& c, cudaStream_t stream) { return launch_chain<false>(c, stream); }
-int launch_delta_states(const DeltaCall& c, cudaStream_t stream) { return launch_chain<true>(c, stream); }
+int launch_delta_fwd(const DeltaCall& c, cudaStream_t stream) {
+  return two_terms(c) ? launch_chain<false, 2>(c, stream) : launch_chain<false, kTerms>(c, stream);
+}
+int launch_delta_states(const DeltaCall& c, cudaStream_t stream) { return launch_chain<true, kTerms>(c, stream); }
 
 }  // namespace cattn

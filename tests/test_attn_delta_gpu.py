@@ -77,8 +77,12 @@ def test_parity(lens, Hk, Hv, K, V, states):
     _check(gfin, fin.detach(), STATE_TOL, "final state")
     if sum(lens):
         _check(go, o.detach(), O_TOL, "o")
+    # without a final state the factors have 16 bits each, not 24: a result that is stored with 9 bits (half a
+    # step: 2^-9 of a value at least, 2^-8 at most) moves by no more than 2^-17 a factor, so O_TOL holds for it too
     alone, none, _ = cc.cattn_delta_fwd(*args, cu, initial_state=init)
-    assert none is None and torch.equal(alone, go)
+    assert none is None and torch.equal(alone, cc.cattn_delta_fwd(*args, cu, initial_state=init)[0])
+    if sum(lens):
+        _check(alone, o.detach(), O_TOL, "o alone")
 
     grads = cc.cattn_delta_bwd(*args, do.cuda(), cu, initial_state=init)
     again = cc.cattn_delta_bwd(*args, do.cuda(), cu, initial_state=init)
@@ -119,6 +123,8 @@ def test_ends_of_the_ranges(kind):
     args = [t.cuda() for t in (q, k, v, g, beta)]
     go, gfin, _ = cc.cattn_delta_fwd(*args, _cu(lens), initial_state=s0.cuda(), final_state=True)
     _check(go, o, O_TOL, "o")
+    alone = cc.cattn_delta_fwd(*args, _cu(lens), initial_state=s0.cuda())[0]
+    _check(alone, o, O_TOL, "o alone")
     _check(gfin, fin, STATE_TOL, "final state")
 
 

@@ -272,7 +272,7 @@ def test_rows_behind_the_last_sequence_of_a_pool_stay():
 def test_a_nan_gate_or_step_reaches_what_comes_after_it():
     n, at = 300, 130
     q, k, v, g, beta, do, s0 = (t.cuda() for t in _inputs([n], 1, 2, 64, 64, seed=n))
-    clean = cc.cattn_delta_fwd(q, k, v, g, beta, _cu([n]), initial_state=s0)[0]
+    clean = cc.cattn_delta_fwd(q, k, v, g, beta, _cu([n]), initial_state=s0, final_state=True)[0]
     for i in (3, 4):
         args = [t.clone() for t in (q, k, v, g, beta)]
         args[i][at, 1] = float("nan")
@@ -305,6 +305,6 @@ def test_a_cache_behind_2_to_the_31_elements():
     wide = torch.empty(73, 1 << 25, dtype=torch.bfloat16, device="cuda")[:, -Hv * V:].view(73, Hv, V)
     wide.copy_(v)
     assert wide.stride(0) * 72 > 1 << 31
-    o, _, _ = cc.cattn_delta_fwd(q, k, wide, g, beta, _cu([70, 3]), initial_state=s0)
+    o, _, _ = cc.cattn_delta_fwd(q, k, wide, g, beta, _cu([70, 3]), initial_state=s0, final_state=True)
     assert torch.equal(o, want[0])
     assert torch.equal(cc.cattn_layernorm_fwd(wide), cc.cattn_layernorm_fwd(v))
