@@ -34,7 +34,7 @@ static DeltaWork delta_work(int64_t total, int64_t nseq, int64_t Hv, int64_t V) 
   };
   DeltaWork w{};
   w.records = take(record_bytes(total, nseq, Hv));
-  w.z = take(rows * V * 4);
+  w.z = take(states / kStatePanel * kDelta * kColumns * 4);
   w.u = take(states / kStatePanel * kUTile);
   w.heads = take(2 * states);
   w.ends = take(2 * states);

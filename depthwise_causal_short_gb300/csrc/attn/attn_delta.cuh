@@ -195,11 +195,42 @@ __device__ __forceinline__ void put_pairs(uint32_t base, int row, int h, int lan
       }
     }
 }
-// The words of a bf16 row at `src` (NULL: zeros) that hold this thread's pairs of columns.
-__device__ __forceinline__ void load_words(const uint16_t* src, int width, int lane, uint32_t (&x)[2]) {
+// Four words of each of four neighbouring lanes, turned: lane q gets word q of all (and the other way round).
+__device__ __forceinline__ void quad_turn(uint32_t (&w)[4], int lane) {
+  const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[i] : w[i + 1], 1);
+    (odd ? w[i] : w[i + 1]) = got;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w[i] : w[i + 2], 2);
+    (high ? w[i] : w[i + 2]) = got;
+  }
+}
+// Pairs as bf16, in global memory 16 bytes a lane: lane q of four has token lane / 4 + 8 (q % 2), columns
+// 8 (q / 2) on.
+__device__ __forceinline__ int quad_token(int lane) { return lane / 4 + 8 * (lane & 1); }
+__device__ __forceinline__ int quad_column(int lane) { return 8 * ((lane >> 1) & 1); }
+__device__ __forceinline__ Pairs quad_pairs(const uint4& x, int lane) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  quad_turn(w, lane);
+  Pairs p;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
-    x[j] = src && 8 * j < width ? *reinterpret_cast<const uint32_t*>(src + 8 * j + 2 * (lane & 3)) : 0u;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) p.v[j][r] = bf16x2_to_f2(w[2 * j + r]);
+  return p;
+}
+__device__ __forceinline__ uint4 quad_words(uint32_t (&w)[4], int lane) {
+  quad_turn(w, lane);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Where the gradient's chains keep z: a row warp's pairs, 16 bytes a thread and behind them (kPairsNext) 16 more.
+constexpr int kPairsNext = 32;  // ulonglong2
+__device__ __forceinline__ int64_t pairs_at(int64_t tile, int row_warp, int lane) {
+  return (tile * kRowWarps + row_warp) * 256 + lane * 4;
 }
 
 // 16 columns of this thread's row in N groups of kColumns columns: the sum.
@@ -303,7 +334,7 @@ struct DeltaCall {
   uint16_t* o;
   uint8_t* records;       // [slots][Hv] of kRecordBytes
   // the gradient's
-  float* z;               // [total][Hv][V]
+  float* z;               // [slots][Hv][tiles] of 64 rows of kColumns, as pairs_at has them
   uint8_t* u;             // [slots][Hv][tiles] two terms of u
   uint8_t *heads, *ends;  // [slots][Hv][tiles] two terms of S_0 and of D
   float *odots, *vdots, *bdots;  // [2 tiles][Hv][total] parts of o . do, v . dv and dbeta

@@ -271,28 +271,25 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
     __syncwarp();
     if (lane == 0) bar_arrive(dready);
     const uint16_t* v_at = p.v.p + hv * p.v.sh + col;
-    uint32_t vw[2][2];
+    const int turned = quarter * 16 + quad_token(lane), turned_col = quad_column(lane);
+    const bool inside = turned_col < width;
+    uint4 vw;
     Pairs zin;
     auto fetch = [&](int c) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int64_t at = static_cast<int64_t>(row_a) + c * kDelta + t + 8 * r;
-        const bool on = c >= 0 && at < row_b;
-        load_words(on ? v_at + at * p.v.st : nullptr, width, lane, vw[r]);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          zin.v[j][r] = on && 8 * j < width ? *reinterpret_cast<const f2*>(p.z + (at * p.Hv + hv) * p.V + col + 8 * j + 2 * (lane & 3)) : 0;
-      }
+      const int64_t at = static_cast<int64_t>(row_a) + c * kDelta + turned;
+      vw = make_uint4(0, 0, 0, 0);
+      if (c < 0) return;
+      if (at < row_b && inside) vw = *reinterpret_cast<const uint4*>(v_at + at * p.v.st + turned_col);
+      const ulonglong2* z = reinterpret_cast<const ulonglong2*>(
+          p.z + pairs_at(((slot0 + c) * p.Hv + hv) * p.tiles + tile, warp - 4, lane));
+      const ulonglong2 a = z[0], b = z[kPairsNext];
+      zin.v[0][0] = a.x, zin.v[0][1] = a.y, zin.v[1][0] = b.x, zin.v[1][1] = b.y;
     };
     fetch(chunks - 1);
     for (int i = 0; i < chunks; ++i) {
       const int st = i & 1, c = chunks - 1 - i, row0 = row_a + c * kDelta, n = min(kDelta, row_b - row0);
       const float* gates = reinterpret_cast<const float*>(base + st * kBackSlot + kSlotKq + kRecordGates);
-      Pairs v, z = zin;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) v.v[j][r] = bf16x2_to_f2(vw[r][j]);
+      Pairs v = quad_pairs(vw, lane), z = zin;
       fetch(c - 1);
       const bool anchor = c > 0 && c % kAnchorChunks == 0;
       const int64_t anchor_at = (anchor_of(row_a, seq, c) * p.Hv + hv) * p.tiles + tile;
@@ -341,9 +338,9 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
       tc_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(uready);
+      uint32_t words[4];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const bool on = t + 8 * r < n;
         float du_z = 0.f, dv_v = 0.f;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -353,20 +350,21 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
           du_z += a + b;
           cconv::f2_unpack(f2_mul(dv, v.v[j][r]), a, b);
           dv_v += a + b;
-          if (on && 8 * j < width)
-            *reinterpret_cast<uint32_t*>(p.dv + (static_cast<int64_t>(row0 + t + 8 * r) * p.Hv + hv) * p.V + col + 8 * j +
-                                         2 * (lane & 3)) = f2_to_bf16x2(dv);
+          words[2 * j + r] = f2_to_bf16x2(dv);
         }
         du_z += __shfl_xor_sync(0xffffffffu, du_z, 1);
         dv_v += __shfl_xor_sync(0xffffffffu, dv_v, 1);
         du_z += __shfl_xor_sync(0xffffffffu, du_z, 2);
         dv_v += __shfl_xor_sync(0xffffffffu, dv_v, 2);
-        if (on && (lane & 3) == 0) {
+        if (t + 8 * r < n && (lane & 3) == 0) {
           const int64_t at = (static_cast<int64_t>(tile * 2 + h) * p.Hv + hv) * p.total + row0 + t + 8 * r;
           p.bdots[at] = du_z;
           p.vdots[at] = dv_v;
         }
       }
+      const uint4 dv = quad_words(words, lane);
+      if (turned < n && inside)
+        *reinterpret_cast<uint4*>(p.dv + (static_cast<int64_t>(row0 + turned) * p.Hv + hv) * p.V + col + turned_col) = dv;
       if (i + 1 < chunks || p.dinit) {
         float g[16];
         if (!(ok = DELTA_WARP_WAIT(acc3, i))) break;

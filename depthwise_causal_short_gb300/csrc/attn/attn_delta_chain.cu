@@ -52,7 +52,7 @@ struct ChainArgs {
   float* fin;
   uint16_t* o;
   const uint8_t* records;
-  float* z;        // [total][Hv][V]
+  float* z;        // [slots][Hv][tiles], see pairs_at
   uint8_t* heads;  // [slots][Hv][tiles] two terms of S_0
   uint8_t* u;      // [slots][Hv][tiles] two terms of u
   float* dots;     // [2 tiles][Hv][total] parts of o . do
@@ -259,27 +259,35 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
     __syncwarp();
     if (lane == 0) bar_arrive(sready);
     const uint16_t *v_at = p.v.p + w.hv * p.v.sh + col, *do_at = p.d_o.p + w.hv * p.d_o.sh + col;
-    uint32_t vw[2][2], dw[2][2];  // [token][columns] of v and do
+    const int turned = quarter * 16 + quad_token(lane), turned_col = quad_column(lane);
+    const bool inside = turned_col < width;
+    uint4 vw;
+    uint32_t dw[2][2];  // of do: [token][columns]
     auto fetch = [&](int c) {
+      const int64_t at = static_cast<int64_t>(w.a) + c * kDelta + turned;
+      const bool on = at < w.b && inside;
+      vw = make_uint4(0, 0, 0, 0);
+      if (on) vw = *reinterpret_cast<const uint4*>(v_at + at * p.v.st + turned_col);
+      if (BWD)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int64_t at = static_cast<int64_t>(w.a) + c * kDelta + t + 8 * r;
-        load_words(at < w.b ? v_at + at * p.v.st : nullptr, width, lane, vw[r]);
-        if (BWD) load_words(at < w.b ? do_at + at * p.d_o.st : nullptr, width, lane, dw[r]);
-      }
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int64_t row = static_cast<int64_t>(w.a) + c * kDelta + t + 8 * r;
+            dw[r][j] = row < w.b && 8 * j < width
+                           ? *reinterpret_cast<const uint32_t*>(do_at + row * p.d_o.st + 8 * j + 2 * (lane & 3)) : 0u;
+          }
     };
     fetch(0);
     for (int c = 0; c < chunks; ++c) {
       const int st = c & 1, row0 = w.a + c * kDelta, n = min(kDelta, w.b - row0);
       const float* gates = reinterpret_cast<const float*>(base + st * kSlotBytes + kSlotKq + kRecordGates);
-      Pairs v, d;
+      Pairs v = quad_pairs(vw, lane), d;
+      if (BWD)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          v.v[j][r] = bf16x2_to_f2(vw[r][j]);
-          if (BWD) d.v[j][r] = bf16x2_to_f2(dw[r][j]);
-        }
+          for (int r = 0; r < 2; ++r) d.v[j][r] = bf16x2_to_f2(dw[r][j]);
       fetch(c + 1);
       if (!(ok = DELTA_WARP_WAIT(rfull + 8 * st, c / 2))) break;
       float ef[2], eb[2], beta[2];
@@ -322,37 +330,44 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
       // what waits for nothing more: o, or o . do, z and u
       y = load_sum<TERMS>(other + kTmSecond);
       x = load_sum<TERMS>(other + kTmFirst);
+      const int64_t at = ((slot0 + c) * p.Hv + w.hv) * p.tiles + w.tile;
+      uint32_t words[4], second[4];
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const bool on = t + 8 * r < n;
-        const int64_t at = static_cast<int64_t>(row0 + t + 8 * r) * p.Hv + w.hv;
-        float sum = 0.f;
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int c8 = 8 * j + 2 * (lane & 3);
+        for (int r = 0; r < 2; ++r) {
           const f2 o = f2_mul(f2_splat(p.scale), f2_fma(f2_splat(ef[r]), x.v[j][r], y.v[j][r]));
           if (BWD) {
             float a, b;
             cconv::f2_unpack(f2_mul(o, d.v[j][r]), a, b);
-            sum += a + b;
+            sum[r] += a + b;
             f2 u = f2_mul(f2_splat(beta[r]), v.v[j][r]);
-            if (!on) u = 0;
-            const uint32_t hi = f2_to_bf16x2(u);
-            uint8_t* to = p.u + (((slot0 + c) * p.Hv + w.hv) * p.tiles + w.tile) * kUTile +
-                          term_piece(t + 8 * r, 2 * h + j) + (lane & 3) * 4;
-            *reinterpret_cast<uint32_t*>(to) = hi;
-            *reinterpret_cast<uint32_t*>(to + kTokenPanel) = f2_to_bf16x2(f2_fma(bf16x2_to_f2(hi), f2_splat(-1.f), u));
-            if (on && 8 * j < width) *reinterpret_cast<f2*>(p.z + at * p.V + col + c8) = v.v[j][r];
-          } else if (on && 8 * j < width) {
-            *reinterpret_cast<uint32_t*>(p.o + at * p.V + col + c8) = f2_to_bf16x2(o);
+            if (t + 8 * r >= n) u = 0;
+            words[2 * j + r] = f2_to_bf16x2(u);
+            second[2 * j + r] = f2_to_bf16x2(f2_fma(bf16x2_to_f2(words[2 * j + r]), f2_splat(-1.f), u));
+          } else {
+            words[2 * j + r] = f2_to_bf16x2(o);
           }
         }
-        if (BWD) {
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          if (on && (lane & 3) == 0)
-            p.dots[(static_cast<int64_t>(w.tile * 2 + h) * p.Hv + w.hv) * p.total + row0 + t + 8 * r] = sum;
+      if (BWD) {
+        uint8_t* to = p.u + at * kUTile + term_piece(turned, 2 * h + turned_col / 8);
+        *reinterpret_cast<uint4*>(to) = quad_words(words, lane);
+        *reinterpret_cast<uint4*>(to + kTokenPanel) = quad_words(second, lane);
+        ulonglong2* z = reinterpret_cast<ulonglong2*>(p.z + pairs_at(at, warp - 4, lane));
+        z[0] = make_ulonglong2(v.v[0][0], v.v[0][1]);
+        z[kPairsNext] = make_ulonglong2(v.v[1][0], v.v[1][1]);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+          sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+          if (t + 8 * r < n && (lane & 3) == 0)
+            p.dots[(static_cast<int64_t>(w.tile * 2 + h) * p.Hv + w.hv) * p.total + row0 + t + 8 * r] = sum[r];
         }
+      } else {
+        const uint4 o = quad_words(words, lane);
+        if (turned < n && inside)
+          *reinterpret_cast<uint4*>(p.o + (static_cast<int64_t>(row0 + turned) * p.Hv + w.hv) * p.V + col + turned_col) = o;
       }
       if (BWD && c > 0 && c % kAnchorChunks == 0) {
         float4* to = reinterpret_cast<float4*>(
