@@ -213,15 +213,11 @@ __device__ __forceinline__ void quad_turn(uint32_t (&w)[4], int lane) {
 // 8 (q / 2) on.
 __device__ __forceinline__ int quad_token(int lane) { return lane / 4 + 8 * (lane & 1); }
 __device__ __forceinline__ int quad_column(int lane) { return 8 * ((lane >> 1) & 1); }
-__device__ __forceinline__ Pairs quad_pairs(const uint4& x, int lane) {
-  uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  quad_turn(w, lane);
-  Pairs p;
+// (Read in words of 4 bytes all the same: turned, they cost the gradient's chain 5 % of its time.)
+__device__ __forceinline__ void load_words(const uint16_t* src, int width, int lane, uint32_t (&x)[2]) {
 #pragma unroll
   for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) p.v[j][r] = bf16x2_to_f2(w[2 * j + r]);
-  return p;
+    x[j] = src && 8 * j < width ? *reinterpret_cast<const uint32_t*>(src + 8 * j + 2 * (lane & 3)) : 0u;
 }
 __device__ __forceinline__ uint4 quad_words(uint32_t (&w)[4], int lane) {
   quad_turn(w, lane);

@@ -273,13 +273,15 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
     const uint16_t* v_at = p.v.p + hv * p.v.sh + col;
     const int turned = quarter * 16 + quad_token(lane), turned_col = quad_column(lane);
     const bool inside = turned_col < width;
-    uint4 vw;
+    uint32_t vw[2][2];
     Pairs zin;
     auto fetch = [&](int c) {
-      const int64_t at = static_cast<int64_t>(row_a) + c * kDelta + turned;
-      vw = make_uint4(0, 0, 0, 0);
       if (c < 0) return;
-      if (at < row_b && inside) vw = *reinterpret_cast<const uint4*>(v_at + at * p.v.st + turned_col);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int64_t at = static_cast<int64_t>(row_a) + c * kDelta + t + 8 * r;
+        load_words(at < row_b ? v_at + at * p.v.st : nullptr, width, lane, vw[r]);
+      }
       const ulonglong2* z = reinterpret_cast<const ulonglong2*>(
           p.z + pairs_at(((slot0 + c) * p.Hv + hv) * p.tiles + tile, warp - 4, lane));
       const ulonglong2 a = z[0], b = z[kPairsNext];
@@ -289,7 +291,11 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
     for (int i = 0; i < chunks; ++i) {
       const int st = i & 1, c = chunks - 1 - i, row0 = row_a + c * kDelta, n = min(kDelta, row_b - row0);
       const float* gates = reinterpret_cast<const float*>(base + st * kBackSlot + kSlotKq + kRecordGates);
-      Pairs v = quad_pairs(vw, lane), z = zin;
+      Pairs v, z = zin;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) v.v[j][r] = bf16x2_to_f2(vw[r][j]);
       fetch(c - 1);
       const bool anchor = c > 0 && c % kAnchorChunks == 0;
       const int64_t anchor_at = (anchor_of(row_a, seq, c) * p.Hv + hv) * p.tiles + tile;

@@ -261,33 +261,27 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
     const uint16_t *v_at = p.v.p + w.hv * p.v.sh + col, *do_at = p.d_o.p + w.hv * p.d_o.sh + col;
     const int turned = quarter * 16 + quad_token(lane), turned_col = quad_column(lane);
     const bool inside = turned_col < width;
-    uint4 vw;
-    uint32_t dw[2][2];  // of do: [token][columns]
+    uint32_t vw[2][2], dw[2][2];  // [token][columns] of v and do
     auto fetch = [&](int c) {
-      const int64_t at = static_cast<int64_t>(w.a) + c * kDelta + turned;
-      const bool on = at < w.b && inside;
-      vw = make_uint4(0, 0, 0, 0);
-      if (on) vw = *reinterpret_cast<const uint4*>(v_at + at * p.v.st + turned_col);
-      if (BWD)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int64_t row = static_cast<int64_t>(w.a) + c * kDelta + t + 8 * r;
-            dw[r][j] = row < w.b && 8 * j < width
-                           ? *reinterpret_cast<const uint32_t*>(do_at + row * p.d_o.st + 8 * j + 2 * (lane & 3)) : 0u;
-          }
+      for (int r = 0; r < 2; ++r) {
+        const int64_t at = static_cast<int64_t>(w.a) + c * kDelta + t + 8 * r;
+        load_words(at < w.b ? v_at + at * p.v.st : nullptr, width, lane, vw[r]);
+        if (BWD) load_words(at < w.b ? do_at + at * p.d_o.st : nullptr, width, lane, dw[r]);
+      }
     };
     fetch(0);
     for (int c = 0; c < chunks; ++c) {
       const int st = c & 1, row0 = w.a + c * kDelta, n = min(kDelta, w.b - row0);
       const float* gates = reinterpret_cast<const float*>(base + st * kSlotBytes + kSlotKq + kRecordGates);
-      Pairs v = quad_pairs(vw, lane), d;
-      if (BWD)
+      Pairs v, d;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) d.v[j][r] = bf16x2_to_f2(dw[r][j]);
+        for (int r = 0; r < 2; ++r) {
+          v.v[j][r] = bf16x2_to_f2(vw[r][j]);
+          if (BWD) d.v[j][r] = bf16x2_to_f2(dw[r][j]);
+        }
       fetch(c + 1);
       if (!(ok = DELTA_WARP_WAIT(rfull + 8 * st, c / 2))) break;
       float ef[2], eb[2], beta[2];
