@@ -204,10 +204,10 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
       drain(alldone, 1);
     }
   } else if (warp == 2) {
-    // ---- two terms of every D ----
+    // ---- two terms of every D, once K D does not read beside it ----
     if (elect_one()) {
       for (int i = 0; i < chunks && ok; ++i) {
-        if (!(ok = DELTA_WAIT(dready, i))) break;
+        if (!(ok = DELTA_WAIT(dready, i)) || !(ok = DELTA_WAIT(acc1, i))) break;
         bulk_store(p.ends + (((slot0 + chunks - 1 - i) * p.Hv + hv) * p.tiles + tile) * 2 * kStatePanel, smem + kOffD,
                    2 * kStatePanel);
         stores_commit();
