@@ -33,8 +33,9 @@ constexpr int kMaxNorm = 8192;
 constexpr int ln_threads(int group) { return group > kLnThreads ? group : group > 32 ? group : kLnThreads; }
 // Threads an SM that a kernel's registers leave room for: the grids are that many, and each CTA goes on to
 // the rows that are left.
-constexpr int kLnFwdRoom = 1024;
-constexpr int ln_bwd_room(int pieces) { return pieces > 1 ? 512 : 768; }
+// (16384 rows of 16 heads of 128: forward 31 us, 36 with room for 768, 34 for 1536; gradient 55, 59 with room for
+// 768, 72 for 1024.)
+constexpr int kLnFwdRoom = 1024, kLnBwdRoom = 512;
 
 using cconv::f2_unpack;
 
@@ -260,7 +261,7 @@ __device__ __forceinline__ void put_sums(f2 (&s)[PIECES][4], const bool (&on)[PI
 }
 
 template <int GROUP, int PIECES, bool GATE>
-__global__ void __launch_bounds__(ln_threads(GROUP), ln_bwd_room(PIECES) / ln_threads(GROUP))
+__global__ void __launch_bounds__(ln_threads(GROUP), kLnBwdRoom / ln_threads(GROUP))
     cattn_layernorm_bwd_kernel(const LnArgs p) {
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
@@ -391,36 +392,50 @@ __global__ void __launch_bounds__(kSumCols * kSumRows)
 }
 
 struct LnKernel {
-  void (*fwd[2])(LnArgs);
-  void (*bwd[2])(LnArgs);
-  int threads, rows;  // of a CTA
-  int piece_bytes;    // shared memory of a tensor's rows ahead
-  int bwd_room;
+  void (*run[2])(LnArgs);  // without a gate, with one
+  int threads, rows;       // of a CTA
+  int piece_bytes;         // shared memory of a tensor's rows ahead
+  int room;
 };
-template <int GROUP, int PIECES>
+template <int GROUP, int PIECES, bool BWD>
 static LnKernel kernel_of() {
-  return LnKernel{{cattn_layernorm_fwd_kernel<GROUP, PIECES, false>, cattn_layernorm_fwd_kernel<GROUP, PIECES, true>},
-                  {cattn_layernorm_bwd_kernel<GROUP, PIECES, false>, cattn_layernorm_bwd_kernel<GROUP, PIECES, true>},
-                  ln_threads(GROUP), ln_threads(GROUP) / GROUP,
-                  kLnAhead * PIECES * ln_threads(GROUP) * 16,
-                  ln_bwd_room(PIECES)};
+  constexpr int threads = ln_threads(GROUP);
+  LnKernel k{{}, threads, threads / GROUP, kLnAhead * PIECES * threads * 16, 0};
+  if constexpr (BWD) {
+    k.run[0] = cattn_layernorm_bwd_kernel<GROUP, PIECES, false>, k.run[1] = cattn_layernorm_bwd_kernel<GROUP, PIECES, true>;
+    k.room = kLnBwdRoom;
+  } else {
+    k.run[0] = cattn_layernorm_fwd_kernel<GROUP, PIECES, false>, k.run[1] = cattn_layernorm_fwd_kernel<GROUP, PIECES, true>;
+    k.room = kLnFwdRoom;
+  }
+  return k;
 }
-// The smallest group that holds a row in one piece a thread, to 1024 channels, and in two above: 8192 rows of
-// 4096 channels 44 us with 256 threads (their gradient; two CTAs an SM), 57 with 512 and a piece each, 51 with
-// 128 and four.
-static LnKernel pick(int64_t C) {
-  if (C <= 32) return kernel_of<4, 1>();
-  if (C <= 64) return kernel_of<8, 1>();
-  if (C <= 128) return kernel_of<16, 1>();
-  if (C <= 256) return kernel_of<32, 1>();
-  if (C <= 512) return kernel_of<64, 1>();
-  if (C <= 1024) return kernel_of<128, 1>();
-  if (C <= 2048) return kernel_of<128, 2>();
-  if (C <= 4096) return kernel_of<256, 2>();
-  return kernel_of<512, 2>();
+// The smallest group that holds a row in one piece a thread, to 128 channels, and in two above; in four in a
+// forward without a gate, to 1024 (more tensors or more threads a row, and they cost more than they save).
+// Measured, us, 33.5 million elements; pieces 1 / 2 / 4:
+//   rows of 256     forward 21.9 / 21.8 / 18.9    with a gate 35.0 / 33.6 / 41.7    its gradient 71.3 / 60.7 / 136
+//   512             29.5 / 25.3 / 20.6            - / 35.5 / 43.5                   without a gate 52.9 / 34.3 / 72
+//   1024            30.3 / 26.0 / 24.0            40.9 / 36.3 / 46.9                52.5 / 40.6 / 78
+//   4096            - / 23.4 / 26.0               - / 37.0 / 39.9                   57 / 43.2 / 83
+template <bool BWD>
+static LnKernel pick(int64_t C, bool gate) {
+  if (!BWD && !gate && C > 128 && C <= 1024) {
+    if (C <= 256) return kernel_of<8, 4, BWD>();
+    if (C <= 512) return kernel_of<16, 4, BWD>();
+    return kernel_of<32, 4, BWD>();
+  }
+  if (C <= 32) return kernel_of<4, 1, BWD>();
+  if (C <= 64) return kernel_of<8, 1, BWD>();
+  if (C <= 128) return kernel_of<16, 1, BWD>();
+  if (C <= 256) return kernel_of<16, 2, BWD>();
+  if (C <= 512) return kernel_of<32, 2, BWD>();
+  if (C <= 1024) return kernel_of<64, 2, BWD>();
+  if (C <= 2048) return kernel_of<128, 2, BWD>();
+  if (C <= 4096) return kernel_of<256, 2, BWD>();
+  return kernel_of<512, 2, BWD>();
 }
-static int64_t ctas_of(int64_t rows, const LnKernel& kern, int sms, int room) {
-  const int64_t ctas = (rows + kern.rows - 1) / kern.rows, most = static_cast<int64_t>(sms) * (room / kern.threads);
+static int64_t ctas_of(int64_t rows, const LnKernel& kern, int sms) {
+  const int64_t ctas = (rows + kern.rows - 1) / kern.rows, most = static_cast<int64_t>(sms) * (kern.room / kern.threads);
   return ctas < most ? ctas : most;
 }
 
@@ -477,9 +492,9 @@ extern "C" CCONV_API int cattn_layernorm_fwd(const void* x, int64_t sxt, int64_t
   a.y = static_cast<uint16_t*>(y);
   int sms = 0;
   if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
-  const LnKernel kern = pick(C);
-  const int64_t ctas = ctas_of(a.rows, kern, sms, kern.threads > kLnFwdRoom ? kern.threads : kLnFwdRoom);
-  return launch_rows(kern.fwd[gate != nullptr], kern, ctas, gate ? 2 : 1, a, stream);
+  const LnKernel kern = pick<false>(C, gate != nullptr);
+  const int64_t ctas = ctas_of(a.rows, kern, sms);
+  return launch_rows(kern.run[gate != nullptr], kern, ctas, gate ? 2 : 1, a, stream);
 }
 
 extern "C" CCONV_API int cattn_layernorm_bwd_workspace_bytes(int64_t total, int64_t H, int64_t C, size_t* bytes) {
@@ -488,8 +503,8 @@ extern "C" CCONV_API int cattn_layernorm_bwd_workspace_bytes(int64_t total, int6
   if (total < 0 || total > kMaxRows || H < 1 || H > 65535 || C < 1 || C > kMaxNorm) return CCONV_ERR_SHAPE;
   int sms = 0;
   if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
-  const LnKernel kern = pick(C);
-  const int64_t ctas = ctas_of(total * H, kern, sms, kern.bwd_room);
+  const LnKernel kern = pick<true>(C, false);
+  const int64_t ctas = ctas_of(total * H, kern, sms);
   *bytes = static_cast<size_t>(ctas > 0 ? ctas : 1) * 2 * static_cast<size_t>(C) * 4;
   return CCONV_OK;
 }
@@ -516,8 +531,8 @@ extern "C" CCONV_API int cattn_layernorm_bwd(const void* x, int64_t sxt, int64_t
   a.y = static_cast<uint16_t*>(dx), a.dz = static_cast<uint16_t*>(dgate);
   int sms = 0;
   if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
-  const LnKernel kern = pick(C);
-  const int64_t ctas = ctas_of(a.rows, kern, sms, kern.bwd_room);
+  const LnKernel kern = pick<true>(C, gate != nullptr);
+  const int64_t ctas = ctas_of(a.rows, kern, sms);
   const bool sums = dw || db;
   if (sums) {
     if (!workspace || workspace_bytes < static_cast<size_t>(ctas > 0 ? ctas : 1) * 2 * C * 4)
@@ -525,7 +540,7 @@ extern "C" CCONV_API int cattn_layernorm_bwd(const void* x, int64_t sxt, int64_t
     if (!aligned(workspace, 16)) return CCONV_ERR_ALIGN;
     a.part = static_cast<float*>(workspace);
   }
-  if (total > 0 && launch_rows(kern.bwd[gate != nullptr], kern, ctas, gate ? 3 : 2, a, stream) != CCONV_OK)
+  if (total > 0 && launch_rows(kern.run[gate != nullptr], kern, ctas, gate ? 3 : 2, a, stream) != CCONV_OK)
     return CCONV_ERR_CUDA;
   if (!sums) return CCONV_OK;
   return launch_pdl(cattn_layernorm_sums_kernel, dim3(static_cast<unsigned>((2 * C + kSumCols - 1) / kSumCols)),
