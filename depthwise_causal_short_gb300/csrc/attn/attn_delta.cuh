@@ -25,7 +25,8 @@
 //
 // Precision: products run on bf16 with fp32 accumulators; an fp32 factor is split into three bf16
 // terms (24 bits), and for two such factors the products of terms down to 2^-16 are summed.  A forward that
-// leaves no state takes two terms (16 bits, products down to 2^-8): its one result is bf16, 9 bits.
+// leaves no state takes two terms (16 bits, products down to 2^-8): its one result is bf16, 9 bits (16384 rows of
+// 16 heads: 336 us, 373 with three).
 #pragma once
 
 #include "attn_chunk.cuh"

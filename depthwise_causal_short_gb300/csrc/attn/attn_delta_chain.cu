@@ -13,7 +13,11 @@
 // every kAnchorChunks-th in fp32), and o . do in place of o.  Its own chain, from the last chunk to the first,
 // is attn_delta_back.cu.
 //
-// Bound by that chain: a product, its results to registers, the next operand to shared memory.
+// Bound by that chain: a product, its results to registers, the next operand to shared memory.  2 sequences of
+// 8192 rows, 16 heads of 128 x 128 (128 CTAs, 128 chunks each): 260 us with two terms, 285 with three, 357 BWD;
+// 4000 to 4400 cycles a chunk, of which the three products take 1600 and their operands some 1400 between them.
+// Tensor cores are busy 15 to 18 % of the time, memory 16 to 33 %, shared memory about half.  A CTA is one on its
+// SM (204 KB); 28 warps in place of 12 were slower, and so was A from shared memory (by a tenth).
 #include <cudaTypedefs.h>
 
 #include "attn_chunk_host.h"

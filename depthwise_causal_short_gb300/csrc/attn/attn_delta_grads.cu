@@ -15,6 +15,8 @@
 // of V at a time, through a ring for what X and Y need and one for the states.  dv is
 // rounded to bf16 once, as it is stored; the other factors keep two terms (with one, dk's error in the 2-norm
 // was 2.8e-3, of which its store makes 1.7e-3).
+// Bound by memory, and the loads' latency behind it: 197 us for 16384 rows of 16 heads on 8 of 128 x 128, 966 MB
+// (4.9 TB/s, 72 % of a copy's rate), of which two terms of S_0 and of D are 537.  One CTA an SM (225 KB).
 #include <cudaTypedefs.h>
 
 #include "attn_chunk_host.h"

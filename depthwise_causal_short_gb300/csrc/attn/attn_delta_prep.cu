@@ -6,8 +6,9 @@
 // against rows of B M that all threads read from shared memory at the same time: 32 columns at a time, with a
 // product on the tensor cores between the two halves (rows 32 on; X's later columns times B M's corner, both
 // in three terms).
-// Bound by these reads, one step behind the other: the same 16 bytes for all of a warp still take four turns
-// of shared memory.
+// Bound by these reads, one step behind the other (the same 16 bytes for all of a warp still take four turns
+// of shared memory): 88 us for 16384 rows of 16 heads, four CTAs an SM, where the records' 217 MB take 32; 80 us
+// with two terms.  Both rows in one of 64 threads, each read serving two: 113 us in one piece, 106 in two blocks.
 #include <cudaTypedefs.h>
 
 #include "attn_chunk_host.h"

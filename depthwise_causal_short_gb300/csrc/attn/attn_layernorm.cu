@@ -7,7 +7,9 @@
 //   dx = r (dn - n mean(dn n) - mean(dn)),  dw = sum of du n,  db = sum of du     (rms: no mean(dn))
 //
 // Bound by memory: every tensor is read or written once, and the gradient makes the statistics again
-// from x, which it reads anyway.  A group of GROUP threads owns a row, 8 channels (16 bytes) of each
+// from x, which it reads anyway: 16384 rows of 16 heads of 128 with a gate 31 us (6.5 TB/s, 96 % of a copy's rate),
+// its gradient 55 (6.1, 90 %); 8192 rows of 4096 with a bias 23 and 44 (85 and 67 %: three sums across the
+// CTA's warps a row, two CTAs of 128 registers a thread on an SM).  A group of GROUP threads owns a row, 8 channels (16 bytes) of each
 // of PIECES pieces a thread; three rows ahead are on the way to shared memory.  The squares are
 // summed after the mean is known (as sum(x^2) - C m^2 they would cancel for rows far from zero).
 // The sums over rows stay in registers for all rows of a thread, meet in the CTA, and then, a row of
