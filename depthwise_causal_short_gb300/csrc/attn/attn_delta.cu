@@ -21,8 +21,14 @@ static Rows rows(const void* p, int64_t st, int64_t sh) {
 
 // What a backward call keeps in its workspace, from a 256-byte boundary.
 struct DeltaWork {
-  size_t records, z, u, heads, ends, odots, vdots, bdots, sums, anchors, adots, bytes;
+  size_t records, z, u, heads, ends, odots, vdots, bdots, sums, anchors, adots, du, danchors, bytes;
+  bool both;  // the two chains run at once
 };
+// The two chains run at once up to this many CTAs each: half of the 152 SMs; and some more with several sequences,
+// whose CTAs end at different times.  The gradient, us at once / in turn: 8192 rows of 8 heads of 128 (32 CTAs)
+// 524 / 790, of 16 (64) 614 / 869; 7 uneven sequences, 3108 rows of 4 heads (84) 102 / 154; 2 even ones of 12 heads
+// (96) 528 / 503, for 128 CTAs 1146 / 1034.
+constexpr int64_t kBothCtas = 76, kBothCtasRagged = 96;
 static DeltaWork delta_work(int64_t total, int64_t nseq, int64_t Hv, int64_t V) {
   const size_t tiles = static_cast<size_t>(delta_tiles(V)), rows = static_cast<size_t>(total) * Hv;
   const size_t states = total > 0 ? static_cast<size_t>(delta_slots(total, nseq)) * Hv * tiles * kStatePanel : 0;
@@ -45,6 +51,11 @@ static DeltaWork delta_work(int64_t total, int64_t nseq, int64_t Hv, int64_t V) 
   const size_t anchors = total > 0 ? static_cast<size_t>(delta_anchors(total, nseq)) * Hv * tiles : 0;
   w.anchors = take(anchors * kAnchorFloats * 4);
   w.adots = take(anchors * kRowWarps * 4);
+  w.both = total > 0 && nseq * Hv * static_cast<int64_t>(tiles) <= (nseq > 1 ? kBothCtasRagged : kBothCtas);
+  if (w.both) {
+    w.du = take(states / kStatePanel * kDelta * kColumns * 4);
+    w.danchors = take(anchors * kAnchorFloats * 4);
+  }
   w.bytes = at + 256;
   return w;
 }
@@ -176,6 +187,10 @@ extern "C" CCONV_API int cattn_delta_bwd(
   c.sums = reinterpret_cast<double*>(ws + w.sums);
   c.anchors = reinterpret_cast<float*>(ws + w.anchors);
   c.adots = reinterpret_cast<float*>(ws + w.adots);
+  if (w.both) {
+    c.du = reinterpret_cast<float*>(ws + w.du);
+    c.danchors = reinterpret_cast<float*>(ws + w.danchors);
+  }
   c.dq = static_cast<uint16_t*>(dq), c.dk = static_cast<uint16_t*>(dk), c.dv = static_cast<uint16_t*>(dv);
   c.dg = dg, c.dbeta = dbeta, c.dinit = d_initial_state;
   rc = launch_delta_prep(c, stream);

@@ -338,6 +338,7 @@ struct DeltaCall {
   uint16_t *dq, *dk, *dv;
   float *dg, *dbeta, *dinit;
   double* sums;           // [Hv][slots] of the chunks' terms of dg
+  float *du, *danchors;   // where both chains run at once: du as z, D as the anchors; else NULL
   float *anchors, *adots; // [anchors][Hv][tiles] states, [anchors][Hv][tiles * kRowWarps] parts of products
 };
 

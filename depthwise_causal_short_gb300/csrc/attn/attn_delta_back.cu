@@ -12,6 +12,8 @@
 // Bound as that chain is: 377 us of the same 128 CTAs, 5600 cycles a chunk (the rows' part between the first two
 // products 1400 of them, beside the next record's load); tensor cores 20 %, memory 30 %.  K and Q copied to
 // tensor memory as a first operand gained nothing here (400 us).
+// It needs nothing of the chain of the states but for dbeta and the anchors: where SMs are free it runs beside it
+// (EARLY) and makes those two at its end.
 // It leaves dv, two terms of every D, dbeta = du . z, v . dv, and at every kAnchorChunks-th chunk <S_0, D_0>.
 #include <cudaTypedefs.h>
 
@@ -55,6 +57,7 @@ struct BackArgs {
   uint8_t* ends;          // [slots][Hv][tiles] two terms of D
   const float* anchors;   // [anchors][Hv][tiles]
   float* adots;           // [anchors][Hv][tiles * kRowWarps]
+  float *du, *danchors;   // EARLY: du as z is kept, D as the states
   float *vdots, *bdots;   // [2 tiles][Hv][total]
   uint16_t* dv;
   float* dinit;
@@ -62,6 +65,12 @@ struct BackArgs {
   int total, nseq, ratio, Hv, K, V, tiles;
 };
 
+__device__ __forceinline__ float dot4(const float4& a, const float4& b) {
+  return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, a.x * b.x)));
+}
+
+// EARLY: beside the chain of the states, which leaves SMs free.  Only dbeta and <S_0, D_0> need both, and wait.
+template <bool EARLY>
 __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const __grid_constant__ BackArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -95,7 +104,9 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_at;
-  cconv::grid_dependency_wait();
+  // (EARLY: the chain of the states may still run.  Its CTAs let this kernel start after they had waited for the
+  // records, and so for all that was enqueued before)
+  if (!EARLY) cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
   const int tile = static_cast<int>(blockIdx.x % p.tiles);
   const int hv = static_cast<int>(blockIdx.x / p.tiles % p.Hv);
@@ -285,6 +296,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
         const int64_t at = static_cast<int64_t>(row_a) + c * kDelta + t + 8 * r;
         load_words(at < row_b ? v_at + at * p.v.st : nullptr, width, lane, vw[r]);
       }
+      if (EARLY) return;
       const ulonglong2* z = reinterpret_cast<const ulonglong2*>(
           p.z + pairs_at(((slot0 + c) * p.Hv + hv) * p.tiles + tile, warp - 4, lane));
       const ulonglong2 a = z[0], b = z[kPairsNext];
@@ -294,7 +306,8 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
     for (int i = 0; i < chunks; ++i) {
       const int st = i & 1, c = chunks - 1 - i, row0 = row_a + c * kDelta, n = min(kDelta, row_b - row0);
       const float* gates = reinterpret_cast<const float*>(base + st * kBackSlot + kSlotKq + kRecordGates);
-      Pairs v, z = zin;
+      Pairs v, z;
+      if (!EARLY) z = zin;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -303,7 +316,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
       const bool anchor = c > 0 && c % kAnchorChunks == 0;
       const int64_t anchor_at = (anchor_of(row_a, seq, c) * p.Hv + hv) * p.tiles + tile;
       const float* state = p.anchors + anchor_at * kAnchorFloats + row * kColumns + h * 16;
-      if (anchor) asm volatile("prefetch.global.L2 [%0];" ::"l"(state));
+      if (anchor && !EARLY) asm volatile("prefetch.global.L2 [%0];" ::"l"(state));
       if (!(ok = DELTA_WARP_WAIT(rfull + 8 * st, i / 2))) break;
       float ef[2], eb[2], beta[2];
 #pragma unroll
@@ -355,21 +368,29 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
         for (int j = 0; j < 2; ++j) {
           const f2 dv = f2_mul(f2_splat(beta[r]), y.v[j][r]);
           float a, b;
-          cconv::f2_unpack(f2_mul(y.v[j][r], z.v[j][r]), a, b);
-          du_z += a + b;
+          if (!EARLY) {
+            cconv::f2_unpack(f2_mul(y.v[j][r], z.v[j][r]), a, b);
+            du_z += a + b;
+          }
           cconv::f2_unpack(f2_mul(dv, v.v[j][r]), a, b);
           dv_v += a + b;
           words[2 * j + r] = f2_to_bf16x2(dv);
         }
-        du_z += __shfl_xor_sync(0xffffffffu, du_z, 1);
+        if (!EARLY) du_z += __shfl_xor_sync(0xffffffffu, du_z, 1);
         dv_v += __shfl_xor_sync(0xffffffffu, dv_v, 1);
-        du_z += __shfl_xor_sync(0xffffffffu, du_z, 2);
+        if (!EARLY) du_z += __shfl_xor_sync(0xffffffffu, du_z, 2);
         dv_v += __shfl_xor_sync(0xffffffffu, dv_v, 2);
         if (t + 8 * r < n && (lane & 3) == 0) {
           const int64_t at = (static_cast<int64_t>(tile * 2 + h) * p.Hv + hv) * p.total + row0 + t + 8 * r;
-          p.bdots[at] = du_z;
+          if (!EARLY) p.bdots[at] = du_z;
           p.vdots[at] = dv_v;
         }
+      }
+      if (EARLY) {
+        ulonglong2* du = reinterpret_cast<ulonglong2*>(
+            p.du + pairs_at(((slot0 + c) * p.Hv + hv) * p.tiles + tile, warp - 4, lane));
+        du[0] = make_ulonglong2(y.v[0][0], y.v[0][1]);
+        du[kPairsNext] = make_ulonglong2(y.v[1][0], y.v[1][1]);
       }
       const uint4 dv = quad_words(words, lane);
       if (turned < n && inside)
@@ -389,14 +410,15 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
           tc_fence_before();
           __syncwarp();
           if (lane == 0) bar_arrive(dready);
-          if (anchor) {
+          if (EARLY && anchor) {
+            float4* to = reinterpret_cast<float4*>(p.danchors + (state - p.anchors));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) to[j] = make_float4(D[4 * j], D[4 * j + 1], D[4 * j + 2], D[4 * j + 3]);
+          } else if (anchor) {
             const float4* s = reinterpret_cast<const float4*>(state);
             float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float4 x = s[j];
-              sum = fmaf(D[4 * j + 3], x.w, fmaf(D[4 * j + 2], x.z, fmaf(D[4 * j + 1], x.y, fmaf(D[4 * j], x.x, sum))));
-            }
+            for (int j = 0; j < 4; ++j) sum += dot4(make_float4(D[4 * j], D[4 * j + 1], D[4 * j + 2], D[4 * j + 3]), s[j]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             if (lane == 0) p.adots[anchor_at * kRowWarps + warp - 4] = sum;
@@ -421,6 +443,54 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
     tc_fence_after();
     tmem_free(tmem, 512);
   }
+  if (!EARLY) return;
+  // With z and the states of the other chain: dbeta = du . z, and <S_0, D_0>.  (All warps wait at once: one that
+  // did so beside the others' work held the whole CTA up.  And what comes next counts on both chains.)
+  cconv::grid_dependency_wait();
+  // two warps for each row warp's place, in turn
+  constexpr int kTurns = kBackThreads / 32 / kRowWarps, kAhead = 4;
+  const int place = warp % kRowWarps, turn = warp / kRowWarps;
+  const int quarter = place % 4, h = place / 4, row = quarter * 32 + lane, t = quarter * 16 + lane / 4;
+  for (int first = turn; first < chunks; first += kTurns * kAhead) {
+    ulonglong2 z[kAhead][2], du[kAhead][2];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int c = min(first + i * kTurns, chunks - 1);
+      const int64_t from = pairs_at(((slot0 + c) * p.Hv + hv) * p.tiles + tile, place, lane);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        z[i][j] = reinterpret_cast<const ulonglong2*>(p.z + from)[j * kPairsNext];
+        du[i][j] = reinterpret_cast<const ulonglong2*>(p.du + from)[j * kPairsNext];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t at = static_cast<int64_t>(row_a) + (first + i * kTurns) * kDelta + t;
+      const f2 sums[2] = {f2_fma(z[i][0].x, du[i][0].x, f2_mul(z[i][1].x, du[i][1].x)),
+                          f2_fma(z[i][0].y, du[i][0].y, f2_mul(z[i][1].y, du[i][1].y))};
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float a, b;
+        cconv::f2_unpack(sums[r], a, b);
+        float du_z = a + b;
+        du_z += __shfl_xor_sync(0xffffffffu, du_z, 1);
+        du_z += __shfl_xor_sync(0xffffffffu, du_z, 2);
+        if (at + 8 * r < row_b && (lane & 3) == 0)
+          p.bdots[(static_cast<int64_t>(tile * 2 + h) * p.Hv + hv) * p.total + at + 8 * r] = du_z;
+      }
+    }
+  }
+  for (int c = (1 + turn) * kAnchorChunks; c < chunks; c += kTurns * kAnchorChunks) {
+    const int64_t at = (anchor_of(row_a, seq, c) * p.Hv + hv) * p.tiles + tile;
+    const int64_t from = at * kAnchorFloats + row * kColumns + h * 16;
+    const float4 *s = reinterpret_cast<const float4*>(p.anchors + from), *d = reinterpret_cast<const float4*>(p.danchors + from);
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum += dot4(d[j], s[j]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) p.adots[at * kRowWarps + place] = sum;
+  }
 }
 
 int launch_delta_back(const DeltaCall& c, cudaStream_t stream) {
@@ -435,15 +505,17 @@ int launch_delta_back(const DeltaCall& c, cudaStream_t stream) {
   a.z = c.z;
   a.ends = c.ends;
   a.anchors = c.anchors, a.adots = c.adots;
+  a.du = c.du, a.danchors = c.danchors;
   a.vdots = c.vdots, a.bdots = c.bdots;
   a.dv = c.dv, a.dinit = c.dinit;
   a.scale = c.scale;
   a.total = c.s.total, a.nseq = c.s.nseq, a.ratio = c.s.Hv / c.s.Hk, a.Hv = c.s.Hv, a.K = c.s.K, a.V = c.s.V;
   a.tiles = delta_tiles(c.s.V);
   const int64_t ctas = static_cast<int64_t>(c.s.nseq) * c.s.Hv * a.tiles;
-  if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(cattn_delta_back_kernel), kBackBytes) != CCONV_OK)
+  auto kern = c.du ? cattn_delta_back_kernel<true> : cattn_delta_back_kernel<false>;
+  if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(kern), kBackBytes) != CCONV_OK)
     return CCONV_ERR_CUDA;
-  return launch_pdl(cattn_delta_back_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kBackThreads), kBackBytes,
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kBackThreads), kBackBytes,
                     stream, a) == cudaSuccess
              ? CCONV_OK
              : CCONV_ERR_CUDA;
