@@ -413,18 +413,18 @@ static LnKernel kernel_of() {
   return k;
 }
 // The smallest group that holds a row in one piece a thread, to 128 channels, and in two above; in four in a
-// forward without a gate, to 1024 (more tensors or more threads a row, and they cost more than they save).
+// forward without a gate, to 1024 (more tensors or more threads a row, and they cost more than they save), where
+// that makes a CTA for each SM (1000 rows of 256: 2.7 us with four, 2.2 with two).
 // Measured, us, 33.5 million elements; pieces 1 / 2 / 4:
 //   rows of 256     forward 21.9 / 21.8 / 18.9    with a gate 35.0 / 33.6 / 41.7    its gradient 71.3 / 60.7 / 136
 //   512             29.5 / 25.3 / 20.6            - / 35.5 / 43.5                   without a gate 52.9 / 34.3 / 72
 //   1024            30.3 / 26.0 / 24.0            40.9 / 36.3 / 46.9                52.5 / 40.6 / 78
 //   4096            - / 23.4 / 26.0               - / 37.0 / 39.9                   57 / 43.2 / 83
 template <bool BWD>
-static LnKernel pick(int64_t C, bool gate) {
+static LnKernel pick(int64_t C, bool gate, int64_t rows, int sms) {
   if (!BWD && !gate && C > 128 && C <= 1024) {
-    if (C <= 256) return kernel_of<8, 4, BWD>();
-    if (C <= 512) return kernel_of<16, 4, BWD>();
-    return kernel_of<32, 4, BWD>();
+    const LnKernel four = C <= 256 ? kernel_of<8, 4, BWD>() : C <= 512 ? kernel_of<16, 4, BWD>() : kernel_of<32, 4, BWD>();
+    if (rows >= static_cast<int64_t>(sms) * four.rows) return four;
   }
   if (C <= 32) return kernel_of<4, 1, BWD>();
   if (C <= 64) return kernel_of<8, 1, BWD>();
@@ -494,7 +494,7 @@ extern "C" CCONV_API int cattn_layernorm_fwd(const void* x, int64_t sxt, int64_t
   a.y = static_cast<uint16_t*>(y);
   int sms = 0;
   if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
-  const LnKernel kern = pick<false>(C, gate != nullptr);
+  const LnKernel kern = pick<false>(C, gate != nullptr, a.rows, sms);
   const int64_t ctas = ctas_of(a.rows, kern, sms);
   return launch_rows(kern.run[gate != nullptr], kern, ctas, gate ? 2 : 1, a, stream);
 }
@@ -505,7 +505,7 @@ extern "C" CCONV_API int cattn_layernorm_bwd_workspace_bytes(int64_t total, int6
   if (total < 0 || total > kMaxRows || H < 1 || H > 65535 || C < 1 || C > kMaxNorm) return CCONV_ERR_SHAPE;
   int sms = 0;
   if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
-  const LnKernel kern = pick<true>(C, false);
+  const LnKernel kern = pick<true>(C, false, total * H, sms);
   const int64_t ctas = ctas_of(total * H, kern, sms);
   *bytes = static_cast<size_t>(ctas > 0 ? ctas : 1) * 2 * static_cast<size_t>(C) * 4;
   return CCONV_OK;
@@ -533,7 +533,7 @@ extern "C" CCONV_API int cattn_layernorm_bwd(const void* x, int64_t sxt, int64_t
   a.y = static_cast<uint16_t*>(dx), a.dz = static_cast<uint16_t*>(dgate);
   int sms = 0;
   if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
-  const LnKernel kern = pick<true>(C, gate != nullptr);
+  const LnKernel kern = pick<true>(C, gate != nullptr, a.rows, sms);
   const int64_t ctas = ctas_of(a.rows, kern, sms);
   const bool sums = dw || db;
   if (sums) {

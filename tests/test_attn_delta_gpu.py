@@ -55,6 +55,7 @@ CASES = [
     ([63, 64, 65, 0, 1, 200, 31], 2, 4, 128, 128), ([257, 300], 1, 3, 96, 40), ([5, 500], 1, 1, 40, 136),
     ([384], 1, 8, 32, 128), ([130, 2, 126], 3, 3, 72, 256), ([700], 1, 1, 64, 96), ([1] * 40, 2, 2, 64, 32),
     ([1, 255, 256, 1], 1, 2, 120, 200), ([1] * 200, 1, 4, 32, 32), ([90, 2, 300] * 5, 4, 16, 24, 136),
+    ([2200], 1, 2, 64, 64), ([1100, 3], 8, 16, 32, 200),
 ]
 
 

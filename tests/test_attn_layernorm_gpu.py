@@ -68,7 +68,9 @@ CASES = [
     ((13, 520), F32, True, True), ((6, 1024), BF16, True, True), ((11, 1032), F32, True, True),
     ((5, 2048), F32, True, False), ((9, 2056), BF16, True, True), ((700, 4096), F32, True, True),
     ((3, 4104), F32, True, True), ((2, 2, 8192), BF16, True, True), ((2000, 16, 128), F32, True, True),
-    ((20000, 8), F32, True, True),
+    ((20000, 8), F32, True, True), ((6000, 200), F32, True, False), ((5000, 256), None, False, False),
+    ((2600, 504), BF16, True, False), ((1300, 1000), F32, True, False), ((1250, 1024), F32, True, False),
+    ((90, 1000), F32, False, False),
 ]
 
 
