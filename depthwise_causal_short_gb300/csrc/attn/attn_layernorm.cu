@@ -26,7 +26,7 @@ struct LnArgs {
   float* part;       // [CTAs][2][C], or NULL
   int64_t rows;
   int H, C, wdt, layer;
-  float inv, eps;
+  float count, inv, eps;  // C, 1 / C
 };
 
 constexpr int kLnThreads = 256;
@@ -135,7 +135,11 @@ __device__ __forceinline__ float normalise(f2 (&x)[PIECES][4], const bool (&on)[
       for (int j = 0; j < 4; ++j) m = f2_add(m, x[i][j]);
     float mean[1] = {both(m)};
     group_sum<GROUP>(mean, buf, turn);
-    m = f2_splat(-mean[0] * p.inv);
+    // sum / C with one Newton step of the quotient: q = s inv is off by up to 2^-23 of itself (f), q + (s - q C) inv
+    // by 2^-24 f and its rounding.  So a row of equal values, whose sum is exact, is its own mean; one step off,
+    // the mean would be all that such a row's variance holds.  (8192 rows of 4096, gradient: 44.4 us; divided, 47.)
+    const float q = mean[0] * p.inv;
+    m = f2_splat(-fmaf(fmaf(-q, p.count, mean[0]), p.inv, q));
 #pragma unroll
     for (int i = 0; i < PIECES; ++i)
 #pragma unroll
@@ -475,7 +479,7 @@ static LnArgs args_of(const void* x, int64_t sxt, int64_t sxh, const void* z, in
   a.w = w, a.b = b;
   a.rows = total * H;
   a.H = static_cast<int>(H), a.C = static_cast<int>(C), a.wdt = wdt, a.layer = mode == CATTN_NORM_LAYER;
-  a.inv = 1.f / static_cast<float>(C), a.eps = eps;
+  a.count = static_cast<float>(C), a.inv = 1.f / a.count, a.eps = eps;
   return a;
 }
 
