@@ -24,9 +24,9 @@
 // (attn_delta_chain.cu): a CTA takes 32 of them.
 //
 // Precision: products run on bf16 with fp32 accumulators; an fp32 factor is split into three bf16
-// terms (24 bits), and for two such factors the products of terms down to 2^-16 are summed.  A forward that
-// leaves no state takes two terms (16 bits, products down to 2^-8): its one result is bf16, 9 bits (16384 rows of
-// 16 heads: 336 us, 373 with three).
+// terms (24 bits), and for two such factors the products of terms down to 2^-16 are summed.  (Two terms, 16 bits, in
+// a forward that leaves no state saved a tenth of its time, and its o differed from that of the same call
+// with a final state.)
 #pragma once
 
 #include "attn_chunk.cuh"
@@ -34,7 +34,7 @@
 namespace cattn {
 
 constexpr int kDelta = 64;                         // tokens of a chunk
-constexpr int kTerms = 3;                          // bf16 terms of an fp32 factor, at most
+constexpr int kTerms = 3;                          // bf16 terms of an fp32 factor
 constexpr int kSideBytes = kDelta * 128;           // 64 rows of a 64-column panel
 constexpr int kPieceBytes = 128 * 16;              // 8 columns (16 bytes a row) of J's and P~'s rows
 constexpr int kTermBytes = 8 * kPieceBytes;        // one term of them
@@ -102,22 +102,21 @@ __device__ __forceinline__ uint32_t term_piece(int row, int piece) {
   return static_cast<uint32_t>(row * kTermRow + ((piece ^ ((row >> 1) & 3)) << 4));
 }
 
-// Eight fp32 values as N bf16 terms of 16 bytes each.
-template <int N>
-__device__ __forceinline__ void split8(const float* x, uint4 (&out)[N]) {
+// Eight fp32 values as bf16 terms of 16 bytes each.
+__device__ __forceinline__ void split8(const float* x, uint4 (&out)[kTerms]) {
   const f2 minus = f2_splat(-1.f);
-  uint32_t t[N][4];
+  uint32_t t[kTerms][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     f2 v = f2_pack(x[2 * i], x[2 * i + 1]);
 #pragma unroll
-    for (int s = 0; s < N; ++s) {
+    for (int s = 0; s < kTerms; ++s) {
       t[s][i] = f2_to_bf16x2(v);
-      if (s + 1 < N) v = f2_fma(bf16x2_to_f2(t[s][i]), minus, v);
+      if (s + 1 < kTerms) v = f2_fma(bf16x2_to_f2(t[s][i]), minus, v);
     }
   }
 #pragma unroll
-  for (int s = 0; s < N; ++s) out[s] = make_uint4(t[s][0], t[s][1], t[s][2], t[s][3]);
+  for (int s = 0; s < kTerms; ++s) out[s] = make_uint4(t[s][0], t[s][1], t[s][2], t[s][3]);
 }
 
 // Contiguous bytes (a multiple of 16, both ends 16-byte aligned) from and to shared memory.
@@ -180,7 +179,6 @@ __device__ __forceinline__ Pairs load_sum(uint32_t at, int step = kColumns) {
   return s;
 }
 // Pairs of token row `row` (+ 8), columns of half h, to the terms at `base`.
-template <int N = kTerms>
 __device__ __forceinline__ void put_pairs(uint32_t base, int row, int h, int lane, const Pairs& p) {
 #pragma unroll
   for (int j = 0; j < 2; ++j)
@@ -189,10 +187,10 @@ __device__ __forceinline__ void put_pairs(uint32_t base, int row, int h, int lan
       const uint32_t at = base + term_piece(row + 8 * r, 2 * h + j) + (lane & 3) * 4;
       f2 v = p.v[j][r];
 #pragma unroll
-      for (int s = 0; s < N; ++s) {
+      for (int s = 0; s < kTerms; ++s) {
         const uint32_t w = f2_to_bf16x2(v);
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + s * kTokenPanel), "r"(w) : "memory");
-        if (s + 1 < N) v = f2_fma(bf16x2_to_f2(w), f2_splat(-1.f), v);
+        if (s + 1 < kTerms) v = f2_fma(bf16x2_to_f2(w), f2_splat(-1.f), v);
       }
     }
 }
@@ -230,30 +228,28 @@ __device__ __forceinline__ int64_t pairs_at(int64_t tile, int row_warp, int lane
   return (tile * kRowWarps + row_warp) * 256 + lane * 4;
 }
 
-// 16 columns of this thread's row in N groups of kColumns columns: the sum.
-template <int N = kTerms>
+// 16 columns of this thread's row in the terms' groups of kColumns columns: the sum.
 __device__ __forceinline__ void load_sum16(uint32_t at, float* x) {
-  uint32_t a[N][16];
+  uint32_t a[kTerms][16];
 #pragma unroll
-  for (int s = 0; s < N; ++s) tmem_ld16(at + s * kColumns, a[s]);
+  for (int s = 0; s < kTerms; ++s) tmem_ld16(at + s * kColumns, a[s]);
   tmem_wait_ld();
 #pragma unroll
-  for (int s = 0; s < N; ++s) tmem_use16(a[s]);
+  for (int s = 0; s < kTerms; ++s) tmem_use16(a[s]);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    x[i] = __uint_as_float(a[N - 1][i]);
+    x[i] = __uint_as_float(a[kTerms - 1][i]);
 #pragma unroll
-    for (int s = N - 2; s >= 0; --s) x[i] += __uint_as_float(a[s][i]);
+    for (int s = kTerms - 2; s >= 0; --s) x[i] += __uint_as_float(a[s][i]);
   }
 }
 // Eight values of row `row` to the terms at `base`.
-template <int N = kTerms>
 __device__ __forceinline__ void put_terms8(uint32_t base, uint32_t panel, int row, int piece, const float* x) {
-  uint4 t[N];
-  split8<N>(x, t);
+  uint4 t[kTerms];
+  split8(x, t);
   const uint32_t at = base + term_piece(row, piece);
 #pragma unroll
-  for (int s = 0; s < N; ++s) sts128(at + s * panel, t[s].x, t[s].y, t[s].z, t[s].w);
+  for (int s = 0; s < kTerms; ++s) sts128(at + s * panel, t[s].x, t[s].y, t[s].z, t[s].w);
 }
 __device__ __forceinline__ void unpack8(const uint4& x, float* y) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -341,9 +337,6 @@ struct DeltaCall {
   float *du, *danchors;   // where both chains run at once: du as z, D as the anchors; else NULL
   float *anchors, *adots; // [anchors][Hv][tiles] states, [anchors][Hv][tiles * kRowWarps] parts of products
 };
-
-// The result is bf16 only (see above).
-inline bool two_terms(const DeltaCall& c) { return !c.z && !c.fin; }
 
 int launch_delta_prep(const DeltaCall& c, cudaStream_t stream);
 int launch_delta_fwd(const DeltaCall& c, cudaStream_t stream);

@@ -8,13 +8,13 @@
 //   [J; P~] X      -> z = r + J X,  u = beta z;          o = scale (ef . (Q S) + P~ X)
 //   K^T (eb . u)   -> S = total S + ..
 // The three terms of S, X and eb . u lie side by side as columns of one operand (N = 96), so that A is
-// read once for all three; their products are added up in registers.  (Two terms without a state to leave.)
+// read once for all three; their products are added up in registers.
 // The gradient runs the same chain first (BWD): it leaves z, two terms of u and of every S_0 (and
 // every kAnchorChunks-th in fp32), and o . do in place of o.  Its own chain, from the last chunk to the first,
 // is attn_delta_back.cu.
 //
 // Bound by that chain: a product, its results to registers, the next operand to shared memory.  2 sequences of
-// 8192 rows, 16 heads of 128 x 128 (128 CTAs, 128 chunks each): 260 us with two terms, 285 with three, 357 BWD;
+// 8192 rows, 16 heads of 128 x 128 (128 CTAs, 128 chunks each): 285 us, 357 BWD;
 // 4000 to 4400 cycles a chunk, of which the three products take 1600 and their operands some 1400 between them.
 // Tensor cores are busy 15 to 18 % of the time, memory 16 to 33 %, shared memory about half.  A CTA is one on its
 // SM (204 KB); 28 warps in place of 12 were slower, and so was A from shared memory (by a tenth).
@@ -100,7 +100,7 @@ __device__ __forceinline__ ChainPlace chain_place(const ChainArgs& p, int lane) 
   return w;
 }
 
-template <bool BWD, int TERMS>
+template <bool BWD>
 __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(const __grid_constant__ ChainArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -156,9 +156,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
         load_kq(slot, kfull + 8 * st, &p.mk, &p.mq, panels, hk, w.a + c * kDelta);
         part = 1;
         if (c > 0 && !(ok = DELTA_WAIT(acc2, c - 1))) break;
-        constexpr int bytes = TERMS == kTerms ? kRecordBytes : kRecordThird;
-        bar_expect(rfull + 8 * st, bytes);
-        bulk_load(slot + kSlotKq, p.records + ((slot0 + c) * p.Hv + w.hv) * kRecordBytes, bytes, rfull + 8 * st);
+        bar_expect(rfull + 8 * st, kRecordBytes);
+        bulk_load(slot + kSlotKq, p.records + ((slot0 + c) * p.Hv + w.hv) * kRecordBytes, kRecordBytes, rfull + 8 * st);
         part = 0;
       }
       for (int st = 0; st < 2; ++st) {
@@ -171,9 +170,9 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
     if (elect_one()) {
       const int ksteps = (p.K + 15) / 16;
       const uint64_t ds = term_desc(smem + kOffState, kStatePanel), dx = term_desc(smem + kOffX, kTokenPanel);
-      const uint32_t all = mma_desc(TERMS * kColumns, false, true), less = mma_desc((TERMS - 1) * kColumns, false, true);
+      const uint32_t all = mma_desc(kTerms * kColumns, false, true), less = mma_desc((kTerms - 1) * kColumns, false, true);
       const uint32_t one = mma_desc(kColumns, false, true);
-      const uint32_t last = mma_desc(TERMS * kColumns, true, true);
+      const uint32_t last = mma_desc(kTerms * kColumns, true, true);
       auto copy_kq = [&](int c) {
         const int st = c & 1;
         if (!(ok = DELTA_WAIT(kfull + 8 * st, c / 2))) return;
@@ -197,8 +196,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
         for (int j = 0; j < kDelta / 16; ++j) {
           tmem_copy(tmem + kTmJp + 8 * j, djp + j * kRecordCols);
           tmem_copy(tmem + kTmJp + 32 + 8 * j, djp + j * kRecordCols + kRecordTerm);
-          if (TERMS == kTerms)
-            tmem_copy(tmem + kTmJp + 64 + 8 * j, djp + kRecordThird / 16 + j * kRecordTerm);
+          tmem_copy(tmem + kTmJp + 64 + 8 * j, djp + kRecordThird / 16 + j * kRecordTerm);
         }
         if (!(ok = DELTA_WAIT(xready, c))) break;
         tc_fence_after();
@@ -206,8 +204,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
         for (int j = 0; j < kDelta / 16; ++j) {  // [J; P~] X
           mma_ts(tmem + kTmSecond, tmem + kTmJp + 8 * j, dx + j * kTermStep, all, j > 0);
           mma_ts(tmem + kTmSecond, tmem + kTmJp + 32 + 8 * j, dx + j * kTermStep, less, true);
-          if (TERMS == kTerms)
-            mma_ts(tmem + kTmSecond, tmem + kTmJp + 64 + 8 * j, dx + j * kTermStep, one, true);
+          mma_ts(tmem + kTmSecond, tmem + kTmJp + 64 + 8 * j, dx + j * kTermStep, one, true);
         }
         mma_commit(acc2);
         if (c + 1 < chunks) copy_kq(c + 1);
@@ -257,8 +254,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
         S[4 * i] = x.x, S[4 * i + 1] = x.y, S[4 * i + 2] = x.z, S[4 * i + 3] = x.w;
       }
     }
-    put_terms8<TERMS>(smem + kOffState, kStatePanel, row, 2 * h, S);
-    put_terms8<TERMS>(smem + kOffState, kStatePanel, row, 2 * h + 1, S + 8);
+    put_terms8(smem + kOffState, kStatePanel, row, 2 * h, S);
+    put_terms8(smem + kOffState, kStatePanel, row, 2 * h + 1, S + 8);
     cconv::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) bar_arrive(sready);
@@ -294,7 +291,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
       const float total = gates[kTotal];
       if (!(ok = DELTA_WARP_WAIT(acc1, c))) break;
       tc_fence_after();
-      Pairs y = load_sum<TERMS>(mine + kTmFirst), x;
+      Pairs y = load_sum<kTerms>(mine + kTmFirst), x;
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -303,7 +300,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
           if (t + 8 * r >= n) v.v[j][r] = 0;
           x.v[j][r] = f2_mul(f2_splat(beta[r]), v.v[j][r]);
         }
-      put_pairs<TERMS>(smem + kOffX, t, h, lane, x);
+      put_pairs(smem + kOffX, t, h, lane, x);
       if (n < kDelta) zero_tokens(smem + st * kSlotBytes, panels, n, false, threadIdx.x - 128);
       cconv::fence_proxy_async_smem();
       tc_fence_before();
@@ -311,7 +308,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
       if (lane == 0) bar_arrive(xready);
       if (!(ok = DELTA_WARP_WAIT(acc2, c))) break;
       tc_fence_after();
-      y = load_sum<TERMS>(mine + kTmSecond);
+      y = load_sum<kTerms>(mine + kTmSecond);
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -320,14 +317,14 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
           x.v[j][r] = f2_mul(f2_splat(eb[r] * beta[r]), v.v[j][r]);
           if (t + 8 * r >= n) x.v[j][r] = 0;
         }
-      put_pairs<TERMS>(smem + kOffX, t, h, lane, x);
+      put_pairs(smem + kOffX, t, h, lane, x);
       cconv::fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(uready);
       // what waits for nothing more: o, or o . do, z and u
-      y = load_sum<TERMS>(other + kTmSecond);
-      x = load_sum<TERMS>(other + kTmFirst);
+      y = load_sum<kTerms>(other + kTmSecond);
+      x = load_sum<kTerms>(other + kTmFirst);
       const int64_t at = ((slot0 + c) * p.Hv + w.hv) * p.tiles + w.tile;
       uint32_t words[4], second[4];
       float sum[2] = {0.f, 0.f};
@@ -377,13 +374,13 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
         float z[16];
         if (!(ok = DELTA_WARP_WAIT(acc3, c))) break;
         tc_fence_after();
-        load_sum16<TERMS>(mine + kTmThird, z);
+        load_sum16(mine + kTmThird, z);
 #pragma unroll
         for (int i = 0; i < 16; ++i) S[i] = row < p.K ? fmaf(total, S[i], z[i]) : 0.f;
         if (c + 1 < chunks) {
           if (BWD && !(ok = DELTA_WARP_WAIT(kept, c))) break;
-          put_terms8<TERMS>(smem + kOffState, kStatePanel, row, 2 * h, S);
-          put_terms8<TERMS>(smem + kOffState, kStatePanel, row, 2 * h + 1, S + 8);
+          put_terms8(smem + kOffState, kStatePanel, row, 2 * h, S);
+          put_terms8(smem + kOffState, kStatePanel, row, 2 * h + 1, S + 8);
           cconv::fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
@@ -409,7 +406,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) cattn_delta_chain_kernel(con
   }
 }
 
-template <bool BWD, int TERMS>
+template <bool BWD>
 static int launch_chain(const DeltaCall& c, cudaStream_t stream) {
   ChainArgs a{};
   int rc = CCONV_OK;
@@ -428,7 +425,7 @@ static int launch_chain(const DeltaCall& c, cudaStream_t stream) {
   a.scale = c.scale;
   a.total = c.s.total, a.nseq = c.s.nseq, a.ratio = c.s.Hv / c.s.Hk, a.Hv = c.s.Hv, a.K = c.s.K, a.V = c.s.V;
   a.tiles = delta_tiles(c.s.V);
-  auto kern = cattn_delta_chain_kernel<BWD, TERMS>;
+  auto kern = cattn_delta_chain_kernel<BWD>;
   const int64_t ctas = static_cast<int64_t>(c.s.nseq) * c.s.Hv * a.tiles;
   if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(kern), kChainBytes) != CCONV_OK)
     return CCONV_ERR_CUDA;
@@ -438,9 +435,7 @@ static int launch_chain(const DeltaCall& c, cudaStream_t stream) {
              : CCONV_ERR_CUDA;
 }
 
-int launch_delta_fwd(const DeltaCall& c, cudaStream_t stream) {
-  return two_terms(c) ? launch_chain<false, 2>(c, stream) : launch_chain<false, kTerms>(c, stream);
-}
-int launch_delta_states(const DeltaCall& c, cudaStream_t stream) { return launch_chain<true, kTerms>(c, stream); }
+int launch_delta_fwd(const DeltaCall& c, cudaStream_t stream) { return launch_chain<false>(c, stream); }
+int launch_delta_states(const DeltaCall& c, cudaStream_t stream) { return launch_chain<true>(c, stream); }
 
 }  // namespace cattn

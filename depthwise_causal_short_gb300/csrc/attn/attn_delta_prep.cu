@@ -7,8 +7,8 @@
 // product on the tensor cores between the two halves (rows 32 on; X's later columns times B M's corner, both
 // in three terms).
 // Bound by these reads, one step behind the other (the same 16 bytes for all of a warp still take four turns
-// of shared memory): 88 us for 16384 rows of 16 heads, four CTAs an SM, where the records' 217 MB take 32; 80 us
-// with two terms.  Both rows in one of 64 threads, each read serving two: 113 us in one piece, 106 in two blocks.
+// of shared memory): 88 us for 16384 rows of 16 heads, four CTAs an SM, where the records' 217 MB take 32.
+// Both rows in one of 64 threads, each read serving two: 113 us in one piece, 106 in two blocks.
 #include <cudaTypedefs.h>
 
 #include "attn_chunk_host.h"
@@ -73,20 +73,18 @@ __device__ __forceinline__ void unpack_pairs(const f2* x, float* y) {
 }
 
 // A row's terms to the record (neighbouring threads have neighbouring rows).
-template <int TERMS>
 __device__ __forceinline__ void store_row(const f2 (&x)[kDelta / 2], uint8_t* record, int row) {
 #pragma unroll
   for (int i = 0; i < kDelta / 8; ++i) {
-    uint4 t[TERMS];
+    uint4 t[kTerms];
     float v[8];
     unpack_pairs(x + 4 * i, v);
-    split8<TERMS>(v, t);
+    split8(v, t);
 #pragma unroll
-    for (int s = 0; s < TERMS; ++s) *reinterpret_cast<uint4*>(record + record_piece(s, i, row)) = t[s];
+    for (int s = 0; s < kTerms; ++s) *reinterpret_cast<uint4*>(record + record_piece(s, i, row)) = t[s];
   }
 }
 
-template <int TERMS>
 __global__ void __launch_bounds__(kPrepThreads, 4) cattn_delta_prep_kernel(const __grid_constant__ PrepArgs p) {
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -241,7 +239,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) cattn_delta_prep_kernel(const
       for (int i = 0; i < kBlock / 2; ++i) x[i] = f2_fma(pair(y, i), f2_splat(-1.f), x[i]);
     }
     solve<0>(x, smem);
-    store_row<TERMS>(x, record, lane_of(t) + (own_p ? kOther : 0));
+    store_row(x, record, lane_of(t) + (own_p ? kOther : 0));
     if (!ok) atomicOr(&g_fault_prep, kFaultWait);
   }
   tc_fence_before();
@@ -263,10 +261,9 @@ int launch_delta_prep(const DeltaCall& c, cudaStream_t stream) {
   a.records = c.records;
   a.total = c.s.total, a.nseq = c.s.nseq, a.ratio = c.s.Hv / c.s.Hk, a.Hv = c.s.Hv, a.K = c.s.K;
   const int64_t ctas = delta_slots(c.s.total, c.s.nseq) * c.s.Hv;
-  auto kern = two_terms(c) ? cattn_delta_prep_kernel<2> : cattn_delta_prep_kernel<kTerms>;
-  if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(kern), kPrepBytes) != CCONV_OK)
+  if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(cattn_delta_prep_kernel), kPrepBytes) != CCONV_OK)
     return CCONV_ERR_CUDA;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kPrepThreads), kPrepBytes,
+  return launch_pdl(cattn_delta_prep_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kPrepThreads), kPrepBytes,
                     stream, a) == cudaSuccess
              ? CCONV_OK
              : CCONV_ERR_CUDA;

@@ -40,8 +40,7 @@
  *     and inside the linear attention's matrix products the decayed scores (in calls of at most
  *     64 rows they keep 16 bits) and, in the forward, the states as the queries read them: errors
  *     of 2.3e-3 in the 2-norm, of which the store alone makes 1.7e-3.  In the delta rule only the
- *     results are rounded to bf16, and dv where dk is made of it; a forward without a final state
- *     keeps its factors in 16 bits (its o may differ from that of a call with one in the last bit).
+ *     results are rounded to bf16, and dv where dk is made of it.
  *     States, their gradients, dg and dbeta are as exact as sums in fp32.
  *   - Results are bit-identical from run to run for the same inputs and device.
  */
