@@ -21,7 +21,7 @@ static Rows rows(const void* p, int64_t st, int64_t sh) {
 
 // What a backward call keeps in its workspace, from a 256-byte boundary.
 struct DeltaWork {
-  size_t records, z, u, heads, ends, odots, vdots, bdots, sums, anchors, adots, du, danchors, bytes;
+  size_t records, z, u, heads, ends, rest, odots, vdots, bdots, sums, anchors, adots, du, danchors, bytes;
   bool both;  // the two chains run at once
 };
 // The two chains run at once up to this many CTAs each: half of the 152 SMs; and some more with several sequences,
@@ -44,6 +44,7 @@ static DeltaWork delta_work(int64_t total, int64_t nseq, int64_t Hv, int64_t V) 
   w.u = take(states / kStatePanel * kUTile);
   w.heads = take(2 * states);
   w.ends = take(2 * states);
+  w.rest = take(states / kStatePanel * kTokenPanel);
   w.odots = take(2 * tiles * rows * 4);
   w.vdots = take(2 * tiles * rows * 4);
   w.bdots = take(2 * tiles * rows * 4);
@@ -180,7 +181,7 @@ extern "C" CCONV_API int cattn_delta_bwd(
   c.records = ws + w.records;
   c.z = reinterpret_cast<float*>(ws + w.z);
   c.u = ws + w.u;
-  c.heads = ws + w.heads, c.ends = ws + w.ends;
+  c.heads = ws + w.heads, c.ends = ws + w.ends, c.rest = ws + w.rest;
   c.odots = reinterpret_cast<float*>(ws + w.odots);
   c.vdots = reinterpret_cast<float*>(ws + w.vdots);
   c.bdots = reinterpret_cast<float*>(ws + w.bdots);

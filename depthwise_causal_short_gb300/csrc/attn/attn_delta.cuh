@@ -330,6 +330,7 @@ struct DeltaCall {
   float* z;               // [slots][Hv][tiles] of 64 rows of kColumns, as pairs_at has them
   uint8_t* u;             // [slots][Hv][tiles] two terms of u
   uint8_t *heads, *ends;  // [slots][Hv][tiles] two terms of S_0 and of D
+  uint8_t* rest;          // [slots][Hv][tiles] the second term of dv (the first is dv itself)
   float *odots, *vdots, *bdots;  // [2 tiles][Hv][total] parts of o . do, v . dv and dbeta
   uint16_t *dq, *dk, *dv;
   float *dg, *dbeta, *dinit;

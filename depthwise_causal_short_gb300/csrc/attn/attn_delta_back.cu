@@ -14,7 +14,7 @@
 // tensor memory as a first operand gained nothing here (400 us).
 // It needs nothing of the chain of the states but for dbeta and the anchors: where SMs are free it runs beside it
 // (EARLY) and makes those two at its end.
-// It leaves dv, two terms of every D, dbeta = du . z, v . dv, and at every kAnchorChunks-th chunk <S_0, D_0>.
+// It leaves dv, a second term of it, two terms of every D, dbeta = du . z, v . dv, and at every kAnchorChunks-th chunk <S_0, D_0>.
 #include <cudaTypedefs.h>
 
 #include "attn_chunk_host.h"
@@ -55,6 +55,7 @@ struct BackArgs {
   const uint8_t* records;
   const float* z;
   uint8_t* ends;          // [slots][Hv][tiles] two terms of D
+  uint8_t* rest;          // [slots][Hv][tiles] what dv's rounding leaves, 64 rows of kColumns as the terms lie
   const float* anchors;   // [anchors][Hv][tiles]
   float* adots;           // [anchors][Hv][tiles * kRowWarps]
   float *du, *danchors;   // EARLY: du as z is kept, D as the states
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
       tc_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(uready);
-      uint32_t words[4];
+      uint32_t words[4], second[4];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         float du_z = 0.f, dv_v = 0.f;
@@ -375,6 +376,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
           cconv::f2_unpack(f2_mul(dv, v.v[j][r]), a, b);
           dv_v += a + b;
           words[2 * j + r] = f2_to_bf16x2(dv);
+          second[2 * j + r] = f2_to_bf16x2(f2_fma(bf16x2_to_f2(words[2 * j + r]), f2_splat(-1.f), dv));
         }
         if (!EARLY) du_z += __shfl_xor_sync(0xffffffffu, du_z, 1);
         dv_v += __shfl_xor_sync(0xffffffffu, dv_v, 1);
@@ -392,6 +394,8 @@ __global__ void __launch_bounds__(kBackThreads, 1) cattn_delta_back_kernel(const
         du[0] = make_ulonglong2(y.v[0][0], y.v[0][1]);
         du[kPairsNext] = make_ulonglong2(y.v[1][0], y.v[1][1]);
       }
+      *reinterpret_cast<uint4*>(p.rest + (((slot0 + c) * p.Hv + hv) * p.tiles + tile) * kTokenPanel +
+                                term_piece(turned, 2 * h + turned_col / 8)) = quad_words(second, lane);
       const uint4 dv = quad_words(words, lane);
       if (turned < n && inside)
         *reinterpret_cast<uint4*>(p.dv + (static_cast<int64_t>(row0 + turned) * p.Hv + hv) * p.V + col + turned_col) = dv;
@@ -503,7 +507,7 @@ int launch_delta_back(const DeltaCall& c, cudaStream_t stream) {
   a.cu = c.cu;
   a.records = c.records;
   a.z = c.z;
-  a.ends = c.ends;
+  a.ends = c.ends, a.rest = c.rest;
   a.anchors = c.anchors, a.adots = c.adots;
   a.du = c.du, a.danchors = c.danchors;
   a.vdots = c.vdots, a.bdots = c.bdots;

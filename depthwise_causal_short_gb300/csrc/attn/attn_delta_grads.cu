@@ -7,14 +7,14 @@
 //   dk = X^T Q - (Y + Y^T) K + eb . (u D^T) - ef . (dv S_0^T)
 // summed over the value heads of a key head in the CTA's registers.  do and dv lie one over the other
 // as a first operand of 128 rows, and so do dq and dk as results:
-//   [do; dv] u^T                             -> X, -Y
-//   [do; dv] S_0^T     rows scaled by scale ef and -ef afterwards
-//   [  ; u ] D^T       rows 64.. scaled by eb afterwards
+//   [do; dv] u^T,  [0; dv'] u^T              -> X, -Y
+//   [do; dv] S_0^T,  [0; dv'] S_0^T          rows scaled by scale ef and -ef afterwards
+//   [  ; u ] D^T                             rows 64.. scaled by eb afterwards
 //   [X; -Y] K,  [0; -Y^T] K,  [0; X^T] Q
 // A CTA goes through (chunk, key head) items; do, dv, u and the tiles of S_0 and D come by TMA, 32 columns
-// of V at a time, through a ring for what X and Y need and one for the states.  dv is
-// rounded to bf16 once, as it is stored; the other factors keep two terms (with one, dk's error in the 2-norm
-// was 2.8e-3, of which its store makes 1.7e-3).
+// of V at a time, through a ring for what X and Y need and one for the states.  Every factor that is no input keeps
+// two terms, dv as it is stored and what that leaves (dv'): 16 bits, for results of 9.  With all of them in one term
+// dk's error in the 2-norm was 2.8e-3, with dv alone 1.8e-3 to 2.1e-3; the store makes 1.7e-3.
 // Bound by memory, and the loads' latency behind it: 197 us for 16384 rows of 16 heads on 8 of 128 x 128, 966 MB
 // (4.9 TB/s, 72 % of a copy's rate), of which two terms of S_0 and of D are 537.  One CTA an SM (225 KB).
 #include <cudaTypedefs.h>
@@ -37,10 +37,11 @@ static FaultReader reader(read_fault);
 
 // shared memory, from a 1024-byte boundary
 constexpr int kHalf = kDelta * 128;                       // 64 rows of 64 columns
-constexpr int kUPart = 3 * kTokenPanel;                   // second, first and again second terms of u
-constexpr int kPairSlot = 2 * kTokenPanel + kUPart;       // do over dv; u
+// do over dv; two terms of u; zeros over dv'
+constexpr int kPairDv = kTokenPanel, kPairU = 2 * kTokenPanel, kPairRest = kPairU + kUTile;
+constexpr int kPairLoads = kPairRest + kTokenPanel, kPairSlot = kPairRest + 2 * kTokenPanel;
 constexpr int kStateSlot = 4 * kStatePanel;               // two terms of S_0 and of D
-constexpr int kPairSlots = 4, kStateSlots = 2;
+constexpr int kPairSlots = 3, kStateSlots = 2;
 constexpr int kOffStates = kPairSlots * kPairSlot;
 constexpr int kOffGradKq = kOffStates + kStateSlots * kStateSlot;
 constexpr int kOffZero = kOffGradKq + kSlotKq;           // zeros; X, -Y; their second terms: 64 rows each
@@ -59,7 +60,7 @@ struct GradArgs {
   CUtensorMap mq, mk, mo, mv;  // q, k; do, dv in boxes of 32 columns
   Gates g;
   const int32_t* cu;
-  const uint8_t *u, *heads, *ends;
+  const uint8_t *u, *heads, *ends, *rest;
   const float *odots, *vdots, *bdots;
   uint16_t *dq, *dk;
   float *dg, *dbeta;
@@ -105,6 +106,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
     cconv::fence_mbar_init();
   }
   for (int i = threadIdx.x; i < kHalf / 16; i += kGradThreads) sts128(smem + kOffZero + i * 16, 0, 0, 0, 0);
+  for (int i = threadIdx.x; i < kPairSlots * kTokenPanel / 16; i += kGradThreads)
+    sts128(smem + i / (kTokenPanel / 16) * kPairSlot + kPairRest + i % (kTokenPanel / 16) * 16, 0, 0, 0, 0);
   cconv::fence_proxy_async_smem();
   if (warp == 1) tmem_alloc(&tmem_at, 512);
   tc_fence_before();
@@ -152,13 +155,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
           for (int s = 0; s < p.tiles && ok; ++s, ++pairs) {
             const int st = pairs % kPairSlots;
             if (pairs >= kPairSlots && !(ok = DELTA_WAIT(pempty + 8 * st, pairs / kPairSlots - 1))) break;
-            const uint32_t dst = smem + st * kPairSlot, u = dst + 2 * kTokenPanel, bar = pfull + 8 * st;
-            bar_expect(bar, kPairSlot);
+            const uint32_t dst = smem + st * kPairSlot, bar = pfull + 8 * st;
+            bar_expect(bar, kPairLoads);
             load_box(dst, &p.mo, bar, s * kColumns, hv, x.row0);
-            load_box(dst + kTokenPanel, &p.mv, bar, s * kColumns, hv, x.row0);
-            const uint8_t* from = p.u + (first + s) * kUTile;
-            bulk_load(u + kTokenPanel, from, kUTile, bar);
-            bulk_load(u, from + kTokenPanel, kTokenPanel, bar);
+            load_box(dst + kPairDv, &p.mv, bar, s * kColumns, hv, x.row0);
+            bulk_load(dst + kPairU, p.u + (first + s) * kUTile, kUTile, bar);
+            bulk_load(dst + kPairRest + kTokenPanel, p.rest + (first + s) * kTokenPanel, kTokenPanel, bar);
             if (s + 1 == p.tiles)
               load_states(p.tiles);
             else if (s + 1 >= kPairSlots)
@@ -200,19 +202,20 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
               const int at_pair = (pairs + done) % kPairSlots, at_state = states % kStateSlots;
               if (!(ok = DELTA_WAIT(sfull + 8 * at_state, states / kStateSlots))) return;
               tc_fence_after();
-              const uint32_t pair = smem + at_pair * kPairSlot, u = pair + 2 * kTokenPanel;
+              const uint32_t pair = smem + at_pair * kPairSlot;
               const uint32_t state = smem + kOffStates + at_state * kStateSlot;
               const int ks = (min(kColumns, p.V - kColumns * done) + 15) / 16;
 #pragma unroll 1
               for (int j = 0; j < ks; ++j) {
-                const uint64_t second = term_desc(u, 0) + 2 * j, first = second + kTokenPanel / 16;  // at row 64: the other
-                const uint64_t rows = term_desc(pair, 0) + 2 * j, start = term_desc(state, 0) + 2 * j;
-                const uint64_t end = term_desc(state + 2 * kStatePanel, 0) + 2 * j;
+                const uint64_t rows = term_desc(pair, 0) + 2 * j, rest = rows + kPairRest / 16;
+                const uint64_t start = term_desc(state, 0) + 2 * j, end = start + 2 * kStatePanel / 16;
                 mma_ss(tmem + kAccState, rows, start, d_state, done + j > 0);
                 mma_ss(tmem + kAccState, rows, start + kStatePanel / 16, d_state, true);
-                mma_ss(tmem + kAccEnd, second, end, d_state, done + j > 0);          // rows 64 on: u's first terms
-                mma_ss(tmem + kAccEnd, second, end + kStatePanel / 16, d_state, true);
-                mma_ss(tmem + kAccEnd, first, end, d_state, true);                    // u's second terms
+                mma_ss(tmem + kAccState, rest, start, d_state, true);
+                const uint64_t first = rows + kPairDv / 16, second = rows + kPairU / 16;  // rows 64 on: terms of u
+                mma_ss(tmem + kAccEnd, first, end, d_state, done + j > 0);
+                mma_ss(tmem + kAccEnd, first, end + kStatePanel / 16, d_state, true);
+                mma_ss(tmem + kAccEnd, second, end, d_state, true);
               }
               mma_commit(pempty + 8 * at_pair);
               mma_commit(sempty + 8 * at_state);
@@ -220,15 +223,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
           };
           for (int s = 0; s < p.tiles && ok; ++s) {
             const int st = (pairs + s) % kPairSlots;
-            const uint32_t pair = smem + st * kPairSlot, u = pair + 2 * kTokenPanel;
+            const uint32_t pair = smem + st * kPairSlot;
             const int ks = (min(kColumns, p.V - kColumns * s) + 15) / 16;
             if (!(ok = DELTA_WAIT(pfull + 8 * st, (pairs + s) / kPairSlots))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int j = 0; j < ks; ++j) {
-              const uint64_t a = term_desc(pair, 0) + 2 * j, second = term_desc(u, 0) + 2 * j;
-              mma_ss(xy_acc, a, second + kTokenPanel / 16, d_xy, s + j > 0);
-              mma_ss(xy_acc, a, second, d_xy, true);
+              const uint64_t a = term_desc(pair, 0) + 2 * j, u = a + kPairU / 16;
+              mma_ss(xy_acc, a, u, d_xy, s + j > 0);
+              mma_ss(xy_acc, a, u + kTokenPanel / 16, d_xy, true);
+              mma_ss(xy_acc, a + kPairRest / 16, u, d_xy, true);
             }
             if (s + 1 == p.tiles) {
               mma_commit(xyfull);
@@ -557,7 +561,7 @@ int launch_delta_grads(const DeltaCall& c, cudaStream_t stream) {
   if (rc != CCONV_OK) return rc;
   a.g = c.g;
   a.cu = c.cu;
-  a.u = c.u, a.heads = c.heads, a.ends = c.ends;
+  a.u = c.u, a.heads = c.heads, a.ends = c.ends, a.rest = c.rest;
   a.odots = c.odots, a.vdots = c.vdots, a.bdots = c.bdots;
   a.dq = c.dq, a.dk = c.dk, a.dg = c.dg, a.dbeta = c.dbeta;
   a.sums = c.sums;

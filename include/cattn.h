@@ -40,7 +40,8 @@
  *     and inside the linear attention's matrix products the decayed scores (in calls of at most
  *     64 rows they keep 16 bits) and, in the forward, the states as the queries read them: errors
  *     of 2.3e-3 in the 2-norm, of which the store alone makes 1.7e-3.  In the delta rule only the
- *     results are rounded to bf16, and dv where dk is made of it.
+ *     results are rounded to bf16; in the products that make dq and dk, factors that are no inputs
+ *     (decayed pairs, states and their gradients, u, dv) keep 16 bits.
  *     States, their gradients, dg and dbeta are as exact as sums in fp32.
  *   - Results are bit-identical from run to run for the same inputs and device.
  */

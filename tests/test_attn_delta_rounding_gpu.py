@@ -4,8 +4,11 @@ Two results that are rounded alike differ where a step of bf16 lies between them
 store (root mean square, of the result's norm) and steps of at most 2^-7 of a value, that happens to a share of at
 most d / 2^-7 of them, and leaves a distance of at most sqrt(d 2^-7) of the norm.
 
-  o        d = 1e-6 (products that keep 24 bits of every factor, sums in fp32 of up to 64 + 128 values:
+  o, dv    d = 1e-6 (products that keep 24 bits of every factor, sums in fp32 of up to 64 + 128 values:
            2^-24 sqrt(192) = 8e-7): 9e-5, so 1e-4
+  dq, dk   d = 2^-15: factors of two bf16 terms (2^-18 of each at most, 2^-17 for a product of two), as parts of
+           a sum that may cancel to a quarter: 4.9e-4, so 5e-4.  With any factor in one term (2^-9 of it at most,
+           2^-9 / sqrt(3) = 1.1e-3 in the root mean square) it is 2e-3 and more.
 """
 import pytest
 import torch
@@ -51,3 +54,16 @@ def test_outputs(lens, Hk, Hv, K, V, states):
     assert _distance(alone, want) <= 1e-4
     # whether a final state is asked for changes nothing in o
     assert torch.equal(alone, cc.cattn_delta_fwd(*args, _cu(lens), initial_state=init, final_state=True)[0])
+
+
+@pytest.mark.parametrize("lens,Hk,Hv,K,V", SHAPES)
+@pytest.mark.parametrize("states", [False, True])
+def test_gradients(lens, Hk, Hv, K, V, states):
+    q, k, v, g, beta, do, s0 = plain.delta_inputs(lens, Hk, Hv, K, V, seed=K + V + 2)
+    cu = [0] + torch.tensor(lens).cumsum(0).tolist()
+    leaves = [t.double().requires_grad_() for t in (q, k, v)]
+    o = plain.delta(*leaves, g.double(), beta.double(), cu, K ** -0.5, s0.double() if states else None)[0]
+    want = torch.autograd.grad(o, leaves, do.double())
+    got = cc.cattn_delta_bwd(*[t.cuda() for t in (q, k, v, g, beta, do)], _cu(lens), initial_state=s0.cuda() if states else None)
+    for name, tol, a, b in zip(("dq", "dk", "dv"), (5e-4, 5e-4, 1e-4), got, want):
+        assert _distance(a, b) <= tol, (name, _distance(a, b))
