@@ -21,7 +21,7 @@ static Rows rows(const void* p, int64_t st, int64_t sh) {
 
 // What a backward call keeps in its workspace, from a 256-byte boundary.
 struct DeltaWork {
-  size_t records, z, u, heads, ends, rest, odots, vdots, bdots, sums, anchors, adots, du, danchors, bytes;
+  size_t records, z, u, heads, ends, rest, odots, vdots, bdots, sums, shut, anchors, adots, du, danchors, bytes;
   bool both;  // the two chains run at once
 };
 // The two chains run at once up to this many CTAs each: half of the 152 SMs; and some more with several sequences,
@@ -49,6 +49,7 @@ static DeltaWork delta_work(int64_t total, int64_t nseq, int64_t Hv, int64_t V) 
   w.vdots = take(2 * tiles * rows * 4);
   w.bdots = take(2 * tiles * rows * 4);
   w.sums = take(static_cast<size_t>(delta_slots(total, nseq)) * Hv * 8);
+  w.shut = take(static_cast<size_t>(delta_slots(total, nseq)) * Hv * 4);
   const size_t anchors = total > 0 ? static_cast<size_t>(delta_anchors(total, nseq)) * Hv * tiles : 0;
   w.anchors = take(anchors * kAnchorFloats * 4);
   w.adots = take(anchors * kRowWarps * 4);
@@ -186,6 +187,7 @@ extern "C" CCONV_API int cattn_delta_bwd(
   c.vdots = reinterpret_cast<float*>(ws + w.vdots);
   c.bdots = reinterpret_cast<float*>(ws + w.bdots);
   c.sums = reinterpret_cast<double*>(ws + w.sums);
+  c.shut = reinterpret_cast<int*>(ws + w.shut);
   c.anchors = reinterpret_cast<float*>(ws + w.anchors);
   c.adots = reinterpret_cast<float*>(ws + w.adots);
   if (w.both) {

@@ -303,7 +303,8 @@ __device__ __forceinline__ void tmem_copy(uint32_t tmem, uint64_t rows) {
 
 // dg_t is the sum of o_i . do_i - v_i . dv_i over the tokens i >= t of the sequence.  Rounding adds up along it,
 // so it starts anew at every kAnchorChunks-th chunk, where it is <S_0, D_0>: the chain of the states leaves S_0
-// in fp32 there, its way back the product with D, one part from each row warp.
+// in fp32 there, its way back the product with D, one part from each row warp.  And where e^{g_t} is 0 so is dg_t, the
+// sum behind it, which starts anew there too: what rounding left of it is not the gradient of a gate that is shut.
 constexpr int kAnchorChunks = 8;
 constexpr int kAnchorFloats = 128 * kColumns;
 __host__ __device__ inline int64_t delta_anchors(int64_t total, int64_t nseq) {
@@ -334,7 +335,8 @@ struct DeltaCall {
   float *odots, *vdots, *bdots;  // [2 tiles][Hv][total] parts of o . do, v . dv and dbeta
   uint16_t *dq, *dk, *dv;
   float *dg, *dbeta, *dinit;
-  double* sums;           // [Hv][slots] of the chunks' terms of dg
+  double* sums;           // [Hv][slots] of the chunks' terms of dg, up to the first shut gate
+  int* shut;              // [Hv][slots] the last token of the chunk whose gate is shut, or -1
   float *du, *danchors;   // where both chains run at once: du as z, D as the anchors; else NULL
   float *anchors, *adots; // [anchors][Hv][tiles] states, [anchors][Hv][tiles * kRowWarps] parts of products
 };

@@ -64,7 +64,8 @@ struct GradArgs {
   const float *odots, *vdots, *bdots;
   uint16_t *dq, *dk;
   float *dg, *dbeta;
-  double* sums;  // [Hv][slots] of the chunks' terms of dg
+  double* sums;  // [Hv][slots], see DeltaCall
+  int* shut;
   float scale;
   int total, nseq, Hk, Hv, K, V, tiles;
   int64_t items;  // slots * Hk
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
       drain(alldone, 1);
     }
   } else if (warp == 2) {
-    // ---- dbeta, and dg summed up from each token to its chunk's end ----
+    // ---- dbeta, and dg summed up from each token to its chunk's end, or to the next shut gate ----
     for (int64_t at = blockIdx.x; at < p.items; at += gridDim.x) {
       const int64_t slot = at / p.Hk;
       Chunk chunk;
@@ -281,14 +282,20 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
       const int row0 = chunk.row0, n = chunk.n;
       for (int h = 0; h < ratio; ++h) {
         const int hv = static_cast<int>(at % p.Hk) * ratio + h;
-        double x[2] = {0.0, 0.0}, up;
+        double x[2] = {0.0, 0.0};
         float db[2] = {0.f, 0.f};
+        bool shut[2];  // of tokens 63 - 2 lane, 62 - 2 lane
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int t = kDelta - 1 - 2 * lane - j;
+          shut[j] = t < n && exp2_fast(kLog2e * p.g.at(row0 + t, hv)) == 0.f;
+        }
         for (int first = 0; first < 2 * p.tiles; first += kPartsAhead) {
           float o[kPartsAhead][2], v[kPartsAhead][2], d[kPartsAhead][2];
 #pragma unroll
           for (int i = 0; i < kPartsAhead; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {  // tokens 63 - 2 lane, 62 - 2 lane
+            for (int j = 0; j < 2; ++j) {
               const int t = kDelta - 1 - 2 * lane - j;
               const int64_t from = (static_cast<int64_t>(first + i) * p.Hv + hv) * p.total + row0 + t;
               o[i][j] = v[i][j] = d[i][j] = 0.f;
@@ -302,13 +309,24 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
               db[j] += d[i][j];
             }
         }
-        up = x[0] + x[1];
+        // the sum from a token on: 0 where its gate is shut
+        double up = shut[1] ? 0.0 : shut[0] ? x[1] : x[0] + x[1];
+        int cut = shut[0] | shut[1];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const double y = __shfl_up_sync(0xffffffffu, up, o);
-          if (lane >= o) up += y;
+          const int before = __shfl_up_sync(0xffffffffu, cut, o);
+          if (lane >= o) {
+            if (!cut) up += y;
+            cut |= before;
+          }
         }
-        const float sums[2] = {static_cast<float>(up - x[1]), static_cast<float>(up)};
+        const double behind = __shfl_up_sync(0xffffffffu, up, 1);
+        const double sum0 = shut[0] ? 0.0 : lane > 0 ? x[0] + behind : x[0];
+        const double sum1 = shut[1] ? 0.0 : x[1] + sum0;
+        const float sums[2] = {static_cast<float>(sum0), static_cast<float>(sum1)};
+        const int last = shut[0] ? kDelta - 1 - 2 * lane : shut[1] ? kDelta - 2 - 2 * lane : -1;
+        const int last_shut = __reduce_max_sync(0xffffffffu, last);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int t = kDelta - 1 - 2 * lane - j;
@@ -316,7 +334,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
           p.dbeta[static_cast<int64_t>(row0 + t) * p.Hv + hv] = db[j];
           p.dg[static_cast<int64_t>(row0 + t) * p.Hv + hv] = sums[j];
         }
-        if (lane == 31) p.sums[hv * (p.items / p.Hk) + slot] = up;
+        if (lane == 31) {
+          p.sums[hv * (p.items / p.Hk) + slot] = sum1;
+          p.shut[hv * (p.items / p.Hk) + slot] = last_shut;
+        }
       }
     }
   } else if (warp == 3) {
@@ -496,11 +517,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
   }
 }
 
-// dg, second part: what the chunks behind a token's add, to the next anchor or the sequence's end.  A CTA
+// dg, second part: what the chunks behind a token's add, to the next shut gate, anchor or the sequence's end.  A CTA
 // for each chunk, a warp for each value head in turn; kept in 64 bits, since terms of both signs cancel.
 struct GateArgs {
   const int32_t* cu;
   const double* sums;
+  const int* shut;
   const float* adots;
   float* dg;
   int total, nseq, Hv, parts;  // parts of an anchor
@@ -511,6 +533,7 @@ __global__ void __launch_bounds__(kGateThreads) cattn_delta_gates_kernel(const G
   cconv::grid_dependency_wait();
   cconv::grid_launch_dependents();
   __shared__ double later[kGateThreads];
+  __shared__ int shut[kGateThreads];  // the last token of this chunk whose gate is shut
   const int lane = threadIdx.x % 32;
   Chunk x;
   const int64_t slot = blockIdx.x;
@@ -521,20 +544,23 @@ __global__ void __launch_bounds__(kGateThreads) cattn_delta_gates_kernel(const G
     const int heads = min(kGateThreads, p.Hv - first);
     for (int i = threadIdx.x / 32; i < heads; i += kGateThreads / 32) {
       const int hv = first + i;
-      double sum = 0.0;
-      if (x.c + 1 + lane < min(next, chunks)) sum = p.sums[hv * p.slots + slot + 1 + lane];
-      if (next < chunks) {
+      // (the chunks up to the next anchor are fewer than 32)
+      const bool in = x.c + 1 + lane < min(next, chunks);
+      const int64_t at = hv * p.slots + slot + 1 + lane;
+      const unsigned cuts = __ballot_sync(0xffffffffu, in && p.shut[at] >= 0);
+      double sum = in && lane < (cuts ? __ffs(cuts) : 32) ? p.sums[at] : 0.0;
+      if (next < chunks && !cuts) {
         const float* part = p.adots + (anchor_of(x.a, x.seq, next) * p.Hv + hv) * p.parts;
         for (int j = lane; j < p.parts; j += 32) sum += static_cast<double>(part[j]);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == 0) later[i] = sum;
+      if (lane == 0) later[i] = sum, shut[i] = p.shut[hv * p.slots + slot];
     }
     __syncthreads();
     for (int i = threadIdx.x; i < x.n * heads; i += kGateThreads) {
       float* at = dg + static_cast<int64_t>(i / heads) * p.Hv + first + i % heads;
-      *at = static_cast<float>(later[i % heads] + static_cast<double>(*at));
+      if (i / heads > shut[i % heads]) *at = static_cast<float>(later[i % heads] + static_cast<double>(*at));
     }
     __syncthreads();
   }
@@ -542,7 +568,7 @@ __global__ void __launch_bounds__(kGateThreads) cattn_delta_gates_kernel(const G
 
 int launch_delta_gates(const DeltaCall& c, cudaStream_t stream) {
   const int64_t slots = delta_slots(c.s.total, c.s.nseq);
-  const GateArgs a{c.cu, c.sums, c.adots, c.dg, c.s.total, c.s.nseq, c.s.Hv, delta_tiles(c.s.V) * kRowWarps, slots};
+  const GateArgs a{c.cu, c.sums, c.shut, c.adots, c.dg, c.s.total, c.s.nseq, c.s.Hv, delta_tiles(c.s.V) * kRowWarps, slots};
   return launch_pdl(cattn_delta_gates_kernel, dim3(static_cast<unsigned>(slots)), dim3(kGateThreads), 0, stream, a) ==
                  cudaSuccess
              ? CCONV_OK
@@ -564,7 +590,7 @@ int launch_delta_grads(const DeltaCall& c, cudaStream_t stream) {
   a.u = c.u, a.heads = c.heads, a.ends = c.ends, a.rest = c.rest;
   a.odots = c.odots, a.vdots = c.vdots, a.bdots = c.bdots;
   a.dq = c.dq, a.dk = c.dk, a.dg = c.dg, a.dbeta = c.dbeta;
-  a.sums = c.sums;
+  a.sums = c.sums, a.shut = c.shut;
   a.scale = c.scale;
   a.total = c.s.total, a.nseq = c.s.nseq, a.Hk = c.s.Hk, a.Hv = c.s.Hv, a.K = c.s.K, a.V = c.s.V;
   a.tiles = delta_tiles(c.s.V);
