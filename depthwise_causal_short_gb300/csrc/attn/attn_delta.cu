@@ -197,8 +197,12 @@ extern "C" CCONV_API int cattn_delta_bwd(
   c.dq = static_cast<uint16_t*>(dq), c.dk = static_cast<uint16_t*>(dk), c.dv = static_cast<uint16_t*>(dv);
   c.dg = dg, c.dbeta = dbeta, c.dinit = d_initial_state;
   rc = launch_delta_prep(c, stream);
-  if (rc == CCONV_OK) rc = launch_delta_states(c, stream);
-  if (rc == CCONV_OK) rc = launch_delta_back(c, stream);
+  if (w.both) {
+    if (rc == CCONV_OK) rc = launch_delta_both(c, stream);
+  } else {
+    if (rc == CCONV_OK) rc = launch_delta_states(c, stream);
+    if (rc == CCONV_OK) rc = launch_delta_back(c, stream);
+  }
   if (rc == CCONV_OK) rc = launch_delta_grads(c, stream);
   if (rc == CCONV_OK) rc = launch_delta_gates(c, stream);
   return rc;

@@ -21,7 +21,7 @@
 // J, P~ and the gates depend on q, k, g and beta only: a first kernel makes them for all chunks at
 // once (attn_delta_prep.cu) and leaves them in the workspace, a record for each chunk and value head.
 // What is left is a chain over the chunks of a sequence, whose columns of V are independent
-// (attn_delta_chain.cu): a CTA takes 32 of them.
+// (attn_delta_chain.cuh): a CTA takes 32 of them.
 //
 // Precision: products run on bf16 with fp32 accumulators; an fp32 factor is split into three bf16
 // terms (24 bits), and for two such factors the products of terms down to 2^-16 are summed.  (Two terms, 16 bits, in
@@ -314,6 +314,10 @@ __device__ __forceinline__ int64_t anchor_of(int a, int seq, int c) {
   return a / (kAnchorChunks * kDelta) + seq + c / kAnchorChunks;
 }
 
+__device__ __forceinline__ float dot4(const float4& a, const float4& b) {
+  return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, a.x * b.x)));
+}
+
 struct DeltaCall {
   Rows q, k, v, d_o;
   Gates g, beta;          // (beta's values are taken as they are)
@@ -345,6 +349,7 @@ int launch_delta_prep(const DeltaCall& c, cudaStream_t stream);
 int launch_delta_fwd(const DeltaCall& c, cudaStream_t stream);
 int launch_delta_states(const DeltaCall& c, cudaStream_t stream);  // the gradient's chain of states
 int launch_delta_back(const DeltaCall& c, cudaStream_t stream);    // its chain backwards
+int launch_delta_both(const DeltaCall& c, cudaStream_t stream);    // both in one launch
 int launch_delta_grads(const DeltaCall& c, cudaStream_t stream);   // dq, dk, dbeta
 int launch_delta_gates(const DeltaCall& c, cudaStream_t stream);   // dg, from the chunks' parts and the anchors
 
