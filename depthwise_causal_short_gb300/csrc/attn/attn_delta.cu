@@ -22,13 +22,18 @@ static Rows rows(const void* p, int64_t st, int64_t sh) {
 // What a backward call keeps in its workspace, from a 256-byte boundary.
 struct DeltaWork {
   size_t records, z, u, heads, ends, rest, odots, vdots, bdots, sums, shut, anchors, adots, du, danchors, bytes;
-  bool both;  // the two chains run at once
+  bool room;  // for both chains at once
 };
-// The two chains run at once up to this many CTAs each: half of the 152 SMs; and some more with several sequences,
-// whose CTAs end at different times.  The gradient, us at once / in turn: 8192 rows of 8 heads of 128 (32 CTAs)
-// 524 / 790, of 16 (64) 614 / 869; 7 uneven sequences, 3108 rows of 4 heads (84) 102 / 154; 2 even ones of 12 heads
-// (96) 528 / 503, for 128 CTAs 1146 / 1034.
-constexpr int64_t kBothCtas = 76, kBothCtasRagged = 96;
+// Both chains run at once where the device has room for both, with one sequence: up to half of the SMs.  With several,
+// whose CTAs mostly end at different times, up to 5/8.  The gradient's time at once over in turn, by CTAs of a chain
+// (152 SMs; heads of 128 x 128 or 128 x 96):
+//   one sequence of 4096 rows           32 0.62   64 0.78   76 0.78   80 1.09   96 1.09   128 1.09
+//   2 sequences, 3000 + 1000            72 0.78   88 0.81   96 0.81  112 0.92   128 0.92  144 0.93
+//   4 to 7 uneven sequences, 4000       63 0.72   80 0.81   84 0.73   96 0.88   128 0.95  144 1.00
+//   2 to 4 even ones of 1024 to 2048    64 0.87   72 0.89   80 1.08   96 1.17   128 1.30
+// So even sequences lose some 10 % from 77 CTAs to 95 and uneven ones win 20 %; the lengths are not known here.
+static bool at_once(int64_t ctas, int64_t nseq, int sms) { return 8 * ctas <= (nseq > 1 ? 5 : 4) * int64_t(sms); }
+constexpr int64_t kBothRoom = 96;  // the workspace, which no device is asked for, has room for it up to here
 static DeltaWork delta_work(int64_t total, int64_t nseq, int64_t Hv, int64_t V) {
   const size_t tiles = static_cast<size_t>(delta_tiles(V)), rows = static_cast<size_t>(total) * Hv;
   const size_t states = total > 0 ? static_cast<size_t>(delta_slots(total, nseq)) * Hv * tiles * kStatePanel : 0;
@@ -53,8 +58,8 @@ static DeltaWork delta_work(int64_t total, int64_t nseq, int64_t Hv, int64_t V) 
   const size_t anchors = total > 0 ? static_cast<size_t>(delta_anchors(total, nseq)) * Hv * tiles : 0;
   w.anchors = take(anchors * kAnchorFloats * 4);
   w.adots = take(anchors * kRowWarps * 4);
-  w.both = total > 0 && nseq * Hv * static_cast<int64_t>(tiles) <= (nseq > 1 ? kBothCtasRagged : kBothCtas);
-  if (w.both) {
+  w.room = total > 0 && nseq * Hv * static_cast<int64_t>(tiles) <= kBothRoom;
+  if (w.room) {
     w.du = take(states / kStatePanel * kDelta * kColumns * 4);
     w.danchors = take(anchors * kAnchorFloats * 4);
   }
@@ -190,14 +195,20 @@ extern "C" CCONV_API int cattn_delta_bwd(
   c.shut = reinterpret_cast<int*>(ws + w.shut);
   c.anchors = reinterpret_cast<float*>(ws + w.anchors);
   c.adots = reinterpret_cast<float*>(ws + w.adots);
-  if (w.both) {
+  bool both = false;
+  if (w.room) {
+    int sms = 0;
+    if (sm_count(&sms) != CCONV_OK) return CCONV_ERR_CUDA;
+    both = at_once(nseq * Hv * delta_tiles(V), nseq, sms);
+  }
+  if (both) {
     c.du = reinterpret_cast<float*>(ws + w.du);
     c.danchors = reinterpret_cast<float*>(ws + w.danchors);
   }
   c.dq = static_cast<uint16_t*>(dq), c.dk = static_cast<uint16_t*>(dk), c.dv = static_cast<uint16_t*>(dv);
   c.dg = dg, c.dbeta = dbeta, c.dinit = d_initial_state;
   rc = launch_delta_prep(c, stream);
-  if (w.both) {
+  if (both) {
     if (rc == CCONV_OK) rc = launch_delta_both(c, stream);
   } else {
     if (rc == CCONV_OK) rc = launch_delta_states(c, stream);

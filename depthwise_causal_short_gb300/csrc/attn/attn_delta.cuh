@@ -341,7 +341,7 @@ struct DeltaCall {
   float *dg, *dbeta, *dinit;
   double* sums;           // [Hv][slots] of the chunks' terms of dg, up to the first shut gate
   int* shut;              // [Hv][slots] the last token of the chunk whose gate is shut, or -1
-  float *du, *danchors;   // where both chains run at once: du as z, D as the anchors; else NULL
+  float *du, *danchors;   // where both chains run at once: du as z, D as the anchors
   float *anchors, *adots; // [anchors][Hv][tiles] states, [anchors][Hv][tiles * kRowWarps] parts of products
 };
 

@@ -73,3 +73,19 @@ def test_inputs_written_by_the_kernel_before(lens, Hv):
         for a, b in zip(out, want[i % 2]):
             wrong += (a != b).sum()
     assert wrong.item() == 0
+
+
+@pytest.mark.parametrize("nseq", [1, 2])
+def test_where_the_chains_run_at_once(nseq):
+    # half of the SMs for the chain of one sequence, 5/8 with several; a CTA a head here
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    most = (sms // 2 if nseq == 1 else 5 * sms // 8) // nseq
+    lens = [70] * nseq
+
+    def call(heads):
+        a = [t.cuda() for t in plain.delta_inputs(lens, heads, heads, 32, 32, seed=heads)[:6]]
+        return lambda: cc.cattn_delta_bwd(*a, _cu(lens))
+
+    assert _at_once(call(most)) and not _at_once(call(most + 1))
+    for heads in (most, most + 1):
+        assert all(bool(torch.isfinite(t).all()) for t in call(heads)() if t is not None)
