@@ -418,7 +418,10 @@ static LnKernel kernel_of() {
 }
 // The smallest group that holds a row in one piece a thread, to 128 channels, and in two above; in four in a
 // forward without a gate, to 1024 (more tensors or more threads a row, and they cost more than they save), where
-// that makes a CTA for each SM (1000 rows of 256: 2.7 us with four, 2.2 with two).
+// that makes a CTA for each SM, and to 256 channels eight.  Four pieces over two, a forward's time, by rows:
+//   256 channels    600 1.25   2400 1.12   4864 1.00   7000 1.10   14000 1.04   28000 1.03   40000 0.96  131072 0.87
+//   512             600 1.14   1200 1.14   2400 0.84   4864 0.66   7000 0.89   14000 0.96   28000 0.92
+//   1024            600 1.14   1200 0.74   2400 0.75   4864 1.10   7000 1.16   14000 1.06   28000 0.94  40000 0.92
 // Measured, us, 33.5 million elements; pieces 1 / 2 / 4:
 //   rows of 256     forward 21.9 / 21.8 / 18.9    with a gate 35.0 / 33.6 / 41.7    its gradient 71.3 / 60.7 / 136
 //   512             29.5 / 25.3 / 20.6            - / 35.5 / 43.5                   without a gate 52.9 / 34.3 / 72
@@ -428,7 +431,7 @@ template <bool BWD>
 static LnKernel pick(int64_t C, bool gate, int64_t rows, int sms) {
   if (!BWD && !gate && C > 128 && C <= 1024) {
     const LnKernel four = C <= 256 ? kernel_of<8, 4, BWD>() : C <= 512 ? kernel_of<16, 4, BWD>() : kernel_of<32, 4, BWD>();
-    if (rows >= static_cast<int64_t>(sms) * four.rows) return four;
+    if (rows >= static_cast<int64_t>(sms) * four.rows * (C <= 256 ? 8 : 1)) return four;
   }
   if (C <= 32) return kernel_of<4, 1, BWD>();
   if (C <= 64) return kernel_of<8, 1, BWD>();
