@@ -55,7 +55,7 @@ static DeltaWork delta_work(int64_t total, int64_t nseq, int64_t Hv, int64_t V) 
   w.bdots = take(2 * tiles * rows * 4);
   w.sums = take(static_cast<size_t>(delta_slots(total, nseq)) * Hv * 8);
   w.shut = take(static_cast<size_t>(delta_slots(total, nseq)) * Hv * 4);
-  const size_t anchors = total > 0 ? static_cast<size_t>(delta_anchors(total, nseq)) * Hv * tiles : 0;
+  const size_t anchors = total > 0 ? static_cast<size_t>(delta_anchors(total)) * Hv * tiles : 0;
   w.anchors = take(anchors * kAnchorFloats * 4);
   w.adots = take(anchors * kRowWarps * 4);
   w.room = total > 0 && nseq * Hv * static_cast<int64_t>(tiles) <= kBothRoom;

@@ -307,12 +307,11 @@ __device__ __forceinline__ void tmem_copy(uint32_t tmem, uint64_t rows) {
 // sum behind it, which starts anew there too: what rounding left of it is not the gradient of a gate that is shut.
 constexpr int kAnchorChunks = 8;
 constexpr int kAnchorFloats = 128 * kColumns;
-__host__ __device__ inline int64_t delta_anchors(int64_t total, int64_t nseq) {
-  return total / (kAnchorChunks * kDelta) + nseq;
-}
-__device__ __forceinline__ int64_t anchor_of(int a, int seq, int c) {
-  return a / (kAnchorChunks * kDelta) + seq + c / kAnchorChunks;
-}
+// An anchor's place goes by its token: those of a sequence are 512 tokens apart, and the next sequence's first one
+// lies as far behind its start.
+constexpr int kAnchorTokens = kAnchorChunks * kDelta;
+__host__ __device__ inline int64_t delta_anchors(int64_t total) { return total / kAnchorTokens + 1; }
+__device__ __forceinline__ int64_t anchor_of(int a, int c) { return a / kAnchorTokens + (a % kAnchorTokens + c * kDelta) / kAnchorTokens; }
 
 __device__ __forceinline__ float dot4(const float4& a, const float4& b) {
   return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, a.x * b.x)));

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) cattn_delta_join_kernel(const 
         p.bdots[(static_cast<int64_t>(tile * 2 + h) * p.Hv + hv) * p.total + x.row0 + t + 8 * r] = du_z;
     }
     if (anchor) {
-      const int64_t at = (anchor_of(x.a, x.seq, x.c) * p.Hv + hv) * p.tiles + tile;
+      const int64_t at = (anchor_of(x.a, x.c) * p.Hv + hv) * p.tiles + tile;
       const int64_t first = at * kAnchorFloats + row * kColumns + h * 16;
       const float4 *s = reinterpret_cast<const float4*>(p.anchors + first);
       const float4 *d = reinterpret_cast<const float4*>(p.danchors + first);

@@ -303,7 +303,7 @@ __device__ __forceinline__ void run(const Args& p, int cta, unsigned* fault) {
         for (int r = 0; r < 2; ++r) v.v[j][r] = bf16x2_to_f2(vw[r][j]);
       fetch(c - 1);
       const bool anchor = c > 0 && c % kAnchorChunks == 0;
-      const int64_t anchor_at = (anchor_of(row_a, seq, c) * p.Hv + hv) * p.tiles + tile;
+      const int64_t anchor_at = (anchor_of(row_a, c) * p.Hv + hv) * p.tiles + tile;
       const float* state = p.anchors + anchor_at * kAnchorFloats + row * kColumns + h * 16;
       if (anchor && !BESIDE) asm volatile("prefetch.global.L2 [%0];" ::"l"(state));
       if (!(ok = DELTA_WARP_WAIT(rfull + 8 * st, i / 2))) break;

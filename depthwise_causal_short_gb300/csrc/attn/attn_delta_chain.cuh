@@ -359,7 +359,7 @@ __device__ __forceinline__ void run(const Args& p, int cta, unsigned* fault) {
       }
       if (BWD && c > 0 && c % kAnchorChunks == 0) {
         float4* to = reinterpret_cast<float4*>(
-            p.anchors + ((anchor_of(w.a, w.seq, c) * p.Hv + w.hv) * p.tiles + w.tile) * kAnchorFloats + row * kColumns + h * 16);
+            p.anchors + ((anchor_of(w.a, c) * p.Hv + w.hv) * p.tiles + w.tile) * kAnchorFloats + row * kColumns + h * 16);
 #pragma unroll
         for (int i = 0; i < 4; ++i) to[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
       }

@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kGateThreads) cattn_delta_gates_kernel(const G
       const unsigned cuts = __ballot_sync(0xffffffffu, in && p.shut[at] >= 0);
       double sum = in && lane < (cuts ? __ffs(cuts) : 32) ? p.sums[at] : 0.0;
       if (next < chunks && !cuts) {
-        const float* part = p.adots + (anchor_of(x.a, x.seq, next) * p.Hv + hv) * p.parts;
+        const float* part = p.adots + (anchor_of(x.a, next) * p.Hv + hv) * p.parts;
         for (int j = lane; j < p.parts; j += 32) sum += static_cast<double>(part[j]);
       }
 #pragma unroll

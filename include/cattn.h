@@ -190,8 +190,9 @@ CCONV_API int cattn_linear_update(const void* q, int64_t sqt, int64_t sqh, const
 /*
  * Workspace cattn_delta_fwd / cattn_delta_bwd need (16-byte aligned).  For each value head and each chunk of
  * 64 tokens (a sequence's last one counts in full, and so does an empty or one-token sequence's: total / 64 +
- * nseq of them) 49 KB forward; backward 49 KB and 52 KB for every 32 columns of V (60 KB in small calls).
- * 16384 rows of 16 heads of 128 x 128: 0.2 GB and 1.1 GB; 4096 sequences of one token: 3.3 GB and 17 GB.
+ * nseq of them) 49 KB forward; backward 49 KB, and up to 56 KB (66 KB where nseq * Hv * ceil(V / 32) <= 96) for
+ * every 32 columns of V.
+ * 16384 rows of 16 heads of 128 x 128: 0.2 GB and 1.1 GB; 4096 sequences of one token: 3.3 GB and 18 GB.
  */
 CCONV_API int cattn_delta_fwd_workspace_bytes(int64_t total, int64_t nseq, int64_t Hk, int64_t Hv,
                                               int64_t K, int64_t V, size_t* bytes);
