@@ -9,9 +9,9 @@
 // in lanes 0 to 15 of each quarter, those of the second ones in lanes 16 to 31 (in place of Q D).  The products
 // that have do in them wait for nothing of the chain: P~^T do is made a chunk ahead, while the rows work; four
 // warps prepare do for them.
-// Bound as that chain is: 377 us of the same 128 CTAs, 5600 cycles a chunk (the rows' part between the first two
-// products 1400 of them, beside the next record's load); tensor cores 20 %, memory 30 %.  K and Q copied to
-// tensor memory as a first operand gained nothing here (400 us).
+// Bound as that chain is: 395 us of the same 128 CTAs, 5800 cycles a chunk (the rows' part between the first two
+// products 1400 of them, beside the next record's load); tensor cores 16 %, memory 30 %.  dv's second term takes 15 us
+// of it.  K and Q copied to tensor memory as a first operand gained nothing here.
 // It needs nothing of the chain of the states but for dbeta and the anchors: where SMs are free both run in one
 // launch (BESIDE), and a kernel behind them makes those two.
 // It leaves dv, a second term of it, two terms of every D, dbeta = du . z, v . dv, and at every kAnchorChunks-th

@@ -14,9 +14,9 @@
 // is attn_delta_back.cuh.
 //
 // Bound by that chain: a product, its results to registers, the next operand to shared memory.  2 sequences of
-// 8192 rows, 16 heads of 128 x 128 (128 CTAs, 128 chunks each): 285 us, 357 BWD;
-// 4000 to 4400 cycles a chunk, of which the three products take 1600 and their operands some 1400 between them.
-// Tensor cores are busy 15 to 18 % of the time, memory 16 to 33 %, shared memory about half.  A CTA is one on its
+// 8192 rows, 16 heads of 128 x 128 (128 CTAs, 128 chunks each): 290 us, 360 BWD; 4200 to 4600 cycles a chunk, of which
+// the three products take 1600 and their operands some 1400 between them.  Tensor cores are busy 15 to 18 % of the
+// time, memory 17 to 33 %.  A CTA is one on its
 // SM (204 KB); 28 warps in place of 12 were slower, and so was A from shared memory (by a tenth).
 #pragma once
 

@@ -15,8 +15,8 @@
 // of V at a time, through a ring for what X and Y need and one for the states.  Every factor that is no input keeps
 // two terms, dv as it is stored and what that leaves (dv'): 16 bits, for results of 9.  With all of them in one term
 // dk's error in the 2-norm was 2.8e-3, with dv alone 1.8e-3 to 2.1e-3; the store makes 1.7e-3.
-// Bound by memory, and the loads' latency behind it: 197 us for 16384 rows of 16 heads on 8 of 128 x 128, 966 MB
-// (4.9 TB/s, 72 % of a copy's rate), of which two terms of S_0 and of D are 537.  One CTA an SM (225 KB).
+// Bound by memory, and the loads' latency behind it: 209 us for 16384 rows of 16 heads on 8 of 128 x 128, 1032 MB
+// (4.9 TB/s, 73 % of a copy's rate), of which two terms of S_0 and of D are 537.  One CTA an SM (212 KB).
 #include <cudaTypedefs.h>
 
 #include "attn_chunk_host.h"
