@@ -255,7 +255,7 @@ def cattn_delta_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
                     workspace: torch.Tensor | None = None, stream=None):
     """Gradient of cattn_delta_fwd's o: (dq, dk, dv, dg, dbeta, d_initial_state or None).  The final
     states count as constants.  Arguments as in cattn_linear_bwd; dbeta is [total, Hv] fp32.  dg is 0 where
-    exp(g) is 0 in fp32."""
+    exp(g) is 0 in fp32 and at first tokens without an initial state."""
     return _calls().delta_bwd(q, k, v, g, scale, do, cu_seqlens, initial_state, state_indices, status,
                               want_dinit, dq, dk, dv, dg, d_initial_state, workspace, stream, beta, dbeta)
 

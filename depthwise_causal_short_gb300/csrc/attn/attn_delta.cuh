@@ -303,8 +303,9 @@ __device__ __forceinline__ void tmem_copy(uint32_t tmem, uint64_t rows) {
 
 // dg_t is the sum of o_i . do_i - v_i . dv_i over the tokens i >= t of the sequence.  Rounding adds up along it,
 // so it starts anew at every kAnchorChunks-th chunk, where it is <S_0, D_0>: the chain of the states leaves S_0
-// in fp32 there, its way back the product with D, one part from each row warp.  And where e^{g_t} is 0 so is dg_t, the
-// sum behind it, which starts anew there too: what rounding left of it is not the gradient of a gate that is shut.
+// in fp32 there, its way back the product with D, one part from each row warp.  And where e^{g_t} is 0, or the state
+// that it acts on (a sequence's first token without an initial state), so is dg_t, the sum behind it, which starts anew
+// there too: what rounding left of it is no gradient of a gate that lets nothing through.
 constexpr int kAnchorChunks = 8;
 constexpr int kAnchorFloats = 128 * kColumns;
 // An anchor's place goes by its token: those of a sequence are 512 tokens apart, and the next sequence's first one

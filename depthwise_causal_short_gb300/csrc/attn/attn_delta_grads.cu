@@ -67,7 +67,7 @@ struct GradArgs {
   double* sums;  // [Hv][slots], see DeltaCall
   int* shut;
   float scale;
-  int total, nseq, Hk, Hv, K, V, tiles;
+  int total, nseq, Hk, Hv, K, V, tiles, fresh;
   int64_t items;  // slots * Hk
 };
 
@@ -284,11 +284,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) cattn_delta_grads_kernel(cons
         const int hv = static_cast<int>(at % p.Hk) * ratio + h;
         double x[2] = {0.0, 0.0};
         float db[2] = {0.f, 0.f};
-        bool shut[2];  // of tokens 63 - 2 lane, 62 - 2 lane
+        bool shut[2];  // of tokens 63 - 2 lane, 62 - 2 lane; the first gate on no state counts as shut
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int t = kDelta - 1 - 2 * lane - j;
-          shut[j] = t < n && exp2_fast(kLog2e * p.g.at(row0 + t, hv)) == 0.f;
+          shut[j] = t < n && ((p.fresh && row0 + t == chunk.a) || exp2_fast(kLog2e * p.g.at(row0 + t, hv)) == 0.f);
         }
         for (int first = 0; first < 2 * p.tiles; first += kPartsAhead) {
           float o[kPartsAhead][2], v[kPartsAhead][2], d[kPartsAhead][2];
@@ -594,6 +594,7 @@ int launch_delta_grads(const DeltaCall& c, cudaStream_t stream) {
   a.scale = c.scale;
   a.total = c.s.total, a.nseq = c.s.nseq, a.Hk = c.s.Hk, a.Hv = c.s.Hv, a.K = c.s.K, a.V = c.s.V;
   a.tiles = delta_tiles(c.s.V);
+  a.fresh = c.initial == nullptr;
   a.items = delta_slots(c.s.total, c.s.nseq) * c.s.Hk;
   const int64_t ctas = a.items < sms ? a.items : sms;
   if (cconv::set_max_dynamic_smem(reinterpret_cast<const void*>(cattn_delta_grads_kernel), kGradBytes) != CCONV_OK)

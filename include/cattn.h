@@ -229,7 +229,7 @@ CCONV_API int cattn_delta_fwd(const void* q, int64_t sqt, int64_t sqh, const voi
  *   dbeta     [total, Hv] fp32 contiguous output, 16-byte aligned.
  *   dg is a sum over the tokens behind its own, of up to 512 products o_i . do_i and v_i . dv_i that
  *   cancel where little of the state is kept: its error goes by their size (about 1e-6 of it), however
- *   small dg is.  Where exp(g) is 0 in fp32, dg is 0.
+ *   small dg is.  Where exp(g) is 0 in fp32, and at first tokens without an initial state, dg is 0.
  */
 CCONV_API int cattn_delta_bwd(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt,
                               int64_t skh, const void* v, int64_t svt, int64_t svh, const float* g,

@@ -104,3 +104,21 @@ def test_what_is_before_a_shut_gate_does_not_count_on_what_is_behind():
     whole = cc.cattn_delta_bwd(q, k, v, g, beta, do, _cu([900]), initial_state=s0[:1])
     alone = cc.cattn_delta_bwd(*[t[:640] for t in (q, k, v, g, beta, do)], _cu([640]), initial_state=s0[:1])
     assert torch.equal(whole[3][:640], alone[3]) and not whole[3][640].any()
+
+
+@pytest.mark.parametrize("lens", [[1], [1, 0, 1, 130, 64, 1, 700]])
+def test_the_first_gate_on_no_state(lens):
+    # it acts on nothing: dg is 0, and the gates behind it are as right as ever
+    q, k, v, g, beta, do, s0 = _inputs(lens, seed=8)
+    leaf = g.double().requires_grad_()
+    cu = [0] + torch.tensor(lens).cumsum(0).tolist()
+    o, _ = plain.delta(q.double(), k.double(), v.double(), leaf, beta.double(), cu, 0.125)
+    want, = torch.autograd.grad(o, leaf, do.double())
+    args = [t.cuda() for t in (q, k, v, g, beta, do)]
+    dg = cc.cattn_delta_bwd(*args, _cu(lens))[3].double().cpu()
+    first = [a for a, b in zip(cu, cu[1:]) if b > a]
+    assert not want[first].any() and not dg[first].any()
+    off = (dg - want).abs().amax(0) / (o.detach().norm(dim=-1) * do.double().norm(dim=-1)).amax(0)
+    assert (off <= 2e-4).all(), off
+    # on a state it has one
+    assert cc.cattn_delta_bwd(*args, _cu(lens), initial_state=s0.cuda())[3][first].any()
