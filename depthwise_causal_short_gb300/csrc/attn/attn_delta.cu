@@ -31,7 +31,7 @@ struct DeltaWork {
 //   2 sequences, 3000 + 1000            72 0.78   88 0.81   96 0.81  112 0.92   128 0.92  144 0.93
 //   4 to 7 uneven sequences, 4000       63 0.72   80 0.81   84 0.73   96 0.88   128 0.95  144 1.00
 //   2 to 4 even ones of 1024 to 2048    64 0.87   72 0.89   80 1.08   96 1.17   128 1.30
-// So even sequences lose some 10 % from 77 CTAs to 95 and uneven ones win 20 %; the lengths are not known here.
+// So from 77 CTAs to 95 even sequences lose 8 to 17 % and uneven ones win 20 %; the lengths are not known here.
 static bool at_once(int64_t ctas, int64_t nseq, int sms) { return 8 * ctas <= (nseq > 1 ? 5 : 4) * int64_t(sms); }
 constexpr int64_t kBothRoom = 96;  // the workspace, which no device is asked for, has room for it up to here
 static DeltaWork delta_work(int64_t total, int64_t nseq, int64_t Hv, int64_t V) {
